@@ -27,6 +27,9 @@ __all__ = [
     "engram_selftest_mod", "engram_project_gate", "project_gate_workspace", "partials_shape", "EngramLayer",
     "library_path", "ST_BAD_TOKEN", "ST_BAD_ROW", "ST_BAD_SLOT", "ST_TIMEOUT", "DEAD", "ROW_BYTES", "DecodeGraph",
     "set_kernel_options", "kernel_options", "sf_cols", "sf_word_index",
+    "engram_lookup", "engram_lookup_grad", "engram_lookup_grad_rows", "lookup_grad_workspace",
+    "engram_recurrence", "engram_recurrence_grad", "engram_recurrence_step", "recurrence_carry",
+    "recurrence_workspace", "engram_distill",
 ]
 
 MAX_LAYERS = 8
@@ -143,6 +146,16 @@ _SIGS = {
     "engram_get_kernel_options": [_P],
     "engram_short_conv_add": [_P, _P, _P, _P, _I64, _I32, _I32, _P, _I64, _P, _P, _P, _I32, _I32, _F32, _P, _P,
                               _I64, _P, ctypes.c_size_t, _P, _P],
+    "engram_lookup": [_P, _I32, _I64, _I32, _P, _I64, _I32, _F32, _P, _I64, _P, _P],
+    "engram_lookup_grad": [_P, _I32, _I64, _P, _I64, _I32, _I32, _I64, _F32, _P, _P, ctypes.c_size_t, _P, _P],
+    "engram_lookup_grad_rows": [_P, _I32, _I64, _P, _I64, _I32, _I32, _I64, _F32, _P, _P, _P, _P, ctypes.c_size_t,
+                                _P, _P],
+    "engram_recurrence": [_P, _I64, _P, _I64, _I32, _I64, _I32, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P, _P,
+                          ctypes.c_size_t, _P, _P],
+    "engram_recurrence_grad": [_P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _P, _I64, _P, _P, _P, _P, _P, _I64,
+                               _P, _I64, _P, _I64, _P, ctypes.c_size_t, _P, _P],
+    "engram_recurrence_step": [_P, _I64, _P, _I64, _I32, _I64, _I32, _P, _P, _P, _I64, _P, _I64, _P, _P],
+    "engram_distill": [_P, _I32, _I64, _I64, _I64, _P, _P, _I32, _F32, _P, _P, _P, _P, _I64, _P, _P],
 }
 
 
@@ -168,6 +181,12 @@ def _load():
         lib.engram_project_gate_workspace_bytes.argtypes = [_I64, _I32, _I32]
         lib.engram_short_conv_workspace_bytes.restype = ctypes.c_size_t
         lib.engram_short_conv_workspace_bytes.argtypes = [_I64, _I32]
+        lib.engram_lookup_grad_workspace_bytes.restype = ctypes.c_size_t
+        lib.engram_lookup_grad_workspace_bytes.argtypes = [_I64, _I32, _I32]
+        lib.engram_recurrence_carry_bytes.restype = ctypes.c_size_t
+        lib.engram_recurrence_carry_bytes.argtypes = [_I64, _I32]
+        lib.engram_recurrence_workspace_bytes.restype = ctypes.c_size_t
+        lib.engram_recurrence_workspace_bytes.argtypes = [_I64, _I32]
         lib.engram_layout_size.restype = ctypes.c_size_t
         lib.engram_layout_params_size.restype = ctypes.c_size_t
         if lib.engram_layout_size() != ctypes.sizeof(_Layout) or \
@@ -960,6 +979,294 @@ def engram_selftest_mod(layout: Layout, layer: int, x: torch.Tensor) -> torch.Te
     _check(L.engram_selftest_mod(layout.ref, layer, _ptr(x), x.numel(), _ptr(out), _stream(x.device)),
            "engram_selftest_mod")
     return out
+
+
+# --------------------------------------------------------------------------- training operators
+
+
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _need_rows(t: torch.Tensor, name: str, dtype, device, n_rows: int, width: int) -> int:
+    """Checks a [n_rows][width] device matrix with unit column stride; returns its row stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if tuple(t.shape) != (n_rows, width):
+        raise ValueError(f"{name} must be [{n_rows}][{width}], is {list(t.shape)}")
+    if width > 1 and n_rows > 0 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if n_rows <= 1:
+        return max(t.stride(0), width)
+    if t.stride(0) < width:
+        raise ValueError(f"the rows of {name} overlap")
+    return t.stride(0)
+
+
+def _elem_type(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _TYPES:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return _TYPES[t.dtype]
+
+
+def _ids_shape(ids: torch.Tensor, device) -> tuple:
+    _need(ids, "ids", torch.int32, device)
+    if ids.dim() not in (1, 2):
+        raise ValueError("ids must be [T] or [T][n_cols]")
+    if ids.dim() == 2 and ids.shape[1] < 1:
+        raise ValueError("ids must have at least one column")
+    return ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1
+
+
+def engram_lookup(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rows of table (bf16 or f32 [R][D]) times scale: returns [T][n_cols*D]; ids int32 [T] or [T][n_cols],
+    DEAD gives zeros."""
+    L = _load()
+    dev = table.device
+    ty = _elem_type(table, "table")
+    _need(table, "table", table.dtype)
+    if table.dim() != 2:
+        raise ValueError("table must be [rows][row_dim]")
+    R, D = table.shape
+    T, C = _ids_shape(ids, dev)
+    if out is None:
+        out = torch.empty((T, C * D), dtype=table.dtype, device=dev)
+    ld = _need_rows(out, "out", table.dtype, dev, T, C * D)
+    _check(L.engram_lookup(_ptr(table), ty, R, D, _ptr(ids), T, C, scale, _ptr(out), ld, _ptr(status), _stream(dev)),
+           "engram_lookup")
+    return out
+
+
+def lookup_grad_workspace(n_tokens: int, n_cols: int, row_dim: int, device) -> torch.Tensor:
+    n = _load().engram_lookup_grad_workspace_bytes(n_tokens, n_cols, row_dim)
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+
+
+def _grad_args(dout: torch.Tensor, ids: torch.Tensor, workspace: Optional[torch.Tensor]):
+    """Checks shared by the lookup gradients; returns (type, stride, T, n_cols, D, workspace)."""
+    dev = dout.device
+    ty = _elem_type(dout, "dout")
+    T, C = _ids_shape(ids, dev)
+    if dout.dim() != 2 or dout.shape[1] % C or dout.shape[1] == 0:
+        raise ValueError("dout must be [T][n_cols*row_dim]")
+    D = dout.shape[1] // C
+    ld = _need_rows(dout, "dout", dout.dtype, dev, T, C * D)
+    if workspace is None:
+        workspace = lookup_grad_workspace(T, C, D, dev)
+    _need(workspace, "workspace", torch.uint8, dev)
+    return ty, ld, T, C, D, workspace
+
+
+def engram_lookup_grad(dout: torch.Tensor, ids: torch.Tensor, total_rows: int, scale: float = 1.0,
+                       grad: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                       status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The table's gradient under engram_lookup, every row: f32 [total_rows][D]."""
+    L = _load()
+    dev = dout.device
+    ty, ld, T, C, D, workspace = _grad_args(dout, ids, workspace)
+    if grad is None:
+        grad = torch.empty((total_rows, D), dtype=torch.float32, device=dev)
+    _need(grad, "grad", torch.float32, dev, total_rows * D)
+    _check(L.engram_lookup_grad(_ptr(dout), ty, ld, _ptr(ids), T, C, D, total_rows, scale, _ptr(grad),
+                                _ptr(workspace), workspace.numel(), _ptr(status), _stream(dev)),
+           "engram_lookup_grad")
+    return grad
+
+
+def engram_lookup_grad_rows(dout: torch.Tensor, ids: torch.Tensor, total_rows: int, scale: float = 1.0,
+                            rows: Optional[torch.Tensor] = None, grad: Optional[torch.Tensor] = None,
+                            count: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                            status: Optional[torch.Tensor] = None):
+    """The table's gradient under engram_lookup as its distinct rows: (rows int32 [n] ascending then -1,
+    grad f32 [n][D] then 0, count int32 [1]), n = ids.numel()."""
+    L = _load()
+    dev = dout.device
+    ty, ld, T, C, D, workspace = _grad_args(dout, ids, workspace)
+    n = T * C
+    if rows is None:
+        rows = torch.empty(n, dtype=torch.int32, device=dev)
+    if grad is None:
+        grad = torch.empty((n, D), dtype=torch.float32, device=dev)
+    if count is None:
+        count = torch.empty(1, dtype=torch.int32, device=dev)
+    _need(rows, "rows", torch.int32, dev, n)
+    _need(grad, "grad", torch.float32, dev, n * D)
+    _need(count, "count", torch.int32, dev, 1)
+    _check(L.engram_lookup_grad_rows(_ptr(dout), ty, ld, _ptr(ids), T, C, D, total_rows, scale, _ptr(rows),
+                                     _ptr(grad), _ptr(count), _ptr(workspace), workspace.numel(), _ptr(status),
+                                     _stream(dev)), "engram_lookup_grad_rows")
+    return rows, grad, count
+
+
+def recurrence_carry(n_tokens: int, dim: int, device) -> torch.Tensor:
+    """Buffer for the states that engram_recurrence saves for its backward pass."""
+    n = _load().engram_recurrence_carry_bytes(n_tokens, dim) // 4
+    return torch.empty(max(n, 1), dtype=torch.float32, device=device)
+
+
+def recurrence_workspace(n_tokens: int, dim: int, device) -> torch.Tensor:
+    n = _load().engram_recurrence_workspace_bytes(n_tokens, dim)
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+
+
+def _recurrence_args(x, g, cu_seqlens, mask, state, state_out, slots, workspace):
+    """Checks shared by the scan and its gradient; returns (type, T, D, x stride, g stride, n_seqs, n_slots,
+    workspace)."""
+    dev = x.device
+    ty = _elem_type(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [T][dim]")
+    T, D = x.shape
+    xs = _need_rows(x, "x", x.dtype, dev, T, D)
+    gs = _need_rows(g, "g", x.dtype, dev, T, D)
+    _need(cu_seqlens, "cu_seqlens", torch.int64, dev)
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be [n_seqs+1]")
+    n_seqs = cu_seqlens.numel() - 1
+    if mask is not None:
+        _need(mask, "mask", torch.uint8, dev, T)
+    if slots is not None:
+        _need(slots, "slots", torch.int32, dev, n_seqs)
+    n_slots = 0
+    for name, s in (("state", state), ("state_out or dstate", state_out)):
+        if s is not None:
+            _need(s, name, torch.float32, dev)
+            if s.dim() != 2 or s.shape[1] != D or (n_slots and s.shape[0] != n_slots):
+                raise ValueError(f"{name} must be [n_slots][dim]")
+            n_slots = s.shape[0]
+    if slots is None and n_slots and n_slots < n_seqs:
+        raise ValueError("without slots the state needs a row for every sequence")
+    if workspace is None:
+        workspace = recurrence_workspace(T, D, dev)
+    _need(workspace, "workspace", torch.uint8, dev)
+    return ty, T, D, xs, gs, n_seqs, n_slots, workspace
+
+
+def engram_recurrence(x: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor,
+                      mask: Optional[torch.Tensor] = None, state: Optional[torch.Tensor] = None,
+                      slots: Optional[torch.Tensor] = None, state_out: Optional[torch.Tensor] = None,
+                      y: Optional[torch.Tensor] = None, carry: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y_t = s_t = sigmoid(g_t) s_{t-1} + sigmoid(-g_t) x_t along packed sequences; x, g bf16 or f32 [T][dim].
+
+    state f32 [n_slots][dim] holds the states before the first positions and gets the last ones, unless
+    state_out takes those.  carry (recurrence_carry) is filled for engram_recurrence_grad."""
+    L = _load()
+    dev = x.device
+    if state_out is None:
+        state_out = state
+    ty, T, D, xs, gs, n_seqs, n_slots, workspace = _recurrence_args(x, g, cu_seqlens, mask, state, state_out, slots,
+                                                                    workspace)
+    if y is None:
+        y = torch.empty((T, D), dtype=x.dtype, device=dev)
+    ys = _need_rows(y, "y", x.dtype, dev, T, D)
+    if carry is not None:
+        _need(carry, "carry", torch.float32, dev)
+        if carry.numel() * 4 < L.engram_recurrence_carry_bytes(T, D):
+            raise ValueError("carry is too small (recurrence_carry)")
+    _check(L.engram_recurrence(_ptr(x), xs, _ptr(g), gs, ty, T, D, _ptr(cu_seqlens), n_seqs, _ptr(slots), _ptr(mask),
+                               _ptr(state), _ptr(state_out), n_slots, _ptr(y), ys, _ptr(carry), _ptr(workspace),
+                               workspace.numel(), _ptr(status), _stream(dev)), "engram_recurrence")
+    return y
+
+
+def engram_recurrence_grad(dy: torch.Tensor, x: torch.Tensor, g: torch.Tensor, carry: torch.Tensor,
+                           cu_seqlens: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                           state: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                           dstate: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                           dg: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                           status: Optional[torch.Tensor] = None):
+    """The gradients (dx, dg) of engram_recurrence.  state: the states the forward call began with; dstate f32
+    [n_slots][dim]: the gradient of the last states, replaced by that of the first."""
+    L = _load()
+    dev = x.device
+    ty, T, D, xs, gs, n_seqs, n_slots, workspace = _recurrence_args(x, g, cu_seqlens, mask, state, dstate, slots,
+                                                                    workspace)
+    dys = _need_rows(dy, "dy", x.dtype, dev, T, D)
+    _need(carry, "carry", torch.float32, dev)
+    if carry.numel() * 4 < L.engram_recurrence_carry_bytes(T, D):
+        raise ValueError("carry is too small (recurrence_carry)")
+    if dx is None:
+        dx = torch.empty((T, D), dtype=x.dtype, device=dev)
+    if dg is None:
+        dg = torch.empty((T, D), dtype=x.dtype, device=dev)
+    dxs = _need_rows(dx, "dx", x.dtype, dev, T, D)
+    dgs = _need_rows(dg, "dg", x.dtype, dev, T, D)
+    _check(L.engram_recurrence_grad(_ptr(dy), dys, _ptr(x), xs, _ptr(g), gs, ty, T, D, _ptr(cu_seqlens), n_seqs,
+                                    _ptr(slots), _ptr(mask), _ptr(state), _ptr(carry), _ptr(dstate), n_slots,
+                                    _ptr(dx), dxs, _ptr(dg), dgs, _ptr(workspace), workspace.numel(), _ptr(status),
+                                    _stream(dev)), "engram_recurrence_grad")
+    return dx, dg
+
+
+def engram_recurrence_step(x: torch.Tensor, g: torch.Tensor, slots: torch.Tensor, state: torch.Tensor,
+                           state_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                           status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One position of every batch entry: x, g bf16 or f32 [B][dim], slots int32 [B] (-1: padding), state f32
+    [n_slots][dim] updated in place unless state_out takes the new states; returns y [B][dim]."""
+    L = _load()
+    dev = x.device
+    ty = _elem_type(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [B][dim]")
+    B, D = x.shape
+    xs = _need_rows(x, "x", x.dtype, dev, B, D)
+    gs = _need_rows(g, "g", x.dtype, dev, B, D)
+    _need(slots, "slots", torch.int32, dev, B)
+    if state_out is None:
+        state_out = state
+    _need(state, "state", torch.float32, dev)
+    if state.dim() != 2 or state.shape[1] != D:
+        raise ValueError("state must be [n_slots][dim]")
+    _need(state_out, "state_out", torch.float32, dev, state.numel())
+    if y is None:
+        y = torch.empty((B, D), dtype=x.dtype, device=dev)
+    ys = _need_rows(y, "y", x.dtype, dev, B, D)
+    _check(L.engram_recurrence_step(_ptr(x), xs, _ptr(g), gs, ty, B, D, _ptr(slots), _ptr(state), _ptr(state_out),
+                                    state.shape[0], _ptr(y), ys, _ptr(status), _stream(dev)),
+           "engram_recurrence_step")
+    return y
+
+
+def engram_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                   temperature: float = 1.0, weight: Optional[torch.Tensor] = None,
+                   teacher_lse: Optional[torch.Tensor] = None, loss: Optional[torch.Tensor] = None,
+                   dlogits: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Distillation loss of every position, f32 [T]: logits bf16 or f32 [T][vocab], the teacher's top entries as
+    ids int32 [T][K] (negative: unused) and logits f32 [T][K].  dlogits [T][vocab], when given, gets the gradient
+    (it may be logits itself)."""
+    L = _load()
+    dev = logits.device
+    ty = _elem_type(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T][vocab]")
+    T, V = logits.shape
+    zs = _need_rows(logits, "logits", logits.dtype, dev, T, V)
+    _need(teacher_ids, "teacher_ids", torch.int32, dev)
+    if teacher_ids.dim() != 2 or teacher_ids.shape[0] != T:
+        raise ValueError("teacher_ids must be [T][K]")
+    K = teacher_ids.shape[1]
+    _need(teacher_logits, "teacher_logits", torch.float32, dev, T * K)
+    if weight is not None:
+        _need(weight, "weight", torch.float32, dev, T)
+    if teacher_lse is not None:
+        _need(teacher_lse, "teacher_lse", torch.float32, dev, T)
+    if loss is None:
+        loss = torch.empty(T, dtype=torch.float32, device=dev)
+    _need(loss, "loss", torch.float32, dev, T)
+    ds = _need_rows(dlogits, "dlogits", logits.dtype, dev, T, V) if dlogits is not None else 0
+    _check(L.engram_distill(_ptr(logits), ty, T, V, zs, _ptr(teacher_ids), _ptr(teacher_logits), K, temperature,
+                            _ptr(teacher_lse), _ptr(weight), _ptr(loss), _ptr(dlogits), ds, _ptr(status),
+                            _stream(dev)), "engram_distill")
+    return loss
 
 
 # --------------------------------------------------------------------------- layer

@@ -593,6 +593,149 @@ int engram_project_gate_add_noalloc(const uint16_t* e_d, int64_t n_tokens, int64
                                     float* gate_out_d, int32_t* status_d, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Training: row lookup and its gradient                                      */
+/* ------------------------------------------------------------------------ */
+
+/* The pages describe the trained table (row-sharded, its gradients buffered
+ * between steps: [P-V41] §"196B 参数怎么存、怎么取"; [P-DETAIL] §8.1) and show no
+ * code for it.  The entry points from here to the kernel options are this
+ * library's own: what a memory layer with bf16 or fp32 rows needs in order to
+ * be trained, and the same operators' forms for serving. */
+
+/* Element types of the training operators. */
+enum { ENGRAM_T_BF16 = 0, ENGRAM_T_F32 = 1 };
+
+/* out[t][j*row_dim + c] = round(scale * table[row_ids[t][j]][c]), the product
+ * in fp32, rounded once to the element type.
+ *   table_d    [total_rows][row_dim] of `type`
+ *   row_ids_d  int32 [n_tokens][n_cols]; ENGRAM_DEAD gives zeros, any other id
+ *              outside [0, total_rows) gives zeros and sets ENGRAM_ST_BAD_ROW
+ *   out_d      [n_tokens][n_cols*row_dim] of `type`, rows out_stride elements
+ *              apart (>= n_cols*row_dim)
+ * Any row_dim >= 1 and element-aligned pointers; 16-byte aligned rows are the
+ * fast case.  total_rows < 2^31 - 1, n_tokens * n_cols < 2^31. */
+int engram_lookup(const void* table_d, int32_t type, int64_t total_rows, int32_t row_dim, const int32_t* row_ids_d,
+                  int64_t n_tokens, int32_t n_cols, float scale, void* out_d, int64_t out_stride, int32_t* status_d,
+                  void* stream);
+
+/* The gradient of engram_lookup with respect to the table.  With the entries
+ * i = t*n_cols + j:
+ *   G[r] = scale * sum_{i: row_ids[i] == r} dout[i]      (fp32)
+ * Entries are sorted by (id, i) and each row's sum is taken in a fixed order,
+ * so results are the same from run to run.  Ids without a row (as in
+ * engram_lookup) contribute nothing.
+ *   dout_d       [n_tokens][n_cols*row_dim] of `type`, rows dout_stride apart
+ *   workspace_d  engram_lookup_grad_workspace_bytes(...) bytes, 256-byte aligned
+ *
+ * engram_lookup_grad writes every row of grad_d, float32 [total_rows][row_dim]
+ * (a vocabulary-sized table).  engram_lookup_grad_rows, for tables too large
+ * for that, writes the distinct rows in ascending order, n = n_tokens*n_cols:
+ *   rows_d   int32 [n]            row ids, -1 after the last
+ *   grad_d   float32 [n][row_dim] their gradients, 0 after the last
+ *   count_d  int32 [1]            how many there are */
+size_t engram_lookup_grad_workspace_bytes(int64_t n_tokens, int32_t n_cols, int32_t row_dim);
+int engram_lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int32_t* row_ids_d,
+                       int64_t n_tokens, int32_t n_cols, int32_t row_dim, int64_t total_rows, float scale,
+                       float* grad_d, void* workspace_d, size_t workspace_bytes, int32_t* status_d, void* stream);
+int engram_lookup_grad_rows(const void* dout_d, int32_t type, int64_t dout_stride, const int32_t* row_ids_d,
+                            int64_t n_tokens, int32_t n_cols, int32_t row_dim, int64_t total_rows, float scale,
+                            int32_t* rows_d, float* grad_d, int32_t* count_d, void* workspace_d,
+                            size_t workspace_bytes, int32_t* status_d, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Gated linear recurrence                                                    */
+/* ------------------------------------------------------------------------ */
+
+/* Per channel of packed sequences, with f_t = sigmoid(g_t):
+ *   s_t = f_t s_{t-1} + (1 - f_t) x_t,   y_t = s_t
+ * the state in fp32 throughout, y rounded once.  It mixes a memory's values
+ * along the whole sequence where the short convolution sees a few positions.
+ * A masked position (mask_d[t] != 0) holds the state, gives y = 0 and takes no
+ * gradient, whatever its x and g hold.
+ *
+ *   x_d, g_d, y_d  [n_tokens][dim] of `type`, rows *_stride elements apart
+ *                  (x and g may be column ranges of one matrix)
+ *   cu_seqlens_d   int64 [n_seqs+1] as in engram_hash; sequences may be empty
+ *   slots_d        int32 [n_seqs] state slot per sequence, or NULL (slot = s);
+ *                  a negative slot is padding: its positions give y = 0 and it
+ *                  keeps no state; with a state, a slot >= n_slots sets
+ *                  ENGRAM_ST_BAD_SLOT and is padding too.  Slots of one call
+ *                  are distinct.
+ *   mask_d         uint8 [n_tokens] or NULL
+ *   state_d        float32 [n_slots][dim], the states before the first
+ *                  positions, or NULL (zeros)
+ *   state_out_d    float32 [n_slots][dim], the states after the last positions
+ *                  (an empty sequence's is its first), or NULL; may be state_d
+ *   carry_d        float32, engram_recurrence_carry_bytes(...) bytes, or NULL:
+ *                  for the backward pass, the state before every position that
+ *                  is a multiple of ENGRAM_RECURRENCE_TILE
+ *   workspace_d    engram_recurrence_workspace_bytes(...) bytes, 256-byte aligned
+ * Any dim >= 1 and element-aligned pointers; outputs overlap no input (but
+ * state_out_d may be state_d). */
+#define ENGRAM_RECURRENCE_TILE 128
+size_t engram_recurrence_carry_bytes(int64_t n_tokens, int32_t dim);
+size_t engram_recurrence_workspace_bytes(int64_t n_tokens, int32_t dim);
+int engram_recurrence(const void* x_d, int64_t x_stride, const void* g_d, int64_t g_stride, int32_t type,
+                      int64_t n_tokens, int32_t dim, const int64_t* cu_seqlens_d, int64_t n_seqs,
+                      const int32_t* slots_d, const uint8_t* mask_d, const float* state_d, float* state_out_d,
+                      int64_t n_slots, void* y_d, int64_t y_stride, float* carry_d, void* workspace_d,
+                      size_t workspace_bytes, int32_t* status_d, void* stream);
+
+/* The gradients of x, g and the first states.  With l the gradient of the state:
+ *   l_t = dy_t + f_{t+1} l_{t+1},  dx_t = l_t (1 - f_t),
+ *   dg_t = l_t (s_{t-1} - x_t) f_t (1 - f_t)
+ * The states are computed again from carry_d, which a forward call on the
+ * same arguments filled.
+ *   state_d   the states that the forward call began with, or NULL
+ *   dstate_d  float32 [n_slots][dim] in/out, or NULL (zeros in): the gradients
+ *             of the last states on entry, of the first states on return */
+int engram_recurrence_grad(const void* dy_d, int64_t dy_stride, const void* x_d, int64_t x_stride, const void* g_d,
+                           int64_t g_stride, int32_t type, int64_t n_tokens, int32_t dim,
+                           const int64_t* cu_seqlens_d, int64_t n_seqs, const int32_t* slots_d,
+                           const uint8_t* mask_d, const float* state_d, const float* carry_d, float* dstate_d,
+                           int64_t n_slots, void* dx_d, int64_t dx_stride, void* dg_d, int64_t dg_stride,
+                           void* workspace_d, size_t workspace_bytes, int32_t* status_d, void* stream);
+
+/* One position for each of `batch` sequences (decode): row b of x, g and y
+ * belongs to state slots_d[b]; a negative slot is padding (y = 0, no state), a
+ * slot >= n_slots sets ENGRAM_ST_BAD_SLOT and is padding.  state_out_d may be
+ * state_d, or another buffer that leaves the old states in place. */
+int engram_recurrence_step(const void* x_d, int64_t x_stride, const void* g_d, int64_t g_stride, int32_t type,
+                           int64_t batch, int32_t dim, const int32_t* slots_d, const float* state_d,
+                           float* state_out_d, int64_t n_slots, void* y_d, int64_t y_stride, int32_t* status_d,
+                           void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Distillation from a teacher's top logits                                   */
+/* ------------------------------------------------------------------------ */
+
+/* For a memory added to a trained model, whose own top logits teach it.  Per
+ * position, with q = softmax(z / tau) over the vocabulary, p_k the teacher's
+ * probability of its entry k and P = sum_k p_k:
+ *   loss = w tau^2 sum_k p_k (ln p_k - ln q_{id_k})
+ *   dz_v = w tau (P q_v - p_v)        (p_v summed over the entries of v)
+ * p is the softmax of teacher_logits / tau over the entries (P = 1), or with
+ * teacher_lse_d exp(teacher_logits / tau - teacher_lse), the teacher's
+ * probabilities over its whole vocabulary (P <= 1).
+ *   logits_d         [n_tokens][vocab] of `type`, rows logits_stride apart
+ *   teacher_ids_d    int32 [n_tokens][top]; a negative id is an unused entry,
+ *                    an id >= vocab is unused and sets ENGRAM_ST_BAD_TOKEN
+ *   teacher_logits_d float32 [n_tokens][top]
+ *   teacher_lse_d    float32 [n_tokens] (log-sum-exp of the teacher's logits / tau) or NULL
+ *   weight_d         float32 [n_tokens] or NULL (1)
+ *   loss_d           float32 [n_tokens]
+ *   dlogits_d        [n_tokens][vocab] of `type`, rows dlogits_stride apart, or
+ *                    NULL (loss alone); may be logits_d
+ * A position of weight 0, or without any teacher mass, gives loss 0 and a
+ * zero gradient whatever its logits hold.  A student logit of -inf has q = 0.
+ * top <= ENGRAM_DISTILL_MAX_TOP, temperature positive and finite. */
+#define ENGRAM_DISTILL_MAX_TOP 1024
+int engram_distill(const void* logits_d, int32_t type, int64_t n_tokens, int64_t vocab, int64_t logits_stride,
+                   const int32_t* teacher_ids_d, const float* teacher_logits_d, int32_t top, float temperature,
+                   const float* teacher_lse_d, const float* weight_d, float* loss_d, void* dlogits_d,
+                   int64_t dlogits_stride, int32_t* status_d, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Kernel selection                                                           */
 /* ------------------------------------------------------------------------ */
 
