@@ -667,10 +667,13 @@ int engram_lookup_grad_rows(const void* dout_d, int32_t type, int64_t dout_strid
  *   state_out_d    float32 [n_slots][dim], the states after the last positions
  *                  (an empty sequence's is its first), or NULL; may be state_d
  *   carry_d        float32, engram_recurrence_carry_bytes(...) bytes, or NULL:
- *                  for the backward pass, the state before every position that
- *                  is a multiple of ENGRAM_RECURRENCE_TILE
- *   workspace_d    engram_recurrence_workspace_bytes(...) bytes, 256-byte aligned
- * Any dim >= 1 and element-aligned pointers; outputs overlap no input (but
+ *                  for the backward pass, the state in front of every
+ *                  ENGRAM_RECURRENCE_TILE positions
+ *   workspace_d    engram_recurrence_workspace_bytes(...) bytes, 256-byte
+ *                  aligned; its contents on entry do not matter
+ * The scan runs in one pass over memory, its tiles joined by waits on tiles
+ * already running; a wait that runs out sets ENGRAM_ST_TIMEOUT.  The result is
+ * the same from run to run.  Any dim >= 1 and element-aligned pointers; outputs overlap no input (but
  * state_out_d may be state_d). */
 #define ENGRAM_RECURRENCE_TILE 128
 size_t engram_recurrence_carry_bytes(int64_t n_tokens, int32_t dim);
