@@ -5,8 +5,18 @@
 // probabilities at its K entries and P their sum:
 //   loss = w tau^2 sum_k p_k (ln p_k - ln q_k)
 //   dz_v = w tau (P q_v - p_v)
+//
+// A position's gradient needs its whole row's maximum and sum, so a row is
+// read once and kept: a cluster of 1 to 8 blocks holds it in shared memory
+// (bulk copies), exchanges its blocks' (maximum, sum) pairs through
+// distributed shared memory, and writes the gradient from the copy.  Memory
+// traffic is then the logits once and the gradient once.  Rows are split so
+// that a block's part is at most 72 KB where that is possible: three blocks
+// share an SM, so that one loads while another exchanges or writes.
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "engram_internal.h"
 #include "train_device.cuh"
@@ -15,19 +25,36 @@ namespace engram {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTop = ENGRAM_DISTILL_MAX_TOP;
+constexpr int kMaxCluster = 8;
+constexpr int kChunks = 4;                 // pieces of a part that are awaited one by one
+constexpr int kPartBytes = 72 * 1024;      // a part's size where the cluster can be made large enough
+constexpr int kPartLimit = 200 * 1024;     // beyond this in a cluster of 8 the row is read twice instead
 
 struct Args {
   int64_t vocab, z_stride, dz_stride;
   const int32_t* ids;
   const float* t;
-  int32_t top;
+  int32_t top, cluster;
   float tau;
   const float* lse;
   const float* weight;
   float* loss;
   int32_t* status;
 };
+
+struct Head {  // in front of the dynamic shared memory
+  uint64_t bar[kChunks];
+  float2 part[kMaxCluster];  // the blocks' (maximum, sum of exponentials relative to it)
+  float red[2 * kWarps];
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 // Sum or maximum over the block, the same in every thread and run.
 template <bool kMax>
@@ -42,94 +69,337 @@ __device__ float block_reduce(float v, float* red) {
   __syncthreads();
   v = red[0];
 #pragma unroll
-  for (int w = 1; w < kThreads / 32; ++w) v = kMax ? fmaxf(v, red[w]) : v + red[w];
+  for (int w = 1; w < kWarps; ++w) v = kMax ? fmaxf(v, red[w]) : v + red[w];
   return v;
 }
 
-// One block per position.
+// 16 bytes of a row: 8 bf16 or 4 fp32 values.
 template <class E>
-__global__ void __launch_bounds__(kThreads) distill_kernel(const typename E::T* __restrict__ z,
-                                                           typename E::T* dz, Args a) {
-  __shared__ float red[kThreads / 32];
-  __shared__ float p[kMaxTop];
-  __shared__ int32_t id[kMaxTop];
-  const int64_t row = blockIdx.x;
+constexpr int kVec = 16 / E::kBytes;
+
+__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+template <class E>
+__device__ __forceinline__ void widen(const uint4& x, float (&f)[kVec<E>]) {
+  if constexpr (E::kBytes == 2) {
+    f[0] = lo16(x.x); f[1] = hi16(x.x); f[2] = lo16(x.y); f[3] = hi16(x.y);
+    f[4] = lo16(x.z); f[5] = hi16(x.z); f[6] = lo16(x.w); f[7] = hi16(x.w);
+  } else {
+    f[0] = __uint_as_float(x.x); f[1] = __uint_as_float(x.y);
+    f[2] = __uint_as_float(x.z); f[3] = __uint_as_float(x.w);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+template <class E>
+__device__ __forceinline__ uint4 narrow(const float (&f)[kVec<E>]) {
+  if constexpr (E::kBytes == 2)
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+  else
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+
+// (m, s) <- the pair of both: sums of 2^((z - m) c), -inf maxima count nothing.
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float c) {
+  const float top = fmaxf(m, m2), at = top == -INFINITY ? 0.f : top;
+  s = s * ex2((m - at) * c) + s2 * ex2((m2 - at) * c);
+  m = top;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// One cluster of a.cluster blocks per position.  The row is handled in 16-byte
+// vectors counted from the aligned address at or before its first element
+// (`off` elements before it); vectors that reach over the row's ends are
+// filled up with -inf, which adds nothing to the sums.
+template <class E, bool kResident>
+__global__ void __launch_bounds__(kThreads, kResident ? 3 : 4) distill_kernel(const typename E::T* z,
+                                                                              typename E::T* dz, Args a) {
+  constexpr int N = kVec<E>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  Head& h = *reinterpret_cast<Head*>(smem);
+  float* p = reinterpret_cast<float*>(smem + sizeof(Head));
+  int32_t* id = reinterpret_cast<int32_t*>(p + a.top);
+  float* zk = reinterpret_cast<float*>(id + a.top);
+  uint4* row_s = reinterpret_cast<uint4*>(smem + ((sizeof(Head) + 12 * static_cast<size_t>(a.top) + 127) & ~size_t(127)));
+
+  const int tid = threadIdx.x;
+  const uint32_t rank = a.cluster > 1 ? cluster_rank() : 0u;
+  const int64_t row = blockIdx.x / a.cluster;
   const typename E::T* zr = z + row * a.z_stride;
   typename E::T* dr = dz + row * a.dz_stride;
+  const int V = static_cast<int>(a.vocab);
+  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(zr) & 15) / E::kBytes);
+  const int doff = static_cast<int>((reinterpret_cast<uintptr_t>(dr) & 15) / E::kBytes);
+  const int vecs = (V + off + N - 1) / N, per = (vecs + a.cluster - 1) / a.cluster;
+  const int v0 = static_cast<int>(rank) * per < vecs ? static_cast<int>(rank) * per : vecs;
+  const int v1 = v0 + per < vecs ? v0 + per : vecs;
+  const uint4* zv = reinterpret_cast<const uint4*>(zr - off);
+  // vectors wholly inside the row
+  const int in0 = off > 0 ? 1 : 0, in1 = (V + off) / N;
+
   const float w = a.weight != nullptr ? a.weight[row] : 1.f;
-  const float inv_tau = 1.f / a.tau;
+  if (w == 0.f) {  // nothing to learn here
+    if (rank == 0 && tid == 0) a.loss[row] = 0.f;
+    if (dz != nullptr) {
+      const int e0 = v0 * N - off > 0 ? v0 * N - off : 0, e1 = v1 * N - off < V ? v1 * N - off : V;
+      if (off == doff) {
+        for (int v = v0 + tid; v < v1; v += kThreads)
+          if (v >= in0 && v < in1) reinterpret_cast<uint4*>(dr - off)[v] = make_uint4(0u, 0u, 0u, 0u);
+        if (v0 == 0 && tid < N - off && off > 0 && tid < V) E::store(dr + tid, 0.f);
+        if (v1 == vecs && v0 < vecs && in1 < vecs && (in1 > 0 || off == 0) && in1 * N - off + tid < V)
+          E::store(dr + in1 * N - off + tid, 0.f);
+      } else {
+        for (int e = e0 + tid; e < e1; e += kThreads) E::store(dr + e, 0.f);
+      }
+    }
+    return;
+  }
+
+  // the row's values of a vector, -inf outside
+  auto edge = [&](int v) {
+    float f[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int e = v * N + j - off;
+      f[j] = e >= 0 && e < V ? E::load(zr + e) : -INFINITY;
+    }
+    return narrow<E>(f);
+  };
+  const int chunk = (v1 - v0 + kChunks - 1) / kChunks;
+  if (kResident) {
+    if (tid == 0) {
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) mbar_init(smem_u32(&h.bar[k]), 1);
+      fence_mbar_init();
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        int b0 = v0 + k * chunk, b1 = b0 + chunk < v1 ? b0 + chunk : v1;
+        b0 = b0 > in0 ? b0 : in0;
+        b1 = b1 < in1 ? b1 : in1;
+        const uint32_t bytes = b1 > b0 ? static_cast<uint32_t>(b1 - b0) * 16u : 0u;
+        mbar_arrive_expect_tx(smem_u32(&h.bar[k]), bytes);
+        if (bytes > 0) bulk_g2s(smem_u32(row_s + (b0 - v0)), zv + b0, bytes, smem_u32(&h.bar[k]));
+      }
+    }
+    if (tid == 32 && in0 > 0 && v0 == 0 && v1 > 0) row_s[0] = edge(0);
+    if (tid == 64 && in1 < vecs && v0 <= in1 && in1 < v1 && !(in1 == 0 && in0 > 0)) row_s[in1 - v0] = edge(in1);
+  }
+  __syncwarp();
+  if (a.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
   // the teacher's probabilities
+  const float inv_tau = 1.f / a.tau, c = 1.4426950408889634f * inv_tau;
   float top = -INFINITY;
-  for (int k = threadIdx.x; k < a.top; k += kThreads) {
+  for (int k = tid; k < a.top; k += kThreads) {
     int32_t v = a.ids[row * a.top + k];
     if (v >= a.vocab) {
       if (a.status != nullptr) atomicOr(a.status, ENGRAM_ST_BAD_TOKEN);
       v = -1;
     }
-    id[k] = v;
+    id[k] = v < 0 ? -1 : v;
     p[k] = v >= 0 ? a.t[row * a.top + k] * inv_tau : -INFINITY;
+    zk[k] = v >= 0 ? E::load(zr + v) : 0.f;
     top = fmaxf(top, p[k]);
   }
-  top = block_reduce<true>(top, red);
+  top = block_reduce<true>(top, h.red);  // (the first barrier after the mbarriers' and edges' stores)
   float norm = 0.f;
   if (a.lse != nullptr) {
     norm = a.lse[row];
   } else {
     float sum = 0.f;
-    for (int k = threadIdx.x; k < a.top; k += kThreads) sum += top == -INFINITY ? 0.f : expf(p[k] - top);
-    sum = block_reduce<false>(sum, red);
+    for (int k = tid; k < a.top; k += kThreads) sum += top == -INFINITY ? 0.f : expf(p[k] - top);
+    sum = block_reduce<false>(sum, h.red);
     norm = top == -INFINITY ? 0.f : top + logf(sum);
   }
   float mass = 0.f;
-  for (int k = threadIdx.x; k < a.top; k += kThreads) mass += expf(p[k] - norm);
-  mass = block_reduce<false>(mass, red);
-  if (w == 0.f || mass == 0.f) {  // nothing to learn here
-    if (threadIdx.x == 0) a.loss[row] = 0.f;
-    if (dz != nullptr)
-      for (int64_t v = threadIdx.x; v < a.vocab; v += kThreads) E::store(dr + v, 0.f);
-    return;
+  for (int k = tid; k < a.top; k += kThreads) mass += expf(p[k] - norm);
+  mass = block_reduce<false>(mass, h.red);
+
+  // the maximum and the sum of this block's part
+  float m = -INFINITY, s = 0.f;
+  auto add = [&](const uint4& x) {
+    float f[N], big;
+    widen<E>(x, f);
+    if constexpr (N == 8)
+      big = fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
+    else
+      big = fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));
+    if (big > m) {
+      s *= m == -INFINITY ? 0.f : ex2((m - big) * c);
+      m = big;
+    }
+    const float at = m == -INFINITY ? 0.f : -m;
+    uint64_t sum = f2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+      float x0, x1;
+      f2_split(f2_mul(f2_add(f2(f[j], f[j + 1]), f2(at, at)), f2(c, c)), x0, x1);
+      sum = f2_add(sum, f2(ex2(x0), ex2(x1)));
+    }
+    float s0, s1;
+    f2_split(sum, s0, s1);
+    s += s0 + s1;
+  };
+  bool late = false;
+  if (kResident) {
+#pragma unroll 1
+    for (int k = 0; k < kChunks; ++k) {
+      if (!mbar_wait_bounded(smem_u32(&h.bar[k]), 0, nullptr)) {
+        late = true;  // give the copy one more chance to land before the block goes on
+        mbar_wait_bounded(smem_u32(&h.bar[k]), 0, nullptr);
+      }
+      const int b0 = k * chunk, b1 = b0 + chunk < v1 - v0 ? b0 + chunk : v1 - v0;
+#pragma unroll 2
+      for (int v = b0 + tid; v < b1; v += kThreads) add(row_s[v]);
+    }
+  } else {
+#pragma unroll 4
+    for (int v = v0 + tid; v < v1; v += kThreads) add(v >= in0 && v < in1 ? zv[v] : edge(v));
+  }
+  if (late && a.status != nullptr) atomicOr(a.status, ENGRAM_ST_TIMEOUT);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    // both lanes of a pair join in the same order, so that they agree
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    const bool low = (tid & o) == 0;
+    float ma = low ? m : m2, sa = low ? s : s2;
+    join(ma, sa, low ? m2 : m, low ? s2 : s, c);
+    m = ma;
+    s = sa;
+  }
+  __syncthreads();
+  if ((tid & 31) == 0) {
+    h.red[tid >> 5] = m;
+    h.red[kWarps + (tid >> 5)] = s;
+  }
+  __syncthreads();
+  m = h.red[0];
+  s = h.red[kWarps];
+#pragma unroll
+  for (int k = 1; k < kWarps; ++k) join(m, s, h.red[k], h.red[kWarps + k], c);
+  if (a.cluster > 1) {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every block of the cluster runs
+    if (tid < a.cluster) {
+      uint32_t to;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(&h.part[rank])), "r"(tid));
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(m), "f"(s) : "memory");
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    m = h.part[0].x;
+    s = h.part[0].y;
+    for (int k = 1; k < a.cluster; ++k) join(m, s, h.part[k].x, h.part[k].y, c);
   }
 
-  float m = -INFINITY;
-  for (int64_t v = threadIdx.x; v < a.vocab; v += kThreads) m = fmaxf(m, E::load(zr + v));
-  m = block_reduce<true>(m, red);
-  float sum = 0.f;
-  for (int64_t v = threadIdx.x; v < a.vocab; v += kThreads) sum += expf((E::load(zr + v) - m) * inv_tau);
-  sum = block_reduce<false>(sum, red);
-  const float log_sum = logf(sum);
-
-  float loss = 0.f;
-  for (int k = threadIdx.x; k < a.top; k += kThreads) {
-    const float pk = expf(p[k] - norm);
-    if (pk > 0.f) loss += pk * ((p[k] - norm) - ((E::load(zr + id[k]) - m) * inv_tau - log_sum));
+  const bool none = mass == 0.f;
+  if (rank == 0) {
+    const float log_sum = logf(s);
+    float loss = 0.f;
+    for (int k = tid; k < a.top; k += kThreads) {
+      const float pk = expf(p[k] - norm);
+      if (pk > 0.f || pk != pk) loss += pk * ((p[k] - norm) - ((zk[k] - m) * inv_tau - log_sum));
+    }
+    loss = block_reduce<false>(loss, h.red);
+    if (tid == 0) a.loss[row] = none ? 0.f : w * a.tau * a.tau * loss;
   }
-  loss = block_reduce<false>(loss, red);
-  if (threadIdx.x == 0) a.loss[row] = w * a.tau * a.tau * loss;
   if (dz == nullptr) return;
 
-  const float scale = w * a.tau;
-  const float c = scale * mass / sum;
-  // the entries' gradients first: dz may be z itself
-  float mine[(kMaxTop + kThreads - 1) / kThreads];
+  const float scale = w * a.tau, coef = scale * mass / s;
+  auto grad = [&](const uint4& x, float (&f)[N]) {
+    widen<E>(x, f);
 #pragma unroll
-  for (int j = 0; j < (kMaxTop + kThreads - 1) / kThreads; ++j) {
-    const int k = threadIdx.x + j * kThreads;
-    mine[j] = 0.f;
-    if (k < a.top && id[k] >= 0) {
-      float pk = 0.f;
-      for (int i = 0; i < a.top; ++i) pk += id[i] == id[k] ? expf(p[i] - norm) : 0.f;  // an id given twice adds up
-      mine[j] = c * expf((E::load(zr + id[k]) - m) * inv_tau) - scale * pk;
+    for (int j = 0; j < N; j += 2) {
+      float x0, x1;
+      f2_split(f2_mul(f2_add(f2(f[j], f[j + 1]), f2(-m, -m)), f2(c, c)), x0, x1);
+      f2_split(f2_mul(f2(ex2(x0), ex2(x1)), f2(coef, coef)), f[j], f[j + 1]);
+      if (none) f[j] = f[j + 1] = 0.f;
     }
-  }
-  __syncthreads();
-  for (int64_t v = threadIdx.x; v < a.vocab; v += kThreads) E::store(dr + v, c * expf((E::load(zr + v) - m) * inv_tau));
-  __syncthreads();
+  };
+  const uint4* src = kResident ? row_s - v0 : zv;
+  if (off == doff) {
+    uint4* dv = reinterpret_cast<uint4*>(dr - off);
+#pragma unroll 2
+    for (int v = v0 + tid; v < v1; v += kThreads) {
+      const bool inside = v >= in0 && v < in1;
+      float f[N];
+      grad(kResident || inside ? src[v] : edge(v), f);
+      if (inside) {
+        __stcs(dv + v, narrow<E>(f));
+      } else {
 #pragma unroll
-  for (int j = 0; j < (kMaxTop + kThreads - 1) / kThreads; ++j) {
-    const int k = threadIdx.x + j * kThreads;
-    if (k < a.top && id[k] >= 0) E::store(dr + id[k], mine[j]);
+        for (int j = 0; j < N; ++j) {
+          const int e = v * N + j - off;
+          if (e >= 0 && e < V) E::store(dr + e, f[j]);
+        }
+      }
+    }
+  } else {  // the gradient's rows lie differently: value by value
+    const int e0 = v0 * N - off > 0 ? v0 * N - off : 0, e1 = v1 * N - off < V ? v1 * N - off : V;
+    const typename E::T* part = kResident ? reinterpret_cast<const typename E::T*>(row_s) + off - v0 * N : zr;
+    for (int e = e0 + tid; e < e1; e += kThreads)
+      E::store(dr + e, none ? 0.f : ex2((E::load(part + e) - m) * c) * coef);
   }
+  if (none) return;
+  // the entries' own gradients, over what was just written
+  __syncthreads();
+  for (int k = tid; k < a.top; k += kThreads) {
+    const int v = id[k] < 0 ? -1 : (id[k] + off) / N;
+    if (v < v0 || v >= v1) continue;
+    float pk = 0.f;
+    for (int i = 0; i < a.top; ++i) pk += id[i] == id[k] ? expf(p[i] - norm) : 0.f;  // an id given twice adds up
+    E::store(dr + id[k], ex2((zk[k] - m) * c) * coef - scale * pk);
+  }
+}
+
+template <class E, bool kResident>
+int launch(const void* z, void* dz, const Args& a, int64_t rows, size_t smem, cudaStream_t st) {
+  static std::atomic<uint64_t> attr_set{0};  // one bit per device: the shared-memory opt-in was made
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+  if (bit == 0 || !(attr_set.load(std::memory_order_relaxed) & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(distill_kernel<E, kResident>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kPartLimit + 16 * 1024);
+    if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    attr_set.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * a.cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(a.cluster);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, distill_kernel<E, kResident>, static_cast<const typename E::T*>(z),
+                                     static_cast<typename E::T*>(dz), a);
+  if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "distill_kernel launch: %s", cudaGetErrorString(e));
+  return check_launch("distill_kernel");
+}
+
+template <class E>
+int launch_distill(const void* z, void* dz, Args a, int64_t rows, cudaStream_t st) {
+  const int64_t bytes = a.vocab * E::kBytes + 16;  // with a misaligned row's first vector
+  a.cluster = 1;
+  while (a.cluster < kMaxCluster && bytes / a.cluster > kPartBytes) a.cluster *= 2;
+  const int64_t vecs = (bytes + 15) / 16, per = (vecs + a.cluster - 1) / a.cluster;
+  const size_t head = (sizeof(Head) + 12 * static_cast<size_t>(a.top) + 127) & ~size_t(127);
+  if (per * 16 <= kPartLimit) return launch<E, true>(z, dz, a, rows, head + static_cast<size_t>(per) * 16, st);
+  return launch<E, false>(z, dz, a, rows, head, st);
 }
 
 }  // namespace
@@ -144,8 +414,8 @@ extern "C" int engram_distill(const void* logits_d, int32_t type, int64_t n_toke
                               void* stream) {
   if (!train::known_type(type)) return fail(ENGRAM_E_INVALID, "type %d is not ENGRAM_T_BF16 or ENGRAM_T_F32", type);
   if (n_tokens < 0) return fail(ENGRAM_E_INVALID, "n_tokens < 0");
-  if (n_tokens > 0x7fffffff) return fail(ENGRAM_E_RANGE, "n_tokens must be below 2^31");
-  if (vocab < 1 || vocab > 0x7fffffff) return fail(ENGRAM_E_SHAPE, "vocab must be in [1, 2^31)");
+  if (n_tokens > 0x7fffffff / kMaxCluster) return fail(ENGRAM_E_RANGE, "n_tokens must be below 2^28");
+  if (vocab < 1 || vocab > 0x7fffff00) return fail(ENGRAM_E_SHAPE, "vocab must be in [1, 2^31 - 256]");
   if (top < 0 || top > kMaxTop) return fail(ENGRAM_E_SHAPE, "top %d not in [0, %d]", top, kMaxTop);
   if (!(temperature > 0.f) || temperature > 3.0e38f) return fail(ENGRAM_E_INVALID, "temperature must be positive and finite");
   if (logits_stride < vocab || (dlogits_d && dlogits_stride < vocab))
@@ -159,13 +429,8 @@ extern "C" int engram_distill(const void* logits_d, int32_t type, int64_t n_toke
     return fail(ENGRAM_E_SHAPE, "in place, dlogits has the stride of logits");
   int rc = check_device(nullptr);
   if (rc) return rc;
-  Args a{vocab, logits_stride, dlogits_stride, teacher_ids_d, teacher_logits_d, top, temperature, teacher_lse_d, weight_d,
-         loss_d, status_d};
-  if (type == ENGRAM_T_BF16)
-    distill_kernel<train::Bf16><<<static_cast<int>(n_tokens), kThreads, 0, as_stream(stream)>>>(
-        static_cast<const uint16_t*>(logits_d), static_cast<uint16_t*>(dlogits_d), a);
-  else
-    distill_kernel<train::F32><<<static_cast<int>(n_tokens), kThreads, 0, as_stream(stream)>>>(
-        static_cast<const float*>(logits_d), static_cast<float*>(dlogits_d), a);
-  return check_launch("distill_kernel");
+  Args a{vocab, logits_stride, dlogits_stride, teacher_ids_d, teacher_logits_d, top, 1, temperature, teacher_lse_d,
+         weight_d, loss_d, status_d};
+  return type == ENGRAM_T_BF16 ? launch_distill<train::Bf16>(logits_d, dlogits_d, a, n_tokens, as_stream(stream))
+                               : launch_distill<train::F32>(logits_d, dlogits_d, a, n_tokens, as_stream(stream));
 }

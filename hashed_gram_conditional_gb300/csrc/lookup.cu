@@ -42,56 +42,56 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const typename E::T* _
 
 // ---------------------------------------------------------------- sort by id
 
-constexpr int kItems = 16;                    // entries per thread
-constexpr int kChunk = kThreads * kItems;     // entries per block
-constexpr int kDigits = 256;
+constexpr int kItems = 16;                 // entries per thread
+constexpr int kBlock = kThreads * kItems;  // entries per block
+constexpr int kMaxDigits = 512;            // 9 bits a pass: 26-bit ids take three passes, 17-bit ids two
 
 __device__ __forceinline__ uint32_t entry_key(int32_t id, int64_t total_rows) {
   return id >= 0 && id < total_rows ? static_cast<uint32_t>(id) : static_cast<uint32_t>(total_rows);
 }
 
-// counts[block][digit] of one pass; `first` reads the ids themselves.
-__global__ void __launch_bounds__(kThreads) sort_count_kernel(const uint32_t* __restrict__ keys, bool first,
-                                                              int64_t total_rows, int32_t n, int shift,
-                                                              int32_t* __restrict__ counts, int32_t* status) {
-  __shared__ int32_t hist[kDigits];
-  hist[threadIdx.x] = 0;
+// counts[block][digit] of the first pass, from the ids themselves.
+__global__ void __launch_bounds__(kThreads) sort_count_kernel(const int32_t* __restrict__ ids, int64_t total_rows,
+                                                              int32_t n, int digits, int32_t* __restrict__ counts,
+                                                              int32_t* status) {
+  __shared__ int32_t hist[kMaxDigits];
+  for (int d = threadIdx.x; d < digits; d += kThreads) hist[d] = 0;
   __syncthreads();
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kChunk;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * kBlock;
   bool bad = false;
+#pragma unroll
   for (int k = 0; k < kItems; ++k) {
     const int64_t i = base + k * kThreads + threadIdx.x;
     if (i < n) {
-      uint32_t key = keys[i];
-      if (first) {
-        const int32_t id = static_cast<int32_t>(key);
-        bad |= id != ENGRAM_DEAD && (id < 0 || id >= total_rows);
-        key = entry_key(id, total_rows);
-      }
-      atomicAdd(&hist[(key >> shift) & (kDigits - 1)], 1);
+      const int32_t id = ids[i];
+      bad |= id != ENGRAM_DEAD && (id < 0 || id >= total_rows);
+      atomicAdd(&hist[entry_key(id, total_rows) & (digits - 1)], 1);
     }
   }
   if (bad && status != nullptr) atomicOr(status, ENGRAM_ST_BAD_ROW);
   __syncthreads();
-  counts[static_cast<int64_t>(blockIdx.x) * kDigits + threadIdx.x] = hist[threadIdx.x];
+  for (int d = threadIdx.x; d < digits; d += kThreads)
+    counts[static_cast<int64_t>(blockIdx.x) * digits + d] = hist[d];
 }
 
 // Moves each entry to its place: entries of smaller digits, entries of the
 // same digit in earlier blocks, earlier warps, earlier rounds and lower lanes
-// come before it, which keeps the pass stable.
+// come before it, which keeps the pass stable.  The next pass's counts are
+// taken on the way (integer sums: their order does not matter).
 __global__ void __launch_bounds__(kThreads) sort_move_kernel(const uint32_t* __restrict__ keys,
                                                              const int32_t* __restrict__ idx, bool first,
-                                                             int64_t total_rows, int32_t n, int shift,
+                                                             int64_t total_rows, int32_t n, int bits, int shift,
                                                              const int32_t* __restrict__ counts,
-                                                             uint32_t* __restrict__ keys_out,
+                                                             int32_t* __restrict__ next, uint32_t* __restrict__ keys_out,
                                                              int32_t* __restrict__ idx_out) {
-  __shared__ int32_t hist[kWarps][kDigits];
-  __shared__ int32_t totals[kDigits];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = threadIdx.x;
+  __shared__ int32_t hist[kWarps][kMaxDigits];
+  __shared__ int32_t totals[kMaxDigits];
+  const int digits = 1 << bits;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
+  for (int d = tid; d < digits; d += kThreads)
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) hist[w][d] = 0;
-  __syncthreads();
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kChunk + warp * (32 * kItems);
+    for (int w = 0; w < kWarps; ++w) hist[w][d] = 0;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * kBlock + warp * (32 * kItems);
   uint32_t key[kItems];
   int32_t rank[kItems];
 #pragma unroll
@@ -99,140 +99,401 @@ __global__ void __launch_bounds__(kThreads) sort_move_kernel(const uint32_t* __r
     const int64_t i = base + k * 32 + lane;
     key[k] = i < n ? keys[i] : 0u;
     if (first) key[k] = entry_key(static_cast<int32_t>(key[k]), total_rows);
-    const uint32_t digit = i < n ? (key[k] >> shift) & (kDigits - 1) : kDigits;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const bool in = base + k * 32 + lane < n;
+    const uint32_t digit = in ? (key[k] >> shift) & (digits - 1) : digits;
     const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-    int32_t before = 0;
-    if (i < n) before = hist[warp][digit];
+    const int32_t before = in ? hist[warp][digit] : 0;
     rank[k] = before + __popc(peers & ((1u << lane) - 1u));
     __syncwarp();
-    if (i < n && (peers >> lane) == 1u) hist[warp][digit] = before + __popc(peers);  // the highest lane of each digit
+    if (in && (peers >> lane) == 1u) hist[warp][digit] = before + __popc(peers);  // the highest lane of each digit
     __syncwarp();
   }
-  __syncthreads();
-  int32_t total = 0, prior = 0;
-  for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-    if (b == static_cast<int>(blockIdx.x)) prior = total;
-    total += counts[static_cast<int64_t>(b) * kDigits + d];
-  }
-  totals[d] = total;
-  __syncthreads();
-  for (int o = 1; o < kDigits; o <<= 1) {
-    const int32_t add = d >= o ? totals[d - o] : 0;
-    __syncthreads();
-    totals[d] += add;
-    __syncthreads();
-  }
-  int32_t at = totals[d] - total + prior;
+  // per digit: its entries in all blocks and in the blocks before this one
+  int32_t total[kMaxDigits / kThreads], prior[kMaxDigits / kThreads];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int32_t c = hist[w][d];
-    hist[w][d] = at;
-    at += c;
+  for (int j = 0; j < kMaxDigits / kThreads; ++j) {
+    const int d = tid + j * kThreads;
+    total[j] = prior[j] = 0;
+    if (d < digits) {
+#pragma unroll 8
+      for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
+        const int32_t c = __ldg(counts + static_cast<int64_t>(b) * digits + d);
+        total[j] += c;
+        prior[j] += b < static_cast<int>(blockIdx.x) ? c : 0;
+      }
+      totals[d] = total[j];
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {  // exclusive sums over the digits
+    int32_t run = 0;
+    for (int d0 = 0; d0 < digits; d0 += 32) {
+      const int32_t c = d0 + lane < digits ? totals[d0 + lane] : 0;
+      int32_t x = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (d0 + lane < digits) totals[d0 + lane] = run + x - c;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kMaxDigits / kThreads; ++j) {
+    const int d = tid + j * kThreads;
+    if (d < digits) {
+      int32_t at = totals[d] + prior[j];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const int32_t c = hist[w][d];
+        hist[w][d] = at;
+        at += c;
+      }
+    }
   }
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     const int64_t i = base + k * 32 + lane;
     if (i < n) {
-      const int32_t to = hist[warp][(key[k] >> shift) & (kDigits - 1)] + rank[k];
+      const int32_t to = hist[warp][(key[k] >> shift) & (digits - 1)] + rank[k];
       keys_out[to] = key[k];
       idx_out[to] = first ? static_cast<int32_t>(i) : idx[i];
+      if (next != nullptr)
+        atomicAdd(next + static_cast<int64_t>(to / kBlock) * digits + ((key[k] >> (shift + bits)) & (digits - 1)), 1);
     }
   }
 }
 
 // ------------------------------------------------------- segments of equal id
 
-constexpr int kSegItems = 4;
-constexpr int kSegChunk = kThreads * kSegItems;
+// The sorted entries are summed in chunks of kChunk: equal work however long
+// or short the segments are.  A segment inside its chunk goes straight to the
+// result; one that crosses a border leaves a part in each chunk it touches,
+// and the parts are joined in order afterwards.
+constexpr int kChunk = 64;
 
 __device__ __forceinline__ bool is_head(const uint32_t* keys, int64_t i, int32_t n, uint32_t none) {
   return i < n && keys[i] != none && (i == 0 || keys[i] != keys[i - 1]);
 }
 
-__global__ void __launch_bounds__(kThreads) seg_count_kernel(const uint32_t* __restrict__ keys, int32_t n,
-                                                             uint32_t none, int32_t* __restrict__ counts) {
-  int32_t c = 0;
-  for (int k = 0; k < kSegItems; ++k)
-    c += is_head(keys, static_cast<int64_t>(blockIdx.x) * kSegChunk + threadIdx.x * kSegItems + k, n, none);
-  __shared__ int32_t sum;
-  if (threadIdx.x == 0) sum = 0;
-  __syncthreads();
-  atomicAdd(&sum, c);
-  __syncthreads();
-  if (threadIdx.x == 0) counts[blockIdx.x] = sum;
-}
-
-// start[s] = first entry of segment s, row[s] its id; start[count] = entries
-// with a row; rows past the count get -1.
-__global__ void __launch_bounds__(kThreads) seg_write_kernel(const uint32_t* __restrict__ keys, int32_t n,
-                                                             uint32_t none, const int32_t* __restrict__ counts,
-                                                             int32_t* __restrict__ start, int32_t* __restrict__ row,
-                                                             int32_t* __restrict__ count) {
-  __shared__ int32_t scan[kThreads];
-  __shared__ int32_t base, all;
-  const int t = threadIdx.x;
-  if (t == 0) base = all = 0;
-  __syncthreads();
-  int32_t before = 0, whole = 0;
-  for (int b = t; b < static_cast<int>(gridDim.x); b += kThreads) {
-    const int32_t c = counts[b];
-    whole += c;
-    if (b < static_cast<int>(blockIdx.x)) before += c;
+// base[chunk] = segments that begin before it, *count = all of them; one
+// thread per chunk of heads, then the last block to finish sums them up.
+__global__ void __launch_bounds__(kThreads) seg_base_kernel(const uint32_t* __restrict__ keys, int32_t n, uint32_t none,
+                                                            int32_t chunks, int32_t* base, int32_t* done,
+                                                            int32_t* count) {
+  __shared__ int32_t warp_sum[kWarps];
+  __shared__ int32_t run;
+  __shared__ bool last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int64_t c = static_cast<int64_t>(blockIdx.x) * kWarps + warp; c < chunks;
+       c += static_cast<int64_t>(gridDim.x) * kWarps) {
+    int32_t heads = 0;
+#pragma unroll
+    for (int k = 0; k < kChunk; k += 32)
+      heads += __popc(__ballot_sync(0xffffffffu, is_head(keys, c * kChunk + k + lane, n, none)));
+    if (lane == 0) __stcg(base + c, heads);
   }
-  atomicAdd(&base, before);
-  atomicAdd(&all, whole);
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSegChunk + t * kSegItems;
-  int32_t c = 0;
-  for (int k = 0; k < kSegItems; ++k) c += is_head(keys, i0 + k, n, none);
-  scan[t] = c;
+  __threadfence();
   __syncthreads();
-  for (int o = 1; o < kThreads; o <<= 1) {
-    const int32_t add = t >= o ? scan[t - o] : 0;
-    __syncthreads();
-    scan[t] += add;
-    __syncthreads();
+  if (threadIdx.x == 0) {
+    last = atomicAdd(done, 1) == static_cast<int>(gridDim.x) - 1;
+    run = 0;
   }
-  int32_t s = base + scan[t] - c;
-  for (int k = 0; k < kSegItems; ++k) {
-    const int64_t i = i0 + k;
-    if (is_head(keys, i, n, none)) {
-      start[s] = static_cast<int32_t>(i);
-      row[s] = static_cast<int32_t>(keys[i]);
-      ++s;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  constexpr int kPer = 8;
+  for (int c0 = 0; c0 < chunks; c0 += kThreads * kPer) {
+    int32_t v[kPer], sum = 0;
+    const int at = c0 + threadIdx.x * kPer;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      v[k] = at + k < chunks ? __ldcg(base + at + k) : 0;
+      sum += v[k];
     }
-    if (i < n && i >= all) row[i] = -1;
-    // the first entry without a row ends the last segment
-    if (i < n && keys[i] == none && (i == 0 || keys[i - 1] != none)) start[all] = static_cast<int32_t>(i);
-    if (i == n - 1 && keys[i] != none) start[all] = n;
+    int32_t x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int32_t before = run, whole = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      before += w < warp ? warp_sum[w] : 0;
+      whole += warp_sum[w];
+    }
+    before += x - sum;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (at + k < chunks) base[at + k] = before;
+      before += v[k];
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) run += whole;
+    __syncthreads();
   }
-  if (blockIdx.x == 0 && t == 0) *count = all;
+  if (threadIdx.x == 0) *count = run;
 }
 
-// One warp per segment and 32-column step: the sum over the segment's entries.
+// 8 bf16 or 4 fp32 columns of a row per lane.  Aligned rows are read 16 bytes
+// a lane; others column by column, the lanes next to one another.
 template <class E>
-__global__ void __launch_bounds__(kThreads) seg_sum_kernel(const typename E::T* __restrict__ dout, int64_t dout_stride,
-                                                           int32_t dim, int32_t n_cols, int32_t n, float scale,
-                                                           const int32_t* __restrict__ idx,
-                                                           const int32_t* __restrict__ start,
-                                                           const int32_t* __restrict__ row,
-                                                           const int32_t* __restrict__ count, bool dense,
-                                                           float* __restrict__ grad) {
-  const int lane = threadIdx.x & 31;
-  const int64_t nw = static_cast<int64_t>(gridDim.x) * kWarps;
-  const int32_t segs = *count;
-  for (int64_t s = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); s < n; s += nw) {
-    if (s >= segs && dense) break;
-    const int32_t a = s < segs ? start[s] : 0, b = s < segs ? start[s + 1] : 0;
-    float* o = grad + (dense ? static_cast<int64_t>(row[s]) : s) * dim;
-    for (int c = lane; c < dim; c += 32) {
-      float sum = 0.f;
-      for (int32_t k = a; k < b; ++k) {
-        const int32_t i = idx[k];
-        const int32_t t = i / n_cols;
-        sum += E::load(dout + t * dout_stride + static_cast<int64_t>(i - t * n_cols) * dim + c);
+constexpr int kCols = 16 / E::kBytes;
+
+template <class E, bool kAligned>
+__device__ __forceinline__ int col_of(int j, int lane, int lanes) {
+  return kAligned ? lane * kCols<E> + j : j * lanes + lane;
+}
+
+template <class E, bool kAligned>
+__device__ __forceinline__ uint4 load_cols(const typename E::T* row, int c0, int lane, int lanes, int dim) {
+  uint4 r = make_uint4(0u, 0u, 0u, 0u);
+  if constexpr (kAligned) {
+    const int c = c0 + lane * kCols<E>;
+    if (c < dim) r = __ldg(reinterpret_cast<const uint4*>(row + c));
+  } else {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < kCols<E>; ++j) {
+      const int c = c0 + j * lanes + lane;
+      if (c < dim) {
+        if constexpr (E::kBytes == 2) w[j / 2] |= static_cast<uint32_t>(row[c]) << (16 * (j & 1));
+        else w[j] = __float_as_uint(row[c]);
       }
-      o[c] = scale * sum;
+    }
+    r = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return r;
+}
+
+template <class E>
+__device__ __forceinline__ void add_cols(const uint4& x, float (&acc)[kCols<E>]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int j = 0; j < kCols<E>; ++j) {
+    if constexpr (E::kBytes == 2) acc[j] += __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    else acc[j] += __uint_as_float(w[j]);
+  }
+}
+
+// fp32 rows of results and parts.
+template <class E, bool kAligned>
+__device__ __forceinline__ void store_cols(float* row, int c0, int lane, int lanes, int dim, float scale,
+                                           const float (&v)[kCols<E>]) {
+  if constexpr (kAligned) {
+    const int c = c0 + lane * kCols<E>;
+    if (c < dim) {
+#pragma unroll
+      for (int j = 0; j < kCols<E>; j += 4)
+        *reinterpret_cast<float4*>(row + c + j) =
+            make_float4(scale * v[j], scale * v[j + 1], scale * v[j + 2], scale * v[j + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kCols<E>; ++j) {
+      const int c = c0 + j * lanes + lane;
+      if (c < dim) row[c] = scale * v[j];
+    }
+  }
+}
+
+constexpr int kMaxRange = 256;  // rows that a block clears at a time, at most
+
+template <class E>
+struct SumArgs {
+  const typename E::T* dout;
+  int64_t dout_stride;
+  int32_t dim, n_cols, n, chunks, tiles;  // tiles of a row's columns
+  float scale;
+  const uint32_t* keys;
+  const int32_t* idx;
+  uint32_t none;
+  bool dense, contiguous;
+  const int32_t* base;   // rows form: segments before each chunk
+  const int32_t* count;  // rows form
+  int64_t total_rows;    // dense form
+  int32_t range;         // dense form: rows that a block clears at a time
+  float* grad;
+  int32_t* rows;
+  float *head, *tail;    // [chunk][dim]: the parts of a segment from before, of one that goes on
+};
+
+template <class E>
+__device__ __forceinline__ const typename E::T* entry_row(const SumArgs<E>& a, int32_t i) {
+  if (a.contiguous) return a.dout + static_cast<int64_t>(i) * a.dim;
+  const int32_t t = i / a.n_cols;
+  return a.dout + t * a.dout_stride + static_cast<int64_t>(i - t * a.n_cols) * a.dim;
+}
+
+__device__ __forceinline__ void zero_row(float* row, int32_t dim, int lane) {
+  if ((reinterpret_cast<uintptr_t>(row) & 15) == 0 && dim % 4 == 0) {
+    for (int c = lane * 4; c < dim; c += 128) __stcs(reinterpret_cast<float4*>(row + c), make_float4(0.f, 0.f, 0.f, 0.f));
+  } else {
+    for (int c = lane; c < dim; c += 32) row[c] = 0.f;
+  }
+}
+
+// kLanes lanes handle one (chunk, tile of kLanes * kCols columns).  When its
+// chunks are done, a block fills its share of the rows that no entry names.
+template <class E, int kLanes, bool kAligned>
+__global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
+  constexpr int N = kCols<E>, kGroups = kThreads / kLanes, kAhead = kAligned ? 8 : 4;
+  const int lane = threadIdx.x % kLanes;
+  const int64_t tasks = static_cast<int64_t>(a.chunks) * a.tiles;
+  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / kLanes; task < tasks;
+       task += static_cast<int64_t>(gridDim.x) * kGroups) {
+    const int32_t chunk = static_cast<int32_t>(task / a.tiles), tile = static_cast<int32_t>(task - static_cast<int64_t>(chunk) * a.tiles);
+    const int c0 = tile * kLanes * N;
+    const int32_t e0 = chunk * kChunk, e1 = a.n - e0 < kChunk ? a.n : e0 + kChunk;
+    uint32_t key = a.keys[e0];
+    if (key == a.none) continue;  // sorted: none of the chunk's entries has a row
+    bool from_before = e0 > 0 && a.keys[e0 - 1] == key;
+    int32_t seg = a.dense ? 0 : a.base[chunk];
+    if (from_before) --seg;
+    float acc[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] = 0.f;
+    for (int32_t e = e0; e < e1; e += kAhead) {
+      uint4 x[kAhead];
+      uint32_t after[kAhead];  // the next entry's key
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        x[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (e + k < e1) x[k] = load_cols<E, kAligned>(entry_row(a, __ldg(a.idx + e + k)), c0, lane, kLanes, a.dim);
+        after[k] = e + k + 1 < a.n ? __ldg(a.keys + e + k + 1) : a.none;
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (e + k >= e1 || key == a.none) break;
+        add_cols<E>(x[k], acc);
+        const bool ends = after[k] != key, border = e + k + 1 == e1;
+        if (ends || border) {
+          if (from_before) {
+            store_cols<E, kAligned>(a.head + static_cast<int64_t>(chunk) * a.dim, c0, lane, kLanes, a.dim, 1.f, acc);
+          } else if (!ends) {
+            store_cols<E, kAligned>(a.tail + static_cast<int64_t>(chunk) * a.dim, c0, lane, kLanes, a.dim, 1.f, acc);
+            if (!a.dense && tile == 0 && lane == 0) a.rows[seg] = static_cast<int32_t>(key);
+          } else {
+            store_cols<E, kAligned>(a.grad + (a.dense ? static_cast<int64_t>(key) : seg) * a.dim, c0, lane, kLanes, a.dim,
+                                    a.scale, acc);
+            if (!a.dense && tile == 0 && lane == 0) a.rows[seg] = static_cast<int32_t>(key);
+          }
+#pragma unroll
+          for (int j = 0; j < N; ++j) acc[j] = 0.f;
+          if (ends) ++seg;
+          from_before = false;
+          key = after[k];
+        }
+      }
+    }
+  }
+
+  const int wl = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (!a.dense) {
+    const int32_t segs = *a.count;
+    for (int64_t s = segs + static_cast<int64_t>(blockIdx.x) * kWarps + warp; s < a.n;
+         s += static_cast<int64_t>(gridDim.x) * kWarps) {
+      if (wl == 0) a.rows[s] = -1;
+      zero_row(a.grad + s * a.dim, a.dim, wl);
+    }
+    return;
+  }
+  // ranges of rows: the entries of a range are neighbours in the sorted order,
+  // their rows are marked, the others are cleared
+  const int kRange = a.range;
+  __shared__ uint32_t named[kMaxRange / 32];
+  __shared__ int32_t start;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRange; r0 < a.total_rows;
+       r0 += static_cast<int64_t>(gridDim.x) * kRange) {
+    if (threadIdx.x < kRange / 32) named[threadIdx.x] = 0u;
+    if (warp == 0) {  // the first entry of row r0 or a later one, 32 probes at a time
+      int32_t lo = 0, hi = a.n;
+      while (hi > lo) {
+        const int32_t step = (hi - lo + 31) / 32, q = lo + step * wl;
+        const int k = __popc(__ballot_sync(0xffffffffu, q < hi && q >= lo && a.keys[q] < r0));
+        if (k == 0) break;
+        hi = step * k < hi - lo ? lo + step * k : hi;
+        lo = lo + step * (k - 1) + 1;
+      }
+      if (wl == 0) start = lo;
+    }
+    __syncthreads();
+    for (int32_t e = start + threadIdx.x;; e += kThreads) {
+      const bool in = e < a.n && e >= 0 && a.keys[e] < r0 + kRange && a.keys[e] != a.none;
+      if (in) atomicOr(&named[(a.keys[e] - r0) >> 5], 1u << ((a.keys[e] - r0) & 31));
+      if (!__syncthreads_or(in)) break;
+    }
+    for (int r = warp; r < kRange && r0 + r < a.total_rows; r += kWarps)
+      if (!(named[r >> 5] >> (r & 31) & 1u)) zero_row(a.grad + (r0 + r) * a.dim, a.dim, wl);
+    __syncthreads();
+  }
+}
+
+// Joins the parts of the segments that cross chunks: one block per chunk in
+// which such a segment begins and tile of columns.  Warp w adds the parts of
+// the chunks w, w + 8, ... after it, then the warps' sums are added in order.
+template <class E, bool kAligned>
+__global__ void __launch_bounds__(kThreads) seg_join_kernel(SumArgs<E> a) {
+  constexpr int N = kCols<E>;
+  __shared__ float sums[kWarps][32 * N];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int32_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
+    const int32_t e0 = chunk * kChunk, e1 = e0 + kChunk;
+    if (e1 >= a.n) return;
+    const uint32_t key = a.keys[e1 - 1];
+    // begins here and goes on
+    if (key == a.none || a.keys[e1] != key || (e0 > 0 && a.keys[e0 - 1] == key)) continue;
+    // chunks after this one that the segment reaches into
+    int32_t more = 0;
+    while (true) {
+      const int64_t q = e1 + static_cast<int64_t>(more + lane) * kChunk;
+      const uint32_t in = __ballot_sync(0xffffffffu, q < a.n && a.keys[q] == key);
+      more += in == 0xffffffffu ? 32 : __ffs(~in) - 1;
+      if (in != 0xffffffffu) break;
+    }
+    int32_t seg = 0;
+    if (!a.dense) {  // the last segment that begins in this chunk
+      int32_t heads = 0;
+#pragma unroll
+      for (int k = 0; k < kChunk; k += 32)
+        heads += __popc(__ballot_sync(0xffffffffu, is_head(a.keys, static_cast<int64_t>(e0) + k + lane, a.n, a.none)));
+      seg = a.base[chunk] + heads - 1;
+    }
+    float* out = a.grad + (a.dense ? static_cast<int64_t>(key) : seg) * a.dim;
+    for (int c0 = blockIdx.y * 32 * N; c0 < a.dim; c0 += gridDim.y * 32 * N) {
+      float acc[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] = 0.f;
+#pragma unroll 4
+      for (int32_t k = warp; k <= more; k += kWarps) {
+        const float* part = k == 0 ? a.tail + static_cast<int64_t>(chunk) * a.dim
+                                   : a.head + static_cast<int64_t>(chunk + k) * a.dim;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const int c = c0 + j * 32 + lane;
+          if (c < a.dim) acc[j] += part[c];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) sums[warp][j * 32 + lane] = acc[j];
+      __syncthreads();
+      for (int c = threadIdx.x; c < 32 * N; c += kThreads) {
+        float s = sums[0][c];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) s += sums[w][c];
+        if (c0 + c < a.dim) out[c0 + c] = a.scale * s;
+      }
+      __syncthreads();
     }
   }
 }
@@ -249,36 +510,66 @@ int check_lookup(int32_t type, int64_t total_rows, int32_t row_dim, int64_t n_to
   return ENGRAM_OK;
 }
 
-// The parts of the gradient's workspace.
+// The parts of the gradient's workspace.  The counts of the passes after the
+// first and the counter are zeroed before each call.
 struct GradSpace {
   uint32_t* key[2];
   int32_t* idx[2];
-  int32_t* start;
-  int32_t* row;
+  int32_t* base;
+  int32_t* done;
   int32_t* counts;
-  int32_t* count;
+  float *head, *tail;
   size_t bytes;
 };
 
-GradSpace grad_space(void* base, int64_t n) {
+constexpr int kMaxPasses = 4;
+
+GradSpace grad_space(void* at, int64_t n, int32_t dim) {
   GradSpace s;
-  char* p = static_cast<char*>(base);
-  size_t at = 0;
+  char* p = static_cast<char*>(at);
+  size_t used = 0;
   auto take = [&](size_t bytes) {
-    char* q = p + at;
-    at += round256(bytes);
+    char* q = p + used;
+    used += round256(bytes);
     return q;
   };
-  const size_t words = static_cast<size_t>(n + 1) * 4;
+  const size_t words = static_cast<size_t>(n) * 4;
+  const size_t chunks = static_cast<size_t>((n + kChunk - 1) / kChunk);
   for (int k = 0; k < 2; ++k) s.key[k] = reinterpret_cast<uint32_t*>(take(words));
   for (int k = 0; k < 2; ++k) s.idx[k] = reinterpret_cast<int32_t*>(take(words));
-  s.start = reinterpret_cast<int32_t*>(take(words));
-  s.row = reinterpret_cast<int32_t*>(take(words));
-  const size_t blocks = static_cast<size_t>((n + kChunk - 1) / kChunk);
-  s.counts = reinterpret_cast<int32_t*>(take(blocks * kDigits * 4));
-  s.count = reinterpret_cast<int32_t*>(take(4));
-  s.bytes = at;
+  s.base = reinterpret_cast<int32_t*>(take(chunks * 4));
+  s.head = reinterpret_cast<float*>(take(chunks * dim * 4));
+  s.tail = reinterpret_cast<float*>(take(chunks * dim * 4));
+  const size_t blocks = static_cast<size_t>((n + kBlock - 1) / kBlock);
+  s.done = reinterpret_cast<int32_t*>(take((1 + blocks * kMaxDigits * kMaxPasses) * 4));
+  s.counts = s.done + 1;
+  s.bytes = used;
   return s;
+}
+
+// kLanes: the smallest power of two of lanes that covers a narrow row.
+template <class E, bool kAligned>
+int launch_sums(const SumArgs<E>& a0, int sms, cudaStream_t st) {
+  SumArgs<E> a = a0;
+  int lanes = 32;
+  while (lanes > 4 && (lanes / 2) * kCols<E> >= a.dim) lanes /= 2;
+  a.tiles = (a.dim + lanes * kCols<E> - 1) / (lanes * kCols<E>);
+  const int64_t groups = kThreads / lanes, want = (static_cast<int64_t>(a.chunks) * a.tiles + groups - 1) / groups;
+  const int64_t fill = static_cast<int64_t>(sms) * 4;
+  int64_t blocks = want > fill ? want : fill;
+  if (blocks > 0x7fffffff) blocks = 0x7fffffff;
+  const int g = static_cast<int>(blocks);
+  switch (lanes) {
+    case 32: seg_sum_kernel<E, 32, kAligned><<<g, kThreads, 0, st>>>(a); break;
+    case 16: seg_sum_kernel<E, 16, kAligned><<<g, kThreads, 0, st>>>(a); break;
+    case 8: seg_sum_kernel<E, 8, kAligned><<<g, kThreads, 0, st>>>(a); break;
+    default: seg_sum_kernel<E, 4, kAligned><<<g, kThreads, 0, st>>>(a); break;
+  }
+  if (a.chunks > 1) {
+    const int ty = (a.dim + 32 * kCols<E> - 1) / (32 * kCols<E>);
+    seg_join_kernel<E, kAligned><<<dim3(a.chunks, ty < 65535 ? ty : 65535), kThreads, 0, st>>>(a);
+  }
+  return check_launch("lookup gradient");
 }
 
 int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int32_t* ids_d, int64_t n_tokens,
@@ -301,45 +592,65 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
     return fail(ENGRAM_E_RANGE, "workspace too small");
   int sms = 0;
   if ((rc = check_device(&sms))) return rc;
-  if (dense) cudaMemsetAsync(grad_d, 0, static_cast<size_t>(total_rows) * row_dim * 4, st);
   if (n == 0) {
-    if (!dense) cudaMemsetAsync(count_d, 0, 4, st);
+    if (dense) cudaMemsetAsync(grad_d, 0, static_cast<size_t>(total_rows) * row_dim * 4, st);
+    else cudaMemsetAsync(count_d, 0, 4, st);
     return check_launch("lookup gradient");
   }
-  GradSpace w = grad_space(workspace_d, n);
-  if (dense) {
-    rows_d = w.row;
-    count_d = w.count;
-  }
-  int bits = 0;
-  while ((total_rows >> bits) != 0) ++bits;
-  const int passes = bits == 0 ? 1 : (bits + 7) / 8;
-  const int blocks = (n + kChunk - 1) / kChunk;
+  const GradSpace w = grad_space(workspace_d, n, row_dim);
+  int width = 1;  // bits of the keys, total_rows standing for "no row"
+  while ((total_rows >> width) != 0) ++width;
+  const int passes = (width + 8) / 9, bits = (width + passes - 1) / passes, digits = 1 << bits;
+  const int blocks = (n + kBlock - 1) / kBlock;
+  const size_t per = static_cast<size_t>(blocks) * digits;
+  cudaError_t err = cudaMemsetAsync(w.done, 0, (1 + per * passes) * 4, st);
+  if (err != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(err));
+  sort_count_kernel<<<blocks, kThreads, 0, st>>>(ids_d, total_rows, n, digits, w.counts, status_d);
   const uint32_t* kin = reinterpret_cast<const uint32_t*>(ids_d);
   const int32_t* iin = nullptr;
   for (int p = 0; p < passes; ++p) {
-    const bool first = p == 0;
-    sort_count_kernel<<<blocks, kThreads, 0, st>>>(kin, first, total_rows, n, 8 * p, w.counts, status_d);
-    sort_move_kernel<<<blocks, kThreads, 0, st>>>(kin, iin, first, total_rows, n, 8 * p, w.counts, w.key[p & 1],
+    sort_move_kernel<<<blocks, kThreads, 0, st>>>(kin, iin, p == 0, total_rows, n, bits, bits * p, w.counts + p * per,
+                                                  p + 1 < passes ? w.counts + (p + 1) * per : nullptr, w.key[p & 1],
                                                   w.idx[p & 1]);
     kin = w.key[p & 1];
     iin = w.idx[p & 1];
   }
-  const int sblocks = (n + kSegChunk - 1) / kSegChunk;
+  const int32_t chunks = (n + kChunk - 1) / kChunk;
   const uint32_t none = static_cast<uint32_t>(total_rows);
-  seg_count_kernel<<<sblocks, kThreads, 0, st>>>(kin, n, none, w.counts);
-  seg_write_kernel<<<sblocks, kThreads, 0, st>>>(kin, n, none, w.counts, w.start, rows_d, count_d);
-  const int64_t want = (n64 + kWarps - 1) / kWarps, cap = static_cast<int64_t>(sms) * 8;
-  const int gblocks = static_cast<int>(want < cap ? want : cap);
-  if (type == ENGRAM_T_BF16)
-    seg_sum_kernel<train::Bf16><<<gblocks, kThreads, 0, st>>>(static_cast<const uint16_t*>(dout_d), dout_stride,
-                                                              row_dim, n_cols, n, scale, iin, w.start, rows_d, count_d,
-                                                              dense, grad_d);
-  else
-    seg_sum_kernel<train::F32><<<gblocks, kThreads, 0, st>>>(static_cast<const float*>(dout_d), dout_stride, row_dim,
-                                                             n_cols, n, scale, iin, w.start, rows_d, count_d, dense,
-                                                             grad_d);
-  return check_launch("lookup gradient");
+  if (!dense) {
+    const int want = (chunks + kWarps - 1) / kWarps;
+    seg_base_kernel<<<want < sms * 4 ? want : sms * 4, kThreads, 0, st>>>(kin, n, none, chunks, w.base, w.done, count_d);
+  }
+  if ((rc = check_launch("lookup gradient"))) return rc;
+  auto go = [&](auto e) {
+    using E = decltype(e);
+    SumArgs<E> a{};
+    a.dout = static_cast<const typename E::T*>(dout_d);
+    a.dout_stride = dout_stride;
+    a.dim = row_dim;
+    a.n_cols = n_cols;
+    a.n = n;
+    a.chunks = chunks;
+    a.scale = scale;
+    a.keys = kin;
+    a.idx = iin;
+    a.none = none;
+    a.dense = dense;
+    a.contiguous = dout_stride == static_cast<int64_t>(n_cols) * row_dim;
+    a.base = w.base;
+    a.count = count_d;
+    a.total_rows = total_rows;
+    // about 64 KB of them: enough to hide the search, little enough to spread over the SMs
+    a.range = (1 << 14) / row_dim / 32 * 32;
+    a.range = a.range < 32 ? 32 : a.range > kMaxRange ? kMaxRange : a.range;
+    a.grad = grad_d;
+    a.rows = rows_d;
+    a.head = w.head;
+    a.tail = w.tail;
+    const bool vec = row_dim % kCols<E> == 0 && dout_stride % kCols<E> == 0 && aligned(dout_d, 16) && aligned(grad_d, 16);
+    return vec ? launch_sums<E, true>(a, sms, st) : launch_sums<E, false>(a, sms, st);
+  };
+  return type == ENGRAM_T_BF16 ? go(train::Bf16{}) : go(train::F32{});
 }
 
 }  // namespace
@@ -374,7 +685,7 @@ extern "C" int engram_lookup(const void* table_d, int32_t type, int64_t total_ro
 
 extern "C" size_t engram_lookup_grad_workspace_bytes(int64_t n_tokens, int32_t n_cols, int32_t row_dim) {
   if (n_tokens < 0 || n_cols < 1 || row_dim < 1) return 0;
-  return grad_space(nullptr, n_tokens * n_cols).bytes;
+  return grad_space(nullptr, n_tokens * n_cols, row_dim).bytes;
 }
 
 extern "C" int engram_lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int32_t* row_ids_d,
