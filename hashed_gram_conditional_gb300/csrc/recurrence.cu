@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "engram_internal.h"
 #include "train_device.cuh"
 
@@ -20,46 +22,74 @@ namespace {
 
 using train::round256;
 
-constexpr int kTile = ENGRAM_RECURRENCE_TILE;  // positions between saved states; the tile of the backward pass
-constexpr int kSteps = 8;                      // positions per warp
 constexpr uint32_t kFull = 0xffffffffu;
 
-// Every lane handles 4 bytes of a row: two bf16 channels or one fp32 channel,
-// so a warp reads a row in one 128-byte request.
+// Every lane handles 8 bytes of a row: four bf16 channels or two fp32 ones; a
+// warp reads 256 bytes of a row.
 template <class E>
-constexpr int kLaneCh = 4 / E::kBytes;
+constexpr int kLaneCh = 8 / E::kBytes;
 template <class E>
 constexpr int kGroup = 32 * kLaneCh<E>;  // channels of a block
+constexpr int kRowBytes = 256;
 
-struct Gate {
-  float f, u;  // sigmoid(g), sigmoid(-g)
-};
-
-// With e = exp(-|g|) the larger of the two is 1 / (1 + e) and the smaller
-// e / (1 + e): neither cancels nor overflows, and the smaller one with the
-// sign of g (gate_code) stands for both.  bf16 data takes the hardware's
-// base-2 exponential and reciprocal (2^-22 and 2^-23 relative, plus |g| 2^-24
-// from rounding the exponent), far below its own rounding; fp32 data takes
-// expf and the rounded reciprocal.
+// f = sigmoid(g) and u = sigmoid(-g) of two channels.
+//
+// bf16 data: with e = 2^min(-g log2 e, 60), f = 1 / (1 + e) and u = e / (1 + e),
+// neither of which cancels; one reciprocal of (1 + e0)(1 + e1) serves both
+// channels.  The hardware's base-2 exponential and reciprocal (2^-22 and 2^-23
+// relative, plus |g| 2^-24 from rounding the exponent) are far below the data's
+// own rounding; the clamp leaves f = 2^-60 where it would be smaller.
+// fp32 data: expf and the rounded reciprocal, on exp(-|g|).
 template <class E>
-__device__ __forceinline__ float gate_code(float g) {
-  float small;
-  if (E::kBytes == 2) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * fabsf(g)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    small = e * r;
+__device__ __forceinline__ void gates2(float g0, float g1, float (&f)[2], float (&u)[2]) {
+  if constexpr (E::kBytes == 2) {
+    float t0, t1, e0, e1, r, d0, d1;
+    f2_split(f2_mul(f2(g0, g1), f2(-1.4426950408889634f, -1.4426950408889634f)), t0, t1);
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(t0) : "f"(t0), "f"(60.f));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(t1) : "f"(t1), "f"(60.f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t0));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t1));
+    f2_split(f2_add(f2(e0, e1), f2(1.f, 1.f)), d0, d1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d0 * d1));
+    const uint64_t f2v = f2_mul(f2(r, r), f2(d1, d0));
+    f2_split(f2v, f[0], f[1]);
+    f2_split(f2_mul(f2v, f2(e0, e1)), u[0], u[1]);
   } else {
-    const float e = expf(-fabsf(g));
-    small = e * __frcp_rn(1.f + e);
+    const float g[2] = {g0, g1};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float e = expf(-fabsf(g[j])), big = __frcp_rn(1.f + e), small = e * big;
+      f[j] = g[j] >= 0.f ? big : small;
+      u[j] = g[j] >= 0.f ? small : big;
+    }
   }
-  return copysignf(small, g);  // +: sigmoid(-g), -: sigmoid(g)
 }
 
-__device__ __forceinline__ Gate gate_of(float code) {
-  const float small = fabsf(code), big = 1.f - small;
-  const bool neg = signbit(code);
-  return Gate{neg ? small : big, neg ? big : small};
+template <class E>
+__device__ __forceinline__ void gates(const float (&g)[kLaneCh<E>], float (&f)[kLaneCh<E>], float (&u)[kLaneCh<E>]) {
+#pragma unroll
+  for (int j = 0; j < kLaneCh<E>; j += 2) {
+    float f2v[2], u2v[2];
+    gates2<E>(g[j], g[j + 1], f2v, u2v);
+    f[j] = f2v[0];
+    f[j + 1] = f2v[1];
+    u[j] = u2v[0];
+    u[j + 1] = u2v[1];
+  }
+}
+
+// a b + c and a b of a lane's channels, two at a time.
+template <int V>
+__device__ __forceinline__ void fma_v(const float (&a)[V], const float (&b)[V], const float (&c)[V], float (&r)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; j += 2)
+    f2_split(f2_fma(f2(a[j], a[j + 1]), f2(b[j], b[j + 1]), f2(c[j], c[j + 1])), r[j], r[j + 1]);
+}
+template <int V>
+__device__ __forceinline__ void mul_v(const float (&a)[V], const float (&b)[V], float (&r)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; j += 2)
+    f2_split(f2_mul(f2(a[j], a[j + 1]), f2(b[j], b[j + 1])), r[j], r[j + 1]);
 }
 
 template <class E>
@@ -77,6 +107,8 @@ struct Args {
   int64_t n_slots;
   float* carry;
   int32_t n_tokens, dim, n_tiles, n_groups;
+  uint8_t* flags;   // [n_tokens], see mark_kernel
+  int32_t* slot;    // [n_tokens]: the state slot of a first or last position
   int32_t* ticket;  // [0] next block number, [1] a wait ran out
   int32_t* flag;    // [group][tile]: 0 nothing, 1 the tile's map, 2 the value after it
   float2* map;      // [group][tile][kGroup]: the tile as v -> A v + B
@@ -96,37 +128,72 @@ __device__ __forceinline__ int32_t slot_of(const Args<E>& a, int64_t q) {
   return s;
 }
 
-// ------------------------------------------------ 4 bytes of a row per lane
+// ------------------------------------------------ 8 bytes of a row per lane
 
-template <class E, bool kVec>
-__device__ __forceinline__ uint32_t load4(const typename E::T* row, int c, int dim) {
-  if constexpr (E::kBytes == 4) return c < dim ? __float_as_uint(__ldg(row + c)) : 0u;
-  else if constexpr (kVec) return c < dim ? __ldg(reinterpret_cast<const uint32_t*>(row + c)) : 0u;
-  else {
-    const uint32_t lo = c < dim ? row[c] : 0u, hi = c + 1 < dim ? row[c + 1] : 0u;
-    return lo | hi << 16;
+// A warp's kSteps rows of 256 bytes into shared memory, without waiting.
+// Channels past the width and rows past the end read as zeros.
+template <class E, bool kVec, int kSteps>
+__device__ __forceinline__ void fetch_rows(unsigned char* dst, const typename E::T* src, int64_t stride, int t, int n_tokens,
+                                           int c0, int dim, int lane) {
+  if constexpr (kVec) {
+    constexpr int N = 16 / E::kBytes;
+    const int c = c0 + (lane & 15) * N;
+#pragma unroll
+    for (int k = 0; k < kSteps; k += 2) {
+      const int r = k + (lane >> 4);
+      const bool ok = t + r < n_tokens && c < dim;
+      const typename E::T* p = ok ? src + (t + r) * stride + c : src;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + r * kRowBytes + (lane & 15) * 16)),
+                   "l"(p), "r"(ok ? 16 : 0)
+                   : "memory");
+    }
+  } else {
+    typename E::T* d = reinterpret_cast<typename E::T*>(dst);
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+      for (int j = 0; j < kLaneCh<E>; ++j) {
+        const int c = j * 32 + lane;
+        const bool ok = t + k < n_tokens && c0 + c < dim;
+        d[k * kGroup<E> + c] = ok ? src[(t + k) * stride + c0 + c] : typename E::T(0);
+      }
   }
 }
 
-template <class E, bool kVec>
-__device__ __forceinline__ void store4(typename E::T* row, int c, int dim, const float (&v)[kLaneCh<E>]) {
-  if constexpr (E::kBytes == 4) {
-    if (c < dim) row[c] = v[0];
-  } else if constexpr (kVec) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(v[0], v[1]);
-    if (c < dim) *reinterpret_cast<__nv_bfloat162*>(row + c) = b;
-  } else {
-    if (c < dim) E::store(row + c, v[0]);
-    if (c + 1 < dim) E::store(row + c + 1, v[1]);
-  }
+__device__ __forceinline__ void wait_rows() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
 }
 
 template <class E>
-__device__ __forceinline__ void widen(uint32_t raw, float (&v)[kLaneCh<E>]) {
-  if constexpr (E::kBytes == 4) v[0] = __uint_as_float(raw);
-  else {
-    v[0] = __uint_as_float(raw << 16);
-    v[1] = __uint_as_float(raw & 0xffff0000u);
+__device__ __forceinline__ void lane_row(const unsigned char* row, int lane, float (&v)[kLaneCh<E>]) {
+  const uint2 w = *reinterpret_cast<const uint2*>(row + lane * 8);
+  if constexpr (E::kBytes == 2) {
+    v[0] = __uint_as_float(w.x << 16);
+    v[1] = __uint_as_float(w.x & 0xffff0000u);
+    v[2] = __uint_as_float(w.y << 16);
+    v[3] = __uint_as_float(w.y & 0xffff0000u);
+  } else {
+    v[0] = __uint_as_float(w.x);
+    v[1] = __uint_as_float(w.y);
+  }
+}
+
+template <class E, bool kVec>
+__device__ __forceinline__ void store_row(typename E::T* row, int c, int dim, const float (&v)[kLaneCh<E>]) {
+  if constexpr (kVec) {
+    if (c >= dim) return;
+    if constexpr (E::kBytes == 2) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+      *reinterpret_cast<uint2*>(row + c) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    } else {
+      *reinterpret_cast<float2*>(row + c) = make_float2(v[0], v[1]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kLaneCh<E>; ++j)
+      if (c + j < dim) E::store(row + c + j, v[j]);
   }
 }
 
@@ -142,83 +209,72 @@ __device__ __forceinline__ void store_state(float* row, int c, int dim, const fl
   for (int j = 0; j < kLaneCh<E>; ++j)
     if (c + j < dim) row[c + j] = v[j];
 }
-
-// ------------------------------------------------- what a tile's positions are
-
-// Position p of the tile: first[p] / last[p] = the slot (or -1: without a
-// state) of the sequence that begins / ends there, kNone where none does;
-// dead[p] = masked, in a padding sequence, or past the end.
-constexpr int32_t kNone = -2;
-template <int kLen>
-struct Marks {
-  int32_t first[kLen], last[kLen];
-  uint8_t dead[kLen];
-  bool any_first;
-};
-
-// Filled by one warp.  Empty sequences have no positions; `copy_empty` moves
-// their states for the channels of this block.
-template <class E, int kLen>
-__device__ __forceinline__ void mark_tile(const Args<E>& a, int t0, Marks<kLen>& m, int lane, int c, bool copy_empty,
-                                          bool has_state) {
-  for (int p = lane; p < kLen; p += 32) {
-    m.first[p] = m.last[p] = kNone;
-    const int t = t0 + p;
-    m.dead[p] = t >= a.n_tokens || (a.mask != nullptr && a.mask[t] != 0);
+// a lane's channels of an fp32 row in shared memory
+template <class E>
+__device__ __forceinline__ void get_lane(const float* row, int lane, float (&v)[kLaneCh<E>]) {
+  if constexpr (kLaneCh<E> == 4) {
+    const float4 q = *reinterpret_cast<const float4*>(row + 4 * lane);
+    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+  } else {
+    const float2 q = *reinterpret_cast<const float2*>(row + 2 * lane);
+    v[0] = q.x; v[1] = q.y;
   }
-  if (lane == 0) m.any_first = false;
-  __syncwarp();
-  // the first sequence that begins at t0 or later: the lanes probe 32 equal
-  // parts of the range at a time
-  int64_t lo = 0, hi = a.n_seqs;  // cu[q] < t0 below lo, >= t0 from hi on
-  while (hi > lo) {
-    const int64_t step = (hi - lo + 31) / 32;
-    const int64_t q = lo + step * lane;
-    const uint32_t below = __ballot_sync(kFull, q < hi && a.cu[q] < t0);
-    const int n = __popc(below);  // the probes below t0 are a prefix
-    if (n == 0) break;
-    const int64_t l2 = lo + step * (n - 1) + 1, h2 = lo + step * n;
-    lo = l2;
-    hi = h2 < hi ? h2 : hi;
-  }
-  const bool ends = t0 + kLen >= a.n_tokens;  // empty sequences after the last position belong to the last tile
-  const int t1 = ends ? a.n_tokens : t0 + kLen;
-  for (int64_t q0 = lo > 0 ? lo - 1 : 0;; q0 += 32) {
-    const int64_t q = q0 + lane;
-    int64_t b = INT64_MAX, e = INT64_MAX;
-    if (q < a.n_seqs) {
-      b = a.cu[q];
-      e = a.cu[q + 1];
+}
+template <class E>
+__device__ __forceinline__ void put_lane(float* row, int lane, const float (&v)[kLaneCh<E>]) {
+  if constexpr (kLaneCh<E> == 4) *reinterpret_cast<float4*>(row + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+  else *reinterpret_cast<float2*>(row + 2 * lane) = make_float2(v[0], v[1]);
+}
+
+// ------------------------------------------------------ what the positions are
+
+constexpr int kLive = 1, kFirst = 2, kLast = 4;
+
+// flags[t]: kLive where the position counts (not masked, not in a padding
+// sequence), kFirst / kLast where a sequence begins / ends, whose slot (-1:
+// padding) is then in slot[t].  Also zeroes the scan's counters and moves the
+// states of empty sequences.
+template <class E>
+__global__ void __launch_bounds__(256) mark_kernel(Args<E> a, int64_t zeroed, bool move_empty) {
+  allow_dependent_launch();
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = i0; i < zeroed; i += step) a.ticket[i] = 0;
+  for (int64_t t = i0; t < a.n_tokens; t += step) {
+    int64_t lo = 0, hi = a.n_seqs;  // the last sequence with cu <= t
+    while (hi - lo > 1) {
+      const int64_t mid = (lo + hi) / 2;
+      if (a.cu[mid] <= t) lo = mid;
+      else hi = mid;
     }
-    const bool some = e > b && q < a.n_seqs;
-    const bool here = b < t1 || (ends && b == t1);
-    if (some && here) {
+    const int32_t slot = slot_of(a, lo);
+    const bool first = a.cu[lo] == t, last = a.cu[lo + 1] == t + 1;
+    const bool live = slot >= 0 && (a.mask == nullptr || a.mask[t] == 0);
+    a.flags[t] = static_cast<uint8_t>((live ? kLive : 0) | (first ? kFirst : 0) | (last ? kLast : 0));
+    if (first || last) a.slot[t] = slot;
+  }
+  if (move_empty) {
+    for (int64_t q = blockIdx.x; q < a.n_seqs; q += gridDim.x) {
+      if (a.cu[q] != a.cu[q + 1]) continue;
       const int32_t slot = slot_of(a, q);
-      const int32_t mark = has_state ? slot : -1;
-      if (b >= t0) {
-        m.first[b - t0] = mark;
-        m.any_first = true;
-      }
-      if (e > t0 && e <= t1) m.last[e - 1 - t0] = mark;
-      if (slot < 0) {
-        const int64_t from = b > t0 ? b - t0 : 0, to = (e < t1 ? e : t1) - t0;
-        for (int64_t p = from; p < to; ++p) m.dead[p] = 1;
-      }
+      for (int d = threadIdx.x; slot >= 0 && d < a.dim; d += 256)
+        a.state_out[static_cast<int64_t>(slot) * a.dim + d] =
+            a.state != nullptr ? a.state[static_cast<int64_t>(slot) * a.dim + d] : 0.f;
     }
-    uint32_t empty = __ballot_sync(kFull, copy_empty && q < a.n_seqs && e == b && b >= t0 && here);
-    while (empty != 0) {  // rare: every lane copies its channels
-      const int src = __ffs(empty) - 1;
-      empty &= empty - 1;
-      const int32_t slot = slot_of(a, q0 + src);
-      if (slot >= 0) {
-        float v[kLaneCh<E>] = {};
-        if (a.state != nullptr) load_state<E>(a.state + static_cast<int64_t>(slot) * a.dim, c, a.dim, v);
-        store_state<E>(a.state_out + static_cast<int64_t>(slot) * a.dim, c, a.dim, v);
-      }
-    }
-    if (!__any_sync(kFull, q < a.n_seqs && lane == 31 && here)) break;
   }
-  __syncwarp();
+}
+
+// The flags of a warp's positions as one bit per position.
+struct Marks {
+  uint32_t live, first, last;
+};
+template <class E, int kSteps>
+__device__ __forceinline__ Marks marks_of(const Args<E>& a, int t, int lane) {
+  const int f = lane < kSteps && t + lane < a.n_tokens ? a.flags[t + lane] : 0;
+  Marks m;
+  m.live = __ballot_sync(kFull, f & kLive);
+  m.first = __ballot_sync(kFull, f & kFirst);
+  m.last = __ballot_sync(kFull, f & kLast);
+  return m;
 }
 
 // ------------------------------------------------------------ across the tiles
@@ -230,19 +286,6 @@ __device__ __forceinline__ int32_t load_flag(const int32_t* p) {
 }
 __device__ __forceinline__ void store_flag(int32_t* p, int32_t v) {
   asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-
-// Maps v -> A v + B with A >= 0.  A sequence's first position cuts: nothing
-// before it counts, which A = -0 stands for, so that a product of gates that
-// underflows to +0 still carries a NaN on as the recurrence itself does.
-constexpr float kCut = -0.f;
-
-__device__ __forceinline__ float apply_map(float A, float B, float v) {
-  return signbit(A) ? B : fmaf(A, v, B);
-}
-// The factor of the map p after the map A.
-__device__ __forceinline__ float join_factor(float p, float A) {
-  return signbit(p) || signbit(A) ? kCut : p * A;
 }
 
 // The value that comes into a tile: from the nearest tile behind it (in
@@ -294,13 +337,11 @@ __device__ __forceinline__ void look_back(const Args<E>& a, int group, int tile,
 #pragma unroll 4
   for (int i = depth; i > 0; --i) {
     const float2* m = a.map + (base + tile - step * i) * kGroup<E> + lane * V;
-    if constexpr (V == 2) {
-      const float4 q = __ldcg(reinterpret_cast<const float4*>(m));
-      v[0] = apply_map(q.x, q.y, v[0]);
-      v[1] = apply_map(q.z, q.w, v[1]);
-    } else {
-      const float2 q = __ldcg(m);
-      v[0] = apply_map(q.x, q.y, v[0]);
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      const float4 q = __ldcg(reinterpret_cast<const float4*>(m + j));
+      v[j] = fmaf(q.x, v[j], q.y);
+      v[j + 1] = fmaf(q.z, v[j + 1], q.w);
     }
   }
 }
@@ -311,7 +352,8 @@ __device__ __forceinline__ void publish_map(const Args<E>& a, int group, int til
   const int64_t at = static_cast<int64_t>(group) * a.n_tiles + tile;
   float2* m = a.map + at * kGroup<E> + lane * kLaneCh<E>;
 #pragma unroll
-  for (int j = 0; j < kLaneCh<E>; ++j) __stcg(m + j, make_float2(A[j], B[j]));
+  for (int j = 0; j < kLaneCh<E>; j += 2)
+    __stcg(reinterpret_cast<float4*>(m + j), make_float4(A[j], B[j], A[j + 1], B[j + 1]));
   __threadfence();
   __syncwarp();
   if (lane == 0) store_flag(a.flag + at, 1);
@@ -338,151 +380,155 @@ __device__ __forceinline__ int take_ticket(int32_t* ticket, int32_t* shared) {
 
 // --------------------------------------------------------------------- forward
 
-// A block handles kWarps * kSteps positions of 32 * kLaneCh channels, in one
-// pass over memory: every warp loads its positions, reduces them to a map s ->
-// A s + B per channel, one warp joins the maps, publishes the block's and
-// looks back over the blocks before it for the state that comes in; then the
-// warps walk their positions again, from registers, and write y.
-constexpr int kFwdWarps = 8;
-constexpr int kFwdTile = kFwdWarps * kSteps;
-static_assert(kTile % kFwdTile == 0, "saved states fall on forward tiles");
+// A block handles kWarps * kSteps positions of one group of channels, in one
+// pass over memory: every warp fetches its rows into shared memory and reduces
+// them to a map s -> A s + B per channel; one warp joins the maps, publishes
+// the block's, and looks back over the blocks before it for the state that
+// comes in; then the warps walk their positions again, from shared memory, and
+// write y.  The gates are computed twice rather than kept: that frees the
+// registers, so that five blocks fit an SM and their loads cover one another's
+// waits.
+constexpr int kWarps = 8, kSteps = 8;
+constexpr int kTile = kWarps * kSteps;
+static_assert(ENGRAM_RECURRENCE_TILE % kTile == 0, "saved states fall on tiles");
 
 template <class E, bool kVec>
-__global__ void __launch_bounds__(kFwdWarps * 32, 4) forward_kernel(Args<E> a) {
+__global__ void __launch_bounds__(kWarps * 32, 5) forward_kernel(Args<E> a) {
   constexpr int V = kLaneCh<E>, G = kGroup<E>;
-  __shared__ Marks<kFwdTile> marks;
-  __shared__ float mapA[kFwdWarps][G], mapB[kFwdWarps][G], in[G];
+  __shared__ __align__(16) unsigned char xs[kTile * kRowBytes], gs[kTile * kRowBytes];
+  __shared__ __align__(16) float mapA[kWarps][G], mapB[kWarps][G];
+  __shared__ bool cuts[kWarps];
   __shared__ int32_t number;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  wait_prior_grids();
   const int n = take_ticket(a.ticket, &number);
   const int tile = n / a.n_groups, group = n - tile * a.n_groups;
-  const int c = group * G + lane * V;
-  const int t0 = tile * kFwdTile, tw = t0 + warp * kSteps;
+  const int c0 = group * G, c = c0 + lane * V;
+  const int t0 = tile * kTile, tw = t0 + warp * kSteps;
+  unsigned char* xw = xs + warp * kSteps * kRowBytes;
+  unsigned char* gw = gs + warp * kSteps * kRowBytes;
+  fetch_rows<E, kVec, kSteps>(gw, a.g, a.g_stride, tw, a.n_tokens, c0, a.dim, lane);
+  fetch_rows<E, kVec, kSteps>(xw, a.x, a.x_stride, tw, a.n_tokens, c0, a.dim, lane);
+  const Marks mk = marks_of<E, kSteps>(a, tw, lane);
+  wait_rows();
 
-  uint32_t xr[kSteps], gr[kSteps];
-#pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
-    const int64_t t = tw + k;
-    const bool ok = t < a.n_tokens;
-    xr[k] = ok ? load4<E, kVec>(a.x + t * a.x_stride, c, a.dim) : 0u;
-    gr[k] = ok ? load4<E, kVec>(a.g + t * a.g_stride, c, a.dim) : 0u;
-  }
-  const bool has_state = a.state != nullptr || a.state_out != nullptr;
-  if (warp == 0)
-    mark_tile<E, kFwdTile>(a, t0, marks, lane, c, a.state_out != nullptr && a.state_out != a.state, has_state);
-  __syncthreads();
-  const int at = warp * kSteps + (lane < kSteps ? lane : 0);
-  const uint32_t live = __ballot_sync(kFull, lane < kSteps && marks.dead[at] == 0);
-  const uint32_t first = __ballot_sync(kFull, lane < kSteps && marks.first[at] != kNone);
-  const uint32_t last = __ballot_sync(kFull, lane < kSteps && marks.last[at] != kNone);
-
-  // s_k = f s_{k-1} + b; a sequence's first position has f = 0
-  float f[kSteps][V], b[kSteps][V], A[V], B[V];
+  // s <- f s + u x; a sequence's first position starts from its own state
+  float s[V], A[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     A[j] = 1.f;
-    B[j] = 0.f;
+    s[j] = 0.f;
   }
+  auto begin = [&](int k) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[j] = 0.f;
+    const int32_t slot = a.slot[tw + k];
+    if (slot >= 0 && a.state != nullptr) load_state<E>(a.state + static_cast<int64_t>(slot) * a.dim, c, a.dim, s);
+  };
+  // Where the states are updated in place, the warp that holds a sequence's
+  // end may overwrite the first state before this warp's second walk: the state
+  // of the one sequence that begins here and ends behind this warp is kept, in
+  // the place of the warp's A (which nothing uses where a sequence begins).
+  auto goes_on = [&](int k) { return (mk.last >> k) == 0u; };
+  auto advance = [&](int k, float (&f)[V]) {
+    float gv[V], xv[V], u[V];
+    lane_row<E>(gw + k * kRowBytes, lane, gv);
+    lane_row<E>(xw + k * kRowBytes, lane, xv);
+    gates<E>(gv, f, u);
+    mul_v<V>(u, xv, xv);
+    fma_v<V>(f, s, xv, s);
+  };
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
-    if (live >> k & 1u) {
-      float gv[V], xv[V];
-      widen<E>(gr[k], gv);
-      widen<E>(xr[k], xv);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const Gate q = gate_of(gate_code<E>(gv[j]));
-        f[k][j] = q.f;
-        b[k][j] = q.u * xv[j];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        f[k][j] = 1.f;
-        b[k][j] = 0.f;
-      }
+    if (mk.first >> k & 1u) {
+      begin(k);
+      if (goes_on(k)) put_lane<E>(mapA[warp], lane, s);
     }
-    if (first >> k & 1u) {
-      const int32_t slot = marks.first[warp * kSteps + k];
-      float s0[V] = {};
-      if (slot >= 0 && a.state != nullptr) load_state<E>(a.state + static_cast<int64_t>(slot) * a.dim, c, a.dim, s0);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        b[k][j] = fmaf(f[k][j], s0[j], b[k][j]);
-        f[k][j] = 0.f;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      B[j] = fmaf(f[k][j], first >> k & 1u ? 0.f : B[j], b[k][j]);
-      A[j] = first >> k & 1u ? kCut : A[j] * f[k][j];
+    if (mk.live >> k & 1u) {
+      float f[V];
+      advance(k, f);
+      mul_v<V>(A, f, A);
     }
   }
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    mapA[warp][lane * V + j] = A[j];
-    mapB[warp][lane * V + j] = B[j];
-  }
+  if (mk.first == 0) put_lane<E>(mapA[warp], lane, A);
+  put_lane<E>(mapB[warp], lane, s);
+  if (lane == 0) cuts[warp] = mk.first != 0;
   __syncthreads();
 
   if (warp == 0) {
-    float v[V];
+    // the tile's map; from a warp in which a sequence begins nothing before counts
+    float B[V], v[V];
+    bool cut = false;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      A[j] = 1.f;
-      B[j] = 0.f;
-    }
+    for (int w = 0; w < kWarps; ++w) {
+      float p[V], q[V];
+      get_lane<E>(mapA[w], lane, p);
+      get_lane<E>(mapB[w], lane, q);
+      if (w == 0 || cuts[w]) {
 #pragma unroll
-    for (int w = 0; w < kFwdWarps; ++w)
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float p = mapA[w][lane * V + j], q = mapB[w][lane * V + j];
-        B[j] = apply_map(p, q, B[j]);
-        A[j] = join_factor(p, A[j]);
+        for (int j = 0; j < V; ++j) {
+          A[j] = p[j];
+          B[j] = q[j];
+        }
+        cut |= cuts[w];
+      } else {
+        fma_v<V>(p, B, q, B);
+        mul_v<V>(p, A, A);
       }
-    const bool cut = marks.any_first, more = tile + 1 < a.n_tiles;
+    }
+    const bool more = tile + 1 < a.n_tiles;
     if (more) {
-      if (cut) publish_value<E>(a, group, tile, lane, B);  // a sequence begins here: its state owes nothing to before
+      if (cut) publish_value<E>(a, group, tile, lane, B);
       else if (tile > 0) publish_map<E>(a, group, tile, lane, A, B);
     }
-    if (tile == 0 || marks.first[0] != kNone) {
+    if (tile == 0 || mk.first & 1u) {
 #pragma unroll
       for (int j = 0; j < V; ++j) v[j] = 0.f;
     } else {
       look_back<E>(a, group, tile, 1, lane, v);
     }
     if (more && !cut) {
-      float w[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) w[j] = apply_map(A[j], B[j], v[j]);
-      publish_value<E>(a, group, tile, lane, w);
+      fma_v<V>(A, v, B, B);
+      publish_value<E>(a, group, tile, lane, B);
     }
-    if (a.carry != nullptr && t0 % kTile == 0) store_state<E>(a.carry + static_cast<int64_t>(t0 / kTile) * a.dim, c, a.dim, v);
+    if (a.carry != nullptr && t0 % ENGRAM_RECURRENCE_TILE == 0)
+      store_state<E>(a.carry + static_cast<int64_t>(t0 / ENGRAM_RECURRENCE_TILE) * a.dim, c, a.dim, v);
+    // the state that comes into every warp, in the place of its B
 #pragma unroll
-    for (int j = 0; j < V; ++j) in[lane * V + j] = v[j];
+    for (int w = 0; w < kWarps; ++w) {
+      float p[V], q[V];
+      get_lane<E>(mapA[w], lane, p);
+      get_lane<E>(mapB[w], lane, q);
+      put_lane<E>(mapB[w], lane, v);
+      if (cuts[w]) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = q[j];
+      } else {
+        fma_v<V>(p, v, q, v);
+      }
+    }
   }
   __syncthreads();
 
-  float s[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) s[j] = in[lane * V + j];
-  for (int w = 0; w < warp; ++w)
-#pragma unroll
-    for (int j = 0; j < V; ++j) s[j] = apply_map(mapA[w][lane * V + j], mapB[w][lane * V + j], s[j]);
+  get_lane<E>(mapB[warp], lane, s);
+  typename E::T* y = a.y + tw * a.y_stride;
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
-    const int64_t t = tw + k;
-    if (t >= a.n_tokens) break;
-    const bool start = first >> k & 1u, on = live >> k & 1u;
-    float y[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      s[j] = fmaf(f[k][j], start ? 0.f : s[j], b[k][j]);
-      y[j] = on ? s[j] : 0.f;
+    if (tw + k >= a.n_tokens) break;
+    if (mk.first >> k & 1u) {
+      if (goes_on(k)) get_lane<E>(mapA[warp], lane, s);
+      else begin(k);
     }
-    store4<E, kVec>(a.y + t * a.y_stride, c, a.dim, y);
-    if (last >> k & 1u) {
-      const int32_t slot = marks.last[warp * kSteps + k];
+    float out[V] = {};
+    if (mk.live >> k & 1u) {
+      float f[V];
+      advance(k, f);
+#pragma unroll
+      for (int j = 0; j < V; ++j) out[j] = s[j];
+    }
+    store_row<E, kVec>(y + k * a.y_stride, c, a.dim, out);
+    if (mk.last >> k & 1u) {
+      const int32_t slot = a.slot[tw + k];
       if (slot >= 0 && a.state_out != nullptr)
         store_state<E>(a.state_out + static_cast<int64_t>(slot) * a.dim, c, a.dim, s);
     }
@@ -494,119 +540,110 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 4) forward_kernel(Args<E> a) {
 // The same scheme walked from the last tile to the first.  With m_t = f_t l_t,
 // what position t passes back, m_t = f_t (dy_t + m_{t+1}): a tile maps the m
 // that comes in to A m + C, A being the product of its gates.  The states
-// before its positions come from the state saved in front of the tile.  Of a
-// position only its gate code, w = f u (s_{t-1} - x) and dy stay in registers.
-constexpr int kBwdWarps = kTile / kSteps;
-
+// before its positions come from the state saved in front of the tile.
+//
+// A position's gradients need its state, known in ascending order, and l,
+// known in descending order: the ascending walk leaves w = f u (s_{t-1} - x)
+// in registers and the gates in the place of x and g in shared memory, the
+// smaller of f and u standing for both (u, or -f).
 template <class E, bool kVec>
-__global__ void __launch_bounds__(kBwdWarps * 32, 2) backward_kernel(Args<E> a) {
+__global__ void __launch_bounds__(kWarps * 32, 3) backward_kernel(Args<E> a) {
   constexpr int V = kLaneCh<E>, G = kGroup<E>;
-  __shared__ Marks<kTile> marks;
-  __shared__ float mapA[kBwdWarps][G], mapB[kBwdWarps][G], mapC[kBwdWarps][G], in[G];
-  // the last states' gradients, read before the tile publishes: a block that
-  // waits for this one may then write the first states' in their place
-  __shared__ float held[kTile][G];
+  extern __shared__ __align__(16) unsigned char smem[];
+  unsigned char* xs = smem;
+  unsigned char* gs = xs + kTile * kRowBytes;
+  unsigned char* ds = gs + kTile * kRowBytes;
+  float(*mapA)[G] = reinterpret_cast<float(*)[G]>(ds + kTile * kRowBytes);
+  float(*mapB)[G] = mapA + kWarps;
+  float(*mapC)[G] = mapB + kWarps;
+  // the gradient of the last state of the sequence that ends here and began
+  // before this warp, whose first state's gradient may be written in its place
+  float(*held)[G] = mapC + kWarps;
+  __shared__ bool cuts[kWarps];
   __shared__ int32_t number;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  wait_prior_grids();
   const int n = take_ticket(a.ticket, &number);
   const int back = n / a.n_groups, group = n - back * a.n_groups;
   const int tile = a.n_tiles - 1 - back;
-  const int c = group * G + lane * V;
+  const int c0 = group * G, c = c0 + lane * V;
   const int t0 = tile * kTile, tw = t0 + warp * kSteps;
+  unsigned char* xw = xs + warp * kSteps * kRowBytes;
+  unsigned char* gw = gs + warp * kSteps * kRowBytes;
+  unsigned char* dw = ds + warp * kSteps * kRowBytes;
+  fetch_rows<E, kVec, kSteps>(gw, a.g, a.g_stride, tw, a.n_tokens, c0, a.dim, lane);
+  fetch_rows<E, kVec, kSteps>(xw, a.x, a.x_stride, tw, a.n_tokens, c0, a.dim, lane);
+  fetch_rows<E, kVec, kSteps>(dw, a.dy, a.dy_stride, tw, a.n_tokens, c0, a.dim, lane);
+  const Marks mk = marks_of<E, kSteps>(a, tw, lane);
+  float carry[V];
+  load_state<E>(a.carry + static_cast<int64_t>(tile) * a.dim, c, a.dim, carry);
+  wait_rows();
 
-  uint32_t xr[kSteps], gr[kSteps], dr[kSteps];
+  float s[V], A[V], C[V];
+  auto begin = [&](int k) {
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
-    const int64_t t = tw + k;
-    const bool ok = t < a.n_tokens;
-    xr[k] = ok ? load4<E, kVec>(a.x + t * a.x_stride, c, a.dim) : 0u;
-    gr[k] = ok ? load4<E, kVec>(a.g + t * a.g_stride, c, a.dim) : 0u;
-    dr[k] = ok ? load4<E, kVec>(a.dy + t * a.dy_stride, c, a.dim) : 0u;
-  }
-  if (warp == 0) mark_tile<E, kTile>(a, t0, marks, lane, c, false, a.state != nullptr || a.dstate != nullptr);
-  __syncthreads();
-  const int at = warp * kSteps + (lane < kSteps ? lane : 0);
-  const uint32_t live = __ballot_sync(kFull, lane < kSteps && marks.dead[at] == 0);
-  const uint32_t first = __ballot_sync(kFull, lane < kSteps && marks.first[at] != kNone);
-  const uint32_t last = __ballot_sync(kFull, lane < kSteps && marks.last[at] != kNone);
-
-  float code[kSteps][V], A[V], B[V], C[V];
+    for (int j = 0; j < V; ++j) s[j] = 0.f;
+    const int32_t slot = a.slot[tw + k];
+    if (slot >= 0 && a.state != nullptr) load_state<E>(a.state + static_cast<int64_t>(slot) * a.dim, c, a.dim, s);
+  };
+  auto from_before = [&](int k) { return (mk.first & ((2u << k) - 1u)) == 0u; };
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     A[j] = 1.f;
-    B[j] = 0.f;
-    C[j] = 0.f;
+    s[j] = C[j] = 0.f;
   }
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
-    if (live >> k & 1u) {
-      float gv[V];
-      widen<E>(gr[k], gv);
-#pragma unroll
-      for (int j = 0; j < V; ++j) code[k][j] = gate_code<E>(gv[j]);
-    } else {  // f = 1, u = 0
-      xr[k] = dr[k] = 0u;
-#pragma unroll
-      for (int j = 0; j < V; ++j) code[k][j] = 0.f;
-    }
-    float xv[V], s0[V] = {};
-    widen<E>(xr[k], xv);
-    const bool start = first >> k & 1u;
-    if (start) {
-      const int32_t slot = marks.first[warp * kSteps + k];
-      if (slot >= 0 && a.state != nullptr) load_state<E>(a.state + static_cast<int64_t>(slot) * a.dim, c, a.dim, s0);
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const Gate q = gate_of(code[k][j]);
-      B[j] = fmaf(q.f, start ? s0[j] : B[j], q.u * xv[j]);
-      A[j] = start ? kCut : A[j] * q.f;
-    }
-  }
-#pragma unroll
-  for (int k = kSteps - 1; k >= 0; --k) {
-    float dv[V];
-    widen<E>(dr[k], dv);
-    if (last >> k & 1u) {
-      const int32_t slot = marks.last[warp * kSteps + k];
-      float ds[V] = {};
-      if (slot >= 0 && a.dstate != nullptr) load_state<E>(a.dstate + static_cast<int64_t>(slot) * a.dim, c, a.dim, ds);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {  // nothing comes from the positions behind
-        C[j] = ds[j];
-        held[warp * kSteps + k][lane * V + j] = ds[j];
+    if (mk.first >> k & 1u) begin(k);
+    if (mk.live >> k & 1u) {
+      float gv[V], xv[V], f[V], u[V];
+      lane_row<E>(gw + k * kRowBytes, lane, gv);
+      lane_row<E>(xw + k * kRowBytes, lane, xv);
+      gates<E>(gv, f, u);
+      mul_v<V>(u, xv, xv);
+      fma_v<V>(f, s, xv, s);
+      if (from_before(k)) {  // nothing is passed back over a sequence's beginning
+        float dv[V];
+        lane_row<E>(dw + k * kRowBytes, lane, dv);
+        mul_v<V>(A, f, A);
+        fma_v<V>(A, dv, C, C);
       }
     }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const Gate q = gate_of(code[k][j]);
-      C[j] = first >> k & 1u ? 0.f : q.f * (dv[j] + C[j]);
+    if ((mk.last >> k & 1u) && from_before(k)) {
+      float l[V] = {};
+      const int32_t slot = a.slot[tw + k];
+      if (slot >= 0 && a.dstate != nullptr) load_state<E>(a.dstate + static_cast<int64_t>(slot) * a.dim, c, a.dim, l);
+      put_lane<E>(held[warp], lane, l);
+      fma_v<V>(A, l, C, C);
     }
   }
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    mapA[warp][lane * V + j] = A[j];
-    mapB[warp][lane * V + j] = B[j];
-    mapC[warp][lane * V + j] = C[j];
-  }
+  put_lane<E>(mapA[warp], lane, A);
+  put_lane<E>(mapB[warp], lane, s);
+  put_lane<E>(mapC[warp], lane, C);
+  if (lane == 0) cuts[warp] = mk.first != 0;
   __syncthreads();
 
   if (warp == 0) {
     float v[V];
+    bool cut = false;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      A[j] = 1.f;
-      C[j] = 0.f;
-    }
+    for (int w = kWarps - 1; w >= 0; --w) {
+      float p[V], q[V];
+      get_lane<E>(mapA[w], lane, p);
+      get_lane<E>(mapC[w], lane, q);
+      if (w == kWarps - 1 || cuts[w]) {
 #pragma unroll
-    for (int w = kBwdWarps - 1; w >= 0; --w)
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float p = mapA[w][lane * V + j], q = mapC[w][lane * V + j];
-        C[j] = apply_map(p, q, C[j]);
-        A[j] = join_factor(p, A[j]);
+        for (int j = 0; j < V; ++j) {
+          A[j] = p[j];
+          C[j] = q[j];
+        }
+        cut |= cuts[w];
+      } else {
+        fma_v<V>(p, C, q, C);
+        mul_v<V>(p, A, A);
       }
-    const bool cut = marks.any_first, ends = tile + 1 == a.n_tiles, more = tile > 0;
+    }
+    const bool ends = tile + 1 == a.n_tiles, more = tile > 0;
     if (more) {
       if (cut) publish_value<E>(a, group, tile, lane, C);
       else if (!ends) publish_map<E>(a, group, tile, lane, A, C);
@@ -618,68 +655,104 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) backward_kernel(Args<E> a) 
       look_back<E>(a, group, tile, -1, lane, v);
     }
     if (more && !cut) {
-      float w[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) w[j] = apply_map(A[j], C[j], v[j]);
-      publish_value<E>(a, group, tile, lane, w);
+      fma_v<V>(A, v, C, C);
+      publish_value<E>(a, group, tile, lane, C);
     }
+    // what comes into every warp from behind, in the place of its C
 #pragma unroll
-    for (int j = 0; j < V; ++j) in[lane * V + j] = v[j];
+    for (int w = kWarps - 1; w >= 0; --w) {
+      float p[V], q[V];
+      get_lane<E>(mapA[w], lane, p);
+      get_lane<E>(mapC[w], lane, q);
+      put_lane<E>(mapC[w], lane, v);
+      if (cuts[w]) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = q[j];
+      } else {
+        fma_v<V>(p, v, q, v);
+      }
+    }
   }
-  // meanwhile the other warps: the states before their positions
-  float s[V], w[kSteps][V];
-  load_state<E>(a.carry + static_cast<int64_t>(tile) * a.dim, c, a.dim, s);
-  for (int p = 0; p < warp; ++p)
+  // meanwhile the other warps walk their positions in ascending order
 #pragma unroll
-    for (int j = 0; j < V; ++j) s[j] = apply_map(mapA[p][lane * V + j], mapB[p][lane * V + j], s[j]);
+  for (int j = 0; j < V; ++j) s[j] = carry[j];
+  for (int p = 0; p < warp; ++p) {
+    float f[V], q[V];
+    get_lane<E>(mapA[p], lane, f);
+    get_lane<E>(mapB[p], lane, q);
+    if (cuts[p]) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[j] = q[j];
+    } else {
+      fma_v<V>(f, s, q, s);
+    }
+  }
+  float w[kSteps][V];
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
-    float xv[V];
-    widen<E>(xr[k], xv);
-    if (first >> k & 1u) {
-      const int32_t slot = marks.first[warp * kSteps + k];
+    if (mk.first >> k & 1u) begin(k);
+    if (mk.live >> k & 1u) {
+      float gv[V], xv[V], f[V], u[V], code[V];
+      lane_row<E>(gw + k * kRowBytes, lane, gv);
+      lane_row<E>(xw + k * kRowBytes, lane, xv);
+      gates<E>(gv, f, u);
 #pragma unroll
-      for (int j = 0; j < V; ++j) s[j] = 0.f;
-      if (slot >= 0 && a.state != nullptr) load_state<E>(a.state + static_cast<int64_t>(slot) * a.dim, c, a.dim, s);
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const Gate q = gate_of(code[k][j]);
-      w[k][j] = q.f * (s[j] - xv[j]) * q.u;
-      s[j] = fmaf(q.f, s[j], q.u * xv[j]);
+      for (int j = 0; j < V; ++j) {
+        w[k][j] = f[j] * u[j] * (s[j] - xv[j]);
+        code[j] = f[j] <= u[j] ? -f[j] : u[j];
+      }
+      mul_v<V>(u, xv, xv);
+      fma_v<V>(f, s, xv, s);
+      float* c0p = reinterpret_cast<float*>(gw + k * kRowBytes + lane * 8);
+      float* c1p = reinterpret_cast<float*>(xw + k * kRowBytes + lane * 8);
+      *reinterpret_cast<float2*>(c0p) = make_float2(code[0], code[1]);
+      if constexpr (V == 4) *reinterpret_cast<float2*>(c1p) = make_float2(code[2], code[3]);
     }
   }
   __syncthreads();
 
   float m[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) m[j] = in[lane * V + j];
-  for (int p = kBwdWarps - 1; p > warp; --p)
-#pragma unroll
-    for (int j = 0; j < V; ++j) m[j] = apply_map(mapA[p][lane * V + j], mapC[p][lane * V + j], m[j]);
+  get_lane<E>(mapC[warp], lane, m);
+  typename E::T* dx = a.dx + tw * a.dx_stride;
+  typename E::T* dg = a.dg + tw * a.dg_stride;
 #pragma unroll
   for (int k = kSteps - 1; k >= 0; --k) {
-    const int64_t t = tw + k;
-    if (t >= a.n_tokens) continue;
-    if (last >> k & 1u) {
+    if (tw + k >= a.n_tokens) continue;
+    if (mk.last >> k & 1u) {
+      if (from_before(k)) {
+        get_lane<E>(held[warp], lane, m);
+      } else {
+        const int32_t slot = a.slot[tw + k];
 #pragma unroll
-      for (int j = 0; j < V; ++j) m[j] = held[warp * kSteps + k][lane * V + j];
+        for (int j = 0; j < V; ++j) m[j] = 0.f;
+        if (slot >= 0 && a.dstate != nullptr) load_state<E>(a.dstate + static_cast<int64_t>(slot) * a.dim, c, a.dim, m);
+      }
     }
-    const bool on = live >> k & 1u;
-    float dv[V], dx[V], dg[V];
-    widen<E>(dr[k], dv);
+    float ox[V] = {}, og[V] = {};
+    if (mk.live >> k & 1u) {
+      float dv[V], code[V];
+      lane_row<E>(dw + k * kRowBytes, lane, dv);
+      const float2 lo = *reinterpret_cast<const float2*>(gw + k * kRowBytes + lane * 8);
+      code[0] = lo.x;
+      code[1] = lo.y;
+      if constexpr (V == 4) {
+        const float2 hi = *reinterpret_cast<const float2*>(xw + k * kRowBytes + lane * 8);
+        code[2] = hi.x;
+        code[3] = hi.y;
+      }
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const Gate q = gate_of(code[k][j]);
-      const float l = dv[j] + m[j];
-      dx[j] = on ? l * q.u : 0.f;
-      dg[j] = on ? l * w[k][j] : 0.f;
-      m[j] = q.f * l;
+      for (int j = 0; j < V; ++j) {
+        const float l = dv[j] + m[j], small = fabsf(code[j]), big = 1.f - small;
+        const bool neg = signbit(code[j]);
+        ox[j] = l * (neg ? big : small);
+        og[j] = l * w[k][j];
+        m[j] = l * (neg ? small : big);
+      }
     }
-    store4<E, kVec>(a.dx + t * a.dx_stride, c, a.dim, dx);
-    store4<E, kVec>(a.dg + t * a.dg_stride, c, a.dim, dg);
-    if (first >> k & 1u) {
-      const int32_t slot = marks.first[warp * kSteps + k];
+    store_row<E, kVec>(dx + k * a.dx_stride, c, a.dim, ox);
+    store_row<E, kVec>(dg + k * a.dg_stride, c, a.dim, og);
+    if (mk.first >> k & 1u) {
+      const int32_t slot = a.slot[tw + k];
       if (slot >= 0 && a.dstate != nullptr) store_state<E>(a.dstate + static_cast<int64_t>(slot) * a.dim, c, a.dim, m);
 #pragma unroll
       for (int j = 0; j < V; ++j) m[j] = 0.f;
@@ -687,17 +760,10 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) backward_kernel(Args<E> a) 
   }
 }
 
-// ------------------------------------------------------------------ other parts
-
-// The states of empty sequences when there are no positions at all.
 template <class E>
-__global__ void __launch_bounds__(128) copy_states_kernel(Args<E> a) {
-  const int32_t slot = slot_of(a, blockIdx.x);
-  if (slot < 0) return;
-  for (int d = threadIdx.x; d < a.dim; d += blockDim.x)
-    a.state_out[static_cast<int64_t>(slot) * a.dim + d] =
-        a.state != nullptr ? a.state[static_cast<int64_t>(slot) * a.dim + d] : 0.f;
-}
+constexpr int kBwdSmem = 3 * kTile * kRowBytes + 4 * kWarps * kGroup<E> * 4;
+
+// ------------------------------------------------------------------ other parts
 
 constexpr int kThreads = 128;
 
@@ -707,47 +773,57 @@ __global__ void __launch_bounds__(kThreads) step_kernel(Args<E> a) {
   const int64_t b = blockIdx.x;
   const int c = (blockIdx.y * kThreads + threadIdx.x) * V;
   if (c >= a.dim) return;
-  const uint32_t xr = load4<E, kVec>(a.x + b * a.x_stride, c, a.dim);
-  const uint32_t gr = load4<E, kVec>(a.g + b * a.g_stride, c, a.dim);
-  const int32_t slot = slot_of(a, b);
-  float s[V] = {};
-  if (slot >= 0) {
-    float xv[V], gv[V];
-    load_state<E>(a.state + static_cast<int64_t>(slot) * a.dim, c, a.dim, s);
-    widen<E>(xr, xv);
-    widen<E>(gr, gv);
+  float xv[V], gv[V], s[V] = {};
+  const typename E::T* xr = a.x + b * a.x_stride;
+  const typename E::T* gr = a.g + b * a.g_stride;
+  if constexpr (kVec) {
+    lane_row<E>(reinterpret_cast<const unsigned char*>(xr + c), 0, xv);
+    lane_row<E>(reinterpret_cast<const unsigned char*>(gr + c), 0, gv);
+  } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const Gate q = gate_of(gate_code<E>(gv[j]));
-      s[j] = fmaf(q.f, s[j], q.u * xv[j]);
+      xv[j] = c + j < a.dim ? E::load(xr + c + j) : 0.f;
+      gv[j] = c + j < a.dim ? E::load(gr + c + j) : 0.f;
     }
+  }
+  const int32_t slot = slot_of(a, b);
+  if (slot >= 0) {
+    float f[V], u[V];
+    load_state<E>(a.state + static_cast<int64_t>(slot) * a.dim, c, a.dim, s);
+    gates<E>(gv, f, u);
+    mul_v<V>(u, xv, xv);
+    fma_v<V>(f, s, xv, s);
     store_state<E>(a.state_out + static_cast<int64_t>(slot) * a.dim, c, a.dim, s);
   }
-  store4<E, kVec>(a.y + b * a.y_stride, c, a.dim, s);
+  store_row<E, kVec>(a.y + b * a.y_stride, c, a.dim, s);
 }
 
 // The parts of the scans' workspace: counters and flags (zeroed before each
-// scan), then the tiles' maps and values.
+// scan), the positions' marks, then the tiles' maps and values.
 struct ScanSpace {
   int32_t* ticket;
   int32_t* flag;
+  uint8_t* flags;
+  int32_t* slot;
   float2* map;
   float* value;
-  size_t zeroed, bytes;
+  size_t bytes;
 };
 
-// Sized for the smaller of the two tiles and the narrower group, which serves
-// both passes and both types.
+// Sized for the narrower group, which serves both types.
 ScanSpace scan_space(void* base, int64_t n_tokens, int32_t dim) {
   constexpr int kNarrow = kGroup<train::F32>;
-  const size_t tiles = static_cast<size_t>((n_tokens + kFwdTile - 1) / kFwdTile);
+  const size_t tiles = static_cast<size_t>((n_tokens + kTile - 1) / kTile);
   const size_t groups = static_cast<size_t>((dim + kNarrow - 1) / kNarrow) + 1;  // + 1: a bf16 group may be half empty
   ScanSpace s;
   char* p = static_cast<char*>(base);
   s.ticket = reinterpret_cast<int32_t*>(p);
   s.flag = s.ticket + 2;
-  s.zeroed = (2 + tiles * groups) * 4;
-  size_t at = round256(s.zeroed);
+  size_t at = round256((2 + tiles * groups) * 4);
+  s.flags = reinterpret_cast<uint8_t*>(p + at);
+  at += round256(static_cast<size_t>(n_tokens));
+  s.slot = reinterpret_cast<int32_t*>(p + at);
+  at += round256(static_cast<size_t>(n_tokens) * 4);
   s.map = reinterpret_cast<float2*>(p + at);
   at += round256(tiles * groups * kNarrow * 8);
   s.value = reinterpret_cast<float*>(p + at);
@@ -771,46 +847,74 @@ int check_rows(const void* p, int32_t type, int64_t stride, int32_t dim, const c
   return ENGRAM_OK;
 }
 
-// Whether rows of `stride` elements from p can be read 4 bytes at a time.
+// Whether rows of `stride` elements from p lie on 16-byte boundaries.
 template <class E>
-bool pairs(const void* p, int64_t stride) {
-  return E::kBytes == 4 || (aligned(p, 4) && stride % 2 == 0);
+bool rows16(const void* p, int64_t stride) {
+  return aligned(p, 16) && stride * E::kBytes % 16 == 0;
+}
+
+template <class E, bool kVec>
+int launch_pass(const Args<E>& a, bool backward, int grid, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // launched while the marks are made
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  if (!backward) {
+    e = cudaLaunchKernelEx(&cfg, forward_kernel<E, kVec>, a);
+  } else {
+    static std::atomic<uint64_t> attr_set{0};  // one bit per device: the shared-memory opt-in was made
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+    if (bit == 0 || !(attr_set.load(std::memory_order_relaxed) & bit)) {
+      e = cudaFuncSetAttribute(backward_kernel<E, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem<E>);
+      if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+      attr_set.fetch_or(bit, std::memory_order_relaxed);
+    }
+    cfg.dynamicSmemBytes = kBwdSmem<E>;
+    e = cudaLaunchKernelEx(&cfg, backward_kernel<E, kVec>, a);
+  }
+  if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "recurrence launch: %s", cudaGetErrorString(e));
+  return check_launch("recurrence");
 }
 
 template <class E>
-int launch_scan(Args<E>& a, bool backward, void* workspace, cudaStream_t st) {
+int launch_scan(Args<E>& a, bool backward, void* workspace, int sms, cudaStream_t st) {
   const ScanSpace w = scan_space(workspace, a.n_tokens, a.dim);
-  const int tile = backward ? kTile : kFwdTile;
-  a.n_tiles = (a.n_tokens + tile - 1) / tile;
+  a.n_tiles = (a.n_tokens + kTile - 1) / kTile;
   a.n_groups = (a.dim + kGroup<E> - 1) / kGroup<E>;
   a.ticket = w.ticket;
   a.flag = w.flag;
+  a.flags = w.flags;
+  a.slot = w.slot;
   a.map = w.map;
   a.value = w.value;
   const int64_t blocks = static_cast<int64_t>(a.n_tiles) * a.n_groups;
-  if (blocks > 0x7fffffff) return fail(ENGRAM_E_RANGE, "too many positions times channels");
-  cudaError_t err = cudaMemsetAsync(w.ticket, 0, (2 + static_cast<size_t>(blocks)) * 4, st);
-  if (err != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(err));
-  const int grid = static_cast<int>(blocks);
-  bool vec = a.dim % kLaneCh<E> == 0 && pairs<E>(a.x, a.x_stride) && pairs<E>(a.g, a.g_stride);
-  if (!backward) {
-    vec = vec && pairs<E>(a.y, a.y_stride);
-    if (vec) forward_kernel<E, true><<<grid, kFwdWarps * 32, 0, st>>>(a);
-    else forward_kernel<E, false><<<grid, kFwdWarps * 32, 0, st>>>(a);
-  } else {
-    vec = vec && pairs<E>(a.dy, a.dy_stride) && pairs<E>(a.dx, a.dx_stride) && pairs<E>(a.dg, a.dg_stride);
-    if (vec) backward_kernel<E, true><<<grid, kBwdWarps * 32, 0, st>>>(a);
-    else backward_kernel<E, false><<<grid, kBwdWarps * 32, 0, st>>>(a);
-  }
-  return check_launch("recurrence");
+  if (blocks > 0x7fffff00) return fail(ENGRAM_E_RANGE, "too many positions times channels");
+  const bool move_empty = !backward && a.state_out != nullptr && a.state_out != a.state;
+  const int64_t want = ((a.n_tokens > blocks ? a.n_tokens : blocks) + 255) / 256, cap = static_cast<int64_t>(sms) * 4;
+  mark_kernel<E><<<static_cast<int>(want < cap ? want : cap), 256, 0, st>>>(a, 2 + blocks, move_empty);
+  int rc = check_launch("mark_kernel");
+  if (rc) return rc;
+  bool vec = a.dim * E::kBytes % 16 == 0 && rows16<E>(a.x, a.x_stride) && rows16<E>(a.g, a.g_stride);
+  if (!backward) vec = vec && rows16<E>(a.y, a.y_stride);
+  else vec = vec && rows16<E>(a.dy, a.dy_stride) && rows16<E>(a.dx, a.dx_stride) && rows16<E>(a.dg, a.dg_stride);
+  return vec ? launch_pass<E, true>(a, backward, static_cast<int>(blocks), st)
+             : launch_pass<E, false>(a, backward, static_cast<int>(blocks), st);
 }
 
 template <class E>
 int launch_step(const Args<E>& a, int64_t batch, cudaStream_t st) {
   const int per = kThreads * kLaneCh<E>;
   const dim3 grid(static_cast<unsigned>(batch), (a.dim + per - 1) / per);
-  const bool vec = a.dim % kLaneCh<E> == 0 && pairs<E>(a.x, a.x_stride) && pairs<E>(a.g, a.g_stride) &&
-                   pairs<E>(a.y, a.y_stride);
+  const bool vec = a.dim % kLaneCh<E> == 0 && rows16<E>(a.x, a.x_stride) && rows16<E>(a.g, a.g_stride) &&
+                   rows16<E>(a.y, a.y_stride);
   if (vec) step_kernel<E, true><<<grid, kThreads, 0, st>>>(a);
   else step_kernel<E, false><<<grid, kThreads, 0, st>>>(a);
   return check_launch("step_kernel");
@@ -823,7 +927,7 @@ using namespace engram;
 
 extern "C" size_t engram_recurrence_carry_bytes(int64_t n_tokens, int32_t dim) {
   if (n_tokens < 0 || dim < 1) return 0;
-  return static_cast<size_t>((n_tokens + kTile - 1) / kTile) * dim * sizeof(float);
+  return static_cast<size_t>((n_tokens + ENGRAM_RECURRENCE_TILE - 1) / ENGRAM_RECURRENCE_TILE) * dim * sizeof(float);
 }
 
 extern "C" size_t engram_recurrence_workspace_bytes(int64_t n_tokens, int32_t dim) {
@@ -850,7 +954,8 @@ extern "C" int engram_recurrence(const void* x_d, int64_t x_stride, const void* 
     if (workspace_bytes < engram_recurrence_workspace_bytes(n_tokens, dim))
       return fail(ENGRAM_E_RANGE, "workspace too small");
   }
-  if ((rc = check_device(nullptr))) return rc;
+  int sms = 0;
+  if ((rc = check_device(&sms))) return rc;
   auto go = [&](auto e) {
     using E = decltype(e);
     Args<E> a{};
@@ -871,10 +976,11 @@ extern "C" int engram_recurrence(const void* x_d, int64_t x_stride, const void* 
     a.n_tokens = static_cast<int32_t>(n_tokens);
     a.dim = dim;
     a.status = status_d;
-    if (n_tokens > 0) return launch_scan<E>(a, false, workspace_d, as_stream(stream));
+    if (n_tokens > 0) return launch_scan<E>(a, false, workspace_d, sms, as_stream(stream));
     if (state_out_d == nullptr || state_out_d == state_d) return static_cast<int>(ENGRAM_OK);
-    copy_states_kernel<E><<<static_cast<int>(n_seqs), 128, 0, as_stream(stream)>>>(a);
-    return check_launch("copy_states_kernel");
+    const int64_t cap = static_cast<int64_t>(sms) * 4;
+    mark_kernel<E><<<static_cast<int>(n_seqs < cap ? n_seqs : cap), 256, 0, as_stream(stream)>>>(a, 0, true);
+    return check_launch("mark_kernel");
   };
   return type == ENGRAM_T_BF16 ? go(train::Bf16{}) : go(train::F32{});
 }
@@ -901,7 +1007,8 @@ extern "C" int engram_recurrence_grad(const void* dy_d, int64_t dy_stride, const
   if (!aligned(workspace_d, 256)) return fail(ENGRAM_E_ALIGN, "workspace must be 256-byte aligned");
   if (workspace_bytes < engram_recurrence_workspace_bytes(n_tokens, dim))
     return fail(ENGRAM_E_RANGE, "workspace too small");
-  if ((rc = check_device(nullptr))) return rc;
+  int sms = 0;
+  if ((rc = check_device(&sms))) return rc;
   auto go = [&](auto e) {
     using E = decltype(e);
     Args<E> a{};
@@ -926,7 +1033,7 @@ extern "C" int engram_recurrence_grad(const void* dy_d, int64_t dy_stride, const
     a.n_tokens = static_cast<int32_t>(n_tokens);
     a.dim = dim;
     a.status = status_d;
-    return launch_scan<E>(a, true, workspace_d, as_stream(stream));
+    return launch_scan<E>(a, true, workspace_d, sms, as_stream(stream));
   };
   return type == ENGRAM_T_BF16 ? go(train::Bf16{}) : go(train::F32{});
 }

@@ -675,7 +675,7 @@ int engram_lookup_grad_rows(const void* dout_d, int32_t type, int64_t dout_strid
  * already running; a wait that runs out sets ENGRAM_ST_TIMEOUT.  The result is
  * the same from run to run.  Any dim >= 1 and element-aligned pointers; outputs overlap no input (but
  * state_out_d may be state_d). */
-#define ENGRAM_RECURRENCE_TILE 128
+#define ENGRAM_RECURRENCE_TILE 64
 size_t engram_recurrence_carry_bytes(int64_t n_tokens, int32_t dim);
 size_t engram_recurrence_workspace_bytes(int64_t n_tokens, int32_t dim);
 int engram_recurrence(const void* x_d, int64_t x_stride, const void* g_d, int64_t g_stride, int32_t type,

@@ -63,7 +63,7 @@ def test_lookup_gradients(lib):
 
 def test_recurrence(lib):
     need = lib.engram_recurrence_workspace_bytes(4, 8)
-    assert lib.engram_recurrence_carry_bytes(129, 8) == 2 * 8 * 4
+    assert lib.engram_recurrence_carry_bytes(129, 8) == 3 * 8 * 4
     assert lib.engram_recurrence_carry_bytes(0, 8) == 0
 
     def fwd(x=P(16), xs=8, ty=F32, T=4, D=8, cu=P(16), S=1, state=None, n_slots=0, y=P(16), ys=8, ws=P(256), n=need):
