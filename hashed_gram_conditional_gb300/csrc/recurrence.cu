@@ -110,9 +110,10 @@ struct Args {
   uint8_t* flags;   // [n_tokens], see mark_kernel
   int32_t* slot;    // [n_tokens]: the state slot of a first or last position
   int32_t* ticket;  // [0] next block number, [1] a wait ran out
-  int32_t* flag;    // [group][tile]: 0 nothing, 1 the tile's map, 2 the value after it
-  float2* map;      // [group][tile][kGroup]: the tile as v -> A v + B
-  float* value;     // [group][tile][kGroup]
+  int32_t n_runs;
+  float2* map;      // [group][place][kGroup]: a tile as v -> A v + B
+  float2* run_map;  // [group][run][kGroup]: kRun tiles as one map
+  float* run_value; // [group][run][kGroup]: the value behind a run
   int32_t* status;
 };
 
@@ -226,19 +227,26 @@ __device__ __forceinline__ void put_lane(float* row, int lane, const float (&v)[
   else *reinterpret_cast<float2*>(row + 2 * lane) = make_float2(v[0], v[1]);
 }
 
+// What a tile publishes needs no flag and no fence: the words are kNotYet until
+// they are written (a NaN that no result is: those are stored as the plain
+// NaN), each is valid by itself, and a reader polls the words it needs.
+constexpr uint32_t kNotYet = 0xffffffffu;
+
 // ------------------------------------------------------ what the positions are
 
 constexpr int kLive = 1, kFirst = 2, kLast = 4;
 
 // flags[t]: kLive where the position counts (not masked, not in a padding
 // sequence), kFirst / kLast where a sequence begins / ends, whose slot (-1:
-// padding) is then in slot[t].  Also zeroes the scan's counters and moves the
-// states of empty sequences.
+// padding) is then in slot[t].  Also readies the counters and the tiles' words
+// (`cleared` 16-byte vectors) and moves the states of empty sequences.
 template <class E>
-__global__ void __launch_bounds__(256) mark_kernel(Args<E> a, int64_t zeroed, bool move_empty) {
+__global__ void __launch_bounds__(256) mark_kernel(Args<E> a, uint4* words, int64_t cleared, bool move_empty) {
   allow_dependent_launch();
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, step = static_cast<int64_t>(gridDim.x) * 256;
-  for (int64_t i = i0; i < zeroed; i += step) a.ticket[i] = 0;
+  if (i0 < 2 && cleared > 0) a.ticket[i0] = 0;
+#pragma unroll 4
+  for (int64_t i = i0; i < cleared; i += step) words[i] = make_uint4(kNotYet, kNotYet, kNotYet, kNotYet);
   for (int64_t t = i0; t < a.n_tokens; t += step) {
     int64_t lo = 0, hi = a.n_seqs;  // the last sequence with cu <= t
     while (hi - lo > 1) {
@@ -263,6 +271,15 @@ __global__ void __launch_bounds__(256) mark_kernel(Args<E> a, int64_t zeroed, bo
   }
 }
 
+// A position that does not count is given g = +inf, x = 0 (and dy = 0) in shared
+// memory: f = 1 and u x = 0 hold the state, whatever the row holds.
+template <class E>
+__device__ __forceinline__ void put_neutral(unsigned char* g, unsigned char* x, int lane) {
+  const uint32_t inf = E::kBytes == 2 ? 0x7f807f80u : 0x7f800000u;
+  *reinterpret_cast<uint2*>(g + lane * 8) = make_uint2(inf, inf);
+  *reinterpret_cast<uint2*>(x + lane * 8) = make_uint2(0u, 0u);
+}
+
 // The flags of a warp's positions as one bit per position.
 struct Marks {
   uint32_t live, first, last;
@@ -279,96 +296,155 @@ __device__ __forceinline__ Marks marks_of(const Args<E>& a, int t, int lane) {
 
 // ------------------------------------------------------------ across the tiles
 
-__device__ __forceinline__ int32_t load_flag(const int32_t* p) {
-  int32_t v;
-  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+__device__ __forceinline__ uint32_t load_word(const void* p) {
+  uint32_t v;
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ void store_flag(int32_t* p, int32_t v) {
-  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ uint2 load_pair(const void* p) {
+  uint2 v;
+  asm volatile("ld.relaxed.gpu.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t plain(float v) {
+  const uint32_t w = __float_as_uint(v);
+  return w == kNotYet ? 0x7fffffffu : w;
+}
+__device__ __forceinline__ void store_word(void* p, float v) {
+  asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(plain(v)) : "memory");
+}
+__device__ __forceinline__ void store_pair(void* p, float x, float y) {
+  asm volatile("st.relaxed.gpu.global.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(plain(x)), "r"(plain(y)) : "memory");
 }
 
-// The value that comes into a tile: from the nearest tile behind it (in
-// walking order) that has published its value, through the maps of those
-// between.  Tiles take their numbers from a counter in walking order, so every
-// tile that is waited for is already running.  The maps are applied one by one
-// from the farthest on, which is how the published values themselves arise:
-// the result does not depend on how far the look had to go.
+// Maps v -> A v + B with A >= 0.  Where a sequence begins nothing before it
+// counts, which A = -0 stands for, so that a product of gates that underflows
+// to +0 still carries a NaN on, as the recurrence itself does.
+constexpr float kCut = -0.f;
+
+__device__ __forceinline__ float apply_map(float A, float B, float v) { return fmaf(A, signbit(A) ? 0.f : v, B); }
+__device__ __forceinline__ float apply_map(const uint2& m, float v) {
+  return apply_map(__uint_as_float(m.x), __uint_as_float(m.y), v);
+}
+__device__ __forceinline__ float join_factor(float p, float A) { return signbit(p) || signbit(A) ? kCut : p * A; }
+
+// What comes into the tile at place `pos` of the walk, for one channel: the
+// tiles' maps applied one by one to the value in front of them.  Runs of kRun
+// tiles are joined to one map by their last tile, so that a look back passes
+// over at most kRun - 1 tiles of its own run and then over whole runs.  Every
+// value is built by the same steps in the same order whatever has been
+// published when, so results do not change from run to run.
+//
+// Tiles take their numbers from a counter in walking order, so every tile that
+// is waited for is already running.  (A, B) is the tile's own map; a warp's
+// lanes are neighbouring channels.
+constexpr int kRun = 8;
+
 template <class E>
-__device__ __forceinline__ void look_back(const Args<E>& a, int group, int tile, int step, int lane,
-                                          float (&v)[kLaneCh<E>]) {
-  constexpr int V = kLaneCh<E>;
-  const int64_t base = static_cast<int64_t>(group) * a.n_tiles;
+__device__ __forceinline__ float come_in(const Args<E>& a, int group, int pos, int ch, float A, float B) {
+  constexpr int G = kGroup<E>;
+  const int lane = threadIdx.x & 31;
   const long long begun = clock64();
-  int depth = 0;  // maps to apply
+  auto give_up = [&]() {
+    const bool out = clock64() - begun > kWaitBudgetCycles || load_word(a.ticket + 1) != 0;
+    if (!__any_sync(kFull, out)) return false;
+    if (lane == 0) {
+      atomicExch(a.ticket + 1, 1);
+      if (a.status != nullptr) atomicOr(a.status, ENGRAM_ST_TIMEOUT);
+    }
+    return true;
+  };
+  const int run = pos / kRun, behind = pos % kRun;  // tiles of this run before this one
+  const int64_t base = static_cast<int64_t>(group) * a.n_tiles;
+  const float2* maps = a.map + (base + pos) * G + ch;
+  const bool last_of_all = pos + 1 == a.n_tiles;
+  if (!last_of_all) store_pair(a.map + (base + pos) * G + ch, A, B);
+
+  uint2 m[kRun - 1];  // m[i]: the map of the tile i + 1 places before
 #pragma unroll
-  for (int j = 0; j < V; ++j) v[j] = 0.f;
+  for (int i = 0; i < kRun - 1; ++i) m[i] = i < behind ? load_pair(maps - (i + 1) * G) : make_uint2(0u, 0u);
   while (true) {
-    const int mine = tile - step * (depth + 1 + lane);
-    const bool in = mine >= 0 && mine < a.n_tiles;
-    const int32_t f = in ? load_flag(a.flag + base + mine) : 2;
-    const uint32_t done = __ballot_sync(kFull, f == 2), some = __ballot_sync(kFull, f >= 1);
-    const uint32_t before = done != 0 ? (done & -done) - 1u : kFull;  // the lanes nearer than the first value
-    if ((some & before) == before) {
-      if (done != 0) {
-        depth += __ffs(done) - 1;
-        break;
-      }
-      depth += 32;
-      continue;
-    }
-    depth = 0;
-    const bool out = clock64() - begun > kWaitBudgetCycles || load_flag(a.ticket + 1) != 0;
-    if (__any_sync(kFull, out)) {
-      if (lane == 0) {
-        store_flag(a.ticket + 1, 1);
-        if (a.status != nullptr) atomicOr(a.status, ENGRAM_ST_TIMEOUT);
-      }
-      return;
-    }
-  }
-  __syncwarp();
-  const int from = tile - step * (depth + 1);
-  if (from >= 0 && from < a.n_tiles) {
-    const float* p = a.value + (base + from) * kGroup<E> + lane * V;
+    bool all = true;
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = __ldcg(p + j);
-  }
-#pragma unroll 4
-  for (int i = depth; i > 0; --i) {
-    const float2* m = a.map + (base + tile - step * i) * kGroup<E> + lane * V;
+    for (int i = 0; i < kRun - 1; ++i) all = all && m[i].x != kNotYet && m[i].y != kNotYet;
+    if (__all_sync(kFull, all)) break;
+    if (give_up()) return 0.f;
 #pragma unroll
-    for (int j = 0; j < V; j += 2) {
-      const float4 q = __ldcg(reinterpret_cast<const float4*>(m + j));
-      v[j] = fmaf(q.x, v[j], q.y);
-      v[j + 1] = fmaf(q.z, v[j + 1], q.w);
-    }
+    for (int i = 0; i < kRun - 1; ++i)
+      if (m[i].x == kNotYet || m[i].y == kNotYet) m[i] = load_pair(maps - (i + 1) * G);
   }
-}
 
-template <class E>
-__device__ __forceinline__ void publish_map(const Args<E>& a, int group, int tile, int lane, const float (&A)[kLaneCh<E>],
-                                            const float (&B)[kLaneCh<E>]) {
-  const int64_t at = static_cast<int64_t>(group) * a.n_tiles + tile;
-  float2* m = a.map + at * kGroup<E> + lane * kLaneCh<E>;
+  const int64_t rbase = static_cast<int64_t>(group) * a.n_runs;
+  float RA = A, RB = B;  // the run's map, where this tile ends it
+  const bool ends_run = behind == kRun - 1 && !last_of_all;
+  if (ends_run) {
+    RA = 1.f;
+    RB = 0.f;
 #pragma unroll
-  for (int j = 0; j < kLaneCh<E>; j += 2)
-    __stcg(reinterpret_cast<float4*>(m + j), make_float4(A[j], B[j], A[j + 1], B[j + 1]));
-  __threadfence();
-  __syncwarp();
-  if (lane == 0) store_flag(a.flag + at, 1);
-}
+    for (int i = kRun - 2; i >= 0; --i) {
+      const float p = __uint_as_float(m[i].x);
+      RB = i == kRun - 2 ? __uint_as_float(m[i].y) : apply_map(m[i], RB);
+      RA = i == kRun - 2 ? p : join_factor(p, RA);
+    }
+    RB = apply_map(A, B, RB);
+    RA = join_factor(A, RA);
+    store_pair(a.run_map + (rbase + run) * G + ch, RA, RB);
+  }
 
-template <class E>
-__device__ __forceinline__ void publish_value(const Args<E>& a, int group, int tile, int lane,
-                                              const float (&v)[kLaneCh<E>]) {
-  const int64_t at = static_cast<int64_t>(group) * a.n_tiles + tile;
-  float* p = a.value + at * kGroup<E> + lane * kLaneCh<E>;
+  // the value in front of the run
+  float v = 0.f;
+  if (run > 0) {
+    int depth = 0;  // run maps to apply
+    const int ch0 = ch - lane;
+    while (true) {
+      const int mine = run - 1 - depth - lane;
+      const bool has_value = mine < 0 || load_word(a.run_value + (rbase + mine) * G + ch0) != kNotYet;
+      const bool has_map = mine < 0 || load_word(a.run_map + (rbase + mine) * G + ch0) != kNotYet;
+      const uint32_t done = __ballot_sync(kFull, has_value), some = __ballot_sync(kFull, has_value || has_map);
+      const uint32_t before = done != 0 ? (done & -done) - 1u : kFull;  // the lanes nearer than the first value
+      if ((some & before) == before) {
+        if (done != 0) {
+          depth += __ffs(done) - 1;
+          break;
+        }
+        depth += 32;
+        continue;
+      }
+      depth = 0;
+      if (give_up()) return 0.f;
+    }
+    const int from = run - 1 - depth;
+    if (from >= 0) {
+      const float* p = a.run_value + (rbase + from) * G + ch;
+      uint32_t w = load_word(p);
+      while (!__all_sync(kFull, w != kNotYet)) {
+        if (give_up()) return 0.f;
+        w = load_word(p);
+      }
+      v = __uint_as_float(w);
+    }
+    constexpr int kBatch = 8;
+    for (int r0 = from + 1; r0 < run; r0 += kBatch) {
+      uint2 w[kBatch];
+      const float2* p = a.run_map + (rbase + r0) * G + ch;
 #pragma unroll
-  for (int j = 0; j < kLaneCh<E>; ++j) __stcg(p + j, v[j]);
-  __threadfence();
-  __syncwarp();
-  if (lane == 0) store_flag(a.flag + at, 2);
+      for (int b = 0; b < kBatch; ++b) w[b] = r0 + b < run ? load_pair(p + b * G) : make_uint2(0u, 0u);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (r0 + b >= run) break;
+        while (!__all_sync(kFull, w[b].x != kNotYet && w[b].y != kNotYet)) {
+          if (give_up()) return 0.f;
+          w[b] = load_pair(p + b * G);
+        }
+        v = apply_map(w[b], v);
+      }
+    }
+  }
+  if (ends_run) store_word(a.run_value + (rbase + run) * G + ch, apply_map(RA, RB, v));
+#pragma unroll
+  for (int i = kRun - 2; i >= 0; --i)
+    if (i < behind) v = apply_map(m[i], v);
+  return v;
 }
 
 // The block's number in walking order.
@@ -390,7 +466,7 @@ __device__ __forceinline__ int take_ticket(int32_t* ticket, int32_t* shared) {
 // waits.
 constexpr int kWarps = 8, kSteps = 8;
 constexpr int kTile = kWarps * kSteps;
-static_assert(ENGRAM_RECURRENCE_TILE % kTile == 0, "saved states fall on tiles");
+static_assert(ENGRAM_RECURRENCE_TILE == kTile, "a state is saved in front of every tile");
 
 template <class E, bool kVec>
 __global__ void __launch_bounds__(kWarps * 32, 5) forward_kernel(Args<E> a) {
@@ -411,6 +487,11 @@ __global__ void __launch_bounds__(kWarps * 32, 5) forward_kernel(Args<E> a) {
   fetch_rows<E, kVec, kSteps>(xw, a.x, a.x_stride, tw, a.n_tokens, c0, a.dim, lane);
   const Marks mk = marks_of<E, kSteps>(a, tw, lane);
   wait_rows();
+
+  for (uint32_t dead = ~mk.live & ((1u << kSteps) - 1u); dead != 0; dead &= dead - 1u) {
+    const int k = __ffs(dead) - 1;
+    put_neutral<E>(gw + k * kRowBytes, xw + k * kRowBytes, lane);
+  }
 
   // s <- f s + u x; a sequence's first position starts from its own state
   float s[V], A[V];
@@ -438,16 +519,22 @@ __global__ void __launch_bounds__(kWarps * 32, 5) forward_kernel(Args<E> a) {
     mul_v<V>(u, xv, xv);
     fma_v<V>(f, s, xv, s);
   };
+  if (mk.first == 0) {  // the usual case, without branches
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
-    if (mk.first >> k & 1u) {
-      begin(k);
-      if (goes_on(k)) put_lane<E>(mapA[warp], lane, s);
-    }
-    if (mk.live >> k & 1u) {
+    for (int k = 0; k < kSteps; ++k) {
       float f[V];
       advance(k, f);
       mul_v<V>(A, f, A);
+    }
+  } else {
+#pragma unroll 1
+    for (int k = 0; k < kSteps; ++k) {
+      if (mk.first >> k & 1u) {
+        begin(k);
+        if (goes_on(k)) put_lane<E>(mapA[warp], lane, s);
+      }
+      float f[V];
+      advance(k, f);
     }
   }
   if (mk.first == 0) put_lane<E>(mapA[warp], lane, A);
@@ -455,82 +542,55 @@ __global__ void __launch_bounds__(kWarps * 32, 5) forward_kernel(Args<E> a) {
   if (lane == 0) cuts[warp] = mk.first != 0;
   __syncthreads();
 
-  if (warp == 0) {
-    // the tile's map; from a warp in which a sequence begins nothing before counts
-    float B[V], v[V];
-    bool cut = false;
+  if (warp * 32 < G) {  // a lane per channel: the tile's map, and what comes into it and into every warp
+    const int ch = warp * 32 + lane;
+    float TA = 1.f, TB = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      float p[V], q[V];
-      get_lane<E>(mapA[w], lane, p);
-      get_lane<E>(mapB[w], lane, q);
-      if (w == 0 || cuts[w]) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          A[j] = p[j];
-          B[j] = q[j];
-        }
-        cut |= cuts[w];
-      } else {
-        fma_v<V>(p, B, q, B);
-        mul_v<V>(p, A, A);
-      }
+      const float p = cuts[w] ? kCut : mapA[w][ch];
+      TB = apply_map(p, mapB[w][ch], TB);
+      TA = join_factor(p, TA);
     }
-    const bool more = tile + 1 < a.n_tiles;
-    if (more) {
-      if (cut) publish_value<E>(a, group, tile, lane, B);
-      else if (tile > 0) publish_map<E>(a, group, tile, lane, A, B);
-    }
-    if (tile == 0 || mk.first & 1u) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = 0.f;
-    } else {
-      look_back<E>(a, group, tile, 1, lane, v);
-    }
-    if (more && !cut) {
-      fma_v<V>(A, v, B, B);
-      publish_value<E>(a, group, tile, lane, B);
-    }
-    if (a.carry != nullptr && t0 % ENGRAM_RECURRENCE_TILE == 0)
-      store_state<E>(a.carry + static_cast<int64_t>(t0 / ENGRAM_RECURRENCE_TILE) * a.dim, c, a.dim, v);
-    // the state that comes into every warp, in the place of its B
+    float v = come_in<E>(a, group, tile, ch, TA, TB);
+    if (a.carry != nullptr && c0 + ch < a.dim) a.carry[static_cast<int64_t>(tile) * a.dim + c0 + ch] = v;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      float p[V], q[V];
-      get_lane<E>(mapA[w], lane, p);
-      get_lane<E>(mapB[w], lane, q);
-      put_lane<E>(mapB[w], lane, v);
-      if (cuts[w]) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = q[j];
-      } else {
-        fma_v<V>(p, v, q, v);
-      }
+      const float q = mapB[w][ch];
+      mapB[w][ch] = v;
+      v = apply_map(cuts[w] ? kCut : mapA[w][ch], q, v);
     }
   }
   __syncthreads();
 
   get_lane<E>(mapB[warp], lane, s);
   typename E::T* y = a.y + tw * a.y_stride;
+  const bool plain = (mk.first | mk.last) == 0 && tw + kSteps <= a.n_tokens;
+  if (plain) {
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
-    if (tw + k >= a.n_tokens) break;
-    if (mk.first >> k & 1u) {
-      if (goes_on(k)) get_lane<E>(mapA[warp], lane, s);
-      else begin(k);
-    }
-    float out[V] = {};
-    if (mk.live >> k & 1u) {
-      float f[V];
+    for (int k = 0; k < kSteps; ++k) {
+      float f[V], out[V];
       advance(k, f);
 #pragma unroll
-      for (int j = 0; j < V; ++j) out[j] = s[j];
+      for (int j = 0; j < V; ++j) out[j] = mk.live >> k & 1u ? s[j] : 0.f;
+      store_row<E, kVec>(y + k * a.y_stride, c, a.dim, out);
     }
-    store_row<E, kVec>(y + k * a.y_stride, c, a.dim, out);
-    if (mk.last >> k & 1u) {
-      const int32_t slot = a.slot[tw + k];
-      if (slot >= 0 && a.state_out != nullptr)
-        store_state<E>(a.state_out + static_cast<int64_t>(slot) * a.dim, c, a.dim, s);
+  } else {
+#pragma unroll 1
+    for (int k = 0; k < kSteps && tw + k < a.n_tokens; ++k) {
+      if (mk.first >> k & 1u) {
+        if (goes_on(k)) get_lane<E>(mapA[warp], lane, s);
+        else begin(k);
+      }
+      float f[V], out[V];
+      advance(k, f);
+#pragma unroll
+      for (int j = 0; j < V; ++j) out[j] = mk.live >> k & 1u ? s[j] : 0.f;
+      store_row<E, kVec>(y + k * a.y_stride, c, a.dim, out);
+      if (mk.last >> k & 1u) {
+        const int32_t slot = a.slot[tw + k];
+        if (slot >= 0 && a.state_out != nullptr)
+          store_state<E>(a.state_out + static_cast<int64_t>(slot) * a.dim, c, a.dim, s);
+      }
     }
   }
 }
@@ -579,6 +639,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) backward_kernel(Args<E> a) {
   load_state<E>(a.carry + static_cast<int64_t>(tile) * a.dim, c, a.dim, carry);
   wait_rows();
 
+  for (uint32_t dead = ~mk.live & ((1u << kSteps) - 1u); dead != 0; dead &= dead - 1u) {
+    const int k = __ffs(dead) - 1;
+    put_neutral<E>(gw + k * kRowBytes, xw + k * kRowBytes, lane);
+    *reinterpret_cast<uint2*>(dw + k * kRowBytes + lane * 8) = make_uint2(0u, 0u);
+  }
+
   float s[V], A[V], C[V];
   auto begin = [&](int k) {
 #pragma unroll
@@ -586,35 +652,48 @@ __global__ void __launch_bounds__(kWarps * 32, 3) backward_kernel(Args<E> a) {
     const int32_t slot = a.slot[tw + k];
     if (slot >= 0 && a.state != nullptr) load_state<E>(a.state + static_cast<int64_t>(slot) * a.dim, c, a.dim, s);
   };
+  auto advance = [&](int k, float (&xv)[V], float (&f)[V], float (&u)[V]) {
+    float gv[V], b[V];
+    lane_row<E>(gw + k * kRowBytes, lane, gv);
+    lane_row<E>(xw + k * kRowBytes, lane, xv);
+    gates<E>(gv, f, u);
+    mul_v<V>(u, xv, b);
+    fma_v<V>(f, s, b, s);
+  };
+  auto pass_back = [&](int k, const float (&f)[V]) {
+    float dv[V];
+    lane_row<E>(dw + k * kRowBytes, lane, dv);
+    mul_v<V>(A, f, A);
+    fma_v<V>(A, dv, C, C);
+  };
   auto from_before = [&](int k) { return (mk.first & ((2u << k) - 1u)) == 0u; };
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     A[j] = 1.f;
     s[j] = C[j] = 0.f;
   }
+  const bool straight = (mk.first | mk.last) == 0 && tw + kSteps <= a.n_tokens;  // the usual case, without branches
+  if (straight) {
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
-    if (mk.first >> k & 1u) begin(k);
-    if (mk.live >> k & 1u) {
-      float gv[V], xv[V], f[V], u[V];
-      lane_row<E>(gw + k * kRowBytes, lane, gv);
-      lane_row<E>(xw + k * kRowBytes, lane, xv);
-      gates<E>(gv, f, u);
-      mul_v<V>(u, xv, xv);
-      fma_v<V>(f, s, xv, s);
-      if (from_before(k)) {  // nothing is passed back over a sequence's beginning
-        float dv[V];
-        lane_row<E>(dw + k * kRowBytes, lane, dv);
-        mul_v<V>(A, f, A);
-        fma_v<V>(A, dv, C, C);
-      }
+    for (int k = 0; k < kSteps; ++k) {
+      float xv[V], f[V], u[V];
+      advance(k, xv, f, u);
+      pass_back(k, f);
     }
-    if ((mk.last >> k & 1u) && from_before(k)) {
-      float l[V] = {};
-      const int32_t slot = a.slot[tw + k];
-      if (slot >= 0 && a.dstate != nullptr) load_state<E>(a.dstate + static_cast<int64_t>(slot) * a.dim, c, a.dim, l);
-      put_lane<E>(held[warp], lane, l);
-      fma_v<V>(A, l, C, C);
+  } else {
+#pragma unroll 1
+    for (int k = 0; k < kSteps; ++k) {
+      if (mk.first >> k & 1u) begin(k);
+      float xv[V], f[V], u[V];
+      advance(k, xv, f, u);
+      if (from_before(k)) pass_back(k, f);  // nothing is passed back over a sequence's beginning
+      if ((mk.last >> k & 1u) && from_before(k)) {
+        float l[V] = {};
+        const int32_t slot = a.slot[tw + k];
+        if (slot >= 0 && a.dstate != nullptr) load_state<E>(a.dstate + static_cast<int64_t>(slot) * a.dim, c, a.dim, l);
+        put_lane<E>(held[warp], lane, l);
+        fma_v<V>(A, l, C, C);
+      }
     }
   }
   put_lane<E>(mapA[warp], lane, A);
@@ -623,54 +702,21 @@ __global__ void __launch_bounds__(kWarps * 32, 3) backward_kernel(Args<E> a) {
   if (lane == 0) cuts[warp] = mk.first != 0;
   __syncthreads();
 
-  if (warp == 0) {
-    float v[V];
-    bool cut = false;
+  if (warp * 32 < G) {  // a lane per channel, from behind: the tile's map, and what comes into it and into every warp
+    const int ch = warp * 32 + lane;
+    float TA = 1.f, TC = 0.f;
 #pragma unroll
     for (int w = kWarps - 1; w >= 0; --w) {
-      float p[V], q[V];
-      get_lane<E>(mapA[w], lane, p);
-      get_lane<E>(mapC[w], lane, q);
-      if (w == kWarps - 1 || cuts[w]) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          A[j] = p[j];
-          C[j] = q[j];
-        }
-        cut |= cuts[w];
-      } else {
-        fma_v<V>(p, C, q, C);
-        mul_v<V>(p, A, A);
-      }
+      const float p = cuts[w] ? kCut : mapA[w][ch];
+      TC = apply_map(p, mapC[w][ch], TC);
+      TA = join_factor(p, TA);
     }
-    const bool ends = tile + 1 == a.n_tiles, more = tile > 0;
-    if (more) {
-      if (cut) publish_value<E>(a, group, tile, lane, C);
-      else if (!ends) publish_map<E>(a, group, tile, lane, A, C);
-    }
-    if (ends) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = 0.f;
-    } else {
-      look_back<E>(a, group, tile, -1, lane, v);
-    }
-    if (more && !cut) {
-      fma_v<V>(A, v, C, C);
-      publish_value<E>(a, group, tile, lane, C);
-    }
-    // what comes into every warp from behind, in the place of its C
+    float v = come_in<E>(a, group, back, ch, TA, TC);
 #pragma unroll
     for (int w = kWarps - 1; w >= 0; --w) {
-      float p[V], q[V];
-      get_lane<E>(mapA[w], lane, p);
-      get_lane<E>(mapC[w], lane, q);
-      put_lane<E>(mapC[w], lane, v);
-      if (cuts[w]) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = q[j];
-      } else {
-        fma_v<V>(p, v, q, v);
-      }
+      const float q = mapC[w][ch];
+      mapC[w][ch] = v;
+      v = apply_map(cuts[w] ? kCut : mapA[w][ch], q, v);
     }
   }
   // meanwhile the other warps walk their positions in ascending order
@@ -688,25 +734,27 @@ __global__ void __launch_bounds__(kWarps * 32, 3) backward_kernel(Args<E> a) {
     }
   }
   float w[kSteps][V];
+  auto ascend = [&](int k) {
+    float xv[V], f[V], u[V], before[V], code[V];
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
-    if (mk.first >> k & 1u) begin(k);
-    if (mk.live >> k & 1u) {
-      float gv[V], xv[V], f[V], u[V], code[V];
-      lane_row<E>(gw + k * kRowBytes, lane, gv);
-      lane_row<E>(xw + k * kRowBytes, lane, xv);
-      gates<E>(gv, f, u);
+    for (int j = 0; j < V; ++j) before[j] = s[j];
+    advance(k, xv, f, u);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        w[k][j] = f[j] * u[j] * (s[j] - xv[j]);
-        code[j] = f[j] <= u[j] ? -f[j] : u[j];
-      }
-      mul_v<V>(u, xv, xv);
-      fma_v<V>(f, s, xv, s);
-      float* c0p = reinterpret_cast<float*>(gw + k * kRowBytes + lane * 8);
-      float* c1p = reinterpret_cast<float*>(xw + k * kRowBytes + lane * 8);
-      *reinterpret_cast<float2*>(c0p) = make_float2(code[0], code[1]);
-      if constexpr (V == 4) *reinterpret_cast<float2*>(c1p) = make_float2(code[2], code[3]);
+    for (int j = 0; j < V; ++j) {
+      w[k][j] = f[j] * u[j] * (before[j] - xv[j]);
+      code[j] = f[j] <= u[j] ? -f[j] : u[j];
+    }
+    *reinterpret_cast<float2*>(gw + k * kRowBytes + lane * 8) = make_float2(code[0], code[1]);
+    if constexpr (V == 4) *reinterpret_cast<float2*>(xw + k * kRowBytes + lane * 8) = make_float2(code[2], code[3]);
+  };
+  if (straight) {
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) ascend(k);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      if (mk.first >> k & 1u) begin(k);
+      ascend(k);
     }
   }
   __syncthreads();
@@ -715,47 +763,53 @@ __global__ void __launch_bounds__(kWarps * 32, 3) backward_kernel(Args<E> a) {
   get_lane<E>(mapC[warp], lane, m);
   typename E::T* dx = a.dx + tw * a.dx_stride;
   typename E::T* dg = a.dg + tw * a.dg_stride;
-#pragma unroll
-  for (int k = kSteps - 1; k >= 0; --k) {
-    if (tw + k >= a.n_tokens) continue;
-    if (mk.last >> k & 1u) {
-      if (from_before(k)) {
-        get_lane<E>(held[warp], lane, m);
-      } else {
-        const int32_t slot = a.slot[tw + k];
-#pragma unroll
-        for (int j = 0; j < V; ++j) m[j] = 0.f;
-        if (slot >= 0 && a.dstate != nullptr) load_state<E>(a.dstate + static_cast<int64_t>(slot) * a.dim, c, a.dim, m);
-      }
+  auto descend = [&](int k) {
+    float dv[V], code[V], ox[V], og[V];
+    lane_row<E>(dw + k * kRowBytes, lane, dv);
+    const float2 lo = *reinterpret_cast<const float2*>(gw + k * kRowBytes + lane * 8);
+    code[0] = lo.x;
+    code[1] = lo.y;
+    if constexpr (V == 4) {
+      const float2 hi = *reinterpret_cast<const float2*>(xw + k * kRowBytes + lane * 8);
+      code[2] = hi.x;
+      code[3] = hi.y;
     }
-    float ox[V] = {}, og[V] = {};
-    if (mk.live >> k & 1u) {
-      float dv[V], code[V];
-      lane_row<E>(dw + k * kRowBytes, lane, dv);
-      const float2 lo = *reinterpret_cast<const float2*>(gw + k * kRowBytes + lane * 8);
-      code[0] = lo.x;
-      code[1] = lo.y;
-      if constexpr (V == 4) {
-        const float2 hi = *reinterpret_cast<const float2*>(xw + k * kRowBytes + lane * 8);
-        code[2] = hi.x;
-        code[3] = hi.y;
-      }
+    const bool live = mk.live >> k & 1u;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float l = dv[j] + m[j], small = fabsf(code[j]), big = 1.f - small;
-        const bool neg = signbit(code[j]);
-        ox[j] = l * (neg ? big : small);
-        og[j] = l * w[k][j];
-        m[j] = l * (neg ? small : big);
-      }
+    for (int j = 0; j < V; ++j) {
+      const float l = dv[j] + m[j], small = fabsf(code[j]), big = 1.f - small;
+      const bool neg = signbit(code[j]);
+      ox[j] = live ? l * (neg ? big : small) : 0.f;
+      og[j] = live ? l * w[k][j] : 0.f;
+      m[j] = l * (neg ? small : big);
     }
     store_row<E, kVec>(dx + k * a.dx_stride, c, a.dim, ox);
     store_row<E, kVec>(dg + k * a.dg_stride, c, a.dim, og);
-    if (mk.first >> k & 1u) {
-      const int32_t slot = a.slot[tw + k];
-      if (slot >= 0 && a.dstate != nullptr) store_state<E>(a.dstate + static_cast<int64_t>(slot) * a.dim, c, a.dim, m);
+  };
+  if (straight) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) m[j] = 0.f;
+    for (int k = kSteps - 1; k >= 0; --k) descend(k);
+  } else {
+#pragma unroll
+    for (int k = kSteps - 1; k >= 0; --k) {
+      if (tw + k >= a.n_tokens) continue;
+      if (mk.last >> k & 1u) {
+        if (from_before(k)) {
+          get_lane<E>(held[warp], lane, m);
+        } else {
+          const int32_t slot = a.slot[tw + k];
+#pragma unroll
+          for (int j = 0; j < V; ++j) m[j] = 0.f;
+          if (slot >= 0 && a.dstate != nullptr) load_state<E>(a.dstate + static_cast<int64_t>(slot) * a.dim, c, a.dim, m);
+        }
+      }
+      descend(k);
+      if (mk.first >> k & 1u) {
+        const int32_t slot = a.slot[tw + k];
+        if (slot >= 0 && a.dstate != nullptr) store_state<E>(a.dstate + static_cast<int64_t>(slot) * a.dim, c, a.dim, m);
+#pragma unroll
+        for (int j = 0; j < V; ++j) m[j] = 0.f;
+      }
     }
   }
 }
@@ -798,15 +852,13 @@ __global__ void __launch_bounds__(kThreads) step_kernel(Args<E> a) {
   store_row<E, kVec>(a.y + b * a.y_stride, c, a.dim, s);
 }
 
-// The parts of the scans' workspace: counters and flags (zeroed before each
-// scan), the positions' marks, then the tiles' maps and values.
+// The parts of the scans' workspace: the counters, the positions' marks, then
+// the tiles' maps and values.
 struct ScanSpace {
   int32_t* ticket;
-  int32_t* flag;
   uint8_t* flags;
   int32_t* slot;
-  float2* map;
-  float* value;
+  float* words;
   size_t bytes;
 };
 
@@ -818,16 +870,14 @@ ScanSpace scan_space(void* base, int64_t n_tokens, int32_t dim) {
   ScanSpace s;
   char* p = static_cast<char*>(base);
   s.ticket = reinterpret_cast<int32_t*>(p);
-  s.flag = s.ticket + 2;
-  size_t at = round256((2 + tiles * groups) * 4);
+  size_t at = 256;
   s.flags = reinterpret_cast<uint8_t*>(p + at);
   at += round256(static_cast<size_t>(n_tokens));
   s.slot = reinterpret_cast<int32_t*>(p + at);
   at += round256(static_cast<size_t>(n_tokens) * 4);
-  s.map = reinterpret_cast<float2*>(p + at);
-  at += round256(tiles * groups * kNarrow * 8);
-  s.value = reinterpret_cast<float*>(p + at);
-  s.bytes = at + round256(tiles * groups * kNarrow * 4);
+  s.words = reinterpret_cast<float*>(p + at);
+  const size_t runs = (tiles + kRun - 1) / kRun;
+  s.bytes = at + round256((tiles * 8 + runs * 12) * groups * kNarrow);
   return s;
 }
 
@@ -890,16 +940,20 @@ int launch_scan(Args<E>& a, bool backward, void* workspace, int sms, cudaStream_
   a.n_tiles = (a.n_tokens + kTile - 1) / kTile;
   a.n_groups = (a.dim + kGroup<E> - 1) / kGroup<E>;
   a.ticket = w.ticket;
-  a.flag = w.flag;
   a.flags = w.flags;
   a.slot = w.slot;
-  a.map = w.map;
-  a.value = w.value;
   const int64_t blocks = static_cast<int64_t>(a.n_tiles) * a.n_groups;
   if (blocks > 0x7fffff00) return fail(ENGRAM_E_RANGE, "too many positions times channels");
   const bool move_empty = !backward && a.state_out != nullptr && a.state_out != a.state;
-  const int64_t want = ((a.n_tokens > blocks ? a.n_tokens : blocks) + 255) / 256, cap = static_cast<int64_t>(sms) * 4;
-  mark_kernel<E><<<static_cast<int>(want < cap ? want : cap), 256, 0, st>>>(a, 2 + blocks, move_empty);
+  a.n_runs = (a.n_tiles + kRun - 1) / kRun;
+  const int64_t tile_words = blocks * kGroup<E>, run_words = static_cast<int64_t>(a.n_runs) * a.n_groups * kGroup<E>;
+  a.map = reinterpret_cast<float2*>(w.words);
+  a.run_map = a.map + tile_words;
+  a.run_value = reinterpret_cast<float*>(a.run_map + run_words);
+  const int64_t cleared = (2 * tile_words + 3 * run_words) / 4;  // kGroup is a multiple of 4
+  const int64_t want = ((a.n_tokens > cleared ? a.n_tokens : cleared) + 255) / 256, cap = static_cast<int64_t>(sms) * 8;
+  mark_kernel<E><<<static_cast<int>(want < cap ? want : cap), 256, 0, st>>>(a, reinterpret_cast<uint4*>(w.words), cleared,
+                                                                          move_empty);
   int rc = check_launch("mark_kernel");
   if (rc) return rc;
   bool vec = a.dim * E::kBytes % 16 == 0 && rows16<E>(a.x, a.x_stride) && rows16<E>(a.g, a.g_stride);
@@ -979,7 +1033,7 @@ extern "C" int engram_recurrence(const void* x_d, int64_t x_stride, const void* 
     if (n_tokens > 0) return launch_scan<E>(a, false, workspace_d, sms, as_stream(stream));
     if (state_out_d == nullptr || state_out_d == state_d) return static_cast<int>(ENGRAM_OK);
     const int64_t cap = static_cast<int64_t>(sms) * 4;
-    mark_kernel<E><<<static_cast<int>(n_seqs < cap ? n_seqs : cap), 256, 0, as_stream(stream)>>>(a, 0, true);
+    mark_kernel<E><<<static_cast<int>(n_seqs < cap ? n_seqs : cap), 256, 0, as_stream(stream)>>>(a, nullptr, 0, true);
     return check_launch("mark_kernel");
   };
   return type == ENGRAM_T_BF16 ? go(train::Bf16{}) : go(train::F32{});
