@@ -34,19 +34,18 @@ constexpr int kRowBytes = 256;
 
 // f = sigmoid(g) and u = sigmoid(-g) of two channels.
 //
-// bf16 data: with e = 2^min(-g log2 e, 60), f = 1 / (1 + e) and u = e / (1 + e),
-// neither of which cancels; one reciprocal of (1 + e0)(1 + e1) serves both
-// channels.  The hardware's base-2 exponential and reciprocal (2^-22 and 2^-23
-// relative, plus |g| 2^-24 from rounding the exponent) are far below the data's
-// own rounding; the clamp leaves f = 2^-60 where it would be smaller.
+// bf16 data: with e = exp(-g), f = 1 / (1 + e) and u = e / (1 + e), neither of
+// which cancels; one reciprocal of (1 + e0)(1 + e1) serves both channels.  g is
+// taken as at least -40 (gate_row), so that the product stays in range: f is
+// 4e-18 where it would be smaller.  The hardware's base-2 exponential and
+// reciprocal (2^-22 and 2^-23 relative, plus |g| 2^-24 from rounding the
+// exponent) are far below the data's own rounding.
 // fp32 data: expf and the rounded reciprocal, on exp(-|g|).
 template <class E>
 __device__ __forceinline__ void gates2(float g0, float g1, float (&f)[2], float (&u)[2]) {
   if constexpr (E::kBytes == 2) {
     float t0, t1, e0, e1, r, d0, d1;
     f2_split(f2_mul(f2(g0, g1), f2(-1.4426950408889634f, -1.4426950408889634f)), t0, t1);
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(t0) : "f"(t0), "f"(60.f));
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(t1) : "f"(t1), "f"(60.f));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t0));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t1));
     f2_split(f2_add(f2(e0, e1), f2(1.f, 1.f)), d0, d1);
@@ -138,15 +137,26 @@ __device__ __forceinline__ void fetch_rows(unsigned char* dst, const typename E:
                                            int c0, int dim, int lane) {
   if constexpr (kVec) {
     constexpr int N = 16 / E::kBytes;
-    const int c = c0 + (lane & 15) * N;
+    const int c = c0 + (lane & 15) * N, r0 = lane >> 4;
+    const typename E::T* p = src + (t + r0) * stride + c;
+    const uint32_t d = smem_u32(dst + r0 * kRowBytes + (lane & 15) * 16);
+    if (t + kSteps <= n_tokens) {
+      const int bytes = c < dim ? 16 : 0;
+      if (c >= dim) p = src;
+      const int64_t two = c < dim ? 2 * stride : 0;
 #pragma unroll
-    for (int k = 0; k < kSteps; k += 2) {
-      const int r = k + (lane >> 4);
-      const bool ok = t + r < n_tokens && c < dim;
-      const typename E::T* p = ok ? src + (t + r) * stride + c : src;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + r * kRowBytes + (lane & 15) * 16)),
-                   "l"(p), "r"(ok ? 16 : 0)
-                   : "memory");
+      for (int k = 0; k < kSteps; k += 2) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + k * kRowBytes), "l"(p), "r"(bytes) : "memory");
+        p += two;
+      }
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < kSteps; k += 2) {
+        const bool ok = t + r0 + k < n_tokens && c < dim;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + k * kRowBytes),
+                     "l"(ok ? p + k * stride : src), "r"(ok ? 16 : 0)
+                     : "memory");
+      }
     }
   } else {
     typename E::T* d = reinterpret_cast<typename E::T*>(dst);
@@ -167,8 +177,7 @@ __device__ __forceinline__ void wait_rows() {
 }
 
 template <class E>
-__device__ __forceinline__ void lane_row(const unsigned char* row, int lane, float (&v)[kLaneCh<E>]) {
-  const uint2 w = *reinterpret_cast<const uint2*>(row + lane * 8);
+__device__ __forceinline__ void spread(const uint2& w, float (&v)[kLaneCh<E>]) {
   if constexpr (E::kBytes == 2) {
     v[0] = __uint_as_float(w.x << 16);
     v[1] = __uint_as_float(w.x & 0xffff0000u);
@@ -178,6 +187,24 @@ __device__ __forceinline__ void lane_row(const unsigned char* row, int lane, flo
     v[0] = __uint_as_float(w.x);
     v[1] = __uint_as_float(w.y);
   }
+}
+
+template <class E>
+__device__ __forceinline__ void lane_row(const unsigned char* row, int lane, float (&v)[kLaneCh<E>]) {
+  spread<E>(*reinterpret_cast<const uint2*>(row + lane * 8), v);
+}
+// A row of g, with gates2's lower bound for bf16.
+template <class E>
+__device__ __forceinline__ uint2 bounded(uint2 w) {
+  if constexpr (E::kBytes == 2) {
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.x) : "r"(0xc220c220u));  // -40
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.y) : "r"(0xc220c220u));
+  }
+  return w;
+}
+template <class E>
+__device__ __forceinline__ void gate_row(const unsigned char* row, int lane, float (&v)[kLaneCh<E>]) {
+  spread<E>(bounded<E>(*reinterpret_cast<const uint2*>(row + lane * 8)), v);
 }
 
 template <class E, bool kVec>
@@ -456,23 +483,28 @@ __device__ __forceinline__ int take_ticket(int32_t* ticket, int32_t* shared) {
 
 // --------------------------------------------------------------------- forward
 
-// A block handles kWarps * kSteps positions of one group of channels, in one
+// A block handles kFwdTile positions of one group of channels, in one
 // pass over memory: every warp fetches its rows into shared memory and reduces
 // them to a map s -> A s + B per channel; one warp joins the maps, publishes
 // the block's, and looks back over the blocks before it for the state that
 // comes in; then the warps walk their positions again, from shared memory, and
 // write y.  The gates are computed twice rather than kept: that frees the
-// registers, so that five blocks fit an SM and their loads cover one another's
+// registers, so that three blocks fit an SM and their loads cover one another's
 // waits.
-constexpr int kWarps = 8, kSteps = 8;
-constexpr int kTile = kWarps * kSteps;
-static_assert(ENGRAM_RECURRENCE_TILE == kTile, "a state is saved in front of every tile");
+constexpr int kFwdTile = 128, kBwdTile = ENGRAM_RECURRENCE_TILE;  // a state is saved in front of every backward tile
+static_assert(kFwdTile % kBwdTile == 0, "saved states fall between a forward tile's warps");
+
+constexpr int kFwdWarps = 8;
 
 template <class E, bool kVec>
-__global__ void __launch_bounds__(kWarps * 32, 5) forward_kernel(Args<E> a) {
+__global__ void __launch_bounds__(kFwdWarps * 32, 3) forward_kernel(Args<E> a) {
+  constexpr int kWarps = kFwdWarps, kTile = kFwdTile, kSteps = kTile / kWarps;
   constexpr int V = kLaneCh<E>, G = kGroup<E>;
-  __shared__ __align__(16) unsigned char xs[kTile * kRowBytes], gs[kTile * kRowBytes];
-  __shared__ __align__(16) float mapA[kWarps][G], mapB[kWarps][G];
+  extern __shared__ __align__(16) unsigned char smem[];
+  unsigned char* xs = smem;
+  unsigned char* gs = xs + kTile * kRowBytes;
+  float(*mapA)[G] = reinterpret_cast<float(*)[G]>(gs + kTile * kRowBytes);
+  float(*mapB)[G] = mapA + kWarps;
   __shared__ bool cuts[kWarps];
   __shared__ int32_t number;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -488,7 +520,8 @@ __global__ void __launch_bounds__(kWarps * 32, 5) forward_kernel(Args<E> a) {
   const Marks mk = marks_of<E, kSteps>(a, tw, lane);
   wait_rows();
 
-  for (uint32_t dead = ~mk.live & ((1u << kSteps) - 1u); dead != 0; dead &= dead - 1u) {
+  constexpr uint32_t kAll = (1u << kSteps) - 1u;
+  for (uint32_t dead = ~mk.live & kAll; dead != 0; dead &= dead - 1u) {
     const int k = __ffs(dead) - 1;
     put_neutral<E>(gw + k * kRowBytes, xw + k * kRowBytes, lane);
   }
@@ -513,7 +546,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) forward_kernel(Args<E> a) {
   auto goes_on = [&](int k) { return (mk.last >> k) == 0u; };
   auto advance = [&](int k, float (&f)[V]) {
     float gv[V], xv[V], u[V];
-    lane_row<E>(gw + k * kRowBytes, lane, gv);
+    gate_row<E>(gw + k * kRowBytes, lane, gv);
     lane_row<E>(xw + k * kRowBytes, lane, xv);
     gates<E>(gv, f, u);
     mul_v<V>(u, xv, xv);
@@ -552,9 +585,10 @@ __global__ void __launch_bounds__(kWarps * 32, 5) forward_kernel(Args<E> a) {
       TA = join_factor(p, TA);
     }
     float v = come_in<E>(a, group, tile, ch, TA, TB);
-    if (a.carry != nullptr && c0 + ch < a.dim) a.carry[static_cast<int64_t>(tile) * a.dim + c0 + ch] = v;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
+      if (w * kSteps % kBwdTile == 0 && a.carry != nullptr && c0 + ch < a.dim && t0 + w * kSteps < a.n_tokens)
+        a.carry[static_cast<int64_t>((t0 + w * kSteps) / kBwdTile) * a.dim + c0 + ch] = v;
       const float q = mapB[w][ch];
       mapB[w][ch] = v;
       v = apply_map(cuts[w] ? kCut : mapA[w][ch], q, v);
@@ -568,12 +602,14 @@ __global__ void __launch_bounds__(kWarps * 32, 5) forward_kernel(Args<E> a) {
   if (plain) {
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
-      float f[V], out[V];
+      float f[V];
       advance(k, f);
-#pragma unroll
-      for (int j = 0; j < V; ++j) out[j] = mk.live >> k & 1u ? s[j] : 0.f;
-      store_row<E, kVec>(y + k * a.y_stride, c, a.dim, out);
+      store_row<E, kVec>(y, c, a.dim, s);
+      y += a.y_stride;
     }
+    const float zeros[V] = {};
+    for (uint32_t dead = ~mk.live & kAll; dead != 0; dead &= dead - 1u)  // over what was just written
+      store_row<E, kVec>(a.y + (tw + __ffs(dead) - 1) * a.y_stride, c, a.dim, zeros);
   } else {
 #pragma unroll 1
     for (int k = 0; k < kSteps && tw + k < a.n_tokens; ++k) {
@@ -595,6 +631,9 @@ __global__ void __launch_bounds__(kWarps * 32, 5) forward_kernel(Args<E> a) {
   }
 }
 
+template <class E>
+constexpr int kFwdSmem = 2 * kFwdTile * kRowBytes + 2 * kFwdWarps * kGroup<E> * 4;
+
 // -------------------------------------------------------------------- backward
 
 // The same scheme walked from the last tile to the first.  With m_t = f_t l_t,
@@ -606,8 +645,11 @@ __global__ void __launch_bounds__(kWarps * 32, 5) forward_kernel(Args<E> a) {
 // known in descending order: the ascending walk leaves w = f u (s_{t-1} - x)
 // in registers and the gates in the place of x and g in shared memory, the
 // smaller of f and u standing for both (u, or -f).
+constexpr int kBwdWarps = 8;
+
 template <class E, bool kVec>
-__global__ void __launch_bounds__(kWarps * 32, 3) backward_kernel(Args<E> a) {
+__global__ void __launch_bounds__(kBwdWarps * 32, 3) backward_kernel(Args<E> a) {
+  constexpr int kWarps = kBwdWarps, kTile = kBwdTile, kSteps = kTile / kWarps;
   constexpr int V = kLaneCh<E>, G = kGroup<E>;
   extern __shared__ __align__(16) unsigned char smem[];
   unsigned char* xs = smem;
@@ -654,7 +696,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) backward_kernel(Args<E> a) {
   };
   auto advance = [&](int k, float (&xv)[V], float (&f)[V], float (&u)[V]) {
     float gv[V], b[V];
-    lane_row<E>(gw + k * kRowBytes, lane, gv);
+    gate_row<E>(gw + k * kRowBytes, lane, gv);
     lane_row<E>(xw + k * kRowBytes, lane, xv);
     gates<E>(gv, f, u);
     mul_v<V>(u, xv, b);
@@ -815,7 +857,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) backward_kernel(Args<E> a) {
 }
 
 template <class E>
-constexpr int kBwdSmem = 3 * kTile * kRowBytes + 4 * kWarps * kGroup<E> * 4;
+constexpr int kBwdSmem = 3 * kBwdTile * kRowBytes + 4 * kBwdWarps * kGroup<E> * 4;
 
 // ------------------------------------------------------------------ other parts
 
@@ -832,12 +874,13 @@ __global__ void __launch_bounds__(kThreads) step_kernel(Args<E> a) {
   const typename E::T* gr = a.g + b * a.g_stride;
   if constexpr (kVec) {
     lane_row<E>(reinterpret_cast<const unsigned char*>(xr + c), 0, xv);
-    lane_row<E>(reinterpret_cast<const unsigned char*>(gr + c), 0, gv);
+    gate_row<E>(reinterpret_cast<const unsigned char*>(gr + c), 0, gv);
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       xv[j] = c + j < a.dim ? E::load(xr + c + j) : 0.f;
       gv[j] = c + j < a.dim ? E::load(gr + c + j) : 0.f;
+      if (E::kBytes == 2 && gv[j] < -40.f) gv[j] = -40.f;  // as in gate_row
     }
   }
   const int32_t slot = slot_of(a, b);
@@ -865,7 +908,7 @@ struct ScanSpace {
 // Sized for the narrower group, which serves both types.
 ScanSpace scan_space(void* base, int64_t n_tokens, int32_t dim) {
   constexpr int kNarrow = kGroup<train::F32>;
-  const size_t tiles = static_cast<size_t>((n_tokens + kTile - 1) / kTile);
+  const size_t tiles = static_cast<size_t>((n_tokens + kBwdTile - 1) / kBwdTile);  // the smaller of the two
   const size_t groups = static_cast<size_t>((dim + kNarrow - 1) / kNarrow) + 1;  // + 1: a bf16 group may be half empty
   ScanSpace s;
   char* p = static_cast<char*>(base);
@@ -907,29 +950,27 @@ template <class E, bool kVec>
 int launch_pass(const Args<E>& a, bool backward, int grid, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.blockDim = dim3((backward ? kBwdWarps : kFwdWarps) * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // launched while the marks are made
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  const int smem = backward ? kBwdSmem<E> : kFwdSmem<E>;
+  static std::atomic<uint64_t> attr_set[2] = {{0}, {0}};  // one bit per device: the shared-memory opt-in was made
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
   cudaError_t e;
-  if (!backward) {
-    e = cudaLaunchKernelEx(&cfg, forward_kernel<E, kVec>, a);
-  } else {
-    static std::atomic<uint64_t> attr_set{0};  // one bit per device: the shared-memory opt-in was made
-    int dev = 0;
-    cudaGetDevice(&dev);
-    const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
-    if (bit == 0 || !(attr_set.load(std::memory_order_relaxed) & bit)) {
-      e = cudaFuncSetAttribute(backward_kernel<E, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem<E>);
-      if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-      attr_set.fetch_or(bit, std::memory_order_relaxed);
-    }
-    cfg.dynamicSmemBytes = kBwdSmem<E>;
-    e = cudaLaunchKernelEx(&cfg, backward_kernel<E, kVec>, a);
+  if (bit == 0 || !(attr_set[backward].load(std::memory_order_relaxed) & bit)) {
+    e = backward ? cudaFuncSetAttribute(backward_kernel<E, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
+                 : cudaFuncSetAttribute(forward_kernel<E, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    attr_set[backward].fetch_or(bit, std::memory_order_relaxed);
   }
+  cfg.dynamicSmemBytes = smem;
+  e = backward ? cudaLaunchKernelEx(&cfg, backward_kernel<E, kVec>, a) : cudaLaunchKernelEx(&cfg, forward_kernel<E, kVec>, a);
   if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "recurrence launch: %s", cudaGetErrorString(e));
   return check_launch("recurrence");
 }
@@ -937,7 +978,8 @@ int launch_pass(const Args<E>& a, bool backward, int grid, cudaStream_t st) {
 template <class E>
 int launch_scan(Args<E>& a, bool backward, void* workspace, int sms, cudaStream_t st) {
   const ScanSpace w = scan_space(workspace, a.n_tokens, a.dim);
-  a.n_tiles = (a.n_tokens + kTile - 1) / kTile;
+  const int tile = backward ? kBwdTile : kFwdTile;
+  a.n_tiles = (a.n_tokens + tile - 1) / tile;
   a.n_groups = (a.dim + kGroup<E> - 1) / kGroup<E>;
   a.ticket = w.ticket;
   a.flags = w.flags;
