@@ -12,6 +12,7 @@ Build: ``python -m hashed_gram_conditional_gb300.build`` (or
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional, Sequence
@@ -984,7 +985,11 @@ def engram_selftest_mod(layout: Layout, layer: int, x: torch.Tensor) -> torch.Te
 # --------------------------------------------------------------------------- training operators
 
 
+# The checks below are written for short calls: a tensor that passes costs a
+# few attribute reads, one that does not goes to the function that says why.
+
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _need_rows(t: torch.Tensor, name: str, dtype, device, n_rows: int, width: int) -> int:
@@ -1006,78 +1011,114 @@ def _need_rows(t: torch.Tensor, name: str, dtype, device, n_rows: int, width: in
     return t.stride(0)
 
 
-def _elem_type(t: torch.Tensor, name: str) -> int:
+def _rows(t, name: str, dtype, like: torch.Tensor, idx: int, n_rows: int, width: int) -> int:
+    """_need_rows on the device (number idx) of `like`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == idx and t.shape == (n_rows, width):
+        ld, one = t.stride()
+        if one == 1 and ld >= width:
+            return ld
+    return _need_rows(t, name, dtype, like.device, n_rows, width)
+
+
+def _flat(t, name: str, dtype, like: torch.Tensor, idx: int, numel: Optional[int] = None) -> int:
+    """_need on the device (number idx) of `like`; returns the tensor's address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == idx and t.is_contiguous()
+            and (numel is None or t.numel() == numel)):
+        _need(t, name, dtype, like.device, numel)
+    return t.data_ptr()
+
+
+def _matrix(t, name: str) -> tuple:
+    """(element type, device number, rows, width, row stride) of a bf16 or f32 device matrix."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _TYPES:
+    ty = _TYPES.get(t.dtype)
+    if ty is None:
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    if not t.is_cuda:
+    idx = t.get_device()
+    if idx < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return _TYPES[t.dtype]
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    n, width = t.shape
+    return ty, idx, n, width, _rows(t, name, t.dtype, t, idx, n, width)
 
 
-def _ids_shape(ids: torch.Tensor, device) -> tuple:
-    _need(ids, "ids", torch.int32, device)
-    if ids.dim() not in (1, 2):
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _ids_shape(ids: torch.Tensor, like: torch.Tensor, idx: int) -> tuple:
+    _flat(ids, "ids", torch.int32, like, idx)
+    shape = ids.shape
+    if len(shape) == 2:
+        if shape[1] < 1:
+            raise ValueError("ids must have at least one column")
+        return shape
+    if len(shape) != 1:
         raise ValueError("ids must be [T] or [T][n_cols]")
-    if ids.dim() == 2 and ids.shape[1] < 1:
-        raise ValueError("ids must have at least one column")
-    return ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1
+    return shape[0], 1
+
+
+@functools.lru_cache(maxsize=1024)
+def _bytes_of(name: str, *sizes: int) -> int:
+    """A workspace's size, which depends on the call's sizes alone."""
+    return getattr(_load(), name)(*sizes)
 
 
 def engram_lookup(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
                   status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Rows of table (bf16 or f32 [R][D]) times scale: returns [T][n_cols*D]; ids int32 [T] or [T][n_cols],
     DEAD gives zeros."""
-    L = _load()
-    dev = table.device
-    ty = _elem_type(table, "table")
-    _need(table, "table", table.dtype)
-    if table.dim() != 2:
-        raise ValueError("table must be [rows][row_dim]")
-    R, D = table.shape
-    T, C = _ids_shape(ids, dev)
+    L = _lib or _load()
+    ty, idx, R, D, _ = _matrix(table, "table")
+    _flat(table, "table", table.dtype, table, idx)
+    T, C = _ids_shape(ids, table, idx)
     if out is None:
-        out = torch.empty((T, C * D), dtype=table.dtype, device=dev)
-    ld = _need_rows(out, "out", table.dtype, dev, T, C * D)
-    _check(L.engram_lookup(_ptr(table), ty, R, D, _ptr(ids), T, C, scale, _ptr(out), ld, _ptr(status), _stream(dev)),
-           "engram_lookup")
+        out = torch.empty((T, C * D), dtype=table.dtype, device=table.device)
+        ld = C * D
+    else:
+        ld = _rows(out, "out", table.dtype, table, idx, T, C * D)
+    rc = L.engram_lookup(table.data_ptr(), ty, R, D, ids.data_ptr(), T, C, scale, out.data_ptr(), ld, _addr(status),
+                         _raw_stream(idx))
+    if rc:
+        _check(rc, "engram_lookup")
     return out
 
 
 def lookup_grad_workspace(n_tokens: int, n_cols: int, row_dim: int, device) -> torch.Tensor:
-    n = _load().engram_lookup_grad_workspace_bytes(n_tokens, n_cols, row_dim)
+    n = _bytes_of("engram_lookup_grad_workspace_bytes", n_tokens, n_cols, row_dim)
     return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
 
 
 def _grad_args(dout: torch.Tensor, ids: torch.Tensor, workspace: Optional[torch.Tensor]):
-    """Checks shared by the lookup gradients; returns (type, stride, T, n_cols, D, workspace)."""
-    dev = dout.device
-    ty = _elem_type(dout, "dout")
-    T, C = _ids_shape(ids, dev)
-    if dout.dim() != 2 or dout.shape[1] % C or dout.shape[1] == 0:
+    """Checks shared by the lookup gradients; returns (type, device number, stride, T, n_cols, D, workspace)."""
+    ty, idx, n, width, ld = _matrix(dout, "dout")
+    T, C = _ids_shape(ids, dout, idx)
+    if n != T or width % C or width == 0:
         raise ValueError("dout must be [T][n_cols*row_dim]")
-    D = dout.shape[1] // C
-    ld = _need_rows(dout, "dout", dout.dtype, dev, T, C * D)
+    D = width // C
     if workspace is None:
-        workspace = lookup_grad_workspace(T, C, D, dev)
-    _need(workspace, "workspace", torch.uint8, dev)
-    return ty, ld, T, C, D, workspace
+        workspace = lookup_grad_workspace(T, C, D, dout.device)
+    else:
+        _flat(workspace, "workspace", torch.uint8, dout, idx)
+    return ty, idx, ld, T, C, D, workspace
 
 
 def engram_lookup_grad(dout: torch.Tensor, ids: torch.Tensor, total_rows: int, scale: float = 1.0,
                        grad: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                        status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The table's gradient under engram_lookup, every row: f32 [total_rows][D]."""
-    L = _load()
-    dev = dout.device
-    ty, ld, T, C, D, workspace = _grad_args(dout, ids, workspace)
+    L = _lib or _load()
+    ty, idx, ld, T, C, D, workspace = _grad_args(dout, ids, workspace)
     if grad is None:
-        grad = torch.empty((total_rows, D), dtype=torch.float32, device=dev)
-    _need(grad, "grad", torch.float32, dev, total_rows * D)
-    _check(L.engram_lookup_grad(_ptr(dout), ty, ld, _ptr(ids), T, C, D, total_rows, scale, _ptr(grad),
-                                _ptr(workspace), workspace.numel(), _ptr(status), _stream(dev)),
-           "engram_lookup_grad")
+        grad = torch.empty((total_rows, D), dtype=torch.float32, device=dout.device)
+    else:
+        _flat(grad, "grad", torch.float32, dout, idx, total_rows * D)
+    rc = L.engram_lookup_grad(dout.data_ptr(), ty, ld, ids.data_ptr(), T, C, D, total_rows, scale, grad.data_ptr(),
+                              workspace.data_ptr(), workspace.numel(), _addr(status), _raw_stream(idx))
+    if rc:
+        _check(rc, "engram_lookup_grad")
     return grad
 
 
@@ -1087,67 +1128,67 @@ def engram_lookup_grad_rows(dout: torch.Tensor, ids: torch.Tensor, total_rows: i
                             status: Optional[torch.Tensor] = None):
     """The table's gradient under engram_lookup as its distinct rows: (rows int32 [n] ascending then -1,
     grad f32 [n][D] then 0, count int32 [1]), n = ids.numel()."""
-    L = _load()
-    dev = dout.device
-    ty, ld, T, C, D, workspace = _grad_args(dout, ids, workspace)
+    L = _lib or _load()
+    ty, idx, ld, T, C, D, workspace = _grad_args(dout, ids, workspace)
     n = T * C
     if rows is None:
-        rows = torch.empty(n, dtype=torch.int32, device=dev)
+        rows = torch.empty(n, dtype=torch.int32, device=dout.device)
+    else:
+        _flat(rows, "rows", torch.int32, dout, idx, n)
     if grad is None:
-        grad = torch.empty((n, D), dtype=torch.float32, device=dev)
+        grad = torch.empty((n, D), dtype=torch.float32, device=dout.device)
+    else:
+        _flat(grad, "grad", torch.float32, dout, idx, n * D)
     if count is None:
-        count = torch.empty(1, dtype=torch.int32, device=dev)
-    _need(rows, "rows", torch.int32, dev, n)
-    _need(grad, "grad", torch.float32, dev, n * D)
-    _need(count, "count", torch.int32, dev, 1)
-    _check(L.engram_lookup_grad_rows(_ptr(dout), ty, ld, _ptr(ids), T, C, D, total_rows, scale, _ptr(rows),
-                                     _ptr(grad), _ptr(count), _ptr(workspace), workspace.numel(), _ptr(status),
-                                     _stream(dev)), "engram_lookup_grad_rows")
+        count = torch.empty(1, dtype=torch.int32, device=dout.device)
+    else:
+        _flat(count, "count", torch.int32, dout, idx, 1)
+    rc = L.engram_lookup_grad_rows(dout.data_ptr(), ty, ld, ids.data_ptr(), T, C, D, total_rows, scale,
+                                   rows.data_ptr(), grad.data_ptr(), count.data_ptr(), workspace.data_ptr(),
+                                   workspace.numel(), _addr(status), _raw_stream(idx))
+    if rc:
+        _check(rc, "engram_lookup_grad_rows")
     return rows, grad, count
 
 
 def recurrence_carry(n_tokens: int, dim: int, device) -> torch.Tensor:
     """Buffer for the states that engram_recurrence saves for its backward pass."""
-    n = _load().engram_recurrence_carry_bytes(n_tokens, dim) // 4
+    n = _bytes_of("engram_recurrence_carry_bytes", n_tokens, dim) // 4
     return torch.empty(max(n, 1), dtype=torch.float32, device=device)
 
 
 def recurrence_workspace(n_tokens: int, dim: int, device) -> torch.Tensor:
-    n = _load().engram_recurrence_workspace_bytes(n_tokens, dim)
+    n = _bytes_of("engram_recurrence_workspace_bytes", n_tokens, dim)
     return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
 
 
 def _recurrence_args(x, g, cu_seqlens, mask, state, state_out, slots, workspace):
-    """Checks shared by the scan and its gradient; returns (type, T, D, x stride, g stride, n_seqs, n_slots,
-    workspace)."""
-    dev = x.device
-    ty = _elem_type(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be [T][dim]")
-    T, D = x.shape
-    xs = _need_rows(x, "x", x.dtype, dev, T, D)
-    gs = _need_rows(g, "g", x.dtype, dev, T, D)
-    _need(cu_seqlens, "cu_seqlens", torch.int64, dev)
-    if cu_seqlens.numel() < 1:
-        raise ValueError("cu_seqlens must be [n_seqs+1]")
+    """Checks shared by the scan and its gradient; returns (type, device number, T, D, x stride, g stride, n_seqs,
+    n_slots, workspace)."""
+    ty, idx, T, D, xs = _matrix(x, "x")
+    gs = _rows(g, "g", x.dtype, x, idx, T, D)
+    _flat(cu_seqlens, "cu_seqlens", torch.int64, x, idx)
     n_seqs = cu_seqlens.numel() - 1
+    if n_seqs < 0:
+        raise ValueError("cu_seqlens must be [n_seqs+1]")
     if mask is not None:
-        _need(mask, "mask", torch.uint8, dev, T)
+        _flat(mask, "mask", torch.uint8, x, idx, T)
     if slots is not None:
-        _need(slots, "slots", torch.int32, dev, n_seqs)
+        _flat(slots, "slots", torch.int32, x, idx, n_seqs)
     n_slots = 0
     for name, s in (("state", state), ("state_out or dstate", state_out)):
         if s is not None:
-            _need(s, name, torch.float32, dev)
+            _flat(s, name, torch.float32, x, idx)
             if s.dim() != 2 or s.shape[1] != D or (n_slots and s.shape[0] != n_slots):
                 raise ValueError(f"{name} must be [n_slots][dim]")
             n_slots = s.shape[0]
     if slots is None and n_slots and n_slots < n_seqs:
         raise ValueError("without slots the state needs a row for every sequence")
     if workspace is None:
-        workspace = recurrence_workspace(T, D, dev)
-    _need(workspace, "workspace", torch.uint8, dev)
-    return ty, T, D, xs, gs, n_seqs, n_slots, workspace
+        workspace = recurrence_workspace(T, D, x.device)
+    else:
+        _flat(workspace, "workspace", torch.uint8, x, idx)
+    return ty, idx, T, D, xs, gs, n_seqs, n_slots, workspace
 
 
 def engram_recurrence(x: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -1159,22 +1200,25 @@ def engram_recurrence(x: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor
 
     state f32 [n_slots][dim] holds the states before the first positions and gets the last ones, unless
     state_out takes those.  carry (recurrence_carry) is filled for engram_recurrence_grad."""
-    L = _load()
-    dev = x.device
+    L = _lib or _load()
     if state_out is None:
         state_out = state
-    ty, T, D, xs, gs, n_seqs, n_slots, workspace = _recurrence_args(x, g, cu_seqlens, mask, state, state_out, slots,
-                                                                    workspace)
+    ty, idx, T, D, xs, gs, n_seqs, n_slots, workspace = _recurrence_args(x, g, cu_seqlens, mask, state, state_out,
+                                                                         slots, workspace)
     if y is None:
-        y = torch.empty((T, D), dtype=x.dtype, device=dev)
-    ys = _need_rows(y, "y", x.dtype, dev, T, D)
+        y = torch.empty((T, D), dtype=x.dtype, device=x.device)
+        ys = D
+    else:
+        ys = _rows(y, "y", x.dtype, x, idx, T, D)
     if carry is not None:
-        _need(carry, "carry", torch.float32, dev)
-        if carry.numel() * 4 < L.engram_recurrence_carry_bytes(T, D):
+        _flat(carry, "carry", torch.float32, x, idx)
+        if carry.numel() * 4 < _bytes_of("engram_recurrence_carry_bytes", T, D):
             raise ValueError("carry is too small (recurrence_carry)")
-    _check(L.engram_recurrence(_ptr(x), xs, _ptr(g), gs, ty, T, D, _ptr(cu_seqlens), n_seqs, _ptr(slots), _ptr(mask),
-                               _ptr(state), _ptr(state_out), n_slots, _ptr(y), ys, _ptr(carry), _ptr(workspace),
-                               workspace.numel(), _ptr(status), _stream(dev)), "engram_recurrence")
+    rc = L.engram_recurrence(x.data_ptr(), xs, g.data_ptr(), gs, ty, T, D, cu_seqlens.data_ptr(), n_seqs, _addr(slots),
+                             _addr(mask), _addr(state), _addr(state_out), n_slots, y.data_ptr(), ys, _addr(carry),
+                             workspace.data_ptr(), workspace.numel(), _addr(status), _raw_stream(idx))
+    if rc:
+        _check(rc, "engram_recurrence")
     return y
 
 
@@ -1186,24 +1230,25 @@ def engram_recurrence_grad(dy: torch.Tensor, x: torch.Tensor, g: torch.Tensor, c
                            status: Optional[torch.Tensor] = None):
     """The gradients (dx, dg) of engram_recurrence.  state: the states the forward call began with; dstate f32
     [n_slots][dim]: the gradient of the last states, replaced by that of the first."""
-    L = _load()
-    dev = x.device
-    ty, T, D, xs, gs, n_seqs, n_slots, workspace = _recurrence_args(x, g, cu_seqlens, mask, state, dstate, slots,
-                                                                    workspace)
-    dys = _need_rows(dy, "dy", x.dtype, dev, T, D)
-    _need(carry, "carry", torch.float32, dev)
-    if carry.numel() * 4 < L.engram_recurrence_carry_bytes(T, D):
+    L = _lib or _load()
+    ty, idx, T, D, xs, gs, n_seqs, n_slots, workspace = _recurrence_args(x, g, cu_seqlens, mask, state, dstate, slots,
+                                                                         workspace)
+    dys = _rows(dy, "dy", x.dtype, x, idx, T, D)
+    _flat(carry, "carry", torch.float32, x, idx)
+    if carry.numel() * 4 < _bytes_of("engram_recurrence_carry_bytes", T, D):
         raise ValueError("carry is too small (recurrence_carry)")
     if dx is None:
-        dx = torch.empty((T, D), dtype=x.dtype, device=dev)
+        dx = torch.empty((T, D), dtype=x.dtype, device=x.device)
     if dg is None:
-        dg = torch.empty((T, D), dtype=x.dtype, device=dev)
-    dxs = _need_rows(dx, "dx", x.dtype, dev, T, D)
-    dgs = _need_rows(dg, "dg", x.dtype, dev, T, D)
-    _check(L.engram_recurrence_grad(_ptr(dy), dys, _ptr(x), xs, _ptr(g), gs, ty, T, D, _ptr(cu_seqlens), n_seqs,
-                                    _ptr(slots), _ptr(mask), _ptr(state), _ptr(carry), _ptr(dstate), n_slots,
-                                    _ptr(dx), dxs, _ptr(dg), dgs, _ptr(workspace), workspace.numel(), _ptr(status),
-                                    _stream(dev)), "engram_recurrence_grad")
+        dg = torch.empty((T, D), dtype=x.dtype, device=x.device)
+    dxs = _rows(dx, "dx", x.dtype, x, idx, T, D)
+    dgs = _rows(dg, "dg", x.dtype, x, idx, T, D)
+    rc = L.engram_recurrence_grad(dy.data_ptr(), dys, x.data_ptr(), xs, g.data_ptr(), gs, ty, T, D,
+                                  cu_seqlens.data_ptr(), n_seqs, _addr(slots), _addr(mask), _addr(state),
+                                  carry.data_ptr(), _addr(dstate), n_slots, dx.data_ptr(), dxs, dg.data_ptr(), dgs,
+                                  workspace.data_ptr(), workspace.numel(), _addr(status), _raw_stream(idx))
+    if rc:
+        _check(rc, "engram_recurrence_grad")
     return dx, dg
 
 
@@ -1212,27 +1257,23 @@ def engram_recurrence_step(x: torch.Tensor, g: torch.Tensor, slots: torch.Tensor
                            status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """One position of every batch entry: x, g bf16 or f32 [B][dim], slots int32 [B] (-1: padding), state f32
     [n_slots][dim] updated in place unless state_out takes the new states; returns y [B][dim]."""
-    L = _load()
-    dev = x.device
-    ty = _elem_type(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be [B][dim]")
-    B, D = x.shape
-    xs = _need_rows(x, "x", x.dtype, dev, B, D)
-    gs = _need_rows(g, "g", x.dtype, dev, B, D)
-    _need(slots, "slots", torch.int32, dev, B)
-    if state_out is None:
-        state_out = state
-    _need(state, "state", torch.float32, dev)
+    L = _lib or _load()
+    ty, idx, B, D, xs = _matrix(x, "x")
+    gs = _rows(g, "g", x.dtype, x, idx, B, D)
+    sp = _flat(slots, "slots", torch.int32, x, idx, B)
+    p = _flat(state, "state", torch.float32, x, idx)
     if state.dim() != 2 or state.shape[1] != D:
         raise ValueError("state must be [n_slots][dim]")
-    _need(state_out, "state_out", torch.float32, dev, state.numel())
+    po = p if state_out is None else _flat(state_out, "state_out", torch.float32, x, idx, state.numel())
     if y is None:
-        y = torch.empty((B, D), dtype=x.dtype, device=dev)
-    ys = _need_rows(y, "y", x.dtype, dev, B, D)
-    _check(L.engram_recurrence_step(_ptr(x), xs, _ptr(g), gs, ty, B, D, _ptr(slots), _ptr(state), _ptr(state_out),
-                                    state.shape[0], _ptr(y), ys, _ptr(status), _stream(dev)),
-           "engram_recurrence_step")
+        y = torch.empty((B, D), dtype=x.dtype, device=x.device)
+        ys = D
+    else:
+        ys = _rows(y, "y", x.dtype, x, idx, B, D)
+    rc = L.engram_recurrence_step(x.data_ptr(), xs, g.data_ptr(), gs, ty, B, D, sp, p, po, state.shape[0],
+                                  y.data_ptr(), ys, _addr(status), _raw_stream(idx))
+    if rc:
+        _check(rc, "engram_recurrence_step")
     return y
 
 
@@ -1243,29 +1284,24 @@ def engram_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logi
     """Distillation loss of every position, f32 [T]: logits bf16 or f32 [T][vocab], the teacher's top entries as
     ids int32 [T][K] (negative: unused) and logits f32 [T][K].  dlogits [T][vocab], when given, gets the gradient
     (it may be logits itself)."""
-    L = _load()
-    dev = logits.device
-    ty = _elem_type(logits, "logits")
-    if logits.dim() != 2:
-        raise ValueError("logits must be [T][vocab]")
-    T, V = logits.shape
-    zs = _need_rows(logits, "logits", logits.dtype, dev, T, V)
-    _need(teacher_ids, "teacher_ids", torch.int32, dev)
+    L = _lib or _load()
+    ty, idx, T, V, zs = _matrix(logits, "logits")
+    ip = _flat(teacher_ids, "teacher_ids", torch.int32, logits, idx)
     if teacher_ids.dim() != 2 or teacher_ids.shape[0] != T:
         raise ValueError("teacher_ids must be [T][K]")
     K = teacher_ids.shape[1]
-    _need(teacher_logits, "teacher_logits", torch.float32, dev, T * K)
-    if weight is not None:
-        _need(weight, "weight", torch.float32, dev, T)
-    if teacher_lse is not None:
-        _need(teacher_lse, "teacher_lse", torch.float32, dev, T)
+    tp = _flat(teacher_logits, "teacher_logits", torch.float32, logits, idx, T * K)
+    wp = None if weight is None else _flat(weight, "weight", torch.float32, logits, idx, T)
+    ep = None if teacher_lse is None else _flat(teacher_lse, "teacher_lse", torch.float32, logits, idx, T)
     if loss is None:
-        loss = torch.empty(T, dtype=torch.float32, device=dev)
-    _need(loss, "loss", torch.float32, dev, T)
-    ds = _need_rows(dlogits, "dlogits", logits.dtype, dev, T, V) if dlogits is not None else 0
-    _check(L.engram_distill(_ptr(logits), ty, T, V, zs, _ptr(teacher_ids), _ptr(teacher_logits), K, temperature,
-                            _ptr(teacher_lse), _ptr(weight), _ptr(loss), _ptr(dlogits), ds, _ptr(status),
-                            _stream(dev)), "engram_distill")
+        loss = torch.empty(T, dtype=torch.float32, device=logits.device)
+    else:
+        _flat(loss, "loss", torch.float32, logits, idx, T)
+    ds = _rows(dlogits, "dlogits", logits.dtype, logits, idx, T, V) if dlogits is not None else 0
+    rc = L.engram_distill(logits.data_ptr(), ty, T, V, zs, ip, tp, K, temperature, ep, wp, loss.data_ptr(),
+                          _addr(dlogits), ds, _addr(status), _raw_stream(idx))
+    if rc:
+        _check(rc, "engram_distill")
     return loss
 
 

@@ -42,132 +42,256 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const typename E::T* _
 
 // ---------------------------------------------------------------- sort by id
 
-constexpr int kItems = 16;                 // entries per thread
-constexpr int kBlock = kThreads * kItems;  // entries per block
-constexpr int kMaxDigits = 512;            // 9 bits a pass: 26-bit ids take three passes, 17-bit ids two
+// One kernel sorts: its blocks (all resident, a cooperative launch) share out
+// the entries in order and meet at a barrier between counting and moving.  Ids
+// of 26 bits take three passes of 9 bits.  A few thousand entries are one
+// block's work, without barriers.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kItems = 4;                         // entries per thread and round
+constexpr int kRound = kSortThreads * kItems;     // entries per block and round
+constexpr int kDigitBits = 9;
+constexpr int kMaxDigits = 1 << kDigitBits;
+constexpr int kChunk = 64;  // sorted entries that are summed together, see seg_sum_kernel
 
 __device__ __forceinline__ uint32_t entry_key(int32_t id, int64_t total_rows) {
   return id >= 0 && id < total_rows ? static_cast<uint32_t>(id) : static_cast<uint32_t>(total_rows);
 }
 
-// counts[block][digit] of the first pass, from the ids themselves.
-__global__ void __launch_bounds__(kThreads) sort_count_kernel(const int32_t* __restrict__ ids, int64_t total_rows,
-                                                              int32_t n, int digits, int32_t* __restrict__ counts,
-                                                              int32_t* status) {
-  __shared__ int32_t hist[kMaxDigits];
-  for (int d = threadIdx.x; d < digits; d += kThreads) hist[d] = 0;
-  __syncthreads();
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kBlock;
-  bool bad = false;
-#pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    const int64_t i = base + k * kThreads + threadIdx.x;
-    if (i < n) {
-      const int32_t id = ids[i];
-      bad |= id != ENGRAM_DEAD && (id < 0 || id >= total_rows);
-      atomicAdd(&hist[entry_key(id, total_rows) & (digits - 1)], 1);
-    }
+__device__ __forceinline__ bool is_head(const uint32_t* keys, int64_t i, int32_t n, uint32_t none) {
+  if (i >= n) return false;
+  const uint32_t k = __ldcg(keys + i);
+  return k != none && (i == 0 || k != __ldcg(keys + i - 1));
+}
+
+struct SortArgs {
+  const int32_t* ids;
+  int64_t total_rows;
+  int32_t n, per;  // entries, and how many each block handles
+  int32_t passes, bits;
+  uint32_t* key[2];
+  int32_t* idx[2];
+  int32_t* counts;  // [block][digit], then [block] heads
+  int32_t* barrier;
+  int32_t chunks;
+  int32_t* base;   // segments that begin before each chunk, or null
+  int32_t* count;  // all of them
+  int32_t* status;
+};
+
+// All blocks meet; false when the wait ran out (the blocks are co-resident, so
+// that means a broken launch).
+__device__ __forceinline__ bool meet(const SortArgs& a, int32_t& met) {
+  if (gridDim.x == 1) {
+    __syncthreads();
+    return true;
   }
-  if (bad && status != nullptr) atomicOr(status, ENGRAM_ST_BAD_ROW);
+  __threadfence();
+  const int32_t want = ++met * static_cast<int32_t>(gridDim.x);
   __syncthreads();
-  for (int d = threadIdx.x; d < digits; d += kThreads)
-    counts[static_cast<int64_t>(blockIdx.x) * digits + d] = hist[d];
+  bool ok = true;
+  if (threadIdx.x == 0) {
+    atomicAdd(a.barrier, 1);
+    const long long begun = clock64();
+    while (true) {
+      int32_t v;
+      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(a.barrier) : "memory");
+      if (v >= want) break;
+      if (clock64() - begun > kWaitBudgetCycles) {
+        ok = false;
+        if (a.status != nullptr) atomicOr(a.status, ENGRAM_ST_TIMEOUT);
+        break;
+      }
+    }
+    __threadfence();
+  }
+  return __syncthreads_and(ok);
 }
 
 // Moves each entry to its place: entries of smaller digits, entries of the
-// same digit in earlier blocks, earlier warps, earlier rounds and lower lanes
-// come before it, which keeps the pass stable.  The next pass's counts are
-// taken on the way (integer sums: their order does not matter).
-__global__ void __launch_bounds__(kThreads) sort_move_kernel(const uint32_t* __restrict__ keys,
-                                                             const int32_t* __restrict__ idx, bool first,
-                                                             int64_t total_rows, int32_t n, int bits, int shift,
-                                                             const int32_t* __restrict__ counts,
-                                                             int32_t* __restrict__ next, uint32_t* __restrict__ keys_out,
-                                                             int32_t* __restrict__ idx_out) {
-  __shared__ int32_t hist[kWarps][kMaxDigits];
-  __shared__ int32_t totals[kMaxDigits];
-  const int digits = 1 << bits;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
-  for (int d = tid; d < digits; d += kThreads)
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) hist[w][d] = 0;
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kBlock + warp * (32 * kItems);
-  uint32_t key[kItems];
-  int32_t rank[kItems];
-#pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    const int64_t i = base + k * 32 + lane;
-    key[k] = i < n ? keys[i] : 0u;
-    if (first) key[k] = entry_key(static_cast<int32_t>(key[k]), total_rows);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    const bool in = base + k * 32 + lane < n;
-    const uint32_t digit = in ? (key[k] >> shift) & (digits - 1) : digits;
-    const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-    const int32_t before = in ? hist[warp][digit] : 0;
-    rank[k] = before + __popc(peers & ((1u << lane) - 1u));
-    __syncwarp();
-    if (in && (peers >> lane) == 1u) hist[warp][digit] = before + __popc(peers);  // the highest lane of each digit
-    __syncwarp();
-  }
-  // per digit: its entries in all blocks and in the blocks before this one
-  int32_t total[kMaxDigits / kThreads], prior[kMaxDigits / kThreads];
-#pragma unroll
-  for (int j = 0; j < kMaxDigits / kThreads; ++j) {
-    const int d = tid + j * kThreads;
-    total[j] = prior[j] = 0;
-    if (d < digits) {
-#pragma unroll 8
-      for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-        const int32_t c = __ldg(counts + static_cast<int64_t>(b) * digits + d);
-        total[j] += c;
-        prior[j] += b < static_cast<int>(blockIdx.x) ? c : 0;
+// same digit in earlier blocks, rounds, warps and lanes come before it, which
+// keeps the passes stable.
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
+  __shared__ uint16_t hist[kSortWarps][kMaxDigits];
+  __shared__ int32_t place[kMaxDigits], half[kMaxDigits], warp_sum[kSortWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int digits = 1 << a.bits, blocks = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
+  const int32_t e0 = a.n < static_cast<int64_t>(me) * a.per ? a.n : me * a.per;
+  const int32_t e1 = a.n - e0 < a.per ? a.n : e0 + a.per;
+  int32_t met = 0;
+
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const bool first = pass == 0;
+    const int shift = pass * a.bits;
+    const uint32_t* kin = first ? reinterpret_cast<const uint32_t*>(a.ids) : a.key[(pass - 1) & 1];
+    const int32_t* iin = first ? nullptr : a.idx[(pass - 1) & 1];
+    uint32_t* kout = a.key[pass & 1];
+    int32_t* iout = a.idx[pass & 1];
+    auto digit_of = [&](uint32_t key) { return (key >> shift) & (digits - 1); };
+    auto key_at = [&](int32_t i) {
+      const uint32_t k = __ldcg(kin + i);
+      return first ? entry_key(static_cast<int32_t>(k), a.total_rows) : k;
+    };
+
+    // this block's digits
+    if (tid < digits) place[tid] = 0;
+    __syncthreads();
+    bool bad = false;
+    for (int32_t i = e0 + tid; i < e1; i += kSortThreads) {
+      if (first) {
+        const int32_t id = a.ids[i];
+        bad |= id != ENGRAM_DEAD && (id < 0 || id >= a.total_rows);
       }
-      totals[d] = total[j];
+      atomicAdd(&place[digit_of(key_at(i))], 1);
     }
-  }
-  __syncthreads();
-  if (warp == 0) {  // exclusive sums over the digits
-    int32_t run = 0;
-    for (int d0 = 0; d0 < digits; d0 += 32) {
-      const int32_t c = d0 + lane < digits ? totals[d0 + lane] : 0;
-      int32_t x = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+    if (bad && a.status != nullptr) atomicOr(a.status, ENGRAM_ST_BAD_ROW);
+    __syncthreads();
+    if (blocks > 1) {
+      if (tid < digits) __stcg(a.counts + static_cast<int64_t>(me) * digits + tid, place[tid]);
+      if (!meet(a, met)) return;
+    }
+
+    // per digit: its entries in all blocks, and in the blocks before this one
+    // (two threads a digit, half the blocks each)
+    int32_t total = 0, prior = 0;
+    if (blocks > 1) {
+      const int d = tid & (kMaxDigits - 1), h = tid / kMaxDigits;
+      const int b0 = h == 0 ? 0 : blocks / 2, b1 = h == 0 ? blocks / 2 : blocks;
+      if (d < digits) {
+#pragma unroll 16
+        for (int b = b0; b < b1; ++b) {
+          const int32_t c = __ldcg(a.counts + static_cast<int64_t>(b) * digits + d);
+          total += c;
+          prior += b < me ? c : 0;
+        }
       }
-      if (d0 + lane < digits) totals[d0 + lane] = run + x - c;
-      run += __shfl_sync(0xffffffffu, x, 31);
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kMaxDigits / kThreads; ++j) {
-    const int d = tid + j * kThreads;
-    if (d < digits) {
-      int32_t at = totals[d] + prior[j];
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const int32_t c = hist[w][d];
-        hist[w][d] = at;
-        at += c;
+      if (h == 1 && d < digits) {
+        half[d] = total;
+        place[d] = prior;
       }
+      __syncthreads();
+      if (h == 0 && d < digits) {
+        total += half[d];
+        prior += place[d];
+      }
+    } else if (tid < digits) {
+      total = place[tid];
+    }
+    // exclusive sums over the digits (the first warps' threads hold one each)
+    int32_t x = tid < digits ? total : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    if (tid < digits) {
+      for (int w = 0; w < warp; ++w) x += warp_sum[w];
+      place[tid] = x - total + prior;
+    }
+
+    for (int32_t r0 = e0; r0 < e1; r0 += kRound) {
+      uint32_t key[kItems];
+      int32_t idx[kItems];
+      int rank[kItems];
+      const int32_t at = r0 + warp * (32 * kItems) + lane;  // (below 2^31 where it is used: see `in`)
+      for (int d = lane; d < digits; d += 32) hist[warp][d] = 0;
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        const bool in = static_cast<int64_t>(r0) + warp * (32 * kItems) + lane + 32 * k < e1;
+        key[k] = in ? key_at(at + 32 * k) : 0u;
+        idx[k] = !in || first ? at + 32 * k : __ldcg(iin + at + 32 * k);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        const bool in = static_cast<int64_t>(r0) + warp * (32 * kItems) + lane + 32 * k < e1;
+        const uint32_t d = in ? digit_of(key[k]) : kMaxDigits;
+        const uint32_t peers = __match_any_sync(0xffffffffu, d);
+        const int before = in ? hist[warp][d] : 0;
+        rank[k] = before + __popc(peers & ((1u << lane) - 1u));
+        __syncwarp();
+        if (in && (peers >> lane) == 1u) hist[warp][d] = static_cast<uint16_t>(before + __popc(peers));  // the highest lane
+        __syncwarp();
+      }
+      __syncthreads();
+      if (tid < digits) {  // entries of this round in earlier warps
+        int run = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) {
+          const int c = hist[w][tid];
+          hist[w][tid] = static_cast<uint16_t>(run);
+          run += c;
+        }
+        half[tid] = run;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        if (static_cast<int64_t>(r0) + warp * (32 * kItems) + lane + 32 * k < e1) {
+          const uint32_t d = digit_of(key[k]);
+          const int32_t to = place[d] + hist[warp][d] + rank[k];
+          __stcg(kout + to, key[k]);
+          __stcg(iout + to, idx[k]);
+        }
+      }
+      __syncthreads();
+      if (tid < digits) place[tid] += half[tid];
+      __syncthreads();
+    }
+    if (!meet(a, met)) return;
+  }
+  if (a.base == nullptr) return;
+
+  // segments that begin in each chunk, summed up over the chunks before it
+  const uint32_t none = static_cast<uint32_t>(a.total_rows);
+  const uint32_t* keys = a.key[(a.passes - 1) & 1];
+  const int32_t cper = (a.chunks + blocks - 1) / blocks;
+  const int32_t c0 = a.chunks < static_cast<int64_t>(me) * cper ? a.chunks : me * cper;
+  const int32_t c1 = a.chunks - c0 < cper ? a.chunks : c0 + cper;
+  if (tid == 0) half[0] = 0;
+  __syncthreads();
+  for (int32_t c = c0 + warp; c < c1; c += kSortWarps) {
+    int32_t heads = 0;
+#pragma unroll
+    for (int k = 0; k < kChunk; k += 32)
+      heads += __popc(__ballot_sync(0xffffffffu, is_head(keys, static_cast<int64_t>(c) * kChunk + k + lane, a.n, none)));
+    if (lane == 0) {
+      __stcg(a.base + c, heads);
+      atomicAdd(&half[0], heads);
     }
   }
   __syncthreads();
+  if (tid == 0) __stcg(a.counts + me, half[0]);
+  if (!meet(a, met)) return;
+  int32_t before = 0, all = 0;
+  for (int b = lane; b < blocks; b += 32) {
+    const int32_t c = __ldcg(a.counts + b);
+    all += c;
+    before += b < me ? c : 0;
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  all = __reduce_add_sync(0xffffffffu, all);
+  if (me == 0 && tid == 0) *a.count = all;
+  for (int32_t r0 = c0; r0 < c1; r0 += kSortThreads) {  // (uniform over the block)
+    const int32_t c = r0 + tid, own = c < c1 ? __ldcg(a.base + c) : 0;
+    int32_t x = own;
 #pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    const int64_t i = base + k * 32 + lane;
-    if (i < n) {
-      const int32_t to = hist[warp][(key[k] >> shift) & (digits - 1)] + rank[k];
-      keys_out[to] = key[k];
-      idx_out[to] = first ? static_cast<int32_t>(i) : idx[i];
-      if (next != nullptr)
-        atomicAdd(next + static_cast<int64_t>(to / kBlock) * digits + ((key[k] >> (shift + bits)) & (digits - 1)), 1);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int32_t whole = 0;
+    for (int w = 0; w < kSortWarps; ++w) {
+      if (w < warp) x += warp_sum[w];
+      whole += warp_sum[w];
+    }
+    if (c < c1) a.base[c] = before + x - own;
+    before += whole;
   }
 }
 
@@ -177,74 +301,6 @@ __global__ void __launch_bounds__(kThreads) sort_move_kernel(const uint32_t* __r
 // or short the segments are.  A segment inside its chunk goes straight to the
 // result; one that crosses a border leaves a part in each chunk it touches,
 // and the parts are joined in order afterwards.
-constexpr int kChunk = 64;
-
-__device__ __forceinline__ bool is_head(const uint32_t* keys, int64_t i, int32_t n, uint32_t none) {
-  return i < n && keys[i] != none && (i == 0 || keys[i] != keys[i - 1]);
-}
-
-// base[chunk] = segments that begin before it, *count = all of them; one
-// thread per chunk of heads, then the last block to finish sums them up.
-__global__ void __launch_bounds__(kThreads) seg_base_kernel(const uint32_t* __restrict__ keys, int32_t n, uint32_t none,
-                                                            int32_t chunks, int32_t* base, int32_t* done,
-                                                            int32_t* count) {
-  __shared__ int32_t warp_sum[kWarps];
-  __shared__ int32_t run;
-  __shared__ bool last;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int64_t c = static_cast<int64_t>(blockIdx.x) * kWarps + warp; c < chunks;
-       c += static_cast<int64_t>(gridDim.x) * kWarps) {
-    int32_t heads = 0;
-#pragma unroll
-    for (int k = 0; k < kChunk; k += 32)
-      heads += __popc(__ballot_sync(0xffffffffu, is_head(keys, c * kChunk + k + lane, n, none)));
-    if (lane == 0) __stcg(base + c, heads);
-  }
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    last = atomicAdd(done, 1) == static_cast<int>(gridDim.x) - 1;
-    run = 0;
-  }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  constexpr int kPer = 8;
-  for (int c0 = 0; c0 < chunks; c0 += kThreads * kPer) {
-    int32_t v[kPer], sum = 0;
-    const int at = c0 + threadIdx.x * kPer;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      v[k] = at + k < chunks ? __ldcg(base + at + k) : 0;
-      sum += v[k];
-    }
-    int32_t x = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    int32_t before = run, whole = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      before += w < warp ? warp_sum[w] : 0;
-      whole += warp_sum[w];
-    }
-    before += x - sum;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      if (at + k < chunks) base[at + k] = before;
-      before += v[k];
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) run += whole;
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) *count = run;
-}
-
 // 8 bf16 or 4 fp32 columns of a row per lane.  Aligned rows are read 16 bytes
 // a lane; others column by column, the lanes next to one another.
 template <class E>
@@ -447,54 +503,69 @@ __global__ void __launch_bounds__(kThreads) seg_join_kernel(SumArgs<E> a) {
   constexpr int N = kCols<E>;
   __shared__ float sums[kWarps][32 * N];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int32_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
-    const int32_t e0 = chunk * kChunk, e1 = e0 + kChunk;
-    if (e1 >= a.n) return;
-    const uint32_t key = a.keys[e1 - 1];
-    // begins here and goes on
-    if (key == a.none || a.keys[e1] != key || (e0 > 0 && a.keys[e0 - 1] == key)) continue;
-    // chunks after this one that the segment reaches into
-    int32_t more = 0;
-    while (true) {
-      const int64_t q = e1 + static_cast<int64_t>(more + lane) * kChunk;
-      const uint32_t in = __ballot_sync(0xffffffffu, q < a.n && a.keys[q] == key);
-      more += in == 0xffffffffu ? 32 : __ffs(~in) - 1;
-      if (in != 0xffffffffu) break;
-    }
-    int32_t seg = 0;
-    if (!a.dense) {  // the last segment that begins in this chunk
-      int32_t heads = 0;
+  const int32_t chunk = blockIdx.x, e0 = chunk * kChunk, e1 = e0 + kChunk;
+  if (e1 >= a.n) return;
+  const uint32_t key = a.keys[e1 - 1];
+  // begins here and goes on
+  if (key == a.none || a.keys[e1] != key || (e0 > 0 && a.keys[e0 - 1] == key)) return;
+  // the segment's end, 32 probes at a time: keys[lo - 1] == key, keys[hi] > key
+  int32_t lo = e1 + 1, hi = a.n;
+  while (hi > lo) {
+    const int32_t step = (hi - lo + 31) / 32;
+    const int64_t q = static_cast<int64_t>(lo) + static_cast<int64_t>(step) * lane;
+    const int k = __popc(__ballot_sync(0xffffffffu, q < hi && a.keys[q] == key));
+    if (k == 0) break;
+    hi = static_cast<int64_t>(step) * k < hi - lo ? lo + step * k : hi;
+    lo = lo + step * (k - 1) + 1;
+  }
+  const int32_t more = (lo - 1) / kChunk - chunk;  // chunks after this one that it reaches into
+  int32_t seg = 0;
+  if (!a.dense) {  // the last segment that begins in this chunk
+    int32_t heads = 0;
 #pragma unroll
-      for (int k = 0; k < kChunk; k += 32)
-        heads += __popc(__ballot_sync(0xffffffffu, is_head(a.keys, static_cast<int64_t>(e0) + k + lane, a.n, a.none)));
-      seg = a.base[chunk] + heads - 1;
-    }
-    float* out = a.grad + (a.dense ? static_cast<int64_t>(key) : seg) * a.dim;
-    for (int c0 = blockIdx.y * 32 * N; c0 < a.dim; c0 += gridDim.y * 32 * N) {
-      float acc[N];
+    for (int k = 0; k < kChunk; k += 32)
+      heads += __popc(__ballot_sync(0xffffffffu, is_head(a.keys, static_cast<int64_t>(e0) + k + lane, a.n, a.none)));
+    seg = a.base[chunk] + heads - 1;
+  }
+  float* out = a.grad + (a.dense ? static_cast<int64_t>(key) : seg) * a.dim;
+  for (int c0 = blockIdx.y * 32 * N; c0 < a.dim; c0 += gridDim.y * 32 * N) {
+    float acc[N];
 #pragma unroll
-      for (int j = 0; j < N; ++j) acc[j] = 0.f;
-#pragma unroll 4
-      for (int32_t k = warp; k <= more; k += kWarps) {
-        const float* part = k == 0 ? a.tail + static_cast<int64_t>(chunk) * a.dim
-                                   : a.head + static_cast<int64_t>(chunk + k) * a.dim;
+    for (int j = 0; j < N; ++j) acc[j] = 0.f;
+    auto add = [&](int32_t k) {
+      const float* part = (k == 0 ? a.tail : a.head) + static_cast<int64_t>(chunk + k) * a.dim;
+      if constexpr (kAligned) {
+        const int c = c0 + lane * N;
+        if (c < a.dim) {
+#pragma unroll
+          for (int j = 0; j < N; j += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(part + c + j);
+            acc[j] += q.x;
+            acc[j + 1] += q.y;
+            acc[j + 2] += q.z;
+            acc[j + 3] += q.w;
+          }
+        }
+      } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           const int c = c0 + j * 32 + lane;
           if (c < a.dim) acc[j] += part[c];
         }
       }
+    };
+#pragma unroll 8
+    for (int32_t k = warp; k <= more; k += kWarps) add(k);
 #pragma unroll
-      for (int j = 0; j < N; ++j) sums[warp][j * 32 + lane] = acc[j];
-      __syncthreads();
-      for (int c = threadIdx.x; c < 32 * N; c += kThreads) {
-        float s = sums[0][c];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) s += sums[w][c];
-        if (c0 + c < a.dim) out[c0 + c] = a.scale * s;
-      }
-      __syncthreads();
+    for (int j = 0; j < N; ++j) sums[warp][kAligned ? lane * N + j : j * 32 + lane] = acc[j];
+    __syncthreads();
+    const int used = more + 1 < kWarps ? more + 1 : kWarps;
+    for (int c = threadIdx.x; c < 32 * N; c += kThreads) {
+      float s = sums[0][c];
+      for (int w = 1; w < used; ++w) s += sums[w][c];
+      if (c0 + c < a.dim) out[c0 + c] = a.scale * s;
     }
+    __syncthreads();
   }
 }
 
@@ -504,25 +575,26 @@ int check_lookup(int32_t type, int64_t total_rows, int32_t row_dim, int64_t n_to
   if (total_rows >= (int64_t(1) << 31) - 1) return fail(ENGRAM_E_RANGE, "total_rows must be below 2^31 - 1");
   if (row_dim < 1 || row_dim > (1 << 20)) return fail(ENGRAM_E_SHAPE, "row_dim %d not in [1, 2^20]", row_dim);
   if (n_cols < 1 || n_cols > (1 << 20)) return fail(ENGRAM_E_SHAPE, "n_cols %d not in [1, 2^20]", n_cols);
-  if (n_tokens > (int64_t(1) << 31) / n_cols - 1) return fail(ENGRAM_E_RANGE, "n_tokens * n_cols must be below 2^31");
+  if (n_tokens > ((int64_t(1) << 31) - 8192) / n_cols)
+    return fail(ENGRAM_E_RANGE, "n_tokens * n_cols must be at most 2^31 - 8192");
   if (stride < static_cast<int64_t>(n_cols) * row_dim)
     return fail(ENGRAM_E_SHAPE, "row stride %lld below n_cols * row_dim", static_cast<long long>(stride));
   return ENGRAM_OK;
 }
 
-// The parts of the gradient's workspace.  The counts of the passes after the
-// first and the counter are zeroed before each call.
+// The parts of the gradient's workspace.
 struct GradSpace {
   uint32_t* key[2];
   int32_t* idx[2];
   int32_t* base;
-  int32_t* done;
   int32_t* counts;
+  int32_t* barrier;
+  int32_t* count;
   float *head, *tail;
   size_t bytes;
 };
 
-constexpr int kMaxPasses = 4;
+constexpr int kMaxSortBlocks = 256;  // one per SM
 
 GradSpace grad_space(void* at, int64_t n, int32_t dim) {
   GradSpace s;
@@ -535,14 +607,14 @@ GradSpace grad_space(void* at, int64_t n, int32_t dim) {
   };
   const size_t words = static_cast<size_t>(n) * 4;
   const size_t chunks = static_cast<size_t>((n + kChunk - 1) / kChunk);
+  s.barrier = reinterpret_cast<int32_t*>(take(4));
+  s.count = reinterpret_cast<int32_t*>(take(4));
   for (int k = 0; k < 2; ++k) s.key[k] = reinterpret_cast<uint32_t*>(take(words));
   for (int k = 0; k < 2; ++k) s.idx[k] = reinterpret_cast<int32_t*>(take(words));
   s.base = reinterpret_cast<int32_t*>(take(chunks * 4));
+  s.counts = reinterpret_cast<int32_t*>(take(static_cast<size_t>(kMaxSortBlocks) * kMaxDigits * 4));
   s.head = reinterpret_cast<float*>(take(chunks * dim * 4));
   s.tail = reinterpret_cast<float*>(take(chunks * dim * 4));
-  const size_t blocks = static_cast<size_t>((n + kBlock - 1) / kBlock);
-  s.done = reinterpret_cast<int32_t*>(take((1 + blocks * kMaxDigits * kMaxPasses) * 4));
-  s.counts = s.done + 1;
   s.bytes = used;
   return s;
 }
@@ -600,28 +672,50 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
   const GradSpace w = grad_space(workspace_d, n, row_dim);
   int width = 1;  // bits of the keys, total_rows standing for "no row"
   while ((total_rows >> width) != 0) ++width;
-  const int passes = (width + 8) / 9, bits = (width + passes - 1) / passes, digits = 1 << bits;
-  const int blocks = (n + kBlock - 1) / kBlock;
-  const size_t per = static_cast<size_t>(blocks) * digits;
-  cudaError_t err = cudaMemsetAsync(w.done, 0, (1 + per * passes) * 4, st);
-  if (err != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(err));
-  sort_count_kernel<<<blocks, kThreads, 0, st>>>(ids_d, total_rows, n, digits, w.counts, status_d);
-  const uint32_t* kin = reinterpret_cast<const uint32_t*>(ids_d);
-  const int32_t* iin = nullptr;
-  for (int p = 0; p < passes; ++p) {
-    sort_move_kernel<<<blocks, kThreads, 0, st>>>(kin, iin, p == 0, total_rows, n, bits, bits * p, w.counts + p * per,
-                                                  p + 1 < passes ? w.counts + (p + 1) * per : nullptr, w.key[p & 1],
-                                                  w.idx[p & 1]);
-    kin = w.key[p & 1];
-    iin = w.idx[p & 1];
-  }
   const int32_t chunks = (n + kChunk - 1) / kChunk;
   const uint32_t none = static_cast<uint32_t>(total_rows);
-  if (!dense) {
-    const int want = (chunks + kWarps - 1) / kWarps;
-    seg_base_kernel<<<want < sms * 4 ? want : sms * 4, kThreads, 0, st>>>(kin, n, none, chunks, w.base, w.done, count_d);
+  SortArgs sa{};
+  sa.ids = ids_d;
+  sa.total_rows = total_rows;
+  sa.n = n;
+  sa.passes = (width + kDigitBits - 1) / kDigitBits;
+  sa.bits = (width + sa.passes - 1) / sa.passes;
+  for (int k = 0; k < 2; ++k) {
+    sa.key[k] = w.key[k];
+    sa.idx[k] = w.idx[k];
   }
-  if ((rc = check_launch("lookup gradient"))) return rc;
+  sa.counts = w.counts;
+  sa.barrier = w.barrier;
+  sa.chunks = chunks;
+  sa.base = dense ? nullptr : w.base;
+  sa.count = dense ? w.count : count_d;
+  sa.status = status_d;
+  // one block up to a round of entries; more blocks (at least 1024 entries
+  // each) shorten the passes but cost two barriers a pass
+  int blocks = 1;
+  if (n > kRound) {
+    blocks = sms < kMaxSortBlocks ? sms : kMaxSortBlocks;
+    if (n / 1024 < blocks) blocks = n / 1024;
+  }
+  sa.per = (n + blocks - 1) / blocks;
+  if (blocks > 1) {
+    cudaError_t err = cudaMemsetAsync(w.barrier, 0, 4, st);
+    if (err != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(err));
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = blocks > 1 ? 1 : 0;
+  cudaError_t err = cudaLaunchKernelEx(&cfg, sort_kernel, sa);
+  if (err != cudaSuccess) return fail(ENGRAM_E_CUDA, "sort_kernel launch: %s", cudaGetErrorString(err));
+  const uint32_t* kin = w.key[(sa.passes - 1) & 1];
+  const int32_t* iin = w.idx[(sa.passes - 1) & 1];
+  if ((rc = check_launch("sort_kernel"))) return rc;
   auto go = [&](auto e) {
     using E = decltype(e);
     SumArgs<E> a{};

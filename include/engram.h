@@ -613,7 +613,7 @@ enum { ENGRAM_T_BF16 = 0, ENGRAM_T_F32 = 1 };
  *   out_d      [n_tokens][n_cols*row_dim] of `type`, rows out_stride elements
  *              apart (>= n_cols*row_dim)
  * Any row_dim >= 1 and element-aligned pointers; 16-byte aligned rows are the
- * fast case.  total_rows < 2^31 - 1, n_tokens * n_cols < 2^31. */
+ * fast case.  total_rows < 2^31 - 1, n_tokens * n_cols <= 2^31 - 8192. */
 int engram_lookup(const void* table_d, int32_t type, int64_t total_rows, int32_t row_dim, const int32_t* row_ids_d,
                   int64_t n_tokens, int32_t n_cols, float scale, void* out_d, int64_t out_stride, int32_t* status_d,
                   void* stream);
@@ -623,7 +623,8 @@ int engram_lookup(const void* table_d, int32_t type, int64_t total_rows, int32_t
  *   G[r] = scale * sum_{i: row_ids[i] == r} dout[i]      (fp32)
  * Entries are sorted by (id, i) and each row's sum is taken in a fixed order,
  * so results are the same from run to run.  Ids without a row (as in
- * engram_lookup) contribute nothing.
+ * engram_lookup) contribute nothing.  More than 4096 entries are sorted by a
+ * cooperative launch, whose barriers set ENGRAM_ST_TIMEOUT if they run out.
  *   dout_d       [n_tokens][n_cols*row_dim] of `type`, rows dout_stride apart
  *   workspace_d  engram_lookup_grad_workspace_bytes(...) bytes, 256-byte aligned
  *
