@@ -76,6 +76,7 @@ struct SortArgs {
   int32_t chunks;
   int32_t* base;   // segments that begin before each chunk, or null
   int32_t* count;  // all of them
+  int32_t* next;   // the summing kernel's two counters, zeroed here
   int32_t* status;
 };
 
@@ -112,13 +113,14 @@ __device__ __forceinline__ bool meet(const SortArgs& a, int32_t& met) {
 // same digit in earlier blocks, rounds, warps and lanes come before it, which
 // keeps the passes stable.
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
-  __shared__ uint16_t hist[kSortWarps][kMaxDigits];
+  __shared__ __align__(16) uint16_t hist[kSortWarps][kMaxDigits];
   __shared__ int32_t place[kMaxDigits], half[kMaxDigits], warp_sum[kSortWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int digits = 1 << a.bits, blocks = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
   const int32_t e0 = a.n < static_cast<int64_t>(me) * a.per ? a.n : me * a.per;
   const int32_t e1 = a.n - e0 < a.per ? a.n : e0 + a.per;
   int32_t met = 0;
+  if (me == 0 && tid < 2) a.next[tid] = 0;
 
   for (int pass = 0; pass < a.passes; ++pass) {
     const bool first = pass == 0;
@@ -151,28 +153,40 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
       if (!meet(a, met)) return;
     }
 
-    // per digit: its entries in all blocks, and in the blocks before this one
-    // (two threads a digit, half the blocks each)
+    // per digit: its entries in all blocks, and in the blocks before this one;
+    // a thread sums four digits over an eighth of the blocks
     int32_t total = 0, prior = 0;
     if (blocks > 1) {
-      const int d = tid & (kMaxDigits - 1), h = tid / kMaxDigits;
-      const int b0 = h == 0 ? 0 : blocks / 2, b1 = h == 0 ? blocks / 2 : blocks;
-      if (d < digits) {
-#pragma unroll 16
-        for (int b = b0; b < b1; ++b) {
-          const int32_t c = __ldcg(a.counts + static_cast<int64_t>(b) * digits + d);
-          total += c;
-          prior += b < me ? c : 0;
+      constexpr int kParts = kSortThreads / (kMaxDigits / 4);
+      int32_t(*sums)[kMaxDigits] = reinterpret_cast<int32_t(*)[kMaxDigits]>(&hist[0][0]);
+      int32_t(*priors)[kMaxDigits] = sums + kParts;
+      static_assert(2 * kParts * kMaxDigits * 4 <= sizeof(hist), "the sums fit the histograms' place");
+      const int quad = tid % (kMaxDigits / 4), part = tid / (kMaxDigits / 4);
+      if (4 * quad < digits) {
+        int4 all = make_int4(0, 0, 0, 0), early = make_int4(0, 0, 0, 0);
+#pragma unroll 10
+        for (int b = part; b < blocks; b += kParts) {
+          const int4 c = __ldcg(reinterpret_cast<const int4*>(a.counts + static_cast<int64_t>(b) * digits + 4 * quad));
+          const bool before = b < me;
+          all.x += c.x;
+          all.y += c.y;
+          all.z += c.z;
+          all.w += c.w;
+          early.x += before ? c.x : 0;
+          early.y += before ? c.y : 0;
+          early.z += before ? c.z : 0;
+          early.w += before ? c.w : 0;
         }
-      }
-      if (h == 1 && d < digits) {
-        half[d] = total;
-        place[d] = prior;
+        *reinterpret_cast<int4*>(&sums[part][4 * quad]) = all;
+        *reinterpret_cast<int4*>(&priors[part][4 * quad]) = early;
       }
       __syncthreads();
-      if (h == 0 && d < digits) {
-        total += half[d];
-        prior += place[d];
+      if (tid < digits) {
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+          total += sums[k][tid];
+          prior += priors[k][tid];
+        }
       }
     } else if (tid < digits) {
       total = place[tid];
@@ -349,10 +363,15 @@ __device__ __forceinline__ void store_cols(float* row, int c0, int lane, int lan
   if constexpr (kAligned) {
     const int c = c0 + lane * kCols<E>;
     if (c < dim) {
-#pragma unroll
-      for (int j = 0; j < kCols<E>; j += 4)
-        *reinterpret_cast<float4*>(row + c + j) =
-            make_float4(scale * v[j], scale * v[j + 1], scale * v[j + 2], scale * v[j + 3]);
+      if constexpr (kCols<E> == 8) {
+        // one 32-byte store a lane: whole sectors, rows of 8 n floats on 32-byte boundaries
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + c), "f"(scale * v[0]),
+                     "f"(scale * v[1]), "f"(scale * v[2]), "f"(scale * v[3]), "f"(scale * v[4]), "f"(scale * v[5]),
+                     "f"(scale * v[6]), "f"(scale * v[7])
+                     : "memory");
+      } else {
+        *reinterpret_cast<float4*>(row + c) = make_float4(scale * v[0], scale * v[1], scale * v[2], scale * v[3]);
+      }
     }
   } else {
 #pragma unroll
@@ -382,6 +401,7 @@ struct SumArgs {
   float* grad;
   int32_t* rows;
   float *head, *tail;    // [chunk][dim]: the parts of a segment from before, of one that goes on
+  int32_t* next;         // [0] next task, [1] next rows to clear (zeroed by the sort)
 };
 
 template <class E>
@@ -391,24 +411,34 @@ __device__ __forceinline__ const typename E::T* entry_row(const SumArgs<E>& a, i
   return a.dout + t * a.dout_stride + static_cast<int64_t>(i - t * a.n_cols) * a.dim;
 }
 
-__device__ __forceinline__ void zero_row(float* row, int32_t dim, int lane) {
-  if ((reinterpret_cast<uintptr_t>(row) & 15) == 0 && dim % 4 == 0) {
-    for (int c = lane * 4; c < dim; c += 128) __stcs(reinterpret_cast<float4*>(row + c), make_float4(0.f, 0.f, 0.f, 0.f));
+__device__ __forceinline__ void zero_rows(float* row, int64_t count, int lane) {
+  if ((reinterpret_cast<uintptr_t>(row) & 15) == 0 && count % 4 == 0) {
+#pragma unroll 4
+    for (int64_t c = lane * 4; c < count; c += 128)
+      __stcs(reinterpret_cast<float4*>(row + c), make_float4(0.f, 0.f, 0.f, 0.f));
   } else {
-    for (int c = lane; c < dim; c += 32) row[c] = 0.f;
+    for (int64_t c = lane; c < count; c += 32) row[c] = 0.f;
   }
 }
 
-// kLanes lanes handle one (chunk, tile of kLanes * kCols columns).  When its
-// chunks are done, a block fills its share of the rows that no entry names.
+// kLanes lanes handle one (chunk, tile of kLanes * kCols columns) at a time,
+// taken from a counter; the rows that no entry names are cleared in the same
+// way, when the chunks are given out.  Which warp takes what changes nothing in
+// the results.
 template <class E, int kLanes, bool kAligned>
 __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
-  constexpr int N = kCols<E>, kGroups = kThreads / kLanes, kAhead = kAligned ? 8 : 4;
+  constexpr int N = kCols<E>, kGroups = 32 / kLanes, kAhead = kAligned ? 8 : 4;
+  const int wl = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lane = threadIdx.x % kLanes;
   const int64_t tasks = static_cast<int64_t>(a.chunks) * a.tiles;
-  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / kLanes; task < tasks;
-       task += static_cast<int64_t>(gridDim.x) * kGroups) {
-    const int32_t chunk = static_cast<int32_t>(task / a.tiles), tile = static_cast<int32_t>(task - static_cast<int64_t>(chunk) * a.tiles);
+  while (true) {
+    int32_t got = 0;
+    if (wl == 0) got = atomicAdd(a.next, 1);
+    const int64_t task = static_cast<int64_t>(__shfl_sync(0xffffffffu, got, 0)) * kGroups + wl / kLanes;
+    if (task - wl / kLanes >= tasks) break;
+    if (task >= tasks) continue;
+    const int32_t chunk = static_cast<int32_t>(task / a.tiles);
+    const int32_t tile = static_cast<int32_t>(task - static_cast<int64_t>(chunk) * a.tiles);
     const int c0 = tile * kLanes * N;
     const int32_t e0 = chunk * kChunk, e1 = a.n - e0 < kChunk ? a.n : e0 + kChunk;
     uint32_t key = a.keys[e0];
@@ -454,13 +484,17 @@ __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
     }
   }
 
-  const int wl = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (!a.dense) {
     const int32_t segs = *a.count;
-    for (int64_t s = segs + static_cast<int64_t>(blockIdx.x) * kWarps + warp; s < a.n;
-         s += static_cast<int64_t>(gridDim.x) * kWarps) {
-      if (wl == 0) a.rows[s] = -1;
-      zero_row(a.grad + s * a.dim, a.dim, wl);
+    constexpr int kRows = 16;  // a warp's share at a time
+    while (true) {
+      int32_t got = 0;
+      if (wl == 0) got = atomicAdd(a.next + 1, 1);
+      const int64_t s0 = segs + static_cast<int64_t>(__shfl_sync(0xffffffffu, got, 0)) * kRows;
+      if (s0 >= a.n) break;
+      const int64_t s1 = s0 + kRows < a.n ? s0 + kRows : a.n;
+      if (s0 + wl < s1) a.rows[s0 + wl] = -1;
+      zero_rows(a.grad + s0 * a.dim, (s1 - s0) * a.dim, wl);
     }
     return;
   }
@@ -469,8 +503,13 @@ __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
   const int kRange = a.range;
   __shared__ uint32_t named[kMaxRange / 32];
   __shared__ int32_t start;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRange; r0 < a.total_rows;
-       r0 += static_cast<int64_t>(gridDim.x) * kRange) {
+  __shared__ int32_t taken;
+  while (true) {
+    __syncthreads();
+    if (threadIdx.x == 0) taken = atomicAdd(a.next + 1, 1);
+    __syncthreads();
+    const int64_t r0 = static_cast<int64_t>(taken) * kRange;
+    if (r0 >= a.total_rows) break;
     if (threadIdx.x < kRange / 32) named[threadIdx.x] = 0u;
     if (warp == 0) {  // the first entry of row r0 or a later one, 32 probes at a time
       int32_t lo = 0, hi = a.n;
@@ -490,56 +529,34 @@ __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
       if (!__syncthreads_or(in)) break;
     }
     for (int r = warp; r < kRange && r0 + r < a.total_rows; r += kWarps)
-      if (!(named[r >> 5] >> (r & 31) & 1u)) zero_row(a.grad + (r0 + r) * a.dim, a.dim, wl);
-    __syncthreads();
+      if (!(named[r >> 5] >> (r & 31) & 1u)) zero_rows(a.grad + (r0 + r) * a.dim, a.dim, wl);
   }
 }
 
-// Joins the parts of the segments that cross chunks: one block per chunk in
-// which such a segment begins and tile of columns.  Warp w adds the parts of
-// the chunks w, w + 8, ... after it, then the warps' sums are added in order.
+// Joins the parts of the segments that cross chunks.  Every warp looks at one
+// chunk; where a segment begins in it and goes on, the warp adds the parts, or,
+// if there are many, all warps of the block do: warp w the parts w, w + 8, ...
+// of the segment, then the warps' sums in order.
+constexpr int kOwnParts = 12;  // parts that one warp adds alone
+
 template <class E, bool kAligned>
 __global__ void __launch_bounds__(kThreads) seg_join_kernel(SumArgs<E> a) {
   constexpr int N = kCols<E>;
   __shared__ float sums[kWarps][32 * N];
+  __shared__ int32_t parts[kWarps], segment[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int32_t chunk = blockIdx.x, e0 = chunk * kChunk, e1 = e0 + kChunk;
-  if (e1 >= a.n) return;
-  const uint32_t key = a.keys[e1 - 1];
-  // begins here and goes on
-  if (key == a.none || a.keys[e1] != key || (e0 > 0 && a.keys[e0 - 1] == key)) return;
-  // the segment's end, 32 probes at a time: keys[lo - 1] == key, keys[hi] > key
-  int32_t lo = e1 + 1, hi = a.n;
-  while (hi > lo) {
-    const int32_t step = (hi - lo + 31) / 32;
-    const int64_t q = static_cast<int64_t>(lo) + static_cast<int64_t>(step) * lane;
-    const int k = __popc(__ballot_sync(0xffffffffu, q < hi && a.keys[q] == key));
-    if (k == 0) break;
-    hi = static_cast<int64_t>(step) * k < hi - lo ? lo + step * k : hi;
-    lo = lo + step * (k - 1) + 1;
-  }
-  const int32_t more = (lo - 1) / kChunk - chunk;  // chunks after this one that it reaches into
-  int32_t seg = 0;
-  if (!a.dense) {  // the last segment that begins in this chunk
-    int32_t heads = 0;
-#pragma unroll
-    for (int k = 0; k < kChunk; k += 32)
-      heads += __popc(__ballot_sync(0xffffffffu, is_head(a.keys, static_cast<int64_t>(e0) + k + lane, a.n, a.none)));
-    seg = a.base[chunk] + heads - 1;
-  }
-  float* out = a.grad + (a.dense ? static_cast<int64_t>(key) : seg) * a.dim;
-  for (int c0 = blockIdx.y * 32 * N; c0 < a.dim; c0 += gridDim.y * 32 * N) {
-    float acc[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) acc[j] = 0.f;
-    auto add = [&](int32_t k) {
-      const float* part = (k == 0 ? a.tail : a.head) + static_cast<int64_t>(chunk + k) * a.dim;
+  const int32_t chunk = blockIdx.x * kWarps + warp, e0 = chunk * kChunk, e1 = e0 + kChunk;
+  // the parts begin + step * i, i < count, of the segment that begins in chunk c
+  auto add = [&](int32_t c, int32_t begin, int32_t step, int32_t count, int c0, float (&acc)[N]) {
+#pragma unroll 8
+    for (int32_t k = begin; k < count; k += step) {
+      const float* part = (k == 0 ? a.tail : a.head) + static_cast<int64_t>(c + k) * a.dim;
       if constexpr (kAligned) {
-        const int c = c0 + lane * N;
-        if (c < a.dim) {
+        const int col = c0 + lane * N;
+        if (col < a.dim) {
 #pragma unroll
           for (int j = 0; j < N; j += 4) {
-            const float4 q = *reinterpret_cast<const float4*>(part + c + j);
+            const float4 q = *reinterpret_cast<const float4*>(part + col + j);
             acc[j] += q.x;
             acc[j + 1] += q.y;
             acc[j + 2] += q.z;
@@ -549,23 +566,67 @@ __global__ void __launch_bounds__(kThreads) seg_join_kernel(SumArgs<E> a) {
       } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-          const int c = c0 + j * 32 + lane;
-          if (c < a.dim) acc[j] += part[c];
+          const int col = c0 + j * 32 + lane;
+          if (col < a.dim) acc[j] += part[col];
         }
       }
-    };
-#pragma unroll 8
-    for (int32_t k = warp; k <= more; k += kWarps) add(k);
-#pragma unroll
-    for (int j = 0; j < N; ++j) sums[warp][kAligned ? lane * N + j : j * 32 + lane] = acc[j];
-    __syncthreads();
-    const int used = more + 1 < kWarps ? more + 1 : kWarps;
-    for (int c = threadIdx.x; c < 32 * N; c += kThreads) {
-      float s = sums[0][c];
-      for (int w = 1; w < used; ++w) s += sums[w][c];
-      if (c0 + c < a.dim) out[c0 + c] = a.scale * s;
     }
-    __syncthreads();
+  };
+  int32_t mine = 0, seg = 0;
+  if (chunk < a.chunks && e1 < a.n) {
+    const uint32_t key = a.keys[e1 - 1];
+    if (key != a.none && a.keys[e1] == key && (e0 == 0 || a.keys[e0 - 1] != key)) {
+      // the segment's end, 32 probes at a time: keys[lo - 1] == key, keys[hi] > key
+      int32_t lo = e1 + 1, hi = a.n;
+      while (hi > lo) {
+        const int32_t step = (hi - lo + 31) / 32;
+        const int64_t q = static_cast<int64_t>(lo) + static_cast<int64_t>(step) * lane;
+        const int k = __popc(__ballot_sync(0xffffffffu, q < hi && a.keys[q] == key));
+        if (k == 0) break;
+        hi = static_cast<int64_t>(step) * k < hi - lo ? lo + step * k : hi;
+        lo = lo + step * (k - 1) + 1;
+      }
+      mine = (lo - 1) / kChunk - chunk + 1;
+      seg = static_cast<int32_t>(key);
+      if (!a.dense) {  // the last segment that begins in this chunk
+        int32_t heads = 0;
+#pragma unroll
+        for (int k = 0; k < kChunk; k += 32)
+          heads += __popc(__ballot_sync(0xffffffffu, is_head(a.keys, static_cast<int64_t>(e0) + k + lane, a.n, a.none)));
+        seg = a.base[chunk] + heads - 1;
+      }
+    }
+  }
+  if (lane == 0) {
+    parts[warp] = mine;
+    segment[warp] = seg;
+  }
+  for (int c0 = blockIdx.y * 32 * N; c0 < a.dim; c0 += gridDim.y * 32 * N) {
+    if (mine > 0 && mine <= kOwnParts) {
+      float acc[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] = 0.f;
+      add(chunk, 0, 1, mine, c0, acc);
+      store_cols<E, kAligned>(a.grad + static_cast<int64_t>(seg) * a.dim, c0, lane, 32, a.dim, a.scale, acc);
+    }
+    for (int s = 0; s < kWarps; ++s) {
+      __syncthreads();
+      if (parts[s] <= kOwnParts) continue;  // the same for all warps
+      float acc[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] = 0.f;
+      add(blockIdx.x * kWarps + s, warp, kWarps, parts[s], c0, acc);
+#pragma unroll
+      for (int j = 0; j < N; ++j) sums[warp][kAligned ? lane * N + j : j * 32 + lane] = acc[j];
+      __syncthreads();
+      float* out = a.grad + static_cast<int64_t>(segment[s]) * a.dim;
+      for (int c = threadIdx.x; c < 32 * N; c += kThreads) {
+        float total = sums[0][c];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) total += sums[w][c];
+        if (c0 + c < a.dim) out[c0 + c] = a.scale * total;
+      }
+    }
   }
 }
 
@@ -590,6 +651,7 @@ struct GradSpace {
   int32_t* counts;
   int32_t* barrier;
   int32_t* count;
+  int32_t* next;
   float *head, *tail;
   size_t bytes;
 };
@@ -609,6 +671,7 @@ GradSpace grad_space(void* at, int64_t n, int32_t dim) {
   const size_t chunks = static_cast<size_t>((n + kChunk - 1) / kChunk);
   s.barrier = reinterpret_cast<int32_t*>(take(4));
   s.count = reinterpret_cast<int32_t*>(take(4));
+  s.next = reinterpret_cast<int32_t*>(take(8));
   for (int k = 0; k < 2; ++k) s.key[k] = reinterpret_cast<uint32_t*>(take(words));
   for (int k = 0; k < 2; ++k) s.idx[k] = reinterpret_cast<int32_t*>(take(words));
   s.base = reinterpret_cast<int32_t*>(take(chunks * 4));
@@ -626,11 +689,10 @@ int launch_sums(const SumArgs<E>& a0, int sms, cudaStream_t st) {
   int lanes = 32;
   while (lanes > 4 && (lanes / 2) * kCols<E> >= a.dim) lanes /= 2;
   a.tiles = (a.dim + lanes * kCols<E> - 1) / (lanes * kCols<E>);
-  const int64_t groups = kThreads / lanes, want = (static_cast<int64_t>(a.chunks) * a.tiles + groups - 1) / groups;
-  const int64_t fill = static_cast<int64_t>(sms) * 4;
-  int64_t blocks = want > fill ? want : fill;
-  if (blocks > 0x7fffffff) blocks = 0x7fffffff;
-  const int g = static_cast<int>(blocks);
+  const int64_t groups = kThreads / lanes;
+  const int64_t want = (static_cast<int64_t>(a.chunks) * a.tiles + groups - 1) / groups, full = static_cast<int64_t>(sms) * 4;
+  // the resident blocks at most; all of them where there may be rows to clear
+  const int g = static_cast<int>(a.dense || want > full ? full : want);
   switch (lanes) {
     case 32: seg_sum_kernel<E, 32, kAligned><<<g, kThreads, 0, st>>>(a); break;
     case 16: seg_sum_kernel<E, 16, kAligned><<<g, kThreads, 0, st>>>(a); break;
@@ -639,7 +701,7 @@ int launch_sums(const SumArgs<E>& a0, int sms, cudaStream_t st) {
   }
   if (a.chunks > 1) {
     const int ty = (a.dim + 32 * kCols<E> - 1) / (32 * kCols<E>);
-    seg_join_kernel<E, kAligned><<<dim3(a.chunks, ty < 65535 ? ty : 65535), kThreads, 0, st>>>(a);
+    seg_join_kernel<E, kAligned><<<dim3((a.chunks + kWarps - 1) / kWarps, ty < 65535 ? ty : 65535), kThreads, 0, st>>>(a);
   }
   return check_launch("lookup gradient");
 }
@@ -680,6 +742,7 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
   sa.n = n;
   sa.passes = (width + kDigitBits - 1) / kDigitBits;
   sa.bits = (width + sa.passes - 1) / sa.passes;
+  if (sa.bits < 2) sa.bits = 2;  // counts are read four at a time
   for (int k = 0; k < 2; ++k) {
     sa.key[k] = w.key[k];
     sa.idx[k] = w.idx[k];
@@ -689,6 +752,7 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
   sa.chunks = chunks;
   sa.base = dense ? nullptr : w.base;
   sa.count = dense ? w.count : count_d;
+  sa.next = w.next;
   sa.status = status_d;
   // one block up to a round of entries; more blocks (at least 1024 entries
   // each) shorten the passes but cost two barriers a pass
@@ -741,7 +805,9 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
     a.rows = rows_d;
     a.head = w.head;
     a.tail = w.tail;
-    const bool vec = row_dim % kCols<E> == 0 && dout_stride % kCols<E> == 0 && aligned(dout_d, 16) && aligned(grad_d, 16);
+    a.next = w.next;
+    const bool vec = row_dim % kCols<E> == 0 && dout_stride % kCols<E> == 0 && aligned(dout_d, 16) &&
+                     aligned(grad_d, E::kBytes == 2 ? 32 : 16);
     return vec ? launch_sums<E, true>(a, sms, st) : launch_sums<E, false>(a, sms, st);
   };
   return type == ENGRAM_T_BF16 ? go(train::Bf16{}) : go(train::F32{});
