@@ -24,7 +24,7 @@
 namespace engram {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;  // three blocks of 56 registers a thread fill an SM
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTop = ENGRAM_DISTILL_MAX_TOP;
 constexpr int kMaxCluster = 8;
@@ -48,6 +48,7 @@ struct Head {  // in front of the dynamic shared memory
   uint64_t bar[kChunks];
   float2 part[kMaxCluster];  // the blocks' (maximum, sum of exponentials relative to it)
   float red[2 * kWarps];
+
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -104,6 +105,18 @@ __device__ __forceinline__ uint4 narrow(const float (&f)[kVec<E>]) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
 
+// The largest of a vector's values, NaN passed over.
+template <class E>
+__device__ __forceinline__ float largest(const uint4& x) {
+  if constexpr (E::kBytes == 2) {
+    auto as = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    const __nv_bfloat162 b = __hmax2(__hmax2(as(x.x), as(x.y)), __hmax2(as(x.z), as(x.w)));
+    return fmaxf(__low2float(b), __high2float(b));
+  } else {
+    return fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)), fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
+  }
+}
+
 // (m, s) <- the pair of both: sums of 2^((z - m) c), -inf maxima count nothing.
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float c) {
   const float top = fmaxf(m, m2), at = top == -INFINITY ? 0.f : top;
@@ -146,22 +159,25 @@ __global__ void __launch_bounds__(kThreads, kResident ? 3 : 4) distill_kernel(co
   const uint4* zv = reinterpret_cast<const uint4*>(zr - off);
   // vectors wholly inside the row
   const int in0 = off > 0 ? 1 : 0, in1 = (V + off) / N;
+  // the vector that reaches over the row's end is in this block's part
+  const bool tail = in1 < vecs && v0 <= in1 && in1 < v1 && !(in1 == 0 && in0 > 0);
 
   const float w = a.weight != nullptr ? a.weight[row] : 1.f;
+  auto zeros = [&]() {  // this block's part of a gradient of zeros
+    if (dz == nullptr) return;
+    const int e0 = v0 * N - off > 0 ? v0 * N - off : 0, e1 = v1 * N - off < V ? v1 * N - off : V;
+    if (off == doff) {
+      for (int v = (v0 > in0 ? v0 : in0) + tid; v < v1 && v < in1; v += kThreads)
+        reinterpret_cast<uint4*>(dr - off)[v] = make_uint4(0u, 0u, 0u, 0u);
+      if (in0 > 0 && v0 == 0 && tid < N - off && tid < V) E::store(dr + tid, 0.f);
+      if (tail && in1 * N - off + tid < V) E::store(dr + in1 * N - off + tid, 0.f);
+    } else {
+      for (int e = e0 + tid; e < e1; e += kThreads) E::store(dr + e, 0.f);
+    }
+  };
   if (w == 0.f) {  // nothing to learn here
     if (rank == 0 && tid == 0) a.loss[row] = 0.f;
-    if (dz != nullptr) {
-      const int e0 = v0 * N - off > 0 ? v0 * N - off : 0, e1 = v1 * N - off < V ? v1 * N - off : V;
-      if (off == doff) {
-        for (int v = v0 + tid; v < v1; v += kThreads)
-          if (v >= in0 && v < in1) reinterpret_cast<uint4*>(dr - off)[v] = make_uint4(0u, 0u, 0u, 0u);
-        if (v0 == 0 && tid < N - off && off > 0 && tid < V) E::store(dr + tid, 0.f);
-        if (v1 == vecs && v0 < vecs && in1 < vecs && (in1 > 0 || off == 0) && in1 * N - off + tid < V)
-          E::store(dr + in1 * N - off + tid, 0.f);
-      } else {
-        for (int e = e0 + tid; e < e1; e += kThreads) E::store(dr + e, 0.f);
-      }
-    }
+    zeros();
     return;
   }
 
@@ -175,7 +191,8 @@ __global__ void __launch_bounds__(kThreads, kResident ? 3 : 4) distill_kernel(co
     }
     return narrow<E>(f);
   };
-  const int chunk = (v1 - v0 + kChunks - 1) / kChunks;
+  // whole rounds of the block's threads
+  const int chunk = ((v1 - v0 + kChunks - 1) / kChunks + kThreads - 1) / kThreads * kThreads;
   if (kResident) {
     if (tid == 0) {
 #pragma unroll
@@ -192,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, kResident ? 3 : 4) distill_kernel(co
       }
     }
     if (tid == 32 && in0 > 0 && v0 == 0 && v1 > 0) row_s[0] = edge(0);
-    if (tid == 64 && in1 < vecs && v0 <= in1 && in1 < v1 && !(in1 == 0 && in0 > 0)) row_s[in1 - v0] = edge(in1);
+    if (tid == 64 && tail) row_s[in1 - v0] = edge(in1);
   }
   __syncwarp();
   if (a.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -225,31 +242,33 @@ __global__ void __launch_bounds__(kThreads, kResident ? 3 : 4) distill_kernel(co
   for (int k = tid; k < a.top; k += kThreads) mass += expf(p[k] - norm);
   mass = block_reduce<false>(mass, h.red);
 
-  // the maximum and the sum of this block's part
+  // the maximum and the sum of this block's part, kAhead vectors a step: their
+  // maximum first, so that the exponentials do not wait for one another
+  constexpr int kAhead = 4;
   float m = -INFINITY, s = 0.f;
-  auto add = [&](const uint4& x) {
-    float f[N], big;
-    widen<E>(x, f);
-    if constexpr (N == 8)
-      big = fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
-    else
-      big = fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));
-    if (big > m) {
-      s *= m == -INFINITY ? 0.f : ex2((m - big) * c);
-      m = big;
-    }
-    const float at = m == -INFINITY ? 0.f : -m;
+  auto add = [&](const uint4 (&x)[kAhead]) {
+    const float big = fmaxf(fmaxf(largest<E>(x[0]), largest<E>(x[1])), fmaxf(largest<E>(x[2]), largest<E>(x[3])));
+    const float top = fmaxf(m, big), at = top == -INFINITY ? 0.f : -top;
+    s *= ex2((m + at) * c);
+    m = top;
     uint64_t sum = f2(0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < N; j += 2) {
-      float x0, x1;
-      f2_split(f2_mul(f2_add(f2(f[j], f[j + 1]), f2(at, at)), f2(c, c)), x0, x1);
-      sum = f2_add(sum, f2(ex2(x0), ex2(x1)));
+    for (int u = 0; u < kAhead; ++u) {
+      float f[N];
+      widen<E>(x[u], f);
+#pragma unroll
+      for (int j = 0; j < N; j += 2) {
+        float x0, x1;
+        f2_split(f2_mul(f2_add(f2(f[j], f[j + 1]), f2(at, at)), f2(c, c)), x0, x1);
+        sum = f2_add(sum, f2(ex2(x0), ex2(x1)));
+      }
     }
     float s0, s1;
     f2_split(sum, s0, s1);
     s += s0 + s1;
   };
+  const uint32_t low = E::kBytes == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
+  const uint4 nothing = make_uint4(low, low, low, low);
   bool late = false;
   if (kResident) {
 #pragma unroll 1
@@ -259,12 +278,23 @@ __global__ void __launch_bounds__(kThreads, kResident ? 3 : 4) distill_kernel(co
         mbar_wait_bounded(smem_u32(&h.bar[k]), 0, nullptr);
       }
       const int b0 = k * chunk, b1 = b0 + chunk < v1 - v0 ? b0 + chunk : v1 - v0;
-#pragma unroll 2
-      for (int v = b0 + tid; v < b1; v += kThreads) add(row_s[v]);
+      for (int v = b0 + tid; v < b1; v += kAhead * kThreads) {
+        uint4 x[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) x[u] = v + u * kThreads < b1 ? row_s[v + u * kThreads] : nothing;
+        add(x);
+      }
     }
   } else {
-#pragma unroll 4
-    for (int v = v0 + tid; v < v1; v += kThreads) add(v >= in0 && v < in1 ? zv[v] : edge(v));
+    for (int v = v0 + tid; v < v1; v += kAhead * kThreads) {
+      uint4 x[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int vu = v + u * kThreads;
+        x[u] = vu >= v1 ? nothing : vu >= in0 && vu < in1 ? zv[vu] : edge(vu);
+      }
+      add(x);
+    }
   }
   if (late && a.status != nullptr) atomicOr(a.status, ENGRAM_ST_TIMEOUT);
 #pragma unroll
@@ -314,6 +344,10 @@ __global__ void __launch_bounds__(kThreads, kResident ? 3 : 4) distill_kernel(co
     if (tid == 0) a.loss[row] = none ? 0.f : w * a.tau * a.tau * loss;
   }
   if (dz == nullptr) return;
+  if (none) {
+    zeros();
+    return;
+  }
 
   const float scale = w * a.tau, coef = scale * mass / s;
   auto grad = [&](const uint4& x, float (&f)[N]) {
@@ -323,34 +357,42 @@ __global__ void __launch_bounds__(kThreads, kResident ? 3 : 4) distill_kernel(co
       float x0, x1;
       f2_split(f2_mul(f2_add(f2(f[j], f[j + 1]), f2(-m, -m)), f2(c, c)), x0, x1);
       f2_split(f2_mul(f2(ex2(x0), ex2(x1)), f2(coef, coef)), f[j], f[j + 1]);
-      if (none) f[j] = f[j + 1] = 0.f;
     }
   };
-  const uint4* src = kResident ? row_s - v0 : zv;
-  if (off == doff) {
-    uint4* dv = reinterpret_cast<uint4*>(dr - off);
-#pragma unroll 2
-    for (int v = v0 + tid; v < v1; v += kThreads) {
-      const bool inside = v >= in0 && v < in1;
-      float f[N];
-      grad(kResident || inside ? src[v] : edge(v), f);
-      if (inside) {
-        __stcs(dv + v, narrow<E>(f));
-      } else {
+  auto grad_edge = [&](int v) {
+    float f[N];
+    grad(kResident ? row_s[v - v0] : edge(v), f);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const int e = v * N + j - off;
-          if (e >= 0 && e < V) E::store(dr + e, f[j]);
-        }
+    for (int j = 0; j < N; ++j) {
+      const int e = v * N + j - off;
+      if (e >= 0 && e < V) E::store(dr + e, f[j]);
+    }
+  };
+  if (off == doff) {
+    const uint4* src = kResident ? row_s - v0 : zv;
+    uint4* dv = reinterpret_cast<uint4*>(dr - off);
+    const int end = v1 < in1 ? v1 : in1;
+    int v = (v0 > in0 ? v0 : in0) + tid;
+    for (; v + (kAhead - 1) * kThreads < end; v += kAhead * kThreads) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        float f[N];
+        grad(src[v + u * kThreads], f);
+        __stcs(dv + v + u * kThreads, narrow<E>(f));
       }
     }
+    for (; v < end; v += kThreads) {
+      float f[N];
+      grad(src[v], f);
+      __stcs(dv + v, narrow<E>(f));
+    }
+    if (tid == 32 && in0 > 0 && v0 == 0 && v1 > 0) grad_edge(0);
+    if (tid == 64 && tail) grad_edge(in1);
   } else {  // the gradient's rows lie differently: value by value
     const int e0 = v0 * N - off > 0 ? v0 * N - off : 0, e1 = v1 * N - off < V ? v1 * N - off : V;
     const typename E::T* part = kResident ? reinterpret_cast<const typename E::T*>(row_s) + off - v0 * N : zr;
-    for (int e = e0 + tid; e < e1; e += kThreads)
-      E::store(dr + e, none ? 0.f : ex2((E::load(part + e) - m) * c) * coef);
+    for (int e = e0 + tid; e < e1; e += kThreads) E::store(dr + e, ex2((E::load(part + e) - m) * c) * coef);
   }
-  if (none) return;
   // the entries' own gradients, over what was just written
   __syncthreads();
   for (int k = tid; k < a.top; k += kThreads) {

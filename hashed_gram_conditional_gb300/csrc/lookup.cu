@@ -52,16 +52,26 @@ constexpr int kItems = 4;                         // entries per thread and roun
 constexpr int kRound = kSortThreads * kItems;     // entries per block and round
 constexpr int kDigitBits = 9;
 constexpr int kMaxDigits = 1 << kDigitBits;
-constexpr int kChunk = 64;  // sorted entries that are summed together, see seg_sum_kernel
+constexpr int kGroup = 13;  // blocks whose digits are summed up for the others: 12 groups of 152 blocks
 
 __device__ __forceinline__ uint32_t entry_key(int32_t id, int64_t total_rows) {
   return id >= 0 && id < total_rows ? static_cast<uint32_t>(id) : static_cast<uint32_t>(total_rows);
 }
 
-__device__ __forceinline__ bool is_head(const uint32_t* keys, int64_t i, int32_t n, uint32_t none) {
+// A sorted entry: its id and its place i (one 8-byte store where it is moved to).
+struct __align__(8) Entry {
+  uint32_t key;
+  int32_t idx;
+};
+__device__ __forceinline__ Entry load_entry(const Entry* p) {
+  const uint2 v = __ldcg(reinterpret_cast<const uint2*>(p));
+  return Entry{v.x, static_cast<int32_t>(v.y)};
+}
+
+__device__ __forceinline__ bool is_head(const Entry* e, int64_t i, int32_t n, uint32_t none) {
   if (i >= n) return false;
-  const uint32_t k = __ldcg(keys + i);
-  return k != none && (i == 0 || k != __ldcg(keys + i - 1));
+  const uint32_t k = load_entry(e + i).key;
+  return k != none && (i == 0 || k != load_entry(e + i - 1).key);
 }
 
 struct SortArgs {
@@ -69,11 +79,11 @@ struct SortArgs {
   int64_t total_rows;
   int32_t n, per;  // entries, and how many each block handles
   int32_t passes, bits;
-  uint32_t* key[2];
-  int32_t* idx[2];
+  Entry* list[2];
   int32_t* counts;  // [block][digit], then [block] heads
+  int32_t* groups;  // [pass][group of kGroup blocks][digit], zeroed by the caller
   int32_t* barrier;
-  int32_t chunks;
+  int32_t chunk, chunks;  // sorted entries that are summed together (see seg_sum_kernel), and how many such
   int32_t* base;   // segments that begin before each chunk, or null
   int32_t* count;  // all of them
   int32_t* next;   // the summing kernel's two counters, zeroed here
@@ -125,14 +135,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
   for (int pass = 0; pass < a.passes; ++pass) {
     const bool first = pass == 0;
     const int shift = pass * a.bits;
-    const uint32_t* kin = first ? reinterpret_cast<const uint32_t*>(a.ids) : a.key[(pass - 1) & 1];
-    const int32_t* iin = first ? nullptr : a.idx[(pass - 1) & 1];
-    uint32_t* kout = a.key[pass & 1];
-    int32_t* iout = a.idx[pass & 1];
+    const Entry* in_list = a.list[(pass + 1) & 1];
+    Entry* out_list = a.list[pass & 1];
     auto digit_of = [&](uint32_t key) { return (key >> shift) & (digits - 1); };
-    auto key_at = [&](int32_t i) {
-      const uint32_t k = __ldcg(kin + i);
-      return first ? entry_key(static_cast<int32_t>(k), a.total_rows) : k;
+    auto entry_at = [&](int32_t i) {
+      return first ? Entry{entry_key(__ldg(a.ids + i), a.total_rows), i} : load_entry(in_list + i);
     };
 
     // this block's digits
@@ -144,17 +151,24 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
         const int32_t id = a.ids[i];
         bad |= id != ENGRAM_DEAD && (id < 0 || id >= a.total_rows);
       }
-      atomicAdd(&place[digit_of(key_at(i))], 1);
+      atomicAdd(&place[digit_of(entry_at(i).key)], 1);
     }
     if (bad && a.status != nullptr) atomicOr(a.status, ENGRAM_ST_BAD_ROW);
     __syncthreads();
+    int32_t* groups = nullptr;
     if (blocks > 1) {
-      if (tid < digits) __stcg(a.counts + static_cast<int64_t>(me) * digits + tid, place[tid]);
+      const int n_groups = (blocks + kGroup - 1) / kGroup;
+      groups = a.groups + static_cast<int64_t>(pass) * n_groups * digits;
+      if (tid < digits) {
+        __stcg(a.counts + static_cast<int64_t>(me) * digits + tid, place[tid]);
+        if (place[tid] != 0) atomicAdd(groups + (me / kGroup) * digits + tid, place[tid]);
+      }
       if (!meet(a, met)) return;
     }
 
-    // per digit: its entries in all blocks, and in the blocks before this one;
-    // a thread sums four digits over an eighth of the blocks
+    // per digit: its entries in all blocks, and in the blocks before this one:
+    // whole groups, then the blocks of this one's group.  A thread sums four
+    // digits over an eighth of the groups and blocks.
     int32_t total = 0, prior = 0;
     if (blocks > 1) {
       constexpr int kParts = kSortThreads / (kMaxDigits / 4);
@@ -162,21 +176,24 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
       int32_t(*priors)[kMaxDigits] = sums + kParts;
       static_assert(2 * kParts * kMaxDigits * 4 <= sizeof(hist), "the sums fit the histograms' place");
       const int quad = tid % (kMaxDigits / 4), part = tid / (kMaxDigits / 4);
+      const int my_group = me / kGroup, n_groups = (blocks + kGroup - 1) / kGroup;
       if (4 * quad < digits) {
         int4 all = make_int4(0, 0, 0, 0), early = make_int4(0, 0, 0, 0);
-#pragma unroll 10
-        for (int b = part; b < blocks; b += kParts) {
-          const int4 c = __ldcg(reinterpret_cast<const int4*>(a.counts + static_cast<int64_t>(b) * digits + 4 * quad));
-          const bool before = b < me;
-          all.x += c.x;
-          all.y += c.y;
-          all.z += c.z;
-          all.w += c.w;
-          early.x += before ? c.x : 0;
-          early.y += before ? c.y : 0;
-          early.z += before ? c.z : 0;
-          early.w += before ? c.w : 0;
+        auto add = [](int4& to, const int4& c, bool on) {
+          to.x += on ? c.x : 0;
+          to.y += on ? c.y : 0;
+          to.z += on ? c.z : 0;
+          to.w += on ? c.w : 0;
+        };
+#pragma unroll 4
+        for (int g = part; g < n_groups; g += kParts) {
+          const int4 c = __ldcg(reinterpret_cast<const int4*>(groups + static_cast<int64_t>(g) * digits + 4 * quad));
+          add(all, c, true);
+          add(early, c, g < my_group);
         }
+#pragma unroll 2
+        for (int b = my_group * kGroup + part; b < me; b += kParts)
+          add(early, __ldcg(reinterpret_cast<const int4*>(a.counts + static_cast<int64_t>(b) * digits + 4 * quad)), true);
         *reinterpret_cast<int4*>(&sums[part][4 * quad]) = all;
         *reinterpret_cast<int4*>(&priors[part][4 * quad]) = early;
       }
@@ -206,23 +223,27 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
     }
 
     for (int32_t r0 = e0; r0 < e1; r0 += kRound) {
-      uint32_t key[kItems];
-      int32_t idx[kItems];
+      Entry entry[kItems];
       int rank[kItems];
       const int32_t at = r0 + warp * (32 * kItems) + lane;  // (below 2^31 where it is used: see `in`)
       for (int d = lane; d < digits; d += 32) hist[warp][d] = 0;
 #pragma unroll
       for (int k = 0; k < kItems; ++k) {
         const bool in = static_cast<int64_t>(r0) + warp * (32 * kItems) + lane + 32 * k < e1;
-        key[k] = in ? key_at(at + 32 * k) : 0u;
-        idx[k] = !in || first ? at + 32 * k : __ldcg(iin + at + 32 * k);
+        entry[k] = in ? entry_at(at + 32 * k) : Entry{0u, 0};
       }
       __syncwarp();
 #pragma unroll
       for (int k = 0; k < kItems; ++k) {
         const bool in = static_cast<int64_t>(r0) + warp * (32 * kItems) + lane + 32 * k < e1;
-        const uint32_t d = in ? digit_of(key[k]) : kMaxDigits;
-        const uint32_t peers = __match_any_sync(0xffffffffu, d);
+        const uint32_t d = digit_of(entry[k].key);
+        uint32_t peers = __ballot_sync(0xffffffffu, in);  // the lanes with the same digit, bit by bit
+#pragma unroll
+        for (int bit = 0; bit < kDigitBits; ++bit) {
+          const bool one = d >> bit & 1u;
+          const uint32_t ones = __ballot_sync(0xffffffffu, one);
+          peers &= one ? ones : ~ones;
+        }
         const int before = in ? hist[warp][d] : 0;
         rank[k] = before + __popc(peers & ((1u << lane) - 1u));
         __syncwarp();
@@ -231,12 +252,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
       }
       __syncthreads();
       if (tid < digits) {  // entries of this round in earlier warps
-        int run = 0;
+        int c[kSortWarps], run = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) c[w] = hist[w][tid];
 #pragma unroll
         for (int w = 0; w < kSortWarps; ++w) {
-          const int c = hist[w][tid];
           hist[w][tid] = static_cast<uint16_t>(run);
-          run += c;
+          run += c[w];
         }
         half[tid] = run;
       }
@@ -244,10 +266,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
 #pragma unroll
       for (int k = 0; k < kItems; ++k) {
         if (static_cast<int64_t>(r0) + warp * (32 * kItems) + lane + 32 * k < e1) {
-          const uint32_t d = digit_of(key[k]);
+          const uint32_t d = digit_of(entry[k].key);
           const int32_t to = place[d] + hist[warp][d] + rank[k];
-          __stcg(kout + to, key[k]);
-          __stcg(iout + to, idx[k]);
+          __stcg(reinterpret_cast<uint2*>(out_list + to), make_uint2(entry[k].key, static_cast<uint32_t>(entry[k].idx)));
         }
       }
       __syncthreads();
@@ -260,7 +281,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
 
   // segments that begin in each chunk, summed up over the chunks before it
   const uint32_t none = static_cast<uint32_t>(a.total_rows);
-  const uint32_t* keys = a.key[(a.passes - 1) & 1];
+  const Entry* list = a.list[(a.passes - 1) & 1];
   const int32_t cper = (a.chunks + blocks - 1) / blocks;
   const int32_t c0 = a.chunks < static_cast<int64_t>(me) * cper ? a.chunks : me * cper;
   const int32_t c1 = a.chunks - c0 < cper ? a.chunks : c0 + cper;
@@ -268,9 +289,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
   __syncthreads();
   for (int32_t c = c0 + warp; c < c1; c += kSortWarps) {
     int32_t heads = 0;
-#pragma unroll
-    for (int k = 0; k < kChunk; k += 32)
-      heads += __popc(__ballot_sync(0xffffffffu, is_head(keys, static_cast<int64_t>(c) * kChunk + k + lane, a.n, none)));
+    for (int k = 0; k < a.chunk; k += 32)
+      heads += __popc(__ballot_sync(0xffffffffu, k + lane < a.chunk &&
+                                                     is_head(list, static_cast<int64_t>(c) * a.chunk + k + lane, a.n, none)));
     if (lane == 0) {
       __stcg(a.base + c, heads);
       atomicAdd(&half[0], heads);
@@ -311,10 +332,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
 
 // ------------------------------------------------------- segments of equal id
 
-// The sorted entries are summed in chunks of kChunk: equal work however long
-// or short the segments are.  A segment inside its chunk goes straight to the
-// result; one that crosses a border leaves a part in each chunk it touches,
-// and the parts are joined in order afterwards.
+// The sorted entries are summed in chunks: equal work however long or short the
+// segments are.  A segment inside its chunk goes straight to the result; one
+// that crosses a border leaves a part in each chunk it touches, and the parts
+// are joined in order afterwards.
+
 // 8 bf16 or 4 fp32 columns of a row per lane.  Aligned rows are read 16 bytes
 // a lane; others column by column, the lanes next to one another.
 template <class E>
@@ -388,10 +410,9 @@ template <class E>
 struct SumArgs {
   const typename E::T* dout;
   int64_t dout_stride;
-  int32_t dim, n_cols, n, chunks, tiles;  // tiles of a row's columns
+  int32_t dim, n_cols, n, chunk, chunks, tiles;  // tiles of a row's columns
   float scale;
-  const uint32_t* keys;
-  const int32_t* idx;
+  const Entry* list;
   uint32_t none;
   bool dense, contiguous;
   const int32_t* base;   // rows form: segments before each chunk
@@ -440,10 +461,10 @@ __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
     const int32_t chunk = static_cast<int32_t>(task / a.tiles);
     const int32_t tile = static_cast<int32_t>(task - static_cast<int64_t>(chunk) * a.tiles);
     const int c0 = tile * kLanes * N;
-    const int32_t e0 = chunk * kChunk, e1 = a.n - e0 < kChunk ? a.n : e0 + kChunk;
-    uint32_t key = a.keys[e0];
+    const int32_t e0 = chunk * a.chunk, e1 = a.n - e0 < a.chunk ? a.n : e0 + a.chunk;
+    uint32_t key = a.list[e0].key;
     if (key == a.none) continue;  // sorted: none of the chunk's entries has a row
-    bool from_before = e0 > 0 && a.keys[e0 - 1] == key;
+    bool from_before = e0 > 0 && a.list[e0 - 1].key == key;
     int32_t seg = a.dense ? 0 : a.base[chunk];
     if (from_before) --seg;
     float acc[N];
@@ -452,12 +473,18 @@ __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
     for (int32_t e = e0; e < e1; e += kAhead) {
       uint4 x[kAhead];
       uint32_t after[kAhead];  // the next entry's key
+      // two entries a load; the list's end is padded to whole 256 bytes
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        x[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (e + k < e1) x[k] = load_cols<E, kAligned>(entry_row(a, __ldg(a.idx + e + k)), c0, lane, kLanes, a.dim);
-        after[k] = e + k + 1 < a.n ? __ldg(a.keys + e + k + 1) : a.none;
+      for (int k = 0; k < kAhead; k += 2) {
+        const uint4 two = __ldg(reinterpret_cast<const uint4*>(a.list + e + k));
+        x[k] = x[k + 1] = make_uint4(0u, 0u, 0u, 0u);
+        if (e + k < e1) x[k] = load_cols<E, kAligned>(entry_row(a, static_cast<int32_t>(two.y)), c0, lane, kLanes, a.dim);
+        if (e + k + 1 < e1)
+          x[k + 1] = load_cols<E, kAligned>(entry_row(a, static_cast<int32_t>(two.w)), c0, lane, kLanes, a.dim);
+        if (k > 0) after[k - 1] = e + k < a.n ? two.x : a.none;
+        after[k] = e + k + 1 < a.n ? two.z : a.none;
       }
+      after[kAhead - 1] = e + kAhead < a.n ? __ldg(&a.list[e + kAhead].key) : a.none;
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         if (e + k >= e1 || key == a.none) break;
@@ -515,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
       int32_t lo = 0, hi = a.n;
       while (hi > lo) {
         const int32_t step = (hi - lo + 31) / 32, q = lo + step * wl;
-        const int k = __popc(__ballot_sync(0xffffffffu, q < hi && q >= lo && a.keys[q] < r0));
+        const int k = __popc(__ballot_sync(0xffffffffu, q < hi && q >= lo && a.list[q].key < r0));
         if (k == 0) break;
         hi = step * k < hi - lo ? lo + step * k : hi;
         lo = lo + step * (k - 1) + 1;
@@ -524,8 +551,9 @@ __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
     }
     __syncthreads();
     for (int32_t e = start + threadIdx.x;; e += kThreads) {
-      const bool in = e < a.n && e >= 0 && a.keys[e] < r0 + kRange && a.keys[e] != a.none;
-      if (in) atomicOr(&named[(a.keys[e] - r0) >> 5], 1u << ((a.keys[e] - r0) & 31));
+      const uint32_t key = e < a.n && e >= 0 ? a.list[e].key : a.none;
+      const bool in = key < r0 + kRange && key != a.none;
+      if (in) atomicOr(&named[(key - r0) >> 5], 1u << ((key - r0) & 31));
       if (!__syncthreads_or(in)) break;
     }
     for (int r = warp; r < kRange && r0 + r < a.total_rows; r += kWarps)
@@ -535,64 +563,70 @@ __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
 
 // Joins the parts of the segments that cross chunks.  Every warp looks at one
 // chunk; where a segment begins in it and goes on, the warp adds the parts, or,
-// if there are many, all warps of the block do: warp w the parts w, w + 8, ...
+// if there are many, all warps of the block do: warp w the parts w, w + 16, ...
 // of the segment, then the warps' sums in order.
 constexpr int kOwnParts = 12;  // parts that one warp adds alone
+constexpr int kJoinWarps = 16;
 
 template <class E, bool kAligned>
-__global__ void __launch_bounds__(kThreads) seg_join_kernel(SumArgs<E> a) {
-  constexpr int N = kCols<E>;
+__global__ void __launch_bounds__(kJoinWarps * 32) seg_join_kernel(SumArgs<E> a) {
+  constexpr int N = kCols<E>, kWarps = kJoinWarps;
   __shared__ float sums[kWarps][32 * N];
   __shared__ int32_t parts[kWarps], segment[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int32_t chunk = blockIdx.x * kWarps + warp, e0 = chunk * kChunk, e1 = e0 + kChunk;
-  // the parts begin + step * i, i < count, of the segment that begins in chunk c
+  const int32_t chunk = blockIdx.x * kWarps + warp, e0 = chunk * a.chunk, e1 = e0 + a.chunk;
+  // the parts begin + step * i below count of the segment that begins in chunk c,
+  // kBatch of them in flight
+  constexpr int kBatch = 8;
   auto add = [&](int32_t c, int32_t begin, int32_t step, int32_t count, int c0, float (&acc)[N]) {
-#pragma unroll 8
-    for (int32_t k = begin; k < count; k += step) {
-      const float* part = (k == 0 ? a.tail : a.head) + static_cast<int64_t>(c + k) * a.dim;
-      if constexpr (kAligned) {
-        const int col = c0 + lane * N;
-        if (col < a.dim) {
+    for (int32_t k0 = begin; k0 < count; k0 += kBatch * step) {
+      float q[kBatch][N];
 #pragma unroll
-          for (int j = 0; j < N; j += 4) {
-            const float4 q = *reinterpret_cast<const float4*>(part + col + j);
-            acc[j] += q.x;
-            acc[j + 1] += q.y;
-            acc[j + 2] += q.z;
-            acc[j + 3] += q.w;
+      for (int b = 0; b < kBatch; ++b) {
+        const int32_t k = k0 + b * step;
+        const float* part = (k == 0 ? a.tail : a.head) + static_cast<int64_t>(c + k) * a.dim + c0;
+#pragma unroll
+        for (int j = 0; j < N; j += kAligned ? 4 : 1) {
+          const int col = kAligned ? lane * N + j : j * 32 + lane;
+          const bool in = k < count && c0 + col < a.dim;
+          if constexpr (kAligned) {
+            const float4 v = in ? *reinterpret_cast<const float4*>(part + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+            q[b][j] = v.x;
+            q[b][j + 1] = v.y;
+            q[b][j + 2] = v.z;
+            q[b][j + 3] = v.w;
+          } else {
+            q[b][j] = in ? part[col] : 0.f;
           }
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const int col = c0 + j * 32 + lane;
-          if (col < a.dim) acc[j] += part[col];
-        }
       }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] += q[b][j];
     }
   };
   int32_t mine = 0, seg = 0;
-  if (chunk < a.chunks && e1 < a.n) {
-    const uint32_t key = a.keys[e1 - 1];
-    if (key != a.none && a.keys[e1] == key && (e0 == 0 || a.keys[e0 - 1] != key)) {
-      // the segment's end, 32 probes at a time: keys[lo - 1] == key, keys[hi] > key
+  if (chunk < a.chunks - 1) {
+    const uint32_t key = a.list[e1 - 1].key;
+    if (key != a.none && a.list[e1].key == key && (e0 == 0 || a.list[e0 - 1].key != key)) {
+      // the segment's end, 32 probes at a time: the entry lo - 1 has the key, the entry hi a larger one
       int32_t lo = e1 + 1, hi = a.n;
       while (hi > lo) {
         const int32_t step = (hi - lo + 31) / 32;
         const int64_t q = static_cast<int64_t>(lo) + static_cast<int64_t>(step) * lane;
-        const int k = __popc(__ballot_sync(0xffffffffu, q < hi && a.keys[q] == key));
+        const int k = __popc(__ballot_sync(0xffffffffu, q < hi && a.list[q].key == key));
         if (k == 0) break;
         hi = static_cast<int64_t>(step) * k < hi - lo ? lo + step * k : hi;
         lo = lo + step * (k - 1) + 1;
       }
-      mine = (lo - 1) / kChunk - chunk + 1;
+      mine = (lo - 1) / a.chunk - chunk + 1;
       seg = static_cast<int32_t>(key);
       if (!a.dense) {  // the last segment that begins in this chunk
         int32_t heads = 0;
-#pragma unroll
-        for (int k = 0; k < kChunk; k += 32)
-          heads += __popc(__ballot_sync(0xffffffffu, is_head(a.keys, static_cast<int64_t>(e0) + k + lane, a.n, a.none)));
+        for (int k = 0; k < a.chunk; k += 32)
+          heads += __popc(__ballot_sync(0xffffffffu, k + lane < a.chunk && is_head(a.list, static_cast<int64_t>(e0) + k + lane,
+                                                                                   a.n, a.none)));
         seg = a.base[chunk] + heads - 1;
       }
     }
@@ -620,7 +654,7 @@ __global__ void __launch_bounds__(kThreads) seg_join_kernel(SumArgs<E> a) {
       for (int j = 0; j < N; ++j) sums[warp][kAligned ? lane * N + j : j * 32 + lane] = acc[j];
       __syncthreads();
       float* out = a.grad + static_cast<int64_t>(segment[s]) * a.dim;
-      for (int c = threadIdx.x; c < 32 * N; c += kThreads) {
+      for (int c = threadIdx.x; c < 32 * N; c += kWarps * 32) {
         float total = sums[0][c];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) total += sums[w][c];
@@ -645,11 +679,10 @@ int check_lookup(int32_t type, int64_t total_rows, int32_t row_dim, int64_t n_to
 
 // The parts of the gradient's workspace.
 struct GradSpace {
-  uint32_t* key[2];
-  int32_t* idx[2];
+  Entry* list[2];
   int32_t* base;
   int32_t* counts;
-  int32_t* barrier;
+  int32_t* barrier;  // then the group sums
   int32_t* count;
   int32_t* next;
   float *head, *tail;
@@ -657,6 +690,19 @@ struct GradSpace {
 };
 
 constexpr int kMaxSortBlocks = 256;  // one per SM
+constexpr int kMaxGroups = (kMaxSortBlocks + kGroup - 1) / kGroup, kMaxPasses = 4;
+
+// Entries per chunk: the fewest of 16, 32, 64 and 128 that give no more tasks
+// than five quarters of the lane groups that 152 SMs hold (4 blocks of 8
+// warps).  Fewer entries shorten a small call, whose tasks all run at once;
+// more entries leave fewer parts to join (393,216 entries of 256 columns: 128
+// against 64 takes 184 against 200 us; 16,384 of 5120: 362 against 355).
+int32_t chunk_for(int64_t n, int32_t dim, int cols) {
+  const int64_t tiles = (dim + 32 * cols - 1) / (32 * cols);
+  int32_t chunk = 16;
+  while (chunk < 128 && (n + chunk - 1) / chunk * tiles > 4864 * 5 / 4) chunk *= 2;
+  return chunk;
+}
 
 GradSpace grad_space(void* at, int64_t n, int32_t dim) {
   GradSpace s;
@@ -667,13 +713,12 @@ GradSpace grad_space(void* at, int64_t n, int32_t dim) {
     used += round256(bytes);
     return q;
   };
-  const size_t words = static_cast<size_t>(n) * 4;
-  const size_t chunks = static_cast<size_t>((n + kChunk - 1) / kChunk);
-  s.barrier = reinterpret_cast<int32_t*>(take(4));
+  const int32_t fewest = chunk_for(n, dim, kCols<train::Bf16>);  // serves both types: fp32 has more tiles
+  const size_t chunks = static_cast<size_t>((n + fewest - 1) / fewest);
+  s.barrier = reinterpret_cast<int32_t*>(take((4 + static_cast<size_t>(kMaxPasses) * kMaxGroups * kMaxDigits) * 4));
   s.count = reinterpret_cast<int32_t*>(take(4));
   s.next = reinterpret_cast<int32_t*>(take(8));
-  for (int k = 0; k < 2; ++k) s.key[k] = reinterpret_cast<uint32_t*>(take(words));
-  for (int k = 0; k < 2; ++k) s.idx[k] = reinterpret_cast<int32_t*>(take(words));
+  for (int k = 0; k < 2; ++k) s.list[k] = reinterpret_cast<Entry*>(take(static_cast<size_t>(n) * sizeof(Entry)));
   s.base = reinterpret_cast<int32_t*>(take(chunks * 4));
   s.counts = reinterpret_cast<int32_t*>(take(static_cast<size_t>(kMaxSortBlocks) * kMaxDigits * 4));
   s.head = reinterpret_cast<float*>(take(chunks * dim * 4));
@@ -701,7 +746,8 @@ int launch_sums(const SumArgs<E>& a0, int sms, cudaStream_t st) {
   }
   if (a.chunks > 1) {
     const int ty = (a.dim + 32 * kCols<E> - 1) / (32 * kCols<E>);
-    seg_join_kernel<E, kAligned><<<dim3((a.chunks + kWarps - 1) / kWarps, ty < 65535 ? ty : 65535), kThreads, 0, st>>>(a);
+    seg_join_kernel<E, kAligned>
+        <<<dim3((a.chunks + kJoinWarps - 1) / kJoinWarps, ty < 65535 ? ty : 65535), kJoinWarps * 32, 0, st>>>(a);
   }
   return check_launch("lookup gradient");
 }
@@ -734,7 +780,8 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
   const GradSpace w = grad_space(workspace_d, n, row_dim);
   int width = 1;  // bits of the keys, total_rows standing for "no row"
   while ((total_rows >> width) != 0) ++width;
-  const int32_t chunks = (n + kChunk - 1) / kChunk;
+  const int32_t chunk = chunk_for(n, row_dim, type == ENGRAM_T_BF16 ? kCols<train::Bf16> : kCols<train::F32>);
+  const int32_t chunks = static_cast<int32_t>((n64 + chunk - 1) / chunk);
   const uint32_t none = static_cast<uint32_t>(total_rows);
   SortArgs sa{};
   sa.ids = ids_d;
@@ -743,12 +790,11 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
   sa.passes = (width + kDigitBits - 1) / kDigitBits;
   sa.bits = (width + sa.passes - 1) / sa.passes;
   if (sa.bits < 2) sa.bits = 2;  // counts are read four at a time
-  for (int k = 0; k < 2; ++k) {
-    sa.key[k] = w.key[k];
-    sa.idx[k] = w.idx[k];
-  }
+  for (int k = 0; k < 2; ++k) sa.list[k] = w.list[k];
   sa.counts = w.counts;
   sa.barrier = w.barrier;
+  sa.groups = w.barrier + 4;
+  sa.chunk = chunk;
   sa.chunks = chunks;
   sa.base = dense ? nullptr : w.base;
   sa.count = dense ? w.count : count_d;
@@ -763,7 +809,8 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
   }
   sa.per = (n + blocks - 1) / blocks;
   if (blocks > 1) {
-    cudaError_t err = cudaMemsetAsync(w.barrier, 0, 4, st);
+    const size_t zeroed = 4 + static_cast<size_t>(sa.passes) * ((blocks + kGroup - 1) / kGroup) * (1 << sa.bits);
+    cudaError_t err = cudaMemsetAsync(w.barrier, 0, zeroed * 4, st);
     if (err != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(err));
   }
   cudaLaunchConfig_t cfg = {};
@@ -777,8 +824,6 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
   cfg.numAttrs = blocks > 1 ? 1 : 0;
   cudaError_t err = cudaLaunchKernelEx(&cfg, sort_kernel, sa);
   if (err != cudaSuccess) return fail(ENGRAM_E_CUDA, "sort_kernel launch: %s", cudaGetErrorString(err));
-  const uint32_t* kin = w.key[(sa.passes - 1) & 1];
-  const int32_t* iin = w.idx[(sa.passes - 1) & 1];
   if ((rc = check_launch("sort_kernel"))) return rc;
   auto go = [&](auto e) {
     using E = decltype(e);
@@ -788,10 +833,10 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
     a.dim = row_dim;
     a.n_cols = n_cols;
     a.n = n;
+    a.chunk = chunk;
     a.chunks = chunks;
     a.scale = scale;
-    a.keys = kin;
-    a.idx = iin;
+    a.list = w.list[(sa.passes - 1) & 1];
     a.none = none;
     a.dense = dense;
     a.contiguous = dout_stride == static_cast<int64_t>(n_cols) * row_dim;
