@@ -24,8 +24,9 @@
 namespace engram {
 namespace {
 
-constexpr int kThreads = 384;  // three blocks of 56 registers a thread fill an SM
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 8;               // that go over the row
+constexpr int kData = kWarps * 32;
+constexpr int kThreads = kData + 32;    // and one that prepares the teacher's probabilities meanwhile
 constexpr int kMaxTop = ENGRAM_DISTILL_MAX_TOP;
 constexpr int kMaxCluster = 8;
 constexpr int kChunks = 4;                 // pieces of a part that are awaited one by one
@@ -46,9 +47,10 @@ struct Args {
 
 struct Head {  // in front of the dynamic shared memory
   uint64_t bar[kChunks];
+  uint64_t met;              // completes when every block's pair is here
   float2 part[kMaxCluster];  // the blocks' (maximum, sum of exponentials relative to it)
-  float red[2 * kWarps];
-
+  float2 warp[kWarps];
+  float norm, mass;          // of the teacher's entries
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -57,20 +59,13 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// Sum or maximum over the block, the same in every thread and run.
 template <bool kMax>
-__device__ float block_reduce(float v, float* red) {
+__device__ __forceinline__ float warp_reduce(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float w = __shfl_xor_sync(0xffffffffu, v, o);
     v = kMax ? fmaxf(v, w) : v + w;
   }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) v = kMax ? fmaxf(v, red[w]) : v + red[w];
   return v;
 }
 
@@ -135,7 +130,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // (`off` elements before it); vectors that reach over the row's ends are
 // filled up with -inf, which adds nothing to the sums.
 template <class E, bool kResident>
-__global__ void __launch_bounds__(kThreads, kResident ? 3 : 4) distill_kernel(const typename E::T* z,
+__global__ void __launch_bounds__(kThreads, 3) distill_kernel(const typename E::T* z,
                                                                               typename E::T* dz, Args a) {
   constexpr int N = kVec<E>;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -191,13 +186,15 @@ __global__ void __launch_bounds__(kThreads, kResident ? 3 : 4) distill_kernel(co
     }
     return narrow<E>(f);
   };
-  // whole rounds of the block's threads
-  const int chunk = ((v1 - v0 + kChunks - 1) / kChunks + kThreads - 1) / kThreads * kThreads;
-  if (kResident) {
-    if (tid == 0) {
+  // whole rounds of the threads
+  const int chunk = ((v1 - v0 + kChunks - 1) / kChunks + kData - 1) / kData * kData;
+  if (tid == 0) {
 #pragma unroll
-      for (int k = 0; k < kChunks; ++k) mbar_init(smem_u32(&h.bar[k]), 1);
-      fence_mbar_init();
+    for (int k = 0; k < kChunks; ++k) mbar_init(smem_u32(&h.bar[k]), 1);
+    mbar_init(smem_u32(&h.met), 1);
+    fence_mbar_init();
+    if (a.cluster > 1) mbar_arrive_expect_tx(smem_u32(&h.met), static_cast<uint32_t>(a.cluster) * sizeof(float2));
+    if (kResident) {
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
         int b0 = v0 + k * chunk, b1 = b0 + chunk < v1 ? b0 + chunk : v1;
@@ -208,140 +205,149 @@ __global__ void __launch_bounds__(kThreads, kResident ? 3 : 4) distill_kernel(co
         if (bytes > 0) bulk_g2s(smem_u32(row_s + (b0 - v0)), zv + b0, bytes, smem_u32(&h.bar[k]));
       }
     }
+  }
+  if (kResident) {
     if (tid == 32 && in0 > 0 && v0 == 0 && v1 > 0) row_s[0] = edge(0);
     if (tid == 64 && tail) row_s[in1 - v0] = edge(in1);
   }
-  __syncwarp();
-  if (a.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  __syncthreads();
+  if (a.cluster > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
-  // the teacher's probabilities
-  const float inv_tau = 1.f / a.tau, c = 1.4426950408889634f * inv_tau;
-  float top = -INFINITY;
-  for (int k = tid; k < a.top; k += kThreads) {
-    int32_t v = a.ids[row * a.top + k];
-    if (v >= a.vocab) {
-      if (a.status != nullptr) atomicOr(a.status, ENGRAM_ST_BAD_TOKEN);
-      v = -1;
-    }
-    id[k] = v < 0 ? -1 : v;
-    p[k] = v >= 0 ? a.t[row * a.top + k] * inv_tau : -INFINITY;
-    zk[k] = v >= 0 ? E::load(zr + v) : 0.f;
-    top = fmaxf(top, p[k]);
-  }
-  top = block_reduce<true>(top, h.red);  // (the first barrier after the mbarriers' and edges' stores)
-  float norm = 0.f;
-  if (a.lse != nullptr) {
-    norm = a.lse[row];
-  } else {
-    float sum = 0.f;
-    for (int k = tid; k < a.top; k += kThreads) sum += top == -INFINITY ? 0.f : expf(p[k] - top);
-    sum = block_reduce<false>(sum, h.red);
-    norm = top == -INFINITY ? 0.f : top + logf(sum);
-  }
-  float mass = 0.f;
-  for (int k = tid; k < a.top; k += kThreads) mass += expf(p[k] - norm);
-  mass = block_reduce<false>(mass, h.red);
-
-  // the maximum and the sum of this block's part, kAhead vectors a step: their
-  // maximum first, so that the exponentials do not wait for one another
   constexpr int kAhead = 4;
-  float m = -INFINITY, s = 0.f;
-  auto add = [&](const uint4 (&x)[kAhead]) {
-    const float big = fmaxf(fmaxf(largest<E>(x[0]), largest<E>(x[1])), fmaxf(largest<E>(x[2]), largest<E>(x[3])));
-    const float top = fmaxf(m, big), at = top == -INFINITY ? 0.f : -top;
-    s *= ex2((m + at) * c);
-    m = top;
-    uint64_t sum = f2(0.f, 0.f);
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      float f[N];
-      widen<E>(x[u], f);
-#pragma unroll
-      for (int j = 0; j < N; j += 2) {
-        float x0, x1;
-        f2_split(f2_mul(f2_add(f2(f[j], f[j + 1]), f2(at, at)), f2(c, c)), x0, x1);
-        sum = f2_add(sum, f2(ex2(x0), ex2(x1)));
-      }
-    }
-    float s0, s1;
-    f2_split(sum, s0, s1);
-    s += s0 + s1;
-  };
-  const uint32_t low = E::kBytes == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
-  const uint4 nothing = make_uint4(low, low, low, low);
+  const float inv_tau = 1.f / a.tau, c = 1.4426950408889634f * inv_tau;
+  const int lane = tid & 31, warp = tid >> 5;
   bool late = false;
-  if (kResident) {
-#pragma unroll 1
-    for (int k = 0; k < kChunks; ++k) {
-      if (!mbar_wait_bounded(smem_u32(&h.bar[k]), 0, nullptr)) {
-        late = true;  // give the copy one more chance to land before the block goes on
-        mbar_wait_bounded(smem_u32(&h.bar[k]), 0, nullptr);
+  if (warp == kWarps) {
+    // the teacher's entries: id, logit / tau and the student's logit
+    float top = -INFINITY;
+    for (int k = lane; k < a.top; k += 32) {
+      int32_t v = a.ids[row * a.top + k];
+      if (v >= a.vocab) {
+        if (a.status != nullptr) atomicOr(a.status, ENGRAM_ST_BAD_TOKEN);
+        v = -1;
       }
-      const int b0 = k * chunk, b1 = b0 + chunk < v1 - v0 ? b0 + chunk : v1 - v0;
-      for (int v = b0 + tid; v < b1; v += kAhead * kThreads) {
+      id[k] = v < 0 ? -1 : v;
+      p[k] = v >= 0 ? a.t[row * a.top + k] * inv_tau : -INFINITY;
+      zk[k] = v >= 0 ? E::load(zr + v) : 0.f;
+      top = fmaxf(top, p[k]);
+    }
+    top = warp_reduce<true>(top);
+    float norm = 0.f;
+    if (a.lse != nullptr) {
+      norm = a.lse[row];
+    } else if (top != -INFINITY) {
+      float sum = 0.f;
+      for (int k = lane; k < a.top; k += 32) sum += expf(p[k] - top);
+      norm = top + logf(warp_reduce<false>(sum));
+    }
+    float mass = 0.f;
+    for (int k = lane; k < a.top; k += 32) mass += expf(p[k] - norm);
+    mass = warp_reduce<false>(mass);
+    if (lane == 0) {
+      h.norm = norm;
+      h.mass = mass;
+    }
+  } else {
+    // the maximum and the sum of this block's part, kAhead vectors a step: their
+    // maximum first, so that the exponentials do not wait for one another
+    float m = -INFINITY, s = 0.f;
+    auto add = [&](const uint4 (&x)[kAhead]) {
+      const float big = fmaxf(fmaxf(largest<E>(x[0]), largest<E>(x[1])), fmaxf(largest<E>(x[2]), largest<E>(x[3])));
+      const float top = fmaxf(m, big), at = top == -INFINITY ? 0.f : -top;
+      s *= ex2((m + at) * c);
+      m = top;
+      uint64_t sum = f2(0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        float f[N];
+        widen<E>(x[u], f);
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+          float x0, x1;
+          f2_split(f2_mul(f2_add(f2(f[j], f[j + 1]), f2(at, at)), f2(c, c)), x0, x1);
+          sum = f2_add(sum, f2(ex2(x0), ex2(x1)));
+        }
+      }
+      float s0, s1;
+      f2_split(sum, s0, s1);
+      s += s0 + s1;
+    };
+    const uint32_t low = E::kBytes == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
+    const uint4 nothing = make_uint4(low, low, low, low);
+    if (kResident) {
+#pragma unroll 1
+      for (int k = 0; k < kChunks; ++k) {
+        if (!mbar_wait_bounded(smem_u32(&h.bar[k]), 0, nullptr)) {
+          late = true;  // give the copy one more chance to land before the block goes on
+          mbar_wait_bounded(smem_u32(&h.bar[k]), 0, nullptr);
+        }
+        const int b0 = k * chunk, b1 = b0 + chunk < v1 - v0 ? b0 + chunk : v1 - v0;
+        for (int v = b0 + tid; v < b1; v += kAhead * kData) {
+          uint4 x[kAhead];
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) x[u] = v + u * kData < b1 ? row_s[v + u * kData] : nothing;
+          add(x);
+        }
+      }
+    } else {
+      for (int v = v0 + tid; v < v1; v += kAhead * kData) {
         uint4 x[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) x[u] = v + u * kThreads < b1 ? row_s[v + u * kThreads] : nothing;
+        for (int u = 0; u < kAhead; ++u) {
+          const int vu = v + u * kData;
+          x[u] = vu >= v1 ? nothing : vu >= in0 && vu < in1 ? zv[vu] : edge(vu);
+        }
         add(x);
       }
     }
-  } else {
-    for (int v = v0 + tid; v < v1; v += kAhead * kThreads) {
-      uint4 x[kAhead];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int vu = v + u * kThreads;
-        x[u] = vu >= v1 ? nothing : vu >= in0 && vu < in1 ? zv[vu] : edge(vu);
-      }
-      add(x);
+    for (int o = 16; o > 0; o >>= 1) {
+      // both lanes of a pair join in the same order, so that they agree
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+      const bool first = (tid & o) == 0;
+      float ma = first ? m : m2, sa = first ? s : s2;
+      join(ma, sa, first ? m2 : m, first ? s2 : s, c);
+      m = ma;
+      s = sa;
     }
+    if (lane == 0) h.warp[warp] = make_float2(m, s);
   }
   if (late && a.status != nullptr) atomicOr(a.status, ENGRAM_ST_TIMEOUT);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    // both lanes of a pair join in the same order, so that they agree
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    const bool low = (tid & o) == 0;
-    float ma = low ? m : m2, sa = low ? s : s2;
-    join(ma, sa, low ? m2 : m, low ? s2 : s, c);
-    m = ma;
-    s = sa;
-  }
   __syncthreads();
-  if ((tid & 31) == 0) {
-    h.red[tid >> 5] = m;
-    h.red[kWarps + (tid >> 5)] = s;
-  }
-  __syncthreads();
-  m = h.red[0];
-  s = h.red[kWarps];
+  float m = h.warp[0].x, s = h.warp[0].y;
 #pragma unroll
-  for (int k = 1; k < kWarps; ++k) join(m, s, h.red[k], h.red[kWarps + k], c);
+  for (int k = 1; k < kWarps; ++k) join(m, s, h.warp[k].x, h.warp[k].y, c);
   if (a.cluster > 1) {
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every block of the cluster runs
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every block's barriers are set up
     if (tid < a.cluster) {
-      uint32_t to;
+      uint32_t to, bar;
       asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(&h.part[rank])), "r"(tid));
-      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(m), "f"(s) : "memory");
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&h.met)), "r"(tid));
+      asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to), "f"(m),
+                   "f"(s), "r"(bar)
+                   : "memory");
     }
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // (bounded; the pairs are read by this block alone once all are here, so
+    // that no block needs another one after this)
+    if (!mbar_wait_bounded(smem_u32(&h.met), 0, nullptr) && tid == 0 && a.status != nullptr)
+      atomicOr(a.status, ENGRAM_ST_TIMEOUT);
     m = h.part[0].x;
     s = h.part[0].y;
     for (int k = 1; k < a.cluster; ++k) join(m, s, h.part[k].x, h.part[k].y, c);
   }
 
+  const float mass = h.mass;
   const bool none = mass == 0.f;
-  if (rank == 0) {
-    const float log_sum = logf(s);
+  if (rank == 0 && warp == kWarps) {
+    const float norm = h.norm, log_sum = logf(s);
     float loss = 0.f;
-    for (int k = tid; k < a.top; k += kThreads) {
+    for (int k = lane; k < a.top; k += 32) {
       const float pk = expf(p[k] - norm);
       if (pk > 0.f || pk != pk) loss += pk * ((p[k] - norm) - ((zk[k] - m) * inv_tau - log_sum));
     }
-    loss = block_reduce<false>(loss, h.red);
-    if (tid == 0) a.loss[row] = none ? 0.f : w * a.tau * a.tau * loss;
+    loss = warp_reduce<false>(loss);
+    if (lane == 0) a.loss[row] = none ? 0.f : w * a.tau * a.tau * loss;
   }
   if (dz == nullptr) return;
   if (none) {
@@ -368,20 +374,22 @@ __global__ void __launch_bounds__(kThreads, kResident ? 3 : 4) distill_kernel(co
       if (e >= 0 && e < V) E::store(dr + e, f[j]);
     }
   };
-  if (off == doff) {
+  if (warp == kWarps) {
+    // (the row is the other warps')
+  } else if (off == doff) {
     const uint4* src = kResident ? row_s - v0 : zv;
     uint4* dv = reinterpret_cast<uint4*>(dr - off);
     const int end = v1 < in1 ? v1 : in1;
     int v = (v0 > in0 ? v0 : in0) + tid;
-    for (; v + (kAhead - 1) * kThreads < end; v += kAhead * kThreads) {
+    for (; v + (kAhead - 1) * kData < end; v += kAhead * kData) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         float f[N];
-        grad(src[v + u * kThreads], f);
-        __stcs(dv + v + u * kThreads, narrow<E>(f));
+        grad(src[v + u * kData], f);
+        __stcs(dv + v + u * kData, narrow<E>(f));
       }
     }
-    for (; v < end; v += kThreads) {
+    for (; v < end; v += kData) {
       float f[N];
       grad(src[v], f);
       __stcs(dv + v, narrow<E>(f));
@@ -391,16 +399,19 @@ __global__ void __launch_bounds__(kThreads, kResident ? 3 : 4) distill_kernel(co
   } else {  // the gradient's rows lie differently: value by value
     const int e0 = v0 * N - off > 0 ? v0 * N - off : 0, e1 = v1 * N - off < V ? v1 * N - off : V;
     const typename E::T* part = kResident ? reinterpret_cast<const typename E::T*>(row_s) + off - v0 * N : zr;
-    for (int e = e0 + tid; e < e1; e += kThreads) E::store(dr + e, ex2((E::load(part + e) - m) * c) * coef);
+    for (int e = e0 + tid; e < e1; e += kData) E::store(dr + e, ex2((E::load(part + e) - m) * c) * coef);
   }
   // the entries' own gradients, over what was just written
   __syncthreads();
+  const float norm = h.norm;
   for (int k = tid; k < a.top; k += kThreads) {
-    const int v = id[k] < 0 ? -1 : (id[k] + off) / N;
+    const int mine = id[k], v = mine < 0 ? -1 : (mine + off) / N;
     if (v < v0 || v >= v1) continue;
     float pk = 0.f;
-    for (int i = 0; i < a.top; ++i) pk += id[i] == id[k] ? expf(p[i] - norm) : 0.f;  // an id given twice adds up
-    E::store(dr + id[k], ex2((zk[k] - m) * c) * coef - scale * pk);
+#pragma unroll 4
+    for (int i = 0; i < a.top; ++i)
+      if (id[i] == mine) pk += expf(p[i] - norm);  // an id given twice adds up
+    E::store(dr + mine, ex2((zk[k] - m) * c) * coef - scale * pk);
   }
 }
 
