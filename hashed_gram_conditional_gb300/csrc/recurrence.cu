@@ -642,9 +642,10 @@ constexpr int kFwdSmem = 2 * kFwdTile * kRowBytes + 2 * kFwdWarps * kGroup<E> * 
 // before its positions come from the state saved in front of the tile.
 //
 // A position's gradients need its state, known in ascending order, and l,
-// known in descending order: the ascending walk leaves w = f u (s_{t-1} - x)
-// in registers and the gates in the place of x and g in shared memory, the
-// smaller of f and u standing for both (u, or -f).
+// known in descending order: the ascending walk leaves s_{t-1} - x in registers.
+// The gates are computed in each of the three walks: their smaller one would
+// have to stand for both where one is kept, and telling them apart costs more
+// instructions than the two exponentials and the reciprocal of a pair.
 constexpr int kBwdWarps = 8;
 
 template <class E, bool kVec>
@@ -775,19 +776,14 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) backward_kernel(Args<E> a) 
       fma_v<V>(f, s, q, s);
     }
   }
-  float w[kSteps][V];
+  float gap[kSteps][V];
   auto ascend = [&](int k) {
-    float xv[V], f[V], u[V], before[V], code[V];
+    float xv[V], f[V], u[V], before[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) before[j] = s[j];
     advance(k, xv, f, u);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      w[k][j] = f[j] * u[j] * (before[j] - xv[j]);
-      code[j] = f[j] <= u[j] ? -f[j] : u[j];
-    }
-    *reinterpret_cast<float2*>(gw + k * kRowBytes + lane * 8) = make_float2(code[0], code[1]);
-    if constexpr (V == 4) *reinterpret_cast<float2*>(xw + k * kRowBytes + lane * 8) = make_float2(code[2], code[3]);
+    for (int j = 0; j < V; ++j) gap[k][j] = before[j] - xv[j];
   };
   if (straight) {
 #pragma unroll
@@ -806,25 +802,16 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) backward_kernel(Args<E> a) 
   typename E::T* dx = a.dx + tw * a.dx_stride;
   typename E::T* dg = a.dg + tw * a.dg_stride;
   auto descend = [&](int k) {
-    float dv[V], code[V], ox[V], og[V];
+    float gv[V], dv[V], f[V], u[V], ox[V], og[V];
     lane_row<E>(dw + k * kRowBytes, lane, dv);
-    const float2 lo = *reinterpret_cast<const float2*>(gw + k * kRowBytes + lane * 8);
-    code[0] = lo.x;
-    code[1] = lo.y;
-    if constexpr (V == 4) {
-      const float2 hi = *reinterpret_cast<const float2*>(xw + k * kRowBytes + lane * 8);
-      code[2] = hi.x;
-      code[3] = hi.y;
-    }
-    const bool live = mk.live >> k & 1u;
+    gate_row<E>(gw + k * kRowBytes, lane, gv);
+    gates<E>(gv, f, u);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float l = dv[j] + m[j], small = fabsf(code[j]), big = 1.f - small;
-      const bool neg = signbit(code[j]);
-      ox[j] = live ? l * (neg ? big : small) : 0.f;
-      og[j] = live ? l * w[k][j] : 0.f;
-      m[j] = l * (neg ? small : big);
-    }
+    for (int j = 0; j < V; ++j) dv[j] += m[j];
+    mul_v<V>(dv, f, m);
+    mul_v<V>(dv, u, ox);
+    mul_v<V>(m, u, og);
+    mul_v<V>(og, gap[k], og);
     store_row<E, kVec>(dx + k * a.dx_stride, c, a.dim, ox);
     store_row<E, kVec>(dg + k * a.dg_stride, c, a.dim, og);
   };
@@ -853,6 +840,14 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) backward_kernel(Args<E> a) 
         for (int j = 0; j < V; ++j) m[j] = 0.f;
       }
     }
+  }
+  // positions that do not count, over what was just written
+  const float zeros[V] = {};
+  for (uint32_t dead = ~mk.live & ((1u << kSteps) - 1u); dead != 0; dead &= dead - 1u) {
+    const int64_t t = tw + __ffs(dead) - 1;
+    if (t >= a.n_tokens) break;
+    store_row<E, kVec>(a.dx + t * a.dx_stride, c, a.dim, zeros);
+    store_row<E, kVec>(a.dg + t * a.dg_stride, c, a.dim, zeros);
   }
 }
 
