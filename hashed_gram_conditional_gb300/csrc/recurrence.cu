@@ -364,11 +364,14 @@ __device__ __forceinline__ float join_factor(float p, float A) { return signbit(
 //
 // Tiles take their numbers from a counter in walking order, so every tile that
 // is waited for is already running.  (A, B) is the tile's own map; a warp's
-// lanes are neighbouring channels.
+// lanes are neighbouring channels.  `meanwhile` runs between the publishing of
+// the map and the first look at the others.  A look costs about 1000 cycles
+// whatever it finds, so the maps of the tile's own run and what is usually
+// there of the two runs before it are read together.
 constexpr int kRun = 8;
 
-template <class E>
-__device__ __forceinline__ float come_in(const Args<E>& a, int group, int pos, int ch, float A, float B) {
+template <class E, class F>
+__device__ __forceinline__ float come_in(const Args<E>& a, int group, int pos, int ch, float A, float B, F meanwhile) {
   constexpr int G = kGroup<E>;
   const int lane = threadIdx.x & 31;
   const long long begun = clock64();
@@ -386,7 +389,16 @@ __device__ __forceinline__ float come_in(const Args<E>& a, int group, int pos, i
   const float2* maps = a.map + (base + pos) * G + ch;
   const bool last_of_all = pos + 1 == a.n_tiles;
   if (!last_of_all) store_pair(a.map + (base + pos) * G + ch, A, B);
+  meanwhile();
 
+  const int64_t rbase = static_cast<int64_t>(group) * a.n_runs;
+  uint32_t near = 0u, far = 0u;  // the values behind the last run and the one before it
+  uint2 step = make_uint2(0u, 0u);  // the last run's map
+  if (run > 0) near = load_word(a.run_value + (rbase + run - 1) * G + ch);
+  if (run > 1) {
+    far = load_word(a.run_value + (rbase + run - 2) * G + ch);
+    step = load_pair(a.run_map + (rbase + run - 1) * G + ch);
+  }
   uint2 m[kRun - 1];  // m[i]: the map of the tile i + 1 places before
 #pragma unroll
   for (int i = 0; i < kRun - 1; ++i) m[i] = i < behind ? load_pair(maps - (i + 1) * G) : make_uint2(0u, 0u);
@@ -401,7 +413,6 @@ __device__ __forceinline__ float come_in(const Args<E>& a, int group, int pos, i
       if (m[i].x == kNotYet || m[i].y == kNotYet) m[i] = load_pair(maps - (i + 1) * G);
   }
 
-  const int64_t rbase = static_cast<int64_t>(group) * a.n_runs;
   float RA = A, RB = B;  // the run's map, where this tile ends it
   const bool ends_run = behind == kRun - 1 && !last_of_all;
   if (ends_run) {
@@ -420,7 +431,13 @@ __device__ __forceinline__ float come_in(const Args<E>& a, int group, int pos, i
 
   // the value in front of the run
   float v = 0.f;
-  if (run > 0) {
+  if (run == 0) {
+    // nothing is in front of it
+  } else if (__all_sync(kFull, near != kNotYet)) {
+    v = __uint_as_float(near);
+  } else if (run > 1 && __all_sync(kFull, far != kNotYet && step.x != kNotYet && step.y != kNotYet)) {
+    v = apply_map(step, __uint_as_float(far));
+  } else {
     int depth = 0;  // run maps to apply
     const int ch0 = ch - lane;
     while (true) {
@@ -474,9 +491,12 @@ __device__ __forceinline__ float come_in(const Args<E>& a, int group, int pos, i
   return v;
 }
 
-// The block's number in walking order.
-__device__ __forceinline__ int take_ticket(int32_t* ticket, int32_t* shared) {
-  if (threadIdx.x == 0) *shared = atomicAdd(ticket, 1);
+// The block's number in walking order; also clears the tile's mask.
+__device__ __forceinline__ int take_ticket(int32_t* ticket, int32_t* shared, uint32_t* cuts) {
+  if (threadIdx.x == 0) {
+    *shared = atomicAdd(ticket, 1);
+    *cuts = 0u;
+  }
   __syncthreads();
   return *shared;
 }
@@ -505,11 +525,11 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 3) forward_kernel(Args<E> a) {
   unsigned char* gs = xs + kTile * kRowBytes;
   float(*mapA)[G] = reinterpret_cast<float(*)[G]>(gs + kTile * kRowBytes);
   float(*mapB)[G] = mapA + kWarps;
-  __shared__ bool cuts[kWarps];
+  __shared__ uint32_t cuts;  // a bit per warp in which a sequence begins
   __shared__ int32_t number;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_prior_grids();
-  const int n = take_ticket(a.ticket, &number);
+  const int n = take_ticket(a.ticket, &number, &cuts);
   const int tile = n / a.n_groups, group = n - tile * a.n_groups;
   const int c0 = group * G, c = c0 + lane * V;
   const int t0 = tile * kTile, tw = t0 + warp * kSteps;
@@ -572,26 +592,27 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 3) forward_kernel(Args<E> a) {
   }
   if (mk.first == 0) put_lane<E>(mapA[warp], lane, A);
   put_lane<E>(mapB[warp], lane, s);
-  if (lane == 0) cuts[warp] = mk.first != 0;
+  if (lane == 0 && mk.first != 0) atomicOr(&cuts, 1u << warp);
   __syncthreads();
 
   if (warp * 32 < G) {  // a lane per channel: the tile's map, and what comes into it and into every warp
     const int ch = warp * 32 + lane;
+    const uint32_t cut = cuts;
     float TA = 1.f, TB = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float p = cuts[w] ? kCut : mapA[w][ch];
+      const float p = cut >> w & 1u ? kCut : mapA[w][ch];
       TB = apply_map(p, mapB[w][ch], TB);
       TA = join_factor(p, TA);
     }
-    float v = come_in<E>(a, group, tile, ch, TA, TB);
+    float v = come_in<E>(a, group, tile, ch, TA, TB, [] {});
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w * kSteps % kBwdTile == 0 && a.carry != nullptr && c0 + ch < a.dim && t0 + w * kSteps < a.n_tokens)
         a.carry[static_cast<int64_t>((t0 + w * kSteps) / kBwdTile) * a.dim + c0 + ch] = v;
       const float q = mapB[w][ch];
       mapB[w][ch] = v;
-      v = apply_map(cuts[w] ? kCut : mapA[w][ch], q, v);
+      v = apply_map(cut >> w & 1u ? kCut : mapA[w][ch], q, v);
     }
   }
   __syncthreads();
@@ -662,11 +683,11 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) backward_kernel(Args<E> a) 
   // the gradient of the last state of the sequence that ends here and began
   // before this warp, whose first state's gradient may be written in its place
   float(*held)[G] = mapC + kWarps;
-  __shared__ bool cuts[kWarps];
+  __shared__ uint32_t cuts;  // a bit per warp in which a sequence begins
   __shared__ int32_t number;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_prior_grids();
-  const int n = take_ticket(a.ticket, &number);
+  const int n = take_ticket(a.ticket, &number, &cuts);
   const int back = n / a.n_groups, group = n - back * a.n_groups;
   const int tile = a.n_tiles - 1 - back;
   const int c0 = group * G, c = c0 + lane * V;
@@ -742,58 +763,64 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) backward_kernel(Args<E> a) 
   put_lane<E>(mapA[warp], lane, A);
   put_lane<E>(mapB[warp], lane, s);
   put_lane<E>(mapC[warp], lane, C);
-  if (lane == 0) cuts[warp] = mk.first != 0;
+  if (lane == 0 && mk.first != 0) atomicOr(&cuts, 1u << warp);
   __syncthreads();
 
+  // the walk in ascending order, from the state in front of the tile
+  float gap[kSteps][V];
+  auto ascend = [&]() {
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[j] = carry[j];
+    const uint32_t cut = cuts;
+    for (int p = 0; p < warp; ++p) {
+      float f[V], q[V];
+      get_lane<E>(mapA[p], lane, f);
+      get_lane<E>(mapB[p], lane, q);
+      if (cut >> p & 1u) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] = q[j];
+      } else {
+        fma_v<V>(f, s, q, s);
+      }
+    }
+    auto walk = [&](int k) {
+      float xv[V], f[V], u[V], before[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) before[j] = s[j];
+      advance(k, xv, f, u);
+#pragma unroll
+      for (int j = 0; j < V; ++j) gap[k][j] = before[j] - xv[j];
+    };
+    if (straight) {
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) walk(k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        if (mk.first >> k & 1u) begin(k);
+        walk(k);
+      }
+    }
+  };
   if (warp * 32 < G) {  // a lane per channel, from behind: the tile's map, and what comes into it and into every warp
     const int ch = warp * 32 + lane;
+    const uint32_t cut = cuts;
     float TA = 1.f, TC = 0.f;
 #pragma unroll
     for (int w = kWarps - 1; w >= 0; --w) {
-      const float p = cuts[w] ? kCut : mapA[w][ch];
+      const float p = cut >> w & 1u ? kCut : mapA[w][ch];
       TC = apply_map(p, mapC[w][ch], TC);
       TA = join_factor(p, TA);
     }
-    float v = come_in<E>(a, group, back, ch, TA, TC);
+    float v = come_in<E>(a, group, back, ch, TA, TC, ascend);
 #pragma unroll
     for (int w = kWarps - 1; w >= 0; --w) {
       const float q = mapC[w][ch];
       mapC[w][ch] = v;
-      v = apply_map(cuts[w] ? kCut : mapA[w][ch], q, v);
+      v = apply_map(cut >> w & 1u ? kCut : mapA[w][ch], q, v);
     }
-  }
-  // meanwhile the other warps walk their positions in ascending order
-#pragma unroll
-  for (int j = 0; j < V; ++j) s[j] = carry[j];
-  for (int p = 0; p < warp; ++p) {
-    float f[V], q[V];
-    get_lane<E>(mapA[p], lane, f);
-    get_lane<E>(mapB[p], lane, q);
-    if (cuts[p]) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) s[j] = q[j];
-    } else {
-      fma_v<V>(f, s, q, s);
-    }
-  }
-  float gap[kSteps][V];
-  auto ascend = [&](int k) {
-    float xv[V], f[V], u[V], before[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) before[j] = s[j];
-    advance(k, xv, f, u);
-#pragma unroll
-    for (int j = 0; j < V; ++j) gap[k][j] = before[j] - xv[j];
-  };
-  if (straight) {
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) ascend(k);
   } else {
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      if (mk.first >> k & 1u) begin(k);
-      ascend(k);
-    }
+    ascend();
   }
   __syncthreads();
 
