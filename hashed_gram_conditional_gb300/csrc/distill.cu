@@ -7,16 +7,18 @@
 //   dz_v = w tau (P q_v - p_v)
 //
 // A position's gradient needs its whole row's maximum and sum, so a row is
-// read once and kept: a cluster of 1 to 8 blocks holds it in shared memory
-// (bulk copies), exchanges its blocks' (maximum, sum) pairs through
-// distributed shared memory, and writes the gradient from the copy.  Memory
-// traffic is then the logits once and the gradient once.  Rows are split so
-// that a block's part is at most 72 KB where that is possible: three blocks
-// share an SM, so that one loads while another exchanges or writes.
+// read once and kept: the blocks of a cluster hold its parts in shared memory,
+// exchange their (maximum, sum) pairs through distributed shared memory, and
+// write the gradient from there.  Memory traffic is then the logits once and
+// the gradient once.  The blocks stay and go from row to row, with the copies
+// of the next rows under way (rows_kernel); rows too long for a cluster's
+// shared memory are read twice (long_rows_kernel).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
+#include <mutex>
 
 #include "engram_internal.h"
 #include "train_device.cuh"
@@ -24,33 +26,21 @@
 namespace engram {
 namespace {
 
-constexpr int kWarps = 8;               // that go over the row
-constexpr int kData = kWarps * 32;
-constexpr int kThreads = kData + 32;    // and one that prepares the teacher's probabilities meanwhile
 constexpr int kMaxTop = ENGRAM_DISTILL_MAX_TOP;
 constexpr int kMaxCluster = 8;
-constexpr int kChunks = 4;                 // pieces of a part that are awaited one by one
-constexpr int kPartBytes = 72 * 1024;      // a part's size where the cluster can be made large enough
-constexpr int kPartLimit = 200 * 1024;     // beyond this in a cluster of 8 the row is read twice instead
 
 struct Args {
   int64_t vocab, z_stride, dz_stride;
+  int32_t rows;
   const int32_t* ids;
   const float* t;
-  int32_t top, cluster;
+  int32_t top, cluster, depth, slot_bytes;
+  bool aligned;  // the rows' strides are multiples of 16 bytes
   float tau;
   const float* lse;
   const float* weight;
   float* loss;
   int32_t* status;
-};
-
-struct Head {  // in front of the dynamic shared memory
-  uint64_t bar[kChunks];
-  uint64_t met;              // completes when every block's pair is here
-  float2 part[kMaxCluster];  // the blocks' (maximum, sum of exponentials relative to it)
-  float2 warp[kWarps];
-  float norm, mass;          // of the teacher's entries
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -125,311 +115,625 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
-// One cluster of a.cluster blocks per position.  The row is handled in 16-byte
-// vectors counted from the aligned address at or before its first element
-// (`off` elements before it); vectors that reach over the row's ends are
-// filled up with -inf, which adds nothing to the sums.
-template <class E, bool kResident>
-__global__ void __launch_bounds__(kThreads, 3) distill_kernel(const typename E::T* z,
-                                                                              typename E::T* dz, Args a) {
-  constexpr int N = kVec<E>;
-  extern __shared__ __align__(128) unsigned char smem[];
-  Head& h = *reinterpret_cast<Head*>(smem);
-  float* p = reinterpret_cast<float*>(smem + sizeof(Head));
-  int32_t* id = reinterpret_cast<int32_t*>(p + a.top);
-  float* zk = reinterpret_cast<float*>(id + a.top);
-  uint4* row_s = reinterpret_cast<uint4*>(smem + ((sizeof(Head) + 12 * static_cast<size_t>(a.top) + 127) & ~size_t(127)));
+// A row in 16-byte vectors counted from the aligned address at or before its
+// first element (`off` elements before it).  Vectors that reach over the row's
+// ends are filled up with -inf, which adds nothing to the sums.
+template <class E>
+struct Row {
+  static constexpr int N = kVec<E>;
+  const typename E::T* z;
+  typename E::T* dz;
+  int V, off, doff;  // doff: the same of the gradient's row
+  int in0, in1;      // vectors wholly inside the row
+  int v0, v1;        // this block's part
+  bool head, tail;   // it has the vector over the row's beginning, over its end
 
-  const int tid = threadIdx.x;
-  const uint32_t rank = a.cluster > 1 ? cluster_rank() : 0u;
-  const int64_t row = blockIdx.x / a.cluster;
-  const typename E::T* zr = z + row * a.z_stride;
-  typename E::T* dr = dz + row * a.dz_stride;
-  const int V = static_cast<int>(a.vocab);
-  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(zr) & 15) / E::kBytes);
-  const int doff = static_cast<int>((reinterpret_cast<uintptr_t>(dr) & 15) / E::kBytes);
-  const int vecs = (V + off + N - 1) / N, per = (vecs + a.cluster - 1) / a.cluster;
-  const int v0 = static_cast<int>(rank) * per < vecs ? static_cast<int>(rank) * per : vecs;
-  const int v1 = v0 + per < vecs ? v0 + per : vecs;
-  const uint4* zv = reinterpret_cast<const uint4*>(zr - off);
-  // vectors wholly inside the row
-  const int in0 = off > 0 ? 1 : 0, in1 = (V + off) / N;
-  // the vector that reaches over the row's end is in this block's part
-  const bool tail = in1 < vecs && v0 <= in1 && in1 < v1 && !(in1 == 0 && in0 > 0);
-
-  const float w = a.weight != nullptr ? a.weight[row] : 1.f;
-  auto zeros = [&]() {  // this block's part of a gradient of zeros
-    if (dz == nullptr) return;
-    const int e0 = v0 * N - off > 0 ? v0 * N - off : 0, e1 = v1 * N - off < V ? v1 * N - off : V;
-    if (off == doff) {
-      for (int v = (v0 > in0 ? v0 : in0) + tid; v < v1 && v < in1; v += kThreads)
-        reinterpret_cast<uint4*>(dr - off)[v] = make_uint4(0u, 0u, 0u, 0u);
-      if (in0 > 0 && v0 == 0 && tid < N - off && tid < V) E::store(dr + tid, 0.f);
-      if (tail && in1 * N - off + tid < V) E::store(dr + in1 * N - off + tid, 0.f);
-    } else {
-      for (int e = e0 + tid; e < e1; e += kThreads) E::store(dr + e, 0.f);
-    }
-  };
-  if (w == 0.f) {  // nothing to learn here
-    if (rank == 0 && tid == 0) a.loss[row] = 0.f;
-    zeros();
-    return;
+  // The row's place; its geometry is the same for every row if their strides
+  // are multiples of 16 bytes (`aligned`), and is then worked out once.
+  __device__ __forceinline__ void at(const typename E::T* z_all, typename E::T* dz_all, const Args& a, int64_t row, int rank,
+                                     bool again) {
+    z = z_all + row * a.z_stride;
+    dz = dz_all + row * a.dz_stride;
+    if (again && a.aligned) return;
+    V = static_cast<int>(a.vocab);
+    off = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / E::kBytes);
+    doff = static_cast<int>((reinterpret_cast<uintptr_t>(dz) & 15) / E::kBytes);
+    const int vecs = (V + off + N - 1) / N, per = (vecs + a.cluster - 1) / a.cluster;
+    v0 = rank * per < vecs ? rank * per : vecs;
+    v1 = v0 + per < vecs ? v0 + per : vecs;
+    in0 = off > 0 ? 1 : 0;
+    in1 = (V + off) / N;
+    head = in0 > 0 && v0 == 0 && v1 > 0;
+    tail = in1 < vecs && v0 <= in1 && in1 < v1 && !(in1 == 0 && in0 > 0);
   }
-
-  // the row's values of a vector, -inf outside
-  auto edge = [&](int v) {
+  __device__ __forceinline__ const uint4* vectors() const { return reinterpret_cast<const uint4*>(z - off); }
+  __device__ __forceinline__ int first() const { return v0 > in0 ? v0 : in0; }  // of the part's whole vectors
+  __device__ __forceinline__ int end() const { return v1 < in1 ? v1 : in1; }
+  __device__ __forceinline__ uint4 edge(int v) const {
     float f[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int e = v * N + j - off;
-      f[j] = e >= 0 && e < V ? E::load(zr + e) : -INFINITY;
+      f[j] = e >= 0 && e < V ? E::load(z + e) : -INFINITY;
     }
     return narrow<E>(f);
-  };
-  // whole rounds of the threads
-  const int chunk = ((v1 - v0 + kChunks - 1) / kChunks + kData - 1) / kData * kData;
-  if (tid == 0) {
+  }
+  __device__ __forceinline__ void store_edge(int v, const float (&f)[N]) const {
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k) mbar_init(smem_u32(&h.bar[k]), 1);
-    mbar_init(smem_u32(&h.met), 1);
-    fence_mbar_init();
-    if (a.cluster > 1) mbar_arrive_expect_tx(smem_u32(&h.met), static_cast<uint32_t>(a.cluster) * sizeof(float2));
-    if (kResident) {
-#pragma unroll
-      for (int k = 0; k < kChunks; ++k) {
-        int b0 = v0 + k * chunk, b1 = b0 + chunk < v1 ? b0 + chunk : v1;
-        b0 = b0 > in0 ? b0 : in0;
-        b1 = b1 < in1 ? b1 : in1;
-        const uint32_t bytes = b1 > b0 ? static_cast<uint32_t>(b1 - b0) * 16u : 0u;
-        mbar_arrive_expect_tx(smem_u32(&h.bar[k]), bytes);
-        if (bytes > 0) bulk_g2s(smem_u32(row_s + (b0 - v0)), zv + b0, bytes, smem_u32(&h.bar[k]));
-      }
+    for (int j = 0; j < N; ++j) {
+      const int e = v * N + j - off;
+      if (e >= 0 && e < V) E::store(dz + e, f[j]);
     }
   }
-  if (kResident) {
-    if (tid == 32 && in0 > 0 && v0 == 0 && v1 > 0) row_s[0] = edge(0);
-    if (tid == 64 && tail) row_s[in1 - v0] = edge(in1);
-  }
-  __syncthreads();
-  if (a.cluster > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-
-  constexpr int kAhead = 4;
-  const float inv_tau = 1.f / a.tau, c = 1.4426950408889634f * inv_tau;
-  const int lane = tid & 31, warp = tid >> 5;
-  bool late = false;
-  if (warp == kWarps) {
-    // the teacher's entries: id, logit / tau and the student's logit
-    float top = -INFINITY;
-    for (int k = lane; k < a.top; k += 32) {
-      int32_t v = a.ids[row * a.top + k];
-      if (v >= a.vocab) {
-        if (a.status != nullptr) atomicOr(a.status, ENGRAM_ST_BAD_TOKEN);
-        v = -1;
-      }
-      id[k] = v < 0 ? -1 : v;
-      p[k] = v >= 0 ? a.t[row * a.top + k] * inv_tau : -INFINITY;
-      zk[k] = v >= 0 ? E::load(zr + v) : 0.f;
-      top = fmaxf(top, p[k]);
-    }
-    top = warp_reduce<true>(top);
-    float norm = 0.f;
-    if (a.lse != nullptr) {
-      norm = a.lse[row];
-    } else if (top != -INFINITY) {
-      float sum = 0.f;
-      for (int k = lane; k < a.top; k += 32) sum += expf(p[k] - top);
-      norm = top + logf(warp_reduce<false>(sum));
-    }
-    float mass = 0.f;
-    for (int k = lane; k < a.top; k += 32) mass += expf(p[k] - norm);
-    mass = warp_reduce<false>(mass);
-    if (lane == 0) {
-      h.norm = norm;
-      h.mass = mass;
-    }
-  } else {
-    // the maximum and the sum of this block's part, kAhead vectors a step: their
-    // maximum first, so that the exponentials do not wait for one another
-    float m = -INFINITY, s = 0.f;
-    auto add = [&](const uint4 (&x)[kAhead]) {
-      const float big = fmaxf(fmaxf(largest<E>(x[0]), largest<E>(x[1])), fmaxf(largest<E>(x[2]), largest<E>(x[3])));
-      const float top = fmaxf(m, big), at = top == -INFINITY ? 0.f : -top;
-      s *= ex2((m + at) * c);
-      m = top;
-      uint64_t sum = f2(0.f, 0.f);
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        float f[N];
-        widen<E>(x[u], f);
-#pragma unroll
-        for (int j = 0; j < N; j += 2) {
-          float x0, x1;
-          f2_split(f2_mul(f2_add(f2(f[j], f[j + 1]), f2(at, at)), f2(c, c)), x0, x1);
-          sum = f2_add(sum, f2(ex2(x0), ex2(x1)));
-        }
-      }
-      float s0, s1;
-      f2_split(sum, s0, s1);
-      s += s0 + s1;
-    };
-    const uint32_t low = E::kBytes == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
-    const uint4 nothing = make_uint4(low, low, low, low);
-    if (kResident) {
-#pragma unroll 1
-      for (int k = 0; k < kChunks; ++k) {
-        if (!mbar_wait_bounded(smem_u32(&h.bar[k]), 0, nullptr)) {
-          late = true;  // give the copy one more chance to land before the block goes on
-          mbar_wait_bounded(smem_u32(&h.bar[k]), 0, nullptr);
-        }
-        const int b0 = k * chunk, b1 = b0 + chunk < v1 - v0 ? b0 + chunk : v1 - v0;
-        for (int v = b0 + tid; v < b1; v += kAhead * kData) {
-          uint4 x[kAhead];
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u) x[u] = v + u * kData < b1 ? row_s[v + u * kData] : nothing;
-          add(x);
-        }
-      }
+  // this block's part of a gradient of zeros, by `threads` threads
+  __device__ __forceinline__ void zeros(int tid, int threads) const {
+    if (off == doff) {
+      for (int v = first() + tid; v < end(); v += threads)
+        reinterpret_cast<uint4*>(dz - off)[v] = make_uint4(0u, 0u, 0u, 0u);
+      const float none[N] = {};
+      if (head && tid == 0) store_edge(0, none);
+      if (tail && tid == 0) store_edge(in1, none);
     } else {
-      for (int v = v0 + tid; v < v1; v += kAhead * kData) {
-        uint4 x[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const int vu = v + u * kData;
-          x[u] = vu >= v1 ? nothing : vu >= in0 && vu < in1 ? zv[vu] : edge(vu);
-        }
-        add(x);
-      }
+      const int e1 = v1 * N - off < V ? v1 * N - off : V;
+      for (int e = (v0 * N - off > 0 ? v0 * N - off : 0) + tid; e < e1; e += threads) E::store(dz + e, 0.f);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      // both lanes of a pair join in the same order, so that they agree
-      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-      const bool first = (tid & o) == 0;
-      float ma = first ? m : m2, sa = first ? s : s2;
-      join(ma, sa, first ? m2 : m, first ? s2 : s, c);
-      m = ma;
-      s = sa;
-    }
-    if (lane == 0) h.warp[warp] = make_float2(m, s);
   }
-  if (late && a.status != nullptr) atomicOr(a.status, ENGRAM_ST_TIMEOUT);
-  __syncthreads();
-  float m = h.warp[0].x, s = h.warp[0].y;
-#pragma unroll
-  for (int k = 1; k < kWarps; ++k) join(m, s, h.warp[k].x, h.warp[k].y, c);
-  if (a.cluster > 1) {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every block's barriers are set up
-    if (tid < a.cluster) {
-      uint32_t to, bar;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(&h.part[rank])), "r"(tid));
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&h.met)), "r"(tid));
-      asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to), "f"(m),
-                   "f"(s), "r"(bar)
-                   : "memory");
-    }
-    __syncwarp();
-    // (bounded; the pairs are read by this block alone once all are here, so
-    // that no block needs another one after this)
-    if (!mbar_wait_bounded(smem_u32(&h.met), 0, nullptr) && tid == 0 && a.status != nullptr)
-      atomicOr(a.status, ENGRAM_ST_TIMEOUT);
-    m = h.part[0].x;
-    s = h.part[0].y;
-    for (int k = 1; k < a.cluster; ++k) join(m, s, h.part[k].x, h.part[k].y, c);
-  }
+};
 
-  const float mass = h.mass;
-  const bool none = mass == 0.f;
-  if (rank == 0 && warp == kWarps) {
-    const float norm = h.norm, log_sum = logf(s);
-    float loss = 0.f;
-    for (int k = lane; k < a.top; k += 32) {
-      const float pk = expf(p[k] - norm);
-      if (pk > 0.f || pk != pk) loss += pk * ((p[k] - norm) - ((zk[k] - m) * inv_tau - log_sum));
-    }
-    loss = warp_reduce<false>(loss);
-    if (lane == 0) a.loss[row] = none ? 0.f : w * a.tau * a.tau * loss;
-  }
-  if (dz == nullptr) return;
-  if (none) {
-    zeros();
-    return;
-  }
-
-  const float scale = w * a.tau, coef = scale * mass / s;
-  auto grad = [&](const uint4& x, float (&f)[N]) {
-    widen<E>(x, f);
+// Adds kAhead vectors to (m, s): their maximum first, so that the exponentials
+// do not wait for one another.
+constexpr int kAhead = 4;
+template <class E>
+__device__ __forceinline__ void add_vectors(const uint4 (&x)[kAhead], float c, float& m, float& s) {
+  constexpr int N = kVec<E>;
+  const float big = fmaxf(fmaxf(largest<E>(x[0]), largest<E>(x[1])), fmaxf(largest<E>(x[2]), largest<E>(x[3])));
+  const float top = fmaxf(m, big), at = top == -INFINITY ? 0.f : -top;
+  s *= ex2((m + at) * c);
+  m = top;
+  uint64_t sum = f2(0.f, 0.f);
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    float f[N];
+    widen<E>(x[u], f);
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
       float x0, x1;
-      f2_split(f2_mul(f2_add(f2(f[j], f[j + 1]), f2(-m, -m)), f2(c, c)), x0, x1);
-      f2_split(f2_mul(f2(ex2(x0), ex2(x1)), f2(coef, coef)), f[j], f[j + 1]);
+      f2_split(f2_mul(f2_add(f2(f[j], f[j + 1]), f2(at, at)), f2(c, c)), x0, x1);
+      sum = f2_add(sum, f2(ex2(x0), ex2(x1)));
     }
-  };
-  auto grad_edge = [&](int v) {
-    float f[N];
-    grad(kResident ? row_s[v - v0] : edge(v), f);
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int e = v * N + j - off;
-      if (e >= 0 && e < V) E::store(dr + e, f[j]);
-    }
-  };
-  if (warp == kWarps) {
-    // (the row is the other warps')
-  } else if (off == doff) {
-    const uint4* src = kResident ? row_s - v0 : zv;
-    uint4* dv = reinterpret_cast<uint4*>(dr - off);
-    const int end = v1 < in1 ? v1 : in1;
-    int v = (v0 > in0 ? v0 : in0) + tid;
-    for (; v + (kAhead - 1) * kData < end; v += kAhead * kData) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        float f[N];
-        grad(src[v + u * kData], f);
-        __stcs(dv + v + u * kData, narrow<E>(f));
-      }
-    }
-    for (; v < end; v += kData) {
-      float f[N];
-      grad(src[v], f);
-      __stcs(dv + v, narrow<E>(f));
-    }
-    if (tid == 32 && in0 > 0 && v0 == 0 && v1 > 0) grad_edge(0);
-    if (tid == 64 && tail) grad_edge(in1);
-  } else {  // the gradient's rows lie differently: value by value
-    const int e0 = v0 * N - off > 0 ? v0 * N - off : 0, e1 = v1 * N - off < V ? v1 * N - off : V;
-    const typename E::T* part = kResident ? reinterpret_cast<const typename E::T*>(row_s) + off - v0 * N : zr;
-    for (int e = e0 + tid; e < e1; e += kData) E::store(dr + e, ex2((E::load(part + e) - m) * c) * coef);
   }
-  // the entries' own gradients, over what was just written
-  __syncthreads();
-  const float norm = h.norm;
-  for (int k = tid; k < a.top; k += kThreads) {
-    const int mine = id[k], v = mine < 0 ? -1 : (mine + off) / N;
-    if (v < v0 || v >= v1) continue;
-    float pk = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < a.top; ++i)
-      if (id[i] == mine) pk += expf(p[i] - norm);  // an id given twice adds up
-    E::store(dr + mine, ex2((zk[k] - m) * c) * coef - scale * pk);
+  float s0, s1;
+  f2_split(sum, s0, s1);
+  s += s0 + s1;
+}
+
+template <class E>
+__device__ __forceinline__ uint4 no_vector() {
+  const uint32_t low = E::kBytes == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
+  return make_uint4(low, low, low, low);
+}
+
+// The warp's pairs joined; the lanes of a pair join in the same order, so that
+// they agree.
+__device__ __forceinline__ void join_warp(float& m, float& s, float c, int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    const bool first = (lane & o) == 0;
+    float ma = first ? m : m2, sa = first ? s : s2;
+    join(ma, sa, first ? m2 : m, first ? s2 : s, c);
+    m = ma;
+    s = sa;
   }
 }
 
-template <class E, bool kResident>
-int launch(const void* z, void* dz, const Args& a, int64_t rows, size_t smem, cudaStream_t st) {
-  static std::atomic<uint64_t> attr_set{0};  // one bit per device: the shared-memory opt-in was made
+// coef 2^((z - m) c) of a vector
+template <class E>
+__device__ __forceinline__ void grad_vector(const uint4& x, float m, float c, float coef, float (&f)[kVec<E>]) {
+  widen<E>(x, f);
+#pragma unroll
+  for (int j = 0; j < kVec<E>; j += 2) {
+    float x0, x1;
+    f2_split(f2_mul(f2_add(f2(f[j], f[j + 1]), f2(-m, -m)), f2(c, c)), x0, x1);
+    f2_split(f2_mul(f2(ex2(x0), ex2(x1)), f2(coef, coef)), f[j], f[j + 1]);
+  }
+}
+
+// A position's teacher's entries in shared memory, four arrays of `top`.
+struct Entries {
+  int32_t* id;  // -1 where unused
+  float* p;     // logits / tau
+  float* zk;    // the student's logits
+  float* sum;   // probabilities, an id's entries added up
+
+  __device__ __forceinline__ Entries(void* base, int top) {
+    id = static_cast<int32_t*>(base);
+    p = reinterpret_cast<float*>(id + top);
+    zk = p + top;
+    sum = zk + top;
+  }
+};
+constexpr int kEntryBytes = 16;
+
+// Entries with the same id are told by a table of counts by id modulo its
+// size, all zero before and after: only those that share a count are compared.
+constexpr int kBuckets = 2048;  // 16-bit counts
+
+// The entries, their normaliser and their mass, by one warp.
+template <class E>
+__device__ __forceinline__ void read_teacher(const Args& a, const typename E::T* z, int64_t row, float inv_tau, int lane,
+                                             const Entries& e, uint32_t* buckets, float& norm, float& mass) {
+  float top = -INFINITY;
+  for (int k = lane; k < a.top; k += 32) {
+    int32_t v = a.ids[row * a.top + k];
+    if (v >= a.vocab) {
+      if (a.status != nullptr) atomicOr(a.status, ENGRAM_ST_BAD_TOKEN);
+      v = -1;
+    }
+    const float t = v >= 0 ? a.t[row * a.top + k] * inv_tau : -INFINITY;
+    e.id[k] = v < 0 ? -1 : v;
+    e.p[k] = t;
+    e.zk[k] = v >= 0 ? E::load(z + v) : 0.f;
+    top = fmaxf(top, t);
+    if (v >= 0) atomicAdd(&buckets[(v % kBuckets) / 2], v & 1 ? 0x10000u : 1u);
+  }
+  top = warp_reduce<true>(top);
+  norm = 0.f;
+  if (a.lse != nullptr) {
+    norm = a.lse[row];
+  } else if (top != -INFINITY) {
+    float sum = 0.f;
+    for (int k = lane; k < a.top; k += 32) sum += expf(e.p[k] - top);
+    norm = top + logf(warp_reduce<false>(sum));
+  }
+  mass = 0.f;
+  for (int k = lane; k < a.top; k += 32) {
+    const float pk = expf(e.p[k] - norm);
+    e.sum[k] = pk;
+    mass += pk;
+  }
+  mass = warp_reduce<false>(mass);
+  __syncwarp();
+  for (int k = lane; k < a.top; k += 32) {
+    const int32_t v = e.id[k];
+    if (v < 0) continue;
+    const uint32_t count = buckets[(v % kBuckets) / 2];
+    if ((v & 1 ? count >> 16 : count & 0xffffu) > 1) {
+      float pk = 0.f;
+      for (int i = 0; i < a.top; ++i)
+        if (e.id[i] == v) pk += expf(e.p[i] - norm);
+      e.sum[k] = pk;
+    }
+  }
+  __syncwarp();
+  for (int k = lane; k < a.top; k += 32)
+    if (e.id[k] >= 0) buckets[(e.id[k] % kBuckets) / 2] = 0u;
+  __syncwarp();
+}
+
+// sum_k p_k (ln p_k - ln q_k), by one warp
+__device__ __forceinline__ float sum_loss(const Args& a, const Entries& e, float norm, float m, float s, float inv_tau,
+                                          int lane) {
+  const float log_sum = logf(s);
+  float loss = 0.f;
+  for (int k = lane; k < a.top; k += 32) {
+    const float pk = expf(e.p[k] - norm);
+    if (pk > 0.f || pk != pk) loss += pk * ((e.p[k] - norm) - ((e.zk[k] - m) * inv_tau - log_sum));
+  }
+  return warp_reduce<false>(loss);
+}
+
+// The gradients of the entries in the block's part, over what the row's walk
+// wrote there, by `threads` threads.
+template <class E>
+__device__ __forceinline__ void fix_entries(const Args& a, const Row<E>& r, const Entries& e, float m, float c, float coef,
+                                            float scale, int tid, int threads) {
+  for (int k = tid; k < a.top; k += threads) {
+    const int v = e.id[k] < 0 ? -1 : (e.id[k] + r.off) / Row<E>::N;
+    if (v >= r.v0 && v < r.v1) E::store(r.dz + e.id[k], ex2((e.zk[k] - m) * c) * coef - scale * e.sum[k]);
+  }
+}
+
+// --------------------------------------------------------- rows that stay on chip
+
+// The blocks of a cluster share a row and go from row to row.  In a block
+//   - the copying warp keeps the copies of the next `depth` rows under way, and
+//     finishes a row when its walk is done: the entries' gradients, the loss;
+//   - two warps prepare the teacher's entries of the next rows, in turn;
+//   - kW warps walk the rows: of row i + 1 the maximum and the sum, which they
+//     send to every block of the cluster, then of row i, whose pairs have
+//     arrived meanwhile, the gradient.
+// Waits are for copies, for the other blocks' pairs and for the block's own
+// warps; all are bounded.
+constexpr int kPairs = 4;    // rows whose pairs may be under way: see `send`
+constexpr int kTeacher = 4;  // rows whose teacher's entries are kept
+constexpr int kMaxDepth = 3;
+
+template <int kW>
+struct Head {  // in front of the dynamic shared memory
+  uint64_t full[kMaxDepth];    // a row's copy is here
+  uint64_t walked[kMaxDepth];  // its gradient is written: kW arrivals
+  uint64_t met[kPairs];        // all pairs of a row are here
+  uint64_t known[kTeacher], used[kTeacher];  // the teacher's entries are ready / no longer needed
+  float2 pair[kPairs][kMaxCluster * kW];
+  float2 stats[kMaxDepth];     // a row's (maximum, sum), for the copying warp
+  float weight[kMaxDepth];
+  float2 teacher[kTeacher];    // (normaliser, mass)
+  uint32_t buckets[2][kBuckets / 2];
+  int abort;
+};
+
+template <int kW>
+__host__ __device__ constexpr size_t head_bytes(int top) {
+  return (sizeof(Head<kW>) + kTeacher * kEntryBytes * static_cast<size_t>(top) + 127) & ~size_t(127);
+}
+
+template <class E, int kW>
+__global__ void __launch_bounds__((kW + 3) * 32) rows_kernel(const typename E::T* z, typename E::T* dz, Args a) {
+  constexpr int N = kVec<E>, kData = kW * 32;
+  extern __shared__ __align__(128) unsigned char smem[];
+  Head<kW>& h = *reinterpret_cast<Head<kW>*>(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_rank());
+  const int first_row = static_cast<int>(blockIdx.x) / a.cluster, step = static_cast<int>(gridDim.x) / a.cluster;
+  const int n = first_row < a.rows ? (a.rows - 1 - first_row) / step + 1 : 0;  // this cluster's rows
+  const float inv_tau = 1.f / a.tau, c = 1.4426950408889634f * inv_tau;
+  auto row_at = [&](int i) { return static_cast<int64_t>(first_row) + static_cast<int64_t>(i) * step; };
+  auto slot = [&](int i) { return reinterpret_cast<uint4*>(smem + head_bytes<kW>(a.top) + (i % a.depth) * static_cast<size_t>(a.slot_bytes)); };
+  auto entries = [&](int i) { return Entries(smem + sizeof(Head<kW>) + (i % kTeacher) * kEntryBytes * a.top, a.top); };
+  auto wait = [&](uint64_t& bar, int use) {
+    if (!mbar_wait_bounded(smem_u32(&bar), use & 1, &h.abort)) {
+      if (a.status != nullptr) atomicOr(a.status, ENGRAM_ST_TIMEOUT);
+      *reinterpret_cast<volatile int*>(&h.abort) = 1;  // the other waits give up too, and the block ends
+    }
+  };
+
+  if (tid == 0) {
+    for (int k = 0; k < kMaxDepth; ++k) {
+      mbar_init(smem_u32(&h.full[k]), 1);
+      mbar_init(smem_u32(&h.walked[k]), kW);
+    }
+    for (int k = 0; k < kPairs; ++k) mbar_init(smem_u32(&h.met[k]), 1);
+    for (int k = 0; k < kTeacher; ++k) {
+      mbar_init(smem_u32(&h.known[k]), 1);
+      mbar_init(smem_u32(&h.used[k]), 1);
+    }
+    h.abort = 0;
+    fence_mbar_init();
+  }
+  for (int k = tid; k < kBuckets; k += (kW + 3) * 32) (&h.buckets[0][0])[k] = 0u;
+  __syncthreads();
+  if (a.cluster > 1) {  // every block's barriers are set up before pairs are sent to them
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+
+  if (warp == kW) {
+    // ---- copies, and what is left of a row when it has been walked
+    auto weight_at = [&](int i) { return i < n && a.weight != nullptr ? __ldg(a.weight + row_at(i)) : 1.f; };
+    Row<E> r;
+    auto copy = [&](int i, float w) {
+      r.at(z, dz, a, row_at(i), rank, i > 0);
+      uint4* s = slot(i);
+      const bool on = w != 0.f;  // a row without weight is not read
+      if (lane == 1 && on && r.head) s[0] = r.edge(0);
+      if (lane == 2 && on && r.tail) s[r.in1 - r.v0] = r.edge(r.in1);
+      __syncwarp();
+      if (lane == 0) {
+        h.weight[i % a.depth] = w;
+        // the pairs of the row: expected before any of this block's own
+        mbar_arrive_expect_tx(smem_u32(&h.met[i % kPairs]), static_cast<uint32_t>(a.cluster) * kW * sizeof(float2));
+        const uint32_t bytes = on && r.end() > r.first() ? static_cast<uint32_t>(r.end() - r.first()) * 16u : 0u;
+        mbar_arrive_expect_tx(smem_u32(&h.full[i % a.depth]), bytes);
+        if (bytes > 0)
+          bulk_g2s(smem_u32(s + (r.first() - r.v0)), r.vectors() + r.first(), bytes, smem_u32(&h.full[i % a.depth]));
+      }
+    };
+    for (int i = 0; i < a.depth && i < n; ++i) copy(i, weight_at(i));
+    float next = weight_at(a.depth);
+    for (int i = 0; i < n; ++i) {
+      const float ahead = weight_at(i + a.depth + 1);
+      wait(h.walked[i % a.depth], i / a.depth);
+      const float w = h.weight[i % a.depth];
+      const float2 teacher = h.teacher[i % kTeacher], st = h.stats[i % a.depth];
+      const bool none = w == 0.f || teacher.y == 0.f;
+      const Entries e = entries(i);
+      __syncwarp();
+      if (i + a.depth < n && !h.abort) copy(i + a.depth, next);
+      next = ahead;
+      if (dz != nullptr && !none && !h.abort) {
+        r.at(z, dz, a, row_at(i), rank, true);
+        const float scale = w * a.tau;
+        fix_entries<E>(a, r, e, st.x, c, scale * teacher.y / st.y, scale, lane, 32);
+      }
+      if (rank == 0) {
+        const float loss = none ? 0.f : sum_loss(a, e, teacher.x, st.x, st.y, inv_tau, lane);
+        if (lane == 0) a.loss[row_at(i)] = none ? 0.f : w * a.tau * a.tau * loss;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&h.used[i % kTeacher]));
+    }
+    if (h.abort) {  // copies still under way land before the shared memory is released
+      for (int k = 0; k < a.depth; ++k)
+        for (int use = 0; use < 2; ++use) mbar_wait_bounded(smem_u32(&h.full[k]), use, nullptr);
+    }
+  } else if (warp > kW) {
+    // ---- the teacher's entries, rows in turn
+    for (int i = warp - kW - 1; i < n; i += 2) {
+      if (i >= kTeacher) wait(h.used[i % kTeacher], i / kTeacher - 1);
+      const int64_t row = row_at(i);
+      float norm = 0.f, mass = 0.f;
+      if (a.weight == nullptr || __ldg(a.weight + row) != 0.f) {
+        read_teacher<E>(a, z + row * a.z_stride, row, inv_tau, lane, entries(i), h.buckets[warp - kW - 1], norm, mass);
+      }
+      if (lane == 0) h.teacher[i % kTeacher] = make_float2(norm, mass);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&h.known[i % kTeacher]));
+    }
+  } else {
+    // ---- the walks
+    // A block sends the pairs of row i when it has all those of row i - 2, so
+    // every block has sent those, and had used up those of row i - kPairs before.
+    auto send = [&](int i, float m, float s) {
+      const float2* from = &h.pair[i % kPairs][rank * kW + warp];
+      if (lane < a.cluster) {
+        uint32_t to, bar;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(from)), "r"(lane));
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&h.met[i % kPairs])), "r"(lane));
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to), "f"(m),
+                     "f"(s), "r"(bar)
+                     : "memory");
+      }
+      __syncwarp();
+    };
+    Row<E> r;
+    auto walk = [&](int i) {
+      wait(h.met[i % kPairs], i / kPairs);
+      float m = -INFINITY, s = 0.f;
+      for (int k = lane; k < a.cluster * kW; k += 32) {
+        const float2 q = h.pair[i % kPairs][k];
+        join(m, s, q.x, q.y, c);
+      }
+      join_warp(m, s, c, lane);
+      const float w = h.weight[i % a.depth], mass = h.teacher[i % kTeacher].y;
+      if (tid == 0) h.stats[i % a.depth] = make_float2(m, s);
+      if (dz != nullptr) {
+        r.at(z, dz, a, row_at(i), rank, true);
+        if (w == 0.f || mass == 0.f) {  // nothing to learn here
+          r.zeros(tid, kData);
+        } else {
+          const float coef = w * a.tau * mass / s;
+          const uint4* src = slot(i) - r.v0;
+          if (r.off == r.doff) {
+            uint4* dv = reinterpret_cast<uint4*>(r.dz - r.off);
+            const int end = r.end();
+            int v = r.first() + tid;
+            for (; v + (kAhead - 1) * kData < end; v += kAhead * kData) {
+              uint4 x[kAhead];
+#pragma unroll
+              for (int u = 0; u < kAhead; ++u) x[u] = src[v + u * kData];
+#pragma unroll
+              for (int u = 0; u < kAhead; ++u) {
+                float f[N];
+                grad_vector<E>(x[u], m, c, coef, f);
+                __stcs(dv + v + u * kData, narrow<E>(f));
+              }
+            }
+            for (; v < end; v += kData) {
+              float f[N];
+              grad_vector<E>(src[v], m, c, coef, f);
+              __stcs(dv + v, narrow<E>(f));
+            }
+            float f[N];
+            if (r.head && tid == 0) {
+              grad_vector<E>(src[0], m, c, coef, f);
+              r.store_edge(0, f);
+            }
+            if (r.tail && tid == 32) {
+              grad_vector<E>(src[r.in1], m, c, coef, f);
+              r.store_edge(r.in1, f);
+            }
+          } else {  // the gradient's rows lie differently: value by value
+            const typename E::T* part = reinterpret_cast<const typename E::T*>(src) + r.off;
+            const int e1 = r.v1 * N - r.off < r.V ? r.v1 * N - r.off : r.V;
+            for (int e = (r.v0 * N - r.off > 0 ? r.v0 * N - r.off : 0) + tid; e < e1; e += kData)
+              E::store(r.dz + e, ex2((E::load(part + e) - m) * c) * coef);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&h.walked[i % a.depth]));
+    };
+    for (int i = 0; i < n; ++i) {
+      wait(h.full[i % a.depth], i / a.depth);
+      float m = -INFINITY, s = 0.f;
+      r.at(z, dz, a, row_at(i), rank, i > 0);
+      if (h.weight[i % a.depth] != 0.f) {
+        const uint4* part = slot(i);
+        const int count = r.v1 - r.v0;
+        for (int v = tid; v < count; v += kAhead * kData) {
+          uint4 x[kAhead];
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) x[u] = v + u * kData < count ? part[v + u * kData] : no_vector<E>();
+          add_vectors<E>(x, c, m, s);
+        }
+        join_warp(m, s, c, lane);
+      }
+      // the student's logits of the entries have been read before any block
+      // may write this row's gradient over them
+      wait(h.known[i % kTeacher], i / kTeacher);
+      send(i, m, s);
+      if (i > 0) walk(i - 1);
+    }
+    if (n > 0) walk(n - 1);
+  }
+  // no block leaves while another one may still send to it
+  __syncthreads();
+  if (a.cluster > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+
+// --------------------------------------------------------------------- long rows
+
+// One cluster of 8 blocks per row, which is read twice.
+constexpr int kLongWarps = 8, kLongThreads = kLongWarps * 32;
+
+template <class E>
+__global__ void __launch_bounds__(kLongThreads, 3) long_rows_kernel(const typename E::T* z, typename E::T* dz, Args a) {
+  constexpr int N = kVec<E>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float2 pair[kMaxCluster], warp_pair[kLongWarps], teacher;
+  __shared__ uint32_t buckets[kBuckets / 2];
+  const Entries e(smem, a.top);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_rank());
+  const int64_t row = blockIdx.x / a.cluster;
+  Row<E> r;
+  r.at(z, dz, a, row, rank, false);
+  const float inv_tau = 1.f / a.tau, c = 1.4426950408889634f * inv_tau;
+  const float w = a.weight != nullptr ? a.weight[row] : 1.f;
+  if (w == 0.f) {  // nothing to learn here (the same for the whole cluster)
+    if (rank == 0 && tid == 0) a.loss[row] = 0.f;
+    if (dz != nullptr) r.zeros(tid, kLongThreads);
+    return;
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (warp == 0) {
+    float norm, mass;
+    for (int k = lane; k < kBuckets / 2; k += 32) buckets[k] = 0u;
+    __syncwarp();
+    read_teacher<E>(a, r.z, row, inv_tau, lane, e, buckets, norm, mass);
+    if (lane == 0) teacher = make_float2(norm, mass);
+  }
+  const uint4* zv = r.vectors();
+  float m = -INFINITY, s = 0.f;
+  for (int v = r.v0 + tid; v < r.v1; v += kAhead * kLongThreads) {
+    uint4 x[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int vu = v + u * kLongThreads;
+      x[u] = vu >= r.v1 ? no_vector<E>() : vu >= r.in0 && vu < r.in1 ? zv[vu] : r.edge(vu);
+    }
+    add_vectors<E>(x, c, m, s);
+  }
+  join_warp(m, s, c, lane);
+  if (lane == 0) warp_pair[warp] = make_float2(m, s);
+  __syncthreads();
+  m = warp_pair[0].x;
+  s = warp_pair[0].y;
+#pragma unroll
+  for (int k = 1; k < kLongWarps; ++k) join(m, s, warp_pair[k].x, warp_pair[k].y, c);
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every block of the cluster runs
+  if (tid < a.cluster) {
+    uint32_t to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(&pair[rank])), "r"(tid));
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(m), "f"(s) : "memory");
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  m = pair[0].x;
+  s = pair[0].y;
+  for (int k = 1; k < a.cluster; ++k) join(m, s, pair[k].x, pair[k].y, c);
+
+  const float norm = teacher.x, mass = teacher.y;
+  if (rank == 0 && warp == 0) {
+    const float loss = mass == 0.f ? 0.f : sum_loss(a, e, norm, m, s, inv_tau, lane);
+    if (lane == 0) a.loss[row] = mass == 0.f ? 0.f : w * a.tau * a.tau * loss;
+  }
+  if (dz == nullptr) return;
+  if (mass == 0.f) {
+    r.zeros(tid, kLongThreads);
+    return;
+  }
+  const float scale = w * a.tau, coef = scale * mass / s;
+  if (r.off == r.doff) {
+    uint4* dv = reinterpret_cast<uint4*>(r.dz - r.off);
+#pragma unroll 4
+    for (int v = r.first() + tid; v < r.end(); v += kLongThreads) {
+      float f[N];
+      grad_vector<E>(zv[v], m, c, coef, f);
+      dv[v] = narrow<E>(f);
+    }
+    float f[N];
+    if (r.head && tid == 0) {
+      grad_vector<E>(r.edge(0), m, c, coef, f);
+      r.store_edge(0, f);
+    }
+    if (r.tail && tid == 32) {
+      grad_vector<E>(r.edge(r.in1), m, c, coef, f);
+      r.store_edge(r.in1, f);
+    }
+  } else {
+    const int e1 = r.v1 * N - r.off < r.V ? r.v1 * N - r.off : r.V;
+    for (int e = (r.v0 * N - r.off > 0 ? r.v0 * N - r.off : 0) + tid; e < e1; e += kLongThreads)
+      E::store(r.dz + e, ex2((E::load(r.z + e) - m) * c) * coef);
+  }
+  __syncthreads();
+  fix_entries<E>(a, r, e, m, c, coef, scale, tid, kLongThreads);
+}
+
+// ------------------------------------------------------------------------ launch
+
+constexpr int kSmem = 224 * 1024;  // dynamic shared memory of a block, at most
+
+// Sets the kernel's shared-memory limit once per device.
+int opt_in(const void* kernel, std::atomic<uint64_t>& done) {
   int dev = 0;
   cudaGetDevice(&dev);
   const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
-  if (bit == 0 || !(attr_set.load(std::memory_order_relaxed) & bit)) {
-    cudaError_t e = cudaFuncSetAttribute(distill_kernel<E, kResident>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kPartLimit + 16 * 1024);
-    if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    attr_set.fetch_or(bit, std::memory_order_relaxed);
-  }
+  if (bit != 0 && (done.load(std::memory_order_relaxed) & bit)) return ENGRAM_OK;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return ENGRAM_OK;
+}
+
+// Clusters that are on the GPU at once.  Blocks wait for one another within
+// their cluster alone, so the number matters for speed and nothing else.  The
+// runtime's answer for a kernel and its sizes is kept.
+int clusters_at_once(const void* kernel, int cluster, int threads, size_t smem, int* out) {
+  struct Known {
+    const void* kernel;
+    int dev, cluster;
+    size_t smem;
+    int clusters;
+  };
+  static std::mutex mu;
+  static Known known[64];
+  static int n_known = 0;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lock(mu);
+  for (int k = 0; k < n_known; ++k)
+    if (known[k].kernel == kernel && known[k].dev == dev && known[k].cluster == cluster && known[k].smem == smem) {
+      *out = known[k].clusters;
+      return ENGRAM_OK;
+    }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows * a.cluster));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaOccupancyMaxActiveClusters(out, kernel, &cfg);
+  if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaOccupancyMaxActiveClusters: %s", cudaGetErrorString(e));
+  if (*out < 1) return fail(ENGRAM_E_CUDA, "no cluster of %d blocks fits the device", cluster);
+  known[n_known < 64 ? n_known++ : 0] = Known{kernel, dev, cluster, smem, *out};
+  return ENGRAM_OK;
+}
+
+template <class K, class T>
+int launch(K kernel, int64_t blocks, int threads, size_t smem, const T* z, T* dz, const Args& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -438,21 +742,42 @@ int launch(const void* z, void* dz, const Args& a, int64_t rows, size_t smem, cu
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, distill_kernel<E, kResident>, static_cast<const typename E::T*>(z),
-                                     static_cast<typename E::T*>(dz), a);
-  if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "distill_kernel launch: %s", cudaGetErrorString(e));
-  return check_launch("distill_kernel");
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, z, dz, a);
+  if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "distill launch: %s", cudaGetErrorString(e));
+  return check_launch("distill");
+}
+
+template <class E, int kW>
+int launch_rows(const void* z, void* dz, const Args& a, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  int rc = opt_in(reinterpret_cast<const void*>(rows_kernel<E, kW>), done);
+  if (rc) return rc;
+  constexpr int kThreads = (kW + 3) * 32;
+  const size_t smem = head_bytes<kW>(a.top) + static_cast<size_t>(a.depth) * a.slot_bytes;
+  int clusters = 0;
+  if ((rc = clusters_at_once(reinterpret_cast<const void*>(rows_kernel<E, kW>), a.cluster, kThreads, smem, &clusters)))
+    return rc;
+  return launch(rows_kernel<E, kW>, std::min<int64_t>(a.rows, clusters) * a.cluster, kThreads, smem,
+                static_cast<const typename E::T*>(z), static_cast<typename E::T*>(dz), a, st);
 }
 
 template <class E>
-int launch_distill(const void* z, void* dz, Args a, int64_t rows, cudaStream_t st) {
-  const int64_t bytes = a.vocab * E::kBytes + 16;  // with a misaligned row's first vector
-  a.cluster = 1;
-  while (a.cluster < kMaxCluster && bytes / a.cluster > kPartBytes) a.cluster *= 2;
-  const int64_t vecs = (bytes + 15) / 16, per = (vecs + a.cluster - 1) / a.cluster;
-  const size_t head = (sizeof(Head) + 12 * static_cast<size_t>(a.top) + 127) & ~size_t(127);
-  if (per * 16 <= kPartLimit) return launch<E, true>(z, dz, a, rows, head + static_cast<size_t>(per) * 16, st);
-  return launch<E, false>(z, dz, a, rows, head, st);
+int launch_distill(const void* z, void* dz, Args a, cudaStream_t st) {
+  a.aligned = a.z_stride * E::kBytes % 16 == 0 && (dz == nullptr || a.dz_stride * E::kBytes % 16 == 0);
+  const int64_t vecs = (a.vocab * E::kBytes + 16 + 15) / 16;  // with a misaligned row's first vector
+  const int64_t room = kSmem - 16 * 1024 - static_cast<int64_t>(kTeacher) * kEntryBytes * a.top;  // for rows, beside the head
+  // the smallest cluster that holds three rows; of 4 or 8 blocks two will do
+  for (a.cluster = 1; a.cluster <= kMaxCluster; a.cluster *= 2) {
+    const int64_t part = ((vecs + a.cluster - 1) / a.cluster * 16 + 127) / 128 * 128;
+    for (a.depth = kMaxDepth; a.depth >= (a.cluster >= 4 ? 2 : kMaxDepth); --a.depth) {
+      if (part * a.depth > room) continue;
+      a.slot_bytes = static_cast<int32_t>(part);
+      return part <= 16 * 1024 ? launch_rows<E, 4>(z, dz, a, st) : launch_rows<E, 8>(z, dz, a, st);
+    }
+  }
+  a.cluster = kMaxCluster;
+  return launch(long_rows_kernel<E>, static_cast<int64_t>(a.rows) * a.cluster, kLongThreads, kEntryBytes * static_cast<size_t>(a.top),
+                static_cast<const typename E::T*>(z), static_cast<typename E::T*>(dz), a, st);
 }
 
 }  // namespace
@@ -482,8 +807,19 @@ extern "C" int engram_distill(const void* logits_d, int32_t type, int64_t n_toke
     return fail(ENGRAM_E_SHAPE, "in place, dlogits has the stride of logits");
   int rc = check_device(nullptr);
   if (rc) return rc;
-  Args a{vocab, logits_stride, dlogits_stride, teacher_ids_d, teacher_logits_d, top, 1, temperature, teacher_lse_d,
-         weight_d, loss_d, status_d};
-  return type == ENGRAM_T_BF16 ? launch_distill<train::Bf16>(logits_d, dlogits_d, a, n_tokens, as_stream(stream))
-                               : launch_distill<train::F32>(logits_d, dlogits_d, a, n_tokens, as_stream(stream));
+  Args a{};
+  a.vocab = vocab;
+  a.z_stride = logits_stride;
+  a.dz_stride = dlogits_stride;
+  a.rows = static_cast<int32_t>(n_tokens);
+  a.ids = teacher_ids_d;
+  a.t = teacher_logits_d;
+  a.top = top;
+  a.tau = temperature;
+  a.lse = teacher_lse_d;
+  a.weight = weight_d;
+  a.loss = loss_d;
+  a.status = status_d;
+  return type == ENGRAM_T_BF16 ? launch_distill<train::Bf16>(logits_d, dlogits_d, a, as_stream(stream))
+                               : launch_distill<train::F32>(logits_d, dlogits_d, a, as_stream(stream));
 }
