@@ -34,7 +34,8 @@ struct Args {
   int32_t rows;
   const int32_t* ids;
   const float* t;
-  int32_t top, cluster, depth, slot_bytes;
+  int32_t top, cluster, depth, keep, slot_bytes;
+  int32_t cluster_log2;
   bool aligned;  // the rows' strides are multiples of 16 bytes
   float tau;
   const float* lse;
@@ -47,6 +48,15 @@ __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// 2^x of two values.  (A quarter of the pairs through the FMA units instead, by a
+// sixth-order series, takes 498 us against 418 at 4096 x 129,280 bf16: the walks
+// are bound by instructions issued, not by the exponentials.)
+__device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
+  float x0, x1;
+  f2_split(x, x0, x1);
+  return f2(ex2(x0), ex2(x1));
 }
 
 template <bool kMax>
@@ -138,7 +148,7 @@ struct Row {
     V = static_cast<int>(a.vocab);
     off = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / E::kBytes);
     doff = static_cast<int>((reinterpret_cast<uintptr_t>(dz) & 15) / E::kBytes);
-    const int vecs = (V + off + N - 1) / N, per = (vecs + a.cluster - 1) / a.cluster;
+    const int vecs = (V + off + N - 1) / N, per = (vecs + a.cluster - 1) >> a.cluster_log2;
     v0 = rank * per < vecs ? rank * per : vecs;
     v1 = v0 + per < vecs ? v0 + per : vecs;
     in0 = off > 0 ? 1 : 0;
@@ -157,6 +167,13 @@ struct Row {
       f[j] = e >= 0 && e < V ? E::load(z + e) : -INFINITY;
     }
     return narrow<E>(f);
+  }
+  // The element of the part's edge vectors that a lane stands for, or -1: lanes
+  // 0 .. N - 1 the head's, N .. 2 N - 1 the tail's.
+  __device__ __forceinline__ int edge_element(int lane) const {
+    const bool mine = lane < N ? head : lane < 2 * N && tail;
+    const int e = (lane < N ? 0 : in1) * N + lane % N - off;
+    return mine && e >= 0 && e < V ? e : -1;
   }
   __device__ __forceinline__ void store_edge(int v, const float (&f)[N]) const {
 #pragma unroll
@@ -197,9 +214,8 @@ __device__ __forceinline__ void add_vectors(const uint4 (&x)[kAhead], float c, f
     widen<E>(x[u], f);
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
-      float x0, x1;
-      f2_split(f2_mul(f2_add(f2(f[j], f[j + 1]), f2(at, at)), f2(c, c)), x0, x1);
-      sum = f2_add(sum, f2(ex2(x0), ex2(x1)));
+      const uint64_t x = f2_mul(f2_add(f2(f[j], f[j + 1]), f2(at, at)), f2(c, c));
+      sum = f2_add(sum, ex2_pair(x));
     }
   }
   float s0, s1;
@@ -213,18 +229,16 @@ __device__ __forceinline__ uint4 no_vector() {
   return make_uint4(low, low, low, low);
 }
 
-// The warp's pairs joined; the lanes of a pair join in the same order, so that
-// they agree.
-__device__ __forceinline__ void join_warp(float& m, float& s, float c, int lane) {
+// The warp's pairs joined: the largest maximum, then one rescaled sum a lane,
+// added up in the same order in every lane's view.
+__device__ __forceinline__ void join_warp(float& m, float& s, float c) {
+  float top;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top) : "f"(m));
+  const float at = top == -INFINITY ? 0.f : top;
+  s *= ex2((m - at) * c);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    const bool first = (lane & o) == 0;
-    float ma = first ? m : m2, sa = first ? s : s2;
-    join(ma, sa, first ? m2 : m, first ? s2 : s, c);
-    m = ma;
-    s = sa;
-  }
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  m = top;
 }
 
 // coef 2^((z - m) c) of a vector
@@ -233,9 +247,8 @@ __device__ __forceinline__ void grad_vector(const uint4& x, float m, float c, fl
   widen<E>(x, f);
 #pragma unroll
   for (int j = 0; j < kVec<E>; j += 2) {
-    float x0, x1;
-    f2_split(f2_mul(f2_add(f2(f[j], f[j + 1]), f2(-m, -m)), f2(c, c)), x0, x1);
-    f2_split(f2_mul(f2(ex2(x0), ex2(x1)), f2(coef, coef)), f[j], f[j + 1]);
+    const uint64_t e = f2_mul(f2_add(f2(f[j], f[j + 1]), f2(-m, -m)), f2(c, c));
+    f2_split(f2_mul(ex2_pair(e), f2(coef, coef)), f[j], f[j + 1]);
   }
 }
 
@@ -257,7 +270,7 @@ constexpr int kEntryBytes = 16;
 
 // Entries with the same id are told by a table of counts by id modulo its
 // size, all zero before and after: only those that share a count are compared.
-constexpr int kBuckets = 2048;  // 16-bit counts
+constexpr int kBuckets = 1024;  // 16-bit counts
 
 // The entries, their normaliser and their mass, by one warp.
 template <class E>
@@ -339,15 +352,17 @@ __device__ __forceinline__ void fix_entries(const Args& a, const Row<E>& r, cons
 // The blocks of a cluster share a row and go from row to row.  In a block
 //   - the copying warp keeps the copies of the next `depth` rows under way, and
 //     finishes a row when its walk is done: the entries' gradients, the loss;
-//   - two warps prepare the teacher's entries of the next rows, in turn;
+//   - kPrep warps prepare the teacher's entries of the next rows, in turn (some
+//     14,000 cycles a row, nearly all of them waits for memory);
 //   - kW warps walk the rows: of row i + 1 the maximum and the sum, which they
 //     send to every block of the cluster, then of row i, whose pairs have
 //     arrived meanwhile, the gradient.
 // Waits are for copies, for the other blocks' pairs and for the block's own
 // warps; all are bounded.
 constexpr int kPairs = 4;    // rows whose pairs may be under way: see `send`
-constexpr int kTeacher = 4;  // rows whose teacher's entries are kept
-constexpr int kMaxDepth = 3;
+constexpr int kPrep = 4;
+constexpr int kTeacher = 8;  // rows whose teacher's entries are kept, at most
+constexpr int kMaxDepth = 4;  // rows whose copies may be under way
 
 template <int kW>
 struct Head {  // in front of the dynamic shared memory
@@ -359,17 +374,17 @@ struct Head {  // in front of the dynamic shared memory
   float2 stats[kMaxDepth];     // a row's (maximum, sum), for the copying warp
   float weight[kMaxDepth];
   float2 teacher[kTeacher];    // (normaliser, mass)
-  uint32_t buckets[2][kBuckets / 2];
+  uint32_t buckets[kPrep][kBuckets / 2];
   int abort;
 };
 
 template <int kW>
-__host__ __device__ constexpr size_t head_bytes(int top) {
-  return (sizeof(Head<kW>) + kTeacher * kEntryBytes * static_cast<size_t>(top) + 127) & ~size_t(127);
+__host__ __device__ constexpr size_t head_bytes(int top, int keep) {
+  return (sizeof(Head<kW>) + static_cast<size_t>(keep) * kEntryBytes * top + 127) & ~size_t(127);
 }
 
 template <class E, int kW>
-__global__ void __launch_bounds__((kW + 3) * 32) rows_kernel(const typename E::T* z, typename E::T* dz, Args a) {
+__global__ void __launch_bounds__((kW + 1 + kPrep) * 32) rows_kernel(const typename E::T* z, typename E::T* dz, Args a) {
   constexpr int N = kVec<E>, kData = kW * 32;
   extern __shared__ __align__(128) unsigned char smem[];
   Head<kW>& h = *reinterpret_cast<Head<kW>*>(smem);
@@ -379,8 +394,8 @@ __global__ void __launch_bounds__((kW + 3) * 32) rows_kernel(const typename E::T
   const int n = first_row < a.rows ? (a.rows - 1 - first_row) / step + 1 : 0;  // this cluster's rows
   const float inv_tau = 1.f / a.tau, c = 1.4426950408889634f * inv_tau;
   auto row_at = [&](int i) { return static_cast<int64_t>(first_row) + static_cast<int64_t>(i) * step; };
-  auto slot = [&](int i) { return reinterpret_cast<uint4*>(smem + head_bytes<kW>(a.top) + (i % a.depth) * static_cast<size_t>(a.slot_bytes)); };
-  auto entries = [&](int i) { return Entries(smem + sizeof(Head<kW>) + (i % kTeacher) * kEntryBytes * a.top, a.top); };
+  auto slot = [&](int i) { return reinterpret_cast<uint4*>(smem + head_bytes<kW>(a.top, a.keep) + (i % a.depth) * static_cast<size_t>(a.slot_bytes)); };
+  auto entries = [&](int i) { return Entries(smem + sizeof(Head<kW>) + (i % a.keep) * kEntryBytes * a.top, a.top); };
   auto wait = [&](uint64_t& bar, int use) {
     if (!mbar_wait_bounded(smem_u32(&bar), use & 1, &h.abort)) {
       if (a.status != nullptr) atomicOr(a.status, ENGRAM_ST_TIMEOUT);
@@ -390,7 +405,7 @@ __global__ void __launch_bounds__((kW + 3) * 32) rows_kernel(const typename E::T
 
   if (tid == 0) {
     for (int k = 0; k < kMaxDepth; ++k) {
-      mbar_init(smem_u32(&h.full[k]), 1);
+      mbar_init(smem_u32(&h.full[k]), 2);
       mbar_init(smem_u32(&h.walked[k]), kW);
     }
     for (int k = 0; k < kPairs; ++k) mbar_init(smem_u32(&h.met[k]), 1);
@@ -401,7 +416,7 @@ __global__ void __launch_bounds__((kW + 3) * 32) rows_kernel(const typename E::T
     h.abort = 0;
     fence_mbar_init();
   }
-  for (int k = tid; k < kBuckets; k += (kW + 3) * 32) (&h.buckets[0][0])[k] = 0u;
+  for (int k = tid; k < kPrep * kBuckets / 2; k += (kW + 1 + kPrep) * 32) (&h.buckets[0][0])[k] = 0u;
   __syncthreads();
   if (a.cluster > 1) {  // every block's barriers are set up before pairs are sent to them
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -416,18 +431,25 @@ __global__ void __launch_bounds__((kW + 3) * 32) rows_kernel(const typename E::T
       r.at(z, dz, a, row_at(i), rank, i > 0);
       uint4* s = slot(i);
       const bool on = w != 0.f;  // a row without weight is not read
-      if (lane == 1 && on && r.head) s[0] = r.edge(0);
-      if (lane == 2 && on && r.tail) s[r.in1 - r.v0] = r.edge(r.in1);
-      __syncwarp();
+      const uint32_t bar = smem_u32(&h.full[i % a.depth]);
       if (lane == 0) {
         h.weight[i % a.depth] = w;
         // the pairs of the row: expected before any of this block's own
         mbar_arrive_expect_tx(smem_u32(&h.met[i % kPairs]), static_cast<uint32_t>(a.cluster) * kW * sizeof(float2));
         const uint32_t bytes = on && r.end() > r.first() ? static_cast<uint32_t>(r.end() - r.first()) * 16u : 0u;
-        mbar_arrive_expect_tx(smem_u32(&h.full[i % a.depth]), bytes);
-        if (bytes > 0)
-          bulk_g2s(smem_u32(s + (r.first() - r.v0)), r.vectors() + r.first(), bytes, smem_u32(&h.full[i % a.depth]));
+        mbar_arrive_expect_tx(bar, bytes);
+        if (bytes > 0) bulk_g2s(smem_u32(s + (r.first() - r.v0)), r.vectors() + r.first(), bytes, bar);
       }
+      __syncwarp();
+      if (on && (r.head || r.tail)) {
+        if (lane < 2 * N && (lane < N ? r.head : r.tail)) {
+          const int e = r.edge_element(lane);
+          const int at = ((lane < N ? 0 : r.in1) - r.v0) * N + lane % N;
+          E::store(reinterpret_cast<typename E::T*>(s) + at, e >= 0 ? E::load(r.z + e) : -INFINITY);
+        }
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(bar);
     };
     for (int i = 0; i < a.depth && i < n; ++i) copy(i, weight_at(i));
     float next = weight_at(a.depth);
@@ -435,23 +457,32 @@ __global__ void __launch_bounds__((kW + 3) * 32) rows_kernel(const typename E::T
       const float ahead = weight_at(i + a.depth + 1);
       wait(h.walked[i % a.depth], i / a.depth);
       const float w = h.weight[i % a.depth];
-      const float2 teacher = h.teacher[i % kTeacher], st = h.stats[i % a.depth];
+      const float2 teacher = h.teacher[i % a.keep], st = h.stats[i % a.depth];
       const bool none = w == 0.f || teacher.y == 0.f;
       const Entries e = entries(i);
+      int edge = -1;  // a value of the row's first or last vector that this lane finishes
+      float edge_z = 0.f;
+      if (dz != nullptr && !none) {
+        r.at(z, dz, a, row_at(i), rank, true);
+        edge = r.off == r.doff ? r.edge_element(lane) : -1;
+        if (edge >= 0) edge_z = E::load(reinterpret_cast<const typename E::T*>(slot(i)) + (edge + r.off - r.v0 * N));
+      }
       __syncwarp();
       if (i + a.depth < n && !h.abort) copy(i + a.depth, next);
       next = ahead;
       if (dz != nullptr && !none && !h.abort) {
         r.at(z, dz, a, row_at(i), rank, true);
-        const float scale = w * a.tau;
-        fix_entries<E>(a, r, e, st.x, c, scale * teacher.y / st.y, scale, lane, 32);
+        const float scale = w * a.tau, coef = scale * teacher.y / st.y;
+        if (edge >= 0) E::store(r.dz + edge, ex2((edge_z - st.x) * c) * coef);
+        __syncwarp();
+        fix_entries<E>(a, r, e, st.x, c, coef, scale, lane, 32);
       }
       if (rank == 0) {
         const float loss = none ? 0.f : sum_loss(a, e, teacher.x, st.x, st.y, inv_tau, lane);
         if (lane == 0) a.loss[row_at(i)] = none ? 0.f : w * a.tau * a.tau * loss;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&h.used[i % kTeacher]));
+      if (lane == 0) mbar_arrive(smem_u32(&h.used[i % a.keep]));
     }
     if (h.abort) {  // copies still under way land before the shared memory is released
       for (int k = 0; k < a.depth; ++k)
@@ -459,16 +490,16 @@ __global__ void __launch_bounds__((kW + 3) * 32) rows_kernel(const typename E::T
     }
   } else if (warp > kW) {
     // ---- the teacher's entries, rows in turn
-    for (int i = warp - kW - 1; i < n; i += 2) {
-      if (i >= kTeacher) wait(h.used[i % kTeacher], i / kTeacher - 1);
+    for (int i = warp - kW - 1; i < n; i += kPrep) {
+      if (i >= a.keep) wait(h.used[i % a.keep], i / a.keep - 1);
       const int64_t row = row_at(i);
       float norm = 0.f, mass = 0.f;
       if (a.weight == nullptr || __ldg(a.weight + row) != 0.f) {
         read_teacher<E>(a, z + row * a.z_stride, row, inv_tau, lane, entries(i), h.buckets[warp - kW - 1], norm, mass);
       }
-      if (lane == 0) h.teacher[i % kTeacher] = make_float2(norm, mass);
+      if (lane == 0) h.teacher[i % a.keep] = make_float2(norm, mass);
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&h.known[i % kTeacher]));
+      if (lane == 0) mbar_arrive(smem_u32(&h.known[i % a.keep]));
     }
   } else {
     // ---- the walks
@@ -494,8 +525,8 @@ __global__ void __launch_bounds__((kW + 3) * 32) rows_kernel(const typename E::T
         const float2 q = h.pair[i % kPairs][k];
         join(m, s, q.x, q.y, c);
       }
-      join_warp(m, s, c, lane);
-      const float w = h.weight[i % a.depth], mass = h.teacher[i % kTeacher].y;
+      join_warp(m, s, c);
+      const float w = h.weight[i % a.depth], mass = h.teacher[i % a.keep].y;
       if (tid == 0) h.stats[i % a.depth] = make_float2(m, s);
       if (dz != nullptr) {
         r.at(z, dz, a, row_at(i), rank, true);
@@ -524,15 +555,6 @@ __global__ void __launch_bounds__((kW + 3) * 32) rows_kernel(const typename E::T
               grad_vector<E>(src[v], m, c, coef, f);
               __stcs(dv + v, narrow<E>(f));
             }
-            float f[N];
-            if (r.head && tid == 0) {
-              grad_vector<E>(src[0], m, c, coef, f);
-              r.store_edge(0, f);
-            }
-            if (r.tail && tid == 32) {
-              grad_vector<E>(src[r.in1], m, c, coef, f);
-              r.store_edge(r.in1, f);
-            }
           } else {  // the gradient's rows lie differently: value by value
             const typename E::T* part = reinterpret_cast<const typename E::T*>(src) + r.off;
             const int e1 = r.v1 * N - r.off < r.V ? r.v1 * N - r.off : r.V;
@@ -557,11 +579,11 @@ __global__ void __launch_bounds__((kW + 3) * 32) rows_kernel(const typename E::T
           for (int u = 0; u < kAhead; ++u) x[u] = v + u * kData < count ? part[v + u * kData] : no_vector<E>();
           add_vectors<E>(x, c, m, s);
         }
-        join_warp(m, s, c, lane);
+        join_warp(m, s, c);
       }
       // the student's logits of the entries have been read before any block
       // may write this row's gradient over them
-      wait(h.known[i % kTeacher], i / kTeacher);
+      wait(h.known[i % a.keep], i / a.keep);
       send(i, m, s);
       if (i > 0) walk(i - 1);
     }
@@ -618,7 +640,7 @@ __global__ void __launch_bounds__(kLongThreads, 3) long_rows_kernel(const typena
     }
     add_vectors<E>(x, c, m, s);
   }
-  join_warp(m, s, c, lane);
+  join_warp(m, s, c);
   if (lane == 0) warp_pair[warp] = make_float2(m, s);
   __syncthreads();
   m = warp_pair[0].x;
@@ -752,8 +774,8 @@ int launch_rows(const void* z, void* dz, const Args& a, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   int rc = opt_in(reinterpret_cast<const void*>(rows_kernel<E, kW>), done);
   if (rc) return rc;
-  constexpr int kThreads = (kW + 3) * 32;
-  const size_t smem = head_bytes<kW>(a.top) + static_cast<size_t>(a.depth) * a.slot_bytes;
+  constexpr int kThreads = (kW + 1 + kPrep) * 32;
+  const size_t smem = head_bytes<kW>(a.top, a.keep) + static_cast<size_t>(a.depth) * a.slot_bytes;
   int clusters = 0;
   if ((rc = clusters_at_once(reinterpret_cast<const void*>(rows_kernel<E, kW>), a.cluster, kThreads, smem, &clusters)))
     return rc;
@@ -765,17 +787,25 @@ template <class E>
 int launch_distill(const void* z, void* dz, Args a, cudaStream_t st) {
   a.aligned = a.z_stride * E::kBytes % 16 == 0 && (dz == nullptr || a.dz_stride * E::kBytes % 16 == 0);
   const int64_t vecs = (a.vocab * E::kBytes + 16 + 15) / 16;  // with a misaligned row's first vector
-  const int64_t room = kSmem - 16 * 1024 - static_cast<int64_t>(kTeacher) * kEntryBytes * a.top;  // for rows, beside the head
-  // the smallest cluster that holds three rows; of 4 or 8 blocks two will do
-  for (a.cluster = 1; a.cluster <= kMaxCluster; a.cluster *= 2) {
+  a.keep = a.top <= 128 ? kTeacher : 4;  // fewer where the entries would take the rows' place
+  const int64_t room = kSmem - static_cast<int64_t>(head_bytes<16>(a.top, a.keep));
+  // the smallest cluster that holds three rows (four where they fit); of 4 or 8
+  // blocks two will do
+  for (a.cluster = 1, a.cluster_log2 = 0; a.cluster <= kMaxCluster; a.cluster *= 2, ++a.cluster_log2) {
     const int64_t part = ((vecs + a.cluster - 1) / a.cluster * 16 + 127) / 128 * 128;
-    for (a.depth = kMaxDepth; a.depth >= (a.cluster >= 4 ? 2 : kMaxDepth); --a.depth) {
+    for (a.depth = kMaxDepth; a.depth >= (a.cluster >= 4 ? 2 : 3); --a.depth) {
       if (part * a.depth > room) continue;
       a.slot_bytes = static_cast<int32_t>(part);
-      return part <= 16 * 1024 ? launch_rows<E, 4>(z, dz, a, st) : launch_rows<E, 8>(z, dz, a, st);
+      // warps for the length of their walk: of 16,384 rows of 16,000 bf16 (32 KB)
+      // 8 take 247 and 16 take 350 us, of 4096 rows of 129,280 (64 KB parts) 16
+      // take 401 and 8 take 407
+      return part <= 16 * 1024   ? launch_rows<E, 4>(z, dz, a, st)
+             : part <= 40 * 1024 ? launch_rows<E, 8>(z, dz, a, st)
+                                 : launch_rows<E, 16>(z, dz, a, st);
     }
   }
   a.cluster = kMaxCluster;
+  a.cluster_log2 = 3;
   return launch(long_rows_kernel<E>, static_cast<int64_t>(a.rows) * a.cluster, kLongThreads, kEntryBytes * static_cast<size_t>(a.top),
                 static_cast<const typename E::T*>(z), static_cast<typename E::T*>(dz), a, st);
 }
