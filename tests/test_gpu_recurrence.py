@@ -309,6 +309,24 @@ def test_on_another_stream_and_in_a_graph():
         assert torch.equal(y, want)
 
 
+def test_rows_past_four_giga_elements():
+    """Row offsets beyond 2^32 elements: columns of a very wide matrix, against the same values packed."""
+    T, D, wide = 66_000, 8, 66_000
+    big = torch.empty((T, wide), dtype=torch.bfloat16, device=DEV)
+    x, g, dy = make((T, D), "bf16", 180), make((T, D), "bf16", 181, 1.0, 2.0), make((T, D), "bf16", 182)
+    parts = [big[:, k * 64:k * 64 + D] for k in range(6)]
+    for p, t in zip(parts, (x, g, dy)):
+        p.copy_(t)
+    cu = i64([0, 30_000, T])
+    c1, c2 = eg.recurrence_carry(T, D, DEV), eg.recurrence_carry(T, D, DEV)
+    y = eg.engram_recurrence(x, g, cu, carry=c1)
+    dx, dg = eg.engram_recurrence_grad(dy, x, g, c1, cu)
+    eg.engram_recurrence(parts[0], parts[1], cu, y=parts[3], carry=c2)
+    assert torch.equal(parts[3], y)
+    eg.engram_recurrence_grad(parts[2], parts[0], parts[1], c2, cu, dx=parts[4], dg=parts[5])
+    assert torch.equal(parts[4], dx) and torch.equal(parts[5], dg)
+
+
 def test_refusals():
     x = make((4, 8), "bf16", 170)
     cu = i64([0, 4])
