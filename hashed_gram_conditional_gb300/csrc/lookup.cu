@@ -194,29 +194,28 @@ struct SortArgs {
   int32_t n, per;  // entries, and how many each block handles
   int32_t passes, bits;
   Entry* list[2];
-  int32_t* counts;  // [block][digit], then [block] heads
+  int32_t* counts;  // [block][digit]
   int32_t* groups;  // [pass][group of kGroup blocks][digit], zeroed by the caller
   int32_t* barrier;
   int32_t chunk, chunks;  // sorted entries that are summed together (see seg_sum_kernel), and how many such
-  int32_t* base;   // segments that begin before each chunk, or null
-  int32_t* count;  // all of them
+  int32_t* base;   // segments that begin in the block's chunks before each chunk, or null
+  int32_t chunks_per;  // chunks whose segments each block counts
+  int32_t* heads;      // [block]: segments that begin in its chunks
   int32_t* next;   // the summing kernel's two counters, zeroed here
   int32_t* status;
 };
 
 // All blocks meet; false when the wait ran out (the blocks are co-resident, so
-// that means a broken launch).
+// that means a broken launch).  What a block's threads wrote before is released
+// by its first thread, which they meet first.
 __device__ __forceinline__ bool meet(const SortArgs& a, int32_t& met) {
-  if (gridDim.x == 1) {
-    __syncthreads();
-    return true;
-  }
-  __threadfence();
-  const int32_t want = ++met * static_cast<int32_t>(gridDim.x);
   __syncthreads();
+  if (gridDim.x == 1) return true;
+  const int32_t want = ++met * static_cast<int32_t>(gridDim.x);
   bool ok = true;
   if (threadIdx.x == 0) {
-    atomicAdd(a.barrier, 1);
+    __threadfence();
+    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(a.barrier) : "memory");
     const long long begun = clock64();
     while (true) {
       int32_t v;
@@ -235,14 +234,17 @@ __device__ __forceinline__ bool meet(const SortArgs& a, int32_t& met) {
 
 // Moves each entry to its place: entries of smaller digits, entries of the
 // same digit in earlier blocks, rounds, warps and lanes come before it, which
-// keeps the passes stable.
+// keeps the passes stable.  Where a block's entries are one round (up to
+// 622,592 entries on 152 SMs) they are ranked while they are counted and stay in
+// registers over the barrier; otherwise they are counted first.
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
-  __shared__ __align__(16) uint16_t hist[kSortWarps][kMaxDigits];
+  __shared__ uint16_t hist[kSortWarps][kMaxDigits];
   __shared__ int32_t place[kMaxDigits], half[kMaxDigits], warp_sum[kSortWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int digits = 1 << a.bits, blocks = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
   const int32_t e0 = a.n < static_cast<int64_t>(me) * a.per ? a.n : me * a.per;
   const int32_t e1 = a.n - e0 < a.per ? a.n : e0 + a.per;
+  const bool one_round = a.per <= kRound;
   int32_t met = 0;
   if (me == 0 && tid < 2) a.next[tid] = 0;
 
@@ -255,20 +257,80 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
     auto entry_at = [&](int32_t i) {
       return first ? Entry{entry_key(__ldg(a.ids + i), a.total_rows), i} : load_entry(in_list + i);
     };
+    bool bad = false;
+
+    // a round's entries, each with its rank among those of its warp and digit;
+    // then hist: its digit's entries in earlier warps, half: in the round
+    Entry entry[kItems];
+    int rank[kItems];
+    auto in_round = [&](int32_t r0, int k) {
+      return static_cast<int64_t>(r0) + warp * (32 * kItems) + lane + 32 * k < e1;
+    };
+    auto take = [&](int32_t r0) {
+      const int32_t at = r0 + warp * (32 * kItems) + lane;  // (below 2^31 where it is used)
+      for (int d = lane; d < digits; d += 32) hist[warp][d] = 0;
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        entry[k] = in_round(r0, k) ? entry_at(at + 32 * k) : Entry{0u, 0};
+        if (first && in_round(r0, k) && entry[k].key == static_cast<uint32_t>(a.total_rows))
+          bad |= __ldg(a.ids + at + 32 * k) != ENGRAM_DEAD;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        const bool in = in_round(r0, k);
+        const uint32_t d = digit_of(entry[k].key);
+        uint32_t peers = __ballot_sync(0xffffffffu, in);  // the lanes with the same digit, bit by bit
+#pragma unroll
+        for (int bit = 0; bit < kDigitBits; ++bit) {
+          const bool one = d >> bit & 1u;
+          const uint32_t ones = __ballot_sync(0xffffffffu, one);
+          peers &= one ? ones : ~ones;
+        }
+        const int before = in ? hist[warp][d] : 0;
+        rank[k] = before + __popc(peers & ((1u << lane) - 1u));
+        __syncwarp();
+        if (in && (peers >> lane) == 1u) hist[warp][d] = static_cast<uint16_t>(before + __popc(peers));  // the highest lane
+        __syncwarp();
+      }
+      __syncthreads();
+      if (tid < digits) {
+        int c[kSortWarps], run = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) c[w] = hist[w][tid];
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) {
+          hist[w][tid] = static_cast<uint16_t>(run);
+          run += c[w];
+        }
+        half[tid] = run;
+      }
+      __syncthreads();
+    };
+    auto put = [&](int32_t r0) {
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        if (in_round(r0, k)) {
+          const uint32_t d = digit_of(entry[k].key);
+          const int32_t to = place[d] + hist[warp][d] + rank[k];
+          __stcg(reinterpret_cast<uint2*>(out_list + to), make_uint2(entry[k].key, static_cast<uint32_t>(entry[k].idx)));
+        }
+      }
+    };
 
     // this block's digits
-    if (tid < digits) place[tid] = 0;
-    __syncthreads();
-    bool bad = false;
-    for (int32_t i = e0 + tid; i < e1; i += kSortThreads) {
-      if (first) {
-        const int32_t id = a.ids[i];
-        bad |= id != ENGRAM_DEAD && (id < 0 || id >= a.total_rows);
+    if (one_round) {
+      take(e0);
+      if (tid < digits) place[tid] = half[tid];
+    } else {
+      if (tid < digits) place[tid] = 0;
+      __syncthreads();
+      for (int32_t i = e0 + tid; i < e1; i += kSortThreads) {
+        const Entry e = entry_at(i);
+        atomicAdd(&place[digit_of(e.key)], 1);
       }
-      atomicAdd(&place[digit_of(entry_at(i).key)], 1);
+      __syncthreads();
     }
-    if (bad && a.status != nullptr) atomicOr(a.status, ENGRAM_ST_BAD_ROW);
-    __syncthreads();
     int32_t* groups = nullptr;
     if (blocks > 1) {
       const int n_groups = (blocks + kGroup - 1) / kGroup;
@@ -281,24 +343,22 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
     }
 
     // per digit: its entries in all blocks, and in the blocks before this one:
-    // whole groups, then the blocks of this one's group.  A thread sums four
-    // digits over an eighth of the groups and blocks.
+    // whole groups, then the blocks of this one's group.  Eight neighbouring
+    // lanes sum four digits, an eighth of the groups and blocks each.
     int32_t total = 0, prior = 0;
     if (blocks > 1) {
-      constexpr int kParts = kSortThreads / (kMaxDigits / 4);
-      int32_t(*sums)[kMaxDigits] = reinterpret_cast<int32_t(*)[kMaxDigits]>(&hist[0][0]);
-      int32_t(*priors)[kMaxDigits] = sums + kParts;
-      static_assert(2 * kParts * kMaxDigits * 4 <= sizeof(hist), "the sums fit the histograms' place");
-      const int quad = tid % (kMaxDigits / 4), part = tid / (kMaxDigits / 4);
+      constexpr int kParts = 8;
+      static_assert(kSortThreads / kParts * 4 >= kMaxDigits, "every digit is summed");
+      const int quad = tid / kParts, part = tid % kParts;
       const int my_group = me / kGroup, n_groups = (blocks + kGroup - 1) / kGroup;
+      int all[4] = {}, early[4] = {};
+      auto add = [](int (&to)[4], const int4& c, bool on) {
+        to[0] += on ? c.x : 0;
+        to[1] += on ? c.y : 0;
+        to[2] += on ? c.z : 0;
+        to[3] += on ? c.w : 0;
+      };
       if (4 * quad < digits) {
-        int4 all = make_int4(0, 0, 0, 0), early = make_int4(0, 0, 0, 0);
-        auto add = [](int4& to, const int4& c, bool on) {
-          to.x += on ? c.x : 0;
-          to.y += on ? c.y : 0;
-          to.z += on ? c.z : 0;
-          to.w += on ? c.w : 0;
-        };
 #pragma unroll 4
         for (int g = part; g < n_groups; g += kParts) {
           const int4 c = __ldcg(reinterpret_cast<const int4*>(groups + static_cast<int64_t>(g) * digits + 4 * quad));
@@ -308,16 +368,26 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
 #pragma unroll 2
         for (int b = my_group * kGroup + part; b < me; b += kParts)
           add(early, __ldcg(reinterpret_cast<const int4*>(a.counts + static_cast<int64_t>(b) * digits + 4 * quad)), true);
-        *reinterpret_cast<int4*>(&sums[part][4 * quad]) = all;
-        *reinterpret_cast<int4*>(&priors[part][4 * quad]) = early;
+      }
+#pragma unroll
+      for (int o = 1; o < kParts; o <<= 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          all[j] += __shfl_xor_sync(0xffffffffu, all[j], o);
+          early[j] += __shfl_xor_sync(0xffffffffu, early[j], o);
+        }
+      __syncthreads();  // (half may still be read as this round's counts)
+      if (part == 0 && 4 * quad < digits) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          half[4 * quad + j] = all[j];
+          place[4 * quad + j] = early[j];
+        }
       }
       __syncthreads();
       if (tid < digits) {
-#pragma unroll
-        for (int k = 0; k < kParts; ++k) {
-          total += sums[k][tid];
-          prior += priors[k][tid];
-        }
+        total = half[tid];
+        prior = place[tid];
       }
     } else if (tid < digits) {
       total = place[tid];
@@ -335,103 +405,51 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
       for (int w = 0; w < warp; ++w) x += warp_sum[w];
       place[tid] = x - total + prior;
     }
+    __syncthreads();
 
-    for (int32_t r0 = e0; r0 < e1; r0 += kRound) {
-      Entry entry[kItems];
-      int rank[kItems];
-      const int32_t at = r0 + warp * (32 * kItems) + lane;  // (below 2^31 where it is used: see `in`)
-      for (int d = lane; d < digits; d += 32) hist[warp][d] = 0;
-#pragma unroll
-      for (int k = 0; k < kItems; ++k) {
-        const bool in = static_cast<int64_t>(r0) + warp * (32 * kItems) + lane + 32 * k < e1;
-        entry[k] = in ? entry_at(at + 32 * k) : Entry{0u, 0};
+    if (one_round) {
+      put(e0);
+    } else {
+      for (int32_t r0 = e0; r0 < e1; r0 += kRound) {
+        take(r0);
+        put(r0);
+        __syncthreads();
+        if (tid < digits) place[tid] += half[tid];
+        __syncthreads();
       }
-      __syncwarp();
-#pragma unroll
-      for (int k = 0; k < kItems; ++k) {
-        const bool in = static_cast<int64_t>(r0) + warp * (32 * kItems) + lane + 32 * k < e1;
-        const uint32_t d = digit_of(entry[k].key);
-        uint32_t peers = __ballot_sync(0xffffffffu, in);  // the lanes with the same digit, bit by bit
-#pragma unroll
-        for (int bit = 0; bit < kDigitBits; ++bit) {
-          const bool one = d >> bit & 1u;
-          const uint32_t ones = __ballot_sync(0xffffffffu, one);
-          peers &= one ? ones : ~ones;
-        }
-        const int before = in ? hist[warp][d] : 0;
-        rank[k] = before + __popc(peers & ((1u << lane) - 1u));
-        __syncwarp();
-        if (in && (peers >> lane) == 1u) hist[warp][d] = static_cast<uint16_t>(before + __popc(peers));  // the highest lane
-        __syncwarp();
-      }
-      __syncthreads();
-      if (tid < digits) {  // entries of this round in earlier warps
-        int c[kSortWarps], run = 0;
-#pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) c[w] = hist[w][tid];
-#pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) {
-          hist[w][tid] = static_cast<uint16_t>(run);
-          run += c[w];
-        }
-        half[tid] = run;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < kItems; ++k) {
-        if (static_cast<int64_t>(r0) + warp * (32 * kItems) + lane + 32 * k < e1) {
-          const uint32_t d = digit_of(entry[k].key);
-          const int32_t to = place[d] + hist[warp][d] + rank[k];
-          __stcg(reinterpret_cast<uint2*>(out_list + to), make_uint2(entry[k].key, static_cast<uint32_t>(entry[k].idx)));
-        }
-      }
-      __syncthreads();
-      if (tid < digits) place[tid] += half[tid];
-      __syncthreads();
     }
+    if (bad && a.status != nullptr) atomicOr(a.status, ENGRAM_ST_BAD_ROW);
     if (!meet(a, met)) return;
   }
   if (a.base == nullptr) return;
 
-  // segments that begin in each chunk, summed up over the chunks before it
+  // segments that begin in each chunk, summed up over the chunks before it of
+  // this block's; the blocks' own sums are left to those who read them
   const uint32_t none = static_cast<uint32_t>(a.total_rows);
   const Entry* list = a.list[(a.passes - 1) & 1];
-  const int32_t cper = (a.chunks + blocks - 1) / blocks;
-  const int32_t c0 = a.chunks < static_cast<int64_t>(me) * cper ? a.chunks : me * cper;
-  const int32_t c1 = a.chunks - c0 < cper ? a.chunks : c0 + cper;
-  if (tid == 0) half[0] = 0;
-  __syncthreads();
-  for (int32_t c = c0 + warp; c < c1; c += kSortWarps) {
-    int32_t heads = 0;
-    for (int k = 0; k < a.chunk; k += 32)
-      heads += __popc(__ballot_sync(0xffffffffu, k + lane < a.chunk &&
-                                                     is_head(list, static_cast<int64_t>(c) * a.chunk + k + lane, a.n, none)));
-    if (lane == 0) {
-      __stcg(a.base + c, heads);
-      atomicAdd(&half[0], heads);
-    }
-  }
-  __syncthreads();
-  if (tid == 0) __stcg(a.counts + me, half[0]);
-  if (!meet(a, met)) return;
-  int32_t before = 0, all = 0;
-  for (int b = lane; b < blocks; b += 32) {
-    const int32_t c = __ldcg(a.counts + b);
-    all += c;
-    before += b < me ? c : 0;
-  }
-  before = __reduce_add_sync(0xffffffffu, before);
-  all = __reduce_add_sync(0xffffffffu, all);
-  if (me == 0 && tid == 0) *a.count = all;
+  const int32_t c0 = a.chunks < static_cast<int64_t>(me) * a.chunks_per ? a.chunks : me * a.chunks_per;
+  const int32_t c1 = a.chunks - c0 < a.chunks_per ? a.chunks : c0 + a.chunks_per;
+  int32_t before = 0;
   for (int32_t r0 = c0; r0 < c1; r0 += kSortThreads) {  // (uniform over the block)
-    const int32_t c = r0 + tid, own = c < c1 ? __ldcg(a.base + c) : 0;
+    __syncthreads();
+    place[tid & (kMaxDigits - 1)] = half[tid & (kMaxDigits - 1)] = 0;  // heads of the round's chunks
+    __syncthreads();
+    int32_t* heads_of = tid < kMaxDigits ? place : half;  // the thread's own
+    for (int32_t c = r0 + warp; c < c1 && c < r0 + kSortThreads; c += kSortWarps) {
+      int32_t heads = 0;
+      for (int k = 0; k < a.chunk; k += 32)
+        heads += __popc(__ballot_sync(0xffffffffu, k + lane < a.chunk &&
+                                                       is_head(list, static_cast<int64_t>(c) * a.chunk + k + lane, a.n, none)));
+      if (lane == 0) (c - r0 < kMaxDigits ? place : half)[(c - r0) & (kMaxDigits - 1)] = heads;
+    }
+    __syncthreads();
+    const int32_t c = r0 + tid, own = heads_of[tid & (kMaxDigits - 1)];
     int32_t x = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    __syncthreads();
     if (lane == 31) warp_sum[warp] = x;
     __syncthreads();
     int32_t whole = 0;
@@ -442,6 +460,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
     if (c < c1) a.base[c] = before + x - own;
     before += whole;
   }
+  if (tid == 0) a.heads[me] = before;
 }
 
 // ------------------------------------------------------- segments of equal id
@@ -529,8 +548,10 @@ struct SumArgs {
   const Entry* list;
   uint32_t none;
   bool dense, contiguous;
-  const int32_t* base;   // rows form: segments before each chunk
-  const int32_t* count;  // rows form
+  const int32_t* base;   // rows form: see SortArgs
+  const int32_t* heads;
+  int32_t chunks_per, heads_count;
+  int32_t* count;        // rows form: all segments
   int64_t total_rows;    // dense form
   int32_t range;         // dense form: rows that a block clears at a time
   float* grad;
@@ -539,6 +560,28 @@ struct SumArgs {
   int32_t* next;         // [0] next task, [1] next rows to clear (zeroed by the sort)
 };
 
+// before[b]: segments that begin in the chunks of the sort's blocks before b, and
+// last all of them; filled by the block's first warp.
+constexpr int kMaxSortBlocks = 256;  // one per SM
+template <class E>
+__device__ __forceinline__ void sum_heads(const SumArgs<E>& a, int32_t (&before)[kMaxSortBlocks + 1]) {
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x >= 32) return;
+  int32_t run = 0;
+  for (int b0 = 0; b0 < a.heads_count; b0 += 32) {
+    const int32_t c = b0 + lane < a.heads_count ? a.heads[b0 + lane] : 0;
+    int32_t x = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (b0 + lane < a.heads_count) before[b0 + lane] = run + x - c;
+    run += __shfl_sync(0xffffffffu, x, 31);
+  }
+  if (lane == 0) before[a.heads_count] = run;
+}
+
 template <class E>
 __device__ __forceinline__ const typename E::T* entry_row(const SumArgs<E>& a, int32_t i) {
   if (a.contiguous) return a.dout + static_cast<int64_t>(i) * a.dim;
@@ -546,14 +589,16 @@ __device__ __forceinline__ const typename E::T* entry_row(const SumArgs<E>& a, i
   return a.dout + t * a.dout_stride + static_cast<int64_t>(i - t * a.n_cols) * a.dim;
 }
 
+// count floats from row on, by a warp: 16 bytes a lane from the first 16-byte
+// boundary to the last
 __device__ __forceinline__ void zero_rows(float* row, int64_t count, int lane) {
-  if ((reinterpret_cast<uintptr_t>(row) & 15) == 0 && count % 4 == 0) {
+  const int64_t head = (4 - (reinterpret_cast<uintptr_t>(row) / 4 & 3)) & 3;
+  const int64_t c0 = head < count ? head : count, c1 = c0 + (count - c0) / 4 * 4;
+  if (lane < c0) row[lane] = 0.f;
 #pragma unroll 4
-    for (int64_t c = lane * 4; c < count; c += 128)
-      __stcs(reinterpret_cast<float4*>(row + c), make_float4(0.f, 0.f, 0.f, 0.f));
-  } else {
-    for (int64_t c = lane; c < count; c += 32) row[c] = 0.f;
-  }
+  for (int64_t c = c0 + lane * 4; c < c1; c += 128)
+    __stcs(reinterpret_cast<float4*>(row + c), make_float4(0.f, 0.f, 0.f, 0.f));
+  if (c1 + lane < count) row[c1 + lane] = 0.f;
 }
 
 // kLanes lanes handle one (chunk, tile of kLanes * kCols columns) at a time,
@@ -562,10 +607,15 @@ __device__ __forceinline__ void zero_rows(float* row, int64_t count, int lane) {
 // the results.
 template <class E, int kLanes, bool kAligned>
 __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
-  constexpr int N = kCols<E>, kGroups = 32 / kLanes, kAhead = kAligned ? 8 : 4;
+  constexpr int N = kCols<E>, kGroups = 32 / kLanes, kAhead = 8;
   const int wl = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lane = threadIdx.x % kLanes;
   const int64_t tasks = static_cast<int64_t>(a.chunks) * a.tiles;
+  __shared__ int32_t before[kMaxSortBlocks + 1];
+  if (!a.dense) {
+    sum_heads(a, before);
+    __syncthreads();
+  }
   while (true) {
     int32_t got = 0;
     if (wl == 0) got = atomicAdd(a.next, 1);
@@ -579,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
     uint32_t key = a.list[e0].key;
     if (key == a.none) continue;  // sorted: none of the chunk's entries has a row
     bool from_before = e0 > 0 && a.list[e0 - 1].key == key;
-    int32_t seg = a.dense ? 0 : a.base[chunk];
+    int32_t seg = a.dense ? 0 : a.base[chunk] + before[chunk / a.chunks_per];
     if (from_before) --seg;
     float acc[N];
 #pragma unroll
@@ -626,7 +676,8 @@ __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
   }
 
   if (!a.dense) {
-    const int32_t segs = *a.count;
+    const int32_t segs = before[a.heads_count];
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.count = segs;
     constexpr int kRows = 16;  // a warp's share at a time
     while (true) {
       int32_t got = 0;
@@ -651,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
     __syncthreads();
     const int64_t r0 = static_cast<int64_t>(taken) * kRange;
     if (r0 >= a.total_rows) break;
-    if (threadIdx.x < kRange / 32) named[threadIdx.x] = 0u;
+    if (threadIdx.x < kMaxRange / 32) named[threadIdx.x] = 0u;
     if (warp == 0) {  // the first entry of row r0 or a later one, 32 probes at a time
       int32_t lo = 0, hi = a.n;
       while (hi > lo) {
@@ -720,6 +771,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) seg_join_kernel(SumArgs<E> a)
         for (int j = 0; j < N; ++j) acc[j] += q[b][j];
     }
   };
+  __shared__ int32_t before[kMaxSortBlocks + 1];
+  if (!a.dense) {
+    sum_heads(a, before);
+    __syncthreads();
+  }
   int32_t mine = 0, seg = 0;
   if (chunk < a.chunks - 1) {
     const uint32_t key = a.list[e1 - 1].key;
@@ -741,7 +797,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) seg_join_kernel(SumArgs<E> a)
         for (int k = 0; k < a.chunk; k += 32)
           heads += __popc(__ballot_sync(0xffffffffu, k + lane < a.chunk && is_head(a.list, static_cast<int64_t>(e0) + k + lane,
                                                                                    a.n, a.none)));
-        seg = a.base[chunk] + heads - 1;
+        seg = a.base[chunk] + before[chunk / a.chunks_per] + heads - 1;
       }
     }
   }
@@ -797,13 +853,12 @@ struct GradSpace {
   int32_t* base;
   int32_t* counts;
   int32_t* barrier;  // then the group sums
-  int32_t* count;
+  int32_t* heads;
   int32_t* next;
   float *head, *tail;
   size_t bytes;
 };
 
-constexpr int kMaxSortBlocks = 256;  // one per SM
 constexpr int kMaxGroups = (kMaxSortBlocks + kGroup - 1) / kGroup, kMaxPasses = 4;
 
 // Entries per chunk: the fewest of 16, 32, 64 and 128 that give no more tasks
@@ -830,7 +885,7 @@ GradSpace grad_space(void* at, int64_t n, int32_t dim) {
   const int32_t fewest = chunk_for(n, dim, kCols<train::Bf16>);  // serves both types: fp32 has more tiles
   const size_t chunks = static_cast<size_t>((n + fewest - 1) / fewest);
   s.barrier = reinterpret_cast<int32_t*>(take((4 + static_cast<size_t>(kMaxPasses) * kMaxGroups * kMaxDigits) * 4));
-  s.count = reinterpret_cast<int32_t*>(take(4));
+  s.heads = reinterpret_cast<int32_t*>(take(kMaxSortBlocks * 4));
   s.next = reinterpret_cast<int32_t*>(take(8));
   for (int k = 0; k < 2; ++k) s.list[k] = reinterpret_cast<Entry*>(take(static_cast<size_t>(n) * sizeof(Entry)));
   s.base = reinterpret_cast<int32_t*>(take(chunks * 4));
@@ -911,7 +966,7 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
   sa.chunk = chunk;
   sa.chunks = chunks;
   sa.base = dense ? nullptr : w.base;
-  sa.count = dense ? w.count : count_d;
+  sa.heads = w.heads;
   sa.next = w.next;
   sa.status = status_d;
   // one block up to a round of entries; more blocks (at least 1024 entries
@@ -922,6 +977,7 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
     if (n / 1024 < blocks) blocks = n / 1024;
   }
   sa.per = (n + blocks - 1) / blocks;
+  sa.chunks_per = (chunks + blocks - 1) / blocks;
   if (blocks > 1) {
     const size_t zeroed = 4 + static_cast<size_t>(sa.passes) * ((blocks + kGroup - 1) / kGroup) * (1 << sa.bits);
     cudaError_t err = cudaMemsetAsync(w.barrier, 0, zeroed * 4, st);
@@ -955,11 +1011,15 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
     a.dense = dense;
     a.contiguous = dout_stride == static_cast<int64_t>(n_cols) * row_dim;
     a.base = w.base;
+    a.heads = w.heads;
+    a.heads_count = blocks;
+    a.chunks_per = sa.chunks_per;
     a.count = count_d;
     a.total_rows = total_rows;
-    // about 64 KB of them: enough to hide the search, little enough to spread over the SMs
-    a.range = (1 << 14) / row_dim / 32 * 32;
-    a.range = a.range < 32 ? 32 : a.range > kMaxRange ? kMaxRange : a.range;
+    // 64 KB at least, to hide the search, and no more ranges than needed to spread over the SMs
+    const int64_t spread = total_rows / (static_cast<int64_t>(sms) * 32), bytes = (1 << 14) / row_dim;
+    const int64_t range = spread > bytes ? spread : bytes;
+    a.range = static_cast<int32_t>(range < 1 ? 1 : range > kMaxRange ? kMaxRange : range);
     a.grad = grad_d;
     a.rows = rows_d;
     a.head = w.head;

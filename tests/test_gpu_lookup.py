@@ -145,6 +145,28 @@ def test_gradient_of_long_and_short_segments(T, R, how):
         assert (np.abs(dense - want) <= bound).all()
 
 
+@pytest.mark.parametrize("T,D,R", [(3, 5120, 500), (40, 4299, 700), (700, 257, 5000), (2000, 8, 90000), (9000, 1000, 4000),
+                                   (1, 1, 3), (5000, 6, 6)])
+def test_every_row_of_the_outputs_is_written(T, D, R):
+    """Outputs that hold something else before: rows that no entry names become zeros, with none left out."""
+    rng = np.random.default_rng(31)
+    ids = rng.integers(-1, R, size=T).astype(np.int32)
+    ids[rng.random(T) < 0.3] = ids[0]
+    dout = make((T, D), "bf16", 32)
+    ref, err, uniq = OT.lookup_grad(dout.double().cpu().numpy(), ids[:, None], R, 1.0)
+    grad = torch.full((R, D), float("nan"), device=DEV)
+    eg.engram_lookup_grad(dout, i32(ids), R, 1.0, grad=grad)
+    assert (np.abs(grad.double().cpu().numpy() - ref) <= err).all()
+    rows = torch.full((T,), 12345, dtype=torch.int32, device=DEV)
+    grad = torch.full((T, D), float("nan"), device=DEV)
+    count = torch.full((1,), -5, dtype=torch.int32, device=DEV)
+    eg.engram_lookup_grad_rows(dout, i32(ids), R, 1.0, rows=rows, grad=grad, count=count)
+    m = len(uniq)
+    assert int(count.item()) == m and (rows[:m].cpu().numpy() == uniq).all() and (rows[m:] == -1).all()
+    g = grad.double().cpu().numpy()
+    assert (np.abs(g[:m] - ref[uniq]) <= err[uniq]).all() and (g[m:] == 0).all()
+
+
 def test_gradient_is_the_same_from_run_to_run():
     ids = i32(ids_of(5000, 4, 300, 11))
     dout = make((5000, 4 * 48), "bf16", 12)
