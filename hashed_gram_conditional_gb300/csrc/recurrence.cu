@@ -106,6 +106,7 @@ struct Args {
   int64_t n_slots;
   float* carry;
   int32_t n_tokens, dim, n_tiles, n_groups;
+  bool move_empty;  // the states of empty sequences go from state to state_out
   uint8_t* flags;   // [n_tokens], see mark_kernel
   int32_t* slot;    // [n_tokens]: the state slot of a first or last position
   int32_t* ticket;  // [0] next block number, [1] a wait ran out
@@ -263,39 +264,83 @@ constexpr uint32_t kNotYet = 0xffffffffu;
 
 constexpr int kLive = 1, kFirst = 2, kLast = 4;
 
-// flags[t]: kLive where the position counts (not masked, not in a padding
-// sequence), kFirst / kLast where a sequence begins / ends, whose slot (-1:
-// padding) is then in slot[t].  Also readies the counters and the tiles' words
-// (`cleared` 16-byte vectors) and moves the states of empty sequences.
+// kLive where position t counts (not masked, not in a padding sequence), kFirst /
+// kLast where a sequence begins / ends; `slot`: the sequence's (-1: padding).
 template <class E>
-__global__ void __launch_bounds__(256) mark_kernel(Args<E> a, uint4* words, int64_t cleared, bool move_empty) {
+__device__ __forceinline__ int mark_position(const Args<E>& a, int64_t t, int32_t& slot) {
+  int64_t lo = 0, hi = a.n_seqs;  // the last sequence with cu <= t
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    if (a.cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  slot = slot_of(a, lo);
+  const bool live = slot >= 0 && (a.mask == nullptr || a.mask[t] == 0);
+  return (live ? kLive : 0) | (a.cu[lo] == t ? kFirst : 0) | (a.cu[lo + 1] == t + 1 ? kLast : 0);
+}
+
+// The states of empty sequences move on unchanged: channels d0, d0 + 256, ...
+// below d1, sequences q0, q0 + step, ...
+template <class E>
+__device__ __forceinline__ void move_states(const Args<E>& a, int64_t q0, int64_t step, int d0, int d1, int threads) {
+  for (int64_t q = q0; q < a.n_seqs; q += step) {
+    if (a.cu[q] != a.cu[q + 1]) continue;
+    const int32_t slot = slot_of(a, q);
+    for (int d = d0 + threadIdx.x; slot >= 0 && d < d1; d += threads)
+      a.state_out[static_cast<int64_t>(slot) * a.dim + d] =
+          a.state != nullptr ? a.state[static_cast<int64_t>(slot) * a.dim + d] : 0.f;
+  }
+}
+
+// Marks every position for the scan (flags[t], and slot[t] where a sequence
+// begins or ends), readies the counters and the tiles' words (`cleared` 16-byte
+// vectors) and moves the states of empty sequences.  A scan of one tile does
+// without it: its blocks mark the positions themselves.
+template <class E>
+__global__ void __launch_bounds__(256) mark_kernel(Args<E> a, uint4* words, int64_t cleared) {
   allow_dependent_launch();
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, step = static_cast<int64_t>(gridDim.x) * 256;
   if (i0 < 2 && cleared > 0) a.ticket[i0] = 0;
 #pragma unroll 4
   for (int64_t i = i0; i < cleared; i += step) words[i] = make_uint4(kNotYet, kNotYet, kNotYet, kNotYet);
   for (int64_t t = i0; t < a.n_tokens; t += step) {
-    int64_t lo = 0, hi = a.n_seqs;  // the last sequence with cu <= t
-    while (hi - lo > 1) {
-      const int64_t mid = (lo + hi) / 2;
-      if (a.cu[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    const int32_t slot = slot_of(a, lo);
-    const bool first = a.cu[lo] == t, last = a.cu[lo + 1] == t + 1;
-    const bool live = slot >= 0 && (a.mask == nullptr || a.mask[t] == 0);
-    a.flags[t] = static_cast<uint8_t>((live ? kLive : 0) | (first ? kFirst : 0) | (last ? kLast : 0));
-    if (first || last) a.slot[t] = slot;
+    int32_t slot;
+    const int f = mark_position(a, t, slot);
+    a.flags[t] = static_cast<uint8_t>(f);
+    if (f & (kFirst | kLast)) a.slot[t] = slot;
   }
-  if (move_empty) {
-    for (int64_t q = blockIdx.x; q < a.n_seqs; q += gridDim.x) {
-      if (a.cu[q] != a.cu[q + 1]) continue;
-      const int32_t slot = slot_of(a, q);
-      for (int d = threadIdx.x; slot >= 0 && d < a.dim; d += 256)
-        a.state_out[static_cast<int64_t>(slot) * a.dim + d] =
-            a.state != nullptr ? a.state[static_cast<int64_t>(slot) * a.dim + d] : 0.f;
-    }
+  if (a.move_empty) move_states(a, blockIdx.x, gridDim.x, 0, a.dim, 256);
+}
+
+// What a block needs before its tile: its number in walking order, and the
+// positions' marks, from memory or, where the scan is one tile, made here.
+template <int kLen>
+struct Start {
+  uint32_t cuts;  // a bit per warp in which a sequence begins
+  int32_t number;
+  uint8_t flags[kLen];
+  int32_t slot[kLen];
+};
+template <class E, int kLen>
+__device__ __forceinline__ int begin_tile(Args<E>& a, Start<kLen>& s, int threads) {
+  if (threadIdx.x == 0) s.cuts = 0u;
+  if (a.n_tiles > 1) {
+    wait_prior_grids();
+    if (threadIdx.x == 0) s.number = atomicAdd(a.ticket, 1);
+    __syncthreads();
+    return s.number;
   }
+  for (int t = threadIdx.x; t < a.n_tokens; t += threads) {
+    int32_t slot;
+    s.flags[t] = static_cast<uint8_t>(mark_position(a, t, slot));
+    s.slot[t] = slot;
+  }
+  const int d0 = static_cast<int>(blockIdx.x) * kGroup<E>;
+  if (a.move_empty) move_states(a, 0, 1, d0, d0 + kGroup<E> < a.dim ? d0 + kGroup<E> : a.dim, threads);
+  __syncthreads();
+  a.flags = s.flags;
+  a.slot = s.slot;
+  return static_cast<int>(blockIdx.x);
 }
 
 // A position that does not count is given g = +inf, x = 0 (and dy = 0) in shared
@@ -491,16 +536,6 @@ __device__ __forceinline__ float come_in(const Args<E>& a, int group, int pos, i
   return v;
 }
 
-// The block's number in walking order; also clears the tile's mask.
-__device__ __forceinline__ int take_ticket(int32_t* ticket, int32_t* shared, uint32_t* cuts) {
-  if (threadIdx.x == 0) {
-    *shared = atomicAdd(ticket, 1);
-    *cuts = 0u;
-  }
-  __syncthreads();
-  return *shared;
-}
-
 // --------------------------------------------------------------------- forward
 
 // A block handles kFwdTile positions of one group of channels, in one
@@ -525,11 +560,10 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 3) forward_kernel(Args<E> a) {
   unsigned char* gs = xs + kTile * kRowBytes;
   float(*mapA)[G] = reinterpret_cast<float(*)[G]>(gs + kTile * kRowBytes);
   float(*mapB)[G] = mapA + kWarps;
-  __shared__ uint32_t cuts;  // a bit per warp in which a sequence begins
-  __shared__ int32_t number;
+  __shared__ Start<kTile> start;
+  uint32_t& cuts = start.cuts;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  wait_prior_grids();
-  const int n = take_ticket(a.ticket, &number, &cuts);
+  const int n = begin_tile(a, start, kWarps * 32);
   const int tile = n / a.n_groups, group = n - tile * a.n_groups;
   const int c0 = group * G, c = c0 + lane * V;
   const int t0 = tile * kTile, tw = t0 + warp * kSteps;
@@ -683,11 +717,10 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) backward_kernel(Args<E> a) 
   // the gradient of the last state of the sequence that ends here and began
   // before this warp, whose first state's gradient may be written in its place
   float(*held)[G] = mapC + kWarps;
-  __shared__ uint32_t cuts;  // a bit per warp in which a sequence begins
-  __shared__ int32_t number;
+  __shared__ Start<kTile> start;
+  uint32_t& cuts = start.cuts;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  wait_prior_grids();
-  const int n = take_ticket(a.ticket, &number, &cuts);
+  const int n = begin_tile(a, start, kWarps * 32);
   const int back = n / a.n_groups, group = n - back * a.n_groups;
   const int tile = a.n_tiles - 1 - back;
   const int c0 = group * G, c = c0 + lane * V;
@@ -978,7 +1011,7 @@ int launch_pass(const Args<E>& a, bool backward, int grid, cudaStream_t st) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // launched while the marks are made
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = a.n_tiles > 1 ? 1 : 0;
   const int smem = backward ? kBwdSmem<E> : kFwdSmem<E>;
   static std::atomic<uint64_t> attr_set[2] = {{0}, {0}};  // one bit per device: the shared-memory opt-in was made
   int dev = 0;
@@ -1008,18 +1041,19 @@ int launch_scan(Args<E>& a, bool backward, void* workspace, int sms, cudaStream_
   a.slot = w.slot;
   const int64_t blocks = static_cast<int64_t>(a.n_tiles) * a.n_groups;
   if (blocks > 0x7fffff00) return fail(ENGRAM_E_RANGE, "too many positions times channels");
-  const bool move_empty = !backward && a.state_out != nullptr && a.state_out != a.state;
+  a.move_empty = !backward && a.state_out != nullptr && a.state_out != a.state;
   a.n_runs = (a.n_tiles + kRun - 1) / kRun;
   const int64_t tile_words = blocks * kGroup<E>, run_words = static_cast<int64_t>(a.n_runs) * a.n_groups * kGroup<E>;
   a.map = reinterpret_cast<float2*>(w.words);
   a.run_map = a.map + tile_words;
   a.run_value = reinterpret_cast<float*>(a.run_map + run_words);
   const int64_t cleared = (2 * tile_words + 3 * run_words) / 4;  // kGroup is a multiple of 4
-  const int64_t want = ((a.n_tokens > cleared ? a.n_tokens : cleared) + 255) / 256, cap = static_cast<int64_t>(sms) * 8;
-  mark_kernel<E><<<static_cast<int>(want < cap ? want : cap), 256, 0, st>>>(a, reinterpret_cast<uint4*>(w.words), cleared,
-                                                                          move_empty);
-  int rc = check_launch("mark_kernel");
-  if (rc) return rc;
+  if (a.n_tiles > 1) {
+    const int64_t want = ((a.n_tokens > cleared ? a.n_tokens : cleared) + 255) / 256, cap = static_cast<int64_t>(sms) * 8;
+    mark_kernel<E><<<static_cast<int>(want < cap ? want : cap), 256, 0, st>>>(a, reinterpret_cast<uint4*>(w.words), cleared);
+    int rc = check_launch("mark_kernel");
+    if (rc) return rc;
+  }
   bool vec = a.dim * E::kBytes % 16 == 0 && rows16<E>(a.x, a.x_stride) && rows16<E>(a.g, a.g_stride);
   if (!backward) vec = vec && rows16<E>(a.y, a.y_stride);
   else vec = vec && rows16<E>(a.dy, a.dy_stride) && rows16<E>(a.dx, a.dx_stride) && rows16<E>(a.dg, a.dg_stride);
@@ -1097,7 +1131,8 @@ extern "C" int engram_recurrence(const void* x_d, int64_t x_stride, const void* 
     if (n_tokens > 0) return launch_scan<E>(a, false, workspace_d, sms, as_stream(stream));
     if (state_out_d == nullptr || state_out_d == state_d) return static_cast<int>(ENGRAM_OK);
     const int64_t cap = static_cast<int64_t>(sms) * 4;
-    mark_kernel<E><<<static_cast<int>(n_seqs < cap ? n_seqs : cap), 256, 0, as_stream(stream)>>>(a, nullptr, 0, true);
+    a.move_empty = true;
+    mark_kernel<E><<<static_cast<int>(n_seqs < cap ? n_seqs : cap), 256, 0, as_stream(stream)>>>(a, nullptr, 0);
     return check_launch("mark_kernel");
   };
   return type == ENGRAM_T_BF16 ? go(train::Bf16{}) : go(train::F32{});
