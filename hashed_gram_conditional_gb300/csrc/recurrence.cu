@@ -313,34 +313,34 @@ __global__ void __launch_bounds__(256) mark_kernel(Args<E> a, uint4* words, int6
 }
 
 // What a block needs before its tile: its number in walking order, and the
-// positions' marks, from memory or, where the scan is one tile, made here.
+// positions' marks, from memory or, where the scan is one tile (kAlone), made
+// here.
 template <int kLen>
 struct Start {
   uint32_t cuts;  // a bit per warp in which a sequence begins
   int32_t number;
-  uint8_t flags[kLen];
-  int32_t slot[kLen];
+  uint8_t flags[kLen > 0 ? kLen : 1];
+  int32_t slot[kLen > 0 ? kLen : 1];
 };
-template <class E, int kLen>
-__device__ __forceinline__ int begin_tile(Args<E>& a, Start<kLen>& s, int threads) {
+template <bool kAlone, class E, int kLen>
+__device__ __forceinline__ int begin_tile(const Args<E>& a, Start<kLen>& s, int threads) {
   if (threadIdx.x == 0) s.cuts = 0u;
-  if (a.n_tiles > 1) {
+  if constexpr (!kAlone) {
     wait_prior_grids();
     if (threadIdx.x == 0) s.number = atomicAdd(a.ticket, 1);
     __syncthreads();
     return s.number;
+  } else {
+    for (int t = threadIdx.x; t < a.n_tokens; t += threads) {
+      int32_t slot;
+      s.flags[t] = static_cast<uint8_t>(mark_position(a, t, slot));
+      s.slot[t] = slot;
+    }
+    const int d0 = static_cast<int>(blockIdx.x) * kGroup<E>;
+    if (a.move_empty) move_states(a, 0, 1, d0, d0 + kGroup<E> < a.dim ? d0 + kGroup<E> : a.dim, threads);
+    __syncthreads();
+    return static_cast<int>(blockIdx.x);
   }
-  for (int t = threadIdx.x; t < a.n_tokens; t += threads) {
-    int32_t slot;
-    s.flags[t] = static_cast<uint8_t>(mark_position(a, t, slot));
-    s.slot[t] = slot;
-  }
-  const int d0 = static_cast<int>(blockIdx.x) * kGroup<E>;
-  if (a.move_empty) move_states(a, 0, 1, d0, d0 + kGroup<E> < a.dim ? d0 + kGroup<E> : a.dim, threads);
-  __syncthreads();
-  a.flags = s.flags;
-  a.slot = s.slot;
-  return static_cast<int>(blockIdx.x);
 }
 
 // A position that does not count is given g = +inf, x = 0 (and dy = 0) in shared
@@ -356,9 +356,9 @@ __device__ __forceinline__ void put_neutral(unsigned char* g, unsigned char* x, 
 struct Marks {
   uint32_t live, first, last;
 };
-template <class E, int kSteps>
-__device__ __forceinline__ Marks marks_of(const Args<E>& a, int t, int lane) {
-  const int f = lane < kSteps && t + lane < a.n_tokens ? a.flags[t + lane] : 0;
+template <int kSteps>
+__device__ __forceinline__ Marks marks_of(const uint8_t* flags, int n_tokens, int t, int lane) {
+  const int f = lane < kSteps && t + lane < n_tokens ? flags[t + lane] : 0;
   Marks m;
   m.live = __ballot_sync(kFull, f & kLive);
   m.first = __ballot_sync(kFull, f & kFirst);
@@ -551,8 +551,8 @@ static_assert(kFwdTile % kBwdTile == 0, "saved states fall between a forward til
 
 constexpr int kFwdWarps = 8;
 
-template <class E, bool kVec>
-__global__ void __launch_bounds__(kFwdWarps * 32, 3) forward_kernel(Args<E> a) {
+template <class E, bool kVec, bool kAlone>
+__global__ void __launch_bounds__(kFwdWarps * 32, 3) forward_kernel(const Args<E> a) {
   constexpr int kWarps = kFwdWarps, kTile = kFwdTile, kSteps = kTile / kWarps;
   constexpr int V = kLaneCh<E>, G = kGroup<E>;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -560,10 +560,12 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 3) forward_kernel(Args<E> a) {
   unsigned char* gs = xs + kTile * kRowBytes;
   float(*mapA)[G] = reinterpret_cast<float(*)[G]>(gs + kTile * kRowBytes);
   float(*mapB)[G] = mapA + kWarps;
-  __shared__ Start<kTile> start;
+  __shared__ Start<kAlone ? kTile : 0> start;
   uint32_t& cuts = start.cuts;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = begin_tile(a, start, kWarps * 32);
+  const int n = begin_tile<kAlone>(a, start, kWarps * 32);
+  const uint8_t* flags = kAlone ? start.flags : a.flags;
+  const int32_t* slots = kAlone ? start.slot : a.slot;
   const int tile = n / a.n_groups, group = n - tile * a.n_groups;
   const int c0 = group * G, c = c0 + lane * V;
   const int t0 = tile * kTile, tw = t0 + warp * kSteps;
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 3) forward_kernel(Args<E> a) {
   unsigned char* gw = gs + warp * kSteps * kRowBytes;
   fetch_rows<E, kVec, kSteps>(gw, a.g, a.g_stride, tw, a.n_tokens, c0, a.dim, lane);
   fetch_rows<E, kVec, kSteps>(xw, a.x, a.x_stride, tw, a.n_tokens, c0, a.dim, lane);
-  const Marks mk = marks_of<E, kSteps>(a, tw, lane);
+  const Marks mk = marks_of<kSteps>(flags, a.n_tokens, tw, lane);
   wait_rows();
 
   constexpr uint32_t kAll = (1u << kSteps) - 1u;
@@ -590,7 +592,7 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 3) forward_kernel(Args<E> a) {
   auto begin = [&](int k) {
 #pragma unroll
     for (int j = 0; j < V; ++j) s[j] = 0.f;
-    const int32_t slot = a.slot[tw + k];
+    const int32_t slot = slots[tw + k];
     if (slot >= 0 && a.state != nullptr) load_state<E>(a.state + static_cast<int64_t>(slot) * a.dim, c, a.dim, s);
   };
   // Where the states are updated in place, the warp that holds a sequence's
@@ -678,7 +680,7 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 3) forward_kernel(Args<E> a) {
       for (int j = 0; j < V; ++j) out[j] = mk.live >> k & 1u ? s[j] : 0.f;
       store_row<E, kVec>(y + k * a.y_stride, c, a.dim, out);
       if (mk.last >> k & 1u) {
-        const int32_t slot = a.slot[tw + k];
+        const int32_t slot = slots[tw + k];
         if (slot >= 0 && a.state_out != nullptr)
           store_state<E>(a.state_out + static_cast<int64_t>(slot) * a.dim, c, a.dim, s);
       }
@@ -703,8 +705,8 @@ constexpr int kFwdSmem = 2 * kFwdTile * kRowBytes + 2 * kFwdWarps * kGroup<E> * 
 // instructions than the two exponentials and the reciprocal of a pair.
 constexpr int kBwdWarps = 8;
 
-template <class E, bool kVec>
-__global__ void __launch_bounds__(kBwdWarps * 32, 3) backward_kernel(Args<E> a) {
+template <class E, bool kVec, bool kAlone>
+__global__ void __launch_bounds__(kBwdWarps * 32, 3) backward_kernel(const Args<E> a) {
   constexpr int kWarps = kBwdWarps, kTile = kBwdTile, kSteps = kTile / kWarps;
   constexpr int V = kLaneCh<E>, G = kGroup<E>;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -717,10 +719,12 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) backward_kernel(Args<E> a) 
   // the gradient of the last state of the sequence that ends here and began
   // before this warp, whose first state's gradient may be written in its place
   float(*held)[G] = mapC + kWarps;
-  __shared__ Start<kTile> start;
+  __shared__ Start<kAlone ? kTile : 0> start;
   uint32_t& cuts = start.cuts;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = begin_tile(a, start, kWarps * 32);
+  const int n = begin_tile<kAlone>(a, start, kWarps * 32);
+  const uint8_t* flags = kAlone ? start.flags : a.flags;
+  const int32_t* slots = kAlone ? start.slot : a.slot;
   const int back = n / a.n_groups, group = n - back * a.n_groups;
   const int tile = a.n_tiles - 1 - back;
   const int c0 = group * G, c = c0 + lane * V;
@@ -731,7 +735,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) backward_kernel(Args<E> a) 
   fetch_rows<E, kVec, kSteps>(gw, a.g, a.g_stride, tw, a.n_tokens, c0, a.dim, lane);
   fetch_rows<E, kVec, kSteps>(xw, a.x, a.x_stride, tw, a.n_tokens, c0, a.dim, lane);
   fetch_rows<E, kVec, kSteps>(dw, a.dy, a.dy_stride, tw, a.n_tokens, c0, a.dim, lane);
-  const Marks mk = marks_of<E, kSteps>(a, tw, lane);
+  const Marks mk = marks_of<kSteps>(flags, a.n_tokens, tw, lane);
   float carry[V];
   load_state<E>(a.carry + static_cast<int64_t>(tile) * a.dim, c, a.dim, carry);
   wait_rows();
@@ -746,7 +750,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) backward_kernel(Args<E> a) 
   auto begin = [&](int k) {
 #pragma unroll
     for (int j = 0; j < V; ++j) s[j] = 0.f;
-    const int32_t slot = a.slot[tw + k];
+    const int32_t slot = slots[tw + k];
     if (slot >= 0 && a.state != nullptr) load_state<E>(a.state + static_cast<int64_t>(slot) * a.dim, c, a.dim, s);
   };
   auto advance = [&](int k, float (&xv)[V], float (&f)[V], float (&u)[V]) {
@@ -786,7 +790,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) backward_kernel(Args<E> a) 
       if (from_before(k)) pass_back(k, f);  // nothing is passed back over a sequence's beginning
       if ((mk.last >> k & 1u) && from_before(k)) {
         float l[V] = {};
-        const int32_t slot = a.slot[tw + k];
+        const int32_t slot = slots[tw + k];
         if (slot >= 0 && a.dstate != nullptr) load_state<E>(a.dstate + static_cast<int64_t>(slot) * a.dim, c, a.dim, l);
         put_lane<E>(held[warp], lane, l);
         fma_v<V>(A, l, C, C);
@@ -886,7 +890,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) backward_kernel(Args<E> a) 
         if (from_before(k)) {
           get_lane<E>(held[warp], lane, m);
         } else {
-          const int32_t slot = a.slot[tw + k];
+          const int32_t slot = slots[tw + k];
 #pragma unroll
           for (int j = 0; j < V; ++j) m[j] = 0.f;
           if (slot >= 0 && a.dstate != nullptr) load_state<E>(a.dstate + static_cast<int64_t>(slot) * a.dim, c, a.dim, m);
@@ -894,7 +898,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 3) backward_kernel(Args<E> a) 
       }
       descend(k);
       if (mk.first >> k & 1u) {
-        const int32_t slot = a.slot[tw + k];
+        const int32_t slot = slots[tw + k];
         if (slot >= 0 && a.dstate != nullptr) store_state<E>(a.dstate + static_cast<int64_t>(slot) * a.dim, c, a.dim, m);
 #pragma unroll
         for (int j = 0; j < V; ++j) m[j] = 0.f;
@@ -1001,7 +1005,7 @@ bool rows16(const void* p, int64_t stride) {
   return aligned(p, 16) && stride * E::kBytes % 16 == 0;
 }
 
-template <class E, bool kVec>
+template <class E, bool kVec, bool kAlone>
 int launch_pass(const Args<E>& a, bool backward, int grid, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -1011,7 +1015,7 @@ int launch_pass(const Args<E>& a, bool backward, int grid, cudaStream_t st) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // launched while the marks are made
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = a.n_tiles > 1 ? 1 : 0;
+  cfg.numAttrs = kAlone ? 0 : 1;
   const int smem = backward ? kBwdSmem<E> : kFwdSmem<E>;
   static std::atomic<uint64_t> attr_set[2] = {{0}, {0}};  // one bit per device: the shared-memory opt-in was made
   int dev = 0;
@@ -1019,13 +1023,13 @@ int launch_pass(const Args<E>& a, bool backward, int grid, cudaStream_t st) {
   const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
   cudaError_t e;
   if (bit == 0 || !(attr_set[backward].load(std::memory_order_relaxed) & bit)) {
-    e = backward ? cudaFuncSetAttribute(backward_kernel<E, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
-                 : cudaFuncSetAttribute(forward_kernel<E, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = backward ? cudaFuncSetAttribute(backward_kernel<E, kVec, kAlone>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
+                 : cudaFuncSetAttribute(forward_kernel<E, kVec, kAlone>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     attr_set[backward].fetch_or(bit, std::memory_order_relaxed);
   }
   cfg.dynamicSmemBytes = smem;
-  e = backward ? cudaLaunchKernelEx(&cfg, backward_kernel<E, kVec>, a) : cudaLaunchKernelEx(&cfg, forward_kernel<E, kVec>, a);
+  e = backward ? cudaLaunchKernelEx(&cfg, backward_kernel<E, kVec, kAlone>, a) : cudaLaunchKernelEx(&cfg, forward_kernel<E, kVec, kAlone>, a);
   if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "recurrence launch: %s", cudaGetErrorString(e));
   return check_launch("recurrence");
 }
@@ -1057,8 +1061,10 @@ int launch_scan(Args<E>& a, bool backward, void* workspace, int sms, cudaStream_
   bool vec = a.dim * E::kBytes % 16 == 0 && rows16<E>(a.x, a.x_stride) && rows16<E>(a.g, a.g_stride);
   if (!backward) vec = vec && rows16<E>(a.y, a.y_stride);
   else vec = vec && rows16<E>(a.dy, a.dy_stride) && rows16<E>(a.dx, a.dx_stride) && rows16<E>(a.dg, a.dg_stride);
-  return vec ? launch_pass<E, true>(a, backward, static_cast<int>(blocks), st)
-             : launch_pass<E, false>(a, backward, static_cast<int>(blocks), st);
+  const int grid = static_cast<int>(blocks);
+  if (a.n_tiles == 1)
+    return vec ? launch_pass<E, true, true>(a, backward, grid, st) : launch_pass<E, false, true>(a, backward, grid, st);
+  return vec ? launch_pass<E, true, false>(a, backward, grid, st) : launch_pass<E, false, false>(a, backward, grid, st);
 }
 
 template <class E>
