@@ -54,6 +54,84 @@ def test_loss_and_gradient(T, V, K, kind):
     check(z, ids, t, 2.0, lse=lse.astype(np.float32), kind=kind)
 
 
+def distill_all(z, ids, t, tau, weight):
+    """OT.distill for many rows at once, in torch's 64 bits: the same values and the same bounds."""
+    T, V = z.shape
+    K, U = ids.shape[1], OT.UNIT
+    ok = (ids >= 0) & (ids < V)
+    at = torch.where(ok, ids, 0).long()
+    a = torch.where(ok, t / tau, -torch.inf)
+    top = a.max(1, keepdim=True).values
+    live = (weight != 0) & (top[:, 0] > -torch.inf)
+    top = torch.where(top > -torch.inf, top, 0.0)
+    norm = top + torch.log(torch.exp(a - top).sum(1, keepdim=True))
+    norm = torch.where(live[:, None], norm, 0.0)
+    lnp = a - norm
+    p = torch.exp(lnp)
+    some = p > 0
+    fa = torch.where(some, a.abs(), 0.0)
+    pe = p * (8 + 2 * torch.where(some, lnp.abs(), 0.0) + 2 * K + 2 * norm.abs() + 2 * fa) * U
+    zz = z / tau
+    arg = zz - zz.max(1, keepdim=True).values
+    e = torch.exp(arg)
+    total = e.sum(1, keepdim=True)
+    q = e / total
+    fin = arg.abs()
+    se = (28 + 2 * (q * fin).sum(1, keepdim=True) + V / 256) * U
+    gap = torch.where(some, lnp - (arg.gather(1, at) - total.log()), 0.0)
+    size = fa + norm.abs() + fin.gather(1, at) + total.log().abs()
+    loss = (p * gap).sum(1)
+    le = (pe * gap.abs() + p * (se + 4 * size * U) + 4 * U * p * gap.abs()).sum(1)
+    le = le * (1 + K * U) + (K + 4) * U * loss.abs()
+    pv, pve = torch.zeros_like(zz), torch.zeros_like(zz)
+    pv.scatter_add_(1, at, p * ok)
+    pve.scatter_add_(1, at, pe * ok)
+    w = torch.where(live, weight, 0.0)[:, None]
+    mass = p.sum(1, keepdim=True)
+    dz = w * tau * (mass * q - pv)
+    de = w.abs() * tau * (mass * q * (se + (12 + 2 * fin) * U) + q * pe.sum(1, keepdim=True) + pve + (K + 3) * U * pv)
+    f = w[:, 0] * tau * tau
+    return loss * f, le * f.abs(), dz, de
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V,K", [(3000, 1000, 20), (1201, 4097, 64), (1500, 8192, 1), (900, 20003, 33), (500, 40000, 64),
+                                   (400, 77777, 100), (330, 129280, 64), (2500, 31, 31), (200, 200_001, 7)])
+def test_many_rows_for_each_cluster(T, V, K, kind):
+    """Each block works through several rows, with rows among them that have nothing to do or an odd teacher."""
+    rng = np.random.default_rng(T)
+    pad = 3 if V % 2 else 0  # odd row lengths also get an odd pitch
+    z = (torch.randn((T, V + pad), device=DEV, generator=torch.Generator(DEV).manual_seed(V)) * 2).to(TYPES[kind])[:, :V]
+    ids = rng.integers(0, V, size=(T, K)).astype(np.int32)  # some twice
+    ids[rng.random((T, K)) < 0.1] = -1
+    t = (rng.normal(size=(T, K)) * 2 + 3).astype(np.float32)
+    t[rng.random((T, K)) < 0.05] = -np.inf
+    ids[5::7] = -1
+    ids[3::11] = ids[3::11, :1]
+    w = np.where(rng.random(T) < 0.3, 0.0, rng.normal(size=T)).astype(np.float32)
+    w[40:90] = 0.0  # a stretch of them
+    dz = torch.full((T, V + pad), float("nan"), dtype=TYPES[kind], device=DEV)
+    loss = eg.engram_distill(z, i32(ids), f32(t), 1.5, weight=f32(w), dlogits=dz[:, :V])
+    alone = eg.engram_distill(z, i32(ids), f32(t), 1.5, weight=f32(w))
+    assert torch.equal(loss.view(torch.int32), alone.view(torch.int32))
+    again = torch.empty_like(dz)
+    eg.engram_distill(z, i32(ids), f32(t), 1.5, weight=f32(w), dlogits=again[:, :V])
+    assert torch.equal(dz[:, :V], again[:, :V])
+    if pad:
+        assert torch.isnan(dz[:, V:].float()).all()
+    half = 2.0 ** -8 if kind == "bf16" else 0.0
+    for lo in range(0, T, 100):
+        c = slice(lo, min(lo + 100, T))
+        want, le, wd, de = distill_all(z[c].double(), i32(ids[c]), f32(t[c]).double(), 1.5, f32(w[c]).double())
+        assert ((loss[c].double() - want).abs() <= le + 1e-40).all()
+        assert ((dz[c, :V].double() - wd).abs() <= de * (1 + half) + half * wd.abs() * (1 + 1e-6) + 1e-38).all()
+        if lo == 0:  # the two 64-bit forms agree
+            few = slice(0, 12)
+            o = OT.distill(z[few].double().cpu().numpy(), ids[few], t[few].astype(np.float64), 1.5, w[few].astype(np.float64))
+            for mine, other in zip((want, le, wd, de), o):
+                np.testing.assert_allclose(mine[few].cpu().numpy(), other, rtol=1e-9, atol=1e-15)
+
+
 def test_unused_repeated_and_bad_entries():
     T, V, K = 9, 500, 12
     z, ids, t, _ = inputs(T, V, K, "f32", 1)

@@ -167,6 +167,40 @@ def test_every_row_of_the_outputs_is_written(T, D, R):
     assert (np.abs(g[:m] - ref[uniq]) <= err[uniq]).all() and (g[m:] == 0).all()
 
 
+@pytest.mark.parametrize("T,R", [(511, 90), (512, 90), (513, 90), (4095, 4000), (4097, 5000), (622_592, 200_000),
+                                 (622_593, 200_000), (700_001, 2_000_000_000), (1_300_000, 300)])
+def test_gradient_where_the_sort_changes_its_way(T, R):
+    """Sizes beside each of the sort's limits, and ones that need several rounds; ids outside the table among them."""
+    rng = np.random.default_rng(T)
+    ids = rng.integers(0, R, size=T)
+    ids[rng.random(T) < 0.2] = rng.integers(0, R)
+    ids[rng.random(T) < 0.05] = -1
+    ids[T // 2], ids[T - 1] = -7, R if R < 2 ** 31 else -1
+    ids = ids.astype(np.int32)
+    D = 8
+    dout = make((T, D), "f32", 33)
+    live = (ids >= 0) & (ids < R)
+    uniq, inv, n = np.unique(ids[live], return_inverse=True, return_counts=True)
+    at, d = torch.from_numpy(inv).to(DEV), dout.double()[torch.from_numpy(live).to(DEV)]
+    ref = torch.zeros((len(uniq), D), dtype=torch.float64, device=DEV).index_add_(0, at, d)
+    err = torch.zeros_like(ref).index_add_(0, at, d.abs()) * torch.from_numpy(n + 1).to(DEV)[:, None] * OT.UNIT
+    st = status()
+    rows, grad, count = eg.engram_lookup_grad_rows(dout, i32(ids), R, 1.0, status=st)
+    m = int(count.item())
+    assert m == len(uniq) and (rows[:m].cpu().numpy() == uniq).all() and (rows[m:] == -1).all()
+    assert ((grad[:m].double() - ref).abs() <= err).all() and (grad[m:] == 0).all()
+    assert int(st.item()) == eg.ST_BAD_ROW
+    again = eg.engram_lookup_grad_rows(dout, i32(ids), R, 1.0)
+    assert torch.equal(grad, again[1]) and torch.equal(rows, again[0])
+    if R <= 300_000:
+        dense = torch.full((R, D), float("nan"), device=DEV)
+        eg.engram_lookup_grad(dout, i32(ids), R, 1.0, grad=dense)
+        want, bound = torch.zeros((2, R, D), dtype=torch.float64, device=DEV)
+        want[torch.from_numpy(uniq).long().to(DEV)] = ref
+        bound[torch.from_numpy(uniq).long().to(DEV)] = err
+        assert ((dense.double() - want).abs() <= bound).all()
+
+
 def test_gradient_is_the_same_from_run_to_run():
     ids = i32(ids_of(5000, 4, 300, 11))
     dout = make((5000, 4 * 48), "bf16", 12)
