@@ -1048,6 +1048,11 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _word(status, like: torch.Tensor, idx: int):
+    """The address of a status word on the device (number idx) of `like`."""
+    return None if status is None else _flat(status, "status", torch.int32, like, idx, 1)
+
+
 def _ids_shape(ids: torch.Tensor, like: torch.Tensor, idx: int) -> tuple:
     _flat(ids, "ids", torch.int32, like, idx)
     shape = ids.shape
@@ -1079,8 +1084,8 @@ def engram_lookup(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, ou
         ld = C * D
     else:
         ld = _rows(out, "out", table.dtype, table, idx, T, C * D)
-    rc = L.engram_lookup(table.data_ptr(), ty, R, D, ids.data_ptr(), T, C, scale, out.data_ptr(), ld, _addr(status),
-                         _raw_stream(idx))
+    rc = L.engram_lookup(table.data_ptr(), ty, R, D, ids.data_ptr(), T, C, scale, out.data_ptr(), ld,
+                         _word(status, table, idx), _raw_stream(idx))
     if rc:
         _check(rc, "engram_lookup")
     return out
@@ -1116,7 +1121,7 @@ def engram_lookup_grad(dout: torch.Tensor, ids: torch.Tensor, total_rows: int, s
     else:
         _flat(grad, "grad", torch.float32, dout, idx, total_rows * D)
     rc = L.engram_lookup_grad(dout.data_ptr(), ty, ld, ids.data_ptr(), T, C, D, total_rows, scale, grad.data_ptr(),
-                              workspace.data_ptr(), workspace.numel(), _addr(status), _raw_stream(idx))
+                              workspace.data_ptr(), workspace.numel(), _word(status, dout, idx), _raw_stream(idx))
     if rc:
         _check(rc, "engram_lookup_grad")
     return grad
@@ -1145,7 +1150,7 @@ def engram_lookup_grad_rows(dout: torch.Tensor, ids: torch.Tensor, total_rows: i
         _flat(count, "count", torch.int32, dout, idx, 1)
     rc = L.engram_lookup_grad_rows(dout.data_ptr(), ty, ld, ids.data_ptr(), T, C, D, total_rows, scale,
                                    rows.data_ptr(), grad.data_ptr(), count.data_ptr(), workspace.data_ptr(),
-                                   workspace.numel(), _addr(status), _raw_stream(idx))
+                                   workspace.numel(), _word(status, dout, idx), _raw_stream(idx))
     if rc:
         _check(rc, "engram_lookup_grad_rows")
     return rows, grad, count
@@ -1216,7 +1221,7 @@ def engram_recurrence(x: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor
             raise ValueError("carry is too small (recurrence_carry)")
     rc = L.engram_recurrence(x.data_ptr(), xs, g.data_ptr(), gs, ty, T, D, cu_seqlens.data_ptr(), n_seqs, _addr(slots),
                              _addr(mask), _addr(state), _addr(state_out), n_slots, y.data_ptr(), ys, _addr(carry),
-                             workspace.data_ptr(), workspace.numel(), _addr(status), _raw_stream(idx))
+                             workspace.data_ptr(), workspace.numel(), _word(status, x, idx), _raw_stream(idx))
     if rc:
         _check(rc, "engram_recurrence")
     return y
@@ -1246,7 +1251,7 @@ def engram_recurrence_grad(dy: torch.Tensor, x: torch.Tensor, g: torch.Tensor, c
     rc = L.engram_recurrence_grad(dy.data_ptr(), dys, x.data_ptr(), xs, g.data_ptr(), gs, ty, T, D,
                                   cu_seqlens.data_ptr(), n_seqs, _addr(slots), _addr(mask), _addr(state),
                                   carry.data_ptr(), _addr(dstate), n_slots, dx.data_ptr(), dxs, dg.data_ptr(), dgs,
-                                  workspace.data_ptr(), workspace.numel(), _addr(status), _raw_stream(idx))
+                                  workspace.data_ptr(), workspace.numel(), _word(status, x, idx), _raw_stream(idx))
     if rc:
         _check(rc, "engram_recurrence_grad")
     return dx, dg
@@ -1271,7 +1276,7 @@ def engram_recurrence_step(x: torch.Tensor, g: torch.Tensor, slots: torch.Tensor
     else:
         ys = _rows(y, "y", x.dtype, x, idx, B, D)
     rc = L.engram_recurrence_step(x.data_ptr(), xs, g.data_ptr(), gs, ty, B, D, sp, p, po, state.shape[0],
-                                  y.data_ptr(), ys, _addr(status), _raw_stream(idx))
+                                  y.data_ptr(), ys, _word(status, x, idx), _raw_stream(idx))
     if rc:
         _check(rc, "engram_recurrence_step")
     return y
@@ -1290,7 +1295,9 @@ def engram_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logi
     if teacher_ids.dim() != 2 or teacher_ids.shape[0] != T:
         raise ValueError("teacher_ids must be [T][K]")
     K = teacher_ids.shape[1]
-    tp = _flat(teacher_logits, "teacher_logits", torch.float32, logits, idx, T * K)
+    tp = _flat(teacher_logits, "teacher_logits", torch.float32, logits, idx)
+    if teacher_logits.shape != teacher_ids.shape:
+        raise ValueError("teacher_logits must be [T][K] like teacher_ids")
     wp = None if weight is None else _flat(weight, "weight", torch.float32, logits, idx, T)
     ep = None if teacher_lse is None else _flat(teacher_lse, "teacher_lse", torch.float32, logits, idx, T)
     if loss is None:
@@ -1299,7 +1306,7 @@ def engram_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logi
         _flat(loss, "loss", torch.float32, logits, idx, T)
     ds = _rows(dlogits, "dlogits", logits.dtype, logits, idx, T, V) if dlogits is not None else 0
     rc = L.engram_distill(logits.data_ptr(), ty, T, V, zs, ip, tp, K, temperature, ep, wp, loss.data_ptr(),
-                          _addr(dlogits), ds, _addr(status), _raw_stream(idx))
+                          _addr(dlogits), ds, _word(status, logits, idx), _raw_stream(idx))
     if rc:
         _check(rc, "engram_distill")
     return loss

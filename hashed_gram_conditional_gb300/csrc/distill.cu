@@ -359,6 +359,10 @@ __device__ __forceinline__ void fix_entries(const Args& a, const Row<E>& r, cons
 //     arrived meanwhile, the gradient.
 // Waits are for copies, for the other blocks' pairs and for the block's own
 // warps; all are bounded.
+//
+// 4096 rows of 129,280 bf16 (2.12 GB): 385 us, 5.5 TB/s, 81 % of a copy's rate.
+// Bound by instructions issued in the two walks, each with an exponential a
+// value: the loss alone, one walk without stores, takes 280 us.
 constexpr int kPairs = 4;    // rows whose pairs may be under way: see `send`
 constexpr int kPrep = 4;
 constexpr int kTeacher = 8;  // rows whose teacher's entries are kept, at most
@@ -599,7 +603,9 @@ __global__ void __launch_bounds__((kW + 1 + kPrep) * 32) rows_kernel(const typen
 
 // --------------------------------------------------------------------- long rows
 
-// One cluster of 8 blocks per row, which is read twice.
+// One cluster of 8 blocks per row, which is read twice: a row that does not fit
+// 8 blocks' shared memory would have to be.  Bound by memory: 512 rows of 600,001
+// fp32 (2.46 GB in, 1.23 GB out): 716 us, 5.1 TB/s.
 constexpr int kLongWarps = 8, kLongThreads = kLongWarps * 32;
 
 template <class E>

@@ -674,7 +674,9 @@ int engram_lookup_grad_rows(const void* dout_d, int32_t type, int64_t dout_strid
  *                  aligned; its contents on entry do not matter
  * The scan runs in one pass over memory, its tiles joined by waits on tiles
  * already running; a wait that runs out sets ENGRAM_ST_TIMEOUT.  The result is
- * the same from run to run.  Any dim >= 1 and element-aligned pointers; outputs overlap no input (but
+ * the same from run to run.  bf16 gates below -40 count as -40 (f = 4e-18).  A
+ * state that has become infinite or NaN stays so until its sequence ends.  Any
+ * dim >= 1 and element-aligned pointers; outputs overlap no input (but
  * state_out_d may be state_d). */
 #define ENGRAM_RECURRENCE_TILE 64
 size_t engram_recurrence_carry_bytes(int64_t n_tokens, int32_t dim);

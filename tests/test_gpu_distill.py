@@ -276,6 +276,12 @@ def test_refusals():
     with pytest.raises(ValueError):
         eg.engram_distill(z, i32(ids)[:1], f32(t))
     with pytest.raises(ValueError):
+        eg.engram_distill(z, i32(ids), f32(t.T.copy()))
+    with pytest.raises(ValueError):
+        eg.engram_distill(z, i32(ids), f32(t), status=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        eg.engram_distill(z, i32(ids), f32(t), status=torch.zeros(1, device=DEV))
+    with pytest.raises(ValueError):
         eg.engram_distill(z, i32(ids), f32(t), dlogits=torch.empty((2, 49), device=DEV))
     with pytest.raises(eg.EngramError, match="INVALID"):
         eg.engram_distill(z, i32(ids), f32(t), temperature=0.0)
