@@ -169,6 +169,7 @@ constexpr int kItems = 4;                         // entries per thread and roun
 constexpr int kRound = kSortThreads * kItems;     // entries per block and round
 constexpr int kDigitBits = 9;
 constexpr int kMaxDigits = 1 << kDigitBits;
+constexpr int kMarked = kSortWarps * kMaxDigits * 16;  // rows that clear_meanwhile can mark
 constexpr int kGroup = 13;  // blocks whose digits are summed up for the others: 12 groups of 152 blocks
 
 __device__ __forceinline__ uint32_t entry_key(int32_t id, int64_t total_rows) {
@@ -191,20 +192,37 @@ __device__ __forceinline__ bool is_head(const Entry* e, int64_t i, int32_t n, ui
   return k != none && (i == 0 || k != load_entry(e + i - 1).key);
 }
 
+constexpr int kMaxRange = 256;  // rows that a block clears at a time, at most
+
+// count floats from row on, by a warp: 16 bytes a lane from the first 16-byte
+// boundary to the last
+__device__ __forceinline__ void zero_rows(float* row, int64_t count, int lane) {
+  const int64_t head = (4 - (reinterpret_cast<uintptr_t>(row) / 4 & 3)) & 3;
+  const int64_t c0 = head < count ? head : count, c1 = c0 + (count - c0) / 4 * 4;
+  if (lane < c0) row[lane] = 0.f;
+#pragma unroll 4
+  for (int64_t c = c0 + lane * 4; c < c1; c += 128)
+    __stcs(reinterpret_cast<float4*>(row + c), make_float4(0.f, 0.f, 0.f, 0.f));
+  if (c1 + lane < count) row[c1 + lane] = 0.f;
+}
+
 struct SortArgs {
   const int32_t* ids;
   int64_t total_rows;
   int32_t n, per;  // entries, and how many each block handles
   int32_t passes, bits;
   Entry* list[2];
+  int32_t blocks;   // that sort; further ones clear rows
   int32_t* counts;  // [block][digit]
   int32_t* groups;  // [pass][group of kGroup blocks][digit], zeroed by the caller
-  int32_t* barrier;
+  int32_t* barrier;  // [0] arrivals, [1] whether the list is sorted
   int32_t chunk, chunks;  // sorted entries that are summed together (see seg_sum_kernel), and how many such
   int32_t* base;   // segments that begin in the block's chunks before each chunk, or null
   int32_t chunks_per;  // chunks whose segments each block counts
   int32_t* heads;      // [block]: segments that begin in its chunks
-  int32_t* next;   // the summing kernel's two counters, zeroed here
+  int32_t* next;   // the summing kernel's two counters, zeroed here where a block sorts alone
+  int32_t dim, range;  // the result's columns, and rows that a block clears at a time (dense form)
+  float* grad;
   int32_t* status;
 };
 
@@ -213,8 +231,8 @@ struct SortArgs {
 // by its first thread, which they meet first.
 __device__ __forceinline__ bool meet(const SortArgs& a, int32_t& met) {
   __syncthreads();
-  if (gridDim.x == 1) return true;
-  const int32_t want = ++met * static_cast<int32_t>(gridDim.x);
+  if (a.blocks == 1) return true;
+  const int32_t want = ++met * a.blocks;
   bool ok = true;
   if (threadIdx.x == 0) {
     __threadfence();
@@ -235,6 +253,29 @@ __device__ __forceinline__ bool meet(const SortArgs& a, int32_t& met) {
   return __syncthreads_and(ok);
 }
 
+// What the blocks that do not sort do meanwhile: they clear rows that no entry
+// names, which a bit per row in shared memory tells them, range by range from the
+// summing kernel's counter, until the list is sorted.  They wait for nothing.
+__device__ __forceinline__ void clear_meanwhile(const SortArgs& a, uint32_t* bits, int32_t& taken) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int w = threadIdx.x; w < (a.total_rows + 31) / 32; w += kSortThreads) bits[w] = 0u;
+  __syncthreads();
+#pragma unroll 4
+  for (int32_t i = threadIdx.x; i < a.n; i += kSortThreads) {
+    const int32_t id = __ldg(a.ids + i);
+    if (id >= 0 && id < a.total_rows && !(bits[id >> 5] >> (id & 31) & 1u)) atomicOr(bits + (id >> 5), 1u << (id & 31));
+  }
+  while (true) {
+    __syncthreads();
+    if (threadIdx.x == 0) taken = *reinterpret_cast<volatile int32_t*>(a.barrier + 1) != 0 ? -1 : atomicAdd(a.next + 1, 1);
+    __syncthreads();
+    const int64_t r0 = static_cast<int64_t>(taken) * a.range;
+    if (r0 < 0 || r0 >= a.total_rows) return;
+    for (int r = warp; r < a.range && r0 + r < a.total_rows; r += kSortWarps)
+      if (!(bits[(r0 + r) >> 5] >> ((r0 + r) & 31) & 1u)) zero_rows(a.grad + (r0 + r) * a.dim, a.dim, lane);
+  }
+}
+
 // Moves each entry to its place: entries of smaller digits, entries of the
 // same digit in earlier blocks, rounds, warps and lanes come before it, which
 // keeps the passes stable.  Where a block's entries are one round (up to
@@ -245,15 +286,20 @@ __device__ __forceinline__ bool meet(const SortArgs& a, int32_t& met) {
 // store an entry and the counts in between.  393,216 ids of 26 bits in three
 // passes: 44 us; 16,384 of 17 bits in two, by 16 blocks: 25 us.
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
-  __shared__ uint16_t hist[kSortWarps][kMaxDigits];
+  __shared__ __align__(16) uint16_t hist[kSortWarps][kMaxDigits];
   __shared__ int32_t place[kMaxDigits], half[kMaxDigits], warp_sum[kSortWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int digits = 1 << a.bits, blocks = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
+  const int digits = 1 << a.bits, blocks = a.blocks, me = static_cast<int>(blockIdx.x);
+  if (me >= blocks) {
+    static_assert(sizeof(hist) * 8 == kMarked, "a bit for every row");
+    clear_meanwhile(a, reinterpret_cast<uint32_t*>(hist), place[0]);
+    return;
+  }
   const int32_t e0 = a.n < static_cast<int64_t>(me) * a.per ? a.n : me * a.per;
   const int32_t e1 = a.n - e0 < a.per ? a.n : e0 + a.per;
   const bool one_round = a.per <= kRound;
   int32_t met = 0;
-  if (me == 0 && tid < 2) a.next[tid] = 0;
+  if (gridDim.x == 1 && tid < 2) a.next[tid] = 0;
 
   for (int pass = 0; pass < a.passes; ++pass) {
     const bool first = pass == 0;
@@ -428,7 +474,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
     if (bad && a.status != nullptr) atomicOr(a.status, ENGRAM_ST_BAD_ROW);
     if (!meet(a, met)) return;
   }
-  if (a.base == nullptr) return;
+  if (a.base == nullptr) {
+    if (me == 0 && tid == 0) *reinterpret_cast<volatile int32_t*>(a.barrier + 1) = 1;
+    return;
+  }
 
   // segments that begin in each chunk, summed up over the chunks before it of
   // this block's; the blocks' own sums are left to those who read them
@@ -544,8 +593,6 @@ __device__ __forceinline__ void store_cols(float* row, int c0, int lane, int lan
   }
 }
 
-constexpr int kMaxRange = 256;  // rows that a block clears at a time, at most
-
 template <class E>
 struct SumArgs {
   const typename E::T* dout;
@@ -594,18 +641,6 @@ __device__ __forceinline__ const typename E::T* entry_row(const SumArgs<E>& a, i
   if (a.contiguous) return a.dout + static_cast<int64_t>(i) * a.dim;
   const int32_t t = i / a.n_cols;
   return a.dout + t * a.dout_stride + static_cast<int64_t>(i - t * a.n_cols) * a.dim;
-}
-
-// count floats from row on, by a warp: 16 bytes a lane from the first 16-byte
-// boundary to the last
-__device__ __forceinline__ void zero_rows(float* row, int64_t count, int lane) {
-  const int64_t head = (4 - (reinterpret_cast<uintptr_t>(row) / 4 & 3)) & 3;
-  const int64_t c0 = head < count ? head : count, c1 = c0 + (count - c0) / 4 * 4;
-  if (lane < c0) row[lane] = 0.f;
-#pragma unroll 4
-  for (int64_t c = c0 + lane * 4; c < c1; c += 128)
-    __stcs(reinterpret_cast<float4*>(row + c), make_float4(0.f, 0.f, 0.f, 0.f));
-  if (c1 + lane < count) row[c1 + lane] = 0.f;
 }
 
 // kLanes lanes handle one (chunk, tile of kLanes * kCols columns) at a time,
@@ -988,13 +1023,13 @@ struct GradSpace {
   Entry* list[2];
   int32_t* base;
   int32_t* counts;
-  int32_t* barrier;  // then the group sums
+  int32_t* barrier;  // two words, the summing kernel's counters, then the group sums
   int32_t* heads;
-  int32_t* next;
   float *head, *tail;
   size_t bytes;
 };
 
+constexpr int64_t kMeanwhile = 1 << 22;  // elements of a result that more SMs clear during the sort
 constexpr int kMaxGroups = (kMaxSortBlocks + kGroup - 1) / kGroup, kMaxPasses = 4;
 
 // Lanes per task: the smallest power of two that covers a narrow row.
@@ -1030,7 +1065,6 @@ GradSpace grad_space(void* at, int64_t n, int32_t dim) {
   const size_t chunks = static_cast<size_t>((n + fewest - 1) / fewest);
   s.barrier = reinterpret_cast<int32_t*>(take((4 + static_cast<size_t>(kMaxPasses) * kMaxGroups * kMaxDigits) * 4));
   s.heads = reinterpret_cast<int32_t*>(take(kMaxSortBlocks * 4));
-  s.next = reinterpret_cast<int32_t*>(take(8));
   for (int k = 0; k < 2; ++k) s.list[k] = reinterpret_cast<Entry*>(take(static_cast<size_t>(n) * sizeof(Entry)));
   s.base = reinterpret_cast<int32_t*>(take(chunks * 4));
   s.counts = reinterpret_cast<int32_t*>(take(static_cast<size_t>(kMaxSortBlocks) * kMaxDigits * 4));
@@ -1093,6 +1127,9 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
   const int32_t chunk = chunk_for(n, row_dim, type == ENGRAM_T_BF16 ? kCols<train::Bf16> : kCols<train::F32>);
   const int32_t chunks = static_cast<int32_t>((n64 + chunk - 1) / chunk);
   const uint32_t none = static_cast<uint32_t>(total_rows);
+  // 64 KB at least, to hide the search, and no more ranges than needed to spread over the SMs
+  const int64_t spread = total_rows / (static_cast<int64_t>(sms) * 32), least = std::max((1 << 14) / row_dim, 1);
+  const int32_t range = static_cast<int32_t>(std::min<int64_t>(std::max(spread, least), kMaxRange));
   SortArgs sa{};
   int blocks = 1;
   if (!few) {
@@ -1112,7 +1149,7 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
     sa.chunks = chunks;
     sa.base = dense ? nullptr : w.base;
     sa.heads = w.heads;
-    sa.next = w.next;
+    sa.next = w.barrier + 2;
     sa.status = status_d;
     // one block up to a round of entries; more blocks (at least 1024 entries
     // each) shorten the passes but cost two barriers a pass
@@ -1122,13 +1159,21 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
     }
     sa.per = (n + blocks - 1) / blocks;
     sa.chunks_per = (chunks + blocks - 1) / blocks;
-    if (blocks > 1) {
-      const size_t zeroed = 4 + static_cast<size_t>(sa.passes) * ((blocks + kGroup - 1) / kGroup) * (1 << sa.bits);
+    sa.blocks = blocks;
+    sa.dim = row_dim;
+    sa.range = range;
+    sa.grad = grad_d;
+    // the other SMs clear rows meanwhile
+    int all = blocks;
+    if (dense && total_rows <= kMarked && total_rows * row_dim >= kMeanwhile) all = sms;
+    if (all > 1) {
+      const size_t groups = blocks > 1 ? static_cast<size_t>(sa.passes) * ((blocks + kGroup - 1) / kGroup) * (1 << sa.bits) : 0;
+      const size_t zeroed = 4 + groups;
       cudaError_t err = cudaMemsetAsync(w.barrier, 0, zeroed * 4, st);
       if (err != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(err));
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.gridDim = dim3(static_cast<unsigned>(all));
     cfg.blockDim = dim3(kSortThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr;
@@ -1161,15 +1206,12 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
     a.chunks_per = sa.chunks_per;
     a.count = count_d;
     a.total_rows = total_rows;
-    // 64 KB at least, to hide the search, and no more ranges than needed to spread over the SMs
-    const int64_t spread = total_rows / (static_cast<int64_t>(sms) * 32), bytes = (1 << 14) / row_dim;
-    const int64_t range = spread > bytes ? spread : bytes;
-    a.range = static_cast<int32_t>(range < 1 ? 1 : range > kMaxRange ? kMaxRange : range);
+    a.range = range;
     a.grad = grad_d;
     a.rows = rows_d;
     a.head = w.head;
     a.tail = w.tail;
-    a.next = w.next;
+    a.next = w.barrier + 2;
     const bool vec = row_dim % kCols<E> == 0 && dout_stride % kCols<E> == 0 && aligned(dout_d, 16) &&
                      aligned(grad_d, E::kBytes == 2 ? 32 : 16);
     if (few) return vec ? launch_few<E, true>(a, ids_d, sms, status_d, st) : launch_few<E, false>(a, ids_d, sms, status_d, st);

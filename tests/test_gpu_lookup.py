@@ -146,7 +146,10 @@ def test_gradient_of_long_and_short_segments(T, R, how):
 
 
 @pytest.mark.parametrize("T,D,R", [(3, 5120, 500), (40, 4299, 700), (700, 257, 5000), (2000, 8, 90000), (9000, 1000, 4000),
-                                   (1, 1, 3), (5000, 6, 6)])
+                                   (1, 1, 3), (5000, 6, 6),
+                                   # large enough for rows to be cleared during the sort, and the last number of them
+                                   (513, 257, 20_000), (9000, 1000, 6001), (100_000, 24, 180_000), (2000, 17, 262_144),
+                                   (6000, 17, 262_145)])
 def test_every_row_of_the_outputs_is_written(T, D, R):
     """Outputs that hold something else before: rows that no entry names become zeros, with none left out."""
     rng = np.random.default_rng(31)
