@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
   const int digits = 1 << a.bits, blocks = a.blocks, me = static_cast<int>(blockIdx.x);
   if (me >= blocks) {
     static_assert(sizeof(hist) * 8 == kMarked, "a bit for every row");
+    allow_dependent_launch();
     clear_meanwhile(a, reinterpret_cast<uint32_t*>(hist), place[0]);
     return;
   }
@@ -299,6 +300,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
   const int32_t e1 = a.n - e0 < a.per ? a.n : e0 + a.per;
   const bool one_round = a.per <= kRound;
   int32_t met = 0;
+  allow_dependent_launch();
   if (gridDim.x == 1 && tid < 2) a.next[tid] = 0;
 
   for (int pass = 0; pass < a.passes; ++pass) {
@@ -660,6 +662,8 @@ __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
   const int lane = threadIdx.x % kLanes;
   const int64_t tasks = static_cast<int64_t>(a.chunks) * a.tiles;
   __shared__ int32_t before[kMaxSortBlocks + 1];
+  wait_prior_grids();  // the sort; after it, the joins may be launched and read what it wrote
+  allow_dependent_launch();
   if (!a.dense) {
     sum_heads(a, before);
     __syncthreads();
@@ -854,6 +858,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) seg_join_kernel(SumArgs<E> a)
     parts[warp] = mine;
     segment[warp] = seg;
   }
+  wait_prior_grids();  // the parts
   for (int c0 = blockIdx.y * 32 * N; c0 < a.dim; c0 += gridDim.y * 32 * N) {
     if (mine > 0 && mine <= kOwnParts) {
       float acc[N];
@@ -1083,17 +1088,27 @@ int launch_sums(const SumArgs<E>& a0, int sms, cudaStream_t st) {
   const int64_t want = (static_cast<int64_t>(a.chunks) * a.tiles + groups - 1) / groups, full = static_cast<int64_t>(sms) * 4;
   // the resident blocks at most; all of them where there may be rows to clear
   const int g = static_cast<int>(a.dense || want > full ? full : want);
-  switch (lanes) {
-    case 32: seg_sum_kernel<E, 32, kAligned><<<g, kThreads, 0, st>>>(a); break;
-    case 16: seg_sum_kernel<E, 16, kAligned><<<g, kThreads, 0, st>>>(a); break;
-    case 8: seg_sum_kernel<E, 8, kAligned><<<g, kThreads, 0, st>>>(a); break;
-    default: seg_sum_kernel<E, 4, kAligned><<<g, kThreads, 0, st>>>(a); break;
-  }
-  if (a.chunks > 1) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(g));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // launched while the kernel before it runs
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  auto kernel = lanes == 32   ? seg_sum_kernel<E, 32, kAligned>
+                : lanes == 16 ? seg_sum_kernel<E, 16, kAligned>
+                : lanes == 8  ? seg_sum_kernel<E, 8, kAligned>
+                              : seg_sum_kernel<E, 4, kAligned>;
+  cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a);
+  if (err == cudaSuccess && a.chunks > 1) {
     const int ty = (a.dim + 32 * kCols<E> - 1) / (32 * kCols<E>);
-    seg_join_kernel<E, kAligned>
-        <<<dim3((a.chunks + kJoinWarps - 1) / kJoinWarps, ty < 65535 ? ty : 65535), kJoinWarps * 32, 0, st>>>(a);
+    cfg.gridDim = dim3((a.chunks + kJoinWarps - 1) / kJoinWarps, ty < 65535 ? ty : 65535);
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    err = cudaLaunchKernelEx(&cfg, seg_join_kernel<E, kAligned>, a);
   }
+  if (err != cudaSuccess) return fail(ENGRAM_E_CUDA, "lookup gradient launch: %s", cudaGetErrorString(err));
   return check_launch("lookup gradient");
 }
 
