@@ -284,7 +284,9 @@ __device__ __forceinline__ void clear_meanwhile(const SortArgs& a, uint32_t* bit
 //
 // Bound by waits, not by bytes: a pass is two barriers, one scattered 8-byte
 // store an entry and the counts in between.  393,216 ids of 26 bits in three
-// passes: 44 us; 16,384 of 17 bits in two, by 16 blocks: 25 us.
+// passes: 44 us; 16,384 of 17 bits in two, by 16 blocks: 25 us, in which the other
+// blocks clear rows (dense gradient of 16,384 rows of 5120 into 99,092: 353 us
+// without that, 340 with it).
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
   __shared__ __align__(16) uint16_t hist[kSortWarps][kMaxDigits];
   __shared__ int32_t place[kMaxDigits], half[kMaxDigits], warp_sum[kSortWarps];
@@ -892,17 +894,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) seg_join_kernel(SumArgs<E> a)
 
 // Up to kFew entries need no sort: every block holds all ids and finds by
 // comparing them which entry is the first of its row and which others share
-// it.  A warp adds up one row's entries, in order, for one tile of columns; the
-// blocks then clear the other rows in shares.  One launch where the sort, the
-// sums and the joins take three (300 entries of 64 fp32 columns: 11 against 32 us
-// a call; 464 of 418 bf16 columns: 34 against 33).
-constexpr int kFew = 512;
+// it.  A warp adds up one row's entries, in order, for one tile of columns, a
+// whole block those of a row with many; the blocks then clear the other rows in
+// shares.  One launch where the sort, the sums and the joins take three.  Bound by
+// latency: the comparisons, then the loads of a row's entries, eight at a time.
+// Calls with random ids (with one id): 300 entries of 64 bf16 columns 21 (25) against
+// 34 (32) us by the sort, of 418 bf16 columns 25 (35) against 37 (36); 512 of 1280
+// bf16 columns 42 (43) against 28 (32).
+constexpr int kFew = 320;
 
 template <class E, bool kAligned>
 __global__ void __launch_bounds__(kThreads) few_kernel(SumArgs<E> a, const int32_t* __restrict__ ids, int32_t* status) {
-  constexpr int N = kCols<E>, kBatch = 8;
+  constexpr int N = kCols<E>, kBatch = 8, kOwn = 2 * kBatch;  // entries that one warp adds alone
   __shared__ __align__(16) uint32_t key[kFew];
   __shared__ uint32_t heads[kFew / 32];  // a bit per entry that is the first of its row
+  __shared__ uint32_t longs[kFew / 32];  // of those, the ones whose rows the whole block adds up
+  __shared__ float sums[kWarps][32 * N];
   __shared__ uint32_t named[kMaxRange / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = false;
@@ -917,36 +924,36 @@ __global__ void __launch_bounds__(kThreads) few_kernel(SumArgs<E> a, const int32
   if (bad && blockIdx.x == 0 && status != nullptr) atomicOr(status, ENGRAM_ST_BAD_ROW);
   __syncthreads();
   const int words = (a.n + 31) / 32;
-  for (int w = warp; w < words; w += kWarps) {  // the lane's entry against all before it, four a load
+  for (int w = warp; w < words; w += kWarps) {  // the lane's entry against all, four a load
     const int i = w * 32 + lane;
     const uint32_t mine = key[i];
     bool first = mine != a.none;
-    for (int j = 0; j < w * 32 + 32; j += 4) {
+    int count = 0;
+    for (int j = 0; j < words * 32; j += 4) {
       const uint4 q = *reinterpret_cast<const uint4*>(key + j);
-      first = first && !((q.x == mine && j < i) || (q.y == mine && j + 1 < i) || (q.z == mine && j + 2 < i) ||
-                         (q.w == mine && j + 3 < i));
+      const bool e0 = q.x == mine, e1 = q.y == mine, e2 = q.z == mine, e3 = q.w == mine;
+      first = first && !((e0 && j < i) || (e1 && j + 1 < i) || (e2 && j + 2 < i) || (e3 && j + 3 < i));
+      count += e0 + e1 + e2 + e3;
     }
     const uint32_t bits = __ballot_sync(0xffffffffu, first);
+    const uint32_t many = __ballot_sync(0xffffffffu, first && count > kOwn);
+    if (lane == 0) longs[w] = many;
     if (lane == 0) heads[w] = bits;
   }
   __syncthreads();
 
-  const int64_t tasks = static_cast<int64_t>(a.n) * a.tiles, step = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + warp; task < tasks; task += step) {
-    const int i = static_cast<int>(task / a.tiles), c0 = static_cast<int>(task - static_cast<int64_t>(i) * a.tiles) * 32 * N;
-    if (!(heads[i / 32] >> (i & 31) & 1u)) continue;
-    const uint32_t mine = key[i];
-    int64_t row = mine;
-    if (!a.dense) {  // rows with smaller ids
-      int smaller = 0;
-      for (int w = 0; w < words; ++w) smaller += (heads[w] >> lane & 1u) && key[w * 32 + lane] < mine;
-      row = __reduce_add_sync(0xffffffffu, smaller);
-      if (c0 == 0 && lane == 0) a.rows[row] = static_cast<int32_t>(mine);
-    }
-    float acc[N];
+  // the row of the result
+  auto row_of = [&](uint32_t mine) {
+    if (a.dense) return static_cast<int64_t>(mine);
+    int smaller = 0;  // rows with smaller ids
+    for (int w = 0; w < words; ++w) smaller += (heads[w] >> lane & 1u) && key[w * 32 + lane] < mine;
+    return static_cast<int64_t>(__reduce_add_sync(0xffffffffu, smaller));
+  };
+  // acc: every shares-th entry of the row from the entry i on, in order
+  auto add_row = [&](int i, uint32_t mine, int c0, int share, int shares, float (&acc)[N]) {
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[j] = 0.f;
-    int at[kBatch], held = 0;  // entries found and not added yet
+    int at[kBatch], held = 0, before = 0;  // entries found and not added yet
     auto flush = [&]() {
       uint4 x[kBatch];
 #pragma unroll
@@ -961,6 +968,11 @@ __global__ void __launch_bounds__(kThreads) few_kernel(SumArgs<E> a, const int32
     };
     for (int w = i / 32; w < words; ++w) {
       uint32_t same = __ballot_sync(0xffffffffu, key[w * 32 + lane] == mine);
+      if (shares > 1) {
+        const int place = before + __popc(same & ((1u << lane) - 1u));
+        before += __popc(same);
+        same &= __ballot_sync(0xffffffffu, place % shares == share);
+      }
       while (same != 0) {
         const int e = w * 32 + __ffs(same) - 1;
         same &= same - 1;
@@ -971,7 +983,44 @@ __global__ void __launch_bounds__(kThreads) few_kernel(SumArgs<E> a, const int32
       }
     }
     if (held > 0) flush();
+  };
+
+  const int64_t tasks = static_cast<int64_t>(a.n) * a.tiles, step = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + warp; task < tasks; task += step) {
+    const int i = static_cast<int>(task / a.tiles), c0 = static_cast<int>(task - static_cast<int64_t>(i) * a.tiles) * 32 * N;
+    if (!((heads[i / 32] & ~longs[i / 32]) >> (i & 31) & 1u)) continue;
+    const uint32_t mine = key[i];
+    const int64_t row = row_of(mine);
+    if (!a.dense && c0 == 0 && lane == 0) a.rows[row] = static_cast<int32_t>(mine);
+    float acc[N];
+    add_row(i, mine, c0, 0, 1, acc);
     store_cols<E, kAligned>(a.grad + row * a.dim, c0, lane, 32, a.dim, a.scale, acc);
+  }
+
+  int turn = 0;  // (row, tile) pairs of the long rows, one block each
+  for (int w = 0; w < words; ++w) {
+    for (uint32_t left = longs[w]; left != 0; left &= left - 1) {
+      const int i = w * 32 + __ffs(left) - 1;
+      const uint32_t mine = key[i];
+      for (int tile = 0; tile < a.tiles; ++tile, ++turn) {
+        if (turn % static_cast<int>(gridDim.x) != static_cast<int>(blockIdx.x)) continue;
+        const int c0 = tile * 32 * N;
+        float acc[N];
+        add_row(i, mine, c0, warp, kWarps, acc);
+#pragma unroll
+        for (int j = 0; j < N; ++j) sums[warp][kAligned ? lane * N + j : j * 32 + lane] = acc[j];
+        const int64_t row = row_of(mine);
+        if (!a.dense && tile == 0 && tid == 0) a.rows[row] = static_cast<int32_t>(mine);
+        __syncthreads();
+        for (int c = tid; c < 32 * N && c0 + c < a.dim; c += kThreads) {
+          float total = sums[0][c];
+#pragma unroll
+          for (int v = 1; v < kWarps; ++v) total += sums[v][c];
+          a.grad[row * a.dim + c0 + c] = a.scale * total;
+        }
+        __syncthreads();
+      }
+    }
   }
 
   if (!a.dense) {

@@ -148,7 +148,7 @@ def test_gradient_of_long_and_short_segments(T, R, how):
 @pytest.mark.parametrize("T,D,R", [(3, 5120, 500), (40, 4299, 700), (700, 257, 5000), (2000, 8, 90000), (9000, 1000, 4000),
                                    (1, 1, 3), (5000, 6, 6),
                                    # large enough for rows to be cleared during the sort, and the last number of them
-                                   (513, 257, 20_000), (9000, 1000, 6001), (100_000, 24, 180_000), (2000, 17, 262_144),
+                                   (513, 257, 20_000), (300, 40, 7), (9000, 1000, 6001), (100_000, 24, 180_000), (2000, 17, 262_144),
                                    (6000, 17, 262_145)])
 def test_every_row_of_the_outputs_is_written(T, D, R):
     """Outputs that hold something else before: rows that no entry names become zeros, with none left out."""
@@ -170,7 +170,7 @@ def test_every_row_of_the_outputs_is_written(T, D, R):
     assert (np.abs(g[:m] - ref[uniq]) <= err[uniq]).all() and (g[m:] == 0).all()
 
 
-@pytest.mark.parametrize("T,R", [(511, 90), (512, 90), (513, 90), (4095, 4000), (4097, 5000), (622_592, 200_000),
+@pytest.mark.parametrize("T,R", [(319, 90), (320, 90), (321, 90), (320, 2), (512, 90), (4095, 4000), (4097, 5000), (622_592, 200_000),
                                  (622_593, 200_000), (700_001, 2_000_000_000), (1_300_000, 300)])
 def test_gradient_where_the_sort_changes_its_way(T, R):
     """Sizes beside each of the sort's limits, and ones that need several rounds; ids outside the table among them."""
