@@ -35,7 +35,7 @@ struct Args {
   const int32_t* ids;
   const float* t;
   int32_t top, cluster, depth, keep, slot_bytes;
-  int32_t cluster_log2;
+  int32_t cluster_log2, table_log2;
   bool aligned;  // the rows' strides are multiples of 16 bytes
   float tau;
   const float* lse;
@@ -257,7 +257,7 @@ struct Entries {
   int32_t* id;  // -1 where unused
   float* p;     // logits / tau
   float* zk;    // the student's logits
-  float* sum;   // probabilities, an id's entries added up
+  float* sum;   // probabilities, an id's entries added up (the id's first entry; the others' id is then -1)
 
   __device__ __forceinline__ Entries(void* base, int top) {
     id = static_cast<int32_t*>(base);
@@ -268,28 +268,43 @@ struct Entries {
 };
 constexpr int kEntryBytes = 16;
 
-// Entries with the same id are told by a table of counts by id modulo its
-// size, all zero before and after: only those that share a count are compared.
-constexpr int kBuckets = 1024;  // 16-bit counts
+// Entries with the same id are told by a table in shared memory, open
+// addressing with at least two places an entry: an id's place holds the id and
+// the number of its first entry, with kAgain where it has more.  That entry gets
+// the sum of all of them, which the warp takes together and in a fixed order, and
+// stands for the others.
+constexpr int kAgain = 1 << 30;
+inline int table_log2(int top) {
+  int log2 = 6;
+  while ((1 << log2) < 2 * top) ++log2;
+  return log2;
+}
+__host__ __device__ constexpr size_t table_bytes(int log2) { return size_t(8) << log2; }
 
 // The entries, their normaliser and their mass, by one warp.
 template <class E>
 __device__ __forceinline__ void read_teacher(const Args& a, const typename E::T* z, int64_t row, float inv_tau, int lane,
-                                             const Entries& e, uint32_t* buckets, float& norm, float& mass) {
+                                             const Entries& e, void* table, float& norm, float& mass) {
+  const int places = 1 << a.table_log2;
+  int32_t *held = static_cast<int32_t*>(table), *first = held + places;
+  for (int i = lane * 4; i < places; i += 128) {
+    *reinterpret_cast<int4*>(held + i) = make_int4(-1, -1, -1, -1);
+    *reinterpret_cast<int4*>(first + i) = make_int4(kAgain - 1, kAgain - 1, kAgain - 1, kAgain - 1);
+  }
   float top = -INFINITY;
+  bool bad = false;
+#pragma unroll 4
   for (int k = lane; k < a.top; k += 32) {
-    int32_t v = a.ids[row * a.top + k];
-    if (v >= a.vocab) {
-      if (a.status != nullptr) atomicOr(a.status, ENGRAM_ST_BAD_TOKEN);
-      v = -1;
-    }
-    const float t = v >= 0 ? a.t[row * a.top + k] * inv_tau : -INFINITY;
-    e.id[k] = v < 0 ? -1 : v;
+    int32_t v = __ldg(a.ids + row * a.top + k);
+    bad |= v >= a.vocab;
+    v = v < 0 || v >= a.vocab ? -1 : v;
+    const float t = v >= 0 ? __ldg(a.t + row * a.top + k) * inv_tau : -INFINITY;
+    e.id[k] = v;
     e.p[k] = t;
     e.zk[k] = v >= 0 ? E::load(z + v) : 0.f;
     top = fmaxf(top, t);
-    if (v >= 0) atomicAdd(&buckets[(v % kBuckets) / 2], v & 1 ? 0x10000u : 1u);
   }
+  if (bad && a.status != nullptr) atomicOr(a.status, ENGRAM_ST_BAD_TOKEN);
   top = warp_reduce<true>(top);
   norm = 0.f;
   if (a.lse != nullptr) {
@@ -299,28 +314,48 @@ __device__ __forceinline__ void read_teacher(const Args& a, const typename E::T*
     for (int k = lane; k < a.top; k += 32) sum += expf(e.p[k] - top);
     norm = top + logf(warp_reduce<false>(sum));
   }
+  __syncwarp();
   mass = 0.f;
   for (int k = lane; k < a.top; k += 32) {
-    const float pk = expf(e.p[k] - norm);
-    e.sum[k] = pk;
-    mass += pk;
+    mass += expf(e.p[k] - norm);
+    const int32_t v = e.id[k];
+    if (v < 0) continue;
+    int at = static_cast<int>(static_cast<uint32_t>(v) * 2654435769u >> (32 - a.table_log2));
+    while (true) {  // half of the places at least are never taken
+      const int32_t old = atomicCAS(held + at, -1, v);
+      if (old == -1 || old == v) break;
+      at = (at + 1) & (places - 1);
+    }
+    atomicMin(first + at, k);
+    e.sum[k] = __int_as_float(at);
   }
   mass = warp_reduce<false>(mass);
   __syncwarp();
   for (int k = lane; k < a.top; k += 32) {
-    const int32_t v = e.id[k];
-    if (v < 0) continue;
-    const uint32_t count = buckets[(v % kBuckets) / 2];
-    if ((v & 1 ? count >> 16 : count & 0xffffu) > 1) {
-      float pk = 0.f;
-      for (int i = 0; i < a.top; ++i)
-        if (e.id[i] == v) pk += expf(e.p[i] - norm);
-      e.sum[k] = pk;
+    if (e.id[k] < 0) continue;
+    int32_t* f = first + __float_as_int(e.sum[k]);
+    if ((*f & (kAgain - 1)) != k) atomicOr(f, kAgain);
+  }
+  __syncwarp();
+  for (int k0 = 0; k0 < a.top; k0 += 32) {
+    const int k = k0 + lane;
+    const int32_t v = k < a.top ? e.id[k] : -1;
+    const int32_t f = v >= 0 ? first[__float_as_int(e.sum[k])] : 0;
+    const bool stands = v >= 0 && (f & (kAgain - 1)) == k;
+    float pk = stands ? expf(e.p[k] - norm) : -1.f;  // -1: another entry stands for it
+    for (uint32_t left = __ballot_sync(0xffffffffu, stands && (f & kAgain)); left != 0; left &= left - 1) {
+      const int32_t of = __shfl_sync(0xffffffffu, v, __ffs(left) - 1);
+      float sum = 0.f;
+      for (int i = lane; i < a.top; i += 32)
+        if (e.id[i] == of) sum += expf(e.p[i] - norm);
+      sum = warp_reduce<false>(sum);
+      if (of == v && stands) pk = sum;
     }
+    if (v >= 0) e.sum[k] = pk;
   }
   __syncwarp();
   for (int k = lane; k < a.top; k += 32)
-    if (e.id[k] >= 0) buckets[(e.id[k] % kBuckets) / 2] = 0u;
+    if (e.sum[k] < 0.f) e.id[k] = -1;
   __syncwarp();
 }
 
@@ -345,6 +380,11 @@ __device__ __forceinline__ void fix_entries(const Args& a, const Row<E>& r, cons
     const int v = e.id[k] < 0 ? -1 : (e.id[k] + r.off) / Row<E>::N;
     if (v >= r.v0 && v < r.v1) E::store(r.dz + e.id[k], ex2((e.zk[k] - m) * c) * coef - scale * e.sum[k]);
   }
+}
+
+// a table, and the entries
+__host__ __device__ constexpr size_t short_bytes(int top, int log2) {
+  return table_bytes(log2) + static_cast<size_t>(kEntryBytes) * top;
 }
 
 // --------------------------------------------------------- rows that stay on chip
@@ -378,13 +418,16 @@ struct Head {  // in front of the dynamic shared memory
   float2 stats[kMaxDepth];     // a row's (maximum, sum), for the copying warp
   float weight[kMaxDepth];
   float2 teacher[kTeacher];    // (normaliser, mass)
-  uint32_t buckets[kPrep][kBuckets / 2];
   int abort;
 };
 
 template <int kW>
-__host__ __device__ constexpr size_t head_bytes(int top, int keep) {
+__host__ __device__ constexpr size_t tables_at(int top, int keep) {  // after the teacher's entries
   return (sizeof(Head<kW>) + static_cast<size_t>(keep) * kEntryBytes * top + 127) & ~size_t(127);
+}
+template <int kW>
+__host__ __device__ constexpr size_t head_bytes(int top, int keep, int log2) {
+  return tables_at<kW>(top, keep) + kPrep * table_bytes(log2);
 }
 
 template <class E, int kW>
@@ -398,7 +441,7 @@ __global__ void __launch_bounds__((kW + 1 + kPrep) * 32) rows_kernel(const typen
   const int n = first_row < a.rows ? (a.rows - 1 - first_row) / step + 1 : 0;  // this cluster's rows
   const float inv_tau = 1.f / a.tau, c = 1.4426950408889634f * inv_tau;
   auto row_at = [&](int i) { return static_cast<int64_t>(first_row) + static_cast<int64_t>(i) * step; };
-  auto slot = [&](int i) { return reinterpret_cast<uint4*>(smem + head_bytes<kW>(a.top, a.keep) + (i % a.depth) * static_cast<size_t>(a.slot_bytes)); };
+  auto slot = [&](int i) { return reinterpret_cast<uint4*>(smem + head_bytes<kW>(a.top, a.keep, a.table_log2) + (i % a.depth) * static_cast<size_t>(a.slot_bytes)); };
   auto entries = [&](int i) { return Entries(smem + sizeof(Head<kW>) + (i % a.keep) * kEntryBytes * a.top, a.top); };
   auto wait = [&](uint64_t& bar, int use) {
     if (!mbar_wait_bounded(smem_u32(&bar), use & 1, &h.abort)) {
@@ -420,7 +463,6 @@ __global__ void __launch_bounds__((kW + 1 + kPrep) * 32) rows_kernel(const typen
     h.abort = 0;
     fence_mbar_init();
   }
-  for (int k = tid; k < kPrep * kBuckets / 2; k += (kW + 1 + kPrep) * 32) (&h.buckets[0][0])[k] = 0u;
   __syncthreads();
   if (a.cluster > 1) {  // every block's barriers are set up before pairs are sent to them
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -499,7 +541,8 @@ __global__ void __launch_bounds__((kW + 1 + kPrep) * 32) rows_kernel(const typen
       const int64_t row = row_at(i);
       float norm = 0.f, mass = 0.f;
       if (a.weight == nullptr || __ldg(a.weight + row) != 0.f) {
-        read_teacher<E>(a, z + row * a.z_stride, row, inv_tau, lane, entries(i), h.buckets[warp - kW - 1], norm, mass);
+        read_teacher<E>(a, z + row * a.z_stride, row, inv_tau, lane, entries(i),
+                        smem + tables_at<kW>(a.top, a.keep) + (warp - kW - 1) * table_bytes(a.table_log2), norm, mass);
       }
       if (lane == 0) h.teacher[i % a.keep] = make_float2(norm, mass);
       __syncwarp();
@@ -613,8 +656,7 @@ __global__ void __launch_bounds__(kLongThreads, 3) long_rows_kernel(const typena
   constexpr int N = kVec<E>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float2 pair[kMaxCluster], warp_pair[kLongWarps], teacher;
-  __shared__ uint32_t buckets[kBuckets / 2];
-  const Entries e(smem, a.top);
+  const Entries e(smem + table_bytes(a.table_log2), a.top);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_rank());
   const int64_t row = blockIdx.x / a.cluster;
@@ -630,9 +672,7 @@ __global__ void __launch_bounds__(kLongThreads, 3) long_rows_kernel(const typena
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   if (warp == 0) {
     float norm, mass;
-    for (int k = lane; k < kBuckets / 2; k += 32) buckets[k] = 0u;
-    __syncwarp();
-    read_teacher<E>(a, r.z, row, inv_tau, lane, e, buckets, norm, mass);
+    read_teacher<E>(a, r.z, row, inv_tau, lane, e, smem, norm, mass);
     if (lane == 0) teacher = make_float2(norm, mass);
   }
   const uint4* zv = r.vectors();
@@ -701,6 +741,75 @@ __global__ void __launch_bounds__(kLongThreads, 3) long_rows_kernel(const typena
   }
   __syncthreads();
   fix_entries<E>(a, r, e, m, c, coef, scale, tid, kLongThreads);
+}
+
+// -------------------------------------------------------------------- short rows
+
+// A warp per row: nothing is handed between warps, and the second walk finds the
+// row in the caches.
+constexpr int kShortWarps = 4;
+constexpr int kShortBytes = 8192;
+
+
+template <class E>
+__global__ void __launch_bounds__(kShortWarps * 32, 8) short_rows_kernel(const typename E::T* z, typename E::T* dz, Args a) {
+  constexpr int N = kVec<E>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned char* table = smem + warp * short_bytes(a.top, a.table_log2);
+  const Entries e(table + table_bytes(a.table_log2), a.top);
+  const float inv_tau = 1.f / a.tau, c = 1.4426950408889634f * inv_tau;
+  Row<E> r;
+  bool again = false;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kShortWarps + warp; row < a.rows;
+       row += static_cast<int64_t>(gridDim.x) * kShortWarps, again = true) {
+    __syncwarp();  // the last row's entries are no longer read
+    r.at(z, dz, a, row, 0, again);
+    const float w = a.weight != nullptr ? __ldg(a.weight + row) : 1.f;
+    if (w == 0.f) {  // nothing to learn here
+      if (lane == 0) a.loss[row] = 0.f;
+      if (dz != nullptr) r.zeros(lane, 32);
+      continue;
+    }
+    const uint4* zv = r.vectors();
+    auto vector = [&](int v) { return v >= r.v1 ? no_vector<E>() : v >= r.in0 && v < r.in1 ? zv[v] : r.edge(v); };
+    uint4 x[kAhead];  // on their way while the teacher's entries are read
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) x[u] = vector(lane + u * 32);
+    float norm, mass, m = -INFINITY, s = 0.f;
+    read_teacher<E>(a, r.z, row, inv_tau, lane, e, table, norm, mass);
+    for (int v = lane;;) {
+      add_vectors<E>(x, c, m, s);
+      v += kAhead * 32;
+      if (v - lane >= r.v1) break;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) x[u] = vector(v + u * 32);
+    }
+    join_warp(m, s, c);
+    const float loss = mass == 0.f ? 0.f : sum_loss(a, e, norm, m, s, inv_tau, lane);
+    if (lane == 0) a.loss[row] = mass == 0.f ? 0.f : w * a.tau * a.tau * loss;
+    if (dz == nullptr) continue;
+    if (mass == 0.f) {
+      r.zeros(lane, 32);
+      continue;
+    }
+    const float scale = w * a.tau, coef = scale * mass / s;
+    if (r.off == r.doff) {
+      uint4* dv = reinterpret_cast<uint4*>(r.dz - r.off);
+#pragma unroll 4
+      for (int v = r.first() + lane; v < r.end(); v += 32) {
+        float f[N];
+        grad_vector<E>(zv[v], m, c, coef, f);
+        __stcs(dv + v, narrow<E>(f));
+      }
+      const int edge = r.edge_element(lane);
+      if (edge >= 0) E::store(r.dz + edge, ex2((E::load(r.z + edge) - m) * c) * coef);
+    } else {
+      for (int i = lane; i < r.V; i += 32) E::store(r.dz + i, ex2((E::load(r.z + i) - m) * c) * coef);
+    }
+    __syncwarp();
+    fix_entries<E>(a, r, e, m, c, coef, scale, lane, 32);
+  }
 }
 
 // ------------------------------------------------------------------------ launch
@@ -781,7 +890,7 @@ int launch_rows(const void* z, void* dz, const Args& a, cudaStream_t st) {
   int rc = opt_in(reinterpret_cast<const void*>(rows_kernel<E, kW>), done);
   if (rc) return rc;
   constexpr int kThreads = (kW + 1 + kPrep) * 32;
-  const size_t smem = head_bytes<kW>(a.top, a.keep) + static_cast<size_t>(a.depth) * a.slot_bytes;
+  const size_t smem = head_bytes<kW>(a.top, a.keep, a.table_log2) + static_cast<size_t>(a.depth) * a.slot_bytes;
   int clusters = 0;
   if ((rc = clusters_at_once(reinterpret_cast<const void*>(rows_kernel<E, kW>), a.cluster, kThreads, smem, &clusters)))
     return rc;
@@ -790,11 +899,21 @@ int launch_rows(const void* z, void* dz, const Args& a, cudaStream_t st) {
 }
 
 template <class E>
-int launch_distill(const void* z, void* dz, Args a, cudaStream_t st) {
+int launch_distill(const void* z, void* dz, Args a, int sms, cudaStream_t st) {
   a.aligned = a.z_stride * E::kBytes % 16 == 0 && (dz == nullptr || a.dz_stride * E::kBytes % 16 == 0);
   const int64_t vecs = (a.vocab * E::kBytes + 16 + 15) / 16;  // with a misaligned row's first vector
+  a.table_log2 = table_log2(a.top);
+  if (vecs * 16 <= kShortBytes) {
+    static std::atomic<uint64_t> done{0};
+    int rc = opt_in(reinterpret_cast<const void*>(short_rows_kernel<E>), done);
+    if (rc) return rc;
+    a.cluster = 1;
+    const int64_t want = (static_cast<int64_t>(a.rows) + kShortWarps - 1) / kShortWarps;
+    return launch(short_rows_kernel<E>, std::min<int64_t>(want, static_cast<int64_t>(sms) * 8), kShortWarps * 32,
+                  kShortWarps * short_bytes(a.top, a.table_log2), static_cast<const typename E::T*>(z), static_cast<typename E::T*>(dz), a, st);
+  }
   a.keep = a.top <= 128 ? kTeacher : 4;  // fewer where the entries would take the rows' place
-  const int64_t room = kSmem - static_cast<int64_t>(head_bytes<16>(a.top, a.keep));
+  const int64_t room = kSmem - static_cast<int64_t>(head_bytes<16>(a.top, a.keep, a.table_log2));
   // the smallest cluster that holds three rows (four where they fit); of 4 or 8
   // blocks two will do
   for (a.cluster = 1, a.cluster_log2 = 0; a.cluster <= kMaxCluster; a.cluster *= 2, ++a.cluster_log2) {
@@ -812,7 +931,7 @@ int launch_distill(const void* z, void* dz, Args a, cudaStream_t st) {
   }
   a.cluster = kMaxCluster;
   a.cluster_log2 = 3;
-  return launch(long_rows_kernel<E>, static_cast<int64_t>(a.rows) * a.cluster, kLongThreads, kEntryBytes * static_cast<size_t>(a.top),
+  return launch(long_rows_kernel<E>, static_cast<int64_t>(a.rows) * a.cluster, kLongThreads, short_bytes(a.top, a.table_log2),
                 static_cast<const typename E::T*>(z), static_cast<typename E::T*>(dz), a, st);
 }
 
@@ -841,7 +960,8 @@ extern "C" int engram_distill(const void* logits_d, int32_t type, int64_t n_toke
     return fail(ENGRAM_E_ALIGN, "logits and dlogits must be aligned to their elements");
   if (dlogits_d == logits_d && dlogits_stride != logits_stride)
     return fail(ENGRAM_E_SHAPE, "in place, dlogits has the stride of logits");
-  int rc = check_device(nullptr);
+  int sms = 0;
+  int rc = check_device(&sms);
   if (rc) return rc;
   Args a{};
   a.vocab = vocab;
@@ -856,6 +976,6 @@ extern "C" int engram_distill(const void* logits_d, int32_t type, int64_t n_toke
   a.weight = weight_d;
   a.loss = loss_d;
   a.status = status_d;
-  return type == ENGRAM_T_BF16 ? launch_distill<train::Bf16>(logits_d, dlogits_d, a, as_stream(stream))
-                               : launch_distill<train::F32>(logits_d, dlogits_d, a, as_stream(stream));
+  return type == ENGRAM_T_BF16 ? launch_distill<train::Bf16>(logits_d, dlogits_d, a, sms, as_stream(stream))
+                               : launch_distill<train::F32>(logits_d, dlogits_d, a, sms, as_stream(stream));
 }
