@@ -12,7 +12,8 @@
 // write the gradient from there.  Memory traffic is then the logits once and
 // the gradient once.  The blocks stay and go from row to row, with the copies
 // of the next rows under way (rows_kernel); rows too long for a cluster's
-// shared memory are read twice (long_rows_kernel).
+// shared memory are read twice (long_rows_kernel), and short ones are a warp's
+// work (short_rows_kernel).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -392,19 +393,22 @@ __host__ __device__ constexpr size_t short_bytes(int top, int log2) {
 // The blocks of a cluster share a row and go from row to row.  In a block
 //   - the copying warp keeps the copies of the next `depth` rows under way, and
 //     finishes a row when its walk is done: the entries' gradients, the loss;
-//   - kPrep warps prepare the teacher's entries of the next rows, in turn (some
-//     14,000 cycles a row, nearly all of them waits for memory);
+//   - kPrep warps prepare the teacher's entries of the next rows, in turn (nearly
+//     all of their time are waits for memory);
 //   - kW warps walk the rows: of row i + 1 the maximum and the sum, which they
 //     send to every block of the cluster, then of row i, whose pairs have
 //     arrived meanwhile, the gradient.
 // Waits are for copies, for the other blocks' pairs and for the block's own
 // warps; all are bounded.
 //
-// 4096 rows of 129,280 bf16 (2.12 GB): 385 us, 5.5 TB/s, 81 % of a copy's rate.
+// 4096 rows of 129,280 bf16 (2.12 GB): 366 us, 5.8 TB/s, 85 % of a copy's rate.
 // Bound by instructions issued in the two walks, each with an exponential a
 // value: the loss alone, one walk without stores, takes 280 us.
 constexpr int kPairs = 4;    // rows whose pairs may be under way: see `send`
-constexpr int kPrep = 4;
+// (4096 x 129,280 bf16 with 16 walking warps: 371 us with 4, 366 with 6, 369 with
+// 8; 4096 x 8000 with 4: 50, 53 and 52)
+template <int kW>
+constexpr int kPrep = kW == 16 ? 6 : 4;
 constexpr int kTeacher = 8;  // rows whose teacher's entries are kept, at most
 constexpr int kMaxDepth = 4;  // rows whose copies may be under way
 
@@ -421,17 +425,26 @@ struct Head {  // in front of the dynamic shared memory
   int abort;
 };
 
+// Warps that prepare, at most one for each row that is kept: a warp that waits for
+// row i - keep to be used has waited for row i - keep - preparing before, which
+// must be row i - 2 keep or a later one, as the barriers tell two uses apart and
+// not three.
+template <int kW>
+__host__ __device__ constexpr int preparing(int keep) {
+  return keep < kPrep<kW> ? keep : kPrep<kW>;
+}
+
 template <int kW>
 __host__ __device__ constexpr size_t tables_at(int top, int keep) {  // after the teacher's entries
   return (sizeof(Head<kW>) + static_cast<size_t>(keep) * kEntryBytes * top + 127) & ~size_t(127);
 }
 template <int kW>
 __host__ __device__ constexpr size_t head_bytes(int top, int keep, int log2) {
-  return tables_at<kW>(top, keep) + kPrep * table_bytes(log2);
+  return tables_at<kW>(top, keep) + preparing<kW>(keep) * table_bytes(log2);
 }
 
 template <class E, int kW>
-__global__ void __launch_bounds__((kW + 1 + kPrep) * 32) rows_kernel(const typename E::T* z, typename E::T* dz, Args a) {
+__global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const typename E::T* z, typename E::T* dz, Args a) {
   constexpr int N = kVec<E>, kData = kW * 32;
   extern __shared__ __align__(128) unsigned char smem[];
   Head<kW>& h = *reinterpret_cast<Head<kW>*>(smem);
@@ -536,7 +549,8 @@ __global__ void __launch_bounds__((kW + 1 + kPrep) * 32) rows_kernel(const typen
     }
   } else if (warp > kW) {
     // ---- the teacher's entries, rows in turn
-    for (int i = warp - kW - 1; i < n; i += kPrep) {
+    const int prep = preparing<kW>(a.keep);
+    for (int i = warp - kW - 1; warp - kW - 1 < prep && i < n; i += prep) {
       if (i >= a.keep) wait(h.used[i % a.keep], i / a.keep - 1);
       const int64_t row = row_at(i);
       float norm = 0.f, mass = 0.f;
@@ -746,7 +760,9 @@ __global__ void __launch_bounds__(kLongThreads, 3) long_rows_kernel(const typena
 // -------------------------------------------------------------------- short rows
 
 // A warp per row: nothing is handed between warps, and the second walk finds the
-// row in the caches.
+// row in the caches.  Bound by latency, which 32 warps an SM hide from one
+// another.  16,384 rows of 20 entries, this kernel against rows_kernel: of 1000
+// bf16 32 against 76 us, of 4000 (8 KB) 66 against 95, of 8000 150 against 130.
 constexpr int kShortWarps = 4;
 constexpr int kShortBytes = 8192;
 
@@ -889,7 +905,7 @@ int launch_rows(const void* z, void* dz, const Args& a, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   int rc = opt_in(reinterpret_cast<const void*>(rows_kernel<E, kW>), done);
   if (rc) return rc;
-  constexpr int kThreads = (kW + 1 + kPrep) * 32;
+  constexpr int kThreads = (kW + 1 + kPrep<kW>) * 32;
   const size_t smem = head_bytes<kW>(a.top, a.keep, a.table_log2) + static_cast<size_t>(a.depth) * a.slot_bytes;
   int clusters = 0;
   if ((rc = clusters_at_once(reinterpret_cast<const void*>(rows_kernel<E, kW>), a.cluster, kThreads, smem, &clusters)))

@@ -96,7 +96,8 @@ def distill_all(z, ids, t, tau, weight):
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("T,V,K", [(3000, 1000, 20), (1201, 4097, 64), (1500, 8192, 1), (900, 20003, 33), (500, 40000, 64),
-                                   (400, 77777, 100), (330, 129280, 64), (2500, 31, 31), (200, 200_001, 7)])
+                                   (400, 77777, 100), (330, 129280, 64), (700, 50_000, 200), (600, 9000, 1024), (5000, 4088, 300),
+                                   (2500, 31, 31), (200, 200_001, 7)])
 def test_many_rows_for_each_cluster(T, V, K, kind):
     """Each block works through several rows, with rows among them that have nothing to do or an odd teacher."""
     rng = np.random.default_rng(T)
