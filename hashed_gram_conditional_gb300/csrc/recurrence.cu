@@ -556,7 +556,7 @@ __device__ __forceinline__ float come_in(const Args<E>& a, int group, int pos, i
 // waits.
 //
 // 16,384 x 5120 bf16 (503 MB): 106 us, 4.8 TB/s, 70 % of a copy's rate.  Neither
-// memory nor issue is full (48 % of DRAM, 0.53 instructions a cycle and scheduler
+// memory nor issue is full (46 % of DRAM, 0.50 instructions a cycle and scheduler
 // at half the length); what is left are waits, for the copies and for the tiles
 // before.  Tiles of 64 positions, blocks of 4 warps and runs of 4, 12 or 16
 // tiles are slower.
@@ -719,7 +719,7 @@ constexpr int kFwdSmem = 2 * kFwdTile * kRowBytes + 2 * kFwdWarps * kGroup<E> * 
 // instructions than the two exponentials and the reciprocal of a pair.
 //
 // 16,384 x 5120 bf16 (860 MB with the saved states): 193 us, 4.5 TB/s, 66 % of a
-// copy's rate, at 0.58 instructions a cycle and scheduler and half of DRAM's
+// copy's rate, at 0.56 instructions a cycle and scheduler and half of DRAM's
 // cycles.  Tiles of 128 positions (one block less an SM) and blocks of 4 warps
 // gain nothing.
 constexpr int kBwdWarps = 8;
