@@ -1096,8 +1096,8 @@ int lanes_for(int32_t dim, int cols) {
 // Entries per chunk: the fewest of 16, 32, 64 and 128 that give no more tasks
 // than five quarters of the lane groups that 152 SMs hold (4 blocks of 8
 // warps).  Fewer entries shorten a small call, whose tasks all run at once;
-// more entries leave fewer parts to join (393,216 entries of 256 columns: 128
-// against 64 takes 184 against 200 us; 16,384 of 5120: 362 against 355).
+// more entries leave fewer parts to join (393,216 entries of 256 columns with 32,
+// 64 and 128: 193, 182 and 171 us; 16,384 of 5120: 341, 333 and 333).
 int32_t chunk_for(int64_t n, int32_t dim, int cols) {
   const int lanes = lanes_for(dim, cols);
   const int64_t tiles = (dim + lanes * cols - 1) / (lanes * cols), groups = 4864 * (32 / lanes);
