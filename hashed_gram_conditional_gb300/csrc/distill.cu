@@ -316,7 +316,8 @@ __device__ __forceinline__ void read_teacher(const Args& a, const typename E::T*
     e.p[k] = t;
     if (a.lse == nullptr) sum += expf(t);
   }
-  norm = a.lse != nullptr ? __ldg(a.lse + row) : top == -INFINITY ? 0.f : logf(warp_reduce<false>(sum));
+  // (a position without an entry to learn from has no mass, whatever comes as its normaliser)
+  norm = top == -INFINITY ? 0.f : a.lse != nullptr ? __ldg(a.lse + row) : logf(warp_reduce<false>(sum));
   __syncwarp();
   mass = 0.f;
   for (int k = lane; k < a.top; k += 32) {

@@ -733,7 +733,7 @@ int engram_recurrence_step(const void* x_d, int64_t x_stride, const void* g_d, i
  *   dlogits_d        [n_tokens][vocab] of `type`, rows dlogits_stride apart, or
  *                    NULL (loss alone); may be logits_d
  * A position of weight 0, or without any teacher mass, gives loss 0 and a
- * zero gradient whatever its logits hold.  A student logit of -inf has q = 0.
+ * zero gradient whatever its logits and its teacher_lse hold.  A student logit of -inf has q = 0.
  * top <= ENGRAM_DISTILL_MAX_TOP, temperature positive and finite. */
 #define ENGRAM_DISTILL_MAX_TOP 1024
 int engram_distill(const void* logits_d, int32_t type, int64_t n_tokens, int64_t vocab, int64_t logits_stride,
