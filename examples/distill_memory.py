@@ -89,8 +89,11 @@ class Memory:
         for t in range(raw_ids.numel()):
             ids, mask = eg.engram_hash_step(self.layout, 0, raw_ids[t:t + 1], slot, self.token_map, hist,
                                             status=self.status)
-            e = eg.engram_lookup(self.table, ids, self.scale, status=self.status).bfloat16()
-            y = eg.engram_recurrence_step(e @ self.w_x, e @ self.w_g, slot, state, status=self.status)
+            image = mask != 0  # no rows and no slot: the state stays, and y is 0
+            e = eg.engram_lookup(self.table, ids.masked_fill_(image[:, None], eg.DEAD), self.scale,
+                                 status=self.status).bfloat16()
+            y = eg.engram_recurrence_step(e @ self.w_x, e @ self.w_g, slot.masked_fill(image, -1), state,
+                                          status=self.status)
             out.append(y @ self.w_out)
         return torch.cat(out)
 

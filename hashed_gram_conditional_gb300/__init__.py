@@ -1260,8 +1260,9 @@ def engram_recurrence_grad(dy: torch.Tensor, x: torch.Tensor, g: torch.Tensor, c
 def engram_recurrence_step(x: torch.Tensor, g: torch.Tensor, slots: torch.Tensor, state: torch.Tensor,
                            state_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
                            status: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """One position of every batch entry: x, g bf16 or f32 [B][dim], slots int32 [B] (-1: padding), state f32
-    [n_slots][dim] updated in place unless state_out takes the new states; returns y [B][dim]."""
+    """One position of every batch entry: x, g bf16 or f32 [B][dim], slots int32 [B] (-1: padding, or a masked
+    position: y is 0 and the state stays), state f32 [n_slots][dim] updated in place unless state_out takes the new
+    states; returns y [B][dim]."""
     L = _lib or _load()
     ty, idx, B, D, xs = _matrix(x, "x")
     gs = _rows(g, "g", x.dtype, x, idx, B, D)

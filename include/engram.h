@@ -703,8 +703,9 @@ int engram_recurrence_grad(const void* dy_d, int64_t dy_stride, const void* x_d,
                            void* workspace_d, size_t workspace_bytes, int32_t* status_d, void* stream);
 
 /* One position for each of `batch` sequences (decode): row b of x, g and y
- * belongs to state slots_d[b]; a negative slot is padding (y = 0, no state), a
- * slot >= n_slots sets ENGRAM_ST_BAD_SLOT and is padding.  state_out_d may be
+ * belongs to state slots_d[b]; a negative slot is padding (y = 0, no state),
+ * which is also how a masked position is passed; a slot >= n_slots sets
+ * ENGRAM_ST_BAD_SLOT and is padding.  state_out_d may be
  * state_d, or another buffer that leaves the old states in place. */
 int engram_recurrence_step(const void* x_d, int64_t x_stride, const void* g_d, int64_t g_stride, int32_t type,
                            int64_t batch, int32_t dim, const int32_t* slots_d, const float* state_d,
