@@ -989,7 +989,15 @@ def engram_selftest_mod(layout: Layout, layer: int, x: torch.Tensor) -> torch.Te
 # few attribute reads, one that does not goes to the function that says why.
 
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}
-_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _current_stream(idx: int) -> int:
+    """The current stream of device number idx."""
+    return torch.cuda.current_stream(idx).cuda_stream
+
+
+# the same without a Stream object, where torch has the function (a build without CUDA has not)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
 def _need_rows(t: torch.Tensor, name: str, dtype, device, n_rows: int, width: int) -> int:
