@@ -131,6 +131,8 @@ _SIGS = {
     "engram_hash_gather_fp8": [ctypes.POINTER(_Layout), _I32, _P, _I64, _P, _I32, _P, _I64, _P, _P, _I64, _P, _P,
                                _P, _P, _P, _P],
     "engram_selftest_wait": [_I32, _P, _P, _P],
+    "engram_selftest_grad_wait": [_P, _I32, _I64, _P, _I64, _I32, _I32, _I64, _P, _P, _P, _P, ctypes.c_size_t, _P,
+                                  _P],
     "engram_gather_rows_bf16": [_P, _I64, _I32, _P, _I64, _I32, _P, _P, _P],
     "engram_hash_gather_rows_bf16": [ctypes.POINTER(_Layout), _I32, _P, _I64, _P, _I32, _P, _I64, _P, _P, _I32, _P,
                                      _P, _P, _P, _P],
@@ -1336,6 +1338,23 @@ def engram_selftest_wait(which: int, status: torch.Tensor, scratch: Optional[tor
     _need(scratch, "scratch", torch.int32, dev, 2)
     _check(L.engram_selftest_wait(which, _ptr(scratch), _ptr(status), _stream(dev)), "engram_selftest_wait")
     return scratch
+
+
+def engram_selftest_grad_wait(dout: torch.Tensor, ids: torch.Tensor, total_rows: int, status: torch.Tensor,
+                              grad: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                              count: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Diagnostic: a lookup gradient (its distinct rows, or without rows all of them) whose sort waits for something
+    that never happens; after about a second it sets ST_TIMEOUT in ``status`` and there is no gradient.
+    Asynchronous on the current stream."""
+    L = _load()
+    ty, idx, ld, T, C, D, workspace = _grad_args(dout, ids, workspace)
+    _flat(grad, "grad", torch.float32, dout, idx, (total_rows if rows is None else T * C) * D)
+    if rows is not None:
+        _flat(rows, "rows", torch.int32, dout, idx, T * C)
+        _flat(count, "count", torch.int32, dout, idx, 1)
+    _check(L.engram_selftest_grad_wait(dout.data_ptr(), ty, ld, ids.data_ptr(), T, C, D, total_rows, _addr(rows),
+                                       grad.data_ptr(), _addr(count), workspace.data_ptr(), workspace.numel(),
+                                       _word(status, dout, idx), _raw_stream(idx)), "engram_selftest_grad_wait")
 
 
 class EngramLayer:

@@ -216,6 +216,7 @@ struct SortArgs {
   int32_t* counts;  // [block][digit]
   int32_t* groups;  // [pass][group of kGroup blocks][digit], zeroed by the caller
   int32_t* barrier;  // [0] arrivals, [1] whether the list is sorted
+  int32_t absent;    // arrivals that every wait expects beyond the blocks' (0; see engram_selftest_grad_wait)
   int32_t chunk, chunks;  // sorted entries that are summed together (see seg_sum_kernel), and how many such
   int32_t* base;   // segments that begin in the block's chunks before each chunk, or null
   int32_t chunks_per;  // chunks whose segments each block counts
@@ -227,12 +228,14 @@ struct SortArgs {
 };
 
 // All blocks meet; false when the wait ran out (the blocks are co-resident, so
-// that means a broken launch).  What a block's threads wrote before is released
-// by its first thread, which they meet first.
+// that means a broken launch).  The list may hold anything then, so the counter
+// of the tasks that follow it is set behind the last of them.  What a block's
+// threads wrote before is released by its first thread, which they meet first.
+constexpr int32_t kGaveUp = 1 << 30;  // more than any call's tasks (2^25 for 2^37 elements, which fill the memory)
 __device__ __forceinline__ bool meet(const SortArgs& a, int32_t& met) {
   __syncthreads();
   if (a.blocks == 1) return true;
-  const int32_t want = ++met * a.blocks;
+  const int32_t want = ++met * a.blocks + a.absent;
   bool ok = true;
   if (threadIdx.x == 0) {
     __threadfence();
@@ -244,6 +247,7 @@ __device__ __forceinline__ bool meet(const SortArgs& a, int32_t& met) {
       if (v >= want) break;
       if (clock64() - begun > kWaitBudgetCycles) {
         ok = false;
+        atomicMax(a.next, kGaveUp);
         if (a.status != nullptr) atomicOr(a.status, ENGRAM_ST_TIMEOUT);
         break;
       }
@@ -615,7 +619,7 @@ struct SumArgs {
   float* grad;
   int32_t* rows;
   float *head, *tail;    // [chunk][dim]: the parts of a segment from before, of one that goes on
-  int32_t* next;         // [0] next task, [1] next rows to clear (zeroed by the sort)
+  int32_t* next;         // [0] next task (from kGaveUp on: there is no list), [1] next rows to clear (zeroed by the sort)
 };
 
 // before[b]: segments that begin in the chunks of the sort's blocks before b, and
@@ -647,6 +651,19 @@ __device__ __forceinline__ const typename E::T* entry_row(const SumArgs<E>& a, i
   return a.dout + t * a.dout_stride + static_cast<int64_t>(i - t * a.n_cols) * a.dim;
 }
 
+// A sort that gave up leaves a list of anything, which must not be followed: there
+// is no gradient then, but zeros and no rows.
+template <class E>
+__device__ __forceinline__ void no_gradient(const SumArgs<E>& a) {
+  if (!a.dense && blockIdx.x == 0 && threadIdx.x == 0) *a.count = 0;
+  const int64_t rows = a.dense ? a.total_rows : a.n;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32; r < rows;
+       r += static_cast<int64_t>(gridDim.x) * kWarps) {
+    if (!a.dense && threadIdx.x % 32 == 0) a.rows[r] = -1;
+    zero_rows(a.grad + r * a.dim, a.dim, threadIdx.x % 32);
+  }
+}
+
 // kLanes lanes handle one (chunk, tile of kLanes * kCols columns) at a time,
 // taken from a counter; the rows that no entry names are cleared in the same
 // way, when the chunks are given out.  Which warp takes what changes nothing in
@@ -673,8 +690,13 @@ __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
   while (true) {
     int32_t got = 0;
     if (wl == 0) got = atomicAdd(a.next, 1);
-    const int64_t task = static_cast<int64_t>(__shfl_sync(0xffffffffu, got, 0)) * kGroups + wl / kLanes;
-    if (task - wl / kLanes >= tasks) break;
+    got = __shfl_sync(0xffffffffu, got, 0);
+    const int64_t task = static_cast<int64_t>(got) * kGroups + wl / kLanes;
+    if (task - wl / kLanes >= tasks) {
+      if (got < kGaveUp) break;
+      no_gradient(a);
+      return;
+    }
     if (task >= tasks) continue;
     const int32_t chunk = static_cast<int32_t>(task / a.tiles);
     const int32_t tile = static_cast<int32_t>(task - static_cast<int64_t>(chunk) * a.tiles);
@@ -827,6 +849,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) seg_join_kernel(SumArgs<E> a)
     }
   };
   __shared__ int32_t before[kMaxSortBlocks + 1];
+  const bool no_list = __ldcg(a.next) >= kGaveUp;
   if (!a.dense) {
     sum_heads(a, before);
     __syncthreads();
@@ -856,6 +879,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) seg_join_kernel(SumArgs<E> a)
       }
     }
   }
+  if (no_list) mine = 0;  // (no place of the list was followed so far)
   if (lane == 0) {
     parts[warp] = mine;
     segment[warp] = seg;
@@ -1164,7 +1188,7 @@ int launch_sums(const SumArgs<E>& a0, int sms, cudaStream_t st) {
 int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int32_t* ids_d, int64_t n_tokens,
                 int32_t n_cols, int32_t row_dim, int64_t total_rows, float scale, bool dense, int32_t* rows_d,
                 float* grad_d, int32_t* count_d, void* workspace_d, size_t workspace_bytes, int32_t* status_d,
-                void* stream) {
+                void* stream, int32_t absent = 0) {
   int rc = check_lookup(type, total_rows, row_dim, n_tokens, n_cols, dout_stride);
   if (rc) return rc;
   const int64_t n64 = n_tokens * n_cols;
@@ -1208,6 +1232,7 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
     for (int k = 0; k < 2; ++k) sa.list[k] = w.list[k];
     sa.counts = w.counts;
     sa.barrier = w.barrier;
+    sa.absent = absent;
     sa.groups = w.barrier + 4;
     sa.chunk = chunk;
     sa.chunks = chunks;
@@ -1328,4 +1353,14 @@ extern "C" int engram_lookup_grad_rows(const void* dout_d, int32_t type, int64_t
                                        int32_t* status_d, void* stream) {
   return lookup_grad(dout_d, type, dout_stride, row_ids_d, n_tokens, n_cols, row_dim, total_rows, scale, false, rows_d,
                      grad_d, count_d, workspace_d, workspace_bytes, status_d, stream);
+}
+
+extern "C" int engram_selftest_grad_wait(const void* dout_d, int32_t type, int64_t dout_stride,
+                                         const int32_t* row_ids_d, int64_t n_tokens, int32_t n_cols, int32_t row_dim,
+                                         int64_t total_rows, int32_t* rows_d, float* grad_d, int32_t* count_d,
+                                         void* workspace_d, size_t workspace_bytes, int32_t* status_d, void* stream) {
+  if (n_tokens < 0 || n_cols < 1 || n_tokens > 0x7fffffff / n_cols || n_tokens * n_cols <= kRound)
+    return fail(ENGRAM_E_RANGE, "only the sort of more than %d entries waits", kRound);
+  return lookup_grad(dout_d, type, dout_stride, row_ids_d, n_tokens, n_cols, row_dim, total_rows, 1.f, rows_d == nullptr,
+                     rows_d, grad_d, count_d, workspace_d, workspace_bytes, status_d, stream, 1);
 }

@@ -624,7 +624,8 @@ int engram_lookup(const void* table_d, int32_t type, int64_t total_rows, int32_t
  * Entries are sorted by (id, i) and each row's sum is taken in a fixed order,
  * so results are the same from run to run.  Ids without a row (as in
  * engram_lookup) contribute nothing.  More than 4096 entries are sorted by a
- * cooperative launch, whose barriers set ENGRAM_ST_TIMEOUT if they run out.
+ * cooperative launch, whose barriers set ENGRAM_ST_TIMEOUT if they run out; the
+ * gradient is then zeros, with a count of 0.
  *   dout_d       [n_tokens][n_cols*row_dim] of `type`, rows dout_stride apart
  *   workspace_d  engram_lookup_grad_workspace_bytes(...) bytes, 256-byte aligned
  *
@@ -819,6 +820,16 @@ int engram_selftest_mod(const engram_layout* layout, int32_t layer, const uint64
  *   scratch_d  int32 [2] device scratch, zeroed by the call before the launch
  *   status_d   int32 status word (not cleared) */
 int engram_selftest_wait(int32_t which, int32_t* scratch_d, int32_t* status_d, void* stream);
+
+/* The same for the barriers of the lookup gradient's sort: engram_lookup_grad_rows
+ * (or, where rows_d is NULL, engram_lookup_grad) of more than 4096 entries whose
+ * sorting blocks each expect one arrival more than there are blocks.  The first
+ * wait runs out after about a second, ENGRAM_ST_TIMEOUT is set and the outputs are
+ * those of no gradient. */
+int engram_selftest_grad_wait(const void* dout_d, int32_t type, int64_t dout_stride, const int32_t* row_ids_d,
+                              int64_t n_tokens, int32_t n_cols, int32_t row_dim, int64_t total_rows, int32_t* rows_d,
+                              float* grad_d, int32_t* count_d, void* workspace_d, size_t workspace_bytes,
+                              int32_t* status_d, void* stream);
 
 /* Thread-local message of the last failure (empty string if none). */
 const char* engram_last_error(void);
