@@ -131,6 +131,7 @@ _SIGS = {
     "engram_hash_gather_fp8": [ctypes.POINTER(_Layout), _I32, _P, _I64, _P, _I32, _P, _I64, _P, _P, _I64, _P, _P,
                                _P, _P, _P, _P],
     "engram_selftest_wait": [_I32, _P, _P, _P],
+    "engram_selftest_distill_wait": [_P, _I32, _I64, _I64, _I64, _P, _P, _I32, _P, _P, _I64, _P, _P],
     "engram_selftest_grad_wait": [_P, _I32, _I64, _P, _I64, _I32, _I32, _I64, _P, _P, _P, _P, ctypes.c_size_t, _P,
                                   _P],
     "engram_gather_rows_bf16": [_P, _I64, _I32, _P, _I64, _I32, _P, _P, _P],
@@ -1355,6 +1356,24 @@ def engram_selftest_grad_wait(dout: torch.Tensor, ids: torch.Tensor, total_rows:
     _check(L.engram_selftest_grad_wait(dout.data_ptr(), ty, ld, ids.data_ptr(), T, C, D, total_rows, _addr(rows),
                                        grad.data_ptr(), _addr(count), workspace.data_ptr(), workspace.numel(),
                                        _word(status, dout, idx), _raw_stream(idx)), "engram_selftest_grad_wait")
+
+
+def engram_selftest_distill_wait(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                                 status: torch.Tensor, loss: torch.Tensor, dlogits: Optional[torch.Tensor] = None):
+    """Diagnostic: a distillation whose blocks wait for something that never happens; after about a second it sets
+    ST_TIMEOUT in ``status``, and the outputs are undefined.  Asynchronous on the current stream."""
+    L = _load()
+    ty, idx, T, V, zs = _matrix(logits, "logits")
+    _flat(teacher_ids, "teacher_ids", torch.int32, logits, idx)
+    if teacher_ids.dim() != 2 or teacher_ids.shape[0] != T:
+        raise ValueError("teacher_ids must be [T][K]")
+    _flat(teacher_logits, "teacher_logits", torch.float32, logits, idx, teacher_ids.numel())
+    _flat(loss, "loss", torch.float32, logits, idx, T)
+    ds = _rows(dlogits, "dlogits", logits.dtype, logits, idx, T, V) if dlogits is not None else 0
+    _check(L.engram_selftest_distill_wait(logits.data_ptr(), ty, T, V, zs, teacher_ids.data_ptr(),
+                                          teacher_logits.data_ptr(), teacher_ids.shape[1], loss.data_ptr(),
+                                          _addr(dlogits), ds, _word(status, logits, idx), _raw_stream(idx)),
+           "engram_selftest_distill_wait")
 
 
 class EngramLayer:

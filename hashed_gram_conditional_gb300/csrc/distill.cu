@@ -38,6 +38,7 @@ struct Args {
   int32_t top, cluster, depth, keep, slot_bytes;
   int32_t cluster_log2, table_log2;
   bool aligned;  // the rows' strides are multiples of 16 bytes
+  uint32_t absent;  // bytes that every row's pairs are expected to have beyond theirs (0; see engram_selftest_distill_wait)
   float tau;
   const float* lse;
   const float* weight;
@@ -402,7 +403,8 @@ __host__ __device__ constexpr size_t short_bytes(int top, int log2) {
 //     send to every block of the cluster, then of row i, whose pairs have
 //     arrived meanwhile, the gradient.
 // Waits are for copies, for the other blocks' pairs and for the block's own
-// warps; all are bounded.
+// warps; all are bounded.  Where one runs out, the block's warps leave at their
+// next wait: what they waited for may still be in use.
 //
 // 4096 rows of 129,280 bf16 (2.12 GB): 370 us, 5.7 TB/s, 84 % of a copy's rate.
 // Bound by instructions issued in the two walks, each with an exponential a
@@ -460,10 +462,10 @@ __global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const t
   auto slot = [&](int i) { return reinterpret_cast<uint4*>(smem + head_bytes<kW>(a.top, a.keep, a.table_log2) + (i % a.depth) * static_cast<size_t>(a.slot_bytes)); };
   auto entries = [&](int i) { return Entries(smem + sizeof(Head<kW>) + (i % a.keep) * kEntryBytes * a.top, a.top); };
   auto wait = [&](uint64_t& bar, int use) {
-    if (!mbar_wait_bounded(smem_u32(&bar), use & 1, &h.abort)) {
-      if (a.status != nullptr) atomicOr(a.status, ENGRAM_ST_TIMEOUT);
-      *reinterpret_cast<volatile int*>(&h.abort) = 1;  // the other waits give up too, and the block ends
-    }
+    if (__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar), use & 1, &h.abort))) return true;
+    if (a.status != nullptr) atomicOr(a.status, ENGRAM_ST_TIMEOUT);
+    *reinterpret_cast<volatile int*>(&h.abort) = 1;  // the other waits give up too, and the block ends
+    return false;
   };
 
   if (tid == 0) {
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const t
       if (lane == 0) {
         h.weight[i % a.depth] = w;
         // the pairs of the row: expected before any of this block's own
-        mbar_arrive_expect_tx(smem_u32(&h.met[i % kPairs]), static_cast<uint32_t>(a.cluster) * kW * sizeof(float2));
+        mbar_arrive_expect_tx(smem_u32(&h.met[i % kPairs]), static_cast<uint32_t>(a.cluster) * kW * sizeof(float2) + a.absent);
         const uint32_t bytes = on && r.end() > r.first() ? static_cast<uint32_t>(r.end() - r.first()) * 16u : 0u;
         mbar_arrive_expect_tx(bar, bytes);
         if (bytes > 0) bulk_g2s(smem_u32(s + (r.first() - r.v0)), r.vectors() + r.first(), bytes, bar);
@@ -513,11 +515,12 @@ __global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const t
       }
       if (lane == 0) mbar_arrive(bar);
     };
-    for (int i = 0; i < a.depth && i < n; ++i) copy(i, weight_at(i));
+    int begun = 0;  // copies
+    for (; begun < a.depth && begun < n; ++begun) copy(begun, weight_at(begun));
     float next = weight_at(a.depth);
     for (int i = 0; i < n; ++i) {
       const float ahead = weight_at(i + a.depth + 1);
-      wait(h.walked[i % a.depth], i / a.depth);
+      if (!wait(h.walked[i % a.depth], i / a.depth)) break;
       const float w = h.weight[i % a.depth];
       const float2 teacher = h.teacher[i % a.keep], st = h.stats[i % a.depth];
       const bool none = w == 0.f || teacher.y == 0.f;
@@ -530,9 +533,9 @@ __global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const t
         if (edge >= 0) edge_z = E::load(reinterpret_cast<const typename E::T*>(slot(i)) + (edge + r.off - r.v0 * N));
       }
       __syncwarp();
-      if (i + a.depth < n && !h.abort) copy(i + a.depth, next);
+      if (i + a.depth < n) copy(begun++, next);
       next = ahead;
-      if (dz != nullptr && !none && !h.abort) {
+      if (dz != nullptr && !none) {
         r.at(z, dz, a, row_at(i), rank, true);
         const float scale = w * a.tau, coef = scale * teacher.y / st.y;
         if (edge >= 0) E::store(r.dz + edge, ex2((edge_z - st.x) * c) * coef);
@@ -547,14 +550,14 @@ __global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const t
       if (lane == 0) mbar_arrive(smem_u32(&h.used[i % a.keep]));
     }
     if (h.abort) {  // copies still under way land before the shared memory is released
-      for (int k = 0; k < a.depth; ++k)
-        for (int use = 0; use < 2; ++use) mbar_wait_bounded(smem_u32(&h.full[k]), use, nullptr);
+      for (int i = begun > a.depth ? begun - a.depth : 0; i < begun; ++i)
+        mbar_wait_bounded(smem_u32(&h.full[i % a.depth]), i / a.depth & 1, nullptr);
     }
   } else if (warp > kW) {
     // ---- the teacher's entries, rows in turn
     const int prep = preparing<kW>(a.keep);
     for (int i = warp - kW - 1; warp - kW - 1 < prep && i < n; i += prep) {
-      if (i >= a.keep) wait(h.used[i % a.keep], i / a.keep - 1);
+      if (i >= a.keep && !wait(h.used[i % a.keep], i / a.keep - 1)) break;
       const int64_t row = row_at(i);
       float norm = 0.f, mass = 0.f;
       if (a.weight == nullptr || __ldg(a.weight + row) != 0.f) {
@@ -583,7 +586,7 @@ __global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const t
     };
     Row<E> r;
     auto walk = [&](int i) {
-      wait(h.met[i % kPairs], i / kPairs);
+      if (!wait(h.met[i % kPairs], i / kPairs)) return false;
       float m = -INFINITY, s = 0.f;
       for (int k = lane; k < a.cluster * kW; k += 32) {
         const float2 q = h.pair[i % kPairs][k];
@@ -629,9 +632,11 @@ __global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const t
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&h.walked[i % a.depth]));
+      return true;
     };
+    bool on = n > 0;
     for (int i = 0; i < n; ++i) {
-      wait(h.full[i % a.depth], i / a.depth);
+      if (!(on = wait(h.full[i % a.depth], i / a.depth))) break;
       float m = -INFINITY, s = 0.f;
       r.at(z, dz, a, row_at(i), rank, i > 0);
       if (h.weight[i % a.depth] != 0.f) {
@@ -647,17 +652,22 @@ __global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const t
       }
       // the student's logits of the entries have been read before any block
       // may write this row's gradient over them
-      wait(h.known[i % a.keep], i / a.keep);
+      if (!(on = wait(h.known[i % a.keep], i / a.keep))) break;
       send(i, m, s);
-      if (i > 0) walk(i - 1);
+      if (i > 0 && !(on = walk(i - 1))) break;
     }
-    if (n > 0) walk(n - 1);
+    if (on) walk(n - 1);
   }
   // no block leaves while another one may still send to it
   __syncthreads();
   if (a.cluster > 1) {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  if (h.abort) {  // pairs that it has not waited for may be on their way: they take some microseconds
+    const long long begun = clock64();
+    while (clock64() - begun < (1 << 20)) {
+    }
   }
 }
 
@@ -959,11 +969,11 @@ int launch_distill(const void* z, void* dz, Args a, int sms, cudaStream_t st) {
 
 using namespace engram;
 
-extern "C" int engram_distill(const void* logits_d, int32_t type, int64_t n_tokens, int64_t vocab,
-                              int64_t logits_stride, const int32_t* teacher_ids_d, const float* teacher_logits_d,
-                              int32_t top, float temperature, const float* teacher_lse_d, const float* weight_d,
-                              float* loss_d, void* dlogits_d, int64_t dlogits_stride, int32_t* status_d,
-                              void* stream) {
+namespace {
+int distill(const void* logits_d, int32_t type, int64_t n_tokens, int64_t vocab, int64_t logits_stride,
+            const int32_t* teacher_ids_d, const float* teacher_logits_d, int32_t top, float temperature,
+            const float* teacher_lse_d, const float* weight_d, float* loss_d, void* dlogits_d, int64_t dlogits_stride,
+            int32_t* status_d, void* stream, uint32_t absent) {
   if (!train::known_type(type)) return fail(ENGRAM_E_INVALID, "type %d is not ENGRAM_T_BF16 or ENGRAM_T_F32", type);
   if (n_tokens < 0) return fail(ENGRAM_E_INVALID, "n_tokens < 0");
   if (n_tokens > 0x7fffffff / kMaxCluster) return fail(ENGRAM_E_RANGE, "n_tokens must be below 2^28");
@@ -995,6 +1005,26 @@ extern "C" int engram_distill(const void* logits_d, int32_t type, int64_t n_toke
   a.weight = weight_d;
   a.loss = loss_d;
   a.status = status_d;
+  a.absent = absent;
   return type == ENGRAM_T_BF16 ? launch_distill<train::Bf16>(logits_d, dlogits_d, a, sms, as_stream(stream))
                                : launch_distill<train::F32>(logits_d, dlogits_d, a, sms, as_stream(stream));
+}
+}  // namespace
+
+extern "C" int engram_distill(const void* logits_d, int32_t type, int64_t n_tokens, int64_t vocab,
+                              int64_t logits_stride, const int32_t* teacher_ids_d, const float* teacher_logits_d,
+                              int32_t top, float temperature, const float* teacher_lse_d, const float* weight_d,
+                              float* loss_d, void* dlogits_d, int64_t dlogits_stride, int32_t* status_d,
+                              void* stream) {
+  return distill(logits_d, type, n_tokens, vocab, logits_stride, teacher_ids_d, teacher_logits_d, top, temperature,
+                 teacher_lse_d, weight_d, loss_d, dlogits_d, dlogits_stride, status_d, stream, 0);
+}
+
+extern "C" int engram_selftest_distill_wait(const void* logits_d, int32_t type, int64_t n_tokens, int64_t vocab,
+                                            int64_t logits_stride, const int32_t* teacher_ids_d,
+                                            const float* teacher_logits_d, int32_t top, float* loss_d,
+                                            void* dlogits_d, int64_t dlogits_stride, int32_t* status_d,
+                                            void* stream) {
+  return distill(logits_d, type, n_tokens, vocab, logits_stride, teacher_ids_d, teacher_logits_d, top, 1.f, nullptr,
+                 nullptr, loss_d, dlogits_d, dlogits_stride, status_d, stream, sizeof(float2));
 }

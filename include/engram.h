@@ -736,7 +736,9 @@ int engram_recurrence_step(const void* x_d, int64_t x_stride, const void* g_d, i
  *                    NULL (loss alone); may be logits_d
  * A position of weight 0, or without any teacher mass, gives loss 0 and a
  * zero gradient whatever its logits and its teacher_lse hold.  A student logit of -inf has q = 0.
- * top <= ENGRAM_DISTILL_MAX_TOP, temperature positive and finite. */
+ * top <= ENGRAM_DISTILL_MAX_TOP, temperature positive and finite.  The blocks
+ * that share a row wait for one another; a wait that runs out sets
+ * ENGRAM_ST_TIMEOUT, and losses and gradients are then undefined. */
 #define ENGRAM_DISTILL_MAX_TOP 1024
 int engram_distill(const void* logits_d, int32_t type, int64_t n_tokens, int64_t vocab, int64_t logits_stride,
                    const int32_t* teacher_ids_d, const float* teacher_logits_d, int32_t top, float temperature,
@@ -830,6 +832,15 @@ int engram_selftest_grad_wait(const void* dout_d, int32_t type, int64_t dout_str
                               int64_t n_tokens, int32_t n_cols, int32_t row_dim, int64_t total_rows, int32_t* rows_d,
                               float* grad_d, int32_t* count_d, void* workspace_d, size_t workspace_bytes,
                               int32_t* status_d, void* stream);
+
+/* The same for the waits between the blocks of engram_distill (temperature 1):
+ * every row is expected to have one (maximum, sum) pair more than its blocks send.
+ * Rows of at most 8 KB, and rows too long for eight blocks' shared memory, have no
+ * such wait: with them the call is an ordinary one. */
+int engram_selftest_distill_wait(const void* logits_d, int32_t type, int64_t n_tokens, int64_t vocab,
+                                 int64_t logits_stride, const int32_t* teacher_ids_d, const float* teacher_logits_d,
+                                 int32_t top, float* loss_d, void* dlogits_d, int64_t dlogits_stride,
+                                 int32_t* status_d, void* stream);
 
 /* Thread-local message of the last failure (empty string if none). */
 const char* engram_last_error(void);
