@@ -510,6 +510,8 @@ __global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const t
           const int e = r.edge_element(lane);
           const int at = ((lane < N ? 0 : r.in1) - r.v0) * N + lane % N;
           E::store(reinterpret_cast<typename E::T*>(s) + at, e >= 0 ? E::load(r.z + e) : -INFINITY);
+          // (a later row that lies otherwise has its whole vectors copied over this place)
+          fence_proxy_async_smem();
         }
         __syncwarp();
       }
