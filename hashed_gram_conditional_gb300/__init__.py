@@ -988,6 +988,10 @@ def engram_selftest_mod(layout: Layout, layer: int, x: torch.Tensor) -> torch.Te
 # --------------------------------------------------------------------------- training operators
 
 
+# Values and gradients are calls of their own here.  None of them is an autograd
+# function: whether a tensor requires a gradient is not looked at, nothing is
+# recorded, and backward() does not reach through them.
+
 # The checks below are written for short calls: a tensor that passes costs a
 # few attribute reads, one that does not goes to the function that says why.
 

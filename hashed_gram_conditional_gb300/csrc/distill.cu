@@ -52,9 +52,10 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// 2^x of two values.  (A quarter of the pairs through the FMA units instead, by a
-// sixth-order series, takes 498 us against 418 at 4096 x 129,280 bf16: the walks
-// are bound by instructions issued, not by the exponentials.)
+// 2^x of two values, by the hardware's exponential for either type: results below
+// 2^-126 are zero.  (In an earlier form of the walks a quarter of the pairs through
+// the FMA units, by a sixth-order series, took 498 us against 418 at 4096 x 129,280
+// bf16: they are bound by instructions issued, not by the exponentials.)
 __device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
   float x0, x1;
   f2_split(x, x0, x1);
@@ -408,7 +409,8 @@ __host__ __device__ constexpr size_t short_bytes(int top, int log2) {
 //
 // 4096 rows of 129,280 bf16 (2.12 GB): 370 us, 5.7 TB/s, 84 % of a copy's rate.
 // Bound by instructions issued in the two walks, each with an exponential a
-// value: the loss alone, one walk without stores, takes 280 us.
+// value.  The loss alone, one walk without stores, takes 254 us (4.2 TB/s) through
+// the same slots and pairs, which it could do without.
 constexpr int kPairs = 4;    // rows whose pairs may be under way: see `send`
 // (4096 x 129,280 bf16 with 16 walking warps: 371 us with 4, 366 with 6, 369 with
 // 8; 4096 x 8000 with 4: 50, 53 and 52)
@@ -781,7 +783,6 @@ __global__ void __launch_bounds__(kLongThreads, 3) long_rows_kernel(const typena
 constexpr int kShortWarps = 4;
 constexpr int kShortBytes = 8192;
 
-
 template <class E>
 __global__ void __launch_bounds__(kShortWarps * 32, 8) short_rows_kernel(const typename E::T* z, typename E::T* dz, Args a) {
   constexpr int N = kVec<E>;
@@ -943,7 +944,10 @@ int launch_distill(const void* z, void* dz, Args a, int sms, cudaStream_t st) {
     return launch(short_rows_kernel<E>, std::min<int64_t>(want, static_cast<int64_t>(sms) * 8), kShortWarps * 32,
                   kShortWarps * short_bytes(a.top, a.table_log2), static_cast<const typename E::T*>(z), static_cast<typename E::T*>(dz), a, st);
   }
-  a.keep = a.top <= 128 ? kTeacher : 4;  // fewer where the entries would take the rows' place
+  // fewer where the entries would take the rows' place: 4096 rows of 50,000 bf16 with
+  // 1024 entries take 1950 us with 4 and 2790 with 8 (with 200 entries, where there
+  // still is room, 318 and 222)
+  a.keep = a.top <= 128 ? kTeacher : 4;
   const int64_t room = kSmem - static_cast<int64_t>(head_bytes<16>(a.top, a.keep, a.table_log2));
   // the smallest cluster that holds three rows (four where they fit); of 4 or 8
   // blocks two will do
@@ -952,9 +956,10 @@ int launch_distill(const void* z, void* dz, Args a, int sms, cudaStream_t st) {
     for (a.depth = kMaxDepth; a.depth >= (a.cluster >= 4 ? 2 : 3); --a.depth) {
       if (part * a.depth > room) continue;
       a.slot_bytes = static_cast<int32_t>(part);
-      // warps for the length of their walk: of 16,384 rows of 16,000 bf16 (32 KB)
-      // 8 take 247 and 16 take 350 us, of 4096 rows of 129,280 (64 KB parts) 16
-      // take 401 and 8 take 407
+      // warps for the length of their walk, us with 4, 8 and 16 of them: 16,384 rows of
+      // 5000 bf16 (10 KB) 106, 164 and -, of 8000 131, 177 and -, of 10,000 (20 KB) -,
+      // 189 and 311, of 16,000 -, 344 and 333, of 20,000 (40 KB) -, 359 and 357, 4096 of
+      // 129,280 (64 KB parts) -, 400 and 379 (20 and 64 entries, gradients elsewhere)
       return part <= 16 * 1024   ? launch_rows<E, 4>(z, dz, a, st)
              : part <= 40 * 1024 ? launch_rows<E, 8>(z, dz, a, st)
                                  : launch_rows<E, 16>(z, dz, a, st);

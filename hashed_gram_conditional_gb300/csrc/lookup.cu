@@ -4,9 +4,9 @@
 // G[r] = scale * sum over the entries i with ids[i] == r of dout[i].
 //
 // The gradient sorts the entries by (id, i) with a stable least-significant-
-// digit radix sort, so the entries of a row are neighbours in their original
-// order, and every sum is taken in a fixed order: the result does not change
-// from run to run.
+// digit radix sort (Knuth, The Art of Computer Programming, vol. 3, 5.2.5), so
+// the entries of a row are neighbours in their original order, and every sum is
+// taken in a fixed order: the result does not change from run to run.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -289,8 +289,8 @@ __device__ __forceinline__ void clear_meanwhile(const SortArgs& a, uint32_t* bit
 // Bound by waits, not by bytes: a pass is two barriers, one scattered 8-byte
 // store an entry and the counts in between.  393,216 ids of 26 bits in three
 // passes: 44 us; 16,384 of 17 bits in two, by 16 blocks: 25 us, in which the other
-// blocks clear rows (dense gradient of 16,384 rows of 5120 into 99,092: 353 us
-// without that, 340 with it).
+// blocks clear rows (dense gradient of 16,384 rows of 5120 into 99,092: 348 us
+// without that, 336 with it).
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
   __shared__ __align__(16) uint16_t hist[kSortWarps][kMaxDigits];
   __shared__ int32_t place[kMaxDigits], half[kMaxDigits], warp_sum[kSortWarps];
@@ -671,7 +671,7 @@ __device__ __forceinline__ void no_gradient(const SumArgs<E>& a) {
 //
 // Bound by memory: every entry's row is read once, with the rows of kAhead
 // entries under way, and every row of the result is written once, in whole
-// 32-byte sectors.  393,216 bf16 rows of 256 (201 MB in, 403 MB out): 103 us,
+// 32-byte sectors, the zeros of the rows form behind its count among them.  393,216 bf16 rows of 256 (201 MB in, 403 MB out): 103 us,
 // 5.9 TB/s; 16,384 rows of 5120 into 99,092 (168 MB in, 2.03 GB out): 299 us,
 // 7.3 TB/s.  Four blocks an SM, which 64 registers allow; three are slower.
 template <class E, int kLanes, bool kAligned>
@@ -807,8 +807,10 @@ __global__ void __launch_bounds__(kThreads, 4) seg_sum_kernel(SumArgs<E> a) {
 // if there are many, all warps of the block do: warp w the parts w, w + 16, ...
 // of the segment, then the warps' sums in order.  Bound by the longest segment's
 // chain of loads (12 to 16 us at the sizes above), hence kBatch parts at a time.
-constexpr int kOwnParts = 12;  // parts that one warp adds alone
-constexpr int kJoinWarps = 16;
+constexpr int kOwnParts = 12;  // parts that one warp adds alone (whole calls with 4, 12 and 32: 393,216 rows of 256
+                               // 167, 168 and 171 us, 16,384 of 5120 into 99,092 336, 336 and 342)
+constexpr int kJoinWarps = 16;  // with 8, 16 and 32: 170, 168 and 170 us, 335, 336 and 344; where every entry has one
+                                // id, 393,216 of 256 233, 202 and 198, 5000 of 64 47, 45 and 47
 
 template <class E, bool kAligned>
 __global__ void __launch_bounds__(kJoinWarps * 32) seg_join_kernel(SumArgs<E> a) {
@@ -1118,8 +1120,9 @@ int lanes_for(int32_t dim, int cols) {
 }
 
 // Entries per chunk: the fewest of 16, 32, 64 and 128 that give no more tasks
-// than five quarters of the lane groups that 152 SMs hold (4 blocks of 8
-// warps).  Fewer entries shorten a small call, whose tasks all run at once;
+// than five quarters of the lane groups that 152 SMs hold (4 blocks of 8 warps:
+// 4864, a number here because the workspace's size, which follows from it, is asked
+// for without a device).  Fewer entries shorten a small call, whose tasks all run at once;
 // more entries leave fewer parts to join (393,216 entries of 256 columns with 32,
 // 64 and 128: 193, 182 and 171 us; 16,384 of 5120: 341, 333 and 333).
 int32_t chunk_for(int64_t n, int32_t dim, int cols) {
@@ -1215,7 +1218,8 @@ int lookup_grad(const void* dout_d, int32_t type, int64_t dout_stride, const int
   const int32_t chunk = chunk_for(n, row_dim, type == ENGRAM_T_BF16 ? kCols<train::Bf16> : kCols<train::F32>);
   const int32_t chunks = static_cast<int32_t>((n64 + chunk - 1) / chunk);
   const uint32_t none = static_cast<uint32_t>(total_rows);
-  // 64 KB at least, to hide the search, and no more ranges than needed to spread over the SMs
+  // 64 KB at least, to hide the search, and no more ranges than needed to spread over the SMs; but kMaxRange rows at
+  // most, which are less than 64 KB where a row has fewer than 64 columns
   const int64_t spread = total_rows / (static_cast<int64_t>(sms) * 32), least = std::max((1 << 14) / row_dim, 1);
   const int32_t range = static_cast<int32_t>(std::min<int64_t>(std::max(spread, least), kMaxRange));
   SortArgs sa{};

@@ -412,9 +412,10 @@ __device__ __forceinline__ float join_factor(float p, float A) { return signbit(
 // What comes into the tile at place `pos` of the walk, for one channel: the
 // tiles' maps applied one by one to the value in front of them.  Runs of kRun
 // tiles are joined to one map by their last tile, so that a look back passes
-// over at most kRun - 1 tiles of its own run and then over whole runs.  Every
-// value is built by the same steps in the same order whatever has been
-// published when, so results do not change from run to run.
+// over at most kRun - 1 tiles of its own run and then over whole runs (a scan in
+// one pass by looking back: Merrill and Garland 2016).  Every value is built by
+// the same steps in the same order whatever has been published when, so results
+// do not change from run to run.
 //
 // Tiles take their numbers from a counter in walking order, so every tile that
 // is waited for is already running.  (A, B) is the tile's own map; a warp's
@@ -556,10 +557,10 @@ __device__ __forceinline__ float come_in(const Args<E>& a, int group, int pos, i
 // registers, so that three blocks fit an SM and their loads cover one another's
 // waits.
 //
-// 16,384 x 5120 bf16 (503 MB): 106 us, 4.8 TB/s, 70 % of a copy's rate.  Neither
-// memory nor issue is full (46 % of DRAM, 0.50 instructions a cycle and scheduler
+// 16,384 x 5120 bf16 (503 MB): 107 us, 4.7 TB/s, 69 % of a copy's rate.  Neither
+// memory nor issue is full (46 % of DRAM, 0.48 instructions a cycle and scheduler
 // at half the length); what is left are waits, for the copies and for the tiles
-// before.  Tiles of 64 positions, blocks of 4 warps and runs of 4, 12 or 16
+// before: a block has no loads under way while it looks back and writes.  Tiles of 64 positions, blocks of 4 warps and runs of 4, 12 or 16
 // tiles are slower.
 constexpr int kFwdTile = 128, kBwdTile = ENGRAM_RECURRENCE_TILE;  // a state is saved in front of every backward tile
 static_assert(kFwdTile % kBwdTile == 0, "saved states fall between a forward tile's warps");
@@ -719,8 +720,8 @@ constexpr int kFwdSmem = 2 * kFwdTile * kRowBytes + 2 * kFwdWarps * kGroup<E> * 
 // have to stand for both where one is kept, and telling them apart costs more
 // instructions than a pair's two exponentials and two reciprocals.
 //
-// 16,384 x 5120 bf16 (860 MB with the saved states): 193 us, 4.5 TB/s, 66 % of a
-// copy's rate, at 0.56 instructions a cycle and scheduler and half of DRAM's
+// 16,384 x 5120 bf16 (844 MB with the saved states): 191 us, 4.4 TB/s, 65 % of a
+// copy's rate, at 0.55 instructions a cycle and scheduler and half of DRAM's
 // cycles.  Tiles of 128 positions (one block less an SM) and blocks of 4 warps
 // gain nothing.
 constexpr int kBwdWarps = 8;
