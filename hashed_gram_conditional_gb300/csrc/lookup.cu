@@ -227,11 +227,12 @@ struct SortArgs {
   int32_t* status;
 };
 
+constexpr int32_t kGaveUp = 1 << 30;  // more than any call's tasks (2^25 for 2^37 elements, which fill the memory)
+
 // All blocks meet; false when the wait ran out (the blocks are co-resident, so
 // that means a broken launch).  The list may hold anything then, so the counter
 // of the tasks that follow it is set behind the last of them.  What a block's
 // threads wrote before is released by its first thread, which they meet first.
-constexpr int32_t kGaveUp = 1 << 30;  // more than any call's tasks (2^25 for 2^37 elements, which fill the memory)
 __device__ __forceinline__ bool meet(const SortArgs& a, int32_t& met) {
   __syncthreads();
   if (a.blocks == 1) return true;
