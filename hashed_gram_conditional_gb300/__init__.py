@@ -30,7 +30,8 @@ __all__ = [
     "set_kernel_options", "kernel_options", "sf_cols", "sf_word_index",
     "engram_lookup", "engram_lookup_grad", "engram_lookup_grad_rows", "lookup_grad_workspace",
     "engram_recurrence", "engram_recurrence_grad", "engram_recurrence_step", "recurrence_carry",
-    "recurrence_workspace", "engram_distill",
+    "recurrence_workspace", "engram_distill", "engram_policy",
+    "engram_norm_add", "engram_norm_add_grad", "norm_add_workspace",
 ]
 
 MAX_LAYERS = 8
@@ -159,6 +160,10 @@ _SIGS = {
     "engram_recurrence_grad": [_P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _P, _I64, _P, _P, _P, _P, _P, _I64,
                                _P, _I64, _P, _I64, _P, ctypes.c_size_t, _P, _P],
     "engram_recurrence_step": [_P, _I64, _P, _I64, _I32, _I64, _I32, _P, _P, _P, _I64, _P, _I64, _P, _P],
+    "engram_policy": [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _F32, _F32, _F32, _F32, _P, _P, _P, _P, _I64, _P, _P],
+    "engram_norm_add": [_P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _I32, _F32, _P, _P, _P, _P, _I64, _P, _I64, _P],
+    "engram_norm_add_grad": [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _I32, _F32, _P, _P, _P,
+                             _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, ctypes.c_size_t, _P],
     "engram_distill": [_P, _I32, _I64, _I64, _I64, _P, _P, _I32, _F32, _P, _P, _P, _P, _I64, _P, _P],
 }
 
@@ -191,6 +196,8 @@ def _load():
         lib.engram_recurrence_carry_bytes.argtypes = [_I64, _I32]
         lib.engram_recurrence_workspace_bytes.restype = ctypes.c_size_t
         lib.engram_recurrence_workspace_bytes.argtypes = [_I64, _I32]
+        lib.engram_norm_add_workspace_bytes.restype = ctypes.c_size_t
+        lib.engram_norm_add_workspace_bytes.argtypes = [_I64, _I32]
         lib.engram_layout_size.restype = ctypes.c_size_t
         lib.engram_layout_params_size.restype = ctypes.c_size_t
         if lib.engram_layout_size() != ctypes.sizeof(_Layout) or \
@@ -1326,6 +1333,133 @@ def engram_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logi
     if rc:
         _check(rc, "engram_distill")
     return loss
+
+
+def _call(idx: int, name: str, fn, *args):
+    """An entry point on the device (number idx) of its tensors, which need not be the current one."""
+    if torch.cuda.current_device() == idx:
+        rc = fn(*args, _raw_stream(idx))
+    else:
+        with torch.cuda.device(idx):
+            rc = fn(*args, _raw_stream(idx))
+    if rc:
+        _check(rc, name)
+
+
+def engram_policy(logits: torch.Tensor, ids: torch.Tensor, advantage: torch.Tensor,
+                  old_logp: Optional[torch.Tensor] = None, ref_logp: Optional[torch.Tensor] = None,
+                  clip: Sequence[float] = (0.2, 0.2), kl: float = 0.0, temperature: float = 1.0,
+                  weight: Optional[torch.Tensor] = None, loss: Optional[torch.Tensor] = None,
+                  logp: Optional[torch.Tensor] = None, dlogits: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None):
+    """Clipped policy loss of every position's sampled token, with a KL term towards ref_logp: (loss, logp), both f32
+    [T].  logits bf16 or f32 [T][vocab], ids int32 [T] (negative: no token), advantage, old_logp (None: the ratio is
+    1), ref_logp and weight f32 [T], clip (below 1, above 1).  dlogits [T][vocab], when given, gets the gradient (it
+    may be logits itself)."""
+    L = _lib or _load()
+    ty, idx, T, V, zs = _matrix(logits, "logits")
+    ip = _flat(ids, "ids", torch.int32, logits, idx, T)
+    ap = _flat(advantage, "advantage", torch.float32, logits, idx, T)
+    op = None if old_logp is None else _flat(old_logp, "old_logp", torch.float32, logits, idx, T)
+    rp = None if ref_logp is None else _flat(ref_logp, "ref_logp", torch.float32, logits, idx, T)
+    wp = None if weight is None else _flat(weight, "weight", torch.float32, logits, idx, T)
+    low, high = clip
+    if loss is None:
+        loss = torch.empty(T, dtype=torch.float32, device=logits.device)
+    if logp is None:
+        logp = torch.empty(T, dtype=torch.float32, device=logits.device)
+    lp = _flat(loss, "loss", torch.float32, logits, idx, T)
+    gp = _flat(logp, "logp", torch.float32, logits, idx, T)
+    ds = _rows(dlogits, "dlogits", logits.dtype, logits, idx, T, V) if dlogits is not None else 0
+    _call(idx, "engram_policy", L.engram_policy, logits.data_ptr(), ty, T, V, zs, ip, ap, op, rp, low, high, kl,
+          temperature, wp, lp, gp, _addr(dlogits), ds, _word(status, logits, idx))
+    return loss, logp
+
+
+def _optional_rows(t, name: str, like: torch.Tensor, idx: int, n: int, width: int) -> tuple:
+    """(address, row stride) of a matrix that need not be there."""
+    return (None, 0) if t is None else (t.data_ptr(), _rows(t, name, like.dtype, like, idx, n, width))
+
+
+def _weights(t, name: str, like: torch.Tensor, idx: int, numel: int):
+    return None if t is None else _flat(t, name, torch.float32, like, idx, numel)
+
+
+def engram_norm_add(y: torch.Tensor, w: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                    h: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                    w_next: Optional[torch.Tensor] = None, groups: int = 1, eps: float = 1e-6,
+                    h_out: Optional[torch.Tensor] = None, x: Optional[torch.Tensor] = None):
+    """h + scale * norm(y) * w * silu(gate), and the norm of that for the next block: (h_out, x).
+
+    y, gate and h (None: zeros) bf16 or f32 [n][dim]; the norm is taken over each of `groups` parts of a row; w f32
+    [dim/groups], scale and w_next f32 [dim] (None: ones).  h_out may be h.  x is None unless w_next or x is given."""
+    L = _lib or _load()
+    ty, idx, n, D, ys = _matrix(y, "y")
+    if groups < 1 or D % groups:
+        raise ValueError("groups must divide the rows' width")
+    gp, gs = _optional_rows(gate, "gate", y, idx, n, D)
+    hp, hs = _optional_rows(h, "h", y, idx, n, D)
+    wp = _weights(w, "w", y, idx, D // groups)
+    sp = _weights(scale, "scale", y, idx, D)
+    np = _weights(w_next, "w_next", y, idx, D)
+    if h_out is None:
+        h_out = torch.empty((n, D), dtype=y.dtype, device=y.device)
+    if x is None and w_next is not None:
+        x = torch.empty((n, D), dtype=y.dtype, device=y.device)
+    op, os_ = _optional_rows(h_out, "h_out", y, idx, n, D)
+    xp, xs = _optional_rows(x, "x", y, idx, n, D)
+    _call(idx, "engram_norm_add", L.engram_norm_add, y.data_ptr(), ys, gp, gs, hp, hs, ty, n, D, groups, eps, wp, sp, np,
+          op, os_, xp, xs)
+    return h_out, x
+
+
+def norm_add_workspace(n_rows: int, dim: int, device) -> torch.Tensor:
+    n = _bytes_of("engram_norm_add_workspace_bytes", n_rows, dim)
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+
+
+def engram_norm_add_grad(dh: Optional[torch.Tensor], y: torch.Tensor, w: Optional[torch.Tensor] = None,
+                         gate: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                         h_out: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                         w_next: Optional[torch.Tensor] = None, groups: int = 1, eps: float = 1e-6,
+                         residual: bool = True, dy: Optional[torch.Tensor] = None,
+                         dgate: Optional[torch.Tensor] = None, dres: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None):
+    """The gradients of engram_norm_add: (dy, dgate, dres, dw, dscale, dw_next), None where there is no such input.
+
+    dh and dx: the gradients of h_out and x (either may be None); h_out: what the forward call wrote, needed with dx.
+    dres, the gradient of h, is left out without `residual`; it may be dh itself.  dw, dscale and dw_next are f32."""
+    L = _lib or _load()
+    ty, idx, n, D, ys = _matrix(y, "y")
+    if groups < 1 or D % groups:
+        raise ValueError("groups must divide the rows' width")
+    hp, hs = _optional_rows(dh, "dh", y, idx, n, D)
+    xp, xs = _optional_rows(dx, "dx", y, idx, n, D)
+    gp, gs = _optional_rows(gate, "gate", y, idx, n, D)
+    op, os_ = _optional_rows(h_out, "h_out", y, idx, n, D)
+    wp = _weights(w, "w", y, idx, D // groups)
+    sp = _weights(scale, "scale", y, idx, D)
+    np = _weights(w_next, "w_next", y, idx, D)
+    new = functools.partial(torch.empty, (n, D), dtype=y.dtype, device=y.device)
+    dy = new() if dy is None else dy
+    dgate = new() if dgate is None and gate is not None else dgate
+    dres = new() if dres is None and residual else dres
+    of = functools.partial(torch.empty, dtype=torch.float32, device=y.device)
+    dw = None if w is None else of(D // groups)
+    dscale = None if scale is None else of(D)
+    dw_next = None if w_next is None or dx is None else of(D)
+    if workspace is None:
+        if dw is not None or dscale is not None or dw_next is not None:
+            workspace = norm_add_workspace(n, D, y.device)
+    else:
+        _flat(workspace, "workspace", torch.uint8, y, idx)
+    dyp, dys = _optional_rows(dy, "dy", y, idx, n, D)
+    dgp, dgs = _optional_rows(dgate, "dgate", y, idx, n, D)
+    drp, drs = _optional_rows(dres, "dres", y, idx, n, D)
+    _call(idx, "engram_norm_add_grad", L.engram_norm_add_grad, hp, hs, xp, xs, y.data_ptr(), ys, gp, gs, op, os_, ty, n, D,
+          groups, eps, wp, sp, np, dyp, dys, dgp, dgs, drp, drs, _addr(dw), _addr(dscale), _addr(dw_next),
+          _addr(workspace), 0 if workspace is None else workspace.numel())
+    return dy, dgate, dres, dw, dscale, dw_next
 
 
 # --------------------------------------------------------------------------- layer

@@ -1,0 +1,712 @@
+// The norm behind a block with its gate, the residual add with its scale, and
+// the norm in front of the next block; and the gradient of the three together.
+//
+// With r(u) = (mean(u^2) + eps)^-1/2, over each group of y's row and over h'
+// whole row:
+//   n  = y r(y) w silu(gate)
+//   h' = h + s n                      (rounded to the type)
+//   x  = h' r(h') w_next
+// and, with l the gradient of h' in all, c = (dx w_next . h') r(h')^3 / dim:
+//   l  = dh + dx w_next r(h') - h' c
+//   dn = l s,  dgate = dn y r w silu'(gate),  p = dn silu(gate) w
+//   dy = p r - y r^3 (p . y) / group
+//   dw_next = sum dx h' r(h'),  dscale = sum l n,  dw = sum dn silu(gate) y r
+//
+// Bound by memory: every array is read or written once.  A block holds a row in
+// registers, in 16-byte vectors, from the first sum to the last store; the
+// gradient's blocks stay, go from row to row and keep the weights' sums of
+// their columns in registers.  Rows that are not 16-byte aligned, or longer
+// than a block's registers hold, are walked value by value and read again.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "engram_internal.h"
+#include "train_device.cuh"
+
+namespace engram {
+namespace {
+
+constexpr int kMaxGroups = ENGRAM_NORM_MAX_GROUPS;
+constexpr int kThreads = 512;  // at most, where registers for more than one vector a thread are wanted
+constexpr int kAnyThreads = 256;
+// Blocks that a gradient's sums of the weights are spread over.
+constexpr int kParts = 304;
+
+struct Args {
+  const void *y, *gate, *h, *dh, *dx;
+  void *h_out, *x_out, *dy, *dgate, *dres;
+  int64_t y_stride, gate_stride, h_stride, h_out_stride, x_stride, dh_stride, dx_stride, dy_stride, dgate_stride, dres_stride;
+  const float *w, *scale, *w_next;
+  float* parts;  // [3][blocks][dim]: the sums for w, scale and w_next
+  int64_t rows;
+  int32_t dim, groups, width;  // width: of a group
+  int32_t vecs, vecs_log2;     // 16-byte vectors of a row; log2 of a group's if they are a power of two, else -1
+  float eps;
+};
+
+template <class E>
+constexpr int kVec = 16 / E::kBytes;
+
+template <class E>
+__device__ __forceinline__ void widen(const uint4& x, float (&f)[kVec<E>]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (E::kBytes == 2) {
+      f[2 * j] = __uint_as_float(w[j] << 16);
+      f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    } else {
+      f[j] = __uint_as_float(w[j]);
+    }
+  }
+}
+
+template <class E>
+__device__ __forceinline__ uint4 narrow(const float (&f)[kVec<E>]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (E::kBytes == 2) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+      w[j] = __float_as_uint(f[j]);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <class E>
+__device__ __forceinline__ void load_weights(const float* p, float (&f)[kVec<E>]) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int j = 0; j < kVec<E>; ++j) f[j] = 1.f;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < kVec<E>; j += 4) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p + j));
+    f[j] = x.x;
+    f[j + 1] = x.y;
+    f[j + 2] = x.z;
+    f[j + 3] = x.w;
+  }
+}
+
+// sigmoid(z): bf16's from the hardware's exponential and division (2^-21, far
+// below a bf16 rounding), fp32's from the rounded ones.
+template <class E>
+__device__ __forceinline__ float sigmoid(float z) {
+  if constexpr (E::kBytes == 2) return __fdividef(1.f, 1.f + __expf(-z));
+  return 1.f / (1.f + expf(-z));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The block's sum, the same in every thread.  `slot` has a place for each warp
+// and is free again at the block's next barrier but one.
+__device__ __forceinline__ float block_sum(float v, float* slot) {
+  v = warp_sum(v);
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return v;
+  if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  return warp_sum(lane < warps ? slot[lane] : 0.f);
+}
+
+// The sum over each group of the values that the vectors give, for the groups of
+// this thread's vectors.  Groups of 1, 2, .. 32 vectors are joined among lanes, a
+// row that is one group by the block, and others by way of `part`, which has a
+// place for every vector and is free again at the block's next barrier.
+template <int kPer>
+__device__ __forceinline__ void group_sums(const Args& a, float (&v)[kPer], float* part, float* slot) {
+  if (a.groups == 1) {
+    float all = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) all += v[i];
+    all = block_sum(all, slot);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = all;
+    return;
+  }
+  const int per = a.vecs / a.groups;
+  if (a.vecs_log2 >= 0) {  // lanes of a group lie together: vector t + i * blockDim, and 32 divides blockDim
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      for (int o = per >> 1; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int at = threadIdx.x + i * blockDim.x;
+    if (at < a.vecs) part[at] = v[i];
+  }
+  __syncthreads();
+  float* sums = part + a.vecs;
+  for (int g = threadIdx.x >> 5; g < a.groups; g += blockDim.x >> 5) {
+    float s = 0.f;
+    for (int k = threadIdx.x & 31; k < per; k += 32) s += part[g * per + k];
+    s = warp_sum(s);
+    if ((threadIdx.x & 31) == 0) sums[g] = s;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int at = threadIdx.x + i * blockDim.x;
+    v[i] = at < a.vecs ? sums[at / per] : 0.f;
+  }
+  __syncthreads();
+}
+
+template <class E, class As = typename E::T>
+__device__ __forceinline__ const As* row_of(const void* p, int64_t row, int64_t stride) {
+  return reinterpret_cast<const As*>(static_cast<const typename E::T*>(p) + row * stride);
+}
+template <class E, class As = typename E::T>
+__device__ __forceinline__ As* row_of(void* p, int64_t row, int64_t stride) {
+  return reinterpret_cast<As*>(static_cast<typename E::T*>(p) + row * stride);
+}
+// (cached no longer than the row's own use)
+template <class E>
+__device__ __forceinline__ uint4 vector_at(const void* p, int64_t row, int64_t stride, int v) {
+  return __ldcs(row_of<E, uint4>(p, row, stride) + v);
+}
+
+// ------------------------------------------------------------------- forward
+
+template <class E, int kPer>
+__global__ void __launch_bounds__(kThreads) norm_kernel(Args a) {
+  constexpr int N = kVec<E>;
+  extern __shared__ float part[];
+  __shared__ float slot[2][32];
+  const int64_t row = blockIdx.x;
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  uint4 ry[kPer], rz[kPer], rh[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    ry[i] = v < a.vecs ? vector_at<E>(a.y, row, a.y_stride, v) : none;
+    rz[i] = v < a.vecs && a.gate ? vector_at<E>(a.gate, row, a.gate_stride, v) : none;
+    rh[i] = v < a.vecs && a.h ? vector_at<E>(a.h, row, a.h_stride, v) : none;
+  }
+  float sq[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    float y[N];
+    widen<E>(ry[i], y);
+    sq[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) sq[i] = fmaf(y[j], y[j], sq[i]);
+  }
+  group_sums(a, sq, part, slot[0]);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v >= a.vecs) continue;
+    const float r = rsqrtf(sq[i] / a.width + a.eps);
+    float y[N], h[N], w[N];
+    widen<E>(ry[i], y);
+    widen<E>(rh[i], h);
+    load_weights<E>(a.w ? a.w + v * N % a.width : nullptr, w);
+#pragma unroll
+    for (int j = 0; j < N; ++j) y[j] *= r * w[j];
+    if (a.gate) {
+      float z[N];
+      widen<E>(rz[i], z);
+#pragma unroll
+      for (int j = 0; j < N; ++j) y[j] *= z[j] * sigmoid<E>(z[j]);
+    }
+    load_weights<E>(a.scale ? a.scale + v * N : nullptr, w);
+#pragma unroll
+    for (int j = 0; j < N; ++j) h[j] = fmaf(y[j], w[j], h[j]);
+    rh[i] = narrow<E>(h);
+    row_of<E, uint4>(a.h_out, row, a.h_out_stride)[v] = rh[i];
+    widen<E>(rh[i], h);
+#pragma unroll
+    for (int j = 0; j < N; ++j) sum = fmaf(h[j], h[j], sum);
+  }
+  if (a.x_out == nullptr) return;
+  sum = block_sum(sum, slot[1]);
+  const float r = rsqrtf(sum / a.dim + a.eps);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v >= a.vecs) continue;
+    float h[N], w[N];
+    widen<E>(rh[i], h);
+    load_weights<E>(a.w_next ? a.w_next + v * N : nullptr, w);
+#pragma unroll
+    for (int j = 0; j < N; ++j) h[j] *= r * w[j];
+    row_of<E, uint4>(a.x_out, row, a.x_stride)[v] = narrow<E>(h);
+  }
+}
+
+// r of every group into sums[groups], by the block; a barrier follows.
+template <class E>
+__device__ __forceinline__ void any_groups(const Args& a, const typename E::T* y, float* sums) {
+  for (int g = threadIdx.x >> 5; g < a.groups; g += kAnyThreads / 32) {
+    float s = 0.f;
+    for (int k = threadIdx.x & 31; k < a.width; k += 32) {
+      const float v = E::load(y + static_cast<int64_t>(g) * a.width + k);
+      s = fmaf(v, v, s);
+    }
+    s = warp_sum(s);
+    if ((threadIdx.x & 31) == 0) sums[g] = rsqrtf(s / a.width + a.eps);
+  }
+  __syncthreads();
+}
+
+template <class E>
+__global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(Args a) {
+  __shared__ float sums[kMaxGroups], slot[32];
+  const int64_t row = blockIdx.x;
+  const auto* y = row_of<E>(a.y, row, a.y_stride);
+  auto* out = row_of<E>(a.h_out, row, a.h_out_stride);
+  any_groups<E>(a, y, sums);
+  float sum = 0.f;
+  for (int e = threadIdx.x; e < a.dim; e += kAnyThreads) {
+    const int g = e / a.width;
+    float n = E::load(y + e) * (sums[g] * (a.w ? a.w[e - g * a.width] : 1.f));
+    if (a.gate) {
+      const float z = E::load(row_of<E>(a.gate, row, a.gate_stride) + e);
+      n *= z * sigmoid<E>(z);
+    }
+    const float h = a.h ? E::load(row_of<E>(a.h, row, a.h_stride) + e) : 0.f;
+    E::store(out + e, fmaf(n, a.scale ? a.scale[e] : 1.f, h));
+    const float kept = E::load(out + e);
+    sum = fmaf(kept, kept, sum);
+  }
+  if (a.x_out == nullptr) return;
+  const float r = rsqrtf(block_sum(sum, slot) / a.dim + a.eps);
+  auto* x = row_of<E>(a.x_out, row, a.x_stride);
+  for (int e = threadIdx.x; e < a.dim; e += kAnyThreads)
+    E::store(x + e, E::load(out + e) * (r * (a.w_next ? a.w_next[e] : 1.f)));
+}
+
+// ------------------------------------------------------------------ gradient
+
+template <class E, int kPer, int kMost>
+__global__ void __launch_bounds__(kMost) norm_grad_kernel(Args a) {
+  constexpr int N = kVec<E>;
+  extern __shared__ float part[];
+  __shared__ float slot[4][32];
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  float dw[kPer][N] = {}, ds[kPer][N] = {}, dn[kPer][N] = {};
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    uint4 ry[kPer], rz[kPer], rl[kPer], rh[kPer], rx[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      const bool in = v < a.vecs;
+      ry[i] = in ? vector_at<E>(a.y, row, a.y_stride, v) : none;
+      rh[i] = in && a.dx ? vector_at<E>(a.h, row, a.h_stride, v) : none;
+      rx[i] = in && a.dx ? vector_at<E>(a.dx, row, a.dx_stride, v) : none;
+      rl[i] = in && a.dh ? vector_at<E>(a.dh, row, a.dh_stride, v) : none;
+      rz[i] = in && a.gate ? vector_at<E>(a.gate, row, a.gate_stride, v) : none;
+    }
+    float sq[kPer], l[kPer][N];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      float y[N];
+      widen<E>(ry[i], y);
+      widen<E>(rl[i], l[i]);
+      sq[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) sq[i] = fmaf(y[j], y[j], sq[i]);
+    }
+    if (a.dx) {
+      float hh = 0.f, xh = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (v >= a.vecs) continue;
+        float h[N], x[N], w[N];
+        widen<E>(rh[i], h);
+        widen<E>(rx[i], x);
+        load_weights<E>(a.w_next ? a.w_next + v * N : nullptr, w);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          hh = fmaf(h[j], h[j], hh);
+          xh = fmaf(x[j] * w[j], h[j], xh);
+        }
+      }
+      hh = block_sum(hh, slot[0]);
+      xh = block_sum(xh, slot[1]);
+      const float r = rsqrtf(hh / a.dim + a.eps), c = xh * r * r * r / a.dim;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (v >= a.vecs) continue;
+        float h[N], x[N], w[N];
+        widen<E>(rh[i], h);
+        widen<E>(rx[i], x);
+        load_weights<E>(a.w_next ? a.w_next + v * N : nullptr, w);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          x[j] *= r;
+          l[i][j] += x[j] * w[j] - h[j] * c;
+          dn[i][j] = fmaf(x[j], h[j], dn[i][j]);
+        }
+      }
+    }
+    group_sums(a, sq, part, slot[2]);
+    float along[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      along[i] = 0.f;
+      if (v >= a.vecs) continue;
+      if (a.dres) row_of<E, uint4>(a.dres, row, a.dres_stride)[v] = narrow<E>(l[i]);
+      const float r = rsqrtf(sq[i] / a.width + a.eps);
+      sq[i] = r;
+      float y[N], z[N], w[N], s[N], dz[N];
+      widen<E>(ry[i], y);
+      widen<E>(rz[i], z);
+      load_weights<E>(a.w ? a.w + v * N % a.width : nullptr, w);
+      load_weights<E>(a.scale ? a.scale + v * N : nullptr, s);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float sig = a.gate ? sigmoid<E>(z[j]) : 1.f, act = a.gate ? z[j] * sig : 1.f;
+        const float hat = y[j] * r, g = l[i][j] * s[j];  // g: the gradient of n
+        ds[i][j] = fmaf(l[i][j], hat * w[j] * act, ds[i][j]);
+        dw[i][j] = fmaf(g * act, hat, dw[i][j]);
+        dz[j] = g * hat * w[j] * sig * fmaf(z[j], 1.f - sig, 1.f);
+        l[i][j] = g * act * w[j];
+        along[i] = fmaf(l[i][j], y[j], along[i]);
+      }
+      if (a.dgate) row_of<E, uint4>(a.dgate, row, a.dgate_stride)[v] = narrow<E>(dz);
+    }
+    group_sums(a, along, part, slot[3]);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v >= a.vecs) continue;
+      const float r = sq[i], c = along[i] * r * r * r / a.width;
+      float y[N];
+      widen<E>(ry[i], y);
+#pragma unroll
+      for (int j = 0; j < N; ++j) l[i][j] = l[i][j] * r - y[j] * c;
+      row_of<E, uint4>(a.dy, row, a.dy_stride)[v] = narrow<E>(l[i]);
+    }
+  }
+  if (a.parts == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v >= a.vecs) continue;
+    float* to = a.parts + static_cast<int64_t>(blockIdx.x) * a.dim + v * N;
+    const int64_t next = static_cast<int64_t>(gridDim.x) * a.dim;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      to[j] = dw[i][j];
+      to[next + j] = ds[i][j];
+      to[2 * next + j] = dn[i][j];
+    }
+  }
+}
+
+template <class E>
+__global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(Args a) {
+  __shared__ float sums[kMaxGroups], along[kMaxGroups], slot[2][32];
+  const int64_t next = static_cast<int64_t>(gridDim.x) * a.dim;
+  float* to = a.parts ? a.parts + static_cast<int64_t>(blockIdx.x) * a.dim : nullptr;
+  for (int e = threadIdx.x; to && e < a.dim; e += kAnyThreads) to[e] = to[next + e] = to[2 * next + e] = 0.f;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const auto* y = row_of<E>(a.y, row, a.y_stride);
+    __syncthreads();  // the last row's sums are no longer read
+    any_groups<E>(a, y, sums);
+    float r2 = 0.f, c2 = 0.f;
+    if (a.dx) {
+      float hh = 0.f, xh = 0.f;
+      for (int e = threadIdx.x; e < a.dim; e += kAnyThreads) {
+        const float h = E::load(row_of<E>(a.h, row, a.h_stride) + e);
+        hh = fmaf(h, h, hh);
+        xh = fmaf(E::load(row_of<E>(a.dx, row, a.dx_stride) + e) * (a.w_next ? a.w_next[e] : 1.f), h, xh);
+      }
+      hh = block_sum(hh, slot[0]);
+      xh = block_sum(xh, slot[1]);
+      r2 = rsqrtf(hh / a.dim + a.eps);
+      c2 = xh * r2 * r2 * r2 / a.dim;
+    }
+    // the gradient of h', and from it that of y r w
+    auto at = [&](int e, float& l, float& p, float& sig, float& act, float& z) {
+      l = a.dh ? E::load(row_of<E>(a.dh, row, a.dh_stride) + e) : 0.f;
+      if (a.dx)
+        l += E::load(row_of<E>(a.dx, row, a.dx_stride) + e) * (a.w_next ? a.w_next[e] : 1.f) * r2 -
+             E::load(row_of<E>(a.h, row, a.h_stride) + e) * c2;
+      z = a.gate ? E::load(row_of<E>(a.gate, row, a.gate_stride) + e) : 0.f;
+      sig = a.gate ? sigmoid<E>(z) : 1.f;
+      act = a.gate ? z * sig : 1.f;
+      p = l * (a.scale ? a.scale[e] : 1.f);
+    };
+    for (int g = threadIdx.x >> 5; g < a.groups; g += kAnyThreads / 32) {
+      float s = 0.f;
+      for (int k = threadIdx.x & 31; k < a.width; k += 32) {
+        const int e = g * a.width + k;
+        float l, p, sig, act, z;
+        at(e, l, p, sig, act, z);
+        s = fmaf(p * act * (a.w ? a.w[k] : 1.f), E::load(y + e), s);
+      }
+      s = warp_sum(s);
+      if ((threadIdx.x & 31) == 0) along[g] = s;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.dim; e += kAnyThreads) {
+      const int g = e / a.width;
+      float l, p, sig, act, z;
+      at(e, l, p, sig, act, z);
+      const float r = sums[g], v = E::load(y + e), hat = v * r, w = a.w ? a.w[e - g * a.width] : 1.f;
+      if (to) {
+        to[e] = fmaf(p * act, hat, to[e]);
+        to[next + e] = fmaf(l, hat * w * act, to[next + e]);
+        if (a.dx)
+          to[2 * next + e] = fmaf(E::load(row_of<E>(a.dx, row, a.dx_stride) + e) * r2,
+                                  E::load(row_of<E>(a.h, row, a.h_stride) + e), to[2 * next + e]);
+      }
+      if (a.dres) E::store(row_of<E>(a.dres, row, a.dres_stride) + e, l);
+      if (a.dgate) E::store(row_of<E>(a.dgate, row, a.dgate_stride) + e, p * hat * w * sig * fmaf(z, 1.f - sig, 1.f));
+      E::store(row_of<E>(a.dy, row, a.dy_stride) + e, p * act * w * r - v * (along[g] * r * r * r / a.width));
+    }
+  }
+}
+
+// The blocks' sums joined in order: columns by 32 threads, blocks (and groups, for
+// w) by 8, whose sums are then added.
+__global__ void __launch_bounds__(256) norm_join_kernel(const float* parts, int blocks, int dim, int width, float* dw,
+                                                        float* ds, float* dn) {
+  __shared__ float sum[8][33];
+  float* out = blockIdx.y == 0 ? dw : blockIdx.y == 1 ? ds : dn;
+  const int cols = blockIdx.y == 0 ? width : dim;
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  if (out == nullptr || static_cast<int>(blockIdx.x) * 32 >= cols) return;
+  const float* from = parts + static_cast<int64_t>(blockIdx.y) * blocks * dim;
+  float s = 0.f;
+  if (c < cols)
+    for (int k = threadIdx.y; k < blocks; k += 8)
+      for (int e = c; e < dim; e += cols) s += from[static_cast<int64_t>(k) * dim + e];
+  sum[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y != 0 || c >= cols) return;
+#pragma unroll
+  for (int k = 1; k < 8; ++k) s += sum[k][threadIdx.x];
+  out[c] = s;
+}
+
+// -------------------------------------------------------------------- launch
+
+// Vectors that a thread of a block of at most kThreads holds; 0: the row is too long.
+int per_thread(int vecs, int most) {
+  for (int per = 1; per <= most; per *= 2)
+    if (vecs <= per * kThreads) return per;
+  return 0;
+}
+
+template <class E>
+bool by_vectors(const Args& a, bool grad) {
+  auto ok = [](const void* p, int64_t stride) { return p == nullptr || (aligned(p, 16) && stride * E::kBytes % 16 == 0); };
+  return a.width % kVec<E> == 0 && ok(a.y, a.y_stride) && ok(a.gate, a.gate_stride) && ok(a.h, a.h_stride) &&
+         ok(a.dh, a.dh_stride) && ok(a.dx, a.dx_stride) && ok(a.h_out, a.h_out_stride) && ok(a.x_out, a.x_stride) &&
+         ok(a.dy, a.dy_stride) && ok(a.dgate, a.dgate_stride) && ok(a.dres, a.dres_stride) && aligned(a.w, 16) &&
+         aligned(a.scale, 16) && aligned(a.w_next, 16) && per_thread(a.dim / kVec<E>, 4) != 0;
+}
+
+template <class E>
+void set_vecs(Args& a) {
+  a.vecs = a.dim / kVec<E>;
+  const int per = a.vecs / a.groups;
+  a.vecs_log2 = -1;
+  for (int k = 0; k <= 5; ++k)
+    if (per == 1 << k) a.vecs_log2 = k;
+}
+
+template <class E>
+int launch_norm(Args a, cudaStream_t st) {
+  const unsigned rows = static_cast<unsigned>(a.rows);
+  if (!by_vectors<E>(a, false)) {
+    norm_any_kernel<E><<<rows, kAnyThreads, 0, st>>>(a);
+    return check_launch("norm_any_kernel");
+  }
+  set_vecs<E>(a);
+  const int per = per_thread(a.vecs, 4), threads = ((a.vecs + per - 1) / per + 31) / 32 * 32;
+  const size_t smem = a.groups > 1 && a.vecs_log2 < 0 ? sizeof(float) * (a.vecs + a.groups) : 0;
+  if (per == 1) norm_kernel<E, 1><<<rows, threads, smem, st>>>(a);
+  else if (per == 2) norm_kernel<E, 2><<<rows, threads, smem, st>>>(a);
+  else norm_kernel<E, 4><<<rows, threads, smem, st>>>(a);
+  return check_launch("norm_kernel");
+}
+
+template <class E>
+int launch_grad(Args a, float* dw, float* ds, float* dn, int sms, cudaStream_t st) {
+  const int blocks = static_cast<int>(std::min<int64_t>(a.rows, std::min(kParts, 2 * sms)));
+  if (blocks > 0) {
+    if (!by_vectors<E>(a, true)) {
+      norm_grad_any_kernel<E><<<blocks, kAnyThreads, 0, st>>>(a);
+    } else {
+      set_vecs<E>(a);
+      // two vectors a thread at most: the sums of four's columns would not fit the registers
+      const int per = std::min(2, per_thread(a.vecs, 4)), threads = ((a.vecs + per - 1) / per + 31) / 32 * 32;
+      const size_t smem = a.groups > 1 && a.vecs_log2 < 0 ? sizeof(float) * (a.vecs + a.groups) : 0;
+      if (per == 1) norm_grad_kernel<E, 1, kThreads><<<blocks, threads, smem, st>>>(a);
+      else if (threads <= kThreads) norm_grad_kernel<E, 2, kThreads><<<blocks, threads, smem, st>>>(a);
+      else norm_grad_kernel<E, 2, 2 * kThreads><<<blocks, threads, smem, st>>>(a);
+    }
+    int rc = check_launch("norm_grad_kernel");
+    if (rc) return rc;
+  }
+  if (a.parts == nullptr) return ENGRAM_OK;
+  norm_join_kernel<<<dim3((a.dim + 31) / 32, 3), dim3(32, 8), 0, st>>>(a.parts, blocks, a.dim, a.width, dw, ds, dn);
+  return check_launch("norm_join_kernel");
+}
+
+int check_sizes(int32_t type, int64_t n_rows, int32_t dim, int32_t groups, float eps) {
+  if (!train::known_type(type)) return fail(ENGRAM_E_INVALID, "type %d is not ENGRAM_T_BF16 or ENGRAM_T_F32", type);
+  if (n_rows < 0) return fail(ENGRAM_E_INVALID, "n_rows < 0");
+  if (n_rows > 0x7fffffff) return fail(ENGRAM_E_RANGE, "n_rows must be below 2^31");
+  if (dim < 1 || dim > 0x1000000) return fail(ENGRAM_E_SHAPE, "dim must be in [1, 2^24]");
+  if (groups < 1 || groups > kMaxGroups || dim % groups != 0)
+    return fail(ENGRAM_E_SHAPE, "groups must divide dim and be in [1, %d]", kMaxGroups);
+  if (!(eps >= 0.f) || eps > 3.0e38f) return fail(ENGRAM_E_INVALID, "eps must be finite and not negative");
+  return ENGRAM_OK;
+}
+
+int check_rows(const void* p, int32_t type, int64_t stride, int32_t dim, const char* name, bool needed) {
+  if (p == nullptr) return needed ? fail(ENGRAM_E_INVALID, "null device pointer: %s", name) : ENGRAM_OK;
+  if (stride < dim) return fail(ENGRAM_E_SHAPE, "%s: row stride below dim", name);
+  if (!aligned(p, train::type_bytes(type))) return fail(ENGRAM_E_ALIGN, "%s must be aligned to its elements", name);
+  return ENGRAM_OK;
+}
+
+int check_weights(const float* w, const float* scale, const float* w_next) {
+  if (!aligned(w, 4) || !aligned(scale, 4) || !aligned(w_next, 4))
+    return fail(ENGRAM_E_ALIGN, "w, scale and w_next must be aligned to their elements");
+  return ENGRAM_OK;
+}
+
+}  // namespace
+}  // namespace engram
+
+using namespace engram;
+
+extern "C" int engram_norm_add(const void* y_d, int64_t y_stride, const void* gate_d, int64_t gate_stride,
+                               const void* h_d, int64_t h_stride, int32_t type, int64_t n_rows, int32_t dim,
+                               int32_t groups, float eps, const float* w_d, const float* scale_d,
+                               const float* w_next_d, void* h_out_d, int64_t h_out_stride, void* x_d,
+                               int64_t x_stride, void* stream) {
+  int rc = check_sizes(type, n_rows, dim, groups, eps);
+  if (rc) return rc;
+  if (n_rows == 0) return ENGRAM_OK;
+  if ((rc = check_rows(y_d, type, y_stride, dim, "y", true))) return rc;
+  if ((rc = check_rows(gate_d, type, gate_stride, dim, "gate", false))) return rc;
+  if ((rc = check_rows(h_d, type, h_stride, dim, "h", false))) return rc;
+  if ((rc = check_rows(h_out_d, type, h_out_stride, dim, "h_out", true))) return rc;
+  if ((rc = check_rows(x_d, type, x_stride, dim, "x", false))) return rc;
+  if ((rc = check_weights(w_d, scale_d, w_next_d))) return rc;
+  if (h_out_d == h_d && h_out_stride != h_stride) return fail(ENGRAM_E_SHAPE, "in place, h_out has the stride of h");
+  if ((rc = check_device(nullptr))) return rc;
+  Args a{};
+  a.y = y_d;
+  a.gate = gate_d;
+  a.h = h_d;
+  a.h_out = h_out_d;
+  a.x_out = x_d;
+  a.y_stride = y_stride;
+  a.gate_stride = gate_stride;
+  a.h_stride = h_stride;
+  a.h_out_stride = h_out_stride;
+  a.x_stride = x_stride;
+  a.w = w_d;
+  a.scale = scale_d;
+  a.w_next = w_next_d;
+  a.rows = n_rows;
+  a.dim = dim;
+  a.groups = groups;
+  a.width = dim / groups;
+  a.eps = eps;
+  return type == ENGRAM_T_BF16 ? launch_norm<train::Bf16>(a, as_stream(stream))
+                               : launch_norm<train::F32>(a, as_stream(stream));
+}
+
+extern "C" size_t engram_norm_add_workspace_bytes(int64_t n_rows, int32_t dim) {
+  if (n_rows < 0 || dim < 1) return 0;
+  return sizeof(float) * 3 * static_cast<size_t>(std::min<int64_t>(n_rows, kParts)) * dim;
+}
+
+extern "C" int engram_norm_add_grad(const void* dh_d, int64_t dh_stride, const void* dx_d, int64_t dx_stride,
+                                    const void* y_d, int64_t y_stride, const void* gate_d, int64_t gate_stride,
+                                    const void* h_out_d, int64_t h_out_stride, int32_t type, int64_t n_rows,
+                                    int32_t dim, int32_t groups, float eps, const float* w_d, const float* scale_d,
+                                    const float* w_next_d, void* dy_d, int64_t dy_stride, void* dgate_d,
+                                    int64_t dgate_stride, void* dres_d, int64_t dres_stride, float* dw_d,
+                                    float* dscale_d, float* dw_next_d, void* workspace_d, size_t workspace_bytes,
+                                    void* stream) {
+  int rc = check_sizes(type, n_rows, dim, groups, eps);
+  if (rc) return rc;
+  const bool sums = dw_d || dscale_d || dw_next_d;
+  if (n_rows > 0) {
+    if (!dh_d && !dx_d) return fail(ENGRAM_E_INVALID, "neither dh nor dx");
+    if ((rc = check_rows(dh_d, type, dh_stride, dim, "dh", false))) return rc;
+    if ((rc = check_rows(dx_d, type, dx_stride, dim, "dx", false))) return rc;
+    if ((rc = check_rows(y_d, type, y_stride, dim, "y", true))) return rc;
+    if ((rc = check_rows(gate_d, type, gate_stride, dim, "gate", dgate_d != nullptr))) return rc;
+    if ((rc = check_rows(h_out_d, type, h_out_stride, dim, "h_out", dx_d != nullptr))) return rc;
+    if ((rc = check_rows(dy_d, type, dy_stride, dim, "dy", true))) return rc;
+    if ((rc = check_rows(dgate_d, type, dgate_stride, dim, "dgate", false))) return rc;
+    if ((rc = check_rows(dres_d, type, dres_stride, dim, "dres", false))) return rc;
+    if (dres_d == dh_d && dres_d && dres_stride != dh_stride)
+      return fail(ENGRAM_E_SHAPE, "in place, dres has the stride of dh");
+    if (sums) {
+      if (!workspace_d) return fail(ENGRAM_E_INVALID, "null device pointer: workspace");
+      if (!aligned(workspace_d, 256)) return fail(ENGRAM_E_ALIGN, "workspace must be 256-byte aligned");
+      if (workspace_bytes < engram_norm_add_workspace_bytes(n_rows, dim))
+        return fail(ENGRAM_E_RANGE, "workspace too small");
+    }
+  }
+  if ((rc = check_weights(w_d, scale_d, w_next_d))) return rc;
+  if ((rc = check_weights(dw_d, dscale_d, dw_next_d))) return rc;
+  if (n_rows == 0 && !sums) return ENGRAM_OK;
+  int sms = 0;
+  if ((rc = check_device(&sms))) return rc;
+  Args a{};
+  a.y = y_d;
+  a.gate = gate_d;
+  a.h = dx_d ? h_out_d : nullptr;
+  a.dh = dh_d;
+  a.dx = dx_d;
+  a.dy = dy_d;
+  a.dgate = dgate_d;
+  a.dres = dres_d;
+  a.y_stride = y_stride;
+  a.gate_stride = gate_stride;
+  a.h_stride = h_out_stride;
+  a.dh_stride = dh_stride;
+  a.dx_stride = dx_stride;
+  a.dy_stride = dy_stride;
+  a.dgate_stride = dgate_stride;
+  a.dres_stride = dres_stride;
+  a.w = w_d;
+  a.scale = scale_d;
+  a.w_next = w_next_d;
+  a.parts = sums ? static_cast<float*>(workspace_d) : nullptr;
+  a.rows = n_rows;
+  a.dim = dim;
+  a.groups = groups;
+  a.width = dim / groups;
+  a.eps = eps;
+  if (n_rows == 0) {  // sums of nothing
+    float* const out[3] = {dw_d, dscale_d, dw_next_d};
+    for (int k = 0; k < 3; ++k)
+      if (out[k] && cudaMemsetAsync(out[k], 0, sizeof(float) * (k == 0 ? a.width : dim), as_stream(stream)) != cudaSuccess)
+        return check_launch("cudaMemsetAsync");
+    return ENGRAM_OK;
+  }
+  return type == ENGRAM_T_BF16 ? launch_grad<train::Bf16>(a, dw_d, dscale_d, dw_next_d, sms, as_stream(stream))
+                               : launch_grad<train::F32>(a, dw_d, dscale_d, dw_next_d, sms, as_stream(stream));
+}

@@ -746,6 +746,90 @@ int engram_distill(const void* logits_d, int32_t type, int64_t n_tokens, int64_t
                    int64_t dlogits_stride, int32_t* status_d, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Policy loss of sampled tokens                                              */
+/* ------------------------------------------------------------------------ */
+
+/* For a model trained on rewards: the clipped loss of the tokens it has sampled,
+ * with a KL term towards a reference.  Per position, with q = softmax(z / tau), l =
+ * ln q_id, r = exp(l - old_logp) (1 without old_logp: the tokens are these very
+ * weights' own) and d = ref_logp - l:
+ *   loss = w (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl (e^d - 1 - d))
+ *   dz_v = dloss/dl ([v = id] - q_v) / tau
+ * where the clipped product is the smaller one its part of dloss/dl is 0.
+ *   logits_d     [n_tokens][vocab] of `type`, rows logits_stride apart
+ *   ids_d        int32 [n_tokens], the sampled tokens; a negative id is a position
+ *                without one (a prompt's), an id >= vocab is the same and sets
+ *                ENGRAM_ST_BAD_TOKEN
+ *   advantage_d  float32 [n_tokens] (A)
+ *   old_logp_d   float32 [n_tokens] or NULL
+ *   ref_logp_d   float32 [n_tokens] or NULL; needed if kl > 0, not read if kl = 0
+ *   weight_d     float32 [n_tokens] or NULL (1)
+ *   loss_d       float32 [n_tokens]
+ *   logp_d       float32 [n_tokens], l, or NULL
+ *   dlogits_d    [n_tokens][vocab] of `type`, rows dlogits_stride apart, or NULL
+ *                (loss alone); may be logits_d
+ * A position of weight 0, or without a token, is not read: its loss, l and gradient are
+ * 0.  A logit of -inf has q = 0.  temperature positive and finite, kl and
+ * the clip bounds finite and not negative.  The blocks that share a row wait for one
+ * another; a wait that runs out sets ENGRAM_ST_TIMEOUT, and the outputs are then
+ * undefined. */
+int engram_policy(const void* logits_d, int32_t type, int64_t n_tokens, int64_t vocab, int64_t logits_stride,
+                  const int32_t* ids_d, const float* advantage_d, const float* old_logp_d, const float* ref_logp_d,
+                  float clip_low, float clip_high, float kl, float temperature, const float* weight_d, float* loss_d,
+                  float* logp_d, void* dlogits_d, int64_t dlogits_stride, int32_t* status_d, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Norms around a block, with its gate and residual scale                     */
+/* ------------------------------------------------------------------------ */
+
+/* What lies between one block and the next.  With r(u) = (mean(u^2) + eps)^-1/2:
+ *   n  = y r(y) w silu(gate)     r(y) over each of `groups` equal parts of y's row
+ *   h' = h + scale n             rounded to `type`: the residual stream
+ *   x  = h' r(h') w_next         r(h') over the whole row: the next block's input
+ * Sums and products are fp32.
+ *   y_d       [n_rows][dim] of `type`, rows y_stride elements apart
+ *   gate_d    the same, or NULL (no gate)
+ *   h_d       the same, or NULL (0: no residual)
+ *   w_d       float32 [dim/groups], the same for every group, or NULL (1)
+ *   scale_d   float32 [dim] or NULL (1)
+ *   w_next_d  float32 [dim] or NULL (1); of no use without x_d
+ *   h_out_d   [n_rows][dim]; may be h_d with its stride
+ *   x_d       [n_rows][dim] or NULL (no norm in front of the next block)
+ * groups divides dim and is at most ENGRAM_NORM_MAX_GROUPS.  Any dim up to 2^24 and
+ * element-aligned pointers; outputs overlap no input (but h_out_d may be h_d) and not
+ * one another. */
+#define ENGRAM_NORM_MAX_GROUPS 1024
+int engram_norm_add(const void* y_d, int64_t y_stride, const void* gate_d, int64_t gate_stride, const void* h_d,
+                    int64_t h_stride, int32_t type, int64_t n_rows, int32_t dim, int32_t groups, float eps,
+                    const float* w_d, const float* scale_d, const float* w_next_d, void* h_out_d,
+                    int64_t h_out_stride, void* x_d, int64_t x_stride, void* stream);
+
+/* The gradients of engram_norm_add.  With l the gradient of h' in all:
+ *   l  = dh + dx w_next r(h') - h' r(h')^3 mean(dx w_next h'),   dres = l
+ *   dn = l scale,  dgate = dn y r(y) w silu'(gate),  p = dn silu(gate) w
+ *   dy = p r(y) - y r(y)^3 mean(p y)                (means over the group)
+ *   dw = sum dn silu(gate) y r(y),  dscale = sum l n,  dw_next = sum dx h' r(h')
+ *   dh_d      [n_rows][dim], the gradient of h_out, or NULL (0)
+ *   dx_d      [n_rows][dim], the gradient of x, or NULL (there was no x); one of the
+ *             two is needed
+ *   h_out_d   what the forward call wrote; needed with dx_d
+ *   dy_d      [n_rows][dim]
+ *   dgate_d   [n_rows][dim] or NULL; needs gate_d
+ *   dres_d    [n_rows][dim], the gradient of h_d, or NULL; may be dh_d with its stride
+ *   dw_d      float32 [dim/groups], dscale_d, dw_next_d float32 [dim], each or NULL
+ *   workspace_d  engram_norm_add_workspace_bytes(...) bytes, 256-byte aligned, needed
+ *             for the last three; its contents on entry do not matter
+ * The sums over rows are taken in a fixed order: results are the same from run to run. */
+size_t engram_norm_add_workspace_bytes(int64_t n_rows, int32_t dim);
+int engram_norm_add_grad(const void* dh_d, int64_t dh_stride, const void* dx_d, int64_t dx_stride, const void* y_d,
+                         int64_t y_stride, const void* gate_d, int64_t gate_stride, const void* h_out_d,
+                         int64_t h_out_stride, int32_t type, int64_t n_rows, int32_t dim, int32_t groups, float eps,
+                         const float* w_d, const float* scale_d, const float* w_next_d, void* dy_d,
+                         int64_t dy_stride, void* dgate_d, int64_t dgate_stride, void* dres_d, int64_t dres_stride,
+                         float* dw_d, float* dscale_d, float* dw_next_d, void* workspace_d, size_t workspace_bytes,
+                         void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Kernel selection                                                           */
 /* ------------------------------------------------------------------------ */
 
