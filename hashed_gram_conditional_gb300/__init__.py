@@ -32,6 +32,7 @@ __all__ = [
     "engram_recurrence", "engram_recurrence_grad", "engram_recurrence_step", "recurrence_carry",
     "recurrence_workspace", "engram_distill", "engram_policy",
     "engram_norm_add", "engram_norm_add_grad", "norm_add_workspace",
+    "engram_delta", "engram_delta_step", "delta_carry", "delta_workspace",
 ]
 
 MAX_LAYERS = 8
@@ -160,6 +161,10 @@ _SIGS = {
     "engram_recurrence_grad": [_P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _P, _I64, _P, _P, _P, _P, _P, _I64,
                                _P, _I64, _P, _I64, _P, ctypes.c_size_t, _P, _P],
     "engram_recurrence_step": [_P, _I64, _P, _I64, _I32, _I64, _I32, _P, _P, _P, _I64, _P, _I64, _P, _P],
+    "engram_delta": [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _I32, _I32, _I32, _F32, _P, _I64,
+                     _P, _P, _P, _P, _I64, _P, _I64, _P, _P, ctypes.c_size_t, _P, _P],
+    "engram_delta_step": [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _I32, _I32, _I32, _F32, _P,
+                          _P, _P, _I64, _P, _I64, _P, _P],
     "engram_policy": [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _F32, _F32, _F32, _F32, _P, _P, _P, _P, _I64, _P, _P],
     "engram_norm_add": [_P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _I32, _F32, _P, _P, _P, _P, _I64, _P, _I64, _P],
     "engram_norm_add_grad": [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _I32, _F32, _P, _P, _P,
@@ -196,6 +201,10 @@ def _load():
         lib.engram_recurrence_carry_bytes.argtypes = [_I64, _I32]
         lib.engram_recurrence_workspace_bytes.restype = ctypes.c_size_t
         lib.engram_recurrence_workspace_bytes.argtypes = [_I64, _I32]
+        lib.engram_delta_carry_bytes.restype = ctypes.c_size_t
+        lib.engram_delta_carry_bytes.argtypes = [_I64, _I64, _I32, _I32, _I32]
+        lib.engram_delta_workspace_bytes.restype = ctypes.c_size_t
+        lib.engram_delta_workspace_bytes.argtypes = [_I64, _I64, _I32, _I32, _I32, _I32, _I32]
         lib.engram_norm_add_workspace_bytes.restype = ctypes.c_size_t
         lib.engram_norm_add_workspace_bytes.argtypes = [_I64, _I32]
         lib.engram_layout_size.restype = ctypes.c_size_t
@@ -1344,6 +1353,121 @@ def _call(idx: int, name: str, fn, *args):
             rc = fn(*args, _raw_stream(idx))
     if rc:
         _check(rc, name)
+
+
+def delta_carry(n_tokens: int, n_seqs: int, key_heads: int, heads: int, dk: int, dv: int, device) -> torch.Tensor:
+    """Buffer for the states that engram_delta saves for its backward pass."""
+    n = _bytes_of("engram_delta_carry_bytes", n_tokens, n_seqs, heads, dk, dv) // 4
+    return torch.empty(max(n, 1), dtype=torch.float32, device=device)
+
+
+def delta_workspace(n_tokens: int, n_seqs: int, key_heads: int, heads: int, dk: int, dv: int, device,
+                    backward: bool = False) -> torch.Tensor:
+    n = _bytes_of("engram_delta_workspace_bytes", n_tokens, n_seqs, key_heads, heads, dk, dv, int(backward))
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+
+
+def _delta_inputs(q, k, v, g, b, key_heads: int) -> tuple:
+    """(device number, T, (key heads, heads, dk, dv), the C arguments from q to dv) of the delta rule's inputs."""
+    ty, idx, T, width, qs = _matrix(q, "q")
+    if key_heads < 1 or width % key_heads or width == 0:
+        raise ValueError("q must be [T][key_heads*dk]")
+    if not isinstance(g, torch.Tensor) or g.dim() != 2 or not isinstance(v, torch.Tensor) or v.dim() != 2:
+        raise ValueError("g must be [T][heads] and v [T][heads*dv]")
+    H = g.shape[1]
+    if H < 1 or H % key_heads or v.shape[1] % H or v.shape[1] == 0:
+        raise ValueError("heads must be a multiple of key_heads, and v [T][heads*dv]")
+    ks = _rows(k, "k", q.dtype, q, idx, T, width)
+    vs = _rows(v, "v", q.dtype, q, idx, T, v.shape[1])
+    gs = _rows(g, "g", q.dtype, q, idx, T, H)
+    bs = _rows(b, "b", q.dtype, q, idx, T, H)
+    shape = (key_heads, H, width // key_heads, v.shape[1] // H)
+    return idx, T, shape, (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, g.data_ptr(), gs, b.data_ptr(), bs, ty, T,
+                           *shape)
+
+
+def _delta_state(s, name: str, like: torch.Tensor, idx: int, shape: tuple, n_slots: int = 0) -> int:
+    """Checks a matrix state [n_slots][heads][dk][dv]; returns its n_slots."""
+    _flat(s, name, torch.float32, like, idx)
+    if s.dim() != 4 or tuple(s.shape[1:]) != shape[1:] or (n_slots and s.shape[0] != n_slots):
+        raise ValueError(f"{name} must be [n_slots][heads][dk][dv]")
+    return s.shape[0]
+
+
+def _delta_sequences(cu_seqlens, mask, slots, n_slots: int, like: torch.Tensor, idx: int, T: int) -> int:
+    """Checks what says which positions belong together; returns n_seqs."""
+    _flat(cu_seqlens, "cu_seqlens", torch.int64, like, idx)
+    n_seqs = cu_seqlens.numel() - 1
+    if n_seqs < 0:
+        raise ValueError("cu_seqlens must be [n_seqs+1]")
+    if mask is not None:
+        _flat(mask, "mask", torch.uint8, like, idx, T)
+    if slots is not None:
+        _flat(slots, "slots", torch.int32, like, idx, n_seqs)
+    elif n_slots and n_slots < n_seqs:
+        raise ValueError("without slots the state needs a row for every sequence")
+    return n_seqs
+
+
+def engram_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, b: torch.Tensor,
+                 cu_seqlens: torch.Tensor, key_heads: int, scale: Optional[float] = None,
+                 mask: Optional[torch.Tensor] = None, state: Optional[torch.Tensor] = None,
+                 slots: Optional[torch.Tensor] = None, state_out: Optional[torch.Tensor] = None,
+                 y: Optional[torch.Tensor] = None, carry: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gated delta rule along packed sequences: S <- f S, u = beta (v - S^T k), S <- S + k u^T, y = scale S^T q in each
+    head, f = sigmoid(g), beta = sigmoid(b); scale: dk ** -0.5 if not given.
+
+    q, k bf16 or f32 [T][key_heads*dk], v and y [T][heads*dv], g, b [T][heads].  state f32 [n_slots][heads][dk][dv]
+    holds the states before the first positions and gets the last ones, unless state_out takes those.  carry
+    (delta_carry) is filled for engram_delta_grad."""
+    L = _lib or _load()
+    idx, T, shape, args = _delta_inputs(q, k, v, g, b, key_heads)
+    if state_out is None:
+        state_out = state
+    n_slots = 0
+    for name, s in (("state", state), ("state_out", state_out)):
+        if s is not None:
+            n_slots = _delta_state(s, name, q, idx, shape, n_slots)
+    n_seqs = _delta_sequences(cu_seqlens, mask, slots, n_slots, q, idx, T)
+    if y is None:
+        y = torch.empty((T, v.shape[1]), dtype=q.dtype, device=q.device)
+    ys = _rows(y, "y", q.dtype, q, idx, T, v.shape[1])
+    if carry is not None:
+        _flat(carry, "carry", torch.float32, q, idx)
+        if carry.numel() * 4 < _bytes_of("engram_delta_carry_bytes", T, n_seqs, *shape[1:]):
+            raise ValueError("carry is too small (delta_carry)")
+    if workspace is None:
+        workspace = delta_workspace(T, n_seqs, *shape, q.device)
+    else:
+        _flat(workspace, "workspace", torch.uint8, q, idx)
+    _call(idx, "engram_delta", L.engram_delta, *args, shape[2] ** -0.5 if scale is None else scale, cu_seqlens.data_ptr(),
+          n_seqs, _addr(slots), _addr(mask), _addr(state), _addr(state_out), n_slots, y.data_ptr(), ys, _addr(carry),
+          workspace.data_ptr(), workspace.numel(), _word(status, q, idx))
+    return y
+
+
+def engram_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, b: torch.Tensor,
+                      slots: torch.Tensor, state: torch.Tensor, key_heads: int, scale: Optional[float] = None,
+                      state_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One position of every batch entry under engram_delta's rule: q, k [B][key_heads*dk], v [B][heads*dv], g, b
+    [B][heads], slots int32 [B] (-1: padding, or a masked position: y is 0 and the state stays), state f32
+    [n_slots][heads][dk][dv] updated in place unless state_out takes the new states; returns y [B][heads*dv]."""
+    L = _lib or _load()
+    idx, B, shape, args = _delta_inputs(q, k, v, g, b, key_heads)
+    sp = _flat(slots, "slots", torch.int32, q, idx, B)
+    n_slots = _delta_state(state, "state", q, idx, shape)
+    if state_out is None:
+        state_out = state
+    else:
+        _delta_state(state_out, "state_out", q, idx, shape, n_slots)
+    if y is None:
+        y = torch.empty((B, v.shape[1]), dtype=q.dtype, device=q.device)
+    ys = _rows(y, "y", q.dtype, q, idx, B, v.shape[1])
+    _call(idx, "engram_delta_step", L.engram_delta_step, *args, shape[2] ** -0.5 if scale is None else scale, sp,
+          state.data_ptr(), state_out.data_ptr(), n_slots, y.data_ptr(), ys, _word(status, q, idx))
+    return y
 
 
 def engram_policy(logits: torch.Tensor, ids: torch.Tensor, advantage: torch.Tensor,

@@ -1,0 +1,375 @@
+// What the gated delta rule's forward and backward kernels share: the chunks of
+// packed sequences, operands as sums of bf16 terms in shared memory, and their
+// products on the tensor cores.
+//
+// Within a chunk of 64 positions, with c the running sum of ln f and D_ti =
+// exp(c_t - c_i) for i <= t:
+//   A = beta D (K K^T) below the diagonal,   M = (I + A)^-1 beta
+//   U = M (V - e^c K S),                      the writes of all its positions
+//   Y = scale e^c Q S + P U,                  P = scale D (Q K^T)
+//   S <- e^c_last S + K^T (e^(c_last - c) U)
+// M and P do not depend on the state: prepare_kernel makes them for all chunks at
+// once, and the kernels that follow the chunks one after another take them from
+// there.
+//
+// Precision.  The states and sums are fp32.  A product's operands are sums of bf16
+// terms (8 bits each): an input of type bf16 is one term and exact; what is
+// computed on the way is three (24 bits, as fp32 has) wherever it reaches a state,
+// and two (16 bits, far below bf16's own rounding) where it only reaches outputs of
+// type bf16.  Of the terms' products those are taken that are not below the last
+// bit that is kept.  (mma.sync's bf16 form does 1024 multiply-adds a clock and SM
+// here and its tf32 form 512, measured: three bf16 terms of one operand cost less
+// than two tf32 ones.)  The tcgen05 form, four times as fast, wants 128 rows: a
+// chunk's 64 positions against the whole of a head's state.  One block a head would
+// leave most SMs without work where there are few sequences, and every operand
+// would go through registers between two products all the same, to be scaled and
+// split; the value columns are spread over blocks instead.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "engram_internal.h"
+#include "train_device.cuh"
+
+namespace engram {
+namespace delta {
+
+constexpr int kC = ENGRAM_DELTA_CHUNK;  // 64 positions
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxDim = ENGRAM_DELTA_MAX_DIM;
+// Lower triangles of 64 x 64 are kept as ten blocks of 16 x 16, a term's 512 bytes
+// each, the 16-byte halves of a block's rows 4 to 7 and 12 to 15 exchanged (eight
+// rows then lie in different banks).
+constexpr int kBlocks = 10, kTerm = kBlocks * 512;
+constexpr int kStateTerms = 3;  // of M, and of everything that reaches a state
+
+template <class E>
+constexpr int kIn = E::kBytes == 2 ? 1 : 3;  // terms of an input
+template <class E>
+constexpr int kOut = E::kBytes == 2 ? 2 : 3;  // of what only reaches outputs
+
+// Per (chunk, head) in the workspace.
+constexpr int kTriBytes = kTerm * 2 * kStateTerms;  // M, P
+struct Gates {
+  float into[kC], last[kC], hi[kC], lo[kC], beta[kC];  // e^c, e^(c_last - c), c in two parts, beta (0: masked)
+};
+
+template <class E>
+struct Args {
+  using T = typename E::T;
+  const T *q, *k, *v, *g, *b, *dy;
+  T *y, *dq, *dk_out, *dv_out, *dg, *db;
+  int64_t q_stride, k_stride, v_stride, g_stride, b_stride, y_stride, dy_stride;
+  int64_t dq_stride, dk_stride, dv_stride, dg_stride, db_stride;
+  const int64_t* cu;
+  const int32_t* slots;
+  const uint8_t* mask;
+  const float* state;
+  float *state_out, *carry;
+  int64_t n_slots;
+  int32_t n_tokens, n_seqs, max_chunks, keys, heads, dk, dv;
+  float scale;
+  bool vec;        // rows of q, k, v and dy in 16-byte pieces
+  bool has_state;  // slots are checked against n_slots
+  // workspace
+  int32_t* first;  // [n_seqs + 1] number of a sequence's first chunk
+  unsigned char* tri;
+  Gates* gates;
+  float *after, *writes, *shared;  // backward: states' gradients, those of the values, sums over heads that share a key
+  int32_t* status;
+};
+
+// ------------------------------------------------------------------- chunks
+
+struct Chunk {
+  int start, len;  // positions
+  int seq;
+  bool live;
+};
+
+template <class E>
+__device__ __forceinline__ void bounds(const Args<E>& a, int s, int& lo, int& hi) {
+  const int64_t n = a.n_tokens, x = a.cu[s], y = a.cu[s + 1];
+  lo = static_cast<int>(x < 0 ? 0 : x > n ? n : x);
+  hi = static_cast<int>(y < lo ? lo : y > n ? n : y);
+}
+
+// Whether the sequence has a state slot of its own, or needs none.
+template <class E>
+__device__ __forceinline__ bool live_slot(const Args<E>& a, int s, int64_t& slot) {
+  slot = a.slots != nullptr ? a.slots[s] : s;
+  return slot >= 0 && !(a.has_state && slot >= a.n_slots);
+}
+
+// Chunk number c, or false where there are fewer.
+template <class E>
+__device__ __forceinline__ bool chunk_at(const Args<E>& a, int c, Chunk& ch) {
+  if (c >= a.first[a.n_seqs]) return false;
+  int lo = 0, hi = a.n_seqs - 1;  // the last sequence that begins at or before c, of which the others are empty
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.first[mid] <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  int from, to;
+  bounds(a, lo, from, to);
+  ch.seq = lo;
+  ch.start = from + (c - a.first[lo]) * kC;
+  ch.len = to - ch.start < kC ? to - ch.start : kC;
+  int64_t slot;
+  ch.live = live_slot(a, lo, slot);
+  return ch.len > 0;
+}
+
+// ------------------------------------------------------------ shared memory
+
+__device__ __forceinline__ void st32(uint32_t at, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
+__device__ __forceinline__ uint32_t ld32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Two values as N terms, `term` bytes apart.
+template <int N>
+__device__ __forceinline__ void put(uint32_t at, int term, float x0, float x1) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const uint32_t w = pack(x0, x1);
+    st32(at + n * term, w);
+    x0 -= lo_of(w);
+    x1 -= hi_of(w);
+  }
+}
+// and back
+template <int N>
+__device__ __forceinline__ void get(uint32_t at, int term, float& x0, float& x1) {
+  x0 = x1 = 0.f;
+#pragma unroll
+  for (int n = N - 1; n >= 0; --n) {
+    const uint32_t w = ld32(at + n * term);
+    x0 += lo_of(w);
+    x1 += hi_of(w);
+  }
+}
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_begun() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// A matrix of bf16 terms: rows `pitch` bytes apart (16 bytes more than a multiple of
+// 128 or 64: eight rows lie in different banks), terms `term` bytes apart.
+struct Mat {
+  uint32_t base;
+  int pitch, term;
+};
+__host__ __device__ constexpr int mat_bytes(int rows, int cols) { return rows * (cols + 8) * 2; }
+template <int kRows, int kCols>
+__device__ __forceinline__ Mat mat(uint32_t base) { return Mat{base, (kCols + 8) * 2, mat_bytes(kRows, kCols)}; }
+
+// kC rows of kCols columns (the first `cols` of them), zeros past the chunk's end and at
+// masked positions.  `src` is the first row's first element.
+template <class E, int kCols>
+__device__ __forceinline__ void load_rows(const Mat& m, const typename E::T* src, int64_t stride, int len, int cols,
+                                          const uint8_t* mask, bool vec) {
+  if (E::kBytes == 2 && vec) {
+    for (int i = threadIdx.x; i < kC * (kCols / 8); i += kThreads) {
+      const int r = i / (kCols / 8), c = i % (kCols / 8) * 8;
+      const bool on = r < len && c < cols && !(mask != nullptr && mask[r]);
+      copy16(m.base + r * m.pitch + c * 2, on ? src + r * stride + c : src, on);
+    }
+  } else {
+    for (int i = threadIdx.x; i < kC * (kCols / 2); i += kThreads) {
+      const int r = i / (kCols / 2), c = i % (kCols / 2) * 2;
+      const bool on = r < len && !(mask != nullptr && mask[r]);
+      const float x0 = on && c < cols ? E::load(src + r * stride + c) : 0.f;
+      const float x1 = on && c + 1 < cols ? E::load(src + r * stride + c + 1) : 0.f;
+      put<kIn<E>>(m.base + r * m.pitch + c * 2, m.term, x0, x1);
+    }
+  }
+}
+
+// ----------------------------------------------------------------- products
+
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ld4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ld4t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ld2t(uint32_t& r0, uint32_t& r1, uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ld2(uint32_t& r0, uint32_t& r1, uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(at) : "memory");
+}
+
+// 16 x 16 pieces of an operand A(m, k), as stored or transposed, of a term
+struct Rows {  // A(m, k) = X[m][k]
+  Mat x;
+  __device__ __forceinline__ void operator()(uint32_t (&r)[4], int m, int k, int n) const {
+    const int l = lane_id();
+    ld4(r, x.base + n * x.term + (m + (l & 15)) * x.pitch + (k + (l >> 4) * 8) * 2);
+  }
+};
+struct Cols {  // A(m, k) = X[k][m]
+  Mat x;
+  __device__ __forceinline__ void operator()(uint32_t (&r)[4], int m, int k, int n) const {
+    const int l = lane_id();
+    ld4t(r, x.base + n * x.term + (k + (l & 7) + (l >> 4) * 8) * x.pitch + (m + ((l >> 3) & 1) * 8) * 2);
+  }
+};
+__device__ __forceinline__ uint32_t tri_at(int row, int half) { return row * 32 + ((half ^ ((row >> 2) & 1)) << 4); }
+struct TriRows {  // A(m, k) = X[m][k], a triangle's blocks
+  uint32_t base;
+  __device__ __forceinline__ void operator()(uint32_t (&r)[4], int m, int k, int n) const {
+    const int l = lane_id(), i = m >> 4, j = k >> 4;
+    ld4(r, base + n * kTerm + (i * (i + 1) / 2 + j) * 512 + tri_at(l & 15, l >> 4));
+  }
+};
+struct TriCols {  // A(m, k) = X[k][m]
+  uint32_t base;
+  __device__ __forceinline__ void operator()(uint32_t (&r)[4], int m, int k, int n) const {
+    const int l = lane_id(), i = k >> 4, j = m >> 4;
+    ld4t(r, base + n * kTerm + (i * (i + 1) / 2 + j) * 512 + tri_at((l & 7) + (l >> 4) * 8, (l >> 3) & 1));
+  }
+};
+// 16 x 8 N pieces of an operand B(k, n)
+struct Down {  // B(k, n) = X[k][n]
+  Mat x;
+  template <int N>
+  __device__ __forceinline__ void get(uint32_t (&r)[N][2], int k, int n, int t) const {
+    const int l = lane_id();
+    const uint32_t at = x.base + t * x.term + (k + (l & 15)) * x.pitch + n * 2;
+#pragma unroll
+    for (int j = 0; j + 1 < N; j += 2) {
+      uint32_t w[4];
+      ld4t(w, at + (j * 8 + (l >> 4) * 8) * 2);
+      r[j][0] = w[0]; r[j][1] = w[1]; r[j + 1][0] = w[2]; r[j + 1][1] = w[3];
+    }
+    if (N & 1) ld2t(r[N - 1][0], r[N - 1][1], at + (N - 1) * 16);
+  }
+};
+struct Across {  // B(k, n) = X[n][k]
+  Mat x;
+  template <int N>
+  __device__ __forceinline__ void get(uint32_t (&r)[N][2], int k, int n, int t) const {
+    const int l = lane_id();
+    const uint32_t at = x.base + t * x.term + k * 2 + ((l >> 3) & 1) * 16;
+#pragma unroll
+    for (int j = 0; j + 1 < N; j += 2) {
+      uint32_t w[4];
+      ld4(w, at + (n + j * 8 + (l & 7) + (l >> 4) * 8) * x.pitch);
+      r[j][0] = w[0]; r[j][1] = w[1]; r[j + 1][0] = w[2]; r[j + 1][1] = w[3];
+    }
+    if (N & 1) ld2(r[N - 1][0], r[N - 1][1], at + (n + (N - 1) * 8 + (l & 7)) * x.pitch);
+  }
+};
+
+// c += A(m.., k0 ..k1) B(k0 ..k1, n..), a 16 x 8 N tile, of TA and TB terms: the
+// products of terms i and j with i + j < kLimit.
+template <int TA, int TB, int kLimit, int N, class A, class B>
+__device__ __forceinline__ void product(float (&c)[N][4], const A& a, const B& b, int m, int n, int k0, int k1) {
+#pragma unroll 2
+  for (int k = k0; k < k1; k += 16) {
+    uint32_t fa[TA][4];
+#pragma unroll
+    for (int i = 0; i < TA; ++i) a(fa[i], m, k, i);
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+      uint32_t fb[N][2];
+      b.template get<N>(fb, k, n, j);
+#pragma unroll
+      for (int i = 0; i < TA; ++i)
+        if (i + j < kLimit) {
+#pragma unroll
+          for (int t = 0; t < N; ++t) mma(c[t], fa[i], fb[t][0], fb[t][1]);
+        }
+    }
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void clear(float (&c)[N][4]) {
+#pragma unroll
+  for (int t = 0; t < N; ++t)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[t][j] = 0.f;
+}
+
+// The chunk's triangles and gates, 16 bytes a copy.  kP: terms of P.
+template <int kP>
+__device__ __forceinline__ void load_tri(uint32_t m, uint32_t p, const unsigned char* from) {
+  for (int i = threadIdx.x; i < kStateTerms * kTerm / 16; i += kThreads) copy16(m + i * 16, from + i * 16, true);
+  for (int i = threadIdx.x; i < kP * kTerm / 16; i += kThreads)
+    copy16(p + i * 16, from + kStateTerms * kTerm + i * 16, true);
+}
+__device__ __forceinline__ void load_gates(uint32_t to, const Gates* from) {
+  for (int i = threadIdx.x; i < static_cast<int>(sizeof(Gates)) / 16; i += kThreads)
+    copy16(to + i * 16, reinterpret_cast<const unsigned char*>(from) + i * 16, true);
+}
+
+template <class E>
+__device__ __forceinline__ size_t unit_of(const Args<E>& a, int chunk, int head) {
+  return static_cast<size_t>(chunk) * a.heads + head;
+}
+
+// ------------------------------------------------------------ host: launches
+
+// The space behind a call's chunks.
+struct Space {
+  int32_t* first;
+  unsigned char* tri;
+  Gates* gates;
+  float *after, *writes, *shared;
+  size_t bytes;
+};
+inline int64_t max_chunks(int64_t n_tokens, int64_t n_seqs) {
+  return std::min(n_tokens, (n_tokens + (kC - 1) * n_seqs) / kC);
+}
+Space space(void* base, int64_t n_tokens, int64_t n_seqs, int32_t keys, int32_t heads, int32_t dk, int32_t dv, bool backward);
+
+// first[], M, P and the gates of all chunks.
+template <class E>
+int launch_prepare(const Args<E>& a, cudaStream_t st);
+
+inline int opt_in(const void* kernel, int smem, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+  if (bit != 0 && (done.load(std::memory_order_relaxed) & bit)) return ENGRAM_OK;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return ENGRAM_OK;
+}
+
+inline bool pieces(const void* p, int64_t stride, int bytes) { return aligned(p, 16) && stride * bytes % 16 == 0; }
+
+}  // namespace delta
+}  // namespace engram

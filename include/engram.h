@@ -714,6 +714,61 @@ int engram_recurrence_step(const void* x_d, int64_t x_stride, const void* g_d, i
                            void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Gated delta rule                                                           */
+/* ------------------------------------------------------------------------ */
+
+/* A memory that is a matrix S [dk][dv] for each value head, along packed sequences.  At
+ * each position, with f = sigmoid(g) and beta = sigmoid(b):
+ *   S <- f S,  u = beta (v - S^T k),  S <- S + k u^T,  y = scale S^T q
+ * Where engram_recurrence keeps one number a channel, this keeps what was last written
+ * at a key and finds it again by a query.  Keys are used as they come: norms near 1
+ * (engram_norm_add by heads gives them) keep the rule stable.  A masked position
+ * (mask_d[t] != 0) holds the state, gives y = 0 and takes no gradient, whatever its row
+ * holds.
+ *
+ *   q_d, k_d  [n_tokens][key_heads*dk] of `type`, rows *_stride elements apart
+ *   v_d, y_d  [n_tokens][heads*dv]
+ *   g_d, b_d  [n_tokens][heads]; value head h goes with key head
+ *             h / (heads/key_heads), heads a multiple of key_heads
+ *   cu_seqlens_d, slots_d, mask_d, n_slots  as in engram_recurrence
+ *   state_d      float32 [n_slots][heads][dk][dv], the states before the first
+ *                positions, or NULL (zeros)
+ *   state_out_d  the same, the states after the last positions (an empty sequence's is
+ *                its first), or NULL; may be state_d
+ *   carry_d      float32, engram_delta_carry_bytes(...) bytes, or NULL: for the backward
+ *                pass, the state in front of every ENGRAM_DELTA_CHUNK positions of a
+ *                sequence
+ *   workspace_d  engram_delta_workspace_bytes(..., 0) bytes, 256-byte aligned; its
+ *                contents on entry do not matter
+ * 1 <= dk, dv <= ENGRAM_DELTA_MAX_DIM; any stride and element-aligned pointers; outputs
+ * overlap no input (but state_out_d may be state_d).  States and sums are fp32.  g below
+ * -80 counts as -80 and b below -40 as -40.  An infinity or a NaN in a position that is
+ * not masked spoils its sequence and head from the beginning of its chunk on.  Positions
+ * outside every sequence are left as they are.  Results are the same from run to run. */
+#define ENGRAM_DELTA_CHUNK 64
+#define ENGRAM_DELTA_MAX_DIM 128
+size_t engram_delta_carry_bytes(int64_t n_tokens, int64_t n_seqs, int32_t heads, int32_t dk, int32_t dv);
+size_t engram_delta_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int32_t key_heads, int32_t heads, int32_t dk,
+                                    int32_t dv, int32_t backward);
+int engram_delta(const void* q_d, int64_t q_stride, const void* k_d, int64_t k_stride, const void* v_d,
+                 int64_t v_stride, const void* g_d, int64_t g_stride, const void* b_d, int64_t b_stride, int32_t type,
+                 int64_t n_tokens, int32_t key_heads, int32_t heads, int32_t dk, int32_t dv, float scale,
+                 const int64_t* cu_seqlens_d, int64_t n_seqs, const int32_t* slots_d, const uint8_t* mask_d,
+                 const float* state_d, float* state_out_d, int64_t n_slots, void* y_d, int64_t y_stride,
+                 float* carry_d, void* workspace_d, size_t workspace_bytes, int32_t* status_d, void* stream);
+
+/* One position for each of `batch` sequences (decode): row b belongs to state slots_d[b];
+ * a negative slot is padding (y = 0, no state), which is also how a masked position is
+ * passed; a slot >= n_slots sets ENGRAM_ST_BAD_SLOT and is padding.  Slots are distinct.
+ * state_out_d may be state_d, or another buffer, of which only the named slots are
+ * written. */
+int engram_delta_step(const void* q_d, int64_t q_stride, const void* k_d, int64_t k_stride, const void* v_d,
+                      int64_t v_stride, const void* g_d, int64_t g_stride, const void* b_d, int64_t b_stride,
+                      int32_t type, int64_t batch, int32_t key_heads, int32_t heads, int32_t dk, int32_t dv,
+                      float scale, const int32_t* slots_d, const float* state_d, float* state_out_d, int64_t n_slots,
+                      void* y_d, int64_t y_stride, int32_t* status_d, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Distillation from a teacher's top logits                                   */
 /* ------------------------------------------------------------------------ */
 

@@ -107,3 +107,51 @@ def test_binding_refuses_what_is_not_on_the_device(lib):
         eg.engram_policy(t, torch.zeros(4, dtype=torch.int32), torch.zeros(4))
     with pytest.raises(TypeError):
         eg.engram_norm_add(t.int())
+
+
+def test_delta(lib):
+    need = lib.engram_delta_workspace_bytes(70, 2, 1, 2, 8, 8, 0)
+    assert need > 0 and lib.engram_delta_workspace_bytes(-1, 2, 1, 2, 8, 8, 0) == 0
+    # at most floor((70 + 63 * 2) / 64) chunks
+    assert lib.engram_delta_carry_bytes(70, 2, 2, 8, 8) == 3 * 2 * 8 * 8 * 4
+    assert lib.engram_delta_carry_bytes(0, 2, 2, 8, 8) == 0
+
+    def call(q=P(16), qs=8, k=P(16), ks=8, v=P(16), vs=16, g=P(16), gs=2, b=P(16), bs=2, ty=F32, T=70, keys=1, H=2, dk=8,
+             dv=8, scale=1.0, cu=P(16), S=2, state=None, n_slots=0, y=P(16), ys=16, carry=None, ws=P(256), n=need):
+        return lib.engram_delta(q, qs, k, ks, v, vs, g, gs, b, bs, ty, T, keys, H, dk, dv, scale, cu, S, None, None, state,
+                                state, n_slots, y, ys, carry, ws, n, None, None)
+    assert call(ty=2) == INVALID
+    assert call(T=-1) == INVALID
+    assert call(S=-1) == INVALID
+    assert call(T=2 ** 31 - 1) == RANGE
+    for bad in (dict(keys=0), dict(H=3, keys=2), dict(H=0), dict(dk=0), dict(dk=129), dict(dv=129), dict(dv=0),
+                dict(H=65536), dict(qs=7), dict(ks=7), dict(vs=15), dict(gs=1), dict(bs=1), dict(ys=15), dict(S=0)):
+        assert call(**bad) == SHAPE, bad
+    for name in ("q", "k", "v", "g", "b", "y", "cu", "ws"):
+        assert call(**{name: None}) == INVALID, name
+    for name in ("q", "k", "v", "g", "b", "y", "carry"):
+        assert call(**{name: P(18)}) == ALIGN, name
+    assert call(scale=float("inf")) == INVALID
+    assert call(state=P(16)) == INVALID
+    assert call(state=P(18), n_slots=2) == ALIGN
+    assert call(ws=P(16)) == ALIGN
+    assert call(n=need - 1) == RANGE
+    assert call(T=0, S=0) == OK
+    assert call(T=0, q=None, k=None, v=None, g=None, b=None, y=None, ws=None) == OK
+
+
+def test_delta_step(lib):
+    def call(q=P(16), qs=8, vs=16, ty=BF16, B=3, keys=1, H=2, dk=8, dv=8, slots=P(16), state=P(16), out=P(16), n_slots=3,
+             y=P(16), ys=16, scale=1.0):
+        return lib.engram_delta_step(q, qs, P(16), 8, P(16), vs, P(16), 2, P(16), 2, ty, B, keys, H, dk, dv, scale, slots,
+                                     state, out, n_slots, y, ys, None, None)
+    assert call(ty=9) == INVALID
+    assert call(B=-1) == INVALID
+    for bad in (dict(keys=3), dict(dk=200), dict(qs=7), dict(vs=1), dict(ys=3)):
+        assert call(**bad) == SHAPE, bad
+    for bad in (dict(q=None), dict(slots=None), dict(state=None), dict(out=None), dict(y=None), dict(n_slots=0),
+                dict(scale=float("nan"))):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(q=P(17)), dict(state=P(18)), dict(out=P(18)), dict(y=P(17))):
+        assert call(**bad) == ALIGN, bad
+    assert call(B=0, q=None, slots=None, state=None) == OK
