@@ -32,7 +32,7 @@ __all__ = [
     "engram_recurrence", "engram_recurrence_grad", "engram_recurrence_step", "recurrence_carry",
     "recurrence_workspace", "engram_distill", "engram_policy",
     "engram_norm_add", "engram_norm_add_grad", "norm_add_workspace",
-    "engram_delta", "engram_delta_step", "delta_carry", "delta_workspace",
+    "engram_delta", "engram_delta_grad", "engram_delta_step", "delta_carry", "delta_workspace",
 ]
 
 MAX_LAYERS = 8
@@ -163,6 +163,9 @@ _SIGS = {
     "engram_recurrence_step": [_P, _I64, _P, _I64, _I32, _I64, _I32, _P, _P, _P, _I64, _P, _I64, _P, _P],
     "engram_delta": [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _I32, _I32, _I32, _F32, _P, _I64,
                      _P, _P, _P, _P, _I64, _P, _I64, _P, _P, ctypes.c_size_t, _P, _P],
+    "engram_delta_grad": [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _I32, _I32, _I32,
+                          _F32, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P,
+                          ctypes.c_size_t, _P, _P],
     "engram_delta_step": [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _I32, _I32, _I32, _F32, _P,
                           _P, _P, _I64, _P, _I64, _P, _P],
     "engram_policy": [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _F32, _F32, _F32, _F32, _P, _P, _P, _P, _I64, _P, _P],
@@ -1445,6 +1448,40 @@ def engram_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Ten
           n_seqs, _addr(slots), _addr(mask), _addr(state), _addr(state_out), n_slots, y.data_ptr(), ys, _addr(carry),
           workspace.data_ptr(), workspace.numel(), _word(status, q, idx))
     return y
+
+
+def engram_delta_grad(dy: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                      b: torch.Tensor, carry: torch.Tensor, cu_seqlens: torch.Tensor, key_heads: int,
+                      scale: Optional[float] = None, mask: Optional[torch.Tensor] = None,
+                      slots: Optional[torch.Tensor] = None, dstate: Optional[torch.Tensor] = None,
+                      dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                      dv: Optional[torch.Tensor] = None, dg: Optional[torch.Tensor] = None,
+                      db: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None):
+    """The gradients (dq, dk, dv, dg, db) of engram_delta, from the carry that the forward call filled.  dstate f32
+    [n_slots][heads][dk][dv]: the gradient of the last states, replaced by that of the first."""
+    L = _lib or _load()
+    idx, T, shape, args = _delta_inputs(q, k, v, g, b, key_heads)
+    n_slots = 0 if dstate is None else _delta_state(dstate, "dstate", q, idx, shape)
+    n_seqs = _delta_sequences(cu_seqlens, mask, slots, n_slots, q, idx, T)
+    dys = _rows(dy, "dy", q.dtype, q, idx, T, v.shape[1])
+    _flat(carry, "carry", torch.float32, q, idx)
+    if carry.numel() * 4 < _bytes_of("engram_delta_carry_bytes", T, n_seqs, *shape[1:]):
+        raise ValueError("carry is too small (delta_carry)")
+    outs, ptrs = [], []
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dg", dg, g), ("db", db, b)):
+        if t is None:
+            t = torch.empty(like.shape, dtype=q.dtype, device=q.device)
+        ptrs += [t.data_ptr(), _rows(t, name, q.dtype, q, idx, T, like.shape[1])]
+        outs.append(t)
+    if workspace is None:
+        workspace = delta_workspace(T, n_seqs, *shape, q.device, True)
+    else:
+        _flat(workspace, "workspace", torch.uint8, q, idx)
+    _call(idx, "engram_delta_grad", L.engram_delta_grad, dy.data_ptr(), dys, *args,
+          shape[2] ** -0.5 if scale is None else scale, cu_seqlens.data_ptr(), n_seqs, _addr(slots), _addr(mask),
+          carry.data_ptr(), _addr(dstate), n_slots, *ptrs, workspace.data_ptr(), workspace.numel(), _word(status, q, idx))
+    return tuple(outs)
 
 
 def engram_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, b: torch.Tensor,

@@ -371,5 +371,25 @@ inline int opt_in(const void* kernel, int smem, std::atomic<uint64_t>& done) {
 
 inline bool pieces(const void* p, int64_t stride, int bytes) { return aligned(p, 16) && stride * bytes % 16 == 0; }
 
+inline int check_sizes(int32_t type, int64_t n_tokens, int32_t keys, int32_t heads, int32_t dk, int32_t dv, int64_t n_seqs,
+                int64_t n_slots, bool has_state, float scale) {
+  if (!train::known_type(type)) return fail(ENGRAM_E_INVALID, "type %d is not ENGRAM_T_BF16 or ENGRAM_T_F32", type);
+  if (n_tokens < 0 || n_seqs < 0) return fail(ENGRAM_E_INVALID, "negative number of positions or sequences");
+  if (n_tokens > 0x7fffff00 || n_seqs > 0x7fffff00) return fail(ENGRAM_E_RANGE, "too many positions or sequences");
+  if (keys < 1 || heads < keys || heads % keys != 0 || heads > 65535)
+    return fail(ENGRAM_E_SHAPE, "value heads must be a multiple of the key heads, and at most 65535");
+  if (dk < 1 || dk > kMaxDim || dv < 1 || dv > kMaxDim) return fail(ENGRAM_E_SHAPE, "head widths must be in [1, %d]", kMaxDim);
+  if (has_state && n_slots < 1) return fail(ENGRAM_E_INVALID, "a state needs n_slots >= 1");
+  if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return fail(ENGRAM_E_INVALID, "scale must be finite");
+  return ENGRAM_OK;
+}
+
+inline int check_rows(const void* p, int32_t type, int64_t stride, int64_t width, const char* name) {
+  if (stride < width) return fail(ENGRAM_E_SHAPE, "%s: row stride below its width", name);
+  if (p == nullptr) return fail(ENGRAM_E_INVALID, "null device pointer: %s", name);
+  if (!aligned(p, train::type_bytes(type))) return fail(ENGRAM_E_ALIGN, "%s must be aligned to its elements", name);
+  return ENGRAM_OK;
+}
+
 }  // namespace delta
 }  // namespace engram

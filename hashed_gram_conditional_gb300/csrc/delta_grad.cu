@@ -1,0 +1,598 @@
+// The gradients of the gated delta rule.
+//
+// With the names of delta_device.cuh, dS the gradient of the state behind a chunk
+// and dV = M^T (P^T dY + e^(c_last - c) K dS):
+//   dS <- e^c_last dS + Q^T (scale e^c dY) - K^T (e^c dV)       chunk after chunk, from the last
+// and then, for all chunks at once, with F = scale D (dY U^T) on and below the
+// diagonal and E = -D (dV U^T) below it:
+//   dQ = scale e^c dY S^T + F K
+//   dK = -e^c dV S^T + e^(c_last - c) U dS^T + E K + E^T K + F^T Q
+//   db_t = (dV_t . U_t) (1 - beta_t) / beta_t
+//   dg_t = (1 - f_t) (what crosses t: reads of S at t and later, writes before t that
+//          reach dS, pairs of the two of them, and e^c_last S . dS)
+// The states in front of the chunks come from the forward pass; U, M and P are
+// computed again.
+#include "delta_device.cuh"
+
+namespace engram {
+namespace delta {
+namespace {
+
+// ------------------------------------------------ the state's gradient, backwards
+
+template <class E, int KD, int VS>
+struct Back {
+  static constexpr int kStages = E::kBytes == 2 ? 2 : 1;
+  static constexpr int kQ = 0, kK = kQ + kIn<E> * mat_bytes(kC, KD), kY = kK + kIn<E> * mat_bytes(kC, KD);
+  static constexpr int kM = kY + kIn<E> * mat_bytes(kC, VS), kP = kM + kStateTerms * kTerm, kG = kP + kStateTerms * kTerm;
+  static constexpr int kStage = kG + static_cast<int>(sizeof(Gates));
+  static constexpr int kS = kStages * kStage;                      // dS
+  static constexpr int kX = kS + kStateTerms * mat_bytes(KD, VS);  // dU, then -e^c dV
+  static constexpr int kR = kX + kStateTerms * mat_bytes(kC, VS);  // scale e^c dY
+  static constexpr int kSmem = kR + kStateTerms * mat_bytes(kC, VS);
+  static constexpr int kAcross = kWarps / (KD / 16);
+  static constexpr int kN = VS / 16, kSN = VS / 8 / kAcross;
+};
+
+template <class E, int KD, int VS>
+__global__ void __launch_bounds__(kThreads, 1) back_kernel(Args<E> a) {
+  using L = Back<E, KD, VS>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
+  const int seq = blockIdx.x, h = blockIdx.y, v0 = blockIdx.z * VS, cols = a.dv - v0 < VS ? a.dv - v0 : VS;
+  const int hk = h / (a.heads / a.keys);
+  int lo, hi;
+  bounds(a, seq, lo, hi);
+  const int c0 = a.first[seq], n = min((hi - lo + kC - 1) / kC, a.max_chunks - c0);
+  int64_t slot;
+  const bool live = live_slot(a, seq, slot);
+  if (!live && tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
+  if (!live) {  // padding: zeros
+    for (int64_t i = tid; i < static_cast<int64_t>(hi - lo) * cols; i += kThreads)
+      E::store(a.dv_out + (lo + i / cols) * a.dv_stride + h * a.dv + v0 + i % cols, 0.f);
+    return;
+  }
+  const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
+  const int sm = warp % (KD / 16) * 16, sn = warp / (KD / 16) * (L::kSN * 8);
+  auto each = [&](auto f) {  // f(accumulator's tile and place, the element's place in a state)
+#pragma unroll
+    for (int t = 0; t < L::kSN; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = sm + g + (j >> 1) * 8, c = sn + t * 8 + t2 + (j & 1);
+        if (r < a.dk && c < cols) f(t, j, static_cast<size_t>(r) * a.dv + v0 + c);
+      }
+  };
+  float S[L::kSN][4];
+  clear(S);
+  if (a.state_out != nullptr) {
+    const float* from = a.state_out + (slot * a.heads + h) * matrix;
+    each([&](int t, int j, size_t at) { S[t][j] = from[at]; });
+  }
+  const Mat St = mat<KD, VS>(base + L::kS), X = mat<kC, VS>(base + L::kX), R = mat<kC, VS>(base + L::kR);
+  auto keep = [&]() {
+#pragma unroll
+    for (int t = 0; t < L::kSN; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        put<kStateTerms>(St.base + (sm + g + j * 8) * St.pitch + (sn + t * 8 + t2) * 2, St.term, S[t][2 * j], S[t][2 * j + 1]);
+  };
+  auto load = [&](int i) {
+    const uint32_t stage = base + (i % L::kStages) * L::kStage;
+    const int64_t p = lo + static_cast<int64_t>(i) * kC;
+    const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
+    const uint8_t* mask = a.mask != nullptr ? a.mask + p : nullptr;
+    const size_t unit = unit_of(a, c0 + i, h);
+    load_rows<E, KD>(mat<kC, KD>(stage + L::kK), a.k + p * a.k_stride + hk * a.dk, a.k_stride, len, a.dk, mask, a.vec);
+    load_rows<E, KD>(mat<kC, KD>(stage + L::kQ), a.q + p * a.q_stride + hk * a.dk, a.q_stride, len, a.dk, mask, a.vec);
+    load_rows<E, VS>(mat<kC, VS>(stage + L::kY), a.dy + p * a.dy_stride + h * a.dv + v0, a.dy_stride, len, cols, mask, a.vec);
+    load_tri<kStateTerms>(stage + L::kM, stage + L::kP, a.tri + unit * kTriBytes);
+    load_gates(stage + L::kG, a.gates + unit);
+    copies_begun();
+  };
+  keep();
+  if (n > 0) load(n - 1);
+  const int m = (warp & 3) * 16, nn = (warp >> 2) * (VS / 2);
+  for (int i = n - 1; i >= 0; --i) {
+    const uint32_t stage = base + (i % L::kStages) * L::kStage;
+    const Mat K = mat<kC, KD>(stage + L::kK), Q = mat<kC, KD>(stage + L::kQ), Y = mat<kC, VS>(stage + L::kY);
+    const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
+    copies_done();
+    __syncthreads();  // the chunk and dS are here, and the other stage is free
+    if (L::kStages == 2 && i > 0) load(i - 1);
+    {
+      float* to = a.after + unit_of(a, c0 + i, h) * matrix;
+      each([&](int t, int j, size_t at) { to[at] = S[t][j]; });
+    }
+    float x[L::kN][4], u[L::kN][4];
+    clear(x);
+    clear(u);
+    product<kIn<E>, kStateTerms, kStateTerms>(x, Rows{K}, Down{St}, m, nn, 0, KD);
+    product<kStateTerms, kIn<E>, kStateTerms>(u, TriCols{stage + L::kP}, Down{Y}, m, nn, m, kC);
+#pragma unroll
+    for (int t = 0; t < L::kN; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = m + g + j * 8, c = nn + t * 8 + t2;
+        const float last = gt.last[r], into = a.scale * gt.into[r];
+        put<kStateTerms>(X.base + r * X.pitch + c * 2, X.term, fmaf(last, x[t][2 * j], u[t][2 * j]),
+                         fmaf(last, x[t][2 * j + 1], u[t][2 * j + 1]));
+        float y[2];
+        get<kIn<E>>(Y.base + r * Y.pitch + c * 2, Y.term, y[0], y[1]);
+        put<kStateTerms>(R.base + r * R.pitch + c * 2, R.term, into * y[0], into * y[1]);
+      }
+    __syncthreads();
+    clear(u);
+    product<kStateTerms, kStateTerms, kStateTerms>(u, TriCols{stage + L::kM}, Down{X}, m, nn, m, kC);
+    __syncthreads();  // X is free
+    const int64_t p = lo + static_cast<int64_t>(i) * kC;
+#pragma unroll
+    for (int t = 0; t < L::kN; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = m + g + j * 8, c = nn + t * 8 + t2;
+        const float into = gt.into[r];
+        put<kStateTerms>(X.base + r * X.pitch + c * 2, X.term, -into * u[t][2 * j], -into * u[t][2 * j + 1]);
+        if (p + r >= hi) continue;
+        const bool on = gt.beta[r] != 0.f;  // a masked position takes no gradient
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (c + e >= cols) continue;
+          const float d = on ? u[t][2 * j + e] : 0.f;
+          E::store(a.dv_out + (p + r) * a.dv_stride + h * a.dv + v0 + c + e, d);
+          a.writes[((p + r) * a.heads + h) * a.dv + v0 + c + e] = d;
+        }
+      }
+    __syncthreads();
+    const float total = gt.into[kC - 1];
+#pragma unroll
+    for (int t = 0; t < L::kSN; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) S[t][j] *= total;
+    product<kIn<E>, kStateTerms, kStateTerms>(S, Cols{Q}, Down{R}, sm, sn, 0, kC);
+    product<kIn<E>, kStateTerms, kStateTerms>(S, Cols{K}, Down{X}, sm, sn, 0, kC);
+    keep();
+    if (L::kStages == 1 && i > 0) {
+      __syncthreads();  // the stage is free
+      load(i - 1);
+    }
+  }
+  if (a.state_out != nullptr) {
+    float* to = a.state_out + (slot * a.heads + h) * matrix;
+    each([&](int t, int j, size_t at) { to[at] = S[t][j]; });
+  }
+}
+
+// ------------------------------------------------------- all chunks' gradients
+
+template <class E, int KD, int VS>
+struct Grads {
+  static constexpr int kO = kOut<E>;
+  static constexpr int kQ = 0, kK = kQ + kIn<E> * mat_bytes(kC, KD), kM = kK + kIn<E> * mat_bytes(kC, KD);
+  static constexpr int kG = kM + kO * kTerm, kNum = kG + static_cast<int>(sizeof(Gates));  // kNum: the chunk's sums
+  static constexpr int kSums = 2 * kC * 4 + 4 * kC + kWarps;  // floats
+  static constexpr int kSlice = (kNum + kSums * 4 + 127) / 128 * 128;
+  // a slice of the value columns: S, dS, V then V - e^c K S, U, dY, dV
+  static constexpr int kS = kSlice, kD = kS + kO * mat_bytes(KD, VS), kX = kD + kO * mat_bytes(KD, VS);
+  static constexpr int kU = kX + kO * mat_bytes(kC, VS), kY = kU + kO * mat_bytes(kC, VS), kW = kY + kIn<E> * mat_bytes(kC, VS);
+  static constexpr int kEnd = kW + kO * mat_bytes(kC, VS);
+  // in its place afterwards: F, E
+  static constexpr int kF = kSlice, kE = kF + kO * mat_bytes(kC, kC), kEnd2 = kE + kO * mat_bytes(kC, kC);
+  static constexpr int kSmem = kEnd > kEnd2 ? kEnd : kEnd2;
+  static constexpr int kN = VS / 16, kKN = KD / 16;  // a warp's tiles of a slice's, and of a key's columns
+};
+
+// dk rows of a state's columns v0 .. v0 + cols as terms, zeros around them; returns
+// what `sum` says of the thread's values.
+template <class E, int KD, int VS>
+__device__ __forceinline__ void load_state(const Mat& m, const float* from, int dk, int dv, int cols) {
+  const bool two = dv % 2 == 0 && (reinterpret_cast<uintptr_t>(from) & 7) == 0;
+  for (int i = threadIdx.x; i < KD * (VS / 2); i += kThreads) {
+    const int r = i / (VS / 2), c = i % (VS / 2) * 2;
+    float x0 = 0.f, x1 = 0.f;
+    if (r < dk && c < cols) {
+      const float* p = from + static_cast<size_t>(r) * dv + c;
+      if (two) {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        x0 = x.x;
+        x1 = x.y;
+      } else {
+        x0 = p[0];
+        x1 = c + 1 < cols ? p[1] : 0.f;
+      }
+    }
+    put<kOut<E>>(m.base + r * m.pitch + c * 2, m.term, x0, x1);
+  }
+}
+
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+template <class E, int KD, int VS>
+__global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
+  using L = Grads<E, KD, VS>;
+  constexpr int kO = L::kO;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
+  const int hk = blockIdx.y, group = a.heads / a.keys;
+  Chunk ch;
+  if (!chunk_at(a, blockIdx.x, ch)) return;
+  const int64_t p = ch.start;
+  if (!ch.live) {  // padding: zeros
+    for (int i = tid; i < ch.len * a.dk; i += kThreads) {
+      const int64_t r = p + i / a.dk;
+      const int c = hk * a.dk + i % a.dk;
+      E::store(a.dq + r * a.dq_stride + c, 0.f);
+      E::store(a.dk_out + r * a.dk_stride + c, 0.f);
+    }
+    for (int i = tid; i < ch.len * group; i += kThreads) {
+      const int64_t r = p + i / group;
+      const int h = hk * group + i % group;
+      E::store(a.dg + r * a.dg_stride + h, 0.f);
+      E::store(a.db + r * a.db_stride + h, 0.f);
+    }
+    return;
+  }
+  const uint8_t* mask = a.mask != nullptr ? a.mask + p : nullptr;
+  const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
+  const Mat K = mat<kC, KD>(base + L::kK), Q = mat<kC, KD>(base + L::kQ);
+  const Mat S = mat<KD, VS>(base + L::kS), D = mat<KD, VS>(base + L::kD);
+  const Mat X = mat<kC, VS>(base + L::kX), U = mat<kC, VS>(base + L::kU), Y = mat<kC, VS>(base + L::kY),
+            W = mat<kC, VS>(base + L::kW);
+  const Mat Fm = mat<kC, kC>(base + L::kF), Em = mat<kC, kC>(base + L::kE);
+  const Gates& gt = *reinterpret_cast<const Gates*>(smem + L::kG);
+  float* sums = reinterpret_cast<float*>(smem + L::kNum);
+  float *reads = sums, *writes = reads + 2 * kC, *rows = writes + 2 * kC, *own = rows + 2 * kC, *columns = own + 2 * kC,
+        *wholes = columns + 4 * kC;
+  load_rows<E, KD>(K, a.k + p * a.k_stride + hk * a.dk, a.k_stride, ch.len, a.dk, mask, a.vec);
+  load_rows<E, KD>(Q, a.q + p * a.q_stride + hk * a.dk, a.q_stride, ch.len, a.dk, mask, a.vec);
+  copies_begun();
+  copies_done();
+  __syncthreads();
+  // a warp's tiles: 16 rows, and half of the columns
+  const int m = (warp & 3) * 16, half = warp >> 2, nn = half * (VS / 2), nc = half * (kC / 2), nk = half * (KD / 2);
+  const bool low = nc <= m;  // whether its tile of a triangle has anything
+  float qk[4][4], kk[4][4];
+  clear(qk);
+  clear(kk);
+  if (low) {
+    product<kIn<E>, kIn<E>, kIn<E>>(qk, Rows{Q}, Across{K}, m, nc, 0, KD);
+    product<kIn<E>, kIn<E>, kIn<E>>(kk, Rows{K}, Across{K}, m, nc, 0, KD);
+  }
+  for (int h = hk * group; h < (hk + 1) * group; ++h) {
+    const size_t unit = unit_of(a, blockIdx.x, h);
+    float cf[4][4], ce[4][4], cq[L::kKN][4], ck[L::kKN][4], cw[L::kKN][4];
+    float dot[2] = {0.f, 0.f}, whole = 0.f;
+    clear(cf);
+    clear(ce);
+    clear(cq);
+    clear(ck);
+    clear(cw);
+    __syncthreads();  // the head before has been written
+    for (int i = tid; i < kO * kTerm / 16; i += kThreads)
+      copy16(base + L::kM + i * 16, a.tri + unit * kTriBytes + i * 16, true);
+    load_gates(base + L::kG, a.gates + unit);
+    for (int v0 = 0; v0 < a.dv; v0 += VS) {
+      const int cols = a.dv - v0 < VS ? a.dv - v0 : VS;
+      if (v0 > 0) __syncthreads();  // the slice before has been used
+      const int64_t column = static_cast<int64_t>(h) * a.dv + v0;
+      load_rows<E, VS>(X, a.v + p * a.v_stride + column, a.v_stride, ch.len, cols, mask, a.vec);
+      load_rows<E, VS>(Y, a.dy + p * a.dy_stride + column, a.dy_stride, ch.len, cols, mask, a.vec);
+      copies_begun();
+      load_state<E, KD, VS>(S, a.carry + unit * matrix + v0, a.dk, a.dv, cols);
+      load_state<E, KD, VS>(D, a.after + unit * matrix + v0, a.dk, a.dv, cols);
+      for (int i = tid; i < kC * (VS / 2); i += kThreads) {
+        const int r = i / (VS / 2), c = i % (VS / 2) * 2;
+        const float* from = a.writes + (p + r) * a.heads * a.dv + column + c;
+        const bool on = r < ch.len;
+        put<kO>(W.base + r * W.pitch + c * 2, W.term, on && c < cols ? from[0] : 0.f, on && c + 1 < cols ? from[1] : 0.f);
+      }
+      copies_done();
+      __syncthreads();
+      for (int i = tid; i < KD * (VS / 2); i += kThreads) {
+        const int r = i / (VS / 2), c = i % (VS / 2) * 2;
+        float s[2], d[2];
+        get<kO>(S.base + r * S.pitch + c * 2, S.term, s[0], s[1]);
+        get<kO>(D.base + r * D.pitch + c * 2, D.term, d[0], d[1]);
+        whole = fmaf(s[0], d[0], fmaf(s[1], d[1], whole));
+      }
+      float x[L::kN][4];
+      clear(x);
+      product<kIn<E>, kO, kO>(x, Rows{K}, Down{S}, m, nn, 0, KD);
+#pragma unroll
+      for (int t = 0; t < L::kN; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = m + g + j * 8, c = nn + t * 8 + t2;
+          const uint32_t at = X.base + r * X.pitch + c * 2;
+          float v[2];
+          get<kIn<E>>(at, X.term, v[0], v[1]);
+          const float into = gt.into[r];
+          put<kO>(at, X.term, fmaf(-into, x[t][2 * j], v[0]), fmaf(-into, x[t][2 * j + 1], v[1]));
+        }
+      __syncthreads();
+      clear(x);
+      product<kO, kO, kO>(x, TriRows{base + L::kM}, Down{X}, m, nn, 0, m + 16);
+#pragma unroll
+      for (int t = 0; t < L::kN; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = m + g + j * 8, c = nn + t * 8 + t2;
+          put<kO>(U.base + r * U.pitch + c * 2, U.term, x[t][2 * j], x[t][2 * j + 1]);
+          float w[2];
+          get<kO>(W.base + r * W.pitch + c * 2, W.term, w[0], w[1]);
+          dot[j] = fmaf(w[0], x[t][2 * j], fmaf(w[1], x[t][2 * j + 1], dot[j]));
+        }
+      __syncthreads();
+      if (low) {
+        product<kIn<E>, kO, kO>(cf, Rows{Y}, Across{U}, m, nc, 0, VS);
+        product<kO, kO, kO>(ce, Rows{W}, Across{U}, m, nc, 0, VS);
+      }
+      product<kIn<E>, kO, kO>(cq, Rows{Y}, Across{S}, m, nk, 0, VS);
+      product<kO, kO, kO>(ck, Rows{W}, Across{S}, m, nk, 0, VS);
+      product<kO, kO, kO>(cw, Rows{U}, Across{D}, m, nk, 0, VS);
+    }
+    // ---- F and E, the pairs of reads and writes, and what reads S and reaches dS
+    float row[2] = {0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = nc + t * 8 + t2 + e;
+        float column = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = m + g + j * 8;
+          const float d = i <= r && low ? expf((gt.hi[r] - gt.hi[i]) + (gt.lo[r] - gt.lo[i])) : 0.f;
+          float& f = cf[t][2 * j + e];
+          float& w = ce[t][2 * j + e];
+          f = i <= r && low ? a.scale * d * f : 0.f;
+          w = i < r && low ? -d * w : 0.f;
+          const float pair = i < r && low ? fmaf(f, qk[t][2 * j + e], w * kk[t][2 * j + e]) : 0.f;
+          row[j] += pair;
+          column += pair;
+        }
+        column += __shfl_xor_sync(0xffffffffu, column, 4);
+        column += __shfl_xor_sync(0xffffffffu, column, 8);
+        column += __shfl_xor_sync(0xffffffffu, column, 16);
+        if (g == 0) columns[(m >> 4) * kC + i] = column;
+      }
+    float read[2] = {0.f, 0.f}, write[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = m + g + j * 8;
+      const float into = gt.into[r], last = gt.last[r];
+#pragma unroll
+      for (int t = 0; t < L::kKN; ++t) {
+        const uint32_t at = r * K.pitch + (nk + t * 8 + t2) * 2;
+        float q[2], k[2];
+        get<kIn<E>>(Q.base + at, Q.term, q[0], q[1]);
+        get<kIn<E>>(K.base + at, K.term, k[0], k[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          cq[t][2 * j + e] *= a.scale * into;
+          const float seen = -into * ck[t][2 * j + e], left = last * cw[t][2 * j + e];
+          read[j] = fmaf(q[e], cq[t][2 * j + e], fmaf(k[e], seen, read[j]));
+          write[j] = fmaf(k[e], left, write[j]);
+          ck[t][2 * j + e] = seen + left;
+        }
+      }
+      const float sum_row = quad_sum(row[j]), sum_read = quad_sum(read[j]), sum_write = quad_sum(write[j]),
+                  sum_own = quad_sum(dot[j]);
+      if (t2 == 0) {
+        rows[half * kC + r] = sum_row;
+        reads[half * kC + r] = sum_read;
+        writes[half * kC + r] = sum_write;
+        own[half * kC + r] = sum_own;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, o);
+    if (lane == 0) wholes[warp] = whole;
+    __syncthreads();  // the slice is no longer needed
+    if (low) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t at = (m + g + j * 8) * Fm.pitch + (nc + t * 8 + t2) * 2;
+          put<kO>(Fm.base + at, Fm.term, cf[t][2 * j], cf[t][2 * j + 1]);
+          put<kO>(Em.base + at, Em.term, ce[t][2 * j], ce[t][2 * j + 1]);
+        }
+    }
+    __syncthreads();
+    product<kO, kIn<E>, kO>(cq, Rows{Fm}, Down{K}, m, nk, 0, m + 16);
+    product<kO, kIn<E>, kO>(ck, Rows{Em}, Down{K}, m, nk, 0, m + 16);
+    product<kO, kIn<E>, kO>(ck, Cols{Em}, Down{K}, m, nk, m, kC);
+    product<kO, kIn<E>, kO>(ck, Cols{Fm}, Down{Q}, m, nk, m, kC);
+    // ---- out; heads that share a key are added up in order, each thread its own elements
+    const bool begins = h == hk * group, ends = h + 1 == (hk + 1) * group;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = m + g + j * 8;
+      if (r >= ch.len) continue;
+      const bool on = !(mask != nullptr && mask[r]);
+      float* all = a.shared + ((p + r) * a.keys + hk) * a.dk;
+      float* all_k = all + static_cast<int64_t>(a.n_tokens) * a.keys * a.dk;
+#pragma unroll
+      for (int t = 0; t < L::kKN; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int c = nk + t * 8 + t2 + e;
+          if (c >= a.dk) continue;
+          float x = cq[t][2 * j + e], y = ck[t][2 * j + e];
+          if (!begins) {
+            x += all[c];
+            y += all_k[c];
+          }
+          if (!ends) {
+            all[c] = x;
+            all_k[c] = y;
+          } else {
+            E::store(a.dq + (p + r) * a.dq_stride + hk * a.dk + c, on ? x : 0.f);
+            E::store(a.dk_out + (p + r) * a.dk_stride + hk * a.dk + c, on ? y : 0.f);
+          }
+        }
+    }
+    if (warp == 0) {  // what crosses a position: two positions a lane
+      float later[2], before[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = lane * 2 + j;
+        later[j] = (reads[r] + reads[kC + r]) + (rows[r] + rows[kC + r]) -
+                   (((columns[r] + columns[kC + r]) + columns[2 * kC + r]) + columns[3 * kC + r]);
+        before[j] = writes[r] + writes[kC + r];
+      }
+      float sum = later[0] + later[1], head = before[0] + before[1], all = 0.f;
+      const float mine = head;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float x = __shfl_down_sync(0xffffffffu, sum, o), y = __shfl_up_sync(0xffffffffu, head, o);
+        if (lane + o < 32) sum += x;
+        if (lane >= o) head += y;
+      }
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) all += wholes[w];
+      all *= gt.into[kC - 1];
+      const float cross[2] = {sum + (head - mine) + all, (sum - later[0]) + (head - mine + before[0]) + all};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = lane * 2 + j;
+        if (r >= ch.len) continue;
+        const bool on = gt.beta[r] != 0.f;
+        const int64_t t = p + r;
+        const float gr = E::load(a.g + t * a.g_stride + h), br = E::load(a.b + t * a.b_stride + h);
+        E::store(a.dg + t * a.dg_stride + h, on ? cross[j] / (1.f + expf(gr)) : 0.f);
+        E::store(a.db + t * a.db_stride + h, on ? (own[r] + own[kC + r]) / (gt.beta[r] * (1.f + expf(br))) : 0.f);
+      }
+    }
+  }
+}
+
+template <class E>
+int launch_grad(const Args<E>& a, cudaStream_t st) {
+  int rc = launch_prepare<E>(a, st);
+  if (rc) return rc;
+  static std::atomic<uint64_t> done[4] = {{0}, {0}, {0}, {0}};
+  auto go = [&](auto kernel, int smem, dim3 grid, std::atomic<uint64_t>& flag, const char* name) {
+    int r = opt_in(reinterpret_cast<const void*>(kernel), smem, flag);
+    if (r) return r;
+    kernel<<<grid, kThreads, smem, st>>>(a);
+    return check_launch(name);
+  };
+  constexpr int VB = 32, VG = E::kBytes == 2 ? 32 : 16;
+  const dim3 back(a.n_seqs, a.heads, (a.dv + VB - 1) / VB), grads(a.max_chunks, a.keys);
+  if (a.dk <= 64) {
+    rc = go(back_kernel<E, 64, VB>, Back<E, 64, VB>::kSmem, back, done[0], "back_kernel");
+    return rc ? rc : go(grads_kernel<E, 64, VG>, Grads<E, 64, VG>::kSmem, grads, done[1], "grads_kernel");
+  }
+  constexpr int VB2 = E::kBytes == 2 ? 32 : 16;
+  const dim3 back2(a.n_seqs, a.heads, (a.dv + VB2 - 1) / VB2);
+  rc = go(back_kernel<E, 128, VB2>, Back<E, 128, VB2>::kSmem, back2, done[2], "back_kernel");
+  return rc ? rc : go(grads_kernel<E, 128, VG>, Grads<E, 128, VG>::kSmem, grads, done[3], "grads_kernel");
+}
+
+static_assert(Back<train::Bf16, 128, 32>::kSmem <= 232448 && Back<train::F32, 128, 16>::kSmem <= 232448 &&
+                  Back<train::F32, 64, 32>::kSmem <= 232448 && Grads<train::Bf16, 128, 32>::kSmem <= 232448 &&
+                  Grads<train::F32, 128, 16>::kSmem <= 232448,
+              "a block's shared memory");
+
+}  // namespace
+}  // namespace delta
+}  // namespace engram
+
+using namespace engram;
+using namespace engram::delta;
+
+extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void* q_d, int64_t q_stride, const void* k_d,
+                                 int64_t k_stride, const void* v_d, int64_t v_stride, const void* g_d, int64_t g_stride,
+                                 const void* b_d, int64_t b_stride, int32_t type, int64_t n_tokens, int32_t key_heads,
+                                 int32_t heads, int32_t dk, int32_t dv, float scale, const int64_t* cu_seqlens_d,
+                                 int64_t n_seqs, const int32_t* slots_d, const uint8_t* mask_d, const float* carry_d,
+                                 float* dstate_d, int64_t n_slots, void* dq_d, int64_t dq_stride, void* dk_d,
+                                 int64_t dk_stride, void* dv_d, int64_t dv_stride, void* dg_d, int64_t dg_stride,
+                                 void* db_d, int64_t db_stride, void* workspace_d, size_t workspace_bytes,
+                                 int32_t* status_d, void* stream) {
+  int rc = check_sizes(type, n_tokens, key_heads, heads, dk, dv, n_seqs, n_slots, dstate_d != nullptr, scale);
+  if (rc) return rc;
+  if (n_seqs == 0) return n_tokens == 0 ? ENGRAM_OK : fail(ENGRAM_E_SHAPE, "positions without a sequence");
+  if (n_tokens == 0) return ENGRAM_OK;  // the state's gradient passes through empty sequences
+  if (!cu_seqlens_d || !carry_d) return fail(ENGRAM_E_INVALID, "null device pointer: cu_seqlens or carry");
+  const int64_t wide_k = static_cast<int64_t>(key_heads) * dk, wide_v = static_cast<int64_t>(heads) * dv;
+  if ((rc = check_rows(dy_d, type, dy_stride, wide_v, "dy"))) return rc;
+  if ((rc = check_rows(q_d, type, q_stride, wide_k, "q"))) return rc;
+  if ((rc = check_rows(k_d, type, k_stride, wide_k, "k"))) return rc;
+  if ((rc = check_rows(v_d, type, v_stride, wide_v, "v"))) return rc;
+  if ((rc = check_rows(g_d, type, g_stride, heads, "g"))) return rc;
+  if ((rc = check_rows(b_d, type, b_stride, heads, "b"))) return rc;
+  if ((rc = check_rows(dq_d, type, dq_stride, wide_k, "dq"))) return rc;
+  if ((rc = check_rows(dk_d, type, dk_stride, wide_k, "dk"))) return rc;
+  if ((rc = check_rows(dv_d, type, dv_stride, wide_v, "dv"))) return rc;
+  if ((rc = check_rows(dg_d, type, dg_stride, heads, "dg"))) return rc;
+  if ((rc = check_rows(db_d, type, db_stride, heads, "db"))) return rc;
+  if (!aligned(dstate_d, 4) || !aligned(carry_d, 4))
+    return fail(ENGRAM_E_ALIGN, "states and carry must be aligned to their elements");
+  if (!workspace_d) return fail(ENGRAM_E_INVALID, "null device pointer: workspace");
+  if (!aligned(workspace_d, 256)) return fail(ENGRAM_E_ALIGN, "workspace must be 256-byte aligned");
+  if (workspace_bytes < engram_delta_workspace_bytes(n_tokens, n_seqs, key_heads, heads, dk, dv, 1))
+    return fail(ENGRAM_E_RANGE, "workspace too small");
+  if ((rc = check_device(nullptr))) return rc;
+  auto go = [&](auto e) {
+    using E = decltype(e);
+    using T = typename E::T;
+    Args<E> a{};
+    a.dy = static_cast<const T*>(dy_d);
+    a.q = static_cast<const T*>(q_d);
+    a.k = static_cast<const T*>(k_d);
+    a.v = static_cast<const T*>(v_d);
+    a.g = static_cast<const T*>(g_d);
+    a.b = static_cast<const T*>(b_d);
+    a.dq = static_cast<T*>(dq_d);
+    a.dk_out = static_cast<T*>(dk_d);
+    a.dv_out = static_cast<T*>(dv_d);
+    a.dg = static_cast<T*>(dg_d);
+    a.db = static_cast<T*>(db_d);
+    a.dy_stride = dy_stride;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.g_stride = g_stride;
+    a.b_stride = b_stride;
+    a.dq_stride = dq_stride;
+    a.dk_stride = dk_stride;
+    a.dv_stride = dv_stride;
+    a.dg_stride = dg_stride;
+    a.db_stride = db_stride;
+    a.cu = cu_seqlens_d;
+    a.slots = slots_d;
+    a.mask = mask_d;
+    a.state_out = dstate_d;
+    a.carry = const_cast<float*>(carry_d);
+    a.n_slots = n_slots;
+    a.has_state = dstate_d != nullptr;
+    a.n_tokens = static_cast<int32_t>(n_tokens);
+    a.n_seqs = static_cast<int32_t>(n_seqs);
+    a.max_chunks = static_cast<int32_t>(max_chunks(n_tokens, n_seqs));
+    a.keys = key_heads;
+    a.heads = heads;
+    a.dk = dk;
+    a.dv = dv;
+    a.scale = scale;
+    a.vec = pieces(q_d, q_stride, E::kBytes) && pieces(k_d, k_stride, E::kBytes) && pieces(v_d, v_stride, E::kBytes) &&
+            pieces(dy_d, dy_stride, E::kBytes) && dk % 8 == 0 && dv % 8 == 0;
+    a.status = status_d;
+    const Space s = space(workspace_d, n_tokens, n_seqs, key_heads, heads, dk, dv, true);
+    a.first = s.first;
+    a.tri = s.tri;
+    a.gates = s.gates;
+    a.after = s.after;
+    a.writes = s.writes;
+    a.shared = s.shared;
+    return launch_grad<E>(a, as_stream(stream));
+  };
+  return type == ENGRAM_T_BF16 ? go(train::Bf16{}) : go(train::F32{});
+}

@@ -757,6 +757,21 @@ int engram_delta(const void* q_d, int64_t q_stride, const void* k_d, int64_t k_s
                  const float* state_d, float* state_out_d, int64_t n_slots, void* y_d, int64_t y_stride,
                  float* carry_d, void* workspace_d, size_t workspace_bytes, int32_t* status_d, void* stream);
 
+/* The gradients of q, k, v, g, b and the first states; those of a key head are summed over
+ * the value heads that share it.  carry_d is what a forward call on the same arguments
+ * filled; the chunks are computed again from it.
+ *   dstate_d     float32 [n_slots][heads][dk][dv] in/out, or NULL (zeros in): the
+ *                gradients of the last states on entry, of the first states on return
+ *   workspace_d  engram_delta_workspace_bytes(..., 1) bytes */
+int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void* q_d, int64_t q_stride, const void* k_d,
+                      int64_t k_stride, const void* v_d, int64_t v_stride, const void* g_d, int64_t g_stride,
+                      const void* b_d, int64_t b_stride, int32_t type, int64_t n_tokens, int32_t key_heads,
+                      int32_t heads, int32_t dk, int32_t dv, float scale, const int64_t* cu_seqlens_d, int64_t n_seqs,
+                      const int32_t* slots_d, const uint8_t* mask_d, const float* carry_d, float* dstate_d,
+                      int64_t n_slots, void* dq_d, int64_t dq_stride, void* dk_d, int64_t dk_stride, void* dv_d,
+                      int64_t dv_stride, void* dg_d, int64_t dg_stride, void* db_d, int64_t db_stride,
+                      void* workspace_d, size_t workspace_bytes, int32_t* status_d, void* stream);
+
 /* One position for each of `batch` sequences (decode): row b belongs to state slots_d[b];
  * a negative slot is padding (y = 0, no state), which is also how a masked position is
  * passed; a slot >= n_slots sets ENGRAM_ST_BAD_SLOT and is padding.  Slots are distinct.

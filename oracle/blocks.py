@@ -180,7 +180,8 @@ def delta(q, k, v, g, b, cu: List[int], keys: int, scale: float, mask: Optional[
 def delta_grad(dy, q, k, v, g, b, cu: List[int], keys: int, scale: float, mask: Optional[List[int]] = None,
                state: Optional[torch.Tensor] = None, slots: Optional[List[int]] = None,
                dstate: Optional[torch.Tensor] = None):
-    """dict of dq, dk, dv, dg, db and the first states' gradient dstate."""
+    """dict of dq, dk, dv, dg, db and the first states' gradient dstate; `reach`, the largest value of any position's
+    state's gradient, and `held`, that of any state, for the tests' tolerances."""
     fwd = delta(q, k, v, g, b, cu, keys, scale, mask, state, slots)
     T, H = g.shape
     Q, K, V = _heads(q, keys, H // keys), _heads(k, keys, H // keys), v.view(T, H, -1)
@@ -189,6 +190,7 @@ def delta_grad(dy, q, k, v, g, b, cu: List[int], keys: int, scale: float, mask: 
     dq, dk, dv = torch.zeros_like(Q), torch.zeros_like(K), torch.zeros_like(V)
     dg, db = torch.zeros_like(f), torch.zeros_like(f)
     out = None if dstate is None else dstate.clone()
+    reach = 0.0
     for n in range(len(cu) - 1):
         slot = n if slots is None else slots[n]
         if slot < 0:
@@ -203,6 +205,7 @@ def delta_grad(dy, q, k, v, g, b, cu: List[int], keys: int, scale: float, mask: 
             after = S + K[t][:, :, None] * u[:, None]
             dq[t] = (after * do[t][:, None]).sum(2)
             dS = dS + Q[t][:, :, None] * do[t][:, None]
+            reach = max(reach, float(dS.abs().max()))
             du = (dS * K[t][:, :, None]).sum(1)
             dv[t] = beta[t][:, None] * du
             seen = (S * K[t][:, :, None]).sum(1)
@@ -214,4 +217,5 @@ def delta_grad(dy, q, k, v, g, b, cu: List[int], keys: int, scale: float, mask: 
         if out is not None:
             out[slot] = dS
     shared = lambda x: x.view(T, keys, H // keys, -1).sum(2).reshape(T, -1)  # noqa: E731
-    return dict(dq=shared(dq), dk=shared(dk), dv=dv.reshape(T, -1), dg=dg, db=db, dstate=out)
+    held = max(float(fwd["before"].abs().max()), float(fwd["us"].abs().max())) if T else 0.0
+    return dict(dq=shared(dq), dk=shared(dk), dv=dv.reshape(T, -1), dg=dg, db=db, dstate=out, reach=reach, held=held)
