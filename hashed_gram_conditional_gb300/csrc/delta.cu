@@ -54,7 +54,7 @@ constexpr int kPitch = kC + 4;  // of fp32 64 x 64 matrices
 // terms (22 bits), three products.
 __device__ __forceinline__ void small_product(float* dst, const float* a, const float* b, int depth, float sign) {
   const int l = lane_id(), g = l >> 2, t = l & 3;
-  float c[2][4] = {};
+  float c[2][4] = {}, small[2][4] = {};
   auto tf32 = [](float x) {
     uint32_t r;
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
@@ -77,22 +77,22 @@ __device__ __forceinline__ void small_product(float* dst, const float* a, const 
         bh[j] = tf32(x);
         bl[j] = tf32(x - __uint_as_float(bh[j]));
       }
-      auto step = [&](const uint32_t (&x)[4], const uint32_t (&y)[2]) {
+      auto step = [&](float (&c)[4], const uint32_t (&x)[4], const uint32_t (&y)[2]) {
         asm volatile(
             "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
             "%3};"
-            : "+f"(c[n][0]), "+f"(c[n][1]), "+f"(c[n][2]), "+f"(c[n][3])
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(y[0]), "r"(y[1]));
       };
-      step(al, bh);
-      step(ah, bl);
-      step(ah, bh);
+      step(small[n], al, bh);
+      step(small[n], ah, bl);
+      step(c[n], ah, bh);
     }
   }
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dst[(g + (j >> 1) * 8) * kPitch + n * 8 + 2 * t + (j & 1)] = sign * c[n][j];
+    for (int j = 0; j < 4; ++j) dst[(g + (j >> 1) * 8) * kPitch + n * 8 + 2 * t + (j & 1)] = sign * (c[n][j] + small[n][j]);
 }
 
 // A pair of neighbouring columns of a triangle as N terms in the workspace.
@@ -109,137 +109,165 @@ __device__ __forceinline__ void put_tri(unsigned char* base, int t, int i, float
   }
 }
 
+constexpr int kPrepareThreads = 128;
 template <class E, int KD>
-constexpr int kPrepareSmem = 2 * kIn<E>* mat_bytes(kC, KD) + 4 * kC * kPitch * 4 + static_cast<int>(sizeof(Gates));
+constexpr int kPrepareSmem = std::max(2 * kIn<E> * mat_bytes(kC, KD), 2 * kC * kPitch * 4) + static_cast<int>(sizeof(Gates));
 
-// A block makes M and P for the heads that share a key head, in one chunk.
+// A block of four warps makes M and P of one head in one chunk.  K K^T and Q K^T stay in
+// the registers until they are A and P; A and M take the place of K and Q.  Heads that
+// share a key head compute its products again: a third of a microsecond of the tensor
+// cores for each head, where sharing them left most warps waiting (10,480 chunks and
+// heads: see the figures at scan_rows_kernel).
 template <class E, int KD>
-__global__ void __launch_bounds__(kThreads) prepare_kernel(Args<E> a) {
+__global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(Args<E> a) {
+  constexpr int kRoom = std::max(2 * kIn<E> * mat_bytes(kC, KD), 2 * kC * kPitch * 4);
   extern __shared__ __align__(128) unsigned char smem[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
   Chunk ch;
   if (!chunk_at(a, blockIdx.x, ch) || !ch.live) return;
   const Mat K = mat<kC, KD>(smem_u32(smem)), Q = mat<kC, KD>(K.base + kIn<E> * K.term);
-  float* kk = reinterpret_cast<float*>(smem + 2 * kIn<E> * mat_bytes(kC, KD));
-  float *qk = kk + kC * kPitch, *A = qk + kC * kPitch, *M = A + kC * kPitch;
-  Gates& gt = *reinterpret_cast<Gates*>(M + kC * kPitch);
+  float *A = reinterpret_cast<float*>(smem), *M = A + kC * kPitch;
+  Gates& gt = *reinterpret_cast<Gates*>(smem + kRoom);
   const uint8_t* mask = a.mask != nullptr ? a.mask + ch.start : nullptr;
-  const int hk = blockIdx.y, group = a.heads / a.keys;
-  load_rows<E, KD>(K, a.k + ch.start * a.k_stride + hk * a.dk, a.k_stride, ch.len, a.dk, mask, a.vec);
-  load_rows<E, KD>(Q, a.q + ch.start * a.q_stride + hk * a.dk, a.q_stride, ch.len, a.dk, mask, a.vec);
+  const int h = blockIdx.y, hk = h / (a.heads / a.keys);
+  load_rows<E, KD, kPrepareThreads>(K, a.k + ch.start * a.k_stride + hk * a.dk, a.k_stride, ch.len, a.dk, mask, a.vec);
+  load_rows<E, KD, kPrepareThreads>(Q, a.q + ch.start * a.q_stride + hk * a.dk, a.q_stride, ch.len, a.dk, mask, a.vec);
   copies_begun();
-  copies_done();
-  __syncthreads();
-  {  // K K^T and Q K^T: a warp has 16 rows and 32 columns of each
-    const int m = (warp & 3) * 16, n = (warp >> 2) * 32;
-    if (n <= m) {
-      float ck[4][4], cq[4][4];
-      clear(ck);
-      clear(cq);
-      product<kIn<E>, kIn<E>, kIn<E>>(ck, Rows{K}, Across{K}, m, n, 0, KD);
-      product<kIn<E>, kIn<E>, kIn<E>>(cq, Rows{Q}, Across{K}, m, n, 0, KD);
+  if (warp == 0) {  // c, two positions a lane: multiples of 1/256 as integers, and the rest
+    int hi[2];
+    float lo[2], beta[2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+    for (int j = 0; j < 2; ++j) {
+      const int r = lane * 2 + j;
+      const bool on = r < ch.len && !(mask != nullptr && mask[r]);
+      const int64_t t = ch.start + (on ? r : 0);
+      // gates below -80 count as -80, b below -40 as -40 (a NaN stays)
+      float x = E::load(a.g + t * a.g_stride + h), b = E::load(a.b + t * a.b_stride + h);
+      x = x < -80.f ? -80.f : x;
+      b = b < -40.f ? -40.f : b;
+      x = on ? (x < 0.f ? x - log1pf(expf(x)) : -log1pf(expf(-x))) : 0.f;
+      beta[j] = on ? 1.f / (1.f + expf(-b)) : 0.f;
+      hi[j] = __float2int_rn(x * 256.f);  // (0 for a NaN, which the rest then is)
+      lo[j] = x - static_cast<float>(hi[j]) * (1.f / 256.f);
+    }
+    int sum_hi = hi[0] + hi[1];
+    float sum_lo = lo[0] + lo[1];
+    const int own_hi = sum_hi;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int at = (m + (lane >> 2) + (j >> 1) * 8) * kPitch + n + t * 8 + (lane & 3) * 2 + (j & 1);
-          kk[at] = ck[t][j];
-          qk[at] = cq[t][j];
-        }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sum_hi, o);
+      const float y = __shfl_up_sync(0xffffffffu, sum_lo, o);
+      if (lane >= o) {
+        sum_hi += x;
+        sum_lo += y;
+      }
+    }
+    float before = __shfl_up_sync(0xffffffffu, sum_lo, 1);
+    before = lane == 0 ? 0.f : before;
+    const int all_hi = __shfl_sync(0xffffffffu, sum_hi, 31);
+    const float all_lo = __shfl_sync(0xffffffffu, sum_lo, 31);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = lane * 2 + j, to = sum_hi - own_hi + hi[0] + (j ? hi[1] : 0);
+      const float rest = j ? sum_lo : before + lo[0];
+      gt.hi[r] = static_cast<float>(to) * (1.f / 256.f);  // exact: below 2^24 / 256
+      gt.lo[r] = rest;
+      gt.into[r] = expf(static_cast<float>(to) * (1.f / 256.f) + rest);
+      gt.last[r] = expf(static_cast<float>(all_hi - to) * (1.f / 256.f) + (all_lo - rest));
+      gt.beta[r] = beta[j];
     }
   }
-  for (int h = hk * group; h < (hk + 1) * group; ++h) {
-    unsigned char* tri = a.tri + unit_of(a, blockIdx.x, h) * kTriBytes;
-    if (warp == 0) {  // c, two positions a lane
-      double c[2], sum;
-      float beta[2];
+  copies_done();
+  __syncthreads();
+  const int m = warp * 16;  // a warp has 16 rows, and the columns up to the diagonal
+  float ck[kC / 8][4], cq[kC / 8][4];
+  clear(ck);
+  clear(cq);
+  for (int k = 0; k < KD; k += 16) {
+    uint32_t fk[kIn<E>][4], fq[kIn<E>][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = lane * 2 + j;
-        const bool on = r < ch.len && !(mask != nullptr && mask[r]);
-        const int64_t t = ch.start + (on ? r : 0);
-        // gates below -80 count as -80, b below -40 as -40 (a NaN stays)
-        float g = E::load(a.g + t * a.g_stride + h), b = E::load(a.b + t * a.b_stride + h);
-        g = g < -80.f ? -80.f : g;
-        b = b < -40.f ? -40.f : b;
-        c[j] = on ? static_cast<double>(g < 0.f ? g - log1pf(expf(g)) : -log1pf(expf(-g))) : 0.0;
-        beta[j] = on ? 1.f / (1.f + expf(-b)) : 0.f;
-      }
-      c[1] += c[0];
-      sum = c[1];
+    for (int i = 0; i < kIn<E>; ++i) {
+      Rows{K}(fk[i], m, k, i);
+      Rows{Q}(fq[i], m, k, i);
+    }
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += x;
-      }
-      const double before = sum - c[1], all = __shfl_sync(0xffffffffu, sum, 31);
+    for (int n = 0; n < kC / 16; ++n) {
+      if (n > warp) continue;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = lane * 2 + j;
-        const double x = before + c[j];
-        // c = hi + lo, hi a multiple of 1/16: differences of hi are exact
-        const float hi = rintf(static_cast<float>(x) * 16.f) * 0.0625f;
-        gt.hi[r] = hi;
-        gt.lo[r] = static_cast<float>(x - hi);
-        gt.into[r] = expf(static_cast<float>(x));
-        gt.last[r] = expf(static_cast<float>(all - x));
-        gt.beta[r] = beta[j];
+      for (int j = kIn<E> - 1; j >= 0; --j) {
+        uint32_t fb[2][2];
+        Across{K}.get<2>(fb, k, n * 16, j);
+#pragma unroll
+        for (int i = kIn<E> - 1; i >= 0; --i)
+          if (i + j < kIn<E>) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              mma(ck[n * 2 + e], fk[i], fb[e][0], fb[e][1]);
+              mma(cq[n * 2 + e], fq[i], fb[e][0], fb[e][1]);
+            }
+          }
       }
     }
-    __syncthreads();
-    for (int i = tid; i < static_cast<int>(sizeof(Gates)) / 4; i += kThreads)
-      reinterpret_cast<float*>(a.gates + unit_of(a, blockIdx.x, h))[i] = reinterpret_cast<const float*>(&gt)[i];
-    for (int p = tid; p < kC * kC / 2; p += kThreads) {
-      const int t = p >> 5, i = (p & 31) * 2;
-      if ((i >> 4) > (t >> 4)) continue;
-      float x[2], y[2];
+  }
+  __syncthreads();  // K and Q are no longer needed
+  const size_t unit = unit_of(a, blockIdx.x, h);
+  unsigned char* tri = a.tri + unit * kTriBytes;
+  for (int i = tid; i < static_cast<int>(sizeof(Gates)) / 4; i += kPrepareThreads)
+    reinterpret_cast<float*>(a.gates + unit)[i] = reinterpret_cast<const float*>(&gt)[i];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const bool in = i + j <= t;
-        const float d = in ? expf((gt.hi[t] - gt.hi[i + j]) + (gt.lo[t] - gt.lo[i + j])) : 0.f;
-        x[j] = i + j < t ? gt.beta[t] * d * kk[t * kPitch + i + j] : 0.f;
-        y[j] = in ? a.scale * d * qk[t * kPitch + i + j] : 0.f;
+  for (int n = 0; n < kC / 8; ++n) {
+    if (n / 2 > warp) continue;
+    const int i = n * 8 + t2;
+    const float2 hi = *reinterpret_cast<const float2*>(&gt.hi[i]), lo = *reinterpret_cast<const float2*>(&gt.lo[i]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int t = m + g + j * 8;
+      const float d0 = i <= t ? expf((gt.hi[t] - hi.x) + (gt.lo[t] - lo.x)) : 0.f;
+      const float d1 = i + 1 <= t ? expf((gt.hi[t] - hi.y) + (gt.lo[t] - lo.y)) : 0.f;
+      *reinterpret_cast<float2*>(A + t * kPitch + i) = make_float2(i < t ? gt.beta[t] * d0 * ck[n][2 * j] : 0.f,
+                                                                    i + 1 < t ? gt.beta[t] * d1 * ck[n][2 * j + 1] : 0.f);
+      put_tri<kStateTerms>(tri + kStateTerms * kTerm, t, i, i <= t ? a.scale * d0 * cq[n][2 * j] : 0.f,
+                           i + 1 <= t ? a.scale * d1 * cq[n][2 * j + 1] : 0.f);
+    }
+  }
+  __syncwarp();
+  // (I + A)^-1: a warp's block of 16 by substitution, a column a lane; then twice
+  // [M11 0; -M22 A21 M11 M22].  A's blocks above the diagonal hold what comes in between.
+  if (lane < 16) {
+    const float* D = A + m * (kPitch + 1);
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s0 = i == lane ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+      for (int j = 0; j < i; ++j) {
+        float& s = j & 1 ? s1 : s0;
+        s = fmaf(-D[i * kPitch + j], x[j], s);
       }
-      A[t * kPitch + i] = x[0];
-      A[t * kPitch + i + 1] = x[1];
-      put_tri<kStateTerms>(tri + kStateTerms * kTerm, t, i, y[0], y[1]);
+      x[i] = s0 + s1;
+      M[(m + i) * kPitch + m + lane] = x[i];
     }
-    __syncthreads();
-    // (I + A)^-1: blocks of 16 by substitution, a column a lane; then [M11 0; -M22 A21 M11 M22]
-    if (warp < 4 && lane < 16) {
-      const float* D = A + warp * 16 * (kPitch + 1);
-      float x[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float s = i == lane ? 1.f : 0.f;
-#pragma unroll
-        for (int j = 0; j < i; ++j) s = fmaf(-D[i * kPitch + j], x[j], s);
-        x[i] = s;
-        M[(warp * 16 + i) * kPitch + warp * 16 + lane] = s;
-      }
-    }
-    __syncthreads();
-    if (warp < 2) {  // (A's blocks above the diagonal are free for the products in between)
-      const int o = warp * 32 * (kPitch + 1), down = 16 * kPitch;
-      small_product(A + o + 16, A + o + down, M + o, 16, 1.f);
-      __syncwarp();
-      small_product(M + o + down, M + o + down + 16, A + o + 16, 16, -1.f);
-    }
-    __syncthreads();
-    const int bm = (warp & 1) * 16, bn = (warp >> 1) * 16;
-    // (M's upper block of the first half is not written above: the product of the second
-    // half of the columns starts below it)
-    if (warp < 4) small_product(A + bm * kPitch + 32 + bn, A + (32 + bm) * kPitch + bn, M + bn * kPitch + bn, 32 - bn, 1.f);
-    __syncthreads();
-    if (warp < 4) small_product(M + (32 + bm) * kPitch + bn, M + (32 + bm) * kPitch + 32, A + 32 + bn, 16 + bm, -1.f);
-    __syncthreads();
-    for (int p = tid; p < kC * kC / 2; p += kThreads) {
-      const int t = p >> 5, i = (p & 31) * 2;
-      if ((i >> 4) > (t >> 4)) continue;
-      put_tri<kStateTerms>(tri, t, i, i <= t ? M[t * kPitch + i] * gt.beta[i] : 0.f,
-                           i + 1 <= t ? M[t * kPitch + i + 1] * gt.beta[i + 1] : 0.f);
-    }
-    __syncthreads();
+  }
+  __syncthreads();
+  if (warp < 2) {
+    const int o = warp * 32 * (kPitch + 1), down = 16 * kPitch;
+    small_product(A + o + 16, A + o + down, M + o, 16, 1.f);
+    __syncwarp();
+    small_product(M + o + down, M + o + down + 16, A + o + 16, 16, -1.f);
+  }
+  __syncthreads();
+  const int bm = (warp & 1) * 16, bn = (warp >> 1) * 16;
+  // (a column block's upper half begins at its own rows)
+  small_product(A + bm * kPitch + 32 + bn, A + (32 + bm) * kPitch + bn, M + bn * kPitch + bn, 32 - bn, 1.f);
+  __syncthreads();
+  small_product(M + (32 + bm) * kPitch + bn, M + (32 + bm) * kPitch + 32, A + 32 + bn, 16 + bm, -1.f);
+  __syncthreads();
+#pragma unroll 4
+  for (int p = tid; p < kBlocks * 128; p += kPrepareThreads) {
+    const int b = p >> 7, bt = b >= 6 ? 3 : b >= 3 ? 2 : b >= 1 ? 1 : 0, bi = b - bt * (bt + 1) / 2;
+    const int t = bt * 16 + ((p >> 3) & 15), i = bi * 16 + (p & 7) * 2;
+    const float2 x = *reinterpret_cast<const float2*>(M + t * kPitch + i);
+    put_tri<kStateTerms>(tri, t, i, i <= t ? x.x * gt.beta[i] : 0.f, i + 1 <= t ? x.y * gt.beta[i + 1] : 0.f);
   }
 }
 
@@ -251,7 +279,7 @@ int launch_prepare(const Args<E>& a, cudaStream_t st) {
   auto go = [&](auto kernel, int smem, std::atomic<uint64_t>& done) {
     int r = opt_in(reinterpret_cast<const void*>(kernel), smem, done);
     if (r) return r;
-    kernel<<<dim3(a.max_chunks, a.keys), kThreads, smem, st>>>(a);
+    kernel<<<dim3(a.max_chunks, a.heads), kPrepareThreads, smem, st>>>(a);
     return check_launch("prepare_kernel");
   };
   static std::atomic<uint64_t> done[2] = {{0}, {0}};
@@ -262,6 +290,200 @@ template int launch_prepare<train::Bf16>(const Args<train::Bf16>&, cudaStream_t)
 template int launch_prepare<train::F32>(const Args<train::F32>&, cudaStream_t);
 
 // --------------------------------------------------------------------- scan
+
+// A warp follows one sequence in one head, for 16 of the value columns; a block's W
+// warps share the chunks' inputs.  The state is held transposed, S^T [16][dk], as an
+// accumulator, which is the next product's operand as it lies in the registers: so are
+// X^T = V^T - e^c (K S)^T, U^T = X^T M^T and what is added to S^T.  Nothing but the
+// inputs goes through shared memory, and a chunk needs one barrier, for their copies.
+// Bound by the tensor cores: 692 instructions of 2048 multiply-adds a warp and chunk
+// (dk = 128), of which 192 + 120 + 192 are on the state's way, in three terms.
+template <class E, int KD, int W>
+struct ScanRows {
+  static constexpr int kStages = E::kBytes == 2 ? 2 : 1;
+  static constexpr int kK = 0, kQ = kK + kIn<E> * mat_bytes(kC, KD), kV = kQ + kIn<E> * mat_bytes(kC, KD);
+  static constexpr int kM = kV + kIn<E> * mat_bytes(kC, 16 * W), kP = kM + kStateTerms * kTerm, kG = kP + kOut<E> * kTerm;
+  static constexpr int kStage = kG + static_cast<int>(sizeof(Gates));
+  static constexpr int kSmem = kStages * kStage;
+};
+
+template <class E, int KD, int W>
+__global__ void __launch_bounds__(W * 32, 1) scan_rows_kernel(Args<E> a) {
+  using L = ScanRows<E, KD, W>;
+  constexpr int kT = W * 32, kI = kIn<E>, kO = kOut<E>, kS = kStateTerms;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
+  const int seq = blockIdx.x, h = blockIdx.y, v0 = blockIdx.z * (16 * W), cols = min(a.dv - v0, 16 * W);
+  const int hk = h / (a.heads / a.keys), vw = v0 + warp * 16;  // vw: the warp's first column
+  int lo, hi;
+  bounds(a, seq, lo, hi);
+  const int c0 = a.first[seq], n = min((hi - lo + kC - 1) / kC, a.max_chunks - c0);
+  const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
+  int64_t slot;
+  if (!live_slot(a, seq, slot)) {
+    if (tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
+    padding_zeros(a, lo, hi, c0, n, h, v0, cols, kT);
+    return;
+  }
+  float S[KD / 8][4];  // (column vw + g, or 8 further; row of the state)
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int t = 0; t < KD / 8; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int v = vw + g + (j >> 1) * 8, k = t * 8 + t2 + (j & 1);
+        if (v < a.dv && k < a.dk) f(t, j, static_cast<size_t>(k) * a.dv + v);
+      }
+  };
+  clear(S);
+  if (a.state != nullptr) {
+    const float* from = a.state + (slot * a.heads + h) * matrix;
+    each([&](int t, int j, size_t at) { S[t][j] = from[at]; });
+  }
+  auto load = [&](int i) {
+    const uint32_t stage = base + (i % L::kStages) * L::kStage;
+    const int64_t p = lo + static_cast<int64_t>(i) * kC;
+    const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
+    const uint8_t* mask = a.mask != nullptr ? a.mask + p : nullptr;
+    const size_t unit = unit_of(a, c0 + i, h);
+    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kK), a.k + p * a.k_stride + hk * a.dk, a.k_stride, len, a.dk, mask, a.vec);
+    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kQ), a.q + p * a.q_stride + hk * a.dk, a.q_stride, len, a.dk, mask, a.vec);
+    load_rows<E, 16 * W, kT>(mat<kC, 16 * W>(stage + L::kV), a.v + p * a.v_stride + h * a.dv + v0, a.v_stride, len, cols, mask,
+                             a.vec);
+    load_tri<kO, kT>(stage + L::kM, stage + L::kP, a.tri + unit * kTriBytes);
+    load_gates<kT>(stage + L::kG, a.gates + unit);
+    copies_begun();
+  };
+  if (n > 0) load(0);
+  const bool even = a.dk % 2 == 0 && (reinterpret_cast<uintptr_t>(a.carry) & 7) == 0;
+  for (int i = 0; i < n; ++i) {
+    const uint32_t stage = base + (i % L::kStages) * L::kStage;
+    const Mat K = mat<kC, KD>(stage + L::kK), Q = mat<kC, KD>(stage + L::kQ), V = mat<kC, 16 * W>(stage + L::kV);
+    const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
+    copies_done();
+    __syncthreads();  // the chunk is here, and the other stage is free
+    if (L::kStages == 2 && i + 1 < n) load(i + 1);
+    if (a.carry != nullptr) save_state<E, KD>(a, a.carry, unit_of(a, c0 + i, h), S, vw, even);
+    // ---- (K S)^T and (Q S)^T
+    float x[kC / 8][4], s[kC / 8][4], y[kC / 8][4];
+    clear(x);
+    clear(s);
+    clear(y);
+#pragma unroll
+    for (int kb = 0; kb < KD / 16; ++kb) {
+      uint32_t fa[kS][4];
+      as_operand<kS>(fa, S[2 * kb], S[2 * kb + 1]);
+#pragma unroll
+      for (int cb = 0; cb < kC / 16; ++cb) {
+        uint32_t fb[kI][2][2];
+#pragma unroll
+        for (int j = 0; j < kI; ++j) Across{K}.get<2>(fb[j], kb * 16, cb * 16, j);
+        pair_product<kS, kI, kS>(x[2 * cb], x[2 * cb + 1], s[2 * cb], s[2 * cb + 1], fa, fb);
+        uint32_t fo[kO][4];
+#pragma unroll
+        for (int j = 0; j < kO; ++j)
+#pragma unroll
+          for (int p = 0; p < 4; ++p) fo[j][p] = fa[j][p];
+#pragma unroll
+        for (int j = 0; j < kI; ++j) Across{Q}.get<2>(fb[j], kb * 16, cb * 16, j);
+        pair_product<kO, kI, kO>(y[2 * cb], y[2 * cb + 1], y[2 * cb], y[2 * cb + 1], fo, fb);
+      }
+    }
+    // ---- X^T
+#pragma unroll
+    for (int cb = 0; cb < kC / 16; ++cb) {
+      float v[8] = {};
+#pragma unroll
+      for (int j = kI - 1; j >= 0; --j) {
+        uint32_t f[4];
+        Cols{V}(f, warp * 16, cb * 16, j);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          v[2 * p] += lo_of(f[p]);
+          v[2 * p + 1] += hi_of(f[p]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 into = *reinterpret_cast<const float2*>(&gt.into[cb * 16 + e * 8 + t2]);
+        float(&c)[4] = x[2 * cb + e];
+        const float(&d)[4] = s[2 * cb + e];
+        c[0] = fmaf(-into.x, c[0] + d[0], v[4 * e]);
+        c[1] = fmaf(-into.y, c[1] + d[1], v[4 * e + 1]);
+        c[2] = fmaf(-into.x, c[2] + d[2], v[4 * e + 2]);
+        c[3] = fmaf(-into.y, c[3] + d[3], v[4 * e + 3]);
+        float(&o)[4] = y[2 * cb + e];
+        o[0] *= a.scale * into.x;
+        o[1] *= a.scale * into.y;
+        o[2] *= a.scale * into.x;
+        o[3] *= a.scale * into.y;
+      }
+    }
+    // ---- U^T
+    float u[kC / 8][4];
+    clear(u);
+    clear(s);
+#pragma unroll
+    for (int ib = 0; ib < kC / 16; ++ib) {
+      uint32_t fa[kS][4];
+      as_operand<kS>(fa, x[2 * ib], x[2 * ib + 1]);
+#pragma unroll
+      for (int tb = ib; tb < kC / 16; ++tb) {
+        uint32_t fb[kS][2][2];
+#pragma unroll
+        for (int j = 0; j < kS; ++j) TriAcross{stage + L::kM}.get(fb[j], ib, tb, j);
+        pair_product<kS, kS, kS>(u[2 * tb], u[2 * tb + 1], s[2 * tb], s[2 * tb + 1], fa, fb);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kC / 8; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[t][j] += s[t][j];
+    // ---- Y^T
+#pragma unroll
+    for (int ib = 0; ib < kC / 16; ++ib) {
+      uint32_t fa[kO][4];
+      as_operand<kO>(fa, u[2 * ib], u[2 * ib + 1]);
+#pragma unroll
+      for (int tb = ib; tb < kC / 16; ++tb) {
+        uint32_t fb[kO][2][2];
+#pragma unroll
+        for (int j = 0; j < kO; ++j) TriAcross{stage + L::kP}.get(fb[j], ib, tb, j);
+        pair_product<kO, kO, kO>(y[2 * tb], y[2 * tb + 1], y[2 * tb], y[2 * tb + 1], fa, fb);
+      }
+    }
+    const int64_t p = lo + static_cast<int64_t>(i) * kC;
+    const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
+    store_rows<E>(a.y + p * a.y_stride + h * a.dv, a.y_stride, len, vw, a.dv, a.pairs, gt.beta, y);
+    // ---- S^T
+    uint32_t fa[kC / 16][kS][4];
+#pragma unroll
+    for (int cb = 0; cb < kC / 16; ++cb) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 last = *reinterpret_cast<const float2*>(&gt.last[cb * 16 + e * 8 + t2]);
+        float(&c)[4] = u[2 * cb + e];
+        c[0] *= last.x;
+        c[1] *= last.y;
+        c[2] *= last.x;
+        c[3] *= last.y;
+      }
+      as_operand<kS>(fa[cb], u[2 * cb], u[2 * cb + 1]);
+    }
+    add_outer<E, KD>(S, gt.into[kC - 1], fa, K);
+    if (L::kStages == 1 && i + 1 < n) {
+      __syncthreads();  // the stage is free
+      load(i + 1);
+    }
+  }
+  if (a.state_out != nullptr) {
+    float* to = a.state_out + (slot * a.heads + h) * matrix;
+    each([&](int t, int j, size_t at) { to[at] = S[t][j]; });
+  }
+}
+
+// -------------------------------------------- scan of few sequences and heads
 
 // A block follows one sequence's chunks in one head, for kVS of the value columns.
 // The state stays in registers as the products' accumulator; its terms go to shared
@@ -297,12 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_kernel(Args<E> a) {
   const bool live = live_slot(a, seq, slot);
   if (!live && tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
   const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
-  if (!live) {  // padding: zeros
-    for (int64_t i = tid; i < static_cast<int64_t>(hi - lo) * cols; i += kThreads)
-      E::store(a.y + (lo + i / cols) * a.y_stride + h * a.dv + v0 + i % cols, 0.f);
-    for (int c = 0; a.carry != nullptr && c < n; ++c)
-      for (int i = tid; i < a.dk * cols; i += kThreads)
-        a.carry[unit_of(a, c0 + c, h) * matrix + static_cast<size_t>(i / cols) * a.dv + v0 + i % cols] = 0.f;
+  if (!live) {
+    padding_zeros(a, lo, hi, c0, n, h, v0, cols, kThreads);
     return;
   }
   // the rows and columns of the state that this thread holds
@@ -354,8 +572,14 @@ __global__ void __launch_bounds__(kThreads, 1) scan_kernel(Args<E> a) {
     __syncthreads();  // the chunk and the state are here, and the other stage is free
     if (L::kStages == 2 && i + 1 < n) load(i + 1);
     if (a.carry != nullptr) {
-      float* to = a.carry + unit_of(a, c0 + i, h) * matrix;
-      each([&](int t, int j, size_t at) { to[at] = S[t][j]; });
+      const size_t unit = unit_of(a, c0 + i, h);
+#pragma unroll
+      for (int t = 0; t < L::kSN; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = sm + g + (j >> 1) * 8, c = sn + t * 8 + t2 + (j & 1);
+          if (r < a.dk && c < cols) save<E>(a.carry, unit, matrix, static_cast<size_t>(v0 + c) * a.dk + r, S[t][j]);
+        }
     }
     float x[L::kN][4], y[L::kN][4];
     clear(x);
@@ -421,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_kernel(Args<E> a) {
 }
 
 template <class E>
-int launch_scan(const Args<E>& a, cudaStream_t st) {
+int launch_scan(const Args<E>& a, int sms, cudaStream_t st) {
   static std::atomic<uint64_t> done[2] = {{0}, {0}};
   auto go = [&](auto kernel, int smem, int vs, std::atomic<uint64_t>& flag) {
     int r = opt_in(reinterpret_cast<const void*>(kernel), smem, flag);
@@ -429,8 +653,19 @@ int launch_scan(const Args<E>& a, cudaStream_t st) {
     kernel<<<dim3(a.n_seqs, a.heads, (a.dv + vs - 1) / vs), kThreads, smem, st>>>(a);
     return check_launch("scan_kernel");
   };
-  return a.dk <= 64 ? go(scan_kernel<E, 64, 32>, Scan<E, 64, 32>::kSmem, 32, done[0])
-                    : go(scan_kernel<E, 128, 32>, Scan<E, 128, 32>::kSmem, 32, done[1]);
+  if constexpr (E::kBytes == 2) if (by_warps(a, sms)) {
+    auto rows = [&](auto kernel, int smem, int w, std::atomic<uint64_t>& flag) {
+      int r = opt_in(reinterpret_cast<const void*>(kernel), smem, flag);
+      if (r) return r;
+      kernel<<<dim3(a.n_seqs, a.heads, (a.dv + 16 * w - 1) / (16 * w)), w * 32, smem, st>>>(a);
+      return check_launch("scan_rows_kernel");
+    };
+    static std::atomic<uint64_t> flags[2] = {{0}, {0}};
+    return a.dk <= 64 ? rows(scan_rows_kernel<E, 64, 8>, ScanRows<E, 64, 8>::kSmem, 8, flags[0])
+                      : rows(scan_rows_kernel<E, 128, 8>, ScanRows<E, 128, 8>::kSmem, 8, flags[1]);
+  }
+  return a.dk <= 64 ? go(scan_kernel<E, 64, 16>, Scan<E, 64, 16>::kSmem, 16, done[0])
+                    : go(scan_kernel<E, 128, 16>, Scan<E, 128, 16>::kSmem, 16, done[1]);
 }
 
 // --------------------------------------------------------------------- step
@@ -557,7 +792,7 @@ Space space(void* base, int64_t n_tokens, int64_t n_seqs, int32_t keys, int32_t 
   s.gates = reinterpret_cast<Gates*>(take(units * sizeof(Gates)));
   if (backward) {
     s.after = reinterpret_cast<float*>(take(units * dk * dv * sizeof(float)));
-    s.writes = reinterpret_cast<float*>(take(static_cast<size_t>(n_tokens) * heads * dv * sizeof(float)));
+    s.writes = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(n_tokens) * heads * dv * sizeof(uint16_t)));
     if (heads > keys) s.shared = reinterpret_cast<float*>(take(2 * static_cast<size_t>(n_tokens) * keys * dk * sizeof(float)));
   }
   s.bytes = at;
@@ -609,7 +844,8 @@ extern "C" int engram_delta(const void* q_d, int64_t q_stride, const void* k_d, 
   if (!aligned(workspace_d, 256)) return fail(ENGRAM_E_ALIGN, "workspace must be 256-byte aligned");
   if (workspace_bytes < engram_delta_workspace_bytes(n_tokens, n_seqs, key_heads, heads, dk, dv, 0))
     return fail(ENGRAM_E_RANGE, "workspace too small");
-  if ((rc = check_device(nullptr))) return rc;
+  int sms = 0;
+  if ((rc = check_device(&sms))) return rc;
   auto go = [&](auto e) {
     using E = decltype(e);
     using T = typename E::T;
@@ -644,13 +880,14 @@ extern "C" int engram_delta(const void* q_d, int64_t q_stride, const void* k_d, 
     a.scale = scale;
     a.vec = pieces(q_d, q_stride, E::kBytes) && pieces(k_d, k_stride, E::kBytes) && pieces(v_d, v_stride, E::kBytes) &&
             dk % 8 == 0 && dv % 8 == 0;
+    a.pairs = dv % 2 == 0 && y_stride % 2 == 0 && aligned(y_d, 2 * E::kBytes);
     a.status = status_d;
     const Space s = space(workspace_d, n_tokens, n_seqs, key_heads, heads, dk, dv, false);
     a.first = s.first;
     a.tri = s.tri;
     a.gates = s.gates;
     int r = launch_prepare<E>(a, as_stream(stream));
-    return r ? r : launch_scan<E>(a, as_stream(stream));
+    return r ? r : launch_scan<E>(a, sms, as_stream(stream));
   };
   return type == ENGRAM_T_BF16 ? go(train::Bf16{}) : go(train::F32{});
 }

@@ -40,7 +40,7 @@ namespace engram {
 namespace delta {
 
 constexpr int kC = ENGRAM_DELTA_CHUNK;  // 64 positions
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;  // of most kernels
 constexpr int kMaxDim = ENGRAM_DELTA_MAX_DIM;
 // Lower triangles of 64 x 64 are kept as ten blocks of 16 x 16, a term's 512 bytes
 // each, the 16-byte halves of a block's rows 4 to 7 and 12 to 15 exchanged (eight
@@ -75,12 +75,17 @@ struct Args {
   int32_t n_tokens, n_seqs, max_chunks, keys, heads, dk, dv;
   float scale;
   bool vec;        // rows of q, k, v and dy in 16-byte pieces
+  bool pairs;      // rows of y or dv in pairs of elements
   bool has_state;  // slots are checked against n_slots
   // workspace
   int32_t* first;  // [n_seqs + 1] number of a sequence's first chunk
   unsigned char* tri;
   Gates* gates;
-  float *after, *writes, *shared;  // backward: states' gradients, those of the values, sums over heads that share a key
+  // backward: states' gradients behind the chunks, as `carry` has the states in front of them; the second terms of
+  // the values' gradients (bf16); sums over heads that share a key
+  float* after;
+  uint16_t* writes;
+  float* shared;
   int32_t* status;
 };
 
@@ -182,22 +187,34 @@ __device__ __forceinline__ Mat mat(uint32_t base) { return Mat{base, (kCols + 8)
 
 // kC rows of kCols columns (the first `cols` of them), zeros past the chunk's end and at
 // masked positions.  `src` is the first row's first element.
-template <class E, int kCols>
+template <class E, int kCols, int kT = kThreads>
 __device__ __forceinline__ void load_rows(const Mat& m, const typename E::T* src, int64_t stride, int len, int cols,
                                           const uint8_t* mask, bool vec) {
   if (E::kBytes == 2 && vec) {
-    for (int i = threadIdx.x; i < kC * (kCols / 8); i += kThreads) {
+#pragma unroll
+    for (int i0 = 0; i0 < kC * (kCols / 8); i0 += kT) {
+      const int i = i0 + threadIdx.x;
+      if (kC * (kCols / 8) % kT != 0 && i >= kC * (kCols / 8)) break;
       const int r = i / (kCols / 8), c = i % (kCols / 8) * 8;
       const bool on = r < len && c < cols && !(mask != nullptr && mask[r]);
       copy16(m.base + r * m.pitch + c * 2, on ? src + r * stride + c : src, on);
     }
   } else {
-    for (int i = threadIdx.x; i < kC * (kCols / 2); i += kThreads) {
-      const int r = i / (kCols / 2), c = i % (kCols / 2) * 2;
-      const bool on = r < len && !(mask != nullptr && mask[r]);
-      const float x0 = on && c < cols ? E::load(src + r * stride + c) : 0.f;
-      const float x1 = on && c + 1 < cols ? E::load(src + r * stride + c + 1) : 0.f;
-      put<kIn<E>>(m.base + r * m.pitch + c * 2, m.term, x0, x1);
+    constexpr int kAhead = 4;  // pairs on their way at once
+    for (int i0 = threadIdx.x; i0 < kC * (kCols / 2); i0 += kAhead * kT) {
+      float x[kAhead][2];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kT, r = i / (kCols / 2), c = i % (kCols / 2) * 2;
+        const bool on = r < len && !(mask != nullptr && mask[r]);
+        x[u][0] = on && c < cols ? E::load(src + r * stride + c) : 0.f;
+        x[u][1] = on && c + 1 < cols ? E::load(src + r * stride + c + 1) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kT, r = i / (kCols / 2), c = i % (kCols / 2) * 2;
+        if (i < kC * (kCols / 2)) put<kIn<E>>(m.base + r * m.pitch + c * 2, m.term, x[u][0], x[u][1]);
+      }
     }
   }
 }
@@ -292,9 +309,14 @@ struct Across {  // B(k, n) = X[n][k]
 };
 
 // c += A(m.., k0 ..k1) B(k0 ..k1, n..), a 16 x 8 N tile, of TA and TB terms: the
-// products of terms i and j with i + j < kLimit.
+// products of terms i and j with i + j < kLimit.  The tensor cores cut each sum of an
+// instruction off at the accumulator's last bit: where 24 bits are to be kept, the
+// small terms' products have an accumulator of their own, so that the large ones' is
+// cut once for every 16 of k and not six times (1.8e-6 against 4e-7 of the result).
 template <int TA, int TB, int kLimit, int N, class A, class B>
 __device__ __forceinline__ void product(float (&c)[N][4], const A& a, const B& b, int m, int n, int k0, int k1) {
+  constexpr bool kApart = kLimit > 2;
+  float small[kApart ? N : 1][4] = {};
 #pragma unroll 2
   for (int k = k0; k < k1; k += 16) {
     uint32_t fa[TA][4];
@@ -308,9 +330,99 @@ __device__ __forceinline__ void product(float (&c)[N][4], const A& a, const B& b
       for (int i = 0; i < TA; ++i)
         if (i + j < kLimit) {
 #pragma unroll
-          for (int t = 0; t < N; ++t) mma(c[t], fa[i], fb[t][0], fb[t][1]);
+          for (int t = 0; t < N; ++t) mma(kApart && i + j > 0 ? small[kApart ? t : 0] : c[t], fa[i], fb[t][0], fb[t][1]);
         }
     }
+  }
+  if constexpr (kApart) {
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[t][j] += small[t][j];
+  }
+}
+
+// 16 x 16 pieces of a triangle as an operand B(k, n)
+struct TriAcross {  // B(k, n) = X[n][k]
+  uint32_t base;
+  __device__ __forceinline__ void get(uint32_t (&r)[2][2], int kb, int nb, int t) const {
+    const int l = lane_id();
+    uint32_t w[4];
+    ld4(w, base + t * kTerm + (nb * (nb + 1) / 2 + kb) * 512 + tri_at((l & 7) + (l >> 4) * 8, (l >> 3) & 1));
+    r[0][0] = w[0]; r[0][1] = w[1]; r[1][0] = w[2]; r[1][1] = w[3];
+  }
+};
+struct TriDown {  // B(k, n) = X[k][n]
+  uint32_t base;
+  __device__ __forceinline__ void get(uint32_t (&r)[2][2], int kb, int nb, int t) const {
+    const int l = lane_id();
+    uint32_t w[4];
+    ld4t(w, base + t * kTerm + (kb * (kb + 1) / 2 + nb) * 512 + tri_at(l & 15, l >> 4));
+    r[0][0] = w[0]; r[0][1] = w[1]; r[1][0] = w[2]; r[1][1] = w[3];
+  }
+};
+
+// Two neighbouring 16 x 8 accumulators as an operand A, 16 x 16, of N terms: the
+// places of the one are those of the other, so nothing goes through shared memory.
+template <int N>
+__device__ __forceinline__ void as_operand(uint32_t (&f)[N][4], const float (&lo)[4], const float (&hi)[4]) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    float x0 = p < 2 ? lo[2 * p] : hi[2 * p - 4], x1 = p < 2 ? lo[2 * p + 1] : hi[2 * p - 3];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      f[n][p] = pack(x0, x1);
+      x0 -= lo_of(f[n][p]);
+      x1 -= hi_of(f[n][p]);
+    }
+  }
+}
+// c += A B over 16 of k and two tiles of 8 columns; the small terms' products go to s
+// where 24 bits are to be kept (see `product`).
+template <int TA, int TB, int kLimit>
+__device__ __forceinline__ void pair_product(float (&c0)[4], float (&c1)[4], float (&s0)[4], float (&s1)[4],
+                                             const uint32_t (&a)[TA][4], const uint32_t (&b)[TB][2][2]) {
+#pragma unroll
+  for (int j = 0; j < TB; ++j)
+#pragma unroll
+    for (int i = 0; i < TA; ++i)
+      if (i + j < kLimit) {
+        const bool apart = kLimit > 2 && i + j > 0;
+        mma(apart ? s0 : c0, a[i], b[j][0][0], b[j][0][1]);
+        mma(apart ? s1 : c1, a[i], b[j][1][0], b[j][1][1]);
+      }
+}
+// An 8 x 8 matrix of 16-bit values, a row's pair a lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// States that are kept for the backward pass lie [dv][dk]: fp32, or for inputs of type
+// bf16 two terms, one behind the other, which take the same room and are an operand as
+// they are.
+template <class E>
+__device__ __forceinline__ void save(float* base, size_t unit, size_t matrix, size_t at, float x) {
+  if constexpr (E::kBytes == 4) {
+    base[unit * matrix + at] = x;
+  } else {
+    uint16_t* to = reinterpret_cast<uint16_t*>(base) + unit * 2 * matrix + at;
+    const uint32_t w = pack(x, 0.f);
+    to[0] = static_cast<uint16_t>(w);
+    to[matrix] = static_cast<uint16_t>(pack(x - lo_of(w), 0.f));
+  }
+}
+// two neighbouring ones; `whole`: dk is even and base aligned to their size
+template <class E>
+__device__ __forceinline__ void save2(float* base, size_t unit, size_t matrix, size_t at, float x0, float x1) {
+  if constexpr (E::kBytes == 4) {
+    *reinterpret_cast<float2*>(base + unit * matrix + at) = make_float2(x0, x1);
+  } else {
+    uint32_t* to = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(base) + unit * 2 * matrix + at);
+    const uint32_t w = pack(x0, x1);
+    to[0] = w;
+    to[matrix / 2] = pack(x0 - lo_of(w), x1 - hi_of(w));
   }
 }
 
@@ -323,20 +435,113 @@ __device__ __forceinline__ void clear(float (&c)[N][4]) {
 }
 
 // The chunk's triangles and gates, 16 bytes a copy.  kP: terms of P.
-template <int kP>
+template <int kP, int kT = kThreads>
 __device__ __forceinline__ void load_tri(uint32_t m, uint32_t p, const unsigned char* from) {
-  for (int i = threadIdx.x; i < kStateTerms * kTerm / 16; i += kThreads) copy16(m + i * 16, from + i * 16, true);
-  for (int i = threadIdx.x; i < kP * kTerm / 16; i += kThreads)
-    copy16(p + i * 16, from + kStateTerms * kTerm + i * 16, true);
+  for (int i = threadIdx.x; i < kStateTerms * kTerm / 16; i += kT) copy16(m + i * 16, from + i * 16, true);
+  for (int i = threadIdx.x; i < kP * kTerm / 16; i += kT) copy16(p + i * 16, from + kStateTerms * kTerm + i * 16, true);
 }
+template <int kT = kThreads>
 __device__ __forceinline__ void load_gates(uint32_t to, const Gates* from) {
-  for (int i = threadIdx.x; i < static_cast<int>(sizeof(Gates)) / 16; i += kThreads)
+  for (int i = threadIdx.x; i < static_cast<int>(sizeof(Gates)) / 16; i += kT)
     copy16(to + i * 16, reinterpret_cast<const unsigned char*>(from) + i * 16, true);
 }
 
 template <class E>
 __device__ __forceinline__ size_t unit_of(const Args<E>& a, int chunk, int head) {
   return static_cast<size_t>(chunk) * a.heads + head;
+}
+
+// The outputs (y, or the values' gradient) of a sequence without a slot, and the states
+// that it would have left for the backward pass.
+template <class E>
+__device__ __forceinline__ void padding_zeros(const Args<E>& a, int lo, int hi, int c0, int n, int h, int v0, int cols, int threads) {
+  auto* out = a.y != nullptr ? a.y : a.dv_out;
+  const int64_t stride = a.y != nullptr ? a.y_stride : a.dv_stride;
+  for (int64_t i = threadIdx.x; i < static_cast<int64_t>(hi - lo) * cols; i += threads)
+    E::store(out + (lo + i / cols) * stride + h * a.dv + v0 + i % cols, 0.f);
+  if (a.y == nullptr || a.carry == nullptr) return;
+  const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
+  for (int c = 0; c < n; ++c)
+    for (int i = threadIdx.x; i < a.dk * cols; i += threads)
+      save<E>(a.carry, unit_of(a, c0 + c, h), matrix, static_cast<size_t>(v0) * a.dk + i, 0.f);
+}
+
+// A warp's columns vw .. vw + 15 of a state, held transposed, for the backward pass.
+template <class E, int KD>
+__device__ __forceinline__ void save_state(const Args<E>& a, float* base, size_t unit, const float (&S)[KD / 8][4], int vw,
+                                           bool even) {
+  const int lane = lane_id(), g = lane >> 2, t2 = (lane & 3) * 2;
+  const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
+#pragma unroll
+  for (int t = 0; t < KD / 8; ++t)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int v = vw + g + j * 8, k = t * 8 + t2;
+      if (v >= a.dv || k >= a.dk) continue;
+      const size_t at = static_cast<size_t>(v) * a.dk + k;
+      if (even) {
+        save2<E>(base, unit, matrix, at, S[t][2 * j], S[t][2 * j + 1]);
+      } else {
+        save<E>(base, unit, matrix, at, S[t][2 * j]);
+        if (k + 1 < a.dk) save<E>(base, unit, matrix, at + 1, S[t][2 * j + 1]);
+      }
+    }
+}
+
+// A chunk's rows of a warp's 16 columns, held transposed; masked rows (beta 0) get
+// zeros.  `to` is the first row's column 0 of the head.
+template <class E>
+__device__ __forceinline__ void store_rows(typename E::T* to, int64_t stride, int len, int vw, int dv, bool pairs,
+                                           const float (&beta)[kC], const float (&y)[kC / 8][4]) {
+  const int lane = lane_id(), g = lane >> 2, t2 = (lane & 3) * 2;
+#pragma unroll
+  for (int t = 0; t < kC / 8; ++t)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (E::kBytes == 2) {
+        const uint32_t w = transposed(pack(y[t][2 * j], y[t][2 * j + 1]));  // row t * 8 + g, columns t2, t2 + 1
+        const int r = t * 8 + g, v = vw + j * 8 + t2;
+        if (r >= len) continue;
+        const uint32_t x = beta[r] != 0.f ? w : 0u;
+        typename E::T* at = to + r * stride + v;
+        if (pairs) {
+          if (v < dv) *reinterpret_cast<uint32_t*>(at) = x;
+        } else {
+          if (v < dv) at[0] = static_cast<uint16_t>(x);
+          if (v + 1 < dv) at[1] = static_cast<uint16_t>(x >> 16);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = t * 8 + t2 + e, v = vw + j * 8 + g;
+          if (r < len && v < dv) E::store(to + r * stride + v, beta[r] != 0.f ? y[t][2 * j + e] : 0.f);
+        }
+      }
+    }
+}
+
+// S^T <- total S^T + A X, A of a chunk's 64 positions in three terms, X its rows of keys
+// or queries.  The sum is made apart and added once: S's last bit cuts it off once.
+template <class E, int KD>
+__device__ __forceinline__ void add_outer(float (&S)[KD / 8][4], float total, const uint32_t (&fa)[kC / 16][kStateTerms][4],
+                                          const Mat& X) {
+#pragma unroll
+  for (int kb = 0; kb < KD / 16; ++kb) {
+    float c[2][4], s[2][4];
+    clear(c);
+    clear(s);
+#pragma unroll
+    for (int cb = 0; cb < kC / 16; ++cb) {
+      uint32_t fb[kIn<E>][2][2];
+#pragma unroll
+      for (int j = 0; j < kIn<E>; ++j) Down{X}.get<2>(fb[j], cb * 16, kb * 16, j);
+      pair_product<kStateTerms, kIn<E>, kStateTerms>(c[0], c[1], s[0], s[1], fa[cb], fb);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) S[2 * kb + e][j] = fmaf(S[2 * kb + e][j], total, c[e][j] + s[e][j]);
+  }
 }
 
 // ------------------------------------------------------------ host: launches
@@ -346,7 +551,9 @@ struct Space {
   int32_t* first;
   unsigned char* tri;
   Gates* gates;
-  float *after, *writes, *shared;
+  float* after;
+  uint16_t* writes;
+  float* shared;
   size_t bytes;
 };
 inline int64_t max_chunks(int64_t n_tokens, int64_t n_seqs) {
@@ -367,6 +574,13 @@ inline int opt_in(const void* kernel, int smem, std::atomic<uint64_t>& done) {
   if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
   done.fetch_or(bit, std::memory_order_relaxed);
   return ENGRAM_OK;
+}
+
+// Whether a warp follows a sequence in a head (scan_rows_kernel, back_rows_kernel) or a
+// block does.  (fp32's operands of three terms each leave a warp no registers.)
+template <class E>
+bool by_warps(const Args<E>& a, int sms) {
+  return E::kBytes == 2 && static_cast<int64_t>(a.n_seqs) * a.heads * 2 >= sms;
 }
 
 inline bool pieces(const void* p, int64_t stride, int bytes) { return aligned(p, 16) && stride * bytes % 16 == 0; }

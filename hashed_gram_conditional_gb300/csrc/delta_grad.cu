@@ -48,9 +48,8 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(Args<E> a) {
   int64_t slot;
   const bool live = live_slot(a, seq, slot);
   if (!live && tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
-  if (!live) {  // padding: zeros
-    for (int64_t i = tid; i < static_cast<int64_t>(hi - lo) * cols; i += kThreads)
-      E::store(a.dv_out + (lo + i / cols) * a.dv_stride + h * a.dv + v0 + i % cols, 0.f);
+  if (!live) {
+    padding_zeros(a, lo, hi, c0, n, h, v0, cols, kThreads);
     return;
   }
   const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
@@ -102,8 +101,14 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(Args<E> a) {
     __syncthreads();  // the chunk and dS are here, and the other stage is free
     if (L::kStages == 2 && i > 0) load(i - 1);
     {
-      float* to = a.after + unit_of(a, c0 + i, h) * matrix;
-      each([&](int t, int j, size_t at) { to[at] = S[t][j]; });
+      const size_t unit = unit_of(a, c0 + i, h);
+#pragma unroll
+      for (int t = 0; t < L::kSN; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = sm + g + (j >> 1) * 8, c = sn + t * 8 + t2 + (j & 1);
+          if (r < a.dk && c < cols) save<E>(a.after, unit, matrix, static_cast<size_t>(v0 + c) * a.dk + r, S[t][j]);
+        }
     }
     float x[L::kN][4], u[L::kN][4];
     clear(x);
@@ -140,8 +145,10 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(Args<E> a) {
         for (int e = 0; e < 2; ++e) {
           if (c + e >= cols) continue;
           const float d = on ? u[t][2 * j + e] : 0.f;
-          E::store(a.dv_out + (p + r) * a.dv_stride + h * a.dv + v0 + c + e, d);
-          a.writes[((p + r) * a.heads + h) * a.dv + v0 + c + e] = d;
+          auto* to = a.dv_out + (p + r) * a.dv_stride + h * a.dv + v0 + c + e;
+          E::store(to, d);
+          if constexpr (E::kBytes == 2)  // what the rounding has left
+            a.writes[((p + r) * a.heads + h) * a.dv + v0 + c + e] = static_cast<uint16_t>(pack(d - E::load(to), 0.f));
         }
       }
     __syncthreads();
@@ -164,45 +171,283 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(Args<E> a) {
   }
 }
 
+// A warp follows one sequence in one head backwards, for 16 of the value columns, with
+// dS^T in its registers, as scan_rows_kernel does forwards.
+template <class E, int KD, int W>
+struct BackRows {
+  static constexpr int kStages = 2;
+  static constexpr int kK = 0, kQ = kK + kIn<E> * mat_bytes(kC, KD), kY = kQ + kIn<E> * mat_bytes(kC, KD);
+  static constexpr int kM = kY + kIn<E> * mat_bytes(kC, 16 * W), kP = kM + kStateTerms * kTerm, kG = kP + kStateTerms * kTerm;
+  static constexpr int kStage = kG + static_cast<int>(sizeof(Gates));
+  static constexpr int kSmem = kStages * kStage;
+};
+
+template <class E, int KD, int W>
+__global__ void __launch_bounds__(W * 32, 1) back_rows_kernel(Args<E> a) {
+  using L = BackRows<E, KD, W>;
+  constexpr int kT = W * 32, kI = kIn<E>, kS = kStateTerms, kB = kC / 16;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
+  const int seq = blockIdx.x, h = blockIdx.y, v0 = blockIdx.z * (16 * W), cols = min(a.dv - v0, 16 * W);
+  const int hk = h / (a.heads / a.keys), vw = v0 + warp * 16;
+  int lo, hi;
+  bounds(a, seq, lo, hi);
+  const int c0 = a.first[seq], n = min((hi - lo + kC - 1) / kC, a.max_chunks - c0);
+  const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
+  int64_t slot;
+  if (!live_slot(a, seq, slot)) {
+    if (tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
+    padding_zeros(a, lo, hi, c0, n, h, v0, cols, kT);
+    return;
+  }
+  float S[KD / 8][4];
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int t = 0; t < KD / 8; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int v = vw + g + (j >> 1) * 8, k = t * 8 + t2 + (j & 1);
+        if (v < a.dv && k < a.dk) f(t, j, static_cast<size_t>(k) * a.dv + v);
+      }
+  };
+  clear(S);
+  if (a.state_out != nullptr) {
+    const float* from = a.state_out + (slot * a.heads + h) * matrix;
+    each([&](int t, int j, size_t at) { S[t][j] = from[at]; });
+  }
+  auto load = [&](int i) {
+    const uint32_t stage = base + (i % L::kStages) * L::kStage;
+    const int64_t p = lo + static_cast<int64_t>(i) * kC;
+    const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
+    const uint8_t* mask = a.mask != nullptr ? a.mask + p : nullptr;
+    const size_t unit = unit_of(a, c0 + i, h);
+    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kK), a.k + p * a.k_stride + hk * a.dk, a.k_stride, len, a.dk, mask, a.vec);
+    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kQ), a.q + p * a.q_stride + hk * a.dk, a.q_stride, len, a.dk, mask, a.vec);
+    load_rows<E, 16 * W, kT>(mat<kC, 16 * W>(stage + L::kY), a.dy + p * a.dy_stride + h * a.dv + v0, a.dy_stride, len, cols,
+                             mask, a.vec);
+    load_tri<kS, kT>(stage + L::kM, stage + L::kP, a.tri + unit * kTriBytes);
+    load_gates<kT>(stage + L::kG, a.gates + unit);
+    copies_begun();
+  };
+  if (n > 0) load(n - 1);
+  const bool even = a.dk % 2 == 0;  // (the workspace is aligned)
+  for (int i = n - 1; i >= 0; --i) {
+    const uint32_t stage = base + (i % L::kStages) * L::kStage;
+    const Mat K = mat<kC, KD>(stage + L::kK), Q = mat<kC, KD>(stage + L::kQ), Y = mat<kC, 16 * W>(stage + L::kY);
+    const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
+    copies_done();
+    __syncthreads();  // the chunk is here, and the other stage is free
+    if (i > 0) load(i - 1);
+    save_state<E, KD>(a, a.after, unit_of(a, c0 + i, h), S, vw, even);
+    // ---- dU^T = e^(c_last - c) (K dS)^T + dY^T P
+    float u[kC / 8][4], s[kC / 8][4];
+    clear(u);
+    clear(s);
+#pragma unroll
+    for (int kb = 0; kb < KD / 16; ++kb) {
+      uint32_t fa[kS][4];
+      as_operand<kS>(fa, S[2 * kb], S[2 * kb + 1]);
+#pragma unroll
+      for (int cb = 0; cb < kB; ++cb) {
+        uint32_t fb[kI][2][2];
+#pragma unroll
+        for (int j = 0; j < kI; ++j) Across{K}.get<2>(fb[j], kb * 16, cb * 16, j);
+        pair_product<kS, kI, kS>(u[2 * cb], u[2 * cb + 1], s[2 * cb], s[2 * cb + 1], fa, fb);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kC / 8; ++t) {
+      const float2 last = *reinterpret_cast<const float2*>(&gt.last[t * 8 + t2]);
+      u[t][0] = (u[t][0] + s[t][0]) * last.x;
+      u[t][1] = (u[t][1] + s[t][1]) * last.y;
+      u[t][2] = (u[t][2] + s[t][2]) * last.x;
+      u[t][3] = (u[t][3] + s[t][3]) * last.y;
+    }
+    clear(s);
+#pragma unroll
+    for (int tb = 0; tb < kB; ++tb) {
+      uint32_t fa[kI][4];
+#pragma unroll
+      for (int j = 0; j < kI; ++j) Cols{Y}(fa[j], warp * 16, tb * 16, j);
+#pragma unroll
+      for (int ib = 0; ib <= tb; ++ib) {
+        uint32_t fb[kS][2][2];
+#pragma unroll
+        for (int j = 0; j < kS; ++j) TriDown{stage + L::kP}.get(fb[j], tb, ib, j);
+        pair_product<kI, kS, kS>(u[2 * ib], u[2 * ib + 1], s[2 * ib], s[2 * ib + 1], fa, fb);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kC / 8; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[t][j] += s[t][j];
+    // ---- dV^T = dU^T M
+    float w[kC / 8][4];
+    clear(w);
+    clear(s);
+#pragma unroll
+    for (int tb = 0; tb < kB; ++tb) {
+      uint32_t fa[kS][4];
+      as_operand<kS>(fa, u[2 * tb], u[2 * tb + 1]);
+#pragma unroll
+      for (int ib = 0; ib <= tb; ++ib) {
+        uint32_t fb[kS][2][2];
+#pragma unroll
+        for (int j = 0; j < kS; ++j) TriDown{stage + L::kM}.get(fb[j], tb, ib, j);
+        pair_product<kS, kS, kS>(w[2 * ib], w[2 * ib + 1], s[2 * ib], s[2 * ib + 1], fa, fb);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kC / 8; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[t][j] += s[t][j];
+        s[t][j] = w[t][j] - lo_of(pack(w[t][j], 0.f));  // what the output's rounding leaves
+      }
+    const int64_t p = lo + static_cast<int64_t>(i) * kC;
+    const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
+    store_rows<E>(a.dv_out + p * a.dv_stride + h * a.dv, a.dv_stride, len, vw, a.dv, a.pairs, gt.beta, w);
+    store_rows<E>(a.writes + (p * a.heads + h) * a.dv, static_cast<int64_t>(a.heads) * a.dv, len, vw, a.dv, a.dv % 2 == 0,
+                  gt.beta, s);
+    // ---- dS^T
+    uint32_t fa[kB][kS][4];
+#pragma unroll
+    for (int cb = 0; cb < kB; ++cb) {
+      float r[2][4];
+      clear(r);
+#pragma unroll
+      for (int j = kI - 1; j >= 0; --j) {
+        uint32_t f[4];
+        Cols{Y}(f, warp * 16, cb * 16, j);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          r[q >> 1][(q & 1) * 2] += lo_of(f[q]);
+          r[q >> 1][(q & 1) * 2 + 1] += hi_of(f[q]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 into = *reinterpret_cast<const float2*>(&gt.into[cb * 16 + e * 8 + t2]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x = j & 1 ? into.y : into.x;
+          r[e][j] *= a.scale * x;
+          w[2 * cb + e][j] *= -x;
+        }
+      }
+      as_operand<kS>(fa[cb], r[0], r[1]);
+    }
+    add_outer<E, KD>(S, gt.into[kC - 1], fa, Q);
+#pragma unroll
+    for (int cb = 0; cb < kB; ++cb) as_operand<kS>(fa[cb], w[2 * cb], w[2 * cb + 1]);
+    add_outer<E, KD>(S, 1.f, fa, K);
+  }
+  if (a.state_out != nullptr) {
+    float* to = a.state_out + (slot * a.heads + h) * matrix;
+    each([&](int t, int j, size_t at) { to[at] = S[t][j]; });
+  }
+}
+
 // ------------------------------------------------------- all chunks' gradients
 
+// A block has one chunk and the heads of one key head, one after another, and a head's
+// value columns in slices of VS.  The next slice's inputs are copied while this one is
+// used (bf16: all of them are operands as they lie in memory; fp32 are made terms on
+// the way).
 template <class E, int KD, int VS>
 struct Grads {
-  static constexpr int kO = kOut<E>;
-  static constexpr int kQ = 0, kK = kQ + kIn<E> * mat_bytes(kC, KD), kM = kK + kIn<E> * mat_bytes(kC, KD);
-  static constexpr int kG = kM + kO * kTerm, kNum = kG + static_cast<int>(sizeof(Gates));  // kNum: the chunk's sums
-  static constexpr int kSums = 2 * kC * 4 + 4 * kC + kWarps;  // floats
-  static constexpr int kSlice = (kNum + kSums * 4 + 127) / 128 * 128;
-  // a slice of the value columns: S, dS, V then V - e^c K S, U, dY, dV
-  static constexpr int kS = kSlice, kD = kS + kO * mat_bytes(KD, VS), kX = kD + kO * mat_bytes(KD, VS);
-  static constexpr int kU = kX + kO * mat_bytes(kC, VS), kY = kU + kO * mat_bytes(kC, VS), kW = kY + kIn<E> * mat_bytes(kC, VS);
-  static constexpr int kEnd = kW + kO * mat_bytes(kC, VS);
-  // in its place afterwards: F, E
-  static constexpr int kF = kSlice, kE = kF + kO * mat_bytes(kC, kC), kEnd2 = kE + kO * mat_bytes(kC, kC);
+  static constexpr int kO = kOut<E>, kStages = E::kBytes == 2 ? 2 : 1;
+  static constexpr int kK = 0, kQ = kK + kIn<E> * mat_bytes(kC, KD);
+  static constexpr int kHead = kQ + kIn<E> * mat_bytes(kC, KD);  // M and the gates, of this head and the next
+  static constexpr int kHeadBytes = kO * kTerm + static_cast<int>(sizeof(Gates));
+  static constexpr int kNum = kHead + kStages * kHeadBytes;    // sums
+  static constexpr int kSums = 2 * kC * 4 + 4 * kC + kWarps;   // floats
+  static constexpr int kF = (kNum + kSums * 4 + 127) / 128 * 128, kE = kF + kO * mat_bytes(kC, kC);
+  static constexpr int kU = E::kBytes == 2 ? kE + kO * mat_bytes(kC, kC) : kF;
+  static constexpr int kSlice = kU + kO * mat_bytes(kC, VS);
+  // a slice of the value columns: S^T, dS^T, V then V - e^c K S, dY, dV
+  static constexpr int kS = 0, kD = kS + kO * mat_bytes(VS, KD), kX = kD + kO * mat_bytes(VS, KD);
+  static constexpr int kY = kX + kO * mat_bytes(kC, VS), kW = kY + kIn<E> * mat_bytes(kC, VS);
+  static constexpr int kSliceBytes = kW + kO * mat_bytes(kC, VS);
+  // (fp32: F and E lie over U and the slice)
+  static constexpr int kEnd = kSlice + kStages * kSliceBytes, kEnd2 = kE + kO * mat_bytes(kC, kC);
   static constexpr int kSmem = kEnd > kEnd2 ? kEnd : kEnd2;
   static constexpr int kN = VS / 16, kKN = KD / 16;  // a warp's tiles of a slice's, and of a key's columns
 };
 
-// dk rows of a state's columns v0 .. v0 + cols as terms, zeros around them; returns
-// what `sum` says of the thread's values.
+// `rows` rows of a saved state, from row v0 on, as terms, zeros around them.
 template <class E, int KD, int VS>
-__device__ __forceinline__ void load_state(const Mat& m, const float* from, int dk, int dv, int cols) {
-  const bool two = dv % 2 == 0 && (reinterpret_cast<uintptr_t>(from) & 7) == 0;
-  for (int i = threadIdx.x; i < KD * (VS / 2); i += kThreads) {
-    const int r = i / (VS / 2), c = i % (VS / 2) * 2;
-    float x0 = 0.f, x1 = 0.f;
-    if (r < dk && c < cols) {
-      const float* p = from + static_cast<size_t>(r) * dv + c;
-      if (two) {
-        const float2 x = *reinterpret_cast<const float2*>(p);
-        x0 = x.x;
-        x1 = x.y;
-      } else {
-        x0 = p[0];
-        x1 = c + 1 < cols ? p[1] : 0.f;
+__device__ __forceinline__ void load_state(const Mat& m, const float* base, size_t unit, size_t matrix, int v0, int rows, int dk,
+                                           bool vec) {
+  if constexpr (E::kBytes == 2) {
+    const uint16_t* from = reinterpret_cast<const uint16_t*>(base) + unit * 2 * matrix + static_cast<size_t>(v0) * dk;
+    if (vec) {
+#pragma unroll
+      for (int i0 = 0; i0 < 2 * VS * (KD / 8); i0 += kThreads) {
+        const int i = i0 + threadIdx.x, n = i / (VS * (KD / 8)), r = i / (KD / 8) % VS, c = i % (KD / 8) * 8;
+        const bool on = r < rows && c < dk;
+        copy16(m.base + n * m.term + r * m.pitch + c * 2, on ? from + n * matrix + static_cast<size_t>(r) * dk + c : from, on);
+      }
+    } else {
+      for (int i = threadIdx.x; i < 2 * VS * (KD / 2); i += kThreads) {
+        const int n = i / (VS * (KD / 2)), r = i / (KD / 2) % VS, c = i % (KD / 2) * 2;
+        const uint16_t* p = from + n * matrix + static_cast<size_t>(r) * dk + c;
+        const uint32_t x0 = r < rows && c < dk ? p[0] : 0u, x1 = r < rows && c + 1 < dk ? p[1] : 0u;
+        st32(m.base + n * m.term + r * m.pitch + c * 2, x0 | x1 << 16);
       }
     }
-    put<kOut<E>>(m.base + r * m.pitch + c * 2, m.term, x0, x1);
+  } else {
+    const float* from = base + unit * matrix + static_cast<size_t>(v0) * dk;
+    constexpr int kAhead = 4;
+    for (int i0 = threadIdx.x; i0 < VS * (KD / 2); i0 += kAhead * kThreads) {
+      float x[kAhead][2];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kThreads, r = i / (KD / 2), c = i % (KD / 2) * 2;
+        const float* p = from + static_cast<size_t>(r) * dk + c;
+        x[u][0] = r < rows && c < dk ? p[0] : 0.f;
+        x[u][1] = r < rows && c + 1 < dk ? p[1] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kThreads, r = i / (KD / 2), c = i % (KD / 2) * 2;
+        if (r < VS) put<kOut<E>>(m.base + r * m.pitch + c * 2, m.term, x[u][0], x[u][1]);
+      }
+    }
+  }
+}
+
+// c += A B and d += A2 B, of TA and TB (A2: TB) terms, over k from 0 to k1
+template <int TA, int TB, int N, class A, class A2, class B>
+__device__ __forceinline__ void both_products(float (&c)[N][4], float (&d)[N][4], const A& a, const A2& a2, const B& b, int m,
+                                              int n, int k1) {
+  if constexpr (TA == TB) {
+    product<TA, TB, TB>(c, a, b, m, n, 0, k1);
+    product<TB, TB, TB>(d, a2, b, m, n, 0, k1);
+  } else {
+#pragma unroll
+    for (int k = 0; k < k1; k += 16) {
+      uint32_t fa[TA][4], fd[TB][4];
+#pragma unroll
+      for (int i = 0; i < TA; ++i) a(fa[i], m, k, i);
+#pragma unroll
+      for (int i = 0; i < TB; ++i) a2(fd[i], m, k, i);
+#pragma unroll
+      for (int j = 0; j < TB; ++j) {
+        uint32_t fb[N][2];
+        b.template get<N>(fb, k, n, j);
+#pragma unroll
+        for (int i = 0; i < TB; ++i)
+          if (i + j < TB) {
+#pragma unroll
+            for (int t = 0; t < N; ++t) {
+              if (i < TA) mma(c[t], fa[i < TA ? i : 0], fb[t][0], fb[t][1]);
+              mma(d[t], fd[i], fb[t][0], fb[t][1]);
+            }
+          }
+      }
+    }
   }
 }
 
@@ -239,18 +484,38 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
   }
   const uint8_t* mask = a.mask != nullptr ? a.mask + p : nullptr;
   const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
-  const Mat K = mat<kC, KD>(base + L::kK), Q = mat<kC, KD>(base + L::kQ);
-  const Mat S = mat<KD, VS>(base + L::kS), D = mat<KD, VS>(base + L::kD);
-  const Mat X = mat<kC, VS>(base + L::kX), U = mat<kC, VS>(base + L::kU), Y = mat<kC, VS>(base + L::kY),
-            W = mat<kC, VS>(base + L::kW);
+  const Mat K = mat<kC, KD>(base + L::kK), Q = mat<kC, KD>(base + L::kQ), U = mat<kC, VS>(base + L::kU);
   const Mat Fm = mat<kC, kC>(base + L::kF), Em = mat<kC, kC>(base + L::kE);
-  const Gates& gt = *reinterpret_cast<const Gates*>(smem + L::kG);
   float* sums = reinterpret_cast<float*>(smem + L::kNum);
   float *reads = sums, *writes = reads + 2 * kC, *rows = writes + 2 * kC, *own = rows + 2 * kC, *columns = own + 2 * kC,
         *wholes = columns + 4 * kC;
+  const int slices = (a.dv + VS - 1) / VS, steps = group * slices;
+  auto load = [&](int step) {  // of a head's slice, and with the first one M and the gates
+    const int h = hk * group + step / slices, v0 = step % slices * VS, cols = a.dv - v0 < VS ? a.dv - v0 : VS;
+    const size_t unit = unit_of(a, blockIdx.x, h);
+    const uint32_t at = base + L::kSlice + (step % L::kStages) * L::kSliceBytes;
+    const int64_t column = static_cast<int64_t>(h) * a.dv + v0;
+    if (v0 == 0) {
+      const uint32_t to = base + L::kHead + (h % L::kStages) * L::kHeadBytes;
+      for (int i = tid; i < kO * kTerm / 16; i += kThreads) copy16(to + i * 16, a.tri + unit * kTriBytes + i * 16, true);
+      load_gates(to + kO * kTerm, a.gates + unit);
+    }
+    load_rows<E, VS>(mat<kC, VS>(at + L::kX), a.v + p * a.v_stride + column, a.v_stride, ch.len, cols, mask, a.vec);
+    load_rows<E, VS>(mat<kC, VS>(at + L::kY), a.dy + p * a.dy_stride + column, a.dy_stride, ch.len, cols, mask, a.vec);
+    const Mat W = mat<kC, VS>(at + L::kW);
+    load_rows<E, VS>(W, a.dv_out + p * a.dv_stride + column, a.dv_stride, ch.len, cols, nullptr, a.vec);
+    if constexpr (E::kBytes == 2) {
+      const int64_t wide = static_cast<int64_t>(a.heads) * a.dv;
+      load_rows<E, VS>(Mat{W.base + static_cast<uint32_t>(W.term), W.pitch, W.term}, a.writes + p * wide + column, wide, ch.len,
+                       cols, nullptr, a.vec);
+    }
+    load_state<E, KD, VS>(mat<VS, KD>(at + L::kS), a.carry, unit, matrix, v0, cols, a.dk, a.vec);
+    load_state<E, KD, VS>(mat<VS, KD>(at + L::kD), a.after, unit, matrix, v0, cols, a.dk, a.vec);
+    copies_begun();
+  };
   load_rows<E, KD>(K, a.k + p * a.k_stride + hk * a.dk, a.k_stride, ch.len, a.dk, mask, a.vec);
   load_rows<E, KD>(Q, a.q + p * a.q_stride + hk * a.dk, a.q_stride, ch.len, a.dk, mask, a.vec);
-  copies_begun();
+  load(0);
   copies_done();
   __syncthreads();
   // a warp's tiles: 16 rows, and half of the columns
@@ -264,7 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
     product<kIn<E>, kIn<E>, kIn<E>>(kk, Rows{K}, Across{K}, m, nc, 0, KD);
   }
   for (int h = hk * group; h < (hk + 1) * group; ++h) {
-    const size_t unit = unit_of(a, blockIdx.x, h);
+    const Gates& gt = *reinterpret_cast<const Gates*>(smem + L::kHead + (h % L::kStages) * L::kHeadBytes + kO * kTerm);
+    const uint32_t M = base + L::kHead + (h % L::kStages) * L::kHeadBytes;
     float cf[4][4], ce[4][4], cq[L::kKN][4], ck[L::kKN][4], cw[L::kKN][4];
     float dot[2] = {0.f, 0.f}, whole = 0.f;
     clear(cf);
@@ -272,29 +538,21 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
     clear(cq);
     clear(ck);
     clear(cw);
-    __syncthreads();  // the head before has been written
-    for (int i = tid; i < kO * kTerm / 16; i += kThreads)
-      copy16(base + L::kM + i * 16, a.tri + unit * kTriBytes + i * 16, true);
-    load_gates(base + L::kG, a.gates + unit);
-    for (int v0 = 0; v0 < a.dv; v0 += VS) {
-      const int cols = a.dv - v0 < VS ? a.dv - v0 : VS;
-      if (v0 > 0) __syncthreads();  // the slice before has been used
-      const int64_t column = static_cast<int64_t>(h) * a.dv + v0;
-      load_rows<E, VS>(X, a.v + p * a.v_stride + column, a.v_stride, ch.len, cols, mask, a.vec);
-      load_rows<E, VS>(Y, a.dy + p * a.dy_stride + column, a.dy_stride, ch.len, cols, mask, a.vec);
-      copies_begun();
-      load_state<E, KD, VS>(S, a.carry + unit * matrix + v0, a.dk, a.dv, cols);
-      load_state<E, KD, VS>(D, a.after + unit * matrix + v0, a.dk, a.dv, cols);
-      for (int i = tid; i < kC * (VS / 2); i += kThreads) {
-        const int r = i / (VS / 2), c = i % (VS / 2) * 2;
-        const float* from = a.writes + (p + r) * a.heads * a.dv + column + c;
-        const bool on = r < ch.len;
-        put<kO>(W.base + r * W.pitch + c * 2, W.term, on && c < cols ? from[0] : 0.f, on && c + 1 < cols ? from[1] : 0.f);
+    for (int sl = 0; sl < slices; ++sl) {
+      const int step = (h - hk * group) * slices + sl;
+      const uint32_t at = base + L::kSlice + (step % L::kStages) * L::kSliceBytes;
+      const Mat S = mat<VS, KD>(at + L::kS), D = mat<VS, KD>(at + L::kD);
+      const Mat X = mat<kC, VS>(at + L::kX), Y = mat<kC, VS>(at + L::kY), W = mat<kC, VS>(at + L::kW);
+      if (L::kStages == 1 && step > 0) {
+        __syncthreads();  // the slice before has been used
+        load(step);
       }
       copies_done();
-      __syncthreads();
-      for (int i = tid; i < KD * (VS / 2); i += kThreads) {
-        const int r = i / (VS / 2), c = i % (VS / 2) * 2;
+      __syncthreads();  // the slice is here, and the other stage is free
+      if (L::kStages == 2 && step + 1 < steps) load(step + 1);
+#pragma unroll
+      for (int i0 = 0; i0 < VS * (KD / 2); i0 += kThreads) {
+        const int i = i0 + tid, r = i / (KD / 2), c = i % (KD / 2) * 2;
         float s[2], d[2];
         get<kO>(S.base + r * S.pitch + c * 2, S.term, s[0], s[1]);
         get<kO>(D.base + r * D.pitch + c * 2, D.term, d[0], d[1]);
@@ -302,21 +560,23 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
       }
       float x[L::kN][4];
       clear(x);
-      product<kIn<E>, kO, kO>(x, Rows{K}, Down{S}, m, nn, 0, KD);
+      product<kIn<E>, kO, kO>(x, Rows{K}, Across{S}, m, nn, 0, KD);
 #pragma unroll
       for (int t = 0; t < L::kN; ++t)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int r = m + g + j * 8, c = nn + t * 8 + t2;
-          const uint32_t at = X.base + r * X.pitch + c * 2;
+          const uint32_t to = X.base + r * X.pitch + c * 2;
           float v[2];
-          get<kIn<E>>(at, X.term, v[0], v[1]);
+          get<kIn<E>>(to, X.term, v[0], v[1]);
           const float into = gt.into[r];
-          put<kO>(at, X.term, fmaf(-into, x[t][2 * j], v[0]), fmaf(-into, x[t][2 * j + 1], v[1]));
+          put<kO>(to, X.term, fmaf(-into, x[t][2 * j], v[0]), fmaf(-into, x[t][2 * j + 1], v[1]));
         }
+      // what reads S does not wait for U
+      both_products<kIn<E>, kO>(cq, ck, Rows{Y}, Rows{W}, Down{S}, m, nk, VS);
       __syncthreads();
       clear(x);
-      product<kO, kO, kO>(x, TriRows{base + L::kM}, Down{X}, m, nn, 0, m + 16);
+      product<kO, kO, kO>(x, TriRows{M}, Down{X}, m, nn, 0, m + 16);
 #pragma unroll
       for (int t = 0; t < L::kN; ++t)
 #pragma unroll
@@ -328,13 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
           dot[j] = fmaf(w[0], x[t][2 * j], fmaf(w[1], x[t][2 * j + 1], dot[j]));
         }
       __syncthreads();
-      if (low) {
-        product<kIn<E>, kO, kO>(cf, Rows{Y}, Across{U}, m, nc, 0, VS);
-        product<kO, kO, kO>(ce, Rows{W}, Across{U}, m, nc, 0, VS);
-      }
-      product<kIn<E>, kO, kO>(cq, Rows{Y}, Across{S}, m, nk, 0, VS);
-      product<kO, kO, kO>(ck, Rows{W}, Across{S}, m, nk, 0, VS);
-      product<kO, kO, kO>(cw, Rows{U}, Across{D}, m, nk, 0, VS);
+      if (low) both_products<kIn<E>, kO>(cf, ce, Rows{Y}, Rows{W}, Across{U}, m, nc, VS);
+      product<kO, kO, kO>(cw, Rows{U}, Down{D}, m, nk, 0, VS);
     }
     // ---- F and E, the pairs of reads and writes, and what reads S and reaches dS
     float row[2] = {0.f, 0.f};
@@ -474,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
 }
 
 template <class E>
-int launch_grad(const Args<E>& a, cudaStream_t st) {
+int launch_grad(const Args<E>& a, int sms, cudaStream_t st) {
   int rc = launch_prepare<E>(a, st);
   if (rc) return rc;
   static std::atomic<uint64_t> done[4] = {{0}, {0}, {0}, {0}};
@@ -484,20 +739,28 @@ int launch_grad(const Args<E>& a, cudaStream_t st) {
     kernel<<<grid, kThreads, smem, st>>>(a);
     return check_launch(name);
   };
-  constexpr int VB = 32, VG = E::kBytes == 2 ? 32 : 16;
+  constexpr int VB = 16, VG = E::kBytes == 2 ? 32 : 16;
   const dim3 back(a.n_seqs, a.heads, (a.dv + VB - 1) / VB), grads(a.max_chunks, a.keys);
-  if (a.dk <= 64) {
-    rc = go(back_kernel<E, 64, VB>, Back<E, 64, VB>::kSmem, back, done[0], "back_kernel");
-    return rc ? rc : go(grads_kernel<E, 64, VG>, Grads<E, 64, VG>::kSmem, grads, done[1], "grads_kernel");
+  bool rows = false;
+  if constexpr (E::kBytes == 2) {
+    rows = by_warps(a, sms);
+    if (rows) {
+      static std::atomic<uint64_t> flags[2] = {{0}, {0}};
+      const dim3 grid(a.n_seqs, a.heads, (a.dv + 127) / 128);
+      rc = a.dk <= 64 ? go(back_rows_kernel<E, 64, 8>, BackRows<E, 64, 8>::kSmem, grid, flags[0], "back_rows_kernel")
+                      : go(back_rows_kernel<E, 128, 8>, BackRows<E, 128, 8>::kSmem, grid, flags[1], "back_rows_kernel");
+    }
   }
-  constexpr int VB2 = E::kBytes == 2 ? 32 : 16;
-  const dim3 back2(a.n_seqs, a.heads, (a.dv + VB2 - 1) / VB2);
-  rc = go(back_kernel<E, 128, VB2>, Back<E, 128, VB2>::kSmem, back2, done[2], "back_kernel");
-  return rc ? rc : go(grads_kernel<E, 128, VG>, Grads<E, 128, VG>::kSmem, grads, done[3], "grads_kernel");
+  if (!rows)
+    rc = a.dk <= 64 ? go(back_kernel<E, 64, VB>, Back<E, 64, VB>::kSmem, back, done[0], "back_kernel")
+                    : go(back_kernel<E, 128, VB>, Back<E, 128, VB>::kSmem, back, done[1], "back_kernel");
+  if (rc) return rc;
+  return a.dk <= 64 ? go(grads_kernel<E, 64, VG>, Grads<E, 64, VG>::kSmem, grads, done[2], "grads_kernel")
+                    : go(grads_kernel<E, 128, VG>, Grads<E, 128, VG>::kSmem, grads, done[3], "grads_kernel");
 }
 
-static_assert(Back<train::Bf16, 128, 32>::kSmem <= 232448 && Back<train::F32, 128, 16>::kSmem <= 232448 &&
-                  Back<train::F32, 64, 32>::kSmem <= 232448 && Grads<train::Bf16, 128, 32>::kSmem <= 232448 &&
+static_assert(Back<train::Bf16, 128, 16>::kSmem <= 232448 && Back<train::F32, 128, 16>::kSmem <= 232448 &&
+                  BackRows<train::Bf16, 128, 8>::kSmem <= 232448 && Grads<train::Bf16, 128, 32>::kSmem <= 232448 &&
                   Grads<train::F32, 128, 16>::kSmem <= 232448,
               "a block's shared memory");
 
@@ -540,7 +803,8 @@ extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void
   if (!aligned(workspace_d, 256)) return fail(ENGRAM_E_ALIGN, "workspace must be 256-byte aligned");
   if (workspace_bytes < engram_delta_workspace_bytes(n_tokens, n_seqs, key_heads, heads, dk, dv, 1))
     return fail(ENGRAM_E_RANGE, "workspace too small");
-  if ((rc = check_device(nullptr))) return rc;
+  int sms = 0;
+  if ((rc = check_device(&sms))) return rc;
   auto go = [&](auto e) {
     using E = decltype(e);
     using T = typename E::T;
@@ -583,7 +847,9 @@ extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void
     a.dv = dv;
     a.scale = scale;
     a.vec = pieces(q_d, q_stride, E::kBytes) && pieces(k_d, k_stride, E::kBytes) && pieces(v_d, v_stride, E::kBytes) &&
-            pieces(dy_d, dy_stride, E::kBytes) && dk % 8 == 0 && dv % 8 == 0;
+            pieces(dy_d, dy_stride, E::kBytes) && pieces(dv_d, dv_stride, E::kBytes) && aligned(carry_d, 16) && dk % 8 == 0 &&
+            dv % 8 == 0;
+    a.pairs = dv % 2 == 0 && dv_stride % 2 == 0 && aligned(dv_d, 2 * E::kBytes);
     a.status = status_d;
     const Space s = space(workspace_d, n_tokens, n_seqs, key_heads, heads, dk, dv, true);
     a.first = s.first;
@@ -592,7 +858,7 @@ extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void
     a.after = s.after;
     a.writes = s.writes;
     a.shared = s.shared;
-    return launch_grad<E>(a, as_stream(stream));
+    return launch_grad<E>(a, sms, as_stream(stream));
   };
   return type == ENGRAM_T_BF16 ? go(train::Bf16{}) : go(train::F32{});
 }

@@ -86,6 +86,14 @@ def test_packed_sequences(T, S, masked, state, kind):
     run(T, 2, 4, 48, 40, cuts(T, S, S), kind, 30, masked, state)
 
 
+@pytest.mark.parametrize("T,S,keys,H,dk,dv,masked,state", [(900, 10, 4, 8, 128, 128, 0.1, True), (700, 20, 2, 8, 64, 40, 0.0, True),
+                                                           (300, 80, 1, 2, 33, 125, 0.3, True), (500, 1, 38, 76, 128, 24, 0.0, False),
+                                                           (400, 2, 20, 40, 65, 128, 0.0, False), (130, 40, 2, 2, 8, 1, 0.0, True)])
+def test_many_sequences_and_heads(T, S, keys, H, dk, dv, masked, state):
+    """Where a warp follows a sequence in a head."""
+    run(T, keys, H, dk, dv, cuts(T, S, S), "bf16", 35, masked, state)
+
+
 def test_sequence_edges_at_chunk_edges():
     run(4 * C, 1, 2, 64, 64, [0, C - 1, C, C, C + 1, 2 * C, 3 * C + 1, 4 * C], "f32", 40, state=True)
 
