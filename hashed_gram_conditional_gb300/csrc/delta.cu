@@ -307,6 +307,26 @@ struct ScanRows {
   static constexpr int kSmem = kStages * kStage;
 };
 
+// c += A B, A 16 of the positions from block ib on, B a triangle's blocks (ib, tb >= ib).
+template <int TA, int TB, int kLimit>
+__device__ __forceinline__ void below(float (&c)[kC / 8][4], float (&s)[kC / 8][4], const uint32_t (&fa)[TA][4],
+                                      const TriAcross& b, int ib) {
+#pragma unroll
+  for (int j = 0; j < TB; ++j) {
+    uint32_t fb[kC / 16][2][2];
+#pragma unroll
+    for (int tb = 0; tb < kC / 16; ++tb)
+      if (tb >= ib) b.get(fb[tb], ib, tb, j);
+#pragma unroll
+    for (int i = 0; i < TA; ++i)
+      if (i + j < kLimit) {
+#pragma unroll
+        for (int t = 0; t < kC / 8; ++t)
+          if (t >= 2 * ib) mma(kLimit > 2 && i + j > 0 ? s[t] : c[t], fa[i], fb[t >> 1][t & 1][0], fb[t >> 1][t & 1][1]);
+      }
+  }
+}
+
 template <class E, int KD, int W>
 __global__ void __launch_bounds__(W * 32, 1) scan_rows_kernel(Args<E> a) {
   using L = ScanRows<E, KD, W>;
@@ -356,7 +376,6 @@ __global__ void __launch_bounds__(W * 32, 1) scan_rows_kernel(Args<E> a) {
     copies_begun();
   };
   if (n > 0) load(0);
-  const bool even = a.dk % 2 == 0 && (reinterpret_cast<uintptr_t>(a.carry) & 7) == 0;
   for (int i = 0; i < n; ++i) {
     const uint32_t stage = base + (i % L::kStages) * L::kStage;
     const Mat K = mat<kC, KD>(stage + L::kK), Q = mat<kC, KD>(stage + L::kQ), V = mat<kC, 16 * W>(stage + L::kV);
@@ -364,7 +383,7 @@ __global__ void __launch_bounds__(W * 32, 1) scan_rows_kernel(Args<E> a) {
     copies_done();
     __syncthreads();  // the chunk is here, and the other stage is free
     if (L::kStages == 2 && i + 1 < n) load(i + 1);
-    if (a.carry != nullptr) save_state<E, KD>(a, a.carry, unit_of(a, c0 + i, h), S, vw, even);
+    float* kept = a.carry != nullptr && vw < a.dv ? a.carry + unit_of(a, c0 + i, h) * saved_floats<E>(a.dk, a.dv) : nullptr;
     // ---- (K S)^T and (Q S)^T
     float x[kC / 8][4], s[kC / 8][4], y[kC / 8][4];
     clear(x);
@@ -374,20 +393,17 @@ __global__ void __launch_bounds__(W * 32, 1) scan_rows_kernel(Args<E> a) {
     for (int kb = 0; kb < KD / 16; ++kb) {
       uint32_t fa[kS][4];
       as_operand<kS>(fa, S[2 * kb], S[2 * kb + 1]);
+      if (kept != nullptr && kb * 16 < a.dk) save_block(block_of(kept, a.dk, vw >> 4, kb), fa);
 #pragma unroll
-      for (int cb = 0; cb < kC / 16; ++cb) {
-        uint32_t fb[kI][2][2];
+      for (int j = 0; j < kI; ++j) {
+        uint32_t fb[kC / 16][2][2];
 #pragma unroll
-        for (int j = 0; j < kI; ++j) Across{K}.get<2>(fb[j], kb * 16, cb * 16, j);
-        pair_product<kS, kI, kS>(x[2 * cb], x[2 * cb + 1], s[2 * cb], s[2 * cb + 1], fa, fb);
-        uint32_t fo[kO][4];
+        for (int cb = 0; cb < kC / 16; ++cb) Across{K}.get<2>(fb[cb], kb * 16, cb * 16, j);
+        pairs_product<kS, kS, kC / 16>(x, s, fa, fb, j);
 #pragma unroll
-        for (int j = 0; j < kO; ++j)
-#pragma unroll
-          for (int p = 0; p < 4; ++p) fo[j][p] = fa[j][p];
-#pragma unroll
-        for (int j = 0; j < kI; ++j) Across{Q}.get<2>(fb[j], kb * 16, cb * 16, j);
-        pair_product<kO, kI, kO>(y[2 * cb], y[2 * cb + 1], y[2 * cb], y[2 * cb + 1], fo, fb);
+        for (int cb = 0; cb < kC / 16; ++cb) Across{Q}.get<2>(fb[cb], kb * 16, cb * 16, j);
+        const uint32_t(&fo)[kO][4] = reinterpret_cast<const uint32_t(&)[kO][4]>(fa);
+        pairs_product<kO, kO, kC / 16>(y, y, fo, fb, j);
       }
     }
     // ---- X^T
@@ -428,13 +444,7 @@ __global__ void __launch_bounds__(W * 32, 1) scan_rows_kernel(Args<E> a) {
     for (int ib = 0; ib < kC / 16; ++ib) {
       uint32_t fa[kS][4];
       as_operand<kS>(fa, x[2 * ib], x[2 * ib + 1]);
-#pragma unroll
-      for (int tb = ib; tb < kC / 16; ++tb) {
-        uint32_t fb[kS][2][2];
-#pragma unroll
-        for (int j = 0; j < kS; ++j) TriAcross{stage + L::kM}.get(fb[j], ib, tb, j);
-        pair_product<kS, kS, kS>(u[2 * tb], u[2 * tb + 1], s[2 * tb], s[2 * tb + 1], fa, fb);
-      }
+      below<kS, kS, kS>(u, s, fa, TriAcross{stage + L::kM}, ib);
     }
 #pragma unroll
     for (int t = 0; t < kC / 8; ++t)
@@ -445,13 +455,7 @@ __global__ void __launch_bounds__(W * 32, 1) scan_rows_kernel(Args<E> a) {
     for (int ib = 0; ib < kC / 16; ++ib) {
       uint32_t fa[kO][4];
       as_operand<kO>(fa, u[2 * ib], u[2 * ib + 1]);
-#pragma unroll
-      for (int tb = ib; tb < kC / 16; ++tb) {
-        uint32_t fb[kO][2][2];
-#pragma unroll
-        for (int j = 0; j < kO; ++j) TriAcross{stage + L::kP}.get(fb[j], ib, tb, j);
-        pair_product<kO, kO, kO>(y[2 * tb], y[2 * tb + 1], y[2 * tb], y[2 * tb + 1], fa, fb);
-      }
+      below<kO, kO, kO>(y, y, fa, TriAcross{stage + L::kP}, ib);
     }
     const int64_t p = lo + static_cast<int64_t>(i) * kC;
     const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
@@ -571,16 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_kernel(Args<E> a) {
     copies_done();
     __syncthreads();  // the chunk and the state are here, and the other stage is free
     if (L::kStages == 2 && i + 1 < n) load(i + 1);
-    if (a.carry != nullptr) {
-      const size_t unit = unit_of(a, c0 + i, h);
-#pragma unroll
-      for (int t = 0; t < L::kSN; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = sm + g + (j >> 1) * 8, c = sn + t * 8 + t2 + (j & 1);
-          if (r < a.dk && c < cols) save<E>(a.carry, unit, matrix, static_cast<size_t>(v0 + c) * a.dk + r, S[t][j]);
-        }
-    }
+    if (a.carry != nullptr)
+      save_tile<E, L::kSN>(a, a.carry + unit_of(a, c0 + i, h) * saved_floats<E>(a.dk, a.dv), S, sm, v0 + sn);
     float x[L::kN][4], y[L::kN][4];
     clear(x);
     clear(y);
@@ -791,7 +787,7 @@ Space space(void* base, int64_t n_tokens, int64_t n_seqs, int32_t keys, int32_t 
   s.tri = take(units * kTriBytes);
   s.gates = reinterpret_cast<Gates*>(take(units * sizeof(Gates)));
   if (backward) {
-    s.after = reinterpret_cast<float*>(take(units * dk * dv * sizeof(float)));
+    s.after = reinterpret_cast<float*>(take(units * saved_floats<train::Bf16>(dk, dv) * sizeof(float)));
     s.writes = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(n_tokens) * heads * dv * sizeof(uint16_t)));
     if (heads > keys) s.shared = reinterpret_cast<float*>(take(2 * static_cast<size_t>(n_tokens) * keys * dk * sizeof(float)));
   }
@@ -807,7 +803,8 @@ using namespace engram::delta;
 
 extern "C" size_t engram_delta_carry_bytes(int64_t n_tokens, int64_t n_seqs, int32_t heads, int32_t dk, int32_t dv) {
   if (n_tokens < 0 || n_seqs < 0 || heads < 1 || dk < 1 || dv < 1) return 0;
-  return static_cast<size_t>(max_chunks(n_tokens, n_seqs)) * heads * dk * dv * sizeof(float);
+  // (both types' room: bf16's blocks are padded, fp32's matrices are not)
+  return static_cast<size_t>(max_chunks(n_tokens, n_seqs)) * heads * saved_floats<train::Bf16>(dk, dv) * sizeof(float);
 }
 
 extern "C" size_t engram_delta_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int32_t key_heads, int32_t heads, int32_t dk,

@@ -377,20 +377,19 @@ __device__ __forceinline__ void as_operand(uint32_t (&f)[N][4], const float (&lo
     }
   }
 }
-// c += A B over 16 of k and two tiles of 8 columns; the small terms' products go to s
-// where 24 bits are to be kept (see `product`).
-template <int TA, int TB, int kLimit>
-__device__ __forceinline__ void pair_product(float (&c0)[4], float (&c1)[4], float (&s0)[4], float (&s1)[4],
-                                             const uint32_t (&a)[TA][4], const uint32_t (&b)[TB][2][2]) {
+// c += A B over 16 of k and N pairs of tiles of 8 columns, of term j of B and all of A's
+// that go with it; the small terms' products go to s where 24 bits are to be kept (see
+// `product`).  The tiles take turns: an accumulator's next product waits for its last.
+template <int TA, int kLimit, int N>
+__device__ __forceinline__ void pairs_product(float (*c)[4], float (*s)[4], const uint32_t (&a)[TA][4],
+                                              const uint32_t (&b)[N][2][2], int j) {
 #pragma unroll
-  for (int j = 0; j < TB; ++j)
+  for (int i = 0; i < TA; ++i)
+    if (i + j < kLimit) {
+      float(*to)[4] = kLimit > 2 && i + j > 0 ? s : c;
 #pragma unroll
-    for (int i = 0; i < TA; ++i)
-      if (i + j < kLimit) {
-        const bool apart = kLimit > 2 && i + j > 0;
-        mma(apart ? s0 : c0, a[i], b[j][0][0], b[j][0][1]);
-        mma(apart ? s1 : c1, a[i], b[j][1][0], b[j][1][1]);
-      }
+      for (int t = 0; t < 2 * N; ++t) mma(to[t], a[i], b[t >> 1][t & 1][0], b[t >> 1][t & 1][1]);
+    }
 }
 // An 8 x 8 matrix of 16-bit values, a row's pair a lane, transposed.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
@@ -399,32 +398,60 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   return r;
 }
 
-// States that are kept for the backward pass lie [dv][dk]: fp32, or for inputs of type
-// bf16 two terms, one behind the other, which take the same room and are an operand as
-// they are.
+// States that are kept for the backward pass: fp32 as they are, transposed, [dv][dk]; for
+// inputs of type bf16 two terms in blocks of 16 columns and 16 rows, 1 KB each: for
+// either term four 8 x 8 matrices, S^T's (columns, rows) 0 0, 8 0, 0 8 and 8 8.  A warp
+// writes a matrix as its lanes hold it, 128 bytes, and reads it as an operand from where
+// it was copied to.
+constexpr int kBlockBytes = 1024;
 template <class E>
-__device__ __forceinline__ void save(float* base, size_t unit, size_t matrix, size_t at, float x) {
-  if constexpr (E::kBytes == 4) {
-    base[unit * matrix + at] = x;
-  } else {
-    uint16_t* to = reinterpret_cast<uint16_t*>(base) + unit * 2 * matrix + at;
-    const uint32_t w = pack(x, 0.f);
-    to[0] = static_cast<uint16_t>(w);
-    to[matrix] = static_cast<uint16_t>(pack(x - lo_of(w), 0.f));
-  }
+__host__ __device__ size_t saved_floats(int dk, int dv) {  // of a chunk's state
+  if (E::kBytes == 4) return static_cast<size_t>(dk) * dv;
+  return static_cast<size_t>((dk + 15) / 16) * ((dv + 15) / 16) * (kBlockBytes / 4);
 }
-// two neighbouring ones; `whole`: dk is even and base aligned to their size
-template <class E>
-__device__ __forceinline__ void save2(float* base, size_t unit, size_t matrix, size_t at, float x0, float x1) {
-  if constexpr (E::kBytes == 4) {
-    *reinterpret_cast<float2*>(base + unit * matrix + at) = make_float2(x0, x1);
-  } else {
-    uint32_t* to = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(base) + unit * 2 * matrix + at);
-    const uint32_t w = pack(x0, x1);
-    to[0] = w;
-    to[matrix / 2] = pack(x0 - lo_of(w), x1 - hi_of(w));
-  }
+__device__ __forceinline__ uint32_t* block_of(float* base, int dk, int vb, int kb) {
+  return reinterpret_cast<uint32_t*>(base) + (static_cast<size_t>(vb) * ((dk + 15) / 16) + kb) * (kBlockBytes / 4);
 }
+// a lane's part of a block: the first two terms of an operand
+__device__ __forceinline__ void save_block(uint32_t* block, const uint32_t (&f)[kStateTerms][4]) {
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) block[n * 128 + j * 32 + lane_id()] = f[n][j];
+}
+// S^T's blocks in shared memory as an operand B(k, n), 16 x 16 pieces
+struct BlocksAcross {  // k: rows of the state, n: columns
+  uint32_t base;
+  int across;  // blocks of rows
+  template <int N>
+  __device__ __forceinline__ void get(uint32_t (&r)[N][2], int k, int n, int t) const {
+    const int l = lane_id();
+    const uint32_t at = base + ((n >> 4) * across + (k >> 4)) * kBlockBytes + t * 512 + (l & 7) * 16;
+    if constexpr (N == 1) {
+      ld2(r[0][0], r[0][1], at + ((n >> 3) & 1) * 128 + ((l >> 3) & 1) * 256);
+    } else {
+      static_assert(N == 2, "a block's columns");
+      uint32_t w[4];
+      ld4(w, at + ((l >> 3) & 1) * 256 + (l >> 4) * 128);
+      r[0][0] = w[0]; r[0][1] = w[1]; r[1][0] = w[2]; r[1][1] = w[3];
+    }
+  }
+};
+struct BlocksDown {  // k: columns, n: rows
+  uint32_t base;
+  int across;
+  template <int N>
+  __device__ __forceinline__ void get(uint32_t (&r)[N][2], int k, int n, int t) const {
+    static_assert(N % 2 == 0, "blocks of 16 rows");
+    const int l = lane_id();
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+      uint32_t w[4];
+      ld4t(w, base + ((k >> 4) * across + (n >> 4) + j / 2) * kBlockBytes + t * 512 + l * 16);
+      r[j][0] = w[0]; r[j][1] = w[1]; r[j + 1][0] = w[2]; r[j + 1][1] = w[3];
+    }
+  }
+};
 
 template <int N>
 __device__ __forceinline__ void clear(float (&c)[N][4]) {
@@ -460,30 +487,32 @@ __device__ __forceinline__ void padding_zeros(const Args<E>& a, int lo, int hi, 
   for (int64_t i = threadIdx.x; i < static_cast<int64_t>(hi - lo) * cols; i += threads)
     E::store(out + (lo + i / cols) * stride + h * a.dv + v0 + i % cols, 0.f);
   if (a.y == nullptr || a.carry == nullptr) return;
-  const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
+  const size_t saved = saved_floats<E>(a.dk, a.dv), at = v0 == 0 ? 0 : saved_floats<E>(a.dk, v0);
+  const size_t mine = saved_floats<E>(a.dk, cols);
   for (int c = 0; c < n; ++c)
-    for (int i = threadIdx.x; i < a.dk * cols; i += threads)
-      save<E>(a.carry, unit_of(a, c0 + c, h), matrix, static_cast<size_t>(v0) * a.dk + i, 0.f);
+    for (size_t i = threadIdx.x; i < mine; i += threads) a.carry[unit_of(a, c0 + c, h) * saved + at + i] = 0.f;
 }
 
-// A warp's columns vw .. vw + 15 of a state, held transposed, for the backward pass.
-template <class E, int KD>
-__device__ __forceinline__ void save_state(const Args<E>& a, float* base, size_t unit, const float (&S)[KD / 8][4], int vw,
-                                           bool even) {
+// A warp's tile of a state held as it is, rows r .. r + 15 and 8 N columns from c on (of
+// all columns), for the backward pass.
+template <class E, int N>
+__device__ __forceinline__ void save_tile(const Args<E>& a, float* to, const float (&S)[N][4], int r, int c) {
   const int lane = lane_id(), g = lane >> 2, t2 = (lane & 3) * 2;
-  const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
 #pragma unroll
-  for (int t = 0; t < KD / 8; ++t)
+  for (int t = 0; t < N; ++t)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int v = vw + g + j * 8, k = t * 8 + t2;
-      if (v >= a.dv || k >= a.dk) continue;
-      const size_t at = static_cast<size_t>(v) * a.dk + k;
-      if (even) {
-        save2<E>(base, unit, matrix, at, S[t][2 * j], S[t][2 * j + 1]);
-      } else {
-        save<E>(base, unit, matrix, at, S[t][2 * j]);
-        if (k + 1 < a.dk) save<E>(base, unit, matrix, at + 1, S[t][2 * j + 1]);
+      if constexpr (E::kBytes == 4) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = r + g + j * 8, column = c + t * 8 + t2 + e;
+          if (row < a.dk && column < a.dv) to[static_cast<size_t>(column) * a.dk + row] = S[t][2 * j + e];
+        }
+      } else if (r < a.dk && ((c + t * 8) & ~15) < a.dv) {  // (whole blocks, zeros in their padding)
+        const uint32_t w = pack(S[t][2 * j], S[t][2 * j + 1]);
+        uint32_t* at = block_of(to, a.dk, (c + t * 8) >> 4, r >> 4) + (((c + t * 8) >> 3) & 1) * 32 + j * 64 + lane;
+        at[0] = transposed(w);
+        at[128] = transposed(pack(S[t][2 * j] - lo_of(w), S[t][2 * j + 1] - hi_of(w)));
       }
     }
 }
@@ -526,19 +555,21 @@ template <class E, int KD>
 __device__ __forceinline__ void add_outer(float (&S)[KD / 8][4], float total, const uint32_t (&fa)[kC / 16][kStateTerms][4],
                                           const Mat& X) {
 #pragma unroll
-  for (int kb = 0; kb < KD / 16; ++kb) {
-    float c[2][4], s[2][4];
+  for (int kb = 0; kb < KD / 16; kb += 2) {
+    float c[4][4], s[4][4];
     clear(c);
     clear(s);
 #pragma unroll
-    for (int cb = 0; cb < kC / 16; ++cb) {
-      uint32_t fb[kIn<E>][2][2];
+    for (int cb = 0; cb < kC / 16; ++cb)
 #pragma unroll
-      for (int j = 0; j < kIn<E>; ++j) Down{X}.get<2>(fb[j], cb * 16, kb * 16, j);
-      pair_product<kStateTerms, kIn<E>, kStateTerms>(c[0], c[1], s[0], s[1], fa[cb], fb);
-    }
+      for (int j = 0; j < kIn<E>; ++j) {
+        uint32_t fb[2][2][2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < 2; ++e) Down{X}.get<2>(fb[e], cb * 16, (kb + e) * 16, j);
+        pairs_product<kStateTerms, kStateTerms, 2>(c, s, fa[cb], fb, j);
+      }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
 #pragma unroll
       for (int j = 0; j < 4; ++j) S[2 * kb + e][j] = fmaf(S[2 * kb + e][j], total, c[e][j] + s[e][j]);
   }

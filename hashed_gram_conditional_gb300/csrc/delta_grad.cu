@@ -100,16 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1) back_kernel(Args<E> a) {
     copies_done();
     __syncthreads();  // the chunk and dS are here, and the other stage is free
     if (L::kStages == 2 && i > 0) load(i - 1);
-    {
-      const size_t unit = unit_of(a, c0 + i, h);
-#pragma unroll
-      for (int t = 0; t < L::kSN; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = sm + g + (j >> 1) * 8, c = sn + t * 8 + t2 + (j & 1);
-          if (r < a.dk && c < cols) save<E>(a.after, unit, matrix, static_cast<size_t>(v0 + c) * a.dk + r, S[t][j]);
-        }
-    }
+    save_tile<E, L::kSN>(a, a.after + unit_of(a, c0 + i, h) * saved_floats<E>(a.dk, a.dv), S, sm, v0 + sn);
     float x[L::kN][4], u[L::kN][4];
     clear(x);
     clear(u);
@@ -182,6 +173,26 @@ struct BackRows {
   static constexpr int kSmem = kStages * kStage;
 };
 
+// c += A B, A 16 of the positions, block tb, B a triangle's blocks (tb, ib <= tb).
+template <int TA>
+__device__ __forceinline__ void above(float (&c)[kC / 8][4], float (&s)[kC / 8][4], const uint32_t (&fa)[TA][4],
+                                      const TriDown& b, int tb) {
+#pragma unroll
+  for (int j = 0; j < kStateTerms; ++j) {
+    uint32_t fb[kC / 16][2][2];
+#pragma unroll
+    for (int ib = 0; ib < kC / 16; ++ib)
+      if (ib <= tb) b.get(fb[ib], tb, ib, j);
+#pragma unroll
+    for (int i = 0; i < TA; ++i)
+      if (i + j < kStateTerms) {
+#pragma unroll
+        for (int t = 0; t < kC / 8; ++t)
+          if (t / 2 <= tb) mma(i + j > 0 ? s[t] : c[t], fa[i], fb[t >> 1][t & 1][0], fb[t >> 1][t & 1][1]);
+      }
+  }
+}
+
 template <class E, int KD, int W>
 __global__ void __launch_bounds__(W * 32, 1) back_rows_kernel(Args<E> a) {
   using L = BackRows<E, KD, W>;
@@ -231,7 +242,6 @@ __global__ void __launch_bounds__(W * 32, 1) back_rows_kernel(Args<E> a) {
     copies_begun();
   };
   if (n > 0) load(n - 1);
-  const bool even = a.dk % 2 == 0;  // (the workspace is aligned)
   for (int i = n - 1; i >= 0; --i) {
     const uint32_t stage = base + (i % L::kStages) * L::kStage;
     const Mat K = mat<kC, KD>(stage + L::kK), Q = mat<kC, KD>(stage + L::kQ), Y = mat<kC, 16 * W>(stage + L::kY);
@@ -239,7 +249,7 @@ __global__ void __launch_bounds__(W * 32, 1) back_rows_kernel(Args<E> a) {
     copies_done();
     __syncthreads();  // the chunk is here, and the other stage is free
     if (i > 0) load(i - 1);
-    save_state<E, KD>(a, a.after, unit_of(a, c0 + i, h), S, vw, even);
+    float* kept = a.after + unit_of(a, c0 + i, h) * saved_floats<E>(a.dk, a.dv);
     // ---- dU^T = e^(c_last - c) (K dS)^T + dY^T P
     float u[kC / 8][4], s[kC / 8][4];
     clear(u);
@@ -248,12 +258,13 @@ __global__ void __launch_bounds__(W * 32, 1) back_rows_kernel(Args<E> a) {
     for (int kb = 0; kb < KD / 16; ++kb) {
       uint32_t fa[kS][4];
       as_operand<kS>(fa, S[2 * kb], S[2 * kb + 1]);
+      if (vw < a.dv && kb * 16 < a.dk) save_block(block_of(kept, a.dk, vw >> 4, kb), fa);
 #pragma unroll
-      for (int cb = 0; cb < kB; ++cb) {
-        uint32_t fb[kI][2][2];
+      for (int j = 0; j < kI; ++j) {
+        uint32_t fb[kB][2][2];
 #pragma unroll
-        for (int j = 0; j < kI; ++j) Across{K}.get<2>(fb[j], kb * 16, cb * 16, j);
-        pair_product<kS, kI, kS>(u[2 * cb], u[2 * cb + 1], s[2 * cb], s[2 * cb + 1], fa, fb);
+        for (int cb = 0; cb < kB; ++cb) Across{K}.get<2>(fb[cb], kb * 16, cb * 16, j);
+        pairs_product<kS, kS, kB>(u, s, fa, fb, j);
       }
     }
 #pragma unroll
@@ -270,13 +281,7 @@ __global__ void __launch_bounds__(W * 32, 1) back_rows_kernel(Args<E> a) {
       uint32_t fa[kI][4];
 #pragma unroll
       for (int j = 0; j < kI; ++j) Cols{Y}(fa[j], warp * 16, tb * 16, j);
-#pragma unroll
-      for (int ib = 0; ib <= tb; ++ib) {
-        uint32_t fb[kS][2][2];
-#pragma unroll
-        for (int j = 0; j < kS; ++j) TriDown{stage + L::kP}.get(fb[j], tb, ib, j);
-        pair_product<kI, kS, kS>(u[2 * ib], u[2 * ib + 1], s[2 * ib], s[2 * ib + 1], fa, fb);
-      }
+      above<kI>(u, s, fa, TriDown{stage + L::kP}, tb);
     }
 #pragma unroll
     for (int t = 0; t < kC / 8; ++t)
@@ -290,13 +295,7 @@ __global__ void __launch_bounds__(W * 32, 1) back_rows_kernel(Args<E> a) {
     for (int tb = 0; tb < kB; ++tb) {
       uint32_t fa[kS][4];
       as_operand<kS>(fa, u[2 * tb], u[2 * tb + 1]);
-#pragma unroll
-      for (int ib = 0; ib <= tb; ++ib) {
-        uint32_t fb[kS][2][2];
-#pragma unroll
-        for (int j = 0; j < kS; ++j) TriDown{stage + L::kM}.get(fb[j], tb, ib, j);
-        pair_product<kS, kS, kS>(w[2 * ib], w[2 * ib + 1], s[2 * ib], s[2 * ib + 1], fa, fb);
-      }
+      above<kS>(w, s, fa, TriDown{stage + L::kM}, tb);
     }
 #pragma unroll
     for (int t = 0; t < kC / 8; ++t)
@@ -354,68 +353,85 @@ __global__ void __launch_bounds__(W * 32, 1) back_rows_kernel(Args<E> a) {
 // A block has one chunk and the heads of one key head, one after another, and a head's
 // value columns in slices of VS.  The next slice's inputs are copied while this one is
 // used (bf16: all of them are operands as they lie in memory; fp32 are made terms on
-// the way).
+// the way).  A warp has 16 rows and a part of the columns of each product: a quarter
+// (bf16: with half of them 8 warps had 255 registers each, and waited for one another),
+// or half.
 template <class E, int KD, int VS>
 struct Grads {
-  static constexpr int kO = kOut<E>, kStages = E::kBytes == 2 ? 2 : 1;
+  static constexpr int kO = kOut<E>, kStages = E::kBytes == 2 ? 2 : 1, kParts = E::kBytes == 2 ? 4 : 2;
+  static constexpr int kT = 4 * kParts * 32;  // threads
   static constexpr int kK = 0, kQ = kK + kIn<E> * mat_bytes(kC, KD);
   static constexpr int kHead = kQ + kIn<E> * mat_bytes(kC, KD);  // M and the gates, of this head and the next
   static constexpr int kHeadBytes = kO * kTerm + static_cast<int>(sizeof(Gates));
-  static constexpr int kNum = kHead + kStages * kHeadBytes;    // sums
-  static constexpr int kSums = 2 * kC * 4 + 4 * kC + kWarps;   // floats
+  static constexpr int kNum = kHead + kStages * kHeadBytes;                   // sums
+  static constexpr int kSums = kParts * kC * 4 + 4 * kC + 4 * kParts;         // floats
   static constexpr int kF = (kNum + kSums * 4 + 127) / 128 * 128, kE = kF + kO * mat_bytes(kC, kC);
   static constexpr int kU = E::kBytes == 2 ? kE + kO * mat_bytes(kC, kC) : kF;
-  static constexpr int kSlice = kU + kO * mat_bytes(kC, VS);
+  static constexpr int kSlice = (kU + kO * mat_bytes(kC, VS) + 127) / 128 * 128;
   // a slice of the value columns: S^T, dS^T, V then V - e^c K S, dY, dV
-  static constexpr int kS = 0, kD = kS + kO * mat_bytes(VS, KD), kX = kD + kO * mat_bytes(VS, KD);
+  static constexpr int kState = E::kBytes == 2 ? VS / 16 * (KD / 16) * kBlockBytes : kO * mat_bytes(VS, KD);
+  static constexpr int kS = 0, kD = kS + kState, kX = kD + kState;
   static constexpr int kY = kX + kO * mat_bytes(kC, VS), kW = kY + kIn<E> * mat_bytes(kC, VS);
   static constexpr int kSliceBytes = kW + kO * mat_bytes(kC, VS);
   // (fp32: F and E lie over U and the slice)
   static constexpr int kEnd = kSlice + kStages * kSliceBytes, kEnd2 = kE + kO * mat_bytes(kC, kC);
   static constexpr int kSmem = kEnd > kEnd2 ? kEnd : kEnd2;
-  static constexpr int kN = VS / 16, kKN = KD / 16;  // a warp's tiles of a slice's, and of a key's columns
+  static constexpr int kN = VS / 8 / kParts, kCN = kC / 8 / kParts, kKN = KD / 8 / kParts;  // a warp's tiles of 8 columns
 };
 
-// `rows` rows of a saved state, from row v0 on, as terms, zeros around them.
-template <class E, int KD, int VS>
-__device__ __forceinline__ void load_state(const Mat& m, const float* base, size_t unit, size_t matrix, int v0, int rows, int dk,
-                                           bool vec) {
+// `cols` columns of a saved state, from column v0 on, zeros around them.
+template <class E, int KD, int VS, int kT>
+__device__ __forceinline__ void load_state(uint32_t to, const float* from, int v0, int cols, int dk, bool vec) {
   if constexpr (E::kBytes == 2) {
-    const uint16_t* from = reinterpret_cast<const uint16_t*>(base) + unit * 2 * matrix + static_cast<size_t>(v0) * dk;
+    // blocks as they lie, and zeros where the head has none
+    const int across = (dk + 15) / 16;
+    const uint32_t* blocks = reinterpret_cast<const uint32_t*>(from) + static_cast<size_t>(v0 / 16) * across * (kBlockBytes / 4);
     if (vec) {
 #pragma unroll
-      for (int i0 = 0; i0 < 2 * VS * (KD / 8); i0 += kThreads) {
-        const int i = i0 + threadIdx.x, n = i / (VS * (KD / 8)), r = i / (KD / 8) % VS, c = i % (KD / 8) * 8;
-        const bool on = r < rows && c < dk;
-        copy16(m.base + n * m.term + r * m.pitch + c * 2, on ? from + n * matrix + static_cast<size_t>(r) * dk + c : from, on);
+      for (int i0 = 0; i0 < VS / 16 * (KD / 16) * (kBlockBytes / 16); i0 += kT) {
+        const int i = i0 + threadIdx.x, b = i / (kBlockBytes / 16), vb = b / (KD / 16), kb = b % (KD / 16);
+        const bool on = vb * 16 < cols && kb < across;
+        copy16(to + i * 16, on ? blocks + (vb * across + kb) * (kBlockBytes / 4) + i % (kBlockBytes / 16) * 4 : blocks, on);
       }
     } else {
-      for (int i = threadIdx.x; i < 2 * VS * (KD / 2); i += kThreads) {
-        const int n = i / (VS * (KD / 2)), r = i / (KD / 2) % VS, c = i % (KD / 2) * 2;
-        const uint16_t* p = from + n * matrix + static_cast<size_t>(r) * dk + c;
-        const uint32_t x0 = r < rows && c < dk ? p[0] : 0u, x1 = r < rows && c + 1 < dk ? p[1] : 0u;
-        st32(m.base + n * m.term + r * m.pitch + c * 2, x0 | x1 << 16);
+      for (int i = threadIdx.x; i < VS / 16 * (KD / 16) * (kBlockBytes / 4); i += kT) {
+        const int b = i / (kBlockBytes / 4), vb = b / (KD / 16), kb = b % (KD / 16);
+        const bool on = vb * 16 < cols && kb < across;
+        st32(to + i * 4, on ? blocks[(vb * across + kb) * (kBlockBytes / 4) + i % (kBlockBytes / 4)] : 0u);
       }
     }
   } else {
-    const float* from = base + unit * matrix + static_cast<size_t>(v0) * dk;
+    const Mat m = mat<VS, KD>(to);
+    from += static_cast<size_t>(v0) * dk;
     constexpr int kAhead = 4;
-    for (int i0 = threadIdx.x; i0 < VS * (KD / 2); i0 += kAhead * kThreads) {
+    for (int i0 = threadIdx.x; i0 < VS * (KD / 2); i0 += kAhead * kT) {
       float x[kAhead][2];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int i = i0 + u * kThreads, r = i / (KD / 2), c = i % (KD / 2) * 2;
+        const int i = i0 + u * kT, r = i / (KD / 2), c = i % (KD / 2) * 2;
         const float* p = from + static_cast<size_t>(r) * dk + c;
-        x[u][0] = r < rows && c < dk ? p[0] : 0.f;
-        x[u][1] = r < rows && c + 1 < dk ? p[1] : 0.f;
+        x[u][0] = r < cols && c < dk ? p[0] : 0.f;
+        x[u][1] = r < cols && c + 1 < dk ? p[1] : 0.f;
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int i = i0 + u * kThreads, r = i / (KD / 2), c = i % (KD / 2) * 2;
+        const int i = i0 + u * kT, r = i / (KD / 2), c = i % (KD / 2) * 2;
         if (r < VS) put<kOut<E>>(m.base + r * m.pitch + c * 2, m.term, x[u][0], x[u][1]);
       }
     }
   }
+}
+
+// S^T in shared memory as an operand: rows as k (of K S) or as n (of dY S^T).
+template <class E, int KD, int VS>
+__device__ __forceinline__ auto state_across(uint32_t at) {
+  if constexpr (E::kBytes == 2) return BlocksAcross{at, KD / 16};
+  else return Across{mat<VS, KD>(at)};
+}
+template <class E, int KD, int VS>
+__device__ __forceinline__ auto state_down(uint32_t at) {
+  if constexpr (E::kBytes == 2) return BlocksDown{at, KD / 16};
+  else return Down{mat<VS, KD>(at)};
 }
 
 // c += A B and d += A2 B, of TA and TB (A2: TB) terms, over k from 0 to k1
@@ -457,9 +473,9 @@ __device__ __forceinline__ float quad_sum(float v) {
 }
 
 template <class E, int KD, int VS>
-__global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
+__global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> a) {
   using L = Grads<E, KD, VS>;
-  constexpr int kO = L::kO;
+  constexpr int kO = L::kO, kT = L::kT, kParts = L::kParts;
   extern __shared__ __align__(128) unsigned char smem[];
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
@@ -468,13 +484,13 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
   if (!chunk_at(a, blockIdx.x, ch)) return;
   const int64_t p = ch.start;
   if (!ch.live) {  // padding: zeros
-    for (int i = tid; i < ch.len * a.dk; i += kThreads) {
+    for (int i = tid; i < ch.len * a.dk; i += kT) {
       const int64_t r = p + i / a.dk;
       const int c = hk * a.dk + i % a.dk;
       E::store(a.dq + r * a.dq_stride + c, 0.f);
       E::store(a.dk_out + r * a.dk_stride + c, 0.f);
     }
-    for (int i = tid; i < ch.len * group; i += kThreads) {
+    for (int i = tid; i < ch.len * group; i += kT) {
       const int64_t r = p + i / group;
       const int h = hk * group + i % group;
       E::store(a.dg + r * a.dg_stride + h, 0.f);
@@ -483,11 +499,11 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
     return;
   }
   const uint8_t* mask = a.mask != nullptr ? a.mask + p : nullptr;
-  const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
+  const size_t saved = saved_floats<E>(a.dk, a.dv);
   const Mat K = mat<kC, KD>(base + L::kK), Q = mat<kC, KD>(base + L::kQ), U = mat<kC, VS>(base + L::kU);
   const Mat Fm = mat<kC, kC>(base + L::kF), Em = mat<kC, kC>(base + L::kE);
   float* sums = reinterpret_cast<float*>(smem + L::kNum);
-  float *reads = sums, *writes = reads + 2 * kC, *rows = writes + 2 * kC, *own = rows + 2 * kC, *columns = own + 2 * kC,
+  float *reads = sums, *writes = reads + kParts * kC, *rows = writes + kParts * kC, *own = rows + kParts * kC, *columns = own + kParts * kC,
         *wholes = columns + 4 * kC;
   const int slices = (a.dv + VS - 1) / VS, steps = group * slices;
   auto load = [&](int step) {  // of a head's slice, and with the first one M and the gates
@@ -497,31 +513,31 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
     const int64_t column = static_cast<int64_t>(h) * a.dv + v0;
     if (v0 == 0) {
       const uint32_t to = base + L::kHead + (h % L::kStages) * L::kHeadBytes;
-      for (int i = tid; i < kO * kTerm / 16; i += kThreads) copy16(to + i * 16, a.tri + unit * kTriBytes + i * 16, true);
-      load_gates(to + kO * kTerm, a.gates + unit);
+      for (int i = tid; i < kO * kTerm / 16; i += kT) copy16(to + i * 16, a.tri + unit * kTriBytes + i * 16, true);
+      load_gates<kT>(to + kO * kTerm, a.gates + unit);
     }
-    load_rows<E, VS>(mat<kC, VS>(at + L::kX), a.v + p * a.v_stride + column, a.v_stride, ch.len, cols, mask, a.vec);
-    load_rows<E, VS>(mat<kC, VS>(at + L::kY), a.dy + p * a.dy_stride + column, a.dy_stride, ch.len, cols, mask, a.vec);
+    load_rows<E, VS, kT>(mat<kC, VS>(at + L::kX), a.v + p * a.v_stride + column, a.v_stride, ch.len, cols, mask, a.vec);
+    load_rows<E, VS, kT>(mat<kC, VS>(at + L::kY), a.dy + p * a.dy_stride + column, a.dy_stride, ch.len, cols, mask, a.vec);
     const Mat W = mat<kC, VS>(at + L::kW);
-    load_rows<E, VS>(W, a.dv_out + p * a.dv_stride + column, a.dv_stride, ch.len, cols, nullptr, a.vec);
+    load_rows<E, VS, kT>(W, a.dv_out + p * a.dv_stride + column, a.dv_stride, ch.len, cols, nullptr, a.vec);
     if constexpr (E::kBytes == 2) {
       const int64_t wide = static_cast<int64_t>(a.heads) * a.dv;
-      load_rows<E, VS>(Mat{W.base + static_cast<uint32_t>(W.term), W.pitch, W.term}, a.writes + p * wide + column, wide, ch.len,
+      load_rows<E, VS, kT>(Mat{W.base + static_cast<uint32_t>(W.term), W.pitch, W.term}, a.writes + p * wide + column, wide, ch.len,
                        cols, nullptr, a.vec);
     }
-    load_state<E, KD, VS>(mat<VS, KD>(at + L::kS), a.carry, unit, matrix, v0, cols, a.dk, a.vec);
-    load_state<E, KD, VS>(mat<VS, KD>(at + L::kD), a.after, unit, matrix, v0, cols, a.dk, a.vec);
+    load_state<E, KD, VS, kT>(at + L::kS, a.carry + unit * saved, v0, cols, a.dk, a.vec);
+    load_state<E, KD, VS, kT>(at + L::kD, a.after + unit * saved, v0, cols, a.dk, a.vec);
     copies_begun();
   };
-  load_rows<E, KD>(K, a.k + p * a.k_stride + hk * a.dk, a.k_stride, ch.len, a.dk, mask, a.vec);
-  load_rows<E, KD>(Q, a.q + p * a.q_stride + hk * a.dk, a.q_stride, ch.len, a.dk, mask, a.vec);
+  load_rows<E, KD, kT>(K, a.k + p * a.k_stride + hk * a.dk, a.k_stride, ch.len, a.dk, mask, a.vec);
+  load_rows<E, KD, kT>(Q, a.q + p * a.q_stride + hk * a.dk, a.q_stride, ch.len, a.dk, mask, a.vec);
   load(0);
   copies_done();
   __syncthreads();
-  // a warp's tiles: 16 rows, and half of the columns
-  const int m = (warp & 3) * 16, half = warp >> 2, nn = half * (VS / 2), nc = half * (kC / 2), nk = half * (KD / 2);
+  // a warp's tiles: 16 rows, and a part of the columns
+  const int m = (warp & 3) * 16, part = warp >> 2, nn = part * (VS / kParts), nc = part * (kC / kParts), nk = part * (KD / kParts);
   const bool low = nc <= m;  // whether its tile of a triangle has anything
-  float qk[4][4], kk[4][4];
+  float qk[L::kCN][4], kk[L::kCN][4];
   clear(qk);
   clear(kk);
   if (low) {
@@ -531,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
   for (int h = hk * group; h < (hk + 1) * group; ++h) {
     const Gates& gt = *reinterpret_cast<const Gates*>(smem + L::kHead + (h % L::kStages) * L::kHeadBytes + kO * kTerm);
     const uint32_t M = base + L::kHead + (h % L::kStages) * L::kHeadBytes;
-    float cf[4][4], ce[4][4], cq[L::kKN][4], ck[L::kKN][4], cw[L::kKN][4];
+    float cf[L::kCN][4], ce[L::kCN][4], cq[L::kKN][4], ck[L::kKN][4], cw[L::kKN][4];
     float dot[2] = {0.f, 0.f}, whole = 0.f;
     clear(cf);
     clear(ce);
@@ -541,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
     for (int sl = 0; sl < slices; ++sl) {
       const int step = (h - hk * group) * slices + sl;
       const uint32_t at = base + L::kSlice + (step % L::kStages) * L::kSliceBytes;
-      const Mat S = mat<VS, KD>(at + L::kS), D = mat<VS, KD>(at + L::kD);
+      const auto S = state_down<E, KD, VS>(at + L::kS), D = state_down<E, KD, VS>(at + L::kD);
       const Mat X = mat<kC, VS>(at + L::kX), Y = mat<kC, VS>(at + L::kY), W = mat<kC, VS>(at + L::kW);
       if (L::kStages == 1 && step > 0) {
         __syncthreads();  // the slice before has been used
@@ -550,17 +566,29 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
       copies_done();
       __syncthreads();  // the slice is here, and the other stage is free
       if (L::kStages == 2 && step + 1 < steps) load(step + 1);
+      // S . dS, wherever their values lie
+      if constexpr (E::kBytes == 2) {
 #pragma unroll
-      for (int i0 = 0; i0 < VS * (KD / 2); i0 += kThreads) {
-        const int i = i0 + tid, r = i / (KD / 2), c = i % (KD / 2) * 2;
-        float s[2], d[2];
-        get<kO>(S.base + r * S.pitch + c * 2, S.term, s[0], s[1]);
-        get<kO>(D.base + r * D.pitch + c * 2, D.term, d[0], d[1]);
-        whole = fmaf(s[0], d[0], fmaf(s[1], d[1], whole));
+        for (int i0 = 0; i0 < VS / 16 * (KD / 16) * 128; i0 += kT) {
+          const uint32_t word = static_cast<uint32_t>(i0 + tid), to = at + (word >> 7) * kBlockBytes + (word & 127) * 4;
+          float s[2], d[2];
+          get<kO>(to + L::kS, 512, s[0], s[1]);
+          get<kO>(to + L::kD, 512, d[0], d[1]);
+          whole = fmaf(s[0], d[0], fmaf(s[1], d[1], whole));
+        }
+      } else {
+        const Mat sm = mat<VS, KD>(at + L::kS), dm = mat<VS, KD>(at + L::kD);
+        for (int i = tid; i < VS * (KD / 2); i += kT) {
+          const int r = i / (KD / 2), c = i % (KD / 2) * 2;
+          float s[2], d[2];
+          get<kO>(sm.base + r * sm.pitch + c * 2, sm.term, s[0], s[1]);
+          get<kO>(dm.base + r * dm.pitch + c * 2, dm.term, d[0], d[1]);
+          whole = fmaf(s[0], d[0], fmaf(s[1], d[1], whole));
+        }
       }
       float x[L::kN][4];
       clear(x);
-      product<kIn<E>, kO, kO>(x, Rows{K}, Across{S}, m, nn, 0, KD);
+      product<kIn<E>, kO, kO>(x, Rows{K}, state_across<E, KD, VS>(at + L::kS), m, nn, 0, KD);
 #pragma unroll
       for (int t = 0; t < L::kN; ++t)
 #pragma unroll
@@ -573,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
           put<kO>(to, X.term, fmaf(-into, x[t][2 * j], v[0]), fmaf(-into, x[t][2 * j + 1], v[1]));
         }
       // what reads S does not wait for U
-      both_products<kIn<E>, kO>(cq, ck, Rows{Y}, Rows{W}, Down{S}, m, nk, VS);
+      both_products<kIn<E>, kO>(cq, ck, Rows{Y}, Rows{W}, S, m, nk, VS);
       __syncthreads();
       clear(x);
       product<kO, kO, kO>(x, TriRows{M}, Down{X}, m, nn, 0, m + 16);
@@ -589,12 +617,12 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
         }
       __syncthreads();
       if (low) both_products<kIn<E>, kO>(cf, ce, Rows{Y}, Rows{W}, Across{U}, m, nc, VS);
-      product<kO, kO, kO>(cw, Rows{U}, Down{D}, m, nk, 0, VS);
+      product<kO, kO, kO>(cw, Rows{U}, D, m, nk, 0, VS);
     }
     // ---- F and E, the pairs of reads and writes, and what reads S and reaches dS
     float row[2] = {0.f, 0.f};
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < L::kCN; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = nc + t * 8 + t2 + e;
@@ -639,10 +667,10 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
       const float sum_row = quad_sum(row[j]), sum_read = quad_sum(read[j]), sum_write = quad_sum(write[j]),
                   sum_own = quad_sum(dot[j]);
       if (t2 == 0) {
-        rows[half * kC + r] = sum_row;
-        reads[half * kC + r] = sum_read;
-        writes[half * kC + r] = sum_write;
-        own[half * kC + r] = sum_own;
+        rows[part * kC + r] = sum_row;
+        reads[part * kC + r] = sum_read;
+        writes[part * kC + r] = sum_write;
+        own[part * kC + r] = sum_own;
       }
     }
 #pragma unroll
@@ -651,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
     __syncthreads();  // the slice is no longer needed
     if (low) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < L::kCN; ++t)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const uint32_t at = (m + g + j * 8) * Fm.pitch + (nc + t * 8 + t2) * 2;
@@ -698,9 +726,15 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int r = lane * 2 + j;
-        later[j] = (reads[r] + reads[kC + r]) + (rows[r] + rows[kC + r]) -
-                   (((columns[r] + columns[kC + r]) + columns[2 * kC + r]) + columns[3 * kC + r]);
-        before[j] = writes[r] + writes[kC + r];
+        float read = 0.f, row = 0.f, write = 0.f;
+#pragma unroll
+        for (int n = 0; n < kParts; ++n) {
+          read += reads[n * kC + r];
+          row += rows[n * kC + r];
+          write += writes[n * kC + r];
+        }
+        later[j] = read + row - (((columns[r] + columns[kC + r]) + columns[2 * kC + r]) + columns[3 * kC + r]);
+        before[j] = write;
       }
       float sum = later[0] + later[1], head = before[0] + before[1], all = 0.f;
       const float mine = head;
@@ -711,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
         if (lane >= o) head += y;
       }
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) all += wholes[w];
+      for (int w = 0; w < 4 * kParts; ++w) all += wholes[w];
       all *= gt.into[kC - 1];
       const float cross[2] = {sum + (head - mine) + all, (sum - later[0]) + (head - mine + before[0]) + all};
 #pragma unroll
@@ -722,7 +756,10 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(Args<E> a) {
         const int64_t t = p + r;
         const float gr = E::load(a.g + t * a.g_stride + h), br = E::load(a.b + t * a.b_stride + h);
         E::store(a.dg + t * a.dg_stride + h, on ? cross[j] / (1.f + expf(gr)) : 0.f);
-        E::store(a.db + t * a.db_stride + h, on ? (own[r] + own[kC + r]) / (gt.beta[r] * (1.f + expf(br))) : 0.f);
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < kParts; ++n) sum += own[n * kC + r];
+        E::store(a.db + t * a.db_stride + h, on ? sum / (gt.beta[r] * (1.f + expf(br))) : 0.f);
       }
     }
   }
@@ -733,10 +770,10 @@ int launch_grad(const Args<E>& a, int sms, cudaStream_t st) {
   int rc = launch_prepare<E>(a, st);
   if (rc) return rc;
   static std::atomic<uint64_t> done[4] = {{0}, {0}, {0}, {0}};
-  auto go = [&](auto kernel, int smem, dim3 grid, std::atomic<uint64_t>& flag, const char* name) {
+  auto go = [&](auto kernel, int smem, dim3 grid, std::atomic<uint64_t>& flag, const char* name, int threads = kThreads) {
     int r = opt_in(reinterpret_cast<const void*>(kernel), smem, flag);
     if (r) return r;
-    kernel<<<grid, kThreads, smem, st>>>(a);
+    kernel<<<grid, threads, smem, st>>>(a);
     return check_launch(name);
   };
   constexpr int VB = 16, VG = E::kBytes == 2 ? 32 : 16;
@@ -755,8 +792,8 @@ int launch_grad(const Args<E>& a, int sms, cudaStream_t st) {
     rc = a.dk <= 64 ? go(back_kernel<E, 64, VB>, Back<E, 64, VB>::kSmem, back, done[0], "back_kernel")
                     : go(back_kernel<E, 128, VB>, Back<E, 128, VB>::kSmem, back, done[1], "back_kernel");
   if (rc) return rc;
-  return a.dk <= 64 ? go(grads_kernel<E, 64, VG>, Grads<E, 64, VG>::kSmem, grads, done[2], "grads_kernel")
-                    : go(grads_kernel<E, 128, VG>, Grads<E, 128, VG>::kSmem, grads, done[3], "grads_kernel");
+  return a.dk <= 64 ? go(grads_kernel<E, 64, VG>, Grads<E, 64, VG>::kSmem, grads, done[2], "grads_kernel", Grads<E, 64, VG>::kT)
+                    : go(grads_kernel<E, 128, VG>, Grads<E, 128, VG>::kSmem, grads, done[3], "grads_kernel", Grads<E, 128, VG>::kT);
 }
 
 static_assert(Back<train::Bf16, 128, 16>::kSmem <= 232448 && Back<train::F32, 128, 16>::kSmem <= 232448 &&
