@@ -21,6 +21,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "engram_internal.h"
 #include "train_device.cuh"
@@ -413,6 +414,175 @@ __global__ void __launch_bounds__(kMost) norm_grad_kernel(Args a) {
   }
 }
 
+// The same with the rows on their way through shared memory: a thread copies its own
+// vectors of the block's next rows ahead, and reads them when it wants them, so that
+// registers hold little more than the weights' sums and no barrier is for the copies.
+__device__ __forceinline__ void copy_vec(uint32_t to, const uint4* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ uint4 own_vec(uint32_t at) {
+  uint4 x;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+  return x;
+}
+template <int kPer>
+constexpr int kRing = kPer == 1 ? 3 : 2;  // rows of a block on their way or in use
+constexpr int kRingThreads = 640;  // of a vector each: 102 registers
+constexpr int kArrays = 5;   // y, gate, dh, h', dx
+constexpr int kRingSmem = 200 * 1024;
+
+template <class E, int kPer>
+__global__ void __launch_bounds__(kPer == 1 ? kRingThreads : kThreads) norm_grad_ring_kernel(Args a) {
+  constexpr int N = kVec<E>;
+  extern __shared__ __align__(16) float part[];
+  __shared__ float slot[2][3][32], slot_along[32];
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const uint32_t ring = smem_u32(part) + (a.groups > 1 && a.vecs_log2 < 0 ? (a.vecs + a.groups + 3) / 4 * 16 : 0);
+  auto place = [&](int stage, int array, int v) { return ring + ((stage * kArrays + array) * a.vecs + v) * 16; };
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < a.rows) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (v >= a.vecs) continue;
+        copy_vec(place(stage, 0, v), row_of<E, uint4>(a.y, row, a.y_stride) + v);
+        if (a.gate) copy_vec(place(stage, 1, v), row_of<E, uint4>(a.gate, row, a.gate_stride) + v);
+        if (a.dh) copy_vec(place(stage, 2, v), row_of<E, uint4>(a.dh, row, a.dh_stride) + v);
+        if (a.dx) {
+          copy_vec(place(stage, 3, v), row_of<E, uint4>(a.h, row, a.h_stride) + v);
+          copy_vec(place(stage, 4, v), row_of<E, uint4>(a.dx, row, a.dx_stride) + v);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  float dw[kPer][N] = {}, ds[kPer][N] = {}, dn[kPer][N] = {};
+  for (int k = 0; k < kRing<kPer> - 1; ++k) fetch(blockIdx.x + static_cast<int64_t>(k) * gridDim.x, k);
+  int stage = 0, parity = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, stage = stage + 1 == kRing<kPer> ? 0 : stage + 1, parity ^= 1) {
+    fetch(row + static_cast<int64_t>(kRing<kPer> - 1) * gridDim.x, stage == 0 ? kRing<kPer> - 1 : stage - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing<kPer> - 1) : "memory");
+    float sq[kPer], l[kPer][N], sum[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      sq[i] = 0.f;
+      if (v >= a.vecs) continue;
+      float y[N];
+      widen<E>(own_vec(place(stage, 0, v)), y);
+#pragma unroll
+      for (int j = 0; j < N; ++j) sq[i] = fmaf(y[j], y[j], sq[i]);
+      sum[2] += sq[i];
+      if (a.dx) {
+        float h[N], x[N], w[N];
+        widen<E>(own_vec(place(stage, 3, v)), h);
+        widen<E>(own_vec(place(stage, 4, v)), x);
+        load_weights<E>(a.w_next ? a.w_next + v * N : nullptr, w);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          sum[0] = fmaf(h[j], h[j], sum[0]);
+          sum[1] = fmaf(x[j] * w[j], h[j], sum[1]);
+        }
+      }
+    }
+    // the block's three sums at one barrier
+#pragma unroll
+    for (int k = 0; k < 3; ++k) sum[k] = warp_sum(sum[k]);
+    if (warps > 1) {
+      float(&to)[3][32] = slot[parity];
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) to[k][threadIdx.x >> 5] = sum[k];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 3; ++k) sum[k] = warp_sum(lane < warps ? to[k][lane] : 0.f);
+    }
+    if (a.groups == 1) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) sq[i] = sum[2];
+    } else {
+      group_sums(a, sq, part, slot_along);
+    }
+    const float r2 = rsqrtf(sum[0] / a.dim + a.eps), c2 = sum[1] * r2 * r2 * r2 / a.dim;
+    float along[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      along[i] = 0.f;
+      if (v >= a.vecs) continue;
+      if (a.dh) {
+        widen<E>(own_vec(place(stage, 2, v)), l[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) l[i][j] = 0.f;
+      }
+      if (a.dx) {
+        float h[N], x[N], w[N];
+        widen<E>(own_vec(place(stage, 3, v)), h);
+        widen<E>(own_vec(place(stage, 4, v)), x);
+        load_weights<E>(a.w_next ? a.w_next + v * N : nullptr, w);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          x[j] *= r2;
+          l[i][j] += x[j] * w[j] - h[j] * c2;
+          dn[i][j] = fmaf(x[j], h[j], dn[i][j]);
+        }
+      }
+      if (a.dres) row_of<E, uint4>(a.dres, row, a.dres_stride)[v] = narrow<E>(l[i]);
+      const float r = rsqrtf(sq[i] / a.width + a.eps);
+      sq[i] = r;
+      float y[N], z[N], w[N], s[N], dz[N];
+      widen<E>(own_vec(place(stage, 0, v)), y);
+      if (a.gate) widen<E>(own_vec(place(stage, 1, v)), z);
+      load_weights<E>(a.w ? a.w + v * N % a.width : nullptr, w);
+      load_weights<E>(a.scale ? a.scale + v * N : nullptr, s);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float hat = y[j] * r, g = l[i][j] * s[j];  // g: the gradient of n
+        float act = 1.f;
+        if (a.gate) {
+          const float sig = sigmoid<E>(z[j]);
+          act = z[j] * sig;
+          dz[j] = g * hat * w[j] * sig * fmaf(z[j], 1.f - sig, 1.f);
+        }
+        ds[i][j] = fmaf(l[i][j], hat * w[j] * act, ds[i][j]);
+        dw[i][j] = fmaf(g * act, hat, dw[i][j]);
+        l[i][j] = g * act * w[j];
+        along[i] = fmaf(l[i][j], y[j], along[i]);
+      }
+      if (a.dgate) row_of<E, uint4>(a.dgate, row, a.dgate_stride)[v] = narrow<E>(dz);
+    }
+    group_sums(a, along, part, slot_along);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v >= a.vecs) continue;
+      const float r = sq[i], c = along[i] * r * r * r / a.width;
+      float y[N];
+      widen<E>(own_vec(place(stage, 0, v)), y);
+#pragma unroll
+      for (int j = 0; j < N; ++j) l[i][j] = l[i][j] * r - y[j] * c;
+      row_of<E, uint4>(a.dy, row, a.dy_stride)[v] = narrow<E>(l[i]);
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (a.parts == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v >= a.vecs) continue;
+    float* to = a.parts + static_cast<int64_t>(blockIdx.x) * a.dim + v * N;
+    const int64_t next = static_cast<int64_t>(gridDim.x) * a.dim;
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      *reinterpret_cast<float4*>(to + j) = make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
+      *reinterpret_cast<float4*>(to + next + j) = make_float4(ds[i][j], ds[i][j + 1], ds[i][j + 2], ds[i][j + 3]);
+      *reinterpret_cast<float4*>(to + 2 * next + j) = make_float4(dn[i][j], dn[i][j + 1], dn[i][j + 2], dn[i][j + 3]);
+    }
+  }
+}
+
 template <class E>
 __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(Args a) {
   __shared__ float sums[kMaxGroups], along[kMaxGroups], slot[2][32];
@@ -478,25 +648,33 @@ __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(Args a) {
   }
 }
 
-// The blocks' sums joined in order: columns by 32 threads, blocks (and groups, for
-// w) by 8, whose sums are then added.
-__global__ void __launch_bounds__(256) norm_join_kernel(const float* parts, int blocks, int dim, int width, float* dw,
-                                                        float* ds, float* dn) {
-  __shared__ float sum[8][33];
+// The blocks' sums joined in order: columns by 32 threads, blocks (and groups, for w) by
+// 32 more, four on their way at a time, whose sums are then added.
+__global__ void __launch_bounds__(1024) norm_join_kernel(const float* parts, int blocks, int dim, int width, float* dw,
+                                                         float* ds, float* dn) {
+  __shared__ float sum[32][33];
   float* out = blockIdx.y == 0 ? dw : blockIdx.y == 1 ? ds : dn;
-  const int cols = blockIdx.y == 0 ? width : dim;
-  const int c = blockIdx.x * 32 + threadIdx.x;
+  const int cols = blockIdx.y == 0 ? width : dim, c = blockIdx.x * 32 + threadIdx.x;
   if (out == nullptr || static_cast<int>(blockIdx.x) * 32 >= cols) return;
-  const float* from = parts + static_cast<int64_t>(blockIdx.y) * blocks * dim;
+  // (a block's groups follow one another: place k is `cols` further than place k - 1)
+  const float* from = parts + static_cast<int64_t>(blockIdx.y) * blocks * dim + c;
+  const int n = blocks * (dim / cols);
   float s = 0.f;
-  if (c < cols)
-    for (int k = threadIdx.y; k < blocks; k += 8)
-      for (int e = c; e < dim; e += cols) s += from[static_cast<int64_t>(k) * dim + e];
+  if (c < cols) {
+    int k = threadIdx.y;
+    for (; k + 96 < n; k += 128) {
+      float x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[u] = from[static_cast<int64_t>(k + u * 32) * cols];
+      s += (x[0] + x[1]) + (x[2] + x[3]);
+    }
+    for (; k < n; k += 32) s += from[static_cast<int64_t>(k) * cols];
+  }
   sum[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y != 0 || c >= cols) return;
 #pragma unroll
-  for (int k = 1; k < 8; ++k) s += sum[k][threadIdx.x];
+  for (int k = 1; k < 32; ++k) s += sum[k][threadIdx.x];
   out[c] = s;
 }
 
@@ -507,6 +685,17 @@ int per_thread(int vecs, int most) {
   for (int per = 1; per <= most; per *= 2)
     if (vecs <= per * kThreads) return per;
   return 0;
+}
+
+int opt_in(const void* kernel, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+  if (bit != 0 && (done.load(std::memory_order_relaxed) & bit)) return ENGRAM_OK;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+  if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return ENGRAM_OK;
 }
 
 template <class E>
@@ -552,17 +741,27 @@ int launch_grad(Args a, float* dw, float* ds, float* dn, int sms, cudaStream_t s
     } else {
       set_vecs<E>(a);
       // two vectors a thread at most: the sums of four's columns would not fit the registers
-      const int per = std::min(2, per_thread(a.vecs, 4)), threads = ((a.vecs + per - 1) / per + 31) / 32 * 32;
-      const size_t smem = a.groups > 1 && a.vecs_log2 < 0 ? sizeof(float) * (a.vecs + a.groups) : 0;
-      if (per == 1) norm_grad_kernel<E, 1, kThreads><<<blocks, threads, smem, st>>>(a);
-      else if (threads <= kThreads) norm_grad_kernel<E, 2, kThreads><<<blocks, threads, smem, st>>>(a);
-      else norm_grad_kernel<E, 2, 2 * kThreads><<<blocks, threads, smem, st>>>(a);
+      const int per = a.vecs <= kRingThreads ? 1 : 2, threads = ((a.vecs + per - 1) / per + 31) / 32 * 32;
+      const size_t smem = a.groups > 1 && a.vecs_log2 < 0 ? static_cast<size_t>(a.vecs + a.groups + 3) / 4 * 16 : 0;
+      if (per == 2 && threads > kThreads) {
+        norm_grad_kernel<E, 2, 2 * kThreads><<<blocks, threads, smem, st>>>(a);
+      } else {
+        const size_t ring = smem + static_cast<size_t>(per == 1 ? kRing<1> : kRing<2>) * kArrays * a.vecs * 16;
+        auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
+          int r = opt_in(reinterpret_cast<const void*>(kernel), done);
+          if (r == ENGRAM_OK) kernel<<<blocks, threads, ring, st>>>(a);
+          return r;
+        };
+        static std::atomic<uint64_t> done[2] = {{0}, {0}};
+        int r = per == 1 ? go(norm_grad_ring_kernel<E, 1>, done[0]) : go(norm_grad_ring_kernel<E, 2>, done[1]);
+        if (r) return r;
+      }
     }
     int rc = check_launch("norm_grad_kernel");
     if (rc) return rc;
   }
   if (a.parts == nullptr) return ENGRAM_OK;
-  norm_join_kernel<<<dim3((a.dim + 31) / 32, 3), dim3(32, 8), 0, st>>>(a.parts, blocks, a.dim, a.width, dw, ds, dn);
+  norm_join_kernel<<<dim3((a.dim + 31) / 32, 3), dim3(32, 32), 0, st>>>(a.parts, blocks, a.dim, a.width, dw, ds, dn);
   return check_launch("norm_join_kernel");
 }
 
