@@ -40,7 +40,7 @@ struct Args {
   void *h_out, *x_out, *dy, *dgate, *dres;
   int64_t y_stride, gate_stride, h_stride, h_out_stride, x_stride, dh_stride, dx_stride, dy_stride, dgate_stride, dres_stride;
   const float *w, *scale, *w_next;
-  float* parts;  // [3][blocks][dim]: the sums for w, scale and w_next
+  float* parts;  // [2][blocks][dim]: the sums of l silu(gate) y r, for w and scale, and of dx h' r, for w_next
   int64_t rows;
   int32_t dim, groups, width;  // width: of a group
   int32_t vecs, vecs_log2;     // 16-byte vectors of a row; log2 of a group's if they are a power of two, else -1
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kMost) norm_grad_kernel(Args a) {
   extern __shared__ float part[];
   __shared__ float slot[4][32];
   const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-  float dw[kPer][N] = {}, ds[kPer][N] = {}, dn[kPer][N] = {};
+  float q[kPer][N] = {}, dn[kPer][N] = {};
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     uint4 ry[kPer], rz[kPer], rl[kPer], rh[kPer], rx[kPer];
 #pragma unroll
@@ -376,11 +376,10 @@ __global__ void __launch_bounds__(kMost) norm_grad_kernel(Args a) {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const float sig = a.gate ? sigmoid<E>(z[j]) : 1.f, act = a.gate ? z[j] * sig : 1.f;
-        const float hat = y[j] * r, g = l[i][j] * s[j];  // g: the gradient of n
-        ds[i][j] = fmaf(l[i][j], hat * w[j] * act, ds[i][j]);
-        dw[i][j] = fmaf(g * act, hat, dw[i][j]);
-        dz[j] = g * hat * w[j] * sig * fmaf(z[j], 1.f - sig, 1.f);
-        l[i][j] = g * act * w[j];
+        const float hat = y[j] * r, g = l[i][j] * s[j] * w[j];  // g: the gradient of y r silu(gate)
+        q[i][j] = fmaf(l[i][j] * act, hat, q[i][j]);
+        dz[j] = g * hat * sig * fmaf(z[j], 1.f - sig, 1.f);
+        l[i][j] = g * act;
         along[i] = fmaf(l[i][j], y[j], along[i]);
       }
       if (a.dgate) row_of<E, uint4>(a.dgate, row, a.dgate_stride)[v] = narrow<E>(dz);
@@ -407,9 +406,8 @@ __global__ void __launch_bounds__(kMost) norm_grad_kernel(Args a) {
     const int64_t next = static_cast<int64_t>(gridDim.x) * a.dim;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      to[j] = dw[i][j];
-      to[next + j] = ds[i][j];
-      to[2 * next + j] = dn[i][j];
+      to[j] = q[i][j];
+      to[next + j] = dn[i][j];
     }
   }
 }
@@ -425,20 +423,24 @@ __device__ __forceinline__ uint4 own_vec(uint32_t at) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
   return x;
 }
-template <int kPer>
-constexpr int kRing = kPer == 1 ? 3 : 2;  // rows of a block on their way or in use
-constexpr int kRingThreads = 640;  // of a vector each: 102 registers
+constexpr int kRing = 3;  // rows of a block in use, next, and on their way
+constexpr int kRingThreads = 640;
 constexpr int kArrays = 5;   // y, gate, dh, h', dx
-constexpr int kRingSmem = 200 * 1024;
+constexpr int kRingSmem = 220 * 1024;
 
 template <class E, int kPer>
 __global__ void __launch_bounds__(kPer == 1 ? kRingThreads : kThreads) norm_grad_ring_kernel(Args a) {
   constexpr int N = kVec<E>;
   extern __shared__ __align__(16) float part[];
-  __shared__ float slot[2][3][32], slot_along[32];
+  __shared__ float slot[2][4][32], slot_along[32];
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const uint32_t ring = smem_u32(part) + (a.groups > 1 && a.vecs_log2 < 0 ? (a.vecs + a.groups + 3) / 4 * 16 : 0);
-  auto place = [&](int stage, int array, int v) { return ring + ((stage * kArrays + array) * a.vecs + v) * 16; };
+  const uint32_t array_bytes = static_cast<uint32_t>(a.vecs) * 16;
+  auto place = [&](int stage, int array, int v) { return ring + (stage * kArrays + array) * array_bytes + v * 16; };
+  const float inv_dim = 1.f / a.dim, inv_width = 1.f / a.width;
+  const float* w_at[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) w_at[i] = a.w ? a.w + (threadIdx.x + i * blockDim.x) * N % a.width : nullptr;
   auto fetch = [&](int64_t row, int stage) {
     if (row < a.rows) {
 #pragma unroll
@@ -456,13 +458,8 @@ __global__ void __launch_bounds__(kPer == 1 ? kRingThreads : kThreads) norm_grad
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  float dw[kPer][N] = {}, ds[kPer][N] = {}, dn[kPer][N] = {};
-  for (int k = 0; k < kRing<kPer> - 1; ++k) fetch(blockIdx.x + static_cast<int64_t>(k) * gridDim.x, k);
-  int stage = 0, parity = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, stage = stage + 1 == kRing<kPer> ? 0 : stage + 1, parity ^= 1) {
-    fetch(row + static_cast<int64_t>(kRing<kPer> - 1) * gridDim.x, stage == 0 ? kRing<kPer> - 1 : stage - 1);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRing<kPer> - 1) : "memory");
-    float sq[kPer], l[kPer][N], sum[3] = {0.f, 0.f, 0.f};
+  // of a row: its sums of h'^2 and dx w_next h', and y^2 of the thread's vectors
+  auto first = [&](int stage, float (&sum)[4], float (&sq)[kPer]) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
@@ -485,27 +482,56 @@ __global__ void __launch_bounds__(kPer == 1 ? kRingThreads : kThreads) norm_grad
         }
       }
     }
-    // the block's three sums at one barrier
-#pragma unroll
-    for (int k = 0; k < 3; ++k) sum[k] = warp_sum(sum[k]);
+  };
+  // The block's four sums at one barrier.  A lane keeps half of what it has at each of
+  // the first two exchanges: eight lanes have one sum each, 6 exchanges and not 20.
+  int parity = 0;
+  const int mine = lane >> 3;
+  auto join = [&](float (&sum)[4]) {
+    const bool up = lane & 16, odd = lane & 8;
+    const float a0 = up ? sum[0] : sum[2], a1 = up ? sum[1] : sum[3];
+    float k0 = (up ? sum[2] : sum[0]) + __shfl_xor_sync(0xffffffffu, a0, 16);
+    float k1 = (up ? sum[3] : sum[1]) + __shfl_xor_sync(0xffffffffu, a1, 16);
+    float s = (odd ? k1 : k0) + __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 4);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
     if (warps > 1) {
-      float(&to)[3][32] = slot[parity];
-      if (lane == 0) {
-#pragma unroll
-        for (int k = 0; k < 3; ++k) to[k][threadIdx.x >> 5] = sum[k];
-      }
+      float(&to)[4][32] = slot[parity];
+      parity ^= 1;
+      if ((lane & 7) == 0) to[mine][threadIdx.x >> 5] = s;
       __syncthreads();
+      s = 0.f;
 #pragma unroll
-      for (int k = 0; k < 3; ++k) sum[k] = warp_sum(lane < warps ? to[k][lane] : 0.f);
+      for (int w = 0; w < 32; w += 8)
+        if (w + (lane & 7) < warps) s += to[mine][w + (lane & 7)];
+      s += __shfl_xor_sync(0xffffffffu, s, 4);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum[k] = __shfl_sync(0xffffffffu, s, k * 8);
+  };
+  // sums over the rows: l silu(gate) y r, of which dw and dscale are multiples by column, and dx h' r
+  float q[kPer][N] = {}, dn[kPer][N] = {};
+  for (int k = 0; k < kRing - 1; ++k) fetch(blockIdx.x + static_cast<int64_t>(k) * gridDim.x, k);
+  asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+  float sum[4] = {0.f, 0.f, 0.f, 0.f}, sq[kPer];
+  first(0, sum, sq);
+  join(sum);
+  int stage = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const int next = stage + 1 == kRing ? 0 : stage + 1;
+    fetch(row + static_cast<int64_t>(kRing - 1) * gridDim.x, stage == 0 ? kRing - 1 : stage - 1);
     if (a.groups == 1) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) sq[i] = sum[2];
     } else {
       group_sums(a, sq, part, slot_along);
     }
-    const float r2 = rsqrtf(sum[0] / a.dim + a.eps), c2 = sum[1] * r2 * r2 * r2 / a.dim;
-    float along[kPer];
+    const float r2 = rsqrtf(sum[0] * inv_dim + a.eps), c2 = sum[1] * r2 * r2 * r2 * inv_dim;
+    float along[kPer], l[kPer][N], r1[kPer];
+    float coming[4] = {0.f, 0.f, 0.f, 0.f};  // the next row's sums, and this one's of p y
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
@@ -530,41 +556,51 @@ __global__ void __launch_bounds__(kPer == 1 ? kRingThreads : kThreads) norm_grad
         }
       }
       if (a.dres) row_of<E, uint4>(a.dres, row, a.dres_stride)[v] = narrow<E>(l[i]);
-      const float r = rsqrtf(sq[i] / a.width + a.eps);
-      sq[i] = r;
+      r1[i] = rsqrtf(sq[i] * inv_width + a.eps);
       float y[N], z[N], w[N], s[N], dz[N];
       widen<E>(own_vec(place(stage, 0, v)), y);
       if (a.gate) widen<E>(own_vec(place(stage, 1, v)), z);
-      load_weights<E>(a.w ? a.w + v * N % a.width : nullptr, w);
+      load_weights<E>(w_at[i], w);
       load_weights<E>(a.scale ? a.scale + v * N : nullptr, s);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const float hat = y[j] * r, g = l[i][j] * s[j];  // g: the gradient of n
+        const float hat = y[j] * r1[i], g = l[i][j] * s[j] * w[j];  // g: the gradient of y r silu(gate)
         float act = 1.f;
         if (a.gate) {
           const float sig = sigmoid<E>(z[j]);
           act = z[j] * sig;
-          dz[j] = g * hat * w[j] * sig * fmaf(z[j], 1.f - sig, 1.f);
+          dz[j] = g * hat * sig * fmaf(z[j], 1.f - sig, 1.f);
         }
-        ds[i][j] = fmaf(l[i][j], hat * w[j] * act, ds[i][j]);
-        dw[i][j] = fmaf(g * act, hat, dw[i][j]);
-        l[i][j] = g * act * w[j];
+        q[i][j] = fmaf(l[i][j] * act, hat, q[i][j]);
+        l[i][j] = g * act;
         along[i] = fmaf(l[i][j], y[j], along[i]);
       }
+      coming[3] += along[i];
       if (a.dgate) row_of<E, uint4>(a.dgate, row, a.dgate_stride)[v] = narrow<E>(dz);
     }
-    group_sums(a, along, part, slot_along);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+    if (row + gridDim.x < a.rows) first(next, coming, sq);
+    join(coming);
+    if (a.groups == 1) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) along[i] = coming[3];
+    } else {
+      group_sums(a, along, part, slot_along);
+    }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= a.vecs) continue;
-      const float r = sq[i], c = along[i] * r * r * r / a.width;
+      const float r = r1[i], c = along[i] * r * r * r * inv_width;
       float y[N];
       widen<E>(own_vec(place(stage, 0, v)), y);
 #pragma unroll
       for (int j = 0; j < N; ++j) l[i][j] = l[i][j] * r - y[j] * c;
       row_of<E, uint4>(a.dy, row, a.dy_stride)[v] = narrow<E>(l[i]);
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum[k] = coming[k];
+    stage = next;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (a.parts == nullptr) return;
@@ -576,9 +612,8 @@ __global__ void __launch_bounds__(kPer == 1 ? kRingThreads : kThreads) norm_grad
     const int64_t next = static_cast<int64_t>(gridDim.x) * a.dim;
 #pragma unroll
     for (int j = 0; j < N; j += 4) {
-      *reinterpret_cast<float4*>(to + j) = make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
-      *reinterpret_cast<float4*>(to + next + j) = make_float4(ds[i][j], ds[i][j + 1], ds[i][j + 2], ds[i][j + 3]);
-      *reinterpret_cast<float4*>(to + 2 * next + j) = make_float4(dn[i][j], dn[i][j + 1], dn[i][j + 2], dn[i][j + 3]);
+      *reinterpret_cast<float4*>(to + j) = make_float4(q[i][j], q[i][j + 1], q[i][j + 2], q[i][j + 3]);
+      *reinterpret_cast<float4*>(to + next + j) = make_float4(dn[i][j], dn[i][j + 1], dn[i][j + 2], dn[i][j + 3]);
     }
   }
 }
@@ -588,7 +623,7 @@ __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(Args a) {
   __shared__ float sums[kMaxGroups], along[kMaxGroups], slot[2][32];
   const int64_t next = static_cast<int64_t>(gridDim.x) * a.dim;
   float* to = a.parts ? a.parts + static_cast<int64_t>(blockIdx.x) * a.dim : nullptr;
-  for (int e = threadIdx.x; to && e < a.dim; e += kAnyThreads) to[e] = to[next + e] = to[2 * next + e] = 0.f;
+  for (int e = threadIdx.x; to && e < a.dim; e += kAnyThreads) to[e] = to[next + e] = 0.f;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const auto* y = row_of<E>(a.y, row, a.y_stride);
     __syncthreads();  // the last row's sums are no longer read
@@ -635,11 +670,10 @@ __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(Args a) {
       at(e, l, p, sig, act, z);
       const float r = sums[g], v = E::load(y + e), hat = v * r, w = a.w ? a.w[e - g * a.width] : 1.f;
       if (to) {
-        to[e] = fmaf(p * act, hat, to[e]);
-        to[next + e] = fmaf(l, hat * w * act, to[next + e]);
+        to[e] = fmaf(l * act, hat, to[e]);
         if (a.dx)
-          to[2 * next + e] = fmaf(E::load(row_of<E>(a.dx, row, a.dx_stride) + e) * r2,
-                                  E::load(row_of<E>(a.h, row, a.h_stride) + e), to[2 * next + e]);
+          to[next + e] = fmaf(E::load(row_of<E>(a.dx, row, a.dx_stride) + e) * r2,
+                              E::load(row_of<E>(a.h, row, a.h_stride) + e), to[next + e]);
       }
       if (a.dres) E::store(row_of<E>(a.dres, row, a.dres_stride) + e, l);
       if (a.dgate) E::store(row_of<E>(a.dgate, row, a.dgate_stride) + e, p * hat * w * sig * fmaf(z, 1.f - sig, 1.f));
@@ -648,17 +682,17 @@ __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(Args a) {
   }
 }
 
-// The blocks' sums joined in order: columns by 32 threads, blocks (and groups, for w) by
+// The blocks' sums joined in order: columns by 32 threads, blocks (and for w groups) by
 // 32 more, four on their way at a time, whose sums are then added.
-__global__ void __launch_bounds__(1024) norm_join_kernel(const float* parts, int blocks, int dim, int width, float* dw,
-                                                         float* ds, float* dn) {
+__global__ void __launch_bounds__(1024) norm_join_kernel(Args a, int blocks, float* dw, float* ds, float* dn) {
   __shared__ float sum[32][33];
   float* out = blockIdx.y == 0 ? dw : blockIdx.y == 1 ? ds : dn;
-  const int cols = blockIdx.y == 0 ? width : dim, c = blockIdx.x * 32 + threadIdx.x;
+  const int cols = blockIdx.y == 0 ? a.width : a.dim, c = blockIdx.x * 32 + threadIdx.x;
   if (out == nullptr || static_cast<int>(blockIdx.x) * 32 >= cols) return;
   // (a block's groups follow one another: place k is `cols` further than place k - 1)
-  const float* from = parts + static_cast<int64_t>(blockIdx.y) * blocks * dim + c;
-  const int n = blocks * (dim / cols);
+  const float* from = a.parts + static_cast<int64_t>(blockIdx.y == 2 ? 1 : 0) * blocks * a.dim + c;
+  const int per = a.dim / cols, n = blocks * per;
+  const float* scale = blockIdx.y == 0 ? a.scale : nullptr;
   float s = 0.f;
   if (c < cols) {
     int k = threadIdx.y;
@@ -666,16 +700,20 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const float* parts, int
       float x[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) x[u] = from[static_cast<int64_t>(k + u * 32) * cols];
+      if (scale != nullptr) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] *= scale[(k + u * 32) % per * cols + c];
+      }
       s += (x[0] + x[1]) + (x[2] + x[3]);
     }
-    for (; k < n; k += 32) s += from[static_cast<int64_t>(k) * cols];
+    for (; k < n; k += 32) s += from[static_cast<int64_t>(k) * cols] * (scale != nullptr ? scale[k % per * cols + c] : 1.f);
   }
   sum[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y != 0 || c >= cols) return;
 #pragma unroll
   for (int k = 1; k < 32; ++k) s += sum[k][threadIdx.x];
-  out[c] = s;
+  out[c] = blockIdx.y == 1 && a.w != nullptr ? s * a.w[c % a.width] : s;
 }
 
 // -------------------------------------------------------------------- launch
@@ -734,7 +772,9 @@ int launch_norm(Args a, cudaStream_t st) {
 
 template <class E>
 int launch_grad(Args a, float* dw, float* ds, float* dn, int sms, cudaStream_t st) {
-  const int blocks = static_cast<int>(std::min<int64_t>(a.rows, std::min(kParts, 2 * sms)));
+  // two blocks an SM, or one where a block's rows take more than half of the shared memory
+  const int at_once = by_vectors<E>(a, true) && kRing * kArrays * static_cast<int64_t>(a.dim) * E::kBytes > 112 * 1024 ? 1 : 2;
+  const int blocks = static_cast<int>(std::min<int64_t>(a.rows, std::min(kParts, at_once * sms)));
   if (blocks > 0) {
     if (!by_vectors<E>(a, true)) {
       norm_grad_any_kernel<E><<<blocks, kAnyThreads, 0, st>>>(a);
@@ -743,10 +783,10 @@ int launch_grad(Args a, float* dw, float* ds, float* dn, int sms, cudaStream_t s
       // two vectors a thread at most: the sums of four's columns would not fit the registers
       const int per = a.vecs <= kRingThreads ? 1 : 2, threads = ((a.vecs + per - 1) / per + 31) / 32 * 32;
       const size_t smem = a.groups > 1 && a.vecs_log2 < 0 ? static_cast<size_t>(a.vecs + a.groups + 3) / 4 * 16 : 0;
-      if (per == 2 && threads > kThreads) {
+      const size_t ring = smem + static_cast<size_t>(kRing) * kArrays * a.vecs * 16;
+      if (ring > kRingSmem) {
         norm_grad_kernel<E, 2, 2 * kThreads><<<blocks, threads, smem, st>>>(a);
       } else {
-        const size_t ring = smem + static_cast<size_t>(per == 1 ? kRing<1> : kRing<2>) * kArrays * a.vecs * 16;
         auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
           int r = opt_in(reinterpret_cast<const void*>(kernel), done);
           if (r == ENGRAM_OK) kernel<<<blocks, threads, ring, st>>>(a);
@@ -761,7 +801,7 @@ int launch_grad(Args a, float* dw, float* ds, float* dn, int sms, cudaStream_t s
     if (rc) return rc;
   }
   if (a.parts == nullptr) return ENGRAM_OK;
-  norm_join_kernel<<<dim3((a.dim + 31) / 32, 3), dim3(32, 32), 0, st>>>(a.parts, blocks, a.dim, a.width, dw, ds, dn);
+  norm_join_kernel<<<dim3((a.dim + 31) / 32, 3), dim3(32, 32), 0, st>>>(a, blocks, dw, ds, dn);
   return check_launch("norm_join_kernel");
 }
 
@@ -835,7 +875,7 @@ extern "C" int engram_norm_add(const void* y_d, int64_t y_stride, const void* ga
 
 extern "C" size_t engram_norm_add_workspace_bytes(int64_t n_rows, int32_t dim) {
   if (n_rows < 0 || dim < 1) return 0;
-  return sizeof(float) * 3 * static_cast<size_t>(std::min<int64_t>(n_rows, kParts)) * dim;
+  return sizeof(float) * 2 * static_cast<size_t>(std::min<int64_t>(n_rows, kParts)) * dim;
 }
 
 extern "C" int engram_norm_add_grad(const void* dh_d, int64_t dh_stride, const void* dx_d, int64_t dx_stride,

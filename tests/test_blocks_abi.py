@@ -46,7 +46,7 @@ def test_norm_add(lib):
 
 def test_norm_add_grad(lib):
     need = lib.engram_norm_add_workspace_bytes(4, 8)
-    assert need == 3 * 4 * 8 * 4 and lib.engram_norm_add_workspace_bytes(-1, 8) == 0
+    assert need == 2 * 4 * 8 * 4 and lib.engram_norm_add_workspace_bytes(-1, 8) == 0
     assert lib.engram_norm_add_workspace_bytes(10 ** 9, 8) == lib.engram_norm_add_workspace_bytes(10 ** 6, 8)
 
     def call(dh=P(16), dx=P(16), y=P(16), gate=P(16), out=P(16), ty=F32, n=4, D=8, G=2, dy=P(16), dgate=P(16), dres=P(32),
