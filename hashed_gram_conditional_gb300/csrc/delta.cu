@@ -291,68 +291,50 @@ template int launch_prepare<train::F32>(const Args<train::F32>&, cudaStream_t);
 
 // --------------------------------------------------------------------- scan
 
-// A warp follows one sequence in one head, for 16 of the value columns; a block's W
-// warps share the chunks' inputs.  The state is held transposed, S^T [16][dk], as an
-// accumulator, which is the next product's operand as it lies in the registers: so are
-// X^T = V^T - e^c (K S)^T, U^T = X^T M^T and what is added to S^T.  Nothing but the
-// inputs goes through shared memory, and a chunk needs one barrier, for their copies.
-// Bound by the tensor cores: 692 instructions of 2048 multiply-adds a warp and chunk
-// (dk = 128), of which 192 + 120 + 192 are on the state's way, in three terms.
-template <class E, int KD, int W>
-struct ScanRows {
-  static constexpr int kStages = E::kBytes == 2 ? 2 : 1;
+// A chunk in a quad (16 value columns, dk = 128) is 48 + 32 + 48 + 24 + 48 tensor
+// instructions a warp at most: K S and U and what is added to S in three terms, Q S and
+// P U in two.  bf16: the next chunk's inputs are copied meanwhile; fp32's terms are made
+// on the way to shared memory and take the room.
+template <class E, int KD, int NQ>
+struct Scan {
+  static constexpr int kT = NQ * 128, kStages = E::kBytes == 2 ? 2 : 1, kB = kC / 16;
   static constexpr int kK = 0, kQ = kK + kIn<E> * mat_bytes(kC, KD), kV = kQ + kIn<E> * mat_bytes(kC, KD);
-  static constexpr int kM = kV + kIn<E> * mat_bytes(kC, 16 * W), kP = kM + kStateTerms * kTerm, kG = kP + kOut<E> * kTerm;
-  static constexpr int kStage = kG + static_cast<int>(sizeof(Gates));
-  static constexpr int kSmem = kStages * kStage;
+  static constexpr int kM = kV + kIn<E> * mat_bytes(kC, 16 * NQ), kP = kM + kStateTerms * kTerm, kG = kP + kOut<E> * kTerm;
+  static constexpr int kStage = kG + static_cast<int>(sizeof(Gates)), kQuads = kStages * kStage;
+  // a quad's operands: S^T; X^T, then in its place (e^(c_last - c) U)^T; U^T
+  static constexpr int kX = KD / 16 * kStateTerms * 512, kU = kX + kB * kStateTerms * 512;
+  static constexpr int kQuad = kU + kB * kOut<E> * 512;
+  static constexpr int kSmem = kQuads + NQ * kQuad;
 };
 
-// c += A B, A 16 of the positions from block ib on, B a triangle's blocks (ib, tb >= ib).
-template <int TA, int TB, int kLimit>
-__device__ __forceinline__ void below(float (&c)[kC / 8][4], float (&s)[kC / 8][4], const uint32_t (&fa)[TA][4],
-                                      const TriAcross& b, int ib) {
-#pragma unroll
-  for (int j = 0; j < TB; ++j) {
-    uint32_t fb[kC / 16][2][2];
-#pragma unroll
-    for (int tb = 0; tb < kC / 16; ++tb)
-      if (tb >= ib) b.get(fb[tb], ib, tb, j);
-#pragma unroll
-    for (int i = 0; i < TA; ++i)
-      if (i + j < kLimit) {
-#pragma unroll
-        for (int t = 0; t < kC / 8; ++t)
-          if (t >= 2 * ib) mma(kLimit > 2 && i + j > 0 ? s[t] : c[t], fa[i], fb[t >> 1][t & 1][0], fb[t >> 1][t & 1][1]);
-      }
-  }
-}
-
-template <class E, int KD, int W>
-__global__ void __launch_bounds__(W * 32, 1) scan_rows_kernel(Args<E> a) {
-  using L = ScanRows<E, KD, W>;
-  constexpr int kT = W * 32, kI = kIn<E>, kO = kOut<E>, kS = kStateTerms;
+template <class E, int KD, int NQ>
+__global__ void __launch_bounds__(NQ * 128, 1) scan_kernel(Args<E> a) {
+  using L = Scan<E, KD, NQ>;
+  constexpr int kT = L::kT, kI = kIn<E>, kO = kOut<E>, kS = kStateTerms, kB = L::kB, kR = KD / 64;  // kR: a warp's blocks of S^T
   extern __shared__ __align__(128) unsigned char smem[];
   const uint32_t base = smem_u32(smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
-  const int seq = blockIdx.x, h = blockIdx.y, v0 = blockIdx.z * (16 * W), cols = min(a.dv - v0, 16 * W);
-  const int hk = h / (a.heads / a.keys), vw = v0 + warp * 16;  // vw: the warp's first column
+  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t2 = (lane & 3) * 2;
+  const int quad = tid >> 7, w = ((tid >> 5) + quad) & 3;  // w: the warp's quarter
+  const int seq = blockIdx.x, h = blockIdx.y, v0 = blockIdx.z * (16 * NQ), cols = min(a.dv - v0, 16 * NQ);
+  const int hk = h / (a.heads / a.keys), vw = v0 + quad * 16;
   int lo, hi;
   bounds(a, seq, lo, hi);
   const int c0 = a.first[seq], n = min((hi - lo + kC - 1) / kC, a.max_chunks - c0);
-  const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
+  const size_t matrix = static_cast<size_t>(a.dk) * a.dv, saved = saved_floats<E>(a.dk, a.dv);
   int64_t slot;
   if (!live_slot(a, seq, slot)) {
     if (tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
     padding_zeros(a, lo, hi, c0, n, h, v0, cols, kT);
     return;
   }
-  float S[KD / 8][4];  // (column vw + g, or 8 further; row of the state)
-  auto each = [&](auto f) {
+  const uint32_t own = base + L::kQuads + quad * L::kQuad;
+  float S[2 * kR][4];
+  auto each = [&](auto f) {  // f(tile, place, the element's place in a state)
 #pragma unroll
-    for (int t = 0; t < KD / 8; ++t)
+    for (int t = 0; t < 2 * kR; ++t)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int v = vw + g + (j >> 1) * 8, k = t * 8 + t2 + (j & 1);
+        const int v = vw + g + (j >> 1) * 8, k = w * kR * 16 + t * 8 + t2 + (j & 1);
         if (v < a.dv && k < a.dk) f(t, j, static_cast<size_t>(k) * a.dv + v);
       }
   };
@@ -361,6 +343,19 @@ __global__ void __launch_bounds__(W * 32, 1) scan_rows_kernel(Args<E> a) {
     const float* from = a.state + (slot * a.heads + h) * matrix;
     each([&](int t, int j, size_t at) { S[t][j] = from[at]; });
   }
+  auto hand_state = [&](int i) {  // the state in front of chunk i
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const int kb = w * kR + r;
+      uint32_t f[kS][4];
+      as_operand<kS>(f, S[2 * r], S[2 * r + 1]);
+      hand<kS>(own + kb * (kS * 512), f);
+      if (a.carry == nullptr || vw >= a.dv || kb * 16 >= a.dk) continue;
+      float* to = a.carry + unit_of(a, c0 + i, h) * saved;
+      if constexpr (E::kBytes == 2) save_block(block_of(to, a.dk, vw >> 4, kb), f);
+      else save_rows(to, a.dk, a.dv, vw, kb * 16, S[2 * r], S[2 * r + 1]);
+    }
+  };
   auto load = [&](int i) {
     const uint32_t stage = base + (i % L::kStages) * L::kStage;
     const int64_t p = lo + static_cast<int64_t>(i) * kC;
@@ -369,266 +364,150 @@ __global__ void __launch_bounds__(W * 32, 1) scan_rows_kernel(Args<E> a) {
     const size_t unit = unit_of(a, c0 + i, h);
     load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kK), a.k + p * a.k_stride + hk * a.dk, a.k_stride, len, a.dk, mask, a.vec);
     load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kQ), a.q + p * a.q_stride + hk * a.dk, a.q_stride, len, a.dk, mask, a.vec);
-    load_rows<E, 16 * W, kT>(mat<kC, 16 * W>(stage + L::kV), a.v + p * a.v_stride + h * a.dv + v0, a.v_stride, len, cols, mask,
-                             a.vec);
+    load_rows<E, 16 * NQ, kT>(mat<kC, 16 * NQ>(stage + L::kV), a.v + p * a.v_stride + static_cast<int64_t>(h) * a.dv + v0,
+                              a.v_stride, len, cols, mask, a.vec);
     load_tri<kO, kT>(stage + L::kM, stage + L::kP, a.tri + unit * kTriBytes);
     load_gates<kT>(stage + L::kG, a.gates + unit);
     copies_begun();
   };
-  if (n > 0) load(0);
+  if (n > 0) {
+    hand_state(0);
+    load(0);
+  }
   for (int i = 0; i < n; ++i) {
     const uint32_t stage = base + (i % L::kStages) * L::kStage;
-    const Mat K = mat<kC, KD>(stage + L::kK), Q = mat<kC, KD>(stage + L::kQ), V = mat<kC, 16 * W>(stage + L::kV);
+    const Mat K = mat<kC, KD>(stage + L::kK), Q = mat<kC, KD>(stage + L::kQ), V = mat<kC, 16 * NQ>(stage + L::kV);
     const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
     copies_done();
-    __syncthreads();  // the chunk is here, and the other stage is free
+    __syncthreads();  // the chunk and the states are here, and the other stage is free
     if (L::kStages == 2 && i + 1 < n) load(i + 1);
-    float* kept = a.carry != nullptr && vw < a.dv ? a.carry + unit_of(a, c0 + i, h) * saved_floats<E>(a.dk, a.dv) : nullptr;
     // ---- (K S)^T and (Q S)^T
-    float x[kC / 8][4], s[kC / 8][4], y[kC / 8][4];
-    clear(x);
-    clear(s);
-    clear(y);
-#pragma unroll
+    Sums<2, true> x;
+    Sums<2, kO == 3> y;
+    x.clear_all();
+    y.clear_all();
+#pragma unroll 4
     for (int kb = 0; kb < KD / 16; ++kb) {
       uint32_t fa[kS][4];
-      as_operand<kS>(fa, S[2 * kb], S[2 * kb + 1]);
-      if (kept != nullptr && kb * 16 < a.dk) save_block(block_of(kept, a.dk, vw >> 4, kb), fa);
+      take<kS>(own + kb * (kS * 512), fa);
 #pragma unroll
       for (int j = 0; j < kI; ++j) {
-        uint32_t fb[kC / 16][2][2];
+        uint32_t fk[2][2], fq[2][2];
+        Across{K}.get<2>(fk, kb * 16, w * 16, j);
+        Across{Q}.get<2>(fq, kb * 16, w * 16, j);
 #pragma unroll
-        for (int cb = 0; cb < kC / 16; ++cb) Across{K}.get<2>(fb[cb], kb * 16, cb * 16, j);
-        pairs_product<kS, kS, kC / 16>(x, s, fa, fb, j);
-#pragma unroll
-        for (int cb = 0; cb < kC / 16; ++cb) Across{Q}.get<2>(fb[cb], kb * 16, cb * 16, j);
-        const uint32_t(&fo)[kO][4] = reinterpret_cast<const uint32_t(&)[kO][4]>(fa);
-        pairs_product<kO, kO, kC / 16>(y, y, fo, fb, j);
+        for (int e = 0; e < kS; ++e) {
+          if (e + j < kS) x.add(e, j, fa[e], fk);
+          if (e + j < kO) y.add(e, j, fa[e], fq);
+        }
       }
     }
-    // ---- X^T
-#pragma unroll
-    for (int cb = 0; cb < kC / 16; ++cb) {
-      float v[8] = {};
+    // ---- X^T, of the warp's positions: rows w * 16 + t2 (+ 1, + 8), columns vw + g (+ 8)
+    {
+      float c[2][4];
+      clear(c);
 #pragma unroll
       for (int j = kI - 1; j >= 0; --j) {
         uint32_t f[4];
-        Cols{V}(f, warp * 16, cb * 16, j);
+        Cols{V}(f, quad * 16, w * 16, j);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          v[2 * p] += lo_of(f[p]);
-          v[2 * p + 1] += hi_of(f[p]);
+        for (int q = 0; q < 4; ++q) {
+          c[q >> 1][(q & 1) * 2] += lo_of(f[q]);
+          c[q >> 1][(q & 1) * 2 + 1] += hi_of(f[q]);
         }
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 into = *reinterpret_cast<const float2*>(&gt.into[cb * 16 + e * 8 + t2]);
-        float(&c)[4] = x[2 * cb + e];
-        const float(&d)[4] = s[2 * cb + e];
-        c[0] = fmaf(-into.x, c[0] + d[0], v[4 * e]);
-        c[1] = fmaf(-into.y, c[1] + d[1], v[4 * e + 1]);
-        c[2] = fmaf(-into.x, c[2] + d[2], v[4 * e + 2]);
-        c[3] = fmaf(-into.y, c[3] + d[3], v[4 * e + 3]);
-        float(&o)[4] = y[2 * cb + e];
-        o[0] *= a.scale * into.x;
-        o[1] *= a.scale * into.y;
-        o[2] *= a.scale * into.x;
-        o[3] *= a.scale * into.y;
+      for (int t = 0; t < 2; ++t) {
+        const float2 into = *reinterpret_cast<const float2*>(&gt.into[w * 16 + t * 8 + t2]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float f = j & 1 ? into.y : into.x;
+          c[t][j] = fmaf(-f, x.sum(t, j), c[t][j]);
+          y.main[t][j] = y.sum(t, j) * (a.scale * f);
+        }
       }
+      if constexpr (kO == 3) {
+        clear(y.small[0]);
+        clear(y.small[1]);
+      }
+      uint32_t f[kS][4];
+      as_operand<kS>(f, c[0], c[1]);
+      hand<kS>(own + L::kX + w * (kS * 512), f);
     }
+    quad_sync(quad);
     // ---- U^T
-    float u[kC / 8][4];
-    clear(u);
-    clear(s);
-#pragma unroll
-    for (int ib = 0; ib < kC / 16; ++ib) {
+    x.clear_all();
+    for (int ib = 0; ib <= w; ++ib) {
       uint32_t fa[kS][4];
-      as_operand<kS>(fa, x[2 * ib], x[2 * ib + 1]);
-      below<kS, kS, kS>(u, s, fa, TriAcross{stage + L::kM}, ib);
+      take<kS>(own + L::kX + ib * (kS * 512), fa);
+#pragma unroll
+      for (int j = 0; j < kS; ++j) {
+        uint32_t fb[2][2];
+        TriAcross{stage + L::kM}.get(fb, ib, w, j);
+        terms<kS, kS>(x, fa, fb, j);
+      }
     }
+    {
+      float u[2][4];
 #pragma unroll
-    for (int t = 0; t < kC / 8; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) u[t][j] += s[t][j];
-    // ---- Y^T
+        for (int j = 0; j < 4; ++j) u[t][j] = x.sum(t, j);
+      uint32_t f[kO][4], fl[kS][4];
+      as_operand<kO>(f, u[0], u[1]);
+      hand<kO>(own + L::kU + w * (kO * 512), f);
 #pragma unroll
-    for (int ib = 0; ib < kC / 16; ++ib) {
-      uint32_t fa[kO][4];
-      as_operand<kO>(fa, u[2 * ib], u[2 * ib + 1]);
-      below<kO, kO, kO>(y, y, fa, TriAcross{stage + L::kP}, ib);
+      for (int t = 0; t < 2; ++t) {
+        const float2 last = *reinterpret_cast<const float2*>(&gt.last[w * 16 + t * 8 + t2]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[t][j] *= j & 1 ? last.y : last.x;
+      }
+      as_operand<kS>(fl, u[0], u[1]);
+      quad_sync(quad);  // X^T is no longer needed
+      hand<kS>(own + L::kX + w * (kS * 512), fl);
     }
-    const int64_t p = lo + static_cast<int64_t>(i) * kC;
-    const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
-    store_rows<E>(a.y + p * a.y_stride + h * a.dv, a.y_stride, len, vw, a.dv, a.pairs, gt.beta, y);
+    quad_sync(quad);
     // ---- S^T
-    uint32_t fa[kC / 16][kS][4];
+    {
+      const float total = gt.into[kC - 1];
+      Sums<2 * kR, true> d;
+      d.clear_all();
 #pragma unroll
-    for (int cb = 0; cb < kC / 16; ++cb) {
+      for (int cb = 0; cb < kB; ++cb) {
+        uint32_t fa[kS][4];
+        take<kS>(own + L::kX + cb * (kS * 512), fa);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 last = *reinterpret_cast<const float2*>(&gt.last[cb * 16 + e * 8 + t2]);
-        float(&c)[4] = u[2 * cb + e];
-        c[0] *= last.x;
-        c[1] *= last.y;
-        c[2] *= last.x;
-        c[3] *= last.y;
+        for (int j = 0; j < kI; ++j) {
+          uint32_t fb[2 * kR][2];
+          Down{K}.get<2 * kR>(fb, cb * 16, w * kR * 16, j);
+          terms<kS, kS>(d, fa, fb, j);
+        }
       }
-      as_operand<kS>(fa[cb], u[2 * cb], u[2 * cb + 1]);
+#pragma unroll
+      for (int t = 0; t < 2 * kR; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) S[t][j] = fmaf(S[t][j], total, d.sum(t, j));
     }
-    add_outer<E, KD>(S, gt.into[kC - 1], fa, K);
-    if (L::kStages == 1 && i + 1 < n) {
-      __syncthreads();  // the stage is free
-      load(i + 1);
+    if (i + 1 < n) hand_state(i + 1);
+    // ---- Y^T
+    for (int ib = 0; ib <= w; ++ib) {
+      uint32_t fa[kO][4];
+      take<kO>(own + L::kU + ib * (kO * 512), fa);
+#pragma unroll
+      for (int j = 0; j < kO; ++j) {
+        uint32_t fb[2][2];
+        TriAcross{stage + L::kP}.get(fb, ib, w, j);
+        terms<kO, kO>(y, fa, fb, j);
+      }
     }
-  }
-  if (a.state_out != nullptr) {
-    float* to = a.state_out + (slot * a.heads + h) * matrix;
-    each([&](int t, int j, size_t at) { to[at] = S[t][j]; });
-  }
-}
-
-// -------------------------------------------- scan of few sequences and heads
-
-// A block follows one sequence's chunks in one head, for kVS of the value columns.
-// The state stays in registers as the products' accumulator; its terms go to shared
-// memory, where they are an operand.  The next chunk's inputs are copied meanwhile
-// (bf16; fp32's terms are made on the way to shared memory and take the room).
-template <class E, int KD, int VS>
-struct Scan {
-  static constexpr int kStages = E::kBytes == 2 ? 2 : 1;
-  static constexpr int kQ = 0, kK = kQ + kIn<E> * mat_bytes(kC, KD), kV = kK + kIn<E> * mat_bytes(kC, KD);
-  static constexpr int kM = kV + kIn<E> * mat_bytes(kC, VS), kP = kM + kStateTerms * kTerm, kG = kP + kOut<E> * kTerm;
-  static constexpr int kStage = kG + static_cast<int>(sizeof(Gates));
-  static constexpr int kS = kStages * kStage;                         // the state
-  static constexpr int kX = kS + kStateTerms * mat_bytes(KD, VS);     // V - e^c K S, then e^(c_last - c) U
-  static constexpr int kU = kX + kStateTerms * mat_bytes(kC, VS);
-  static constexpr int kSmem = kU + kOut<E> * mat_bytes(kC, VS);
-  static constexpr int kAcross = kWarps / (KD / 16);  // warps that share 16 rows of the state
-  static constexpr int kN = VS / 16;                  // a warp's tiles of 8 columns of a chunk's rows
-  static constexpr int kSN = VS / 8 / kAcross;        // and of the state's
-};
-
-template <class E, int KD, int VS>
-__global__ void __launch_bounds__(kThreads, 1) scan_kernel(Args<E> a) {
-  using L = Scan<E, KD, VS>;
-  extern __shared__ __align__(128) unsigned char smem[];
-  const uint32_t base = smem_u32(smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
-  const int seq = blockIdx.x, h = blockIdx.y, v0 = blockIdx.z * VS, cols = a.dv - v0 < VS ? a.dv - v0 : VS;
-  const int hk = h / (a.heads / a.keys);
-  int lo, hi;
-  bounds(a, seq, lo, hi);
-  const int c0 = a.first[seq], n = min((hi - lo + kC - 1) / kC, a.max_chunks - c0);
-  int64_t slot;
-  const bool live = live_slot(a, seq, slot);
-  if (!live && tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
-  const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
-  if (!live) {
-    padding_zeros(a, lo, hi, c0, n, h, v0, cols, kThreads);
-    return;
-  }
-  // the rows and columns of the state that this thread holds
-  const int sm = warp % (KD / 16) * 16, sn = warp / (KD / 16) * (L::kSN * 8);
-  auto each = [&](auto f) {  // f(accumulator's tile and place, row, column)
+    float out[2][4];
 #pragma unroll
-    for (int t = 0; t < L::kSN; ++t)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = sm + g + (j >> 1) * 8, c = sn + t * 8 + t2 + (j & 1);
-        if (r < a.dk && c < cols) f(t, j, static_cast<size_t>(r) * a.dv + v0 + c);
-      }
-  };
-  float S[L::kSN][4];
-  clear(S);
-  if (a.state != nullptr) {
-    const float* from = a.state + (slot * a.heads + h) * matrix;
-    each([&](int t, int j, size_t at) { S[t][j] = from[at]; });
-  }
-  const Mat St = mat<KD, VS>(base + L::kS), X = mat<kC, VS>(base + L::kX), U = mat<kC, VS>(base + L::kU);
-  auto keep = [&]() {
-#pragma unroll
-    for (int t = 0; t < L::kSN; ++t)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        put<kStateTerms>(St.base + (sm + g + j * 8) * St.pitch + (sn + t * 8 + t2) * 2, St.term, S[t][2 * j], S[t][2 * j + 1]);
-  };
-  auto load = [&](int i) {
-    const uint32_t stage = base + (i % L::kStages) * L::kStage;
+      for (int j = 0; j < 4; ++j) out[t][j] = y.sum(t, j);
     const int64_t p = lo + static_cast<int64_t>(i) * kC;
-    const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
-    const uint8_t* mask = a.mask != nullptr ? a.mask + p : nullptr;
-    const size_t unit = unit_of(a, c0 + i, h);
-    load_rows<E, KD>(mat<kC, KD>(stage + L::kK), a.k + p * a.k_stride + hk * a.dk, a.k_stride, len, a.dk, mask, a.vec);
-    load_rows<E, KD>(mat<kC, KD>(stage + L::kQ), a.q + p * a.q_stride + hk * a.dk, a.q_stride, len, a.dk, mask, a.vec);
-    load_rows<E, VS>(mat<kC, VS>(stage + L::kV), a.v + p * a.v_stride + h * a.dv + v0, a.v_stride, len, cols, mask, a.vec);
-    load_tri<kOut<E>>(stage + L::kM, stage + L::kP, a.tri + unit * kTriBytes);
-    load_gates(stage + L::kG, a.gates + unit);
-    copies_begun();
-  };
-  keep();
-  if (n > 0) load(0);
-  const int m = (warp & 3) * 16, nn = (warp >> 2) * (VS / 2);  // the warp's tile of a chunk's rows
-  for (int i = 0; i < n; ++i) {
-    const uint32_t stage = base + (i % L::kStages) * L::kStage;
-    const Mat K = mat<kC, KD>(stage + L::kK), Q = mat<kC, KD>(stage + L::kQ), V = mat<kC, VS>(stage + L::kV);
-    const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
-    copies_done();
-    __syncthreads();  // the chunk and the state are here, and the other stage is free
-    if (L::kStages == 2 && i + 1 < n) load(i + 1);
-    if (a.carry != nullptr)
-      save_tile<E, L::kSN>(a, a.carry + unit_of(a, c0 + i, h) * saved_floats<E>(a.dk, a.dv), S, sm, v0 + sn);
-    float x[L::kN][4], y[L::kN][4];
-    clear(x);
-    clear(y);
-    product<kIn<E>, kStateTerms, kStateTerms>(x, Rows{K}, Down{St}, m, nn, 0, KD);
-    product<kIn<E>, kOut<E>, kOut<E>>(y, Rows{Q}, Down{St}, m, nn, 0, KD);
-#pragma unroll
-    for (int t = 0; t < L::kN; ++t)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = m + g + j * 8, c = nn + t * 8 + t2;
-        float v[2];
-        get<kIn<E>>(V.base + r * V.pitch + c * 2, V.term, v[0], v[1]);
-        const float into = gt.into[r];
-        put<kStateTerms>(X.base + r * X.pitch + c * 2, X.term, fmaf(-into, x[t][2 * j], v[0]), fmaf(-into, x[t][2 * j + 1], v[1]));
-        y[t][2 * j] *= a.scale * into;
-        y[t][2 * j + 1] *= a.scale * into;
-      }
-    __syncthreads();
-    float u[L::kN][4];
-    clear(u);
-    product<kStateTerms, kStateTerms, kStateTerms>(u, TriRows{stage + L::kM}, Down{X}, m, nn, 0, m + 16);
-    __syncthreads();  // X is free
-#pragma unroll
-    for (int t = 0; t < L::kN; ++t)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = m + g + j * 8, c = nn + t * 8 + t2;
-        const float last = gt.last[r];
-        put<kOut<E>>(U.base + r * U.pitch + c * 2, U.term, u[t][2 * j], u[t][2 * j + 1]);
-        put<kStateTerms>(X.base + r * X.pitch + c * 2, X.term, last * u[t][2 * j], last * u[t][2 * j + 1]);
-      }
-    __syncthreads();
-    const float total = gt.into[kC - 1];
-#pragma unroll
-    for (int t = 0; t < L::kSN; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) S[t][j] *= total;
-    product<kIn<E>, kStateTerms, kStateTerms>(S, Cols{K}, Down{X}, sm, sn, 0, kC);
-    keep();
-    product<kOut<E>, kOut<E>, kOut<E>>(y, TriRows{stage + L::kP}, Down{U}, m, nn, 0, m + 16);
-    const int64_t p = lo + static_cast<int64_t>(i) * kC;
-#pragma unroll
-    for (int t = 0; t < L::kN; ++t)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = m + g + j * 8, c = nn + t * 8 + t2;
-        if (p + r >= hi) continue;
-        const bool on = gt.beta[r] != 0.f;  // a masked position gives 0
-        auto* to = a.y + (p + r) * a.y_stride + h * a.dv + v0 + c;
-        if (c < cols) E::store(to, on ? y[t][2 * j] : 0.f);
-        if (c + 1 < cols) E::store(to + 1, on ? y[t][2 * j + 1] : 0.f);
-      }
+    store_rows<E>(a.y + p * a.y_stride + static_cast<int64_t>(h) * a.dv, a.y_stride, w * 16,
+                  hi - p < kC ? static_cast<int>(hi - p) : kC, vw, a.dv, a.pairs, gt.beta, out);
     if (L::kStages == 1 && i + 1 < n) {
       __syncthreads();  // the stage is free
       load(i + 1);
@@ -642,27 +521,21 @@ __global__ void __launch_bounds__(kThreads, 1) scan_kernel(Args<E> a) {
 
 template <class E>
 int launch_scan(const Args<E>& a, int sms, cudaStream_t st) {
-  static std::atomic<uint64_t> done[2] = {{0}, {0}};
-  auto go = [&](auto kernel, int smem, int vs, std::atomic<uint64_t>& flag) {
+  auto go = [&](auto kernel, int smem, int nq, std::atomic<uint64_t>& flag) {
     int r = opt_in(reinterpret_cast<const void*>(kernel), smem, flag);
     if (r) return r;
-    kernel<<<dim3(a.n_seqs, a.heads, (a.dv + vs - 1) / vs), kThreads, smem, st>>>(a);
+    kernel<<<dim3(a.n_seqs, a.heads, (a.dv + 16 * nq - 1) / (16 * nq)), nq * 128, smem, st>>>(a);
     return check_launch("scan_kernel");
   };
-  if constexpr (E::kBytes == 2) if (by_warps(a, sms)) {
-    auto rows = [&](auto kernel, int smem, int w, std::atomic<uint64_t>& flag) {
-      int r = opt_in(reinterpret_cast<const void*>(kernel), smem, flag);
-      if (r) return r;
-      kernel<<<dim3(a.n_seqs, a.heads, (a.dv + 16 * w - 1) / (16 * w)), w * 32, smem, st>>>(a);
-      return check_launch("scan_rows_kernel");
-    };
-    static std::atomic<uint64_t> flags[2] = {{0}, {0}};
-    return a.dk <= 64 ? rows(scan_rows_kernel<E, 64, 8>, ScanRows<E, 64, 8>::kSmem, 8, flags[0])
-                      : rows(scan_rows_kernel<E, 128, 8>, ScanRows<E, 128, 8>::kSmem, 8, flags[1]);
-  }
-  return a.dk <= 64 ? go(scan_kernel<E, 64, 16>, Scan<E, 64, 16>::kSmem, 16, done[0])
-                    : go(scan_kernel<E, 128, 16>, Scan<E, 128, 16>::kSmem, 16, done[1]);
+  static std::atomic<uint64_t> done[4] = {{0}, {0}, {0}, {0}};
+  if constexpr (E::kBytes == 2)
+    if (many_quads(a, sms))
+      return a.dk <= 64 ? go(scan_kernel<E, 64, 4>, Scan<E, 64, 4>::kSmem, 4, done[0])
+                        : go(scan_kernel<E, 128, 4>, Scan<E, 128, 4>::kSmem, 4, done[1]);
+  return a.dk <= 64 ? go(scan_kernel<E, 64, 1>, Scan<E, 64, 1>::kSmem, 1, done[2])
+                    : go(scan_kernel<E, 128, 1>, Scan<E, 128, 1>::kSmem, 1, done[3]);
 }
+static_assert(Scan<train::Bf16, 128, 4>::kSmem <= 232448 && Scan<train::F32, 128, 1>::kSmem <= 232448, "a block's shared memory");
 
 // --------------------------------------------------------------------- step
 

@@ -377,20 +377,6 @@ __device__ __forceinline__ void as_operand(uint32_t (&f)[N][4], const float (&lo
     }
   }
 }
-// c += A B over 16 of k and N pairs of tiles of 8 columns, of term j of B and all of A's
-// that go with it; the small terms' products go to s where 24 bits are to be kept (see
-// `product`).  The tiles take turns: an accumulator's next product waits for its last.
-template <int TA, int kLimit, int N>
-__device__ __forceinline__ void pairs_product(float (*c)[4], float (*s)[4], const uint32_t (&a)[TA][4],
-                                              const uint32_t (&b)[N][2][2], int j) {
-#pragma unroll
-  for (int i = 0; i < TA; ++i)
-    if (i + j < kLimit) {
-      float(*to)[4] = kLimit > 2 && i + j > 0 ? s : c;
-#pragma unroll
-      for (int t = 0; t < 2 * N; ++t) mma(to[t], a[i], b[t >> 1][t & 1][0], b[t >> 1][t & 1][1]);
-    }
-}
 // An 8 x 8 matrix of 16-bit values, a row's pair a lane, transposed.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t r;
@@ -418,6 +404,15 @@ __device__ __forceinline__ void save_block(uint32_t* block, const uint32_t (&f)[
   for (int n = 0; n < 2; ++n)
 #pragma unroll
     for (int j = 0; j < 4; ++j) block[n * 128 + j * 32 + lane_id()] = f[n][j];
+}
+// the same of fp32: 16 columns from vw and 16 rows from k0 of [dv][dk]
+__device__ __forceinline__ void save_rows(float* to, int dk, int dv, int vw, int k0, const float (&lo)[4], const float (&hi)[4]) {
+  const int g = lane_id() >> 2, t2 = (lane_id() & 3) * 2;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int v = vw + g + ((j >> 1) & 1) * 8, k = k0 + (j >> 2) * 8 + t2 + (j & 1);
+    if (v < dv && k < dk) to[static_cast<size_t>(v) * dk + k] = j < 4 ? lo[j & 3] : hi[j & 3];
+  }
 }
 // S^T's blocks in shared memory as an operand B(k, n), 16 x 16 pieces
 struct BlocksAcross {  // k: rows of the state, n: columns
@@ -493,43 +488,19 @@ __device__ __forceinline__ void padding_zeros(const Args<E>& a, int lo, int hi, 
     for (size_t i = threadIdx.x; i < mine; i += threads) a.carry[unit_of(a, c0 + c, h) * saved + at + i] = 0.f;
 }
 
-// A warp's tile of a state held as it is, rows r .. r + 15 and 8 N columns from c on (of
-// all columns), for the backward pass.
-template <class E, int N>
-__device__ __forceinline__ void save_tile(const Args<E>& a, float* to, const float (&S)[N][4], int r, int c) {
-  const int lane = lane_id(), g = lane >> 2, t2 = (lane & 3) * 2;
-#pragma unroll
-  for (int t = 0; t < N; ++t)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if constexpr (E::kBytes == 4) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = r + g + j * 8, column = c + t * 8 + t2 + e;
-          if (row < a.dk && column < a.dv) to[static_cast<size_t>(column) * a.dk + row] = S[t][2 * j + e];
-        }
-      } else if (r < a.dk && ((c + t * 8) & ~15) < a.dv) {  // (whole blocks, zeros in their padding)
-        const uint32_t w = pack(S[t][2 * j], S[t][2 * j + 1]);
-        uint32_t* at = block_of(to, a.dk, (c + t * 8) >> 4, r >> 4) + (((c + t * 8) >> 3) & 1) * 32 + j * 64 + lane;
-        at[0] = transposed(w);
-        at[128] = transposed(pack(S[t][2 * j] - lo_of(w), S[t][2 * j + 1] - hi_of(w)));
-      }
-    }
-}
-
-// A chunk's rows of a warp's 16 columns, held transposed; masked rows (beta 0) get
-// zeros.  `to` is the first row's column 0 of the head.
+// 16 of a chunk's rows, r0 on, of a quad's 16 columns, held transposed; masked rows (beta
+// 0) get zeros.  `to` is the chunk's first row's column 0 of the head.
 template <class E>
-__device__ __forceinline__ void store_rows(typename E::T* to, int64_t stride, int len, int vw, int dv, bool pairs,
-                                           const float (&beta)[kC], const float (&y)[kC / 8][4]) {
+__device__ __forceinline__ void store_rows(typename E::T* to, int64_t stride, int r0, int len, int vw, int dv, bool pairs,
+                                           const float* beta, const float (&y)[2][4]) {
   const int lane = lane_id(), g = lane >> 2, t2 = (lane & 3) * 2;
 #pragma unroll
-  for (int t = 0; t < kC / 8; ++t)
+  for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if constexpr (E::kBytes == 2) {
         const uint32_t w = transposed(pack(y[t][2 * j], y[t][2 * j + 1]));  // row t * 8 + g, columns t2, t2 + 1
-        const int r = t * 8 + g, v = vw + j * 8 + t2;
+        const int r = r0 + t * 8 + g, v = vw + j * 8 + t2;
         if (r >= len) continue;
         const uint32_t x = beta[r] != 0.f ? w : 0u;
         typename E::T* at = to + r * stride + v;
@@ -542,37 +513,72 @@ __device__ __forceinline__ void store_rows(typename E::T* to, int64_t stride, in
       } else {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = t * 8 + t2 + e, v = vw + j * 8 + g;
+          const int r = r0 + t * 8 + t2 + e, v = vw + j * 8 + g;
           if (r < len && v < dv) E::store(to + r * stride + v, beta[r] != 0.f ? y[t][2 * j + e] : 0.f);
         }
       }
     }
 }
 
-// S^T <- total S^T + A X, A of a chunk's 64 positions in three terms, X its rows of keys
-// or queries.  The sum is made apart and added once: S's last bit cuts it off once.
-template <class E, int KD>
-__device__ __forceinline__ void add_outer(float (&S)[KD / 8][4], float total, const uint32_t (&fa)[kC / 16][kStateTerms][4],
-                                          const Mat& X) {
+// ------------------------------------------------------------------- quads
+
+// Four warps, a quad, follow a sequence in a head for 16 of the value columns.  The
+// state is held transposed, S^T [16][dk], a quarter of its rows a warp, as an accumulator;
+// an accumulator is the next product's operand A as it lies in the registers (see
+// as_operand), so what the warps hand to one another are operands: 512 bytes a term,
+// 16 a lane, written and read without conflicts.  Each warp makes a quarter of the
+// chunk's positions of K S, U and Y, and its own rows of the state.  A block's quads share
+// the chunk's inputs; their warps' roles are turned by one from quad to quad, so that the
+// triangles' short and long rows are spread over the SM's four parts.
+__device__ __forceinline__ void quad_sync(int quad) { asm volatile("bar.sync %0, 128;" ::"r"(quad + 1) : "memory"); }
+template <int N>
+__device__ __forceinline__ void hand(uint32_t at, const uint32_t (&f)[N][4]) {
 #pragma unroll
-  for (int kb = 0; kb < KD / 16; kb += 2) {
-    float c[4][4], s[4][4];
-    clear(c);
-    clear(s);
+  for (int n = 0; n < N; ++n)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + n * 512 + lane_id() * 16), "r"(f[n][0]), "r"(f[n][1]),
+                 "r"(f[n][2]), "r"(f[n][3])
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void take(uint32_t at, uint32_t (&f)[N][4]) {
 #pragma unroll
-    for (int cb = 0; cb < kC / 16; ++cb)
-#pragma unroll
-      for (int j = 0; j < kIn<E>; ++j) {
-        uint32_t fb[2][2][2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) Down{X}.get<2>(fb[e], cb * 16, (kb + e) * 16, j);
-        pairs_product<kStateTerms, kStateTerms, 2>(c, s, fa[cb], fb, j);
-      }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) S[2 * kb + e][j] = fmaf(S[2 * kb + e][j], total, c[e][j] + s[e][j]);
+  for (int n = 0; n < N; ++n)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(f[n][0]), "=r"(f[n][1]), "=r"(f[n][2]), "=r"(f[n][3])
+                 : "r"(at + n * 512 + lane_id() * 16)
+                 : "memory");
+}
+// Tiles of 8 columns that accumulate a product.  Where 24 bits are to be kept the small
+// terms' products have accumulators of their own (see `product`), two of them, as a tile's
+// next product waits for its last.
+template <int N, bool kApart>
+struct Sums {
+  float main[N][4], small[kApart ? 2 : 1][kApart ? N : 1][4];
+  __device__ __forceinline__ void clear_all() {
+    clear(main);
+    if constexpr (kApart) {
+      clear(small[0]);
+      clear(small[1]);
+    }
   }
+  // terms i of A and j of B
+  __device__ __forceinline__ void add(int i, int j, const uint32_t (&a)[4], const uint32_t (*b)[2]) {
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+      if constexpr (kApart) mma(i + j == 0 ? main[t] : small[i & 1][t], a, b[t][0], b[t][1]);
+      else mma(main[t], a, b[t][0], b[t][1]);
+    }
+  }
+  __device__ __forceinline__ float sum(int t, int j) const {
+    if constexpr (kApart) return main[t][j] + (small[0][t][j] + small[1][t][j]);
+    else return main[t][j];
+  }
+};
+template <int TA, int kLimit, int N, bool kApart>
+__device__ __forceinline__ void terms(Sums<N, kApart>& c, const uint32_t (&a)[TA][4], const uint32_t (&b)[N][2], int j) {
+#pragma unroll
+  for (int i = 0; i < TA; ++i)
+    if (i + j < kLimit) c.add(i, j, a[i], b);
 }
 
 // ------------------------------------------------------------ host: launches
@@ -607,11 +613,11 @@ inline int opt_in(const void* kernel, int smem, std::atomic<uint64_t>& done) {
   return ENGRAM_OK;
 }
 
-// Whether a warp follows a sequence in a head (scan_rows_kernel, back_rows_kernel) or a
-// block does.  (fp32's operands of three terms each leave a warp no registers.)
+// Quads of a block: four where there are blocks enough for the SMs (they share the copies
+// of a chunk's inputs), else one, so that few sequences and heads spread over more SMs.
 template <class E>
-bool by_warps(const Args<E>& a, int sms) {
-  return E::kBytes == 2 && static_cast<int64_t>(a.n_seqs) * a.heads * 2 >= sms;
+bool many_quads(const Args<E>& a, int sms) {
+  return E::kBytes == 2 && static_cast<int64_t>(a.n_seqs) * a.heads * ((a.dv + 63) / 64) >= sms;
 }
 
 inline bool pieces(const void* p, int64_t stride, int bytes) { return aligned(p, 16) && stride * bytes % 16 == 0; }

@@ -20,205 +20,47 @@ namespace {
 
 // ------------------------------------------------ the state's gradient, backwards
 
-template <class E, int KD, int VS>
+// A quad goes backwards as scan_kernel's go forwards, with dS^T in its registers.
+template <class E, int KD, int NQ>
 struct Back {
-  static constexpr int kStages = E::kBytes == 2 ? 2 : 1;
-  static constexpr int kQ = 0, kK = kQ + kIn<E> * mat_bytes(kC, KD), kY = kK + kIn<E> * mat_bytes(kC, KD);
-  static constexpr int kM = kY + kIn<E> * mat_bytes(kC, VS), kP = kM + kStateTerms * kTerm, kG = kP + kStateTerms * kTerm;
-  static constexpr int kStage = kG + static_cast<int>(sizeof(Gates));
-  static constexpr int kS = kStages * kStage;                      // dS
-  static constexpr int kX = kS + kStateTerms * mat_bytes(KD, VS);  // dU, then -e^c dV
-  static constexpr int kR = kX + kStateTerms * mat_bytes(kC, VS);  // scale e^c dY
-  static constexpr int kSmem = kR + kStateTerms * mat_bytes(kC, VS);
-  static constexpr int kAcross = kWarps / (KD / 16);
-  static constexpr int kN = VS / 16, kSN = VS / 8 / kAcross;
-};
-
-template <class E, int KD, int VS>
-__global__ void __launch_bounds__(kThreads, 1) back_kernel(Args<E> a) {
-  using L = Back<E, KD, VS>;
-  extern __shared__ __align__(128) unsigned char smem[];
-  const uint32_t base = smem_u32(smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
-  const int seq = blockIdx.x, h = blockIdx.y, v0 = blockIdx.z * VS, cols = a.dv - v0 < VS ? a.dv - v0 : VS;
-  const int hk = h / (a.heads / a.keys);
-  int lo, hi;
-  bounds(a, seq, lo, hi);
-  const int c0 = a.first[seq], n = min((hi - lo + kC - 1) / kC, a.max_chunks - c0);
-  int64_t slot;
-  const bool live = live_slot(a, seq, slot);
-  if (!live && tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
-  if (!live) {
-    padding_zeros(a, lo, hi, c0, n, h, v0, cols, kThreads);
-    return;
-  }
-  const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
-  const int sm = warp % (KD / 16) * 16, sn = warp / (KD / 16) * (L::kSN * 8);
-  auto each = [&](auto f) {  // f(accumulator's tile and place, the element's place in a state)
-#pragma unroll
-    for (int t = 0; t < L::kSN; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = sm + g + (j >> 1) * 8, c = sn + t * 8 + t2 + (j & 1);
-        if (r < a.dk && c < cols) f(t, j, static_cast<size_t>(r) * a.dv + v0 + c);
-      }
-  };
-  float S[L::kSN][4];
-  clear(S);
-  if (a.state_out != nullptr) {
-    const float* from = a.state_out + (slot * a.heads + h) * matrix;
-    each([&](int t, int j, size_t at) { S[t][j] = from[at]; });
-  }
-  const Mat St = mat<KD, VS>(base + L::kS), X = mat<kC, VS>(base + L::kX), R = mat<kC, VS>(base + L::kR);
-  auto keep = [&]() {
-#pragma unroll
-    for (int t = 0; t < L::kSN; ++t)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        put<kStateTerms>(St.base + (sm + g + j * 8) * St.pitch + (sn + t * 8 + t2) * 2, St.term, S[t][2 * j], S[t][2 * j + 1]);
-  };
-  auto load = [&](int i) {
-    const uint32_t stage = base + (i % L::kStages) * L::kStage;
-    const int64_t p = lo + static_cast<int64_t>(i) * kC;
-    const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
-    const uint8_t* mask = a.mask != nullptr ? a.mask + p : nullptr;
-    const size_t unit = unit_of(a, c0 + i, h);
-    load_rows<E, KD>(mat<kC, KD>(stage + L::kK), a.k + p * a.k_stride + hk * a.dk, a.k_stride, len, a.dk, mask, a.vec);
-    load_rows<E, KD>(mat<kC, KD>(stage + L::kQ), a.q + p * a.q_stride + hk * a.dk, a.q_stride, len, a.dk, mask, a.vec);
-    load_rows<E, VS>(mat<kC, VS>(stage + L::kY), a.dy + p * a.dy_stride + h * a.dv + v0, a.dy_stride, len, cols, mask, a.vec);
-    load_tri<kStateTerms>(stage + L::kM, stage + L::kP, a.tri + unit * kTriBytes);
-    load_gates(stage + L::kG, a.gates + unit);
-    copies_begun();
-  };
-  keep();
-  if (n > 0) load(n - 1);
-  const int m = (warp & 3) * 16, nn = (warp >> 2) * (VS / 2);
-  for (int i = n - 1; i >= 0; --i) {
-    const uint32_t stage = base + (i % L::kStages) * L::kStage;
-    const Mat K = mat<kC, KD>(stage + L::kK), Q = mat<kC, KD>(stage + L::kQ), Y = mat<kC, VS>(stage + L::kY);
-    const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
-    copies_done();
-    __syncthreads();  // the chunk and dS are here, and the other stage is free
-    if (L::kStages == 2 && i > 0) load(i - 1);
-    save_tile<E, L::kSN>(a, a.after + unit_of(a, c0 + i, h) * saved_floats<E>(a.dk, a.dv), S, sm, v0 + sn);
-    float x[L::kN][4], u[L::kN][4];
-    clear(x);
-    clear(u);
-    product<kIn<E>, kStateTerms, kStateTerms>(x, Rows{K}, Down{St}, m, nn, 0, KD);
-    product<kStateTerms, kIn<E>, kStateTerms>(u, TriCols{stage + L::kP}, Down{Y}, m, nn, m, kC);
-#pragma unroll
-    for (int t = 0; t < L::kN; ++t)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = m + g + j * 8, c = nn + t * 8 + t2;
-        const float last = gt.last[r], into = a.scale * gt.into[r];
-        put<kStateTerms>(X.base + r * X.pitch + c * 2, X.term, fmaf(last, x[t][2 * j], u[t][2 * j]),
-                         fmaf(last, x[t][2 * j + 1], u[t][2 * j + 1]));
-        float y[2];
-        get<kIn<E>>(Y.base + r * Y.pitch + c * 2, Y.term, y[0], y[1]);
-        put<kStateTerms>(R.base + r * R.pitch + c * 2, R.term, into * y[0], into * y[1]);
-      }
-    __syncthreads();
-    clear(u);
-    product<kStateTerms, kStateTerms, kStateTerms>(u, TriCols{stage + L::kM}, Down{X}, m, nn, m, kC);
-    __syncthreads();  // X is free
-    const int64_t p = lo + static_cast<int64_t>(i) * kC;
-#pragma unroll
-    for (int t = 0; t < L::kN; ++t)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = m + g + j * 8, c = nn + t * 8 + t2;
-        const float into = gt.into[r];
-        put<kStateTerms>(X.base + r * X.pitch + c * 2, X.term, -into * u[t][2 * j], -into * u[t][2 * j + 1]);
-        if (p + r >= hi) continue;
-        const bool on = gt.beta[r] != 0.f;  // a masked position takes no gradient
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (c + e >= cols) continue;
-          const float d = on ? u[t][2 * j + e] : 0.f;
-          auto* to = a.dv_out + (p + r) * a.dv_stride + h * a.dv + v0 + c + e;
-          E::store(to, d);
-          if constexpr (E::kBytes == 2)  // what the rounding has left
-            a.writes[((p + r) * a.heads + h) * a.dv + v0 + c + e] = static_cast<uint16_t>(pack(d - E::load(to), 0.f));
-        }
-      }
-    __syncthreads();
-    const float total = gt.into[kC - 1];
-#pragma unroll
-    for (int t = 0; t < L::kSN; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) S[t][j] *= total;
-    product<kIn<E>, kStateTerms, kStateTerms>(S, Cols{Q}, Down{R}, sm, sn, 0, kC);
-    product<kIn<E>, kStateTerms, kStateTerms>(S, Cols{K}, Down{X}, sm, sn, 0, kC);
-    keep();
-    if (L::kStages == 1 && i > 0) {
-      __syncthreads();  // the stage is free
-      load(i - 1);
-    }
-  }
-  if (a.state_out != nullptr) {
-    float* to = a.state_out + (slot * a.heads + h) * matrix;
-    each([&](int t, int j, size_t at) { to[at] = S[t][j]; });
-  }
-}
-
-// A warp follows one sequence in one head backwards, for 16 of the value columns, with
-// dS^T in its registers, as scan_rows_kernel does forwards.
-template <class E, int KD, int W>
-struct BackRows {
-  static constexpr int kStages = 2;
+  static constexpr int kT = NQ * 128, kStages = E::kBytes == 2 ? 2 : 1, kB = kC / 16;
   static constexpr int kK = 0, kQ = kK + kIn<E> * mat_bytes(kC, KD), kY = kQ + kIn<E> * mat_bytes(kC, KD);
-  static constexpr int kM = kY + kIn<E> * mat_bytes(kC, 16 * W), kP = kM + kStateTerms * kTerm, kG = kP + kStateTerms * kTerm;
-  static constexpr int kStage = kG + static_cast<int>(sizeof(Gates));
-  static constexpr int kSmem = kStages * kStage;
+  static constexpr int kM = kY + kIn<E> * mat_bytes(kC, 16 * NQ), kP = kM + kStateTerms * kTerm, kG = kP + kStateTerms * kTerm;
+  static constexpr int kStage = kG + static_cast<int>(sizeof(Gates)), kQuads = kStages * kStage;
+  // a quad's operands: dS^T, then in its place (scale e^c dY)^T; dU^T, then (-e^c dV)^T
+  static constexpr int kR = 0, kState = (KD / 16 > kB ? KD / 16 : kB) * kStateTerms * 512, kU = kState;
+  static constexpr int kQuad = kU + kB * kStateTerms * 512;
+  static constexpr int kSmem = kQuads + NQ * kQuad;
 };
 
-// c += A B, A 16 of the positions, block tb, B a triangle's blocks (tb, ib <= tb).
-template <int TA>
-__device__ __forceinline__ void above(float (&c)[kC / 8][4], float (&s)[kC / 8][4], const uint32_t (&fa)[TA][4],
-                                      const TriDown& b, int tb) {
-#pragma unroll
-  for (int j = 0; j < kStateTerms; ++j) {
-    uint32_t fb[kC / 16][2][2];
-#pragma unroll
-    for (int ib = 0; ib < kC / 16; ++ib)
-      if (ib <= tb) b.get(fb[ib], tb, ib, j);
-#pragma unroll
-    for (int i = 0; i < TA; ++i)
-      if (i + j < kStateTerms) {
-#pragma unroll
-        for (int t = 0; t < kC / 8; ++t)
-          if (t / 2 <= tb) mma(i + j > 0 ? s[t] : c[t], fa[i], fb[t >> 1][t & 1][0], fb[t >> 1][t & 1][1]);
-      }
-  }
-}
-
-template <class E, int KD, int W>
-__global__ void __launch_bounds__(W * 32, 1) back_rows_kernel(Args<E> a) {
-  using L = BackRows<E, KD, W>;
-  constexpr int kT = W * 32, kI = kIn<E>, kS = kStateTerms, kB = kC / 16;
+template <class E, int KD, int NQ>
+__global__ void __launch_bounds__(NQ * 128, 1) back_kernel(Args<E> a) {
+  using L = Back<E, KD, NQ>;
+  constexpr int kT = L::kT, kI = kIn<E>, kS = kStateTerms, kB = L::kB, kR = KD / 64;
   extern __shared__ __align__(128) unsigned char smem[];
   const uint32_t base = smem_u32(smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
-  const int seq = blockIdx.x, h = blockIdx.y, v0 = blockIdx.z * (16 * W), cols = min(a.dv - v0, 16 * W);
-  const int hk = h / (a.heads / a.keys), vw = v0 + warp * 16;
+  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t2 = (lane & 3) * 2;
+  const int quad = tid >> 7, w = ((tid >> 5) + quad) & 3;
+  const int seq = blockIdx.x, h = blockIdx.y, v0 = blockIdx.z * (16 * NQ), cols = min(a.dv - v0, 16 * NQ);
+  const int hk = h / (a.heads / a.keys), vw = v0 + quad * 16;
   int lo, hi;
   bounds(a, seq, lo, hi);
   const int c0 = a.first[seq], n = min((hi - lo + kC - 1) / kC, a.max_chunks - c0);
-  const size_t matrix = static_cast<size_t>(a.dk) * a.dv;
+  const size_t matrix = static_cast<size_t>(a.dk) * a.dv, saved = saved_floats<E>(a.dk, a.dv);
   int64_t slot;
   if (!live_slot(a, seq, slot)) {
     if (tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
     padding_zeros(a, lo, hi, c0, n, h, v0, cols, kT);
     return;
   }
-  float S[KD / 8][4];
-  auto each = [&](auto f) {
+  const uint32_t own = base + L::kQuads + quad * L::kQuad;
+  float S[2 * kR][4];
+  auto each = [&](auto f) {  // f(tile, place, the element's place in a state)
 #pragma unroll
-    for (int t = 0; t < KD / 8; ++t)
+    for (int t = 0; t < 2 * kR; ++t)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int v = vw + g + (j >> 1) * 8, k = t * 8 + t2 + (j & 1);
+        const int v = vw + g + (j >> 1) * 8, k = w * kR * 16 + t * 8 + t2 + (j & 1);
         if (v < a.dv && k < a.dk) f(t, j, static_cast<size_t>(k) * a.dv + v);
       }
   };
@@ -227,6 +69,19 @@ __global__ void __launch_bounds__(W * 32, 1) back_rows_kernel(Args<E> a) {
     const float* from = a.state_out + (slot * a.heads + h) * matrix;
     each([&](int t, int j, size_t at) { S[t][j] = from[at]; });
   }
+  auto hand_state = [&](int i) {  // the gradient of the state behind chunk i
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const int kb = w * kR + r;
+      uint32_t f[kS][4];
+      as_operand<kS>(f, S[2 * r], S[2 * r + 1]);
+      hand<kS>(own + kb * (kS * 512), f);
+      if (vw >= a.dv || kb * 16 >= a.dk) continue;
+      float* to = a.after + unit_of(a, c0 + i, h) * saved;
+      if constexpr (E::kBytes == 2) save_block(block_of(to, a.dk, vw >> 4, kb), f);
+      else save_rows(to, a.dk, a.dv, vw, kb * 16, S[2 * r], S[2 * r + 1]);
+    }
+  };
   auto load = [&](int i) {
     const uint32_t stage = base + (i % L::kStages) * L::kStage;
     const int64_t p = lo + static_cast<int64_t>(i) * kC;
@@ -235,90 +90,77 @@ __global__ void __launch_bounds__(W * 32, 1) back_rows_kernel(Args<E> a) {
     const size_t unit = unit_of(a, c0 + i, h);
     load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kK), a.k + p * a.k_stride + hk * a.dk, a.k_stride, len, a.dk, mask, a.vec);
     load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kQ), a.q + p * a.q_stride + hk * a.dk, a.q_stride, len, a.dk, mask, a.vec);
-    load_rows<E, 16 * W, kT>(mat<kC, 16 * W>(stage + L::kY), a.dy + p * a.dy_stride + h * a.dv + v0, a.dy_stride, len, cols,
-                             mask, a.vec);
+    load_rows<E, 16 * NQ, kT>(mat<kC, 16 * NQ>(stage + L::kY), a.dy + p * a.dy_stride + static_cast<int64_t>(h) * a.dv + v0,
+                              a.dy_stride, len, cols, mask, a.vec);
     load_tri<kS, kT>(stage + L::kM, stage + L::kP, a.tri + unit * kTriBytes);
     load_gates<kT>(stage + L::kG, a.gates + unit);
     copies_begun();
   };
-  if (n > 0) load(n - 1);
+  if (n > 0) {
+    hand_state(n - 1);
+    load(n - 1);
+  }
   for (int i = n - 1; i >= 0; --i) {
     const uint32_t stage = base + (i % L::kStages) * L::kStage;
-    const Mat K = mat<kC, KD>(stage + L::kK), Q = mat<kC, KD>(stage + L::kQ), Y = mat<kC, 16 * W>(stage + L::kY);
+    const Mat K = mat<kC, KD>(stage + L::kK), Q = mat<kC, KD>(stage + L::kQ), Y = mat<kC, 16 * NQ>(stage + L::kY);
     const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
     copies_done();
-    __syncthreads();  // the chunk is here, and the other stage is free
-    if (i > 0) load(i - 1);
-    float* kept = a.after + unit_of(a, c0 + i, h) * saved_floats<E>(a.dk, a.dv);
-    // ---- dU^T = e^(c_last - c) (K dS)^T + dY^T P
-    float u[kC / 8][4], s[kC / 8][4];
-    clear(u);
-    clear(s);
+    __syncthreads();  // the chunk and the states' gradients are here, and the other stage is free
+    if (L::kStages == 2 && i > 0) load(i - 1);
+    float2 into[2], last[2];  // of the warp's positions
 #pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      into[t] = *reinterpret_cast<const float2*>(&gt.into[w * 16 + t * 8 + t2]);
+      last[t] = *reinterpret_cast<const float2*>(&gt.last[w * 16 + t * 8 + t2]);
+    }
+    // ---- dU^T = e^(c_last - c) (K dS)^T + dY^T P
+    Sums<2, true> x;
+    x.clear_all();
+#pragma unroll 4
     for (int kb = 0; kb < KD / 16; ++kb) {
       uint32_t fa[kS][4];
-      as_operand<kS>(fa, S[2 * kb], S[2 * kb + 1]);
-      if (vw < a.dv && kb * 16 < a.dk) save_block(block_of(kept, a.dk, vw >> 4, kb), fa);
+      take<kS>(own + kb * (kS * 512), fa);
 #pragma unroll
       for (int j = 0; j < kI; ++j) {
-        uint32_t fb[kB][2][2];
-#pragma unroll
-        for (int cb = 0; cb < kB; ++cb) Across{K}.get<2>(fb[cb], kb * 16, cb * 16, j);
-        pairs_product<kS, kS, kB>(u, s, fa, fb, j);
+        uint32_t fb[2][2];
+        Across{K}.get<2>(fb, kb * 16, w * 16, j);
+        terms<kS, kS>(x, fa, fb, j);
       }
     }
+    float u[2][4];
 #pragma unroll
-    for (int t = 0; t < kC / 8; ++t) {
-      const float2 last = *reinterpret_cast<const float2*>(&gt.last[t * 8 + t2]);
-      u[t][0] = (u[t][0] + s[t][0]) * last.x;
-      u[t][1] = (u[t][1] + s[t][1]) * last.y;
-      u[t][2] = (u[t][2] + s[t][2]) * last.x;
-      u[t][3] = (u[t][3] + s[t][3]) * last.y;
-    }
-    clear(s);
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int tb = 0; tb < kB; ++tb) {
+      for (int j = 0; j < 4; ++j) u[t][j] = x.sum(t, j) * (j & 1 ? last[t].y : last[t].x);
+    x.clear_all();
+    for (int tb = w; tb < kB; ++tb) {
       uint32_t fa[kI][4];
 #pragma unroll
-      for (int j = 0; j < kI; ++j) Cols{Y}(fa[j], warp * 16, tb * 16, j);
-      above<kI>(u, s, fa, TriDown{stage + L::kP}, tb);
-    }
+      for (int j = 0; j < kI; ++j) Cols{Y}(fa[j], quad * 16, tb * 16, j);
 #pragma unroll
-    for (int t = 0; t < kC / 8; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[t][j] += s[t][j];
-    // ---- dV^T = dU^T M
-    float w[kC / 8][4];
-    clear(w);
-    clear(s);
-#pragma unroll
-    for (int tb = 0; tb < kB; ++tb) {
-      uint32_t fa[kS][4];
-      as_operand<kS>(fa, u[2 * tb], u[2 * tb + 1]);
-      above<kS>(w, s, fa, TriDown{stage + L::kM}, tb);
-    }
-#pragma unroll
-    for (int t = 0; t < kC / 8; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        w[t][j] += s[t][j];
-        s[t][j] = w[t][j] - lo_of(pack(w[t][j], 0.f));  // what the output's rounding leaves
+      for (int j = 0; j < kS; ++j) {
+        uint32_t fb[2][2];
+        TriDown{stage + L::kP}.get(fb, tb, w, j);
+        terms<kI, kS>(x, fa, fb, j);
       }
-    const int64_t p = lo + static_cast<int64_t>(i) * kC;
-    const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
-    store_rows<E>(a.dv_out + p * a.dv_stride + h * a.dv, a.dv_stride, len, vw, a.dv, a.pairs, gt.beta, w);
-    store_rows<E>(a.writes + (p * a.heads + h) * a.dv, static_cast<int64_t>(a.heads) * a.dv, len, vw, a.dv, a.dv % 2 == 0,
-                  gt.beta, s);
-    // ---- dS^T
-    uint32_t fa[kB][kS][4];
+    }
+    {
 #pragma unroll
-    for (int cb = 0; cb < kB; ++cb) {
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[t][j] += x.sum(t, j);
+      uint32_t f[kS][4];
+      as_operand<kS>(f, u[0], u[1]);
+      hand<kS>(own + L::kU + w * (kS * 512), f);
+    }
+    quad_sync(quad);  // and dS^T is no longer needed
+    {
       float r[2][4];
       clear(r);
 #pragma unroll
       for (int j = kI - 1; j >= 0; --j) {
         uint32_t f[4];
-        Cols{Y}(f, warp * 16, cb * 16, j);
+        Cols{Y}(f, quad * 16, w * 16, j);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           r[q >> 1][(q & 1) * 2] += lo_of(f[q]);
@@ -326,21 +168,84 @@ __global__ void __launch_bounds__(W * 32, 1) back_rows_kernel(Args<E> a) {
         }
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 into = *reinterpret_cast<const float2*>(&gt.into[cb * 16 + e * 8 + t2]);
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float x = j & 1 ? into.y : into.x;
-          r[e][j] *= a.scale * x;
-          w[2 * cb + e][j] *= -x;
+        for (int j = 0; j < 4; ++j) r[t][j] *= a.scale * (j & 1 ? into[t].y : into[t].x);
+      uint32_t f[kS][4];
+      as_operand<kS>(f, r[0], r[1]);
+      hand<kS>(own + L::kR + w * (kS * 512), f);
+    }
+    // ---- dV^T = dU^T M
+    x.clear_all();
+    for (int tb = w; tb < kB; ++tb) {
+      uint32_t fa[kS][4];
+      take<kS>(own + L::kU + tb * (kS * 512), fa);
+#pragma unroll
+      for (int j = 0; j < kS; ++j) {
+        uint32_t fb[2][2];
+        TriDown{stage + L::kM}.get(fb, tb, w, j);
+        terms<kS, kS>(x, fa, fb, j);
+      }
+    }
+    float rest[2][4];  // what the output's rounding leaves
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        u[t][j] = x.sum(t, j);
+        rest[t][j] = u[t][j] - lo_of(pack(u[t][j], 0.f));
+      }
+    {
+      float c[2][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[t][j] = -u[t][j] * (j & 1 ? into[t].y : into[t].x);
+      uint32_t f[kS][4];
+      as_operand<kS>(f, c[0], c[1]);
+      quad_sync(quad);  // dU^T is no longer needed
+      hand<kS>(own + L::kU + w * (kS * 512), f);
+    }
+    quad_sync(quad);
+    // ---- dS^T
+    {
+      const float total = gt.into[kC - 1];
+      Sums<2 * kR, true> d;
+      d.clear_all();
+#pragma unroll
+      for (int cb = 0; cb < kB; ++cb) {
+        uint32_t fr[kS][4], fw[kS][4];
+        take<kS>(own + L::kR + cb * (kS * 512), fr);
+        take<kS>(own + L::kU + cb * (kS * 512), fw);
+#pragma unroll
+        for (int j = 0; j < kI; ++j) {
+          uint32_t fb[2 * kR][2];
+          Down{Q}.get<2 * kR>(fb, cb * 16, w * kR * 16, j);
+          terms<kS, kS>(d, fr, fb, j);
+          Down{K}.get<2 * kR>(fb, cb * 16, w * kR * 16, j);
+          terms<kS, kS>(d, fw, fb, j);
         }
       }
-      as_operand<kS>(fa[cb], r[0], r[1]);
-    }
-    add_outer<E, KD>(S, gt.into[kC - 1], fa, Q);
 #pragma unroll
-    for (int cb = 0; cb < kB; ++cb) as_operand<kS>(fa[cb], w[2 * cb], w[2 * cb + 1]);
-    add_outer<E, KD>(S, 1.f, fa, K);
+      for (int t = 0; t < 2 * kR; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) S[t][j] = fmaf(S[t][j], total, d.sum(t, j));
+    }
+    if (i > 0) {
+      quad_sync(quad);  // the operands have been taken
+      hand_state(i - 1);
+    }
+    const int64_t p = lo + static_cast<int64_t>(i) * kC;
+    const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
+    store_rows<E>(a.dv_out + p * a.dv_stride + static_cast<int64_t>(h) * a.dv, a.dv_stride, w * 16, len, vw, a.dv, a.pairs,
+                  gt.beta, u);
+    if constexpr (E::kBytes == 2)
+      store_rows<E>(a.writes + (p * a.heads + h) * a.dv, static_cast<int64_t>(a.heads) * a.dv, w * 16, len, vw, a.dv,
+                    a.dv % 2 == 0, gt.beta, rest);
+    if (L::kStages == 1 && i > 0) {
+      __syncthreads();  // the stage is free
+      load(i - 1);
+    }
   }
   if (a.state_out != nullptr) {
     float* to = a.state_out + (slot * a.heads + h) * matrix;
@@ -776,29 +681,29 @@ int launch_grad(const Args<E>& a, int sms, cudaStream_t st) {
     kernel<<<grid, threads, smem, st>>>(a);
     return check_launch(name);
   };
-  constexpr int VB = 16, VG = E::kBytes == 2 ? 32 : 16;
-  const dim3 back(a.n_seqs, a.heads, (a.dv + VB - 1) / VB), grads(a.max_chunks, a.keys);
-  bool rows = false;
+  constexpr int VG = E::kBytes == 2 ? 32 : 16;
+  const dim3 grads(a.max_chunks, a.keys);
+  auto back = [&](auto kernel, int smem, int nq, std::atomic<uint64_t>& flag) {
+    return go(kernel, smem, dim3(a.n_seqs, a.heads, (a.dv + 16 * nq - 1) / (16 * nq)), flag, "back_kernel", nq * 128);
+  };
+  bool many = false;
   if constexpr (E::kBytes == 2) {
-    rows = by_warps(a, sms);
-    if (rows) {
-      static std::atomic<uint64_t> flags[2] = {{0}, {0}};
-      const dim3 grid(a.n_seqs, a.heads, (a.dv + 127) / 128);
-      rc = a.dk <= 64 ? go(back_rows_kernel<E, 64, 8>, BackRows<E, 64, 8>::kSmem, grid, flags[0], "back_rows_kernel")
-                      : go(back_rows_kernel<E, 128, 8>, BackRows<E, 128, 8>::kSmem, grid, flags[1], "back_rows_kernel");
-    }
+    many = many_quads(a, sms);
+    static std::atomic<uint64_t> flags[2] = {{0}, {0}};
+    if (many)
+      rc = a.dk <= 64 ? back(back_kernel<E, 64, 4>, Back<E, 64, 4>::kSmem, 4, flags[0])
+                      : back(back_kernel<E, 128, 4>, Back<E, 128, 4>::kSmem, 4, flags[1]);
   }
-  if (!rows)
-    rc = a.dk <= 64 ? go(back_kernel<E, 64, VB>, Back<E, 64, VB>::kSmem, back, done[0], "back_kernel")
-                    : go(back_kernel<E, 128, VB>, Back<E, 128, VB>::kSmem, back, done[1], "back_kernel");
+  if (!many)
+    rc = a.dk <= 64 ? back(back_kernel<E, 64, 1>, Back<E, 64, 1>::kSmem, 1, done[0])
+                    : back(back_kernel<E, 128, 1>, Back<E, 128, 1>::kSmem, 1, done[1]);
   if (rc) return rc;
   return a.dk <= 64 ? go(grads_kernel<E, 64, VG>, Grads<E, 64, VG>::kSmem, grads, done[2], "grads_kernel", Grads<E, 64, VG>::kT)
                     : go(grads_kernel<E, 128, VG>, Grads<E, 128, VG>::kSmem, grads, done[3], "grads_kernel", Grads<E, 128, VG>::kT);
 }
 
-static_assert(Back<train::Bf16, 128, 16>::kSmem <= 232448 && Back<train::F32, 128, 16>::kSmem <= 232448 &&
-                  BackRows<train::Bf16, 128, 8>::kSmem <= 232448 && Grads<train::Bf16, 128, 32>::kSmem <= 232448 &&
-                  Grads<train::F32, 128, 16>::kSmem <= 232448,
+static_assert(Back<train::Bf16, 128, 4>::kSmem <= 232448 && Back<train::F32, 128, 1>::kSmem <= 232448 &&
+                  Grads<train::Bf16, 128, 32>::kSmem <= 232448 && Grads<train::F32, 128, 16>::kSmem <= 232448,
               "a block's shared memory");
 
 }  // namespace
