@@ -11,10 +11,11 @@ namespace delta {
 
 // ------------------------------------------------------------------- chunks
 
-// first[s]: how many chunks the sequences before s have.
+// first[s]: how many chunks the sequences before s have.  order[]: the sequences by length,
+// as far as one block sorts them by counting (1024), else as they come.
 template <class E>
 __global__ void __launch_bounds__(1024) first_kernel(Args<E> a) {
-  __shared__ int warp_sum[32];
+  __shared__ int warp_sum[32], counts[1024];
   __shared__ int64_t before;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) before = 0;
@@ -26,6 +27,8 @@ __global__ void __launch_bounds__(1024) first_kernel(Args<E> a) {
       bounds(a, s, lo, hi);
       n = (hi - lo + kC - 1) / kC;
     }
+    if (a.n_seqs <= 1024) counts[threadIdx.x] = n;
+    else if (s < a.n_seqs) a.order[s] = s;
     int sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -44,6 +47,11 @@ __global__ void __launch_bounds__(1024) first_kernel(Args<E> a) {
   }
   __syncthreads();
   if (threadIdx.x == 0) a.first[a.n_seqs] = static_cast<int>(before < a.max_chunks ? before : a.max_chunks);
+  const int s = threadIdx.x;
+  if (a.n_seqs > 1024 || s >= a.n_seqs) return;
+  int rank = 0;
+  for (int o = 0; o < a.n_seqs; ++o) rank += counts[o] > counts[s] || (counts[o] == counts[s] && o < s);
+  a.order[rank] = s;
 }
 
 // ---------------------------------------------------------------- M, P, gates
@@ -315,7 +323,9 @@ __global__ void __launch_bounds__(NQ * 128, 1) scan_kernel(Args<E> a) {
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t2 = (lane & 3) * 2;
   const int quad = tid >> 7, w = ((tid >> 5) + quad) & 3;  // w: the warp's quarter
-  const int seq = blockIdx.x, h = blockIdx.y, v0 = blockIdx.z * (16 * NQ), cols = min(a.dv - v0, 16 * NQ);
+  int seq, h, v0;
+  place_of(a, 16 * NQ, seq, h, v0);
+  const int cols = min(a.dv - v0, 16 * NQ);
   const int hk = h / (a.heads / a.keys), vw = v0 + quad * 16;
   int lo, hi;
   bounds(a, seq, lo, hi);
@@ -524,7 +534,9 @@ int launch_scan(const Args<E>& a, int sms, cudaStream_t st) {
   auto go = [&](auto kernel, int smem, int nq, std::atomic<uint64_t>& flag) {
     int r = opt_in(reinterpret_cast<const void*>(kernel), smem, flag);
     if (r) return r;
-    kernel<<<dim3(a.n_seqs, a.heads, (a.dv + 16 * nq - 1) / (16 * nq)), nq * 128, smem, st>>>(a);
+    const int64_t blocks = static_cast<int64_t>(a.n_seqs) * a.heads * ((a.dv + 16 * nq - 1) / (16 * nq));
+    if (blocks > 0x7fffffff) return fail(ENGRAM_E_RANGE, "too many sequences times heads");
+    kernel<<<static_cast<unsigned>(blocks), nq * 128, smem, st>>>(a);
     return check_launch("scan_kernel");
   };
   static std::atomic<uint64_t> done[4] = {{0}, {0}, {0}, {0}};
@@ -657,12 +669,12 @@ Space space(void* base, int64_t n_tokens, int64_t n_seqs, int32_t keys, int32_t 
     return p;
   };
   s.first = reinterpret_cast<int32_t*>(take(sizeof(int32_t) * (n_seqs + 1)));
+  s.order = reinterpret_cast<int32_t*>(take(sizeof(int32_t) * n_seqs));
   s.tri = take(units * kTriBytes);
   s.gates = reinterpret_cast<Gates*>(take(units * sizeof(Gates)));
   if (backward) {
     s.after = reinterpret_cast<float*>(take(units * saved_floats<train::Bf16>(dk, dv) * sizeof(float)));
     s.writes = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(n_tokens) * heads * dv * sizeof(uint16_t)));
-    if (heads > keys) s.shared = reinterpret_cast<float*>(take(2 * static_cast<size_t>(n_tokens) * keys * dk * sizeof(float)));
   }
   s.bytes = at;
   return s;
@@ -754,6 +766,7 @@ extern "C" int engram_delta(const void* q_d, int64_t q_stride, const void* k_d, 
     a.status = status_d;
     const Space s = space(workspace_d, n_tokens, n_seqs, key_heads, heads, dk, dv, false);
     a.first = s.first;
+    a.order = s.order;
     a.tri = s.tri;
     a.gates = s.gates;
     int r = launch_prepare<E>(a, as_stream(stream));

@@ -79,13 +79,13 @@ struct Args {
   bool has_state;  // slots are checked against n_slots
   // workspace
   int32_t* first;  // [n_seqs + 1] number of a sequence's first chunk
+  int32_t* order;  // [n_seqs] the sequences, long ones first
   unsigned char* tri;
   Gates* gates;
   // backward: states' gradients behind the chunks, as `carry` has the states in front of them; the second terms of
-  // the values' gradients (bf16); sums over heads that share a key
+  // the values' gradients (bf16)
   float* after;
   uint16_t* writes;
-  float* shared;
   int32_t* status;
 };
 
@@ -468,6 +468,16 @@ __device__ __forceinline__ void load_gates(uint32_t to, const Gates* from) {
     copy16(to + i * 16, reinterpret_cast<const unsigned char*>(from) + i * 16, true);
 }
 
+// A block's sequence, head and first value column, of a grid of one dimension with the
+// longest sequences first: a block that follows a long one is not begun last.
+template <class E>
+__device__ __forceinline__ void place_of(const Args<E>& a, int across, int& seq, int& h, int& v0) {
+  const int slices = (a.dv + across - 1) / across, per = slices * a.heads, i = blockIdx.x;
+  seq = a.order[i / per];
+  h = i % per / slices;
+  v0 = i % slices * across;
+}
+
 template <class E>
 __device__ __forceinline__ size_t unit_of(const Args<E>& a, int chunk, int head) {
   return static_cast<size_t>(chunk) * a.heads + head;
@@ -585,12 +595,11 @@ __device__ __forceinline__ void terms(Sums<N, kApart>& c, const uint32_t (&a)[TA
 
 // The space behind a call's chunks.
 struct Space {
-  int32_t* first;
+  int32_t *first, *order;
   unsigned char* tri;
   Gates* gates;
   float* after;
   uint16_t* writes;
-  float* shared;
   size_t bytes;
 };
 inline int64_t max_chunks(int64_t n_tokens, int64_t n_seqs) {

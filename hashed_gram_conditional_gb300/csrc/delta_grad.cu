@@ -41,7 +41,9 @@ __global__ void __launch_bounds__(NQ * 128, 1) back_kernel(Args<E> a) {
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t2 = (lane & 3) * 2;
   const int quad = tid >> 7, w = ((tid >> 5) + quad) & 3;
-  const int seq = blockIdx.x, h = blockIdx.y, v0 = blockIdx.z * (16 * NQ), cols = min(a.dv - v0, 16 * NQ);
+  int seq, h, v0;
+  place_of(a, 16 * NQ, seq, h, v0);
+  const int cols = min(a.dv - v0, 16 * NQ);
   const int hk = h / (a.heads / a.keys), vw = v0 + quad * 16;
   int lo, hi;
   bounds(a, seq, lo, hi);
@@ -270,17 +272,19 @@ struct Grads {
   static constexpr int kHeadBytes = kO * kTerm + static_cast<int>(sizeof(Gates));
   static constexpr int kNum = kHead + kStages * kHeadBytes;                   // sums
   static constexpr int kSums = kParts * kC * 4 + 4 * kC + 4 * kParts;         // floats
+  // R = scale e^c dY, W- = -e^c dV and U+ = e^(c_last - c) U of the slice; when a head's
+  // slices are done F and E, in their place
   static constexpr int kF = (kNum + kSums * 4 + 127) / 128 * 128, kE = kF + kO * mat_bytes(kC, kC);
-  static constexpr int kU = E::kBytes == 2 ? kE + kO * mat_bytes(kC, kC) : kF;
+  static constexpr int kR = kF, kWn = kR + kO * mat_bytes(kC, VS), kUl = kWn + kO * mat_bytes(kC, VS);
+  static constexpr int kEndF = kE + kO * mat_bytes(kC, kC), kEndR = kUl + kO * mat_bytes(kC, VS);
+  static constexpr int kU = kStages == 2 && kEndF > kEndR ? kEndF : kEndR;  // (fp32: F and E lie over U and the slice too)
   static constexpr int kSlice = (kU + kO * mat_bytes(kC, VS) + 127) / 128 * 128;
   // a slice of the value columns: S^T, dS^T, V then V - e^c K S, dY, dV
   static constexpr int kState = E::kBytes == 2 ? VS / 16 * (KD / 16) * kBlockBytes : kO * mat_bytes(VS, KD);
   static constexpr int kS = 0, kD = kS + kState, kX = kD + kState;
   static constexpr int kY = kX + kO * mat_bytes(kC, VS), kW = kY + kIn<E> * mat_bytes(kC, VS);
   static constexpr int kSliceBytes = kW + kO * mat_bytes(kC, VS);
-  // (fp32: F and E lie over U and the slice)
-  static constexpr int kEnd = kSlice + kStages * kSliceBytes, kEnd2 = kE + kO * mat_bytes(kC, kC);
-  static constexpr int kSmem = kEnd > kEnd2 ? kEnd : kEnd2;
+  static constexpr int kEnd = kSlice + kStages * kSliceBytes, kSmem = kEnd > kEndF ? kEnd : kEndF;
   static constexpr int kN = VS / 8 / kParts, kCN = kC / 8 / kParts, kKN = KD / 8 / kParts;  // a warp's tiles of 8 columns
 };
 
@@ -407,6 +411,7 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
   const size_t saved = saved_floats<E>(a.dk, a.dv);
   const Mat K = mat<kC, KD>(base + L::kK), Q = mat<kC, KD>(base + L::kQ), U = mat<kC, VS>(base + L::kU);
   const Mat Fm = mat<kC, kC>(base + L::kF), Em = mat<kC, kC>(base + L::kE);
+  const Mat R = mat<kC, VS>(base + L::kR), Wn = mat<kC, VS>(base + L::kWn), Ul = mat<kC, VS>(base + L::kUl);
   float* sums = reinterpret_cast<float*>(smem + L::kNum);
   float *reads = sums, *writes = reads + kParts * kC, *rows = writes + kParts * kC, *own = rows + kParts * kC, *columns = own + kParts * kC,
         *wholes = columns + 4 * kC;
@@ -449,16 +454,16 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
     product<kIn<E>, kIn<E>, kIn<E>>(qk, Rows{Q}, Across{K}, m, nc, 0, KD);
     product<kIn<E>, kIn<E>, kIn<E>>(kk, Rows{K}, Across{K}, m, nc, 0, KD);
   }
+  float cq[L::kKN][4], ck[L::kKN][4];  // dQ and dK, of all heads that share the key
+  clear(cq);
+  clear(ck);
   for (int h = hk * group; h < (hk + 1) * group; ++h) {
     const Gates& gt = *reinterpret_cast<const Gates*>(smem + L::kHead + (h % L::kStages) * L::kHeadBytes + kO * kTerm);
     const uint32_t M = base + L::kHead + (h % L::kStages) * L::kHeadBytes;
-    float cf[L::kCN][4], ce[L::kCN][4], cq[L::kKN][4], ck[L::kKN][4], cw[L::kKN][4];
-    float dot[2] = {0.f, 0.f}, whole = 0.f;
+    float cf[L::kCN][4], ce[L::kCN][4];
+    float dot[2] = {0.f, 0.f}, read[2] = {0.f, 0.f}, write[2] = {0.f, 0.f}, whole = 0.f;
     clear(cf);
     clear(ce);
-    clear(cq);
-    clear(ck);
-    clear(cw);
     for (int sl = 0; sl < slices; ++sl) {
       const int step = (h - hk * group) * slices + sl;
       const uint32_t at = base + L::kSlice + (step % L::kStages) * L::kSliceBytes;
@@ -491,23 +496,39 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
           whole = fmaf(s[0], d[0], fmaf(s[1], d[1], whole));
         }
       }
-      float x[L::kN][4];
+      // K S, Q S and K dS at the warp's places: X, and what reads S
+      float x[L::kN][4], xq[L::kN][4], xd[L::kN][4];
       clear(x);
+      clear(xq);
+      clear(xd);
       product<kIn<E>, kO, kO>(x, Rows{K}, state_across<E, KD, VS>(at + L::kS), m, nn, 0, KD);
+      product<kIn<E>, kO, kO>(xq, Rows{Q}, state_across<E, KD, VS>(at + L::kS), m, nn, 0, KD);
+      product<kIn<E>, kO, kO>(xd, Rows{K}, state_across<E, KD, VS>(at + L::kD), m, nn, 0, KD);
 #pragma unroll
       for (int t = 0; t < L::kN; ++t)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int r = m + g + j * 8, c = nn + t * 8 + t2;
-          const uint32_t to = X.base + r * X.pitch + c * 2;
-          float v[2];
-          get<kIn<E>>(to, X.term, v[0], v[1]);
-          const float into = gt.into[r];
-          put<kO>(to, X.term, fmaf(-into, x[t][2 * j], v[0]), fmaf(-into, x[t][2 * j + 1], v[1]));
+          const uint32_t off = r * X.pitch + c * 2;
+          float v[2], y[2], w[2];
+          get<kIn<E>>(X.base + off, X.term, v[0], v[1]);
+          get<kIn<E>>(Y.base + off, Y.term, y[0], y[1]);
+          get<kO>(W.base + off, W.term, w[0], w[1]);
+          const float into = gt.into[r], from = a.scale * into;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            v[e] = fmaf(-into, x[t][2 * j + e], v[e]);
+            y[e] *= from;
+            w[e] *= -into;
+            read[j] = fmaf(y[e], xq[t][2 * j + e], fmaf(w[e], x[t][2 * j + e], read[j]));
+          }
+          put<kO>(X.base + off, X.term, v[0], v[1]);
+          put<kO>(R.base + off, R.term, y[0], y[1]);
+          put<kO>(Wn.base + off, Wn.term, w[0], w[1]);
         }
-      // what reads S does not wait for U
-      both_products<kIn<E>, kO>(cq, ck, Rows{Y}, Rows{W}, S, m, nk, VS);
       __syncthreads();
+      product<kO, kO, kO>(cq, Rows{R}, S, m, nk, 0, VS);
+      product<kO, kO, kO>(ck, Rows{Wn}, S, m, nk, 0, VS);
       clear(x);
       product<kO, kO, kO>(x, TriRows{M}, Down{X}, m, nn, 0, m + 16);
 #pragma unroll
@@ -515,14 +536,18 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int r = m + g + j * 8, c = nn + t * 8 + t2;
-          put<kO>(U.base + r * U.pitch + c * 2, U.term, x[t][2 * j], x[t][2 * j + 1]);
+          const uint32_t off = r * U.pitch + c * 2;
+          put<kO>(U.base + off, U.term, x[t][2 * j], x[t][2 * j + 1]);
+          const float last = gt.last[r], l0 = last * x[t][2 * j], l1 = last * x[t][2 * j + 1];
+          put<kO>(Ul.base + off, Ul.term, l0, l1);
           float w[2];
-          get<kO>(W.base + r * W.pitch + c * 2, W.term, w[0], w[1]);
+          get<kO>(W.base + off, W.term, w[0], w[1]);
           dot[j] = fmaf(w[0], x[t][2 * j], fmaf(w[1], x[t][2 * j + 1], dot[j]));
+          write[j] = fmaf(l0, xd[t][2 * j], fmaf(l1, xd[t][2 * j + 1], write[j]));
         }
       __syncthreads();
       if (low) both_products<kIn<E>, kO>(cf, ce, Rows{Y}, Rows{W}, Across{U}, m, nc, VS);
-      product<kO, kO, kO>(cw, Rows{U}, D, m, nk, 0, VS);
+      product<kO, kO, kO>(ck, Rows{Ul}, D, m, nk, 0, VS);
     }
     // ---- F and E, the pairs of reads and writes, and what reads S and reaches dS
     float row[2] = {0.f, 0.f};
@@ -549,26 +574,9 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
         column += __shfl_xor_sync(0xffffffffu, column, 16);
         if (g == 0) columns[(m >> 4) * kC + i] = column;
       }
-    float read[2] = {0.f, 0.f}, write[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int r = m + g + j * 8;
-      const float into = gt.into[r], last = gt.last[r];
-#pragma unroll
-      for (int t = 0; t < L::kKN; ++t) {
-        const uint32_t at = r * K.pitch + (nk + t * 8 + t2) * 2;
-        float q[2], k[2];
-        get<kIn<E>>(Q.base + at, Q.term, q[0], q[1]);
-        get<kIn<E>>(K.base + at, K.term, k[0], k[1]);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          cq[t][2 * j + e] *= a.scale * into;
-          const float seen = -into * ck[t][2 * j + e], left = last * cw[t][2 * j + e];
-          read[j] = fmaf(q[e], cq[t][2 * j + e], fmaf(k[e], seen, read[j]));
-          write[j] = fmaf(k[e], left, write[j]);
-          ck[t][2 * j + e] = seen + left;
-        }
-      }
       const float sum_row = quad_sum(row[j]), sum_read = quad_sum(read[j]), sum_write = quad_sum(write[j]),
                   sum_own = quad_sum(dot[j]);
       if (t2 == 0) {
@@ -597,35 +605,6 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
     product<kO, kIn<E>, kO>(ck, Rows{Em}, Down{K}, m, nk, 0, m + 16);
     product<kO, kIn<E>, kO>(ck, Cols{Em}, Down{K}, m, nk, m, kC);
     product<kO, kIn<E>, kO>(ck, Cols{Fm}, Down{Q}, m, nk, m, kC);
-    // ---- out; heads that share a key are added up in order, each thread its own elements
-    const bool begins = h == hk * group, ends = h + 1 == (hk + 1) * group;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int r = m + g + j * 8;
-      if (r >= ch.len) continue;
-      const bool on = !(mask != nullptr && mask[r]);
-      float* all = a.shared + ((p + r) * a.keys + hk) * a.dk;
-      float* all_k = all + static_cast<int64_t>(a.n_tokens) * a.keys * a.dk;
-#pragma unroll
-      for (int t = 0; t < L::kKN; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int c = nk + t * 8 + t2 + e;
-          if (c >= a.dk) continue;
-          float x = cq[t][2 * j + e], y = ck[t][2 * j + e];
-          if (!begins) {
-            x += all[c];
-            y += all_k[c];
-          }
-          if (!ends) {
-            all[c] = x;
-            all_k[c] = y;
-          } else {
-            E::store(a.dq + (p + r) * a.dq_stride + hk * a.dk + c, on ? x : 0.f);
-            E::store(a.dk_out + (p + r) * a.dk_stride + hk * a.dk + c, on ? y : 0.f);
-          }
-        }
-    }
     if (warp == 0) {  // what crosses a position: two positions a lane
       float later[2], before[2];
 #pragma unroll
@@ -668,6 +647,23 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
       }
     }
   }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int r = m + g + j * 8;
+    if (r >= ch.len) continue;
+    const bool on = !(mask != nullptr && mask[r]);
+    auto* to_q = a.dq + (p + r) * a.dq_stride + hk * a.dk;
+    auto* to_k = a.dk_out + (p + r) * a.dk_stride + hk * a.dk;
+#pragma unroll
+    for (int t = 0; t < L::kKN; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = nk + t * 8 + t2 + e;
+        if (c >= a.dk) continue;
+        E::store(to_q + c, on ? cq[t][2 * j + e] : 0.f);
+        E::store(to_k + c, on ? ck[t][2 * j + e] : 0.f);
+      }
+  }
 }
 
 template <class E>
@@ -684,7 +680,9 @@ int launch_grad(const Args<E>& a, int sms, cudaStream_t st) {
   constexpr int VG = E::kBytes == 2 ? 32 : 16;
   const dim3 grads(a.max_chunks, a.keys);
   auto back = [&](auto kernel, int smem, int nq, std::atomic<uint64_t>& flag) {
-    return go(kernel, smem, dim3(a.n_seqs, a.heads, (a.dv + 16 * nq - 1) / (16 * nq)), flag, "back_kernel", nq * 128);
+    const int64_t blocks = static_cast<int64_t>(a.n_seqs) * a.heads * ((a.dv + 16 * nq - 1) / (16 * nq));
+    if (blocks > 0x7fffffff) return fail(ENGRAM_E_RANGE, "too many sequences times heads");
+    return go(kernel, smem, dim3(static_cast<unsigned>(blocks)), flag, "back_kernel", nq * 128);
   };
   bool many = false;
   if constexpr (E::kBytes == 2) {
@@ -795,11 +793,11 @@ extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void
     a.status = status_d;
     const Space s = space(workspace_d, n_tokens, n_seqs, key_heads, heads, dk, dv, true);
     a.first = s.first;
+    a.order = s.order;
     a.tri = s.tri;
     a.gates = s.gates;
     a.after = s.after;
     a.writes = s.writes;
-    a.shared = s.shared;
     return launch_grad<E>(a, sms, as_stream(stream));
   };
   return type == ENGRAM_T_BF16 ? go(train::Bf16{}) : go(train::F32{});
