@@ -466,6 +466,20 @@ __global__ void __launch_bounds__(NQ * 128, 1) scan_kernel(Args<E> a) {
       uint32_t f[kO][4], fl[kS][4];
       as_operand<kO>(f, u[0], u[1]);
       hand<kO>(own + L::kU + w * (kO * 512), f);
+      if (a.carry != nullptr) {  // for the backward pass
+        const int64_t p = lo + static_cast<int64_t>(i) * kC, wide = static_cast<int64_t>(a.heads) * a.dv;
+        auto* to = kept_writes<E>(a) + p * wide + static_cast<int64_t>(h) * a.dv;
+        const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
+        store_rows<E>(to, wide, w * 16, len, vw, a.dv, a.dv % 2 == 0, gt.beta, u);
+        if constexpr (E::kBytes == 2) {
+          float rest[2][4];
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) rest[t][j] = u[t][j] - lo_of(pack(u[t][j], 0.f));
+          store_rows<E>(to + a.n_tokens * wide, wide, w * 16, len, vw, a.dv, a.dv % 2 == 0, gt.beta, rest);
+        }
+      }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const float2 last = *reinterpret_cast<const float2*>(&gt.last[w * 16 + t * 8 + t2]);
@@ -675,6 +689,9 @@ Space space(void* base, int64_t n_tokens, int64_t n_seqs, int32_t keys, int32_t 
   if (backward) {
     s.after = reinterpret_cast<float*>(take(units * saved_floats<train::Bf16>(dk, dv) * sizeof(float)));
     s.writes = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(n_tokens) * heads * dv * sizeof(uint16_t)));
+    // (a block's threads leave a chunk's sums, 64 x 128 of queries and of keys, as they hold them)
+    if (heads > keys)
+      s.shared = reinterpret_cast<float*>(take(static_cast<size_t>(max_chunks(n_tokens, n_seqs)) * keys * 2 * kC * (dk <= 64 ? 64 : 128) * sizeof(float)));
   }
   s.bytes = at;
   return s;
@@ -689,7 +706,8 @@ using namespace engram::delta;
 extern "C" size_t engram_delta_carry_bytes(int64_t n_tokens, int64_t n_seqs, int32_t heads, int32_t dk, int32_t dv) {
   if (n_tokens < 0 || n_seqs < 0 || heads < 1 || dk < 1 || dv < 1) return 0;
   // (both types' room: bf16's blocks are padded, fp32's matrices are not)
-  return static_cast<size_t>(max_chunks(n_tokens, n_seqs)) * heads * saved_floats<train::Bf16>(dk, dv) * sizeof(float);
+  return (static_cast<size_t>(max_chunks(n_tokens, n_seqs)) * heads * saved_floats<train::Bf16>(dk, dv) +
+          static_cast<size_t>(n_tokens) * heads * dv) * sizeof(float);
 }
 
 extern "C" size_t engram_delta_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int32_t key_heads, int32_t heads, int32_t dk,

@@ -83,9 +83,10 @@ struct Args {
   unsigned char* tri;
   Gates* gates;
   // backward: states' gradients behind the chunks, as `carry` has the states in front of them; the second terms of
-  // the values' gradients (bf16)
+  // the values' gradients (bf16); sums over heads that share a key
   float* after;
   uint16_t* writes;
+  float* shared;
   int32_t* status;
 };
 
@@ -415,23 +416,6 @@ __device__ __forceinline__ void save_rows(float* to, int dk, int dv, int vw, int
   }
 }
 // S^T's blocks in shared memory as an operand B(k, n), 16 x 16 pieces
-struct BlocksAcross {  // k: rows of the state, n: columns
-  uint32_t base;
-  int across;  // blocks of rows
-  template <int N>
-  __device__ __forceinline__ void get(uint32_t (&r)[N][2], int k, int n, int t) const {
-    const int l = lane_id();
-    const uint32_t at = base + ((n >> 4) * across + (k >> 4)) * kBlockBytes + t * 512 + (l & 7) * 16;
-    if constexpr (N == 1) {
-      ld2(r[0][0], r[0][1], at + ((n >> 3) & 1) * 128 + ((l >> 3) & 1) * 256);
-    } else {
-      static_assert(N == 2, "a block's columns");
-      uint32_t w[4];
-      ld4(w, at + ((l >> 3) & 1) * 256 + (l >> 4) * 128);
-      r[0][0] = w[0]; r[0][1] = w[1]; r[1][0] = w[2]; r[1][1] = w[3];
-    }
-  }
-};
 struct BlocksDown {  // k: columns, n: rows
   uint32_t base;
   int across;
@@ -483,6 +467,13 @@ __device__ __forceinline__ size_t unit_of(const Args<E>& a, int chunk, int head)
   return static_cast<size_t>(chunk) * a.heads + head;
 }
 
+// Behind the states, `carry` has the writes U, [n_tokens][heads*dv]: fp32, or for inputs of
+// type bf16 two terms, one array behind the other.
+template <class E>
+__device__ __forceinline__ typename E::T* kept_writes(const Args<E>& a) {
+  return reinterpret_cast<typename E::T*>(a.carry + static_cast<size_t>(a.max_chunks) * a.heads * saved_floats<E>(a.dk, a.dv));
+}
+
 // The outputs (y, or the values' gradient) of a sequence without a slot, and the states
 // that it would have left for the backward pass.
 template <class E>
@@ -492,6 +483,12 @@ __device__ __forceinline__ void padding_zeros(const Args<E>& a, int lo, int hi, 
   for (int64_t i = threadIdx.x; i < static_cast<int64_t>(hi - lo) * cols; i += threads)
     E::store(out + (lo + i / cols) * stride + h * a.dv + v0 + i % cols, 0.f);
   if (a.y == nullptr || a.carry == nullptr) return;
+  const int64_t wide = static_cast<int64_t>(a.heads) * a.dv;
+  for (int64_t i = threadIdx.x; i < static_cast<int64_t>(hi - lo) * cols; i += threads) {
+    auto* to = kept_writes<E>(a) + (lo + i / cols) * wide + static_cast<int64_t>(h) * a.dv + v0 + i % cols;
+    E::store(to, 0.f);
+    if (E::kBytes == 2) E::store(to + a.n_tokens * wide, 0.f);
+  }
   const size_t saved = saved_floats<E>(a.dk, a.dv), at = v0 == 0 ? 0 : saved_floats<E>(a.dk, v0);
   const size_t mine = saved_floats<E>(a.dk, cols);
   for (int c = 0; c < n; ++c)
@@ -600,6 +597,7 @@ struct Space {
   Gates* gates;
   float* after;
   uint16_t* writes;
+  float* shared;
   size_t bytes;
 };
 inline int64_t max_chunks(int64_t n_tokens, int64_t n_seqs) {

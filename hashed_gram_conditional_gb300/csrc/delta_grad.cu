@@ -10,7 +10,7 @@
 //   db_t = (dV_t . U_t) (1 - beta_t) / beta_t
 //   dg_t = (1 - f_t) (what crosses t: reads of S at t and later, writes before t that
 //          reach dS, pairs of the two of them, and e^c_last S . dS)
-// The states in front of the chunks come from the forward pass; U, M and P are
+// The states in front of the chunks and U come from the forward pass; M and P are
 // computed again.
 #include "delta_device.cuh"
 
@@ -268,24 +268,19 @@ struct Grads {
   static constexpr int kO = kOut<E>, kStages = E::kBytes == 2 ? 2 : 1, kParts = E::kBytes == 2 ? 4 : 2;
   static constexpr int kT = 4 * kParts * 32;  // threads
   static constexpr int kK = 0, kQ = kK + kIn<E> * mat_bytes(kC, KD);
-  static constexpr int kHead = kQ + kIn<E> * mat_bytes(kC, KD);  // M and the gates, of this head and the next
-  static constexpr int kHeadBytes = kO * kTerm + static_cast<int>(sizeof(Gates));
+  static constexpr int kHead = kQ + kIn<E> * mat_bytes(kC, KD);  // the gates, of this head and the next
+  static constexpr int kHeadBytes = static_cast<int>(sizeof(Gates));
   static constexpr int kNum = kHead + kStages * kHeadBytes;                   // sums
   static constexpr int kSums = kParts * kC * 4 + 4 * kC + 4 * kParts;         // floats
-  // R = scale e^c dY, W- = -e^c dV and U+ = e^(c_last - c) U of the slice; when a head's
-  // slices are done F and E, in their place
   static constexpr int kF = (kNum + kSums * 4 + 127) / 128 * 128, kE = kF + kO * mat_bytes(kC, kC);
-  static constexpr int kR = kF, kWn = kR + kO * mat_bytes(kC, VS), kUl = kWn + kO * mat_bytes(kC, VS);
-  static constexpr int kEndF = kE + kO * mat_bytes(kC, kC), kEndR = kUl + kO * mat_bytes(kC, VS);
-  static constexpr int kU = kStages == 2 && kEndF > kEndR ? kEndF : kEndR;  // (fp32: F and E lie over U and the slice too)
-  static constexpr int kSlice = (kU + kO * mat_bytes(kC, VS) + 127) / 128 * 128;
-  // a slice of the value columns: S^T, dS^T, V then V - e^c K S, dY, dV
+  static constexpr int kEndF = kE + kO * mat_bytes(kC, kC);
+  static constexpr int kSlice = kStages == 2 ? kEndF : kF;  // (fp32: F and E lie over the slice)
+  // a slice of the value columns: S^T, dS^T, dY, dV, U
   static constexpr int kState = E::kBytes == 2 ? VS / 16 * (KD / 16) * kBlockBytes : kO * mat_bytes(VS, KD);
-  static constexpr int kS = 0, kD = kS + kState, kX = kD + kState;
-  static constexpr int kY = kX + kO * mat_bytes(kC, VS), kW = kY + kIn<E> * mat_bytes(kC, VS);
-  static constexpr int kSliceBytes = kW + kO * mat_bytes(kC, VS);
+  static constexpr int kS = 0, kD = kS + kState, kY = kD + kState, kW = kY + kIn<E> * mat_bytes(kC, VS);
+  static constexpr int kU = kW + kO * mat_bytes(kC, VS), kSliceBytes = kU + kO * mat_bytes(kC, VS);
   static constexpr int kEnd = kSlice + kStages * kSliceBytes, kSmem = kEnd > kEndF ? kEnd : kEndF;
-  static constexpr int kN = VS / 8 / kParts, kCN = kC / 8 / kParts, kKN = KD / 8 / kParts;  // a warp's tiles of 8 columns
+  static constexpr int kCN = kC / 8 / kParts, kKN = KD / 8 / kParts;  // a warp's tiles of 8 columns
 };
 
 // `cols` columns of a saved state, from column v0 on, zeros around them.
@@ -331,12 +326,7 @@ __device__ __forceinline__ void load_state(uint32_t to, const float* from, int v
   }
 }
 
-// S^T in shared memory as an operand: rows as k (of K S) or as n (of dY S^T).
-template <class E, int KD, int VS>
-__device__ __forceinline__ auto state_across(uint32_t at) {
-  if constexpr (E::kBytes == 2) return BlocksAcross{at, KD / 16};
-  else return Across{mat<VS, KD>(at)};
-}
+// S^T in shared memory as an operand B, its columns as k.
 template <class E, int KD, int VS>
 __device__ __forceinline__ auto state_down(uint32_t at) {
   if constexpr (E::kBytes == 2) return BlocksDown{at, KD / 16};
@@ -409,31 +399,29 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
   }
   const uint8_t* mask = a.mask != nullptr ? a.mask + p : nullptr;
   const size_t saved = saved_floats<E>(a.dk, a.dv);
-  const Mat K = mat<kC, KD>(base + L::kK), Q = mat<kC, KD>(base + L::kQ), U = mat<kC, VS>(base + L::kU);
+  const Mat K = mat<kC, KD>(base + L::kK), Q = mat<kC, KD>(base + L::kQ);
   const Mat Fm = mat<kC, kC>(base + L::kF), Em = mat<kC, kC>(base + L::kE);
-  const Mat R = mat<kC, VS>(base + L::kR), Wn = mat<kC, VS>(base + L::kWn), Ul = mat<kC, VS>(base + L::kUl);
   float* sums = reinterpret_cast<float*>(smem + L::kNum);
   float *reads = sums, *writes = reads + kParts * kC, *rows = writes + kParts * kC, *own = rows + kParts * kC, *columns = own + kParts * kC,
         *wholes = columns + 4 * kC;
   const int slices = (a.dv + VS - 1) / VS, steps = group * slices;
-  auto load = [&](int step) {  // of a head's slice, and with the first one M and the gates
+  auto load = [&](int step) {  // of a head's slice, and with the first one the gates
     const int h = hk * group + step / slices, v0 = step % slices * VS, cols = a.dv - v0 < VS ? a.dv - v0 : VS;
     const size_t unit = unit_of(a, blockIdx.x, h);
     const uint32_t at = base + L::kSlice + (step % L::kStages) * L::kSliceBytes;
     const int64_t column = static_cast<int64_t>(h) * a.dv + v0;
-    if (v0 == 0) {
-      const uint32_t to = base + L::kHead + (h % L::kStages) * L::kHeadBytes;
-      for (int i = tid; i < kO * kTerm / 16; i += kT) copy16(to + i * 16, a.tri + unit * kTriBytes + i * 16, true);
-      load_gates<kT>(to + kO * kTerm, a.gates + unit);
-    }
-    load_rows<E, VS, kT>(mat<kC, VS>(at + L::kX), a.v + p * a.v_stride + column, a.v_stride, ch.len, cols, mask, a.vec);
+    if (v0 == 0) load_gates<kT>(base + L::kHead + (h % L::kStages) * L::kHeadBytes, a.gates + unit);
     load_rows<E, VS, kT>(mat<kC, VS>(at + L::kY), a.dy + p * a.dy_stride + column, a.dy_stride, ch.len, cols, mask, a.vec);
-    const Mat W = mat<kC, VS>(at + L::kW);
+    // of type bf16 dV's first term is the output, and U's terms are kept apart
+    const int64_t wide = static_cast<int64_t>(a.heads) * a.dv;
+    const Mat W = mat<kC, VS>(at + L::kW), U = mat<kC, VS>(at + L::kU);
+    const auto* kept = kept_writes<E>(a) + p * wide + column;
     load_rows<E, VS, kT>(W, a.dv_out + p * a.dv_stride + column, a.dv_stride, ch.len, cols, nullptr, a.vec);
+    load_rows<E, VS, kT>(U, kept, wide, ch.len, cols, nullptr, a.vec);
     if constexpr (E::kBytes == 2) {
-      const int64_t wide = static_cast<int64_t>(a.heads) * a.dv;
-      load_rows<E, VS, kT>(Mat{W.base + static_cast<uint32_t>(W.term), W.pitch, W.term}, a.writes + p * wide + column, wide, ch.len,
-                       cols, nullptr, a.vec);
+      auto second = [](const Mat& m) { return Mat{m.base + static_cast<uint32_t>(m.term), m.pitch, m.term}; };
+      load_rows<E, VS, kT>(second(W), a.writes + p * wide + column, wide, ch.len, cols, nullptr, a.vec);
+      load_rows<E, VS, kT>(second(U), kept + a.n_tokens * wide, wide, ch.len, cols, nullptr, a.vec);
     }
     load_state<E, KD, VS, kT>(at + L::kS, a.carry + unit * saved, v0, cols, a.dk, a.vec);
     load_state<E, KD, VS, kT>(at + L::kD, a.after + unit * saved, v0, cols, a.dk, a.vec);
@@ -445,7 +433,7 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
   copies_done();
   __syncthreads();
   // a warp's tiles: 16 rows, and a part of the columns
-  const int m = (warp & 3) * 16, part = warp >> 2, nn = part * (VS / kParts), nc = part * (kC / kParts), nk = part * (KD / kParts);
+  const int m = (warp & 3) * 16, part = warp >> 2, nc = part * (kC / kParts), nk = part * (KD / kParts);
   const bool low = nc <= m;  // whether its tile of a triangle has anything
   float qk[L::kCN][4], kk[L::kCN][4];
   clear(qk);
@@ -454,21 +442,20 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
     product<kIn<E>, kIn<E>, kIn<E>>(qk, Rows{Q}, Across{K}, m, nc, 0, KD);
     product<kIn<E>, kIn<E>, kIn<E>>(kk, Rows{K}, Across{K}, m, nc, 0, KD);
   }
-  float cq[L::kKN][4], ck[L::kKN][4];  // dQ and dK, of all heads that share the key
-  clear(cq);
-  clear(ck);
   for (int h = hk * group; h < (hk + 1) * group; ++h) {
-    const Gates& gt = *reinterpret_cast<const Gates*>(smem + L::kHead + (h % L::kStages) * L::kHeadBytes + kO * kTerm);
-    const uint32_t M = base + L::kHead + (h % L::kStages) * L::kHeadBytes;
-    float cf[L::kCN][4], ce[L::kCN][4];
-    float dot[2] = {0.f, 0.f}, read[2] = {0.f, 0.f}, write[2] = {0.f, 0.f}, whole = 0.f;
+    const Gates& gt = *reinterpret_cast<const Gates*>(smem + L::kHead + (h % L::kStages) * L::kHeadBytes);
+    float cf[L::kCN][4], ce[L::kCN][4], cq[L::kKN][4], ck[L::kKN][4], cw[L::kKN][4];
+    float whole = 0.f, dot = 0.f;
     clear(cf);
     clear(ce);
+    clear(cq);
+    clear(ck);
+    clear(cw);
     for (int sl = 0; sl < slices; ++sl) {
       const int step = (h - hk * group) * slices + sl;
       const uint32_t at = base + L::kSlice + (step % L::kStages) * L::kSliceBytes;
       const auto S = state_down<E, KD, VS>(at + L::kS), D = state_down<E, KD, VS>(at + L::kD);
-      const Mat X = mat<kC, VS>(at + L::kX), Y = mat<kC, VS>(at + L::kY), W = mat<kC, VS>(at + L::kW);
+      const Mat Y = mat<kC, VS>(at + L::kY), W = mat<kC, VS>(at + L::kW), U = mat<kC, VS>(at + L::kU);
       if (L::kStages == 1 && step > 0) {
         __syncthreads();  // the slice before has been used
         load(step);
@@ -496,58 +483,21 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
           whole = fmaf(s[0], d[0], fmaf(s[1], d[1], whole));
         }
       }
-      // K S, Q S and K dS at the warp's places: X, and what reads S
-      float x[L::kN][4], xq[L::kN][4], xd[L::kN][4];
-      clear(x);
-      clear(xq);
-      clear(xd);
-      product<kIn<E>, kO, kO>(x, Rows{K}, state_across<E, KD, VS>(at + L::kS), m, nn, 0, KD);
-      product<kIn<E>, kO, kO>(xq, Rows{Q}, state_across<E, KD, VS>(at + L::kS), m, nn, 0, KD);
-      product<kIn<E>, kO, kO>(xd, Rows{K}, state_across<E, KD, VS>(at + L::kD), m, nn, 0, KD);
+      // dV . U of the block's positions: kT / 64 neighbouring threads a position
+      {
+        constexpr int kBy = kT / kC, kPairs = VS / 2 / kBy;
+        const uint32_t off = (tid / kBy) * W.pitch + tid % kBy * kPairs * 4;
 #pragma unroll
-      for (int t = 0; t < L::kN; ++t)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = m + g + j * 8, c = nn + t * 8 + t2;
-          const uint32_t off = r * X.pitch + c * 2;
-          float v[2], y[2], w[2];
-          get<kIn<E>>(X.base + off, X.term, v[0], v[1]);
-          get<kIn<E>>(Y.base + off, Y.term, y[0], y[1]);
-          get<kO>(W.base + off, W.term, w[0], w[1]);
-          const float into = gt.into[r], from = a.scale * into;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            v[e] = fmaf(-into, x[t][2 * j + e], v[e]);
-            y[e] *= from;
-            w[e] *= -into;
-            read[j] = fmaf(y[e], xq[t][2 * j + e], fmaf(w[e], x[t][2 * j + e], read[j]));
-          }
-          put<kO>(X.base + off, X.term, v[0], v[1]);
-          put<kO>(R.base + off, R.term, y[0], y[1]);
-          put<kO>(Wn.base + off, Wn.term, w[0], w[1]);
+        for (int i = 0; i < kPairs; ++i) {
+          float u[2], w[2];
+          get<kO>(U.base + off + i * 4, U.term, u[0], u[1]);
+          get<kO>(W.base + off + i * 4, W.term, w[0], w[1]);
+          dot = fmaf(u[0], w[0], fmaf(u[1], w[1], dot));
         }
-      __syncthreads();
-      product<kO, kO, kO>(cq, Rows{R}, S, m, nk, 0, VS);
-      product<kO, kO, kO>(ck, Rows{Wn}, S, m, nk, 0, VS);
-      clear(x);
-      product<kO, kO, kO>(x, TriRows{M}, Down{X}, m, nn, 0, m + 16);
-#pragma unroll
-      for (int t = 0; t < L::kN; ++t)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = m + g + j * 8, c = nn + t * 8 + t2;
-          const uint32_t off = r * U.pitch + c * 2;
-          put<kO>(U.base + off, U.term, x[t][2 * j], x[t][2 * j + 1]);
-          const float last = gt.last[r], l0 = last * x[t][2 * j], l1 = last * x[t][2 * j + 1];
-          put<kO>(Ul.base + off, Ul.term, l0, l1);
-          float w[2];
-          get<kO>(W.base + off, W.term, w[0], w[1]);
-          dot[j] = fmaf(w[0], x[t][2 * j], fmaf(w[1], x[t][2 * j + 1], dot[j]));
-          write[j] = fmaf(l0, xd[t][2 * j], fmaf(l1, xd[t][2 * j + 1], write[j]));
-        }
-      __syncthreads();
+      }
+      both_products<kIn<E>, kO>(cq, ck, Rows{Y}, Rows{W}, S, m, nk, VS);
+      product<kO, kO, kO>(cw, Rows{U}, D, m, nk, 0, VS);
       if (low) both_products<kIn<E>, kO>(cf, ce, Rows{Y}, Rows{W}, Across{U}, m, nc, VS);
-      product<kO, kO, kO>(ck, Rows{Ul}, D, m, nk, 0, VS);
     }
     // ---- F and E, the pairs of reads and writes, and what reads S and reaches dS
     float row[2] = {0.f, 0.f};
@@ -577,15 +527,33 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int r = m + g + j * 8;
-      const float sum_row = quad_sum(row[j]), sum_read = quad_sum(read[j]), sum_write = quad_sum(write[j]),
-                  sum_own = quad_sum(dot[j]);
+      const float into = gt.into[r], last = gt.last[r];
+      float read = 0.f, write = 0.f;
+#pragma unroll
+      for (int t = 0; t < L::kKN; ++t) {
+        const uint32_t at = r * K.pitch + (nk + t * 8 + t2) * 2;
+        float q[2], k[2];
+        get<kIn<E>>(Q.base + at, Q.term, q[0], q[1]);
+        get<kIn<E>>(K.base + at, K.term, k[0], k[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          cq[t][2 * j + e] *= a.scale * into;
+          const float seen = -into * ck[t][2 * j + e], left = last * cw[t][2 * j + e];
+          read = fmaf(q[e], cq[t][2 * j + e], fmaf(k[e], seen, read));
+          write = fmaf(k[e], left, write);
+          ck[t][2 * j + e] = seen + left;
+        }
+      }
+      const float sum_row = quad_sum(row[j]), sum_read = quad_sum(read), sum_write = quad_sum(write);
       if (t2 == 0) {
         rows[part * kC + r] = sum_row;
         reads[part * kC + r] = sum_read;
         writes[part * kC + r] = sum_write;
-        own[part * kC + r] = sum_own;
       }
     }
+#pragma unroll
+    for (int o = kT / kC / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (tid % (kT / kC) == 0) own[tid / (kT / kC)] = dot;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, o);
     if (lane == 0) wholes[warp] = whole;
@@ -605,6 +573,49 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
     product<kO, kIn<E>, kO>(ck, Rows{Em}, Down{K}, m, nk, 0, m + 16);
     product<kO, kIn<E>, kO>(ck, Cols{Em}, Down{K}, m, nk, m, kC);
     product<kO, kIn<E>, kO>(ck, Cols{Fm}, Down{Q}, m, nk, m, kC);
+    // ---- heads that share a key are added up in order, each thread its own elements
+    const bool begins = h == hk * group, ends = h + 1 == (hk + 1) * group;
+    if (!(begins && ends)) {
+      float4* all = reinterpret_cast<float4*>(a.shared) +
+                    (static_cast<size_t>(blockIdx.x) * a.keys + hk) * (2 * L::kKN * kT) + tid;
+      if (!begins) {
+        float4 x[2 * L::kKN];
+#pragma unroll
+        for (int t = 0; t < 2 * L::kKN; ++t) x[t] = all[t * kT];
+#pragma unroll
+        for (int t = 0; t < L::kKN; ++t) {
+          cq[t][0] += x[t].x; cq[t][1] += x[t].y; cq[t][2] += x[t].z; cq[t][3] += x[t].w;
+          const float4& y = x[t + L::kKN];
+          ck[t][0] += y.x; ck[t][1] += y.y; ck[t][2] += y.z; ck[t][3] += y.w;
+        }
+      }
+      if (!ends) {
+#pragma unroll
+        for (int t = 0; t < L::kKN; ++t) {
+          all[t * kT] = make_float4(cq[t][0], cq[t][1], cq[t][2], cq[t][3]);
+          all[(t + L::kKN) * kT] = make_float4(ck[t][0], ck[t][1], ck[t][2], ck[t][3]);
+        }
+      }
+    }
+    if (ends) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = m + g + j * 8;
+        if (r >= ch.len) continue;
+        const bool on = !(mask != nullptr && mask[r]);
+        auto* to_q = a.dq + (p + r) * a.dq_stride + hk * a.dk;
+        auto* to_k = a.dk_out + (p + r) * a.dk_stride + hk * a.dk;
+#pragma unroll
+        for (int t = 0; t < L::kKN; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int c = nk + t * 8 + t2 + e;
+            if (c >= a.dk) continue;
+            E::store(to_q + c, on ? cq[t][2 * j + e] : 0.f);
+            E::store(to_k + c, on ? ck[t][2 * j + e] : 0.f);
+          }
+      }
+    }
     if (warp == 0) {  // what crosses a position: two positions a lane
       float later[2], before[2];
 #pragma unroll
@@ -640,29 +651,9 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
         const int64_t t = p + r;
         const float gr = E::load(a.g + t * a.g_stride + h), br = E::load(a.b + t * a.b_stride + h);
         E::store(a.dg + t * a.dg_stride + h, on ? cross[j] / (1.f + expf(gr)) : 0.f);
-        float sum = 0.f;
-#pragma unroll
-        for (int n = 0; n < kParts; ++n) sum += own[n * kC + r];
-        E::store(a.db + t * a.db_stride + h, on ? sum / (gt.beta[r] * (1.f + expf(br))) : 0.f);
+        E::store(a.db + t * a.db_stride + h, on ? own[r] / (gt.beta[r] * (1.f + expf(br))) : 0.f);
       }
     }
-  }
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int r = m + g + j * 8;
-    if (r >= ch.len) continue;
-    const bool on = !(mask != nullptr && mask[r]);
-    auto* to_q = a.dq + (p + r) * a.dq_stride + hk * a.dk;
-    auto* to_k = a.dk_out + (p + r) * a.dk_stride + hk * a.dk;
-#pragma unroll
-    for (int t = 0; t < L::kKN; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int c = nk + t * 8 + t2 + e;
-        if (c >= a.dk) continue;
-        E::store(to_q + c, on ? cq[t][2 * j + e] : 0.f);
-        E::store(to_k + c, on ? ck[t][2 * j + e] : 0.f);
-      }
   }
 }
 
@@ -798,6 +789,7 @@ extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void
     a.gates = s.gates;
     a.after = s.after;
     a.writes = s.writes;
+    a.shared = s.shared;
     return launch_grad<E>(a, sms, as_stream(stream));
   };
   return type == ENGRAM_T_BF16 ? go(train::Bf16{}) : go(train::F32{});
