@@ -305,7 +305,7 @@ template int launch_prepare<train::F32>(const Args<train::F32>&, cudaStream_t);
 // on the way to shared memory and take the room.
 template <class E, int KD, int NQ>
 struct Scan {
-  static constexpr int kT = NQ * 128, kStages = E::kBytes == 2 ? 2 : 1, kB = kC / 16;
+  static constexpr int kT = kCopiers<NQ> ? kCopiers<NQ> : NQ * 128, kStages = E::kBytes == 2 ? 2 : 1, kB = kC / 16;
   static constexpr int kK = 0, kQ = kK + kIn<E> * mat_bytes(kC, KD), kV = kQ + kIn<E> * mat_bytes(kC, KD);
   static constexpr int kM = kV + kIn<E> * mat_bytes(kC, 16 * NQ), kP = kM + kStateTerms * kTerm, kG = kP + kOut<E> * kTerm;
   static constexpr int kStage = kG + static_cast<int>(sizeof(Gates)), kQuads = kStages * kStage;
@@ -316,7 +316,7 @@ struct Scan {
 };
 
 template <class E, int KD, int NQ>
-__global__ void __launch_bounds__(NQ * 128, 1) scan_kernel(Args<E> a) {
+__global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) scan_kernel(Args<E> a) {
   using L = Scan<E, KD, NQ>;
   constexpr int kT = L::kT, kI = kIn<E>, kO = kOut<E>, kS = kStateTerms, kB = L::kB, kR = KD / 64;  // kR: a warp's blocks of S^T
   extern __shared__ __align__(128) unsigned char smem[];
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(NQ * 128, 1) scan_kernel(Args<E> a) {
   int64_t slot;
   if (!live_slot(a, seq, slot)) {
     if (tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
-    padding_zeros(a, lo, hi, c0, n, h, v0, cols, kT);
+    padding_zeros(a, lo, hi, c0, n, h, v0, cols, blockDim.x);
     return;
   }
   const uint32_t own = base + L::kQuads + quad * L::kQuad;
@@ -366,23 +366,34 @@ __global__ void __launch_bounds__(NQ * 128, 1) scan_kernel(Args<E> a) {
       else save_rows(to, a.dk, a.dv, vw, kb * 16, S[2 * r], S[2 * r + 1]);
     }
   };
+  const int copier = tid - (kCopiers<NQ> ? NQ * 128 : 0);  // a copying thread's number
   auto load = [&](int i) {
     const uint32_t stage = base + (i % L::kStages) * L::kStage;
     const int64_t p = lo + static_cast<int64_t>(i) * kC;
     const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
     const uint8_t* mask = a.mask != nullptr ? a.mask + p : nullptr;
     const size_t unit = unit_of(a, c0 + i, h);
-    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kK), a.k + p * a.k_stride + hk * a.dk, a.k_stride, len, a.dk, mask, a.vec);
-    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kQ), a.q + p * a.q_stride + hk * a.dk, a.q_stride, len, a.dk, mask, a.vec);
+    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kK), a.k + p * a.k_stride + hk * a.dk, a.k_stride, len, a.dk, mask, a.vec, copier);
+    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kQ), a.q + p * a.q_stride + hk * a.dk, a.q_stride, len, a.dk, mask, a.vec, copier);
     load_rows<E, 16 * NQ, kT>(mat<kC, 16 * NQ>(stage + L::kV), a.v + p * a.v_stride + static_cast<int64_t>(h) * a.dv + v0,
-                              a.v_stride, len, cols, mask, a.vec);
-    load_tri<kO, kT>(stage + L::kM, stage + L::kP, a.tri + unit * kTriBytes);
-    load_gates<kT>(stage + L::kG, a.gates + unit);
+                              a.v_stride, len, cols, mask, a.vec, copier);
+    load_tri<kO, kT>(stage + L::kM, stage + L::kP, a.tri + unit * kTriBytes, copier);
+    load_gates<kT>(stage + L::kG, a.gates + unit, copier);
     copies_begun();
   };
+  if (kCopiers<NQ> && copier >= 0) {
+    if (n > 0) load(0);
+    for (int i = 0; i < n; ++i) {
+      copies_done();
+      __syncthreads();
+      if (L::kStages == 1 && i + 1 < n) __syncthreads();
+      if (i + 1 < n) load(i + 1);
+    }
+    return;
+  }
   if (n > 0) {
     hand_state(0);
-    load(0);
+    if (!kCopiers<NQ>) load(0);
   }
   for (int i = 0; i < n; ++i) {
     const uint32_t stage = base + (i % L::kStages) * L::kStage;
@@ -390,7 +401,7 @@ __global__ void __launch_bounds__(NQ * 128, 1) scan_kernel(Args<E> a) {
     const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
     copies_done();
     __syncthreads();  // the chunk and the states are here, and the other stage is free
-    if (L::kStages == 2 && i + 1 < n) load(i + 1);
+    if (!kCopiers<NQ> && L::kStages == 2 && i + 1 < n) load(i + 1);
     // ---- (K S)^T and (Q S)^T
     Sums<2, true> x;
     Sums<2, kO == 3> y;
@@ -437,8 +448,7 @@ __global__ void __launch_bounds__(NQ * 128, 1) scan_kernel(Args<E> a) {
         }
       }
       if constexpr (kO == 3) {
-        clear(y.small[0]);
-        clear(y.small[1]);
+        clear(y.small);
       }
       uint32_t f[kS][4];
       as_operand<kS>(f, c[0], c[1]);
@@ -534,7 +544,7 @@ __global__ void __launch_bounds__(NQ * 128, 1) scan_kernel(Args<E> a) {
                   hi - p < kC ? static_cast<int>(hi - p) : kC, vw, a.dv, a.pairs, gt.beta, out);
     if (L::kStages == 1 && i + 1 < n) {
       __syncthreads();  // the stage is free
-      load(i + 1);
+      if (!kCopiers<NQ>) load(i + 1);
     }
   }
   if (a.state_out != nullptr) {
@@ -550,7 +560,7 @@ int launch_scan(const Args<E>& a, int sms, cudaStream_t st) {
     if (r) return r;
     const int64_t blocks = static_cast<int64_t>(a.n_seqs) * a.heads * ((a.dv + 16 * nq - 1) / (16 * nq));
     if (blocks > 0x7fffffff) return fail(ENGRAM_E_RANGE, "too many sequences times heads");
-    kernel<<<static_cast<unsigned>(blocks), nq * 128, smem, st>>>(a);
+    kernel<<<static_cast<unsigned>(blocks), nq == 1 ? 128 + kCopiers<1> : nq * 128, smem, st>>>(a);
     return check_launch("scan_kernel");
   };
   static std::atomic<uint64_t> done[4] = {{0}, {0}, {0}, {0}};

@@ -190,11 +190,11 @@ __device__ __forceinline__ Mat mat(uint32_t base) { return Mat{base, (kCols + 8)
 // masked positions.  `src` is the first row's first element.
 template <class E, int kCols, int kT = kThreads>
 __device__ __forceinline__ void load_rows(const Mat& m, const typename E::T* src, int64_t stride, int len, int cols,
-                                          const uint8_t* mask, bool vec) {
+                                          const uint8_t* mask, bool vec, int tid = threadIdx.x) {
   if (E::kBytes == 2 && vec) {
 #pragma unroll
     for (int i0 = 0; i0 < kC * (kCols / 8); i0 += kT) {
-      const int i = i0 + threadIdx.x;
+      const int i = i0 + tid;
       if (kC * (kCols / 8) % kT != 0 && i >= kC * (kCols / 8)) break;
       const int r = i / (kCols / 8), c = i % (kCols / 8) * 8;
       const bool on = r < len && c < cols && !(mask != nullptr && mask[r]);
@@ -202,7 +202,7 @@ __device__ __forceinline__ void load_rows(const Mat& m, const typename E::T* src
     }
   } else {
     constexpr int kAhead = 4;  // pairs on their way at once
-    for (int i0 = threadIdx.x; i0 < kC * (kCols / 2); i0 += kAhead * kT) {
+    for (int i0 = tid; i0 < kC * (kCols / 2); i0 += kAhead * kT) {
       float x[kAhead][2];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
@@ -442,13 +442,13 @@ __device__ __forceinline__ void clear(float (&c)[N][4]) {
 
 // The chunk's triangles and gates, 16 bytes a copy.  kP: terms of P.
 template <int kP, int kT = kThreads>
-__device__ __forceinline__ void load_tri(uint32_t m, uint32_t p, const unsigned char* from) {
-  for (int i = threadIdx.x; i < kStateTerms * kTerm / 16; i += kT) copy16(m + i * 16, from + i * 16, true);
-  for (int i = threadIdx.x; i < kP * kTerm / 16; i += kT) copy16(p + i * 16, from + kStateTerms * kTerm + i * 16, true);
+__device__ __forceinline__ void load_tri(uint32_t m, uint32_t p, const unsigned char* from, int tid = threadIdx.x) {
+  for (int i = tid; i < kStateTerms * kTerm / 16; i += kT) copy16(m + i * 16, from + i * 16, true);
+  for (int i = tid; i < kP * kTerm / 16; i += kT) copy16(p + i * 16, from + kStateTerms * kTerm + i * 16, true);
 }
 template <int kT = kThreads>
-__device__ __forceinline__ void load_gates(uint32_t to, const Gates* from) {
-  for (int i = threadIdx.x; i < static_cast<int>(sizeof(Gates)) / 16; i += kT)
+__device__ __forceinline__ void load_gates(uint32_t to, const Gates* from, int tid = threadIdx.x) {
+  for (int i = tid; i < static_cast<int>(sizeof(Gates)) / 16; i += kT)
     copy16(to + i * 16, reinterpret_cast<const unsigned char*>(from) + i * 16, true);
 }
 
@@ -538,6 +538,10 @@ __device__ __forceinline__ void store_rows(typename E::T* to, int64_t stride, in
 // the chunk's inputs; their warps' roles are turned by one from quad to quad, so that the
 // triangles' short and long rows are spread over the SM's four parts.
 __device__ __forceinline__ void quad_sync(int quad) { asm volatile("bar.sync %0, 128;" ::"r"(quad + 1) : "memory"); }
+// A block of one quad has four more warps for the copies: the quad's own, one on each of
+// the SM's four parts, are bound by the instructions that they issue one after another.
+template <int NQ>
+constexpr int kCopiers = NQ == 1 ? 128 : 0;
 template <int N>
 __device__ __forceinline__ void hand(uint32_t at, const uint32_t (&f)[N][4]) {
 #pragma unroll
@@ -556,28 +560,24 @@ __device__ __forceinline__ void take(uint32_t at, uint32_t (&f)[N][4]) {
                  : "memory");
 }
 // Tiles of 8 columns that accumulate a product.  Where 24 bits are to be kept the small
-// terms' products have accumulators of their own (see `product`), two of them, as a tile's
-// next product waits for its last.
+// terms' products have accumulators of their own (see `product`).
 template <int N, bool kApart>
 struct Sums {
-  float main[N][4], small[kApart ? 2 : 1][kApart ? N : 1][4];
+  float main[N][4], small[kApart ? N : 1][4];
   __device__ __forceinline__ void clear_all() {
     clear(main);
-    if constexpr (kApart) {
-      clear(small[0]);
-      clear(small[1]);
-    }
+    if constexpr (kApart) clear(small);
   }
   // terms i of A and j of B
   __device__ __forceinline__ void add(int i, int j, const uint32_t (&a)[4], const uint32_t (*b)[2]) {
 #pragma unroll
     for (int t = 0; t < N; ++t) {
-      if constexpr (kApart) mma(i + j == 0 ? main[t] : small[i & 1][t], a, b[t][0], b[t][1]);
+      if constexpr (kApart) mma(i + j == 0 ? main[t] : small[t], a, b[t][0], b[t][1]);
       else mma(main[t], a, b[t][0], b[t][1]);
     }
   }
   __device__ __forceinline__ float sum(int t, int j) const {
-    if constexpr (kApart) return main[t][j] + (small[0][t][j] + small[1][t][j]);
+    if constexpr (kApart) return main[t][j] + small[t][j];
     else return main[t][j];
   }
 };

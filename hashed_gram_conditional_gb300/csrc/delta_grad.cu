@@ -23,7 +23,7 @@ namespace {
 // A quad goes backwards as scan_kernel's go forwards, with dS^T in its registers.
 template <class E, int KD, int NQ>
 struct Back {
-  static constexpr int kT = NQ * 128, kStages = E::kBytes == 2 ? 2 : 1, kB = kC / 16;
+  static constexpr int kT = kCopiers<NQ> ? kCopiers<NQ> : NQ * 128, kStages = E::kBytes == 2 ? 2 : 1, kB = kC / 16;
   static constexpr int kK = 0, kQ = kK + kIn<E> * mat_bytes(kC, KD), kY = kQ + kIn<E> * mat_bytes(kC, KD);
   static constexpr int kM = kY + kIn<E> * mat_bytes(kC, 16 * NQ), kP = kM + kStateTerms * kTerm, kG = kP + kStateTerms * kTerm;
   static constexpr int kStage = kG + static_cast<int>(sizeof(Gates)), kQuads = kStages * kStage;
@@ -34,7 +34,7 @@ struct Back {
 };
 
 template <class E, int KD, int NQ>
-__global__ void __launch_bounds__(NQ * 128, 1) back_kernel(Args<E> a) {
+__global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) back_kernel(Args<E> a) {
   using L = Back<E, KD, NQ>;
   constexpr int kT = L::kT, kI = kIn<E>, kS = kStateTerms, kB = L::kB, kR = KD / 64;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(NQ * 128, 1) back_kernel(Args<E> a) {
   int64_t slot;
   if (!live_slot(a, seq, slot)) {
     if (tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
-    padding_zeros(a, lo, hi, c0, n, h, v0, cols, kT);
+    padding_zeros(a, lo, hi, c0, n, h, v0, cols, blockDim.x);
     return;
   }
   const uint32_t own = base + L::kQuads + quad * L::kQuad;
@@ -84,23 +84,34 @@ __global__ void __launch_bounds__(NQ * 128, 1) back_kernel(Args<E> a) {
       else save_rows(to, a.dk, a.dv, vw, kb * 16, S[2 * r], S[2 * r + 1]);
     }
   };
+  const int copier = tid - (kCopiers<NQ> ? NQ * 128 : 0);  // a copying thread's number
   auto load = [&](int i) {
     const uint32_t stage = base + (i % L::kStages) * L::kStage;
     const int64_t p = lo + static_cast<int64_t>(i) * kC;
     const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
     const uint8_t* mask = a.mask != nullptr ? a.mask + p : nullptr;
     const size_t unit = unit_of(a, c0 + i, h);
-    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kK), a.k + p * a.k_stride + hk * a.dk, a.k_stride, len, a.dk, mask, a.vec);
-    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kQ), a.q + p * a.q_stride + hk * a.dk, a.q_stride, len, a.dk, mask, a.vec);
+    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kK), a.k + p * a.k_stride + hk * a.dk, a.k_stride, len, a.dk, mask, a.vec, copier);
+    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kQ), a.q + p * a.q_stride + hk * a.dk, a.q_stride, len, a.dk, mask, a.vec, copier);
     load_rows<E, 16 * NQ, kT>(mat<kC, 16 * NQ>(stage + L::kY), a.dy + p * a.dy_stride + static_cast<int64_t>(h) * a.dv + v0,
-                              a.dy_stride, len, cols, mask, a.vec);
-    load_tri<kS, kT>(stage + L::kM, stage + L::kP, a.tri + unit * kTriBytes);
-    load_gates<kT>(stage + L::kG, a.gates + unit);
+                              a.dy_stride, len, cols, mask, a.vec, copier);
+    load_tri<kS, kT>(stage + L::kM, stage + L::kP, a.tri + unit * kTriBytes, copier);
+    load_gates<kT>(stage + L::kG, a.gates + unit, copier);
     copies_begun();
   };
+  if (kCopiers<NQ> && copier >= 0) {
+    if (n > 0) load(n - 1);
+    for (int i = n - 1; i >= 0; --i) {
+      copies_done();
+      __syncthreads();
+      if (L::kStages == 1 && i > 0) __syncthreads();
+      if (i > 0) load(i - 1);
+    }
+    return;
+  }
   if (n > 0) {
     hand_state(n - 1);
-    load(n - 1);
+    if (!kCopiers<NQ>) load(n - 1);
   }
   for (int i = n - 1; i >= 0; --i) {
     const uint32_t stage = base + (i % L::kStages) * L::kStage;
@@ -108,7 +119,7 @@ __global__ void __launch_bounds__(NQ * 128, 1) back_kernel(Args<E> a) {
     const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
     copies_done();
     __syncthreads();  // the chunk and the states' gradients are here, and the other stage is free
-    if (L::kStages == 2 && i > 0) load(i - 1);
+    if (!kCopiers<NQ> && L::kStages == 2 && i > 0) load(i - 1);
     float2 into[2], last[2];  // of the warp's positions
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -246,7 +257,7 @@ __global__ void __launch_bounds__(NQ * 128, 1) back_kernel(Args<E> a) {
                     a.dv % 2 == 0, gt.beta, rest);
     if (L::kStages == 1 && i > 0) {
       __syncthreads();  // the stage is free
-      load(i - 1);
+      if (!kCopiers<NQ>) load(i - 1);
     }
   }
   if (a.state_out != nullptr) {
@@ -673,7 +684,8 @@ int launch_grad(const Args<E>& a, int sms, cudaStream_t st) {
   auto back = [&](auto kernel, int smem, int nq, std::atomic<uint64_t>& flag) {
     const int64_t blocks = static_cast<int64_t>(a.n_seqs) * a.heads * ((a.dv + 16 * nq - 1) / (16 * nq));
     if (blocks > 0x7fffffff) return fail(ENGRAM_E_RANGE, "too many sequences times heads");
-    return go(kernel, smem, dim3(static_cast<unsigned>(blocks)), flag, "back_kernel", nq * 128);
+    return go(kernel, smem, dim3(static_cast<unsigned>(blocks)), flag, "back_kernel",
+              nq == 1 ? 128 + kCopiers<1> : nq * 128);
   };
   bool many = false;
   if constexpr (E::kBytes == 2) {
