@@ -305,24 +305,25 @@ template int launch_prepare<train::F32>(const Args<train::F32>&, cudaStream_t);
 // on the way to shared memory and take the room.
 template <class E, int KD, int NQ>
 struct Scan {
-  static constexpr int kT = kCopiers<NQ> ? kCopiers<NQ> : NQ * 128, kStages = E::kBytes == 2 ? 2 : 1, kB = kC / 16;
+  static constexpr int kT = kAlone<NQ> ? kCopiers : NQ * 128, kThreads = kAlone<NQ> ? 256 + kCopiers : kT, kStages = E::kBytes == 2 ? 2 : 1, kB = kC / 16;
   static constexpr int kK = 0, kQ = kK + kIn<E> * mat_bytes(kC, KD), kV = kQ + kIn<E> * mat_bytes(kC, KD);
   static constexpr int kM = kV + kIn<E> * mat_bytes(kC, 16 * NQ), kP = kM + kStateTerms * kTerm, kG = kP + kOut<E> * kTerm;
   static constexpr int kStage = kG + static_cast<int>(sizeof(Gates)), kQuads = kStages * kStage;
-  // a quad's operands: S^T; X^T, then in its place (e^(c_last - c) U)^T; U^T
-  static constexpr int kX = KD / 16 * kStateTerms * 512, kU = kX + kB * kStateTerms * 512;
-  static constexpr int kQuad = kU + kB * kOut<E> * 512;
+  // a quad's operands: S^T; X^T, and (where there are four quads in its place) (e^(c_last - c)
+  // U)^T; U^T
+  static constexpr int kX = KD / 16 * kStateTerms * 512, kL = kAlone<NQ> ? kX + kB * kStateTerms * 512 : kX;
+  static constexpr int kU = kL + kB * kStateTerms * 512, kQuad = kU + kB * kOut<E> * 512;
   static constexpr int kSmem = kQuads + NQ * kQuad;
 };
 
 template <class E, int KD, int NQ>
-__global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) scan_kernel(Args<E> a) {
+__global__ void __launch_bounds__(Scan<E, KD, NQ>::kThreads, 1) scan_kernel(Args<E> a) {
   using L = Scan<E, KD, NQ>;
   constexpr int kT = L::kT, kI = kIn<E>, kO = kOut<E>, kS = kStateTerms, kB = L::kB, kR = KD / 64;  // kR: a warp's blocks of S^T
   extern __shared__ __align__(128) unsigned char smem[];
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t2 = (lane & 3) * 2;
-  const int quad = tid >> 7, w = ((tid >> 5) + quad) & 3;  // w: the warp's quarter
+  const int quad = kAlone<NQ> ? 0 : tid >> 7, w = ((tid >> 5) + quad) & 3;  // w: the warp's quarter
   int seq, h, v0;
   place_of(a, 16 * NQ, seq, h, v0);
   const int cols = min(a.dv - v0, 16 * NQ);
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) scan_kernel(Args<E
       else save_rows(to, a.dk, a.dv, vw, kb * 16, S[2 * r], S[2 * r + 1]);
     }
   };
-  const int copier = tid - (kCopiers<NQ> ? NQ * 128 : 0);  // a copying thread's number
+  const int copier = tid - (kAlone<NQ> ? 256 : 0);  // a copying thread's number
   auto load = [&](int i) {
     const uint32_t stage = base + (i % L::kStages) * L::kStage;
     const int64_t p = lo + static_cast<int64_t>(i) * kC;
@@ -381,7 +382,38 @@ __global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) scan_kernel(Args<E
     load_gates<kT>(stage + L::kG, a.gates + unit, copier);
     copies_begun();
   };
-  if (kCopiers<NQ> && copier >= 0) {
+  // Y^T of the warp's positions: first what Q reads of the state, then of the chunk's writes
+  using Out = Sums<2, kO == 3>;
+  auto scaled = [&](Out& y, const Gates& gt) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const float2 into = *reinterpret_cast<const float2*>(&gt.into[w * 16 + t * 8 + t2]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y.main[t][j] = y.sum(t, j) * (a.scale * (j & 1 ? into.y : into.x));
+    }
+    if constexpr (kO == 3) clear(y.small);
+  };
+  auto finish = [&](Out& y, const Gates& gt, uint32_t stage, int i) {
+    for (int ib = 0; ib <= w; ++ib) {
+      uint32_t fa[kO][4];
+      take<kO>(own + L::kU + ib * (kO * 512), fa);
+#pragma unroll
+      for (int j = 0; j < kO; ++j) {
+        uint32_t fb[2][2];
+        TriAcross{stage + L::kP}.get(fb, ib, w, j);
+        terms<kO, kO>(y, fa, fb, j);
+      }
+    }
+    float out[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) out[t][j] = y.sum(t, j);
+    const int64_t p = lo + static_cast<int64_t>(i) * kC;
+    store_rows<E>(a.y + p * a.y_stride + static_cast<int64_t>(h) * a.dv, a.y_stride, w * 16,
+                  hi - p < kC ? static_cast<int>(hi - p) : kC, vw, a.dv, a.pairs, gt.beta, out);
+  };
+  if (kAlone<NQ> && copier >= 0) {
     if (n > 0) load(0);
     for (int i = 0; i < n; ++i) {
       copies_done();
@@ -391,9 +423,36 @@ __global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) scan_kernel(Args<E
     }
     return;
   }
+  if (kAlone<NQ> && tid >= 128) {  // the quad's Y
+    for (int i = 0; i < n; ++i) {
+      const uint32_t stage = base + (i % L::kStages) * L::kStage;
+      const Mat Q = mat<kC, KD>(stage + L::kQ);
+      const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
+      __syncthreads();
+      Out y;
+      y.clear_all();
+#pragma unroll 4
+      for (int kb = 0; kb < KD / 16; ++kb) {
+        uint32_t fa[kO][4];
+        take<kO>(own + kb * (kS * 512), fa);
+#pragma unroll
+        for (int j = 0; j < kI; ++j) {
+          uint32_t fb[2][2];
+          Across{Q}.get<2>(fb, kb * 16, w * 16, j);
+          terms<kO, kO>(y, fa, fb, j);
+        }
+      }
+      asm volatile("bar.arrive 6, 256;" ::: "memory");  // S^T is no longer needed here
+      scaled(y, gt);
+      asm volatile("bar.sync 5, 256;" ::: "memory");  // U^T is here
+      finish(y, gt, stage, i);
+      if (L::kStages == 1 && i + 1 < n) __syncthreads();
+    }
+    return;
+  }
   if (n > 0) {
     hand_state(0);
-    if (!kCopiers<NQ>) load(0);
+    if (!kAlone<NQ>) load(0);
   }
   for (int i = 0; i < n; ++i) {
     const uint32_t stage = base + (i % L::kStages) * L::kStage;
@@ -401,12 +460,12 @@ __global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) scan_kernel(Args<E
     const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
     copies_done();
     __syncthreads();  // the chunk and the states are here, and the other stage is free
-    if (!kCopiers<NQ> && L::kStages == 2 && i + 1 < n) load(i + 1);
+    if (!kAlone<NQ> && L::kStages == 2 && i + 1 < n) load(i + 1);
     // ---- (K S)^T and (Q S)^T
     Sums<2, true> x;
-    Sums<2, kO == 3> y;
+    Out y;
     x.clear_all();
-    y.clear_all();
+    if (!kAlone<NQ>) y.clear_all();
 #pragma unroll 4
     for (int kb = 0; kb < KD / 16; ++kb) {
       uint32_t fa[kS][4];
@@ -415,11 +474,11 @@ __global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) scan_kernel(Args<E
       for (int j = 0; j < kI; ++j) {
         uint32_t fk[2][2], fq[2][2];
         Across{K}.get<2>(fk, kb * 16, w * 16, j);
-        Across{Q}.get<2>(fq, kb * 16, w * 16, j);
+        if (!kAlone<NQ>) Across{Q}.get<2>(fq, kb * 16, w * 16, j);
 #pragma unroll
         for (int e = 0; e < kS; ++e) {
           if (e + j < kS) x.add(e, j, fa[e], fk);
-          if (e + j < kO) y.add(e, j, fa[e], fq);
+          if (!kAlone<NQ> && e + j < kO) y.add(e, j, fa[e], fq);
         }
       }
     }
@@ -441,15 +500,9 @@ __global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) scan_kernel(Args<E
       for (int t = 0; t < 2; ++t) {
         const float2 into = *reinterpret_cast<const float2*>(&gt.into[w * 16 + t * 8 + t2]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float f = j & 1 ? into.y : into.x;
-          c[t][j] = fmaf(-f, x.sum(t, j), c[t][j]);
-          y.main[t][j] = y.sum(t, j) * (a.scale * f);
-        }
+        for (int j = 0; j < 4; ++j) c[t][j] = fmaf(-(j & 1 ? into.y : into.x), x.sum(t, j), c[t][j]);
       }
-      if constexpr (kO == 3) {
-        clear(y.small);
-      }
+      if (!kAlone<NQ>) scaled(y, gt);
       uint32_t f[kS][4];
       as_operand<kS>(f, c[0], c[1]);
       hand<kS>(own + L::kX + w * (kS * 512), f);
@@ -476,6 +529,7 @@ __global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) scan_kernel(Args<E
       uint32_t f[kO][4], fl[kS][4];
       as_operand<kO>(f, u[0], u[1]);
       hand<kO>(own + L::kU + w * (kO * 512), f);
+      if (kAlone<NQ>) asm volatile("bar.arrive 5, 256;" ::: "memory");
       if (a.carry != nullptr) {  // for the backward pass
         const int64_t p = lo + static_cast<int64_t>(i) * kC, wide = static_cast<int64_t>(a.heads) * a.dv;
         auto* to = kept_writes<E>(a) + p * wide + static_cast<int64_t>(h) * a.dv;
@@ -497,8 +551,8 @@ __global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) scan_kernel(Args<E
         for (int j = 0; j < 4; ++j) u[t][j] *= j & 1 ? last.y : last.x;
       }
       as_operand<kS>(fl, u[0], u[1]);
-      quad_sync(quad);  // X^T is no longer needed
-      hand<kS>(own + L::kX + w * (kS * 512), fl);
+      if (!kAlone<NQ>) quad_sync(quad);  // X^T is no longer needed
+      hand<kS>(own + L::kL + w * (kS * 512), fl);
     }
     quad_sync(quad);
     // ---- S^T
@@ -509,7 +563,7 @@ __global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) scan_kernel(Args<E
 #pragma unroll
       for (int cb = 0; cb < kB; ++cb) {
         uint32_t fa[kS][4];
-        take<kS>(own + L::kX + cb * (kS * 512), fa);
+        take<kS>(own + L::kL + cb * (kS * 512), fa);
 #pragma unroll
         for (int j = 0; j < kI; ++j) {
           uint32_t fb[2 * kR][2];
@@ -522,29 +576,12 @@ __global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) scan_kernel(Args<E
 #pragma unroll
         for (int j = 0; j < 4; ++j) S[t][j] = fmaf(S[t][j], total, d.sum(t, j));
     }
+    if (kAlone<NQ>) asm volatile("bar.sync 6, 256;" ::: "memory");  // Q has read S^T
     if (i + 1 < n) hand_state(i + 1);
-    // ---- Y^T
-    for (int ib = 0; ib <= w; ++ib) {
-      uint32_t fa[kO][4];
-      take<kO>(own + L::kU + ib * (kO * 512), fa);
-#pragma unroll
-      for (int j = 0; j < kO; ++j) {
-        uint32_t fb[2][2];
-        TriAcross{stage + L::kP}.get(fb, ib, w, j);
-        terms<kO, kO>(y, fa, fb, j);
-      }
-    }
-    float out[2][4];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) out[t][j] = y.sum(t, j);
-    const int64_t p = lo + static_cast<int64_t>(i) * kC;
-    store_rows<E>(a.y + p * a.y_stride + static_cast<int64_t>(h) * a.dv, a.y_stride, w * 16,
-                  hi - p < kC ? static_cast<int>(hi - p) : kC, vw, a.dv, a.pairs, gt.beta, out);
+    if (!kAlone<NQ>) finish(y, gt, stage, i);
     if (L::kStages == 1 && i + 1 < n) {
       __syncthreads();  // the stage is free
-      if (!kCopiers<NQ>) load(i + 1);
+      if (!kAlone<NQ>) load(i + 1);
     }
   }
   if (a.state_out != nullptr) {
@@ -560,7 +597,7 @@ int launch_scan(const Args<E>& a, int sms, cudaStream_t st) {
     if (r) return r;
     const int64_t blocks = static_cast<int64_t>(a.n_seqs) * a.heads * ((a.dv + 16 * nq - 1) / (16 * nq));
     if (blocks > 0x7fffffff) return fail(ENGRAM_E_RANGE, "too many sequences times heads");
-    kernel<<<static_cast<unsigned>(blocks), nq == 1 ? 128 + kCopiers<1> : nq * 128, smem, st>>>(a);
+    kernel<<<static_cast<unsigned>(blocks), nq == 1 ? 256 + kCopiers : nq * 128, smem, st>>>(a);
     return check_launch("scan_kernel");
   };
   static std::atomic<uint64_t> done[4] = {{0}, {0}, {0}, {0}};

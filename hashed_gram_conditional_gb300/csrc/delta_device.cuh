@@ -538,10 +538,13 @@ __device__ __forceinline__ void store_rows(typename E::T* to, int64_t stride, in
 // the chunk's inputs; their warps' roles are turned by one from quad to quad, so that the
 // triangles' short and long rows are spread over the SM's four parts.
 __device__ __forceinline__ void quad_sync(int quad) { asm volatile("bar.sync %0, 128;" ::"r"(quad + 1) : "memory"); }
-// A block of one quad has four more warps for the copies: the quad's own, one on each of
-// the SM's four parts, are bound by the instructions that they issue one after another.
+// A block of one quad has more warps: four for the copies and, forwards, four for Y.  The
+// quad's own, one on each of the SM's four parts, are bound by the instructions that they
+// issue one after another (one sequence of 16,381 positions in 10 heads, us: 745 without
+// either, 546 with those for the copies, %s with both).
 template <int NQ>
-constexpr int kCopiers = NQ == 1 ? 128 : 0;
+constexpr bool kAlone = NQ == 1;
+constexpr int kCopiers = 128;
 template <int N>
 __device__ __forceinline__ void hand(uint32_t at, const uint32_t (&f)[N][4]) {
 #pragma unroll

@@ -23,7 +23,7 @@ namespace {
 // A quad goes backwards as scan_kernel's go forwards, with dS^T in its registers.
 template <class E, int KD, int NQ>
 struct Back {
-  static constexpr int kT = kCopiers<NQ> ? kCopiers<NQ> : NQ * 128, kStages = E::kBytes == 2 ? 2 : 1, kB = kC / 16;
+  static constexpr int kT = kAlone<NQ> ? kCopiers : NQ * 128, kThreads = kAlone<NQ> ? 128 + kCopiers : kT, kStages = E::kBytes == 2 ? 2 : 1, kB = kC / 16;
   static constexpr int kK = 0, kQ = kK + kIn<E> * mat_bytes(kC, KD), kY = kQ + kIn<E> * mat_bytes(kC, KD);
   static constexpr int kM = kY + kIn<E> * mat_bytes(kC, 16 * NQ), kP = kM + kStateTerms * kTerm, kG = kP + kStateTerms * kTerm;
   static constexpr int kStage = kG + static_cast<int>(sizeof(Gates)), kQuads = kStages * kStage;
@@ -34,13 +34,13 @@ struct Back {
 };
 
 template <class E, int KD, int NQ>
-__global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) back_kernel(Args<E> a) {
+__global__ void __launch_bounds__(Back<E, KD, NQ>::kThreads, 1) back_kernel(Args<E> a) {
   using L = Back<E, KD, NQ>;
   constexpr int kT = L::kT, kI = kIn<E>, kS = kStateTerms, kB = L::kB, kR = KD / 64;
   extern __shared__ __align__(128) unsigned char smem[];
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t2 = (lane & 3) * 2;
-  const int quad = tid >> 7, w = ((tid >> 5) + quad) & 3;
+  const int quad = kAlone<NQ> ? 0 : tid >> 7, w = ((tid >> 5) + quad) & 3;
   int seq, h, v0;
   place_of(a, 16 * NQ, seq, h, v0);
   const int cols = min(a.dv - v0, 16 * NQ);
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) back_kernel(Args<E
       else save_rows(to, a.dk, a.dv, vw, kb * 16, S[2 * r], S[2 * r + 1]);
     }
   };
-  const int copier = tid - (kCopiers<NQ> ? NQ * 128 : 0);  // a copying thread's number
+  const int copier = tid - (kAlone<NQ> ? NQ * 128 : 0);  // a copying thread's number
   auto load = [&](int i) {
     const uint32_t stage = base + (i % L::kStages) * L::kStage;
     const int64_t p = lo + static_cast<int64_t>(i) * kC;
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) back_kernel(Args<E
     load_gates<kT>(stage + L::kG, a.gates + unit, copier);
     copies_begun();
   };
-  if (kCopiers<NQ> && copier >= 0) {
+  if (kAlone<NQ> && copier >= 0) {
     if (n > 0) load(n - 1);
     for (int i = n - 1; i >= 0; --i) {
       copies_done();
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) back_kernel(Args<E
   }
   if (n > 0) {
     hand_state(n - 1);
-    if (!kCopiers<NQ>) load(n - 1);
+    if (!kAlone<NQ>) load(n - 1);
   }
   for (int i = n - 1; i >= 0; --i) {
     const uint32_t stage = base + (i % L::kStages) * L::kStage;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) back_kernel(Args<E
     const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
     copies_done();
     __syncthreads();  // the chunk and the states' gradients are here, and the other stage is free
-    if (!kCopiers<NQ> && L::kStages == 2 && i > 0) load(i - 1);
+    if (!kAlone<NQ> && L::kStages == 2 && i > 0) load(i - 1);
     float2 into[2], last[2];  // of the warp's positions
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(NQ * 128 + kCopiers<NQ>, 1) back_kernel(Args<E
                     a.dv % 2 == 0, gt.beta, rest);
     if (L::kStages == 1 && i > 0) {
       __syncthreads();  // the stage is free
-      if (!kCopiers<NQ>) load(i - 1);
+      if (!kAlone<NQ>) load(i - 1);
     }
   }
   if (a.state_out != nullptr) {
@@ -685,7 +685,7 @@ int launch_grad(const Args<E>& a, int sms, cudaStream_t st) {
     const int64_t blocks = static_cast<int64_t>(a.n_seqs) * a.heads * ((a.dv + 16 * nq - 1) / (16 * nq));
     if (blocks > 0x7fffffff) return fail(ENGRAM_E_RANGE, "too many sequences times heads");
     return go(kernel, smem, dim3(static_cast<unsigned>(blocks)), flag, "back_kernel",
-              nq == 1 ? 128 + kCopiers<1> : nq * 128);
+              nq == 1 ? 128 + kCopiers : nq * 128);
   };
   bool many = false;
   if constexpr (E::kBytes == 2) {
