@@ -30,7 +30,6 @@ namespace engram {
 namespace {
 
 constexpr int kMaxGroups = ENGRAM_NORM_MAX_GROUPS;
-constexpr int kThreads = 512;  // at most, where registers for more than one vector a thread are wanted
 constexpr int kAnyThreads = 256;
 // Blocks that a gradient's sums of the weights are spread over.
 constexpr int kParts = 304;
@@ -47,52 +46,74 @@ struct Args {
   float eps;
 };
 
-template <class E>
-constexpr int kVec = 16 / E::kBytes;
+constexpr int kThreads = 512;  // at most, where registers for more than one vector a thread are wanted
 
-template <class E>
-__device__ __forceinline__ void widen(const uint4& x, float (&f)[kVec<E>]) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+// What a thread reads and writes at once: 16 bytes, or where rows are not aligned to
+// them one value.
+template <class E_>
+struct Wide {
+  using E = E_;
+  using Raw = uint4;
+  static constexpr int N = 16 / E::kBytes, kMost = kThreads;
+  static __device__ __forceinline__ Raw none() { return make_uint4(0u, 0u, 0u, 0u); }
+  static __device__ __forceinline__ void widen(const Raw& x, float (&f)[N]) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if constexpr (E::kBytes == 2) {
-      f[2 * j] = __uint_as_float(w[j] << 16);
-      f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    } else {
-      f[j] = __uint_as_float(w[j]);
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (E::kBytes == 2) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      } else {
+        f[j] = __uint_as_float(w[j]);
+      }
     }
   }
-}
-
-template <class E>
-__device__ __forceinline__ uint4 narrow(const float (&f)[kVec<E>]) {
-  uint32_t w[4];
+  static __device__ __forceinline__ Raw narrow(const float (&f)[N]) {
+    uint32_t w[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if constexpr (E::kBytes == 2) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-      w[j] = *reinterpret_cast<const uint32_t*>(&b);
-    } else {
-      w[j] = __float_as_uint(f[j]);
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (E::kBytes == 2) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+      } else {
+        w[j] = __float_as_uint(f[j]);
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  static __device__ __forceinline__ void weights(const float* p, float (&f)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(p + j));
+      f[j] = x.x;
+      f[j + 1] = x.y;
+      f[j + 2] = x.z;
+      f[j + 3] = x.w;
     }
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-template <class E>
-__device__ __forceinline__ void load_weights(const float* p, float (&f)[kVec<E>]) {
-  if (p == nullptr) {
-#pragma unroll
-    for (int j = 0; j < kVec<E>; ++j) f[j] = 1.f;
-    return;
+};
+template <class E_>
+struct Single {
+  using E = E_;
+  using Raw = typename E::T;
+  static constexpr int N = 1, kMost = 1024;
+  static __device__ __forceinline__ Raw none() { return Raw(0); }
+  static __device__ __forceinline__ void widen(const Raw& x, float (&f)[1]) { f[0] = E::load(&x); }
+  static __device__ __forceinline__ Raw narrow(const float (&f)[1]) {
+    Raw x;
+    E::store(&x, f[0]);
+    return x;
   }
+  static __device__ __forceinline__ void weights(const float* p, float (&f)[1]) { f[0] = __ldg(p); }
+};
+
+template <class P>
+__device__ __forceinline__ void load_weights(const float* p, float (&f)[P::N]) {
+  if (p != nullptr) {
+    P::weights(p, f);
+  } else {
 #pragma unroll
-  for (int j = 0; j < kVec<E>; j += 4) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(p + j));
-    f[j] = x.x;
-    f[j + 1] = x.y;
-    f[j + 2] = x.z;
-    f[j + 3] = x.w;
+    for (int j = 0; j < P::N; ++j) f[j] = 1.f;
   }
 }
 
@@ -175,62 +196,69 @@ __device__ __forceinline__ As* row_of(void* p, int64_t row, int64_t stride) {
   return reinterpret_cast<As*>(static_cast<typename E::T*>(p) + row * stride);
 }
 // (cached no longer than the row's own use)
-template <class E>
-__device__ __forceinline__ uint4 vector_at(const void* p, int64_t row, int64_t stride, int v) {
-  return __ldcs(row_of<E, uint4>(p, row, stride) + v);
+template <class P>
+__device__ __forceinline__ typename P::Raw vector_at(const void* p, int64_t row, int64_t stride, int v) {
+  return __ldcs(row_of<typename P::E, typename P::Raw>(p, row, stride) + v);
+}
+
+__device__ __forceinline__ const float* weights_at(const Args& a, int e) {
+  return a.w == nullptr ? nullptr : a.w + (a.groups == 1 ? e : e % a.width);
 }
 
 // ------------------------------------------------------------------- forward
 
-template <class E, int kPer>
-__global__ void __launch_bounds__(kThreads) norm_kernel(Args a) {
-  constexpr int N = kVec<E>;
+template <class P, int kPer>
+__global__ void __launch_bounds__(P::kMost) norm_kernel(Args a) {
+  using E = typename P::E;
+  using Raw = typename P::Raw;
+  constexpr int N = P::N;
   extern __shared__ float part[];
   __shared__ float slot[2][32];
   const int64_t row = blockIdx.x;
-  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-  uint4 ry[kPer], rz[kPer], rh[kPer];
+  const Raw none = P::none();
+  Raw ry[kPer], rz[kPer], rh[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
-    ry[i] = v < a.vecs ? vector_at<E>(a.y, row, a.y_stride, v) : none;
-    rz[i] = v < a.vecs && a.gate ? vector_at<E>(a.gate, row, a.gate_stride, v) : none;
-    rh[i] = v < a.vecs && a.h ? vector_at<E>(a.h, row, a.h_stride, v) : none;
+    ry[i] = v < a.vecs ? vector_at<P>(a.y, row, a.y_stride, v) : none;
+    rz[i] = v < a.vecs && a.gate ? vector_at<P>(a.gate, row, a.gate_stride, v) : none;
+    rh[i] = v < a.vecs && a.h ? vector_at<P>(a.h, row, a.h_stride, v) : none;
   }
   float sq[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     float y[N];
-    widen<E>(ry[i], y);
+    P::widen(ry[i], y);
     sq[i] = 0.f;
 #pragma unroll
     for (int j = 0; j < N; ++j) sq[i] = fmaf(y[j], y[j], sq[i]);
   }
   group_sums(a, sq, part, slot[0]);
+  const float inv_width = 1.f / a.width, r_all = rsqrtf(sq[0] * inv_width + a.eps);  // (of a row that is one group)
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
     if (v >= a.vecs) continue;
-    const float r = rsqrtf(sq[i] / a.width + a.eps);
+    const float r = a.groups == 1 ? r_all : rsqrtf(sq[i] * inv_width + a.eps);
     float y[N], h[N], w[N];
-    widen<E>(ry[i], y);
-    widen<E>(rh[i], h);
-    load_weights<E>(a.w ? a.w + v * N % a.width : nullptr, w);
+    P::widen(ry[i], y);
+    P::widen(rh[i], h);
+    load_weights<P>(weights_at(a, v * N), w);
 #pragma unroll
     for (int j = 0; j < N; ++j) y[j] *= r * w[j];
     if (a.gate) {
       float z[N];
-      widen<E>(rz[i], z);
+      P::widen(rz[i], z);
 #pragma unroll
       for (int j = 0; j < N; ++j) y[j] *= z[j] * sigmoid<E>(z[j]);
     }
-    load_weights<E>(a.scale ? a.scale + v * N : nullptr, w);
+    load_weights<P>(a.scale ? a.scale + v * N : nullptr, w);
 #pragma unroll
     for (int j = 0; j < N; ++j) h[j] = fmaf(y[j], w[j], h[j]);
-    rh[i] = narrow<E>(h);
-    row_of<E, uint4>(a.h_out, row, a.h_out_stride)[v] = rh[i];
-    widen<E>(rh[i], h);
+    rh[i] = P::narrow(h);
+    row_of<E, Raw>(a.h_out, row, a.h_out_stride)[v] = rh[i];
+    P::widen(rh[i], h);
 #pragma unroll
     for (int j = 0; j < N; ++j) sum = fmaf(h[j], h[j], sum);
   }
@@ -242,25 +270,33 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(Args a) {
     const int v = threadIdx.x + i * blockDim.x;
     if (v >= a.vecs) continue;
     float h[N], w[N];
-    widen<E>(rh[i], h);
-    load_weights<E>(a.w_next ? a.w_next + v * N : nullptr, w);
+    P::widen(rh[i], h);
+    load_weights<P>(a.w_next ? a.w_next + v * N : nullptr, w);
 #pragma unroll
     for (int j = 0; j < N; ++j) h[j] *= r * w[j];
-    row_of<E, uint4>(a.x_out, row, a.x_stride)[v] = narrow<E>(h);
+    row_of<E, Raw>(a.x_out, row, a.x_stride)[v] = P::narrow(h);
   }
 }
 
-// r of every group into sums[groups], by the block; a barrier follows.
-template <class E>
-__device__ __forceinline__ void any_groups(const Args& a, const typename E::T* y, float* sums) {
+// out[g] = last(sum over the group's values of f(g, place in it)), by a warp for each group
+// or, where there are few, by the block; a barrier follows.
+template <class F, class L>
+__device__ __forceinline__ void any_groups(const Args& a, float* out, float* slot, F f, L last) {
+  if (a.groups < kAnyThreads / 32) {
+    for (int g = 0; g < a.groups; ++g) {
+      float s = 0.f;
+      for (int k = threadIdx.x; k < a.width; k += kAnyThreads) s += f(g, k);
+      s = block_sum(s, slot);
+      if (threadIdx.x == 0) out[g] = last(s);
+      __syncthreads();
+    }
+    return;
+  }
   for (int g = threadIdx.x >> 5; g < a.groups; g += kAnyThreads / 32) {
     float s = 0.f;
-    for (int k = threadIdx.x & 31; k < a.width; k += 32) {
-      const float v = E::load(y + static_cast<int64_t>(g) * a.width + k);
-      s = fmaf(v, v, s);
-    }
+    for (int k = threadIdx.x & 31; k < a.width; k += 32) s += f(g, k);
     s = warp_sum(s);
-    if ((threadIdx.x & 31) == 0) sums[g] = rsqrtf(s / a.width + a.eps);
+    if ((threadIdx.x & 31) == 0) out[g] = last(s);
   }
   __syncthreads();
 }
@@ -271,7 +307,12 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(Args a) {
   const int64_t row = blockIdx.x;
   const auto* y = row_of<E>(a.y, row, a.y_stride);
   auto* out = row_of<E>(a.h_out, row, a.h_out_stride);
-  any_groups<E>(a, y, sums);
+  any_groups(a, sums, slot,
+             [&](int g, int k) {
+               const float v = E::load(y + g * a.width + k);
+               return v * v;
+             },
+             [&](float s) { return rsqrtf(s / a.width + a.eps); });
   float sum = 0.f;
   for (int e = threadIdx.x; e < a.dim; e += kAnyThreads) {
     const int g = e / a.width;
@@ -294,31 +335,37 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(Args a) {
 
 // ------------------------------------------------------------------ gradient
 
-template <class E, int kPer, int kMost>
+template <class P, int kPer, int kMost>
 __global__ void __launch_bounds__(kMost) norm_grad_kernel(Args a) {
-  constexpr int N = kVec<E>;
+  using E = typename P::E;
+  using Raw = typename P::Raw;
+  constexpr int N = P::N;
   extern __shared__ float part[];
   __shared__ float slot[4][32];
-  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-  float q[kPer][N] = {}, dn[kPer][N] = {};
+  const Raw none = P::none();
+  // the columns' sums: single values' threads have them in shared memory, each its own
+  constexpr bool kKept = N > 1;
+  float q[kKept ? kPer : 1][N] = {}, dn[kKept ? kPer : 1][N] = {};
+  float* sums = part + (a.groups > 1 && a.vecs_log2 < 0 ? a.vecs + a.groups : 0);
+  for (int v = threadIdx.x; !kKept && v < a.vecs; v += blockDim.x) sums[v] = sums[a.vecs + v] = 0.f;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    uint4 ry[kPer], rz[kPer], rl[kPer], rh[kPer], rx[kPer];
+    Raw ry[kPer], rz[kPer], rl[kPer], rh[kPer], rx[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       const bool in = v < a.vecs;
-      ry[i] = in ? vector_at<E>(a.y, row, a.y_stride, v) : none;
-      rh[i] = in && a.dx ? vector_at<E>(a.h, row, a.h_stride, v) : none;
-      rx[i] = in && a.dx ? vector_at<E>(a.dx, row, a.dx_stride, v) : none;
-      rl[i] = in && a.dh ? vector_at<E>(a.dh, row, a.dh_stride, v) : none;
-      rz[i] = in && a.gate ? vector_at<E>(a.gate, row, a.gate_stride, v) : none;
+      ry[i] = in ? vector_at<P>(a.y, row, a.y_stride, v) : none;
+      rh[i] = in && a.dx ? vector_at<P>(a.h, row, a.h_stride, v) : none;
+      rx[i] = in && a.dx ? vector_at<P>(a.dx, row, a.dx_stride, v) : none;
+      rl[i] = in && a.dh ? vector_at<P>(a.dh, row, a.dh_stride, v) : none;
+      rz[i] = in && a.gate ? vector_at<P>(a.gate, row, a.gate_stride, v) : none;
     }
     float sq[kPer], l[kPer][N];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       float y[N];
-      widen<E>(ry[i], y);
-      widen<E>(rl[i], l[i]);
+      P::widen(ry[i], y);
+      P::widen(rl[i], l[i]);
       sq[i] = 0.f;
 #pragma unroll
       for (int j = 0; j < N; ++j) sq[i] = fmaf(y[j], y[j], sq[i]);
@@ -330,9 +377,9 @@ __global__ void __launch_bounds__(kMost) norm_grad_kernel(Args a) {
         const int v = threadIdx.x + i * blockDim.x;
         if (v >= a.vecs) continue;
         float h[N], x[N], w[N];
-        widen<E>(rh[i], h);
-        widen<E>(rx[i], x);
-        load_weights<E>(a.w_next ? a.w_next + v * N : nullptr, w);
+        P::widen(rh[i], h);
+        P::widen(rx[i], x);
+        load_weights<P>(a.w_next ? a.w_next + v * N : nullptr, w);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           hh = fmaf(h[j], h[j], hh);
@@ -347,54 +394,57 @@ __global__ void __launch_bounds__(kMost) norm_grad_kernel(Args a) {
         const int v = threadIdx.x + i * blockDim.x;
         if (v >= a.vecs) continue;
         float h[N], x[N], w[N];
-        widen<E>(rh[i], h);
-        widen<E>(rx[i], x);
-        load_weights<E>(a.w_next ? a.w_next + v * N : nullptr, w);
+        P::widen(rh[i], h);
+        P::widen(rx[i], x);
+        load_weights<P>(a.w_next ? a.w_next + v * N : nullptr, w);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           x[j] *= r;
           l[i][j] += x[j] * w[j] - h[j] * c;
-          dn[i][j] = fmaf(x[j], h[j], dn[i][j]);
+          if constexpr (kKept) dn[i][j] = fmaf(x[j], h[j], dn[i][j]);
+          else sums[a.vecs + v] = fmaf(x[j], h[j], sums[a.vecs + v]);
         }
       }
     }
     group_sums(a, sq, part, slot[2]);
+    const float inv_width = 1.f / a.width, r_all = rsqrtf(sq[0] * inv_width + a.eps);
     float along[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       along[i] = 0.f;
       if (v >= a.vecs) continue;
-      if (a.dres) row_of<E, uint4>(a.dres, row, a.dres_stride)[v] = narrow<E>(l[i]);
-      const float r = rsqrtf(sq[i] / a.width + a.eps);
+      if (a.dres) row_of<E, Raw>(a.dres, row, a.dres_stride)[v] = P::narrow(l[i]);
+      const float r = a.groups == 1 ? r_all : rsqrtf(sq[i] * inv_width + a.eps);
       sq[i] = r;
       float y[N], z[N], w[N], s[N], dz[N];
-      widen<E>(ry[i], y);
-      widen<E>(rz[i], z);
-      load_weights<E>(a.w ? a.w + v * N % a.width : nullptr, w);
-      load_weights<E>(a.scale ? a.scale + v * N : nullptr, s);
+      P::widen(ry[i], y);
+      P::widen(rz[i], z);
+      load_weights<P>(weights_at(a, v * N), w);
+      load_weights<P>(a.scale ? a.scale + v * N : nullptr, s);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const float sig = a.gate ? sigmoid<E>(z[j]) : 1.f, act = a.gate ? z[j] * sig : 1.f;
         const float hat = y[j] * r, g = l[i][j] * s[j] * w[j];  // g: the gradient of y r silu(gate)
-        q[i][j] = fmaf(l[i][j] * act, hat, q[i][j]);
+        if constexpr (kKept) q[i][j] = fmaf(l[i][j] * act, hat, q[i][j]);
+        else sums[v] = fmaf(l[i][j] * act, hat, sums[v]);
         dz[j] = g * hat * sig * fmaf(z[j], 1.f - sig, 1.f);
         l[i][j] = g * act;
         along[i] = fmaf(l[i][j], y[j], along[i]);
       }
-      if (a.dgate) row_of<E, uint4>(a.dgate, row, a.dgate_stride)[v] = narrow<E>(dz);
+      if (a.dgate) row_of<E, Raw>(a.dgate, row, a.dgate_stride)[v] = P::narrow(dz);
     }
     group_sums(a, along, part, slot[3]);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= a.vecs) continue;
-      const float r = sq[i], c = along[i] * r * r * r / a.width;
+      const float r = sq[i], c = along[i] * r * r * r * inv_width;
       float y[N];
-      widen<E>(ry[i], y);
+      P::widen(ry[i], y);
 #pragma unroll
       for (int j = 0; j < N; ++j) l[i][j] = l[i][j] * r - y[j] * c;
-      row_of<E, uint4>(a.dy, row, a.dy_stride)[v] = narrow<E>(l[i]);
+      row_of<E, Raw>(a.dy, row, a.dy_stride)[v] = P::narrow(l[i]);
     }
   }
   if (a.parts == nullptr) return;
@@ -406,8 +456,8 @@ __global__ void __launch_bounds__(kMost) norm_grad_kernel(Args a) {
     const int64_t next = static_cast<int64_t>(gridDim.x) * a.dim;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      to[j] = q[i][j];
-      to[next + j] = dn[i][j];
+      to[j] = kKept ? q[kKept ? i : 0][j] : sums[v];
+      to[next + j] = kKept ? dn[kKept ? i : 0][j] : sums[a.vecs + v];
     }
   }
 }
@@ -428,9 +478,11 @@ constexpr int kRingThreads = 640;
 constexpr int kArrays = 5;   // y, gate, dh, h', dx
 constexpr int kRingSmem = 220 * 1024;
 
-template <class E, int kPer>
+template <class P, int kPer>
 __global__ void __launch_bounds__(kPer == 1 ? kRingThreads : kThreads) norm_grad_ring_kernel(Args a) {
-  constexpr int N = kVec<E>;
+  using E = typename P::E;
+  using Raw = typename P::Raw;
+  constexpr int N = P::N;
   extern __shared__ __align__(16) float part[];
   __shared__ float slot[2][4][32], slot_along[32];
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -440,19 +492,19 @@ __global__ void __launch_bounds__(kPer == 1 ? kRingThreads : kThreads) norm_grad
   const float inv_dim = 1.f / a.dim, inv_width = 1.f / a.width;
   const float* w_at[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) w_at[i] = a.w ? a.w + (threadIdx.x + i * blockDim.x) * N % a.width : nullptr;
+  for (int i = 0; i < kPer; ++i) w_at[i] = weights_at(a, (threadIdx.x + i * blockDim.x) * N);
   auto fetch = [&](int64_t row, int stage) {
     if (row < a.rows) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
         if (v >= a.vecs) continue;
-        copy_vec(place(stage, 0, v), row_of<E, uint4>(a.y, row, a.y_stride) + v);
-        if (a.gate) copy_vec(place(stage, 1, v), row_of<E, uint4>(a.gate, row, a.gate_stride) + v);
-        if (a.dh) copy_vec(place(stage, 2, v), row_of<E, uint4>(a.dh, row, a.dh_stride) + v);
+        copy_vec(place(stage, 0, v), row_of<E, Raw>(a.y, row, a.y_stride) + v);
+        if (a.gate) copy_vec(place(stage, 1, v), row_of<E, Raw>(a.gate, row, a.gate_stride) + v);
+        if (a.dh) copy_vec(place(stage, 2, v), row_of<E, Raw>(a.dh, row, a.dh_stride) + v);
         if (a.dx) {
-          copy_vec(place(stage, 3, v), row_of<E, uint4>(a.h, row, a.h_stride) + v);
-          copy_vec(place(stage, 4, v), row_of<E, uint4>(a.dx, row, a.dx_stride) + v);
+          copy_vec(place(stage, 3, v), row_of<E, Raw>(a.h, row, a.h_stride) + v);
+          copy_vec(place(stage, 4, v), row_of<E, Raw>(a.dx, row, a.dx_stride) + v);
         }
       }
     }
@@ -466,15 +518,15 @@ __global__ void __launch_bounds__(kPer == 1 ? kRingThreads : kThreads) norm_grad
       sq[i] = 0.f;
       if (v >= a.vecs) continue;
       float y[N];
-      widen<E>(own_vec(place(stage, 0, v)), y);
+      P::widen(own_vec(place(stage, 0, v)), y);
 #pragma unroll
       for (int j = 0; j < N; ++j) sq[i] = fmaf(y[j], y[j], sq[i]);
       sum[2] += sq[i];
       if (a.dx) {
         float h[N], x[N], w[N];
-        widen<E>(own_vec(place(stage, 3, v)), h);
-        widen<E>(own_vec(place(stage, 4, v)), x);
-        load_weights<E>(a.w_next ? a.w_next + v * N : nullptr, w);
+        P::widen(own_vec(place(stage, 3, v)), h);
+        P::widen(own_vec(place(stage, 4, v)), x);
+        load_weights<P>(a.w_next ? a.w_next + v * N : nullptr, w);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           sum[0] = fmaf(h[j], h[j], sum[0]);
@@ -538,16 +590,16 @@ __global__ void __launch_bounds__(kPer == 1 ? kRingThreads : kThreads) norm_grad
       along[i] = 0.f;
       if (v >= a.vecs) continue;
       if (a.dh) {
-        widen<E>(own_vec(place(stage, 2, v)), l[i]);
+        P::widen(own_vec(place(stage, 2, v)), l[i]);
       } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) l[i][j] = 0.f;
       }
       if (a.dx) {
         float h[N], x[N], w[N];
-        widen<E>(own_vec(place(stage, 3, v)), h);
-        widen<E>(own_vec(place(stage, 4, v)), x);
-        load_weights<E>(a.w_next ? a.w_next + v * N : nullptr, w);
+        P::widen(own_vec(place(stage, 3, v)), h);
+        P::widen(own_vec(place(stage, 4, v)), x);
+        load_weights<P>(a.w_next ? a.w_next + v * N : nullptr, w);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           x[j] *= r2;
@@ -555,13 +607,13 @@ __global__ void __launch_bounds__(kPer == 1 ? kRingThreads : kThreads) norm_grad
           dn[i][j] = fmaf(x[j], h[j], dn[i][j]);
         }
       }
-      if (a.dres) row_of<E, uint4>(a.dres, row, a.dres_stride)[v] = narrow<E>(l[i]);
+      if (a.dres) row_of<E, Raw>(a.dres, row, a.dres_stride)[v] = P::narrow(l[i]);
       r1[i] = rsqrtf(sq[i] * inv_width + a.eps);
       float y[N], z[N], w[N], s[N], dz[N];
-      widen<E>(own_vec(place(stage, 0, v)), y);
-      if (a.gate) widen<E>(own_vec(place(stage, 1, v)), z);
-      load_weights<E>(w_at[i], w);
-      load_weights<E>(a.scale ? a.scale + v * N : nullptr, s);
+      P::widen(own_vec(place(stage, 0, v)), y);
+      if (a.gate) P::widen(own_vec(place(stage, 1, v)), z);
+      load_weights<P>(w_at[i], w);
+      load_weights<P>(a.scale ? a.scale + v * N : nullptr, s);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const float hat = y[j] * r1[i], g = l[i][j] * s[j] * w[j];  // g: the gradient of y r silu(gate)
@@ -576,7 +628,7 @@ __global__ void __launch_bounds__(kPer == 1 ? kRingThreads : kThreads) norm_grad
         along[i] = fmaf(l[i][j], y[j], along[i]);
       }
       coming[3] += along[i];
-      if (a.dgate) row_of<E, uint4>(a.dgate, row, a.dgate_stride)[v] = narrow<E>(dz);
+      if (a.dgate) row_of<E, Raw>(a.dgate, row, a.dgate_stride)[v] = P::narrow(dz);
     }
     asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
     if (row + gridDim.x < a.rows) first(next, coming, sq);
@@ -593,10 +645,10 @@ __global__ void __launch_bounds__(kPer == 1 ? kRingThreads : kThreads) norm_grad
       if (v >= a.vecs) continue;
       const float r = r1[i], c = along[i] * r * r * r * inv_width;
       float y[N];
-      widen<E>(own_vec(place(stage, 0, v)), y);
+      P::widen(own_vec(place(stage, 0, v)), y);
 #pragma unroll
       for (int j = 0; j < N; ++j) l[i][j] = l[i][j] * r - y[j] * c;
-      row_of<E, uint4>(a.dy, row, a.dy_stride)[v] = narrow<E>(l[i]);
+      row_of<E, Raw>(a.dy, row, a.dy_stride)[v] = P::narrow(l[i]);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) sum[k] = coming[k];
@@ -627,7 +679,12 @@ __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(Args a) {
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const auto* y = row_of<E>(a.y, row, a.y_stride);
     __syncthreads();  // the last row's sums are no longer read
-    any_groups<E>(a, y, sums);
+    any_groups(a, sums, slot[0],
+               [&](int g, int k) {
+                 const float v = E::load(y + g * a.width + k);
+                 return v * v;
+               },
+               [&](float s) { return rsqrtf(s / a.width + a.eps); });
     float r2 = 0.f, c2 = 0.f;
     if (a.dx) {
       float hh = 0.f, xh = 0.f;
@@ -638,6 +695,7 @@ __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(Args a) {
       }
       hh = block_sum(hh, slot[0]);
       xh = block_sum(xh, slot[1]);
+      __syncthreads();
       r2 = rsqrtf(hh / a.dim + a.eps);
       c2 = xh * r2 * r2 * r2 / a.dim;
     }
@@ -652,18 +710,14 @@ __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(Args a) {
       act = a.gate ? z * sig : 1.f;
       p = l * (a.scale ? a.scale[e] : 1.f);
     };
-    for (int g = threadIdx.x >> 5; g < a.groups; g += kAnyThreads / 32) {
-      float s = 0.f;
-      for (int k = threadIdx.x & 31; k < a.width; k += 32) {
-        const int e = g * a.width + k;
-        float l, p, sig, act, z;
-        at(e, l, p, sig, act, z);
-        s = fmaf(p * act * (a.w ? a.w[k] : 1.f), E::load(y + e), s);
-      }
-      s = warp_sum(s);
-      if ((threadIdx.x & 31) == 0) along[g] = s;
-    }
-    __syncthreads();
+    any_groups(a, along, slot[0],
+               [&](int g, int k) {
+                 const int e = g * a.width + k;
+                 float l, p, sig, act, z;
+                 at(e, l, p, sig, act, z);
+                 return p * act * (a.w ? a.w[k] : 1.f) * E::load(y + e);
+               },
+               [](float s) { return s; });
     for (int e = threadIdx.x; e < a.dim; e += kAnyThreads) {
       const int g = e / a.width;
       float l, p, sig, act, z;
@@ -718,12 +772,13 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(Args a, int blocks, flo
 
 // -------------------------------------------------------------------- launch
 
-// Vectors that a thread of a block of at most kThreads holds; 0: the row is too long.
-int per_thread(int vecs, int most) {
+// Pieces that a thread of a block of at most kThreads holds; 0: the row is too long.
+int per_thread(int pieces, int most) {
   for (int per = 1; per <= most; per *= 2)
-    if (vecs <= per * kThreads) return per;
+    if (pieces <= per * kThreads) return per;
   return 0;
 }
+constexpr int kSingles = 8;  // values a thread, where rows are not aligned: of 8192 at most
 
 int opt_in(const void* kernel, std::atomic<uint64_t>& done) {
   int dev = 0;
@@ -739,15 +794,15 @@ int opt_in(const void* kernel, std::atomic<uint64_t>& done) {
 template <class E>
 bool by_vectors(const Args& a, bool grad) {
   auto ok = [](const void* p, int64_t stride) { return p == nullptr || (aligned(p, 16) && stride * E::kBytes % 16 == 0); };
-  return a.width % kVec<E> == 0 && ok(a.y, a.y_stride) && ok(a.gate, a.gate_stride) && ok(a.h, a.h_stride) &&
+  return a.width % Wide<E>::N == 0 && ok(a.y, a.y_stride) && ok(a.gate, a.gate_stride) && ok(a.h, a.h_stride) &&
          ok(a.dh, a.dh_stride) && ok(a.dx, a.dx_stride) && ok(a.h_out, a.h_out_stride) && ok(a.x_out, a.x_stride) &&
          ok(a.dy, a.dy_stride) && ok(a.dgate, a.dgate_stride) && ok(a.dres, a.dres_stride) && aligned(a.w, 16) &&
-         aligned(a.scale, 16) && aligned(a.w_next, 16) && per_thread(a.dim / kVec<E>, 4) != 0;
+         aligned(a.scale, 16) && aligned(a.w_next, 16) && per_thread(a.dim / Wide<E>::N, 4) != 0;
 }
 
-template <class E>
+template <class P>
 void set_vecs(Args& a) {
-  a.vecs = a.dim / kVec<E>;
+  a.vecs = a.dim / P::N;
   const int per = a.vecs / a.groups;
   a.vecs_log2 = -1;
   for (int k = 0; k <= 5; ++k)
@@ -757,35 +812,54 @@ void set_vecs(Args& a) {
 template <class E>
 int launch_norm(Args a, cudaStream_t st) {
   const unsigned rows = static_cast<unsigned>(a.rows);
-  if (!by_vectors<E>(a, false)) {
+  const bool wide = by_vectors<E>(a, false);
+  if (!wide && a.dim > kSingles * Single<E>::kMost) {
     norm_any_kernel<E><<<rows, kAnyThreads, 0, st>>>(a);
     return check_launch("norm_any_kernel");
   }
-  set_vecs<E>(a);
-  const int per = per_thread(a.vecs, 4), threads = ((a.vecs + per - 1) / per + 31) / 32 * 32;
+  if (wide) set_vecs<Wide<E>>(a);
+  else set_vecs<Single<E>>(a);
+  const int per = wide ? per_thread(a.vecs, 4) : a.vecs <= 4 * kThreads ? 4 : kSingles;
+  const int threads = ((a.vecs + per - 1) / per + 31) / 32 * 32;
   const size_t smem = a.groups > 1 && a.vecs_log2 < 0 ? sizeof(float) * (a.vecs + a.groups) : 0;
-  if (per == 1) norm_kernel<E, 1><<<rows, threads, smem, st>>>(a);
-  else if (per == 2) norm_kernel<E, 2><<<rows, threads, smem, st>>>(a);
-  else norm_kernel<E, 4><<<rows, threads, smem, st>>>(a);
+  if (!wide && per == 4) norm_kernel<Single<E>, 4><<<rows, threads, smem, st>>>(a);
+  else if (!wide) norm_kernel<Single<E>, kSingles><<<rows, threads, smem, st>>>(a);
+  else if (per == 1) norm_kernel<Wide<E>, 1><<<rows, threads, smem, st>>>(a);
+  else if (per == 2) norm_kernel<Wide<E>, 2><<<rows, threads, smem, st>>>(a);
+  else norm_kernel<Wide<E>, 4><<<rows, threads, smem, st>>>(a);
   return check_launch("norm_kernel");
 }
 
 template <class E>
 int launch_grad(Args a, float* dw, float* ds, float* dn, int sms, cudaStream_t st) {
   // two blocks an SM, or one where a block's rows take more than half of the shared memory
-  const int at_once = by_vectors<E>(a, true) && kRing * kArrays * static_cast<int64_t>(a.dim) * E::kBytes > 112 * 1024 ? 1 : 2;
+  const bool wide = by_vectors<E>(a, true);
+  const int at_once = wide && kRing * kArrays * static_cast<int64_t>(a.dim) * E::kBytes > 112 * 1024 ? 1 : 2;
   const int blocks = static_cast<int>(std::min<int64_t>(a.rows, std::min(kParts, at_once * sms)));
   if (blocks > 0) {
-    if (!by_vectors<E>(a, true)) {
+    if (!wide && a.dim > kSingles * Single<E>::kMost) {
       norm_grad_any_kernel<E><<<blocks, kAnyThreads, 0, st>>>(a);
+    } else if (!wide) {
+      set_vecs<Single<E>>(a);
+      const int per = a.vecs <= 4 * kThreads ? 4 : kSingles, threads = ((a.vecs + per - 1) / per + 31) / 32 * 32;
+      const size_t smem = sizeof(float) * (2 * a.vecs + (a.groups > 1 && a.vecs_log2 < 0 ? a.vecs + a.groups : 0));
+      auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
+        int r = opt_in(reinterpret_cast<const void*>(kernel), done);
+        if (r == ENGRAM_OK) kernel<<<blocks, threads, smem, st>>>(a);
+        return r;
+      };
+      static std::atomic<uint64_t> done[2] = {{0}, {0}};
+      int r = per == 4 ? go(norm_grad_kernel<Single<E>, 4, kThreads>, done[0])
+                       : go(norm_grad_kernel<Single<E>, kSingles, 1024>, done[1]);
+      if (r) return r;
     } else {
-      set_vecs<E>(a);
+      set_vecs<Wide<E>>(a);
       // two vectors a thread at most: the sums of four's columns would not fit the registers
       const int per = a.vecs <= kRingThreads ? 1 : 2, threads = ((a.vecs + per - 1) / per + 31) / 32 * 32;
       const size_t smem = a.groups > 1 && a.vecs_log2 < 0 ? static_cast<size_t>(a.vecs + a.groups + 3) / 4 * 16 : 0;
       const size_t ring = smem + static_cast<size_t>(kRing) * kArrays * a.vecs * 16;
       if (ring > kRingSmem) {
-        norm_grad_kernel<E, 2, 2 * kThreads><<<blocks, threads, smem, st>>>(a);
+        norm_grad_kernel<Wide<E>, 2, 2 * kThreads><<<blocks, threads, smem, st>>>(a);
       } else {
         auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
           int r = opt_in(reinterpret_cast<const void*>(kernel), done);
@@ -793,7 +867,7 @@ int launch_grad(Args a, float* dw, float* ds, float* dn, int sms, cudaStream_t s
           return r;
         };
         static std::atomic<uint64_t> done[2] = {{0}, {0}};
-        int r = per == 1 ? go(norm_grad_ring_kernel<E, 1>, done[0]) : go(norm_grad_ring_kernel<E, 2>, done[1]);
+        int r = per == 1 ? go(norm_grad_ring_kernel<Wide<E>, 1>, done[0]) : go(norm_grad_ring_kernel<Wide<E>, 2>, done[1]);
         if (r) return r;
       }
     }

@@ -65,7 +65,8 @@ def run(T, D, kind, seed, groups=1, gate=True, res=True, scaled=True, weighted=T
 @pytest.mark.parametrize("T,D,groups", [(1, 1, 1), (3, 8, 1), (5, 7, 7), (4, 80, 1), (9, 80, 4), (3, 257, 1), (700, 64, 1),
                                         (17, 1280, 10), (300, 1280, 1), (6, 5120, 40), (330, 5120, 1), (2, 5128, 1),
                                         (5, 4096, 1024), (4, 960, 4), (3, 8200, 5), (7, 8192, 1), (2, 16384, 2),
-                                        (2, 16392, 1), (1, 40001, 1), (2, 2400, 50)])
+                                        (2, 16392, 1), (1, 40001, 1), (2, 2400, 50), (3, 4001, 1), (2, 8191, 1),
+                                        (9, 6003, 3), (4, 2047, 23), (3, 40005, 9)])
 def test_forward_and_gradient(T, D, groups, kind):
     run(T, D, kind, 100, groups)
 
