@@ -1026,6 +1026,10 @@ def _current_stream(idx: int) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
+# the current device's number, likewise
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _need_rows(t: torch.Tensor, name: str, dtype, device, n_rows: int, width: int) -> int:
     """Checks a [n_rows][width] device matrix with unit column stride; returns its row stride in elements."""
     if not isinstance(t, torch.Tensor):
@@ -1349,13 +1353,15 @@ def engram_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logi
 
 def _call(idx: int, name: str, fn, *args):
     """An entry point on the device (number idx) of its tensors, which need not be the current one."""
-    if torch.cuda.current_device() == idx:
+    if _current_device() == idx:
         rc = fn(*args, _raw_stream(idx))
+        if rc:
+            _check(rc, name)
     else:
         with torch.cuda.device(idx):
             rc = fn(*args, _raw_stream(idx))
-    if rc:
-        _check(rc, name)
+            if rc:
+                _check(rc, name)
 
 
 def delta_carry(n_tokens: int, n_seqs: int, key_heads: int, heads: int, dk: int, dv: int, device) -> torch.Tensor:
@@ -1601,14 +1607,15 @@ def engram_norm_add_grad(dh: Optional[torch.Tensor], y: torch.Tensor, w: Optiona
     wp = _weights(w, "w", y, idx, D // groups)
     sp = _weights(scale, "scale", y, idx, D)
     np = _weights(w_next, "w_next", y, idx, D)
-    new = functools.partial(torch.empty, (n, D), dtype=y.dtype, device=y.device)
-    dy = new() if dy is None else dy
-    dgate = new() if dgate is None and gate is not None else dgate
-    dres = new() if dres is None and residual else dres
-    of = functools.partial(torch.empty, dtype=torch.float32, device=y.device)
-    dw = None if w is None else of(D // groups)
-    dscale = None if scale is None else of(D)
-    dw_next = None if w_next is None or dx is None else of(D)
+    if dy is None:
+        dy = torch.empty((n, D), dtype=y.dtype, device=y.device)
+    if dgate is None and gate is not None:
+        dgate = torch.empty((n, D), dtype=y.dtype, device=y.device)
+    if dres is None and residual:
+        dres = torch.empty((n, D), dtype=y.dtype, device=y.device)
+    dw = None if w is None else torch.empty(D // groups, dtype=torch.float32, device=y.device)
+    dscale = None if scale is None else torch.empty(D, dtype=torch.float32, device=y.device)
+    dw_next = None if w_next is None or dx is None else torch.empty(D, dtype=torch.float32, device=y.device)
     if workspace is None:
         if dw is not None or dscale is not None or dw_next is not None:
             workspace = norm_add_workspace(n, D, y.device)

@@ -541,7 +541,7 @@ __device__ __forceinline__ void quad_sync(int quad) { asm volatile("bar.sync %0,
 // A block of one quad has more warps: four for the copies and, forwards, four for Y.  The
 // quad's own, one on each of the SM's four parts, are bound by the instructions that they
 // issue one after another (one sequence of 16,381 positions in 10 heads, us: 745 without
-// either, 546 with those for the copies, %s with both).
+// either, 546 with those for the copies, 520 with both).
 template <int NQ>
 constexpr bool kAlone = NQ == 1;
 constexpr int kCopiers = 128;
@@ -623,11 +623,14 @@ inline int opt_in(const void* kernel, int smem, std::atomic<uint64_t>& done) {
   return ENGRAM_OK;
 }
 
-// Quads of a block: four where there are blocks enough for the SMs (they share the copies
-// of a chunk's inputs), else one, so that few sequences and heads spread over more SMs.
+// Quads of a block: four, which share the copies of a chunk's inputs, where such blocks
+// come to three quarters of the SMs or more; else one, so that few sequences and heads
+// spread over more SMs.  (dk = dv = 128, bf16: a chunk takes a block of four quads 6.4 us
+// and one of one 2.0, measured forwards: four blocks of one on an SM one after another
+// take 8.0, three 6.0.)
 template <class E>
 bool many_quads(const Args<E>& a, int sms) {
-  return E::kBytes == 2 && static_cast<int64_t>(a.n_seqs) * a.heads * ((a.dv + 63) / 64) >= sms;
+  return E::kBytes == 2 && static_cast<int64_t>(a.n_seqs) * a.heads * ((a.dv + 63) / 64) * 4 >= 3 * static_cast<int64_t>(sms);
 }
 
 inline bool pieces(const void* p, int64_t stride, int bytes) { return aligned(p, 16) && stride * bytes % 16 == 0; }

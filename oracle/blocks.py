@@ -169,8 +169,9 @@ def delta(q, k, v, g, b, cu: List[int], keys: int, scale: float, mask: Optional[
                 continue
             before[t] = S
             S = S * f[t][:, None, None]
-            us[t] = beta[t][:, None] * (v[t] - (S * k[t][:, :, None]).sum(1))
-            S = S + k[t][:, :, None] * us[t][:, None]
+            u = beta[t][:, None] * (v[t] - (S * k[t][:, :, None]).sum(1))
+            S = S + k[t][:, :, None] * u[:, None]
+            us[t] = u
             y[t] = scale * (S * q[t][:, :, None]).sum(1)
         if out is not None:
             out[slot] = S
