@@ -142,6 +142,41 @@ def test_masked_and_padding_positions_may_hold_anything():
         assert (t[80:110] == 0).all() and (t[m.bool()] == 0).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_everything_masked(kind):
+    T, keys, H, dk, dv, cu = 150, 1, 2, 32, 24, i64([0, 90, 150])
+    args, dy = inputs(T, keys, H, dk, dv, kind, 87), make((T, H * dv), kind, 88)
+    s0, ds = make((2, H, dk, dv), "f32", 89), make((2, H, dk, dv), "f32", 90)
+    m, out, carry = torch.ones(T, dtype=torch.uint8, device=DEV), torch.zeros_like(s0), eg.delta_carry(T, 2, keys, H, dk, dv, DEV)
+    y = eg.engram_delta(*args, cu, keys, mask=m, state=s0, state_out=out, carry=carry)
+    assert (y == 0).all() and torch.equal(out, s0)
+    back = ds.clone()
+    grads = eg.engram_delta_grad(dy, *args, carry, cu, keys, mask=m, dstate=back)
+    assert all((g == 0).all() for g in grads) and torch.equal(back, ds)
+
+
+def test_arrays_past_two_to_the_31_elements():
+    """The last sequence of arrays of 2^31 values and more gives what it gives alone."""
+    H, d, n = 64, 128, 300
+    T = 2 ** 31 // (H * d) + 1000
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB of device memory")
+    gen = torch.Generator(DEV).manual_seed(7)
+    q, k = (torch.randn((T, 16), generator=gen, device=DEV).mul_(0.25).bfloat16() for _ in range(2))
+    g, b = (torch.randn((T, H), generator=gen, device=DEV).bfloat16() for _ in range(2))
+    v, dy = (torch.empty((T, H * d), dtype=torch.bfloat16, device=DEV).normal_(generator=gen) for _ in range(2))
+    args, cu = (q, k, v, g, b), i64([0, 1000, T - n, T])
+    carry = eg.delta_carry(T, 3, 1, H, 16, d, DEV)
+    y = eg.engram_delta(*args, cu, 1, carry=carry)
+    got = eg.engram_delta_grad(dy, *args, carry, cu, 1)
+    last = [t[T - n:].contiguous() for t in args]
+    carry = eg.delta_carry(n, 2, 1, H, 16, d, DEV)
+    cu = i64([0, 0, n])
+    assert torch.equal(y[T - n:], eg.engram_delta(*last, cu, 1, carry=carry))
+    for u, w in zip(got, eg.engram_delta_grad(dy[T - n:].contiguous(), *last, carry, cu, 1)):
+        assert torch.equal(u[T - n:], w)
+
+
 def test_outputs_between_other_columns_and_positions_outside():
     T, keys, H, dk, dv, cu = 100, 2, 4, 32, 24, [10, 40, 90]
     args, dy = inputs(T, keys, H, dk, dv, "bf16", 90), make((T, H * dv), "bf16", 95)
