@@ -76,6 +76,7 @@ struct Args {
   float scale;
   bool vec;        // rows of q, k, v and dy in 16-byte pieces
   bool pairs;      // rows of y or dv in pairs of elements
+  bool key_pairs;  // rows of dq and dk, likewise
   bool has_state;  // slots are checked against n_slots
   // workspace
   int32_t* first;  // [n_seqs + 1] number of a sequence's first chunk

@@ -617,14 +617,21 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
         auto* to_q = a.dq + (p + r) * a.dq_stride + hk * a.dk;
         auto* to_k = a.dk_out + (p + r) * a.dk_stride + hk * a.dk;
 #pragma unroll
-        for (int t = 0; t < L::kKN; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int c = nk + t * 8 + t2 + e;
-            if (c >= a.dk) continue;
-            E::store(to_q + c, on ? cq[t][2 * j + e] : 0.f);
-            E::store(to_k + c, on ? ck[t][2 * j + e] : 0.f);
+        for (int t = 0; t < L::kKN; ++t) {
+          const int c = nk + t * 8 + t2;
+          if (c >= a.dk) continue;
+          const float q0 = on ? cq[t][2 * j] : 0.f, q1 = on ? cq[t][2 * j + 1] : 0.f;
+          const float k0 = on ? ck[t][2 * j] : 0.f, k1 = on ? ck[t][2 * j + 1] : 0.f;
+          if (E::kBytes == 2 && a.key_pairs) {
+            *reinterpret_cast<uint32_t*>(to_q + c) = pack(q0, q1);
+            *reinterpret_cast<uint32_t*>(to_k + c) = pack(k0, k1);
+          } else {
+            E::store(to_q + c, q0);
+            E::store(to_k + c, k0);
+            if (c + 1 < a.dk) E::store(to_q + c + 1, q1);
+            if (c + 1 < a.dk) E::store(to_k + c + 1, k1);
           }
+        }
       }
     }
     if (warp == 0) {  // what crosses a position: two positions a lane
@@ -793,6 +800,8 @@ extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void
             pieces(dy_d, dy_stride, E::kBytes) && pieces(dv_d, dv_stride, E::kBytes) && aligned(carry_d, 16) && dk % 8 == 0 &&
             dv % 8 == 0;
     a.pairs = dv % 2 == 0 && dv_stride % 2 == 0 && aligned(dv_d, 2 * E::kBytes);
+    a.key_pairs = dk % 2 == 0 && dq_stride % 2 == 0 && dk_stride % 2 == 0 && aligned(dq_d, 2 * E::kBytes) &&
+                  aligned(dk_d, 2 * E::kBytes);
     a.status = status_d;
     const Space s = space(workspace_d, n_tokens, n_seqs, key_heads, heads, dk, dv, true);
     a.first = s.first;
