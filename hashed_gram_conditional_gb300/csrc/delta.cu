@@ -187,35 +187,22 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(Args<E> a) {
   }
   copies_done();
   __syncthreads();
-  const int m = warp * 16;  // a warp has 16 rows, and the columns up to the diagonal
-  float ck[kC / 8][4], cq[kC / 8][4];
-  clear(ck);
-  clear(cq);
-  for (int k = 0; k < KD; k += 16) {
-    uint32_t fk[kIn<E>][4], fq[kIn<E>][4];
+  // K K^T and Q K^T: the triangle's ten blocks of 16 x 16 in turn, three a warp at most
+  float ck[3][2][4], cq[3][2][4];
+  auto block = [&](int n, int& bt, int& bi) {
+    const int b = warp + n * 4;
+    bt = b >= 6 ? 3 : b >= 3 ? 2 : b >= 1 ? 1 : 0;
+    bi = b - bt * (bt + 1) / 2;
+    return b < kBlocks;
+  };
 #pragma unroll
-    for (int i = 0; i < kIn<E>; ++i) {
-      Rows{K}(fk[i], m, k, i);
-      Rows{Q}(fq[i], m, k, i);
-    }
-#pragma unroll
-    for (int n = 0; n < kC / 16; ++n) {
-      if (n > warp) continue;
-#pragma unroll
-      for (int j = kIn<E> - 1; j >= 0; --j) {
-        uint32_t fb[2][2];
-        Across{K}.get<2>(fb, k, n * 16, j);
-#pragma unroll
-        for (int i = kIn<E> - 1; i >= 0; --i)
-          if (i + j < kIn<E>) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              mma(ck[n * 2 + e], fk[i], fb[e][0], fb[e][1]);
-              mma(cq[n * 2 + e], fq[i], fb[e][0], fb[e][1]);
-            }
-          }
-      }
-    }
+  for (int n = 0; n < 3; ++n) {
+    clear(ck[n]);
+    clear(cq[n]);
+    int bt, bi;
+    if (!block(n, bt, bi)) continue;
+    product<kIn<E>, kIn<E>, kIn<E>>(ck[n], Rows{K}, Across{K}, bt * 16, bi * 16, 0, KD);
+    product<kIn<E>, kIn<E>, kIn<E>>(cq[n], Rows{Q}, Across{K}, bt * 16, bi * 16, 0, KD);
   }
   __syncthreads();  // K and Q are no longer needed
   const size_t unit = unit_of(a, blockIdx.x, h);
@@ -223,22 +210,27 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(Args<E> a) {
   for (int i = tid; i < static_cast<int>(sizeof(Gates)) / 4; i += kPrepareThreads)
     reinterpret_cast<float*>(a.gates + unit)[i] = reinterpret_cast<const float*>(&gt)[i];
 #pragma unroll
-  for (int n = 0; n < kC / 8; ++n) {
-    if (n / 2 > warp) continue;
-    const int i = n * 8 + t2;
-    const float2 hi = *reinterpret_cast<const float2*>(&gt.hi[i]), lo = *reinterpret_cast<const float2*>(&gt.lo[i]);
+  for (int n = 0; n < 3; ++n) {
+    int bt, bi;
+    if (!block(n, bt, bi)) continue;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int t = m + g + j * 8;
-      const float d0 = i <= t ? expf((gt.hi[t] - hi.x) + (gt.lo[t] - lo.x)) : 0.f;
-      const float d1 = i + 1 <= t ? expf((gt.hi[t] - hi.y) + (gt.lo[t] - lo.y)) : 0.f;
-      *reinterpret_cast<float2*>(A + t * kPitch + i) = make_float2(i < t ? gt.beta[t] * d0 * ck[n][2 * j] : 0.f,
-                                                                    i + 1 < t ? gt.beta[t] * d1 * ck[n][2 * j + 1] : 0.f);
-      put_tri<kStateTerms>(tri + kStateTerms * kTerm, t, i, i <= t ? a.scale * d0 * cq[n][2 * j] : 0.f,
-                           i + 1 <= t ? a.scale * d1 * cq[n][2 * j + 1] : 0.f);
+    for (int e = 0; e < 2; ++e) {
+      const int i = bi * 16 + e * 8 + t2;
+      const float2 hi = *reinterpret_cast<const float2*>(&gt.hi[i]), lo = *reinterpret_cast<const float2*>(&gt.lo[i]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int t = bt * 16 + g + j * 8;
+        const float d0 = i <= t ? expf((gt.hi[t] - hi.x) + (gt.lo[t] - lo.x)) : 0.f;
+        const float d1 = i + 1 <= t ? expf((gt.hi[t] - hi.y) + (gt.lo[t] - lo.y)) : 0.f;
+        *reinterpret_cast<float2*>(A + t * kPitch + i) =
+            make_float2(i < t ? gt.beta[t] * d0 * ck[n][e][2 * j] : 0.f, i + 1 < t ? gt.beta[t] * d1 * ck[n][e][2 * j + 1] : 0.f);
+        put_tri<kStateTerms>(tri + kStateTerms * kTerm, t, i, i <= t ? a.scale * d0 * cq[n][e][2 * j] : 0.f,
+                             i + 1 <= t ? a.scale * d1 * cq[n][e][2 * j + 1] : 0.f);
+      }
     }
   }
-  __syncwarp();
+  __syncthreads();
+  const int m = warp * 16;
   // (I + A)^-1: a warp's block of 16 by substitution, a column a lane; then twice
   // [M11 0; -M22 A21 M11 M22].  A's blocks above the diagonal hold what comes in between.
   if (lane < 16) {
