@@ -313,7 +313,7 @@ struct Head {  // in front of the dynamic shared memory
   uint64_t known[kTold], used[kTold];  // the target's entries are ready / no longer needed
   float2 pair[kPairs][kMaxCluster * kW];
   float2 stats[kMaxDepth];     // a row's (maximum, sum), for the copying warp
-  float weight[kMaxDepth];
+  float weight[kMaxDepth], mass[kMaxDepth];
   float2 told[kTold];    // what the target keeps of a row
   int abort;
 };
@@ -415,8 +415,8 @@ __global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const t
       const float w = h.weight[i % a.depth];
       const float2 known = h.told[i % a.keep], st = h.stats[i % a.depth];
       const typename G::Entries e = entries(i);
-      const float mass = G::mass(a, e, known, st.x, st.y, inv_tau);
-      const bool none = w == 0.f || mass == 0.f;
+      const float mass = h.mass[i % a.depth];  // (made by the walk: the next copy does not wait for it)
+      const bool none = mass == 0.f;
       int edge = -1;  // a value of the row's first or last vector that this lane finishes
       float edge_z = 0.f;
       if (dz != nullptr && !none) {
@@ -487,7 +487,10 @@ __global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const t
       join_warp(m, s, c);
       const float w = h.weight[i % a.depth];
       const float mass = w == 0.f ? 0.f : G::mass(a, entries(i), h.told[i % a.keep], m, s, inv_tau);
-      if (tid == 0) h.stats[i % a.depth] = make_float2(m, s);
+      if (tid == 0) {
+        h.stats[i % a.depth] = make_float2(m, s);
+        h.mass[i % a.depth] = mass;
+      }
       if (dz != nullptr) {
         r.at(z, dz, a, row_at(i), rank, true);
         if (mass == 0.f) {  // nothing to learn here

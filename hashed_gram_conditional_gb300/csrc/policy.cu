@@ -67,10 +67,18 @@ struct Sampled {
   static __device__ __forceinline__ float clipped(const Args& a, float r) {
     return r < 1.f - a.low ? 1.f - a.low : r > 1.f + a.high ? 1.f + a.high : r;  // (a NaN stays)
   }
+  // Every warp that walks a row computes this, with the hardware's exponential (2^-22) as
+  // for the row's own; the loss, one warp's work, has expf and expm1f.
   static __device__ __forceinline__ float mass(const Args& a, const Entries& e, float2, float m, float s, float inv_tau) {
-    const float l = logp(e, m, s, inv_tau), r = ratio(a, e, l), plain = r * e.at->adv;
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float l = logp(e, m, s, inv_tau), r = a.old != nullptr ? rows::ex2((l - e.at->old) * kLog2e) : 1.f;
+    const float plain = r * e.at->adv;
     float d = plain > clipped(a, r) * e.at->adv ? 0.f : plain;  // -dloss/dl / w
-    if (a.ref != nullptr) d = fmaf(a.kl, expm1f(e.at->ref - l), d);
+    if (a.ref != nullptr) {
+      const float x = e.at->ref - l;
+      // e^x - 1; for small x, where the difference would cancel, from its series
+      d = fmaf(a.kl, fabsf(x) < 0.125f ? fmaf(gap_series(x) * x, x, x) : rows::ex2(x * kLog2e) - 1.f, d);
+    }
     return d * inv_tau * inv_tau;
   }
   template <class E>
@@ -99,7 +107,9 @@ struct Sampled {
   // e^d - 1 - d; for small d, where the difference would cancel, its series, whose
   // next term is below 2^-24 of the first for |d| < 1/8
   static __device__ __forceinline__ float gap(float d) {
-    if (fabsf(d) >= 0.125f) return expm1f(d) - d;
+    return fabsf(d) >= 0.125f ? expm1f(d) - d : gap_series(d) * d * d;
+  }
+  static __device__ __forceinline__ float gap_series(float d) {
     float p = 1.f / 362880.f;
     p = fmaf(p, d, 1.f / 40320.f);
     p = fmaf(p, d, 1.f / 5040.f);
@@ -107,8 +117,7 @@ struct Sampled {
     p = fmaf(p, d, 1.f / 120.f);
     p = fmaf(p, d, 1.f / 24.f);
     p = fmaf(p, d, 1.f / 6.f);
-    p = fmaf(p, d, 0.5f);
-    return p * d * d;
+    return fmaf(p, d, 0.5f);
   }
 };
 
