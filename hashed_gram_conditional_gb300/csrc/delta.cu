@@ -123,9 +123,10 @@ constexpr int kPrepareSmem = std::max(2 * kIn<E> * mat_bytes(kC, KD), 2 * kC * k
 
 // A block of four warps makes M and P of one head in one chunk.  K K^T and Q K^T stay in
 // the registers until they are A and P; A and M take the place of K and Q.  Heads that
-// share a key head compute its products again: a third of a microsecond of the tensor
-// cores for each head, where sharing them left most warps waiting (10,480 chunks and
-// heads: see the figures at scan_rows_kernel).
+// share a key head compute its products again, which is little beside the rest; blocks of
+// eight warps for all of them took twice as long (110 us against 52 for 2560 chunks and
+// heads, dk = 128).  Bound by instructions issued (1.8 a clock and SM) and the waits
+// between the inverse's steps.
 template <class E, int KD>
 __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(Args<E> a) {
   constexpr int kRoom = std::max(2 * kIn<E> * mat_bytes(kC, KD), 2 * kC * kPitch * 4);
@@ -295,6 +296,14 @@ template int launch_prepare<train::F32>(const Args<train::F32>&, cudaStream_t);
 // instructions a warp at most: K S and U and what is added to S in three terms, Q S and
 // P U in two.  bf16: the next chunk's inputs are copied meanwhile; fp32's terms are made
 // on the way to shared memory and take the room.
+//
+// Four quads a block (16,384 positions in 4 sequences, 40 heads of 128, bf16: about 1000 us): the
+// tensor cores are busy for 41 % of the time and shared memory for 70; what is left are
+// waits of warps that have nothing else to do between the barriers.  One quad (16,381
+// positions, 10 heads: 520 us, 2.0 a chunk): instructions that follow one another.  A form
+// with 16 columns and the whole of their state a warp, without anything handed on, read a
+// third of the shared memory and took as long: two warps on each part of an SM are all
+// that its registers allow.
 template <class E, int KD, int NQ>
 struct Scan {
   static constexpr int kT = kAlone<NQ> ? kCopiers : NQ * 128, kThreads = kAlone<NQ> ? 256 + kCopiers : kT, kStages = E::kBytes == 2 ? 2 : 1, kB = kC / 16;
@@ -606,7 +615,8 @@ static_assert(Scan<train::Bf16, 128, 4>::kSmem <= 232448 && Scan<train::F32, 128
 
 // One token: a block has one sequence's state in one head, kV x 32 of the value
 // columns, in registers from the load to the store.  Bound by memory: the state is
-// read once and written once.
+// read once and written once (256 sequences of 40 heads of 128 x 128, 1.35 GB: 212 us, 6.4
+// TB/s, 95 % of a copy's rate).
 constexpr int kStepRows = kMaxDim / kWarps;  // a thread's rows: one in eight
 
 template <class E, int kV>

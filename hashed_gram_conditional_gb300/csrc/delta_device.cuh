@@ -19,11 +19,11 @@
 // type bf16.  Of the terms' products those are taken that are not below the last
 // bit that is kept.  (mma.sync's bf16 form does 1024 multiply-adds a clock and SM
 // here and its tf32 form 512, measured: three bf16 terms of one operand cost less
-// than two tf32 ones.)  The tcgen05 form, four times as fast, wants 128 rows: a
-// chunk's 64 positions against the whole of a head's state.  One block a head would
-// leave most SMs without work where there are few sequences, and every operand
-// would go through registers between two products all the same, to be scaled and
-// split; the value columns are spread over blocks instead.
+// than two tf32 ones.)  The tcgen05 form, three times as fast (1920 TFLOP/s against
+// 592), wants 128 rows: the whole of a head's value columns.  One block a head would
+// leave most SMs without work where there are few sequences, and between any two
+// products every value has to come to registers all the same, to be scaled and
+// split; here that is where they are, and the value columns are spread over blocks.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -40,7 +40,7 @@ namespace engram {
 namespace delta {
 
 constexpr int kC = ENGRAM_DELTA_CHUNK;  // 64 positions
-constexpr int kThreads = 256, kWarps = kThreads / 32;  // of most kernels
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxDim = ENGRAM_DELTA_MAX_DIM;
 // Lower triangles of 64 x 64 are kept as ten blocks of 16 x 16, a term's 512 bytes
 // each, the 16-byte halves of a block's rows 4 to 7 and 12 to 15 exchanged (eight
@@ -264,20 +264,6 @@ struct Cols {  // A(m, k) = X[k][m]
   }
 };
 __device__ __forceinline__ uint32_t tri_at(int row, int half) { return row * 32 + ((half ^ ((row >> 2) & 1)) << 4); }
-struct TriRows {  // A(m, k) = X[m][k], a triangle's blocks
-  uint32_t base;
-  __device__ __forceinline__ void operator()(uint32_t (&r)[4], int m, int k, int n) const {
-    const int l = lane_id(), i = m >> 4, j = k >> 4;
-    ld4(r, base + n * kTerm + (i * (i + 1) / 2 + j) * 512 + tri_at(l & 15, l >> 4));
-  }
-};
-struct TriCols {  // A(m, k) = X[k][m]
-  uint32_t base;
-  __device__ __forceinline__ void operator()(uint32_t (&r)[4], int m, int k, int n) const {
-    const int l = lane_id(), i = k >> 4, j = m >> 4;
-    ld4t(r, base + n * kTerm + (i * (i + 1) / 2 + j) * 512 + tri_at((l & 7) + (l >> 4) * 8, (l >> 3) & 1));
-  }
-};
 // 16 x 8 N pieces of an operand B(k, n)
 struct Down {  // B(k, n) = X[k][n]
   Mat x;
@@ -314,7 +300,7 @@ struct Across {  // B(k, n) = X[n][k]
 // products of terms i and j with i + j < kLimit.  The tensor cores cut each sum of an
 // instruction off at the accumulator's last bit: where 24 bits are to be kept, the
 // small terms' products have an accumulator of their own, so that the large ones' is
-// cut once for every 16 of k and not six times (1.8e-6 against 4e-7 of the result).
+// cut once for every 16 of k and not six times (fp32: 1.8e-6 against 5e-7 of the result).
 template <int TA, int TB, int kLimit, int N, class A, class B>
 __device__ __forceinline__ void product(float (&c)[N][4], const A& a, const B& b, int m, int n, int k0, int k1) {
   constexpr bool kApart = kLimit > 2;
