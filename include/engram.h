@@ -737,9 +737,10 @@ int engram_recurrence_step(const void* x_d, int64_t x_stride, const void* g_d, i
  *                its first), or NULL; may be state_d
  *   carry_d      float32, engram_delta_carry_bytes(...) bytes, or NULL: for the backward
  *                pass, the state in front of every ENGRAM_DELTA_CHUNK positions of a
- *                sequence
+ *                sequence and every position's u, laid out as that pass reads them
  *   workspace_d  engram_delta_workspace_bytes(..., 0) bytes, 256-byte aligned; its
- *                contents on entry do not matter
+ *                contents on entry do not matter, and the call has it to itself until
+ *                it is done (two graphs that may run at once have two)
  * 1 <= dk, dv <= ENGRAM_DELTA_MAX_DIM; any stride and element-aligned pointers; outputs
  * overlap no input (but state_out_d may be state_d).  States and sums are fp32.  g below
  * -80 counts as -80 and b below -40 as -40.  An infinity or a NaN in a position that is
