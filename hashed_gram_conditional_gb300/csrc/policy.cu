@@ -49,13 +49,15 @@ struct Sampled {
   static __device__ __forceinline__ void read(const Args& a, const typename E::T* z, int64_t row, float, int lane,
                                               const Entries& e, void*, float& x0, float& x1) {
     x0 = x1 = 0.f;
-    if (lane != 0) return;
-    const int32_t id = __ldg(a.ids + row);
-    e.at->id = id;
-    e.at->logit = E::load(z + id);
-    e.at->adv = __ldg(a.adv + row);
-    e.at->old = a.old != nullptr ? __ldg(a.old + row) : 0.f;
-    e.at->ref = a.ref != nullptr ? __ldg(a.ref + row) : 0.f;
+    if (lane == 0) {
+      const int32_t id = __ldg(a.ids + row);
+      e.at->id = id;
+      e.at->logit = E::load(z + id);
+      e.at->adv = __ldg(a.adv + row);
+      e.at->old = a.old != nullptr ? __ldg(a.old + row) : 0.f;
+      e.at->ref = a.ref != nullptr ? __ldg(a.ref + row) : 0.f;
+    }
+    __syncwarp();
   }
 
   static __device__ __forceinline__ float logp(const Entries& e, float m, float s, float inv_tau) {
@@ -105,9 +107,10 @@ struct Sampled {
     if (a.logp != nullptr) a.logp[row] = l;
   }
   // e^d - 1 - d; for small d, where the difference would cancel, its series, whose
-  // next term is below 2^-24 of the first for |d| < 1/8
+  // next term is below 2^-24 of the first for |d| < 1/8; infinite with e^d
   static __device__ __forceinline__ float gap(float d) {
-    return fabsf(d) >= 0.125f ? expm1f(d) - d : gap_series(d) * d * d;
+    const float x = expm1f(d);
+    return x == INFINITY ? x : fabsf(d) >= 0.125f ? x - d : gap_series(d) * d * d;
   }
   static __device__ __forceinline__ float gap_series(float d) {
     float p = 1.f / 362880.f;

@@ -840,8 +840,9 @@ int engram_distill(const void* logits_d, int32_t type, int64_t n_tokens, int64_t
  *   dlogits_d    [n_tokens][vocab] of `type`, rows dlogits_stride apart, or NULL
  *                (loss alone); may be logits_d
  * A position of weight 0, or without a token, is not read: its loss, l and gradient are
- * 0.  A logit of -inf has q = 0.  temperature positive and finite, kl and
- * the clip bounds finite and not negative.  The blocks that share a row wait for one
+ * 0.  A logit of -inf has q = 0; a token of such a logit has l = -inf, and with a KL
+ * term an infinite loss.  temperature positive and finite, kl and the clip bounds
+ * finite and not negative.  The blocks that share a row wait for one
  * another; a wait that runs out sets ENGRAM_ST_TIMEOUT, and the outputs are then
  * undefined. */
 int engram_policy(const void* logits_d, int32_t type, int64_t n_tokens, int64_t vocab, int64_t logits_stride,

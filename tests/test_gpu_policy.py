@@ -139,6 +139,36 @@ def test_logits_of_minus_infinity(V, kind):
     assert logp[0] == -math.inf and torch.isfinite(loss[1:]).all()
 
 
+@pytest.mark.parametrize("V", [600, 40000])
+def test_a_token_without_probability_is_infinitely_far(V):
+    z, ids, adv, old, ref, _ = inputs(20, V, "f32", 16, 1.0)
+    clean = eg.engram_policy(z, ids, adv, old_logp=old, ref_logp=ref, kl=0.1)
+    z[3, ids[3].long()] = float("-inf")
+    ref[5] = float("-inf")
+    loss, logp = eg.engram_policy(z, ids, adv, old_logp=old, ref_logp=ref, kl=0.1)
+    assert logp[3] == -math.inf and loss[3] == math.inf and loss[5] == math.inf
+    rest = [t for t in range(20) if t not in (3, 5)]
+    assert torch.equal(loss[rest], clean[0][rest]) and torch.equal(logp[rest], clean[1][rest])
+
+
+@pytest.mark.parametrize("V", [600, 40000])
+def test_two_calls_at_once(V):
+    """Calls on two streams share nothing."""
+    sets = [inputs(200, V, "bf16", 50 + k, 1.0) for k in range(2)]
+    want = [eg.engram_policy(z, ids, adv, old_logp=old, ref_logp=ref, kl=0.1, weight=w) for z, ids, adv, old, ref, w in sets]
+    sides = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for side, (z, ids, adv, old, ref, w) in zip(sides, sets):
+            with torch.cuda.stream(side):
+                got.append(eg.engram_policy(z, ids, adv, old_logp=old, ref_logp=ref, kl=0.1, weight=w,
+                                            dlogits=torch.empty_like(z)))
+        torch.cuda.synchronize()
+        for u, x in zip(got, want):
+            assert torch.equal(u[0], x[0]) and torch.equal(u[1], x[1])
+
+
 def test_small_kl_keeps_its_digits():
     """e^d - 1 - d at d of 1e-3 is 5e-7: the difference of its terms would have no digits left."""
     z, ids, adv, _, _, _ = inputs(50, 300, "f32", 21, 1.0)
