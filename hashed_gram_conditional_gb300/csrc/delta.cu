@@ -15,8 +15,8 @@ namespace delta {
 // as far as one block sorts them by counting (1024), else as they come.
 template <class E>
 __global__ void __launch_bounds__(1024) first_kernel(Args<E> a) {
-  __shared__ int warp_sum[32], counts[1024];
-  __shared__ int64_t before;
+  __shared__ int counts[1024];
+  __shared__ int64_t warp_sum[32], before;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) before = 0;
   for (int s0 = 0; s0 < a.n_seqs; s0 += 1024) {
@@ -29,10 +29,10 @@ __global__ void __launch_bounds__(1024) first_kernel(Args<E> a) {
     }
     if (a.n_seqs <= 1024) counts[threadIdx.x] = n;
     else if (s < a.n_seqs) a.order[s] = s;
-    int sum = n;
+    int64_t sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, sum, o);
+      const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += x;
     }
     __syncthreads();

@@ -241,12 +241,6 @@ __device__ __forceinline__ void ld4t(uint32_t (&r)[4], uint32_t at) {
                : "r"(at)
                : "memory");
 }
-__device__ __forceinline__ void ld2t(uint32_t& r0, uint32_t& r1, uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(at) : "memory");
-}
-__device__ __forceinline__ void ld2(uint32_t& r0, uint32_t& r1, uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(at) : "memory");
-}
 
 // 16 x 16 pieces of an operand A(m, k), as stored or transposed, of a term
 struct Rows {  // A(m, k) = X[m][k]
@@ -271,13 +265,13 @@ struct Down {  // B(k, n) = X[k][n]
   __device__ __forceinline__ void get(uint32_t (&r)[N][2], int k, int n, int t) const {
     const int l = lane_id();
     const uint32_t at = x.base + t * x.term + (k + (l & 15)) * x.pitch + n * 2;
+    static_assert(N % 2 == 0, "pairs of tiles");
 #pragma unroll
-    for (int j = 0; j + 1 < N; j += 2) {
+    for (int j = 0; j < N; j += 2) {
       uint32_t w[4];
       ld4t(w, at + (j * 8 + (l >> 4) * 8) * 2);
       r[j][0] = w[0]; r[j][1] = w[1]; r[j + 1][0] = w[2]; r[j + 1][1] = w[3];
     }
-    if (N & 1) ld2t(r[N - 1][0], r[N - 1][1], at + (N - 1) * 16);
   }
 };
 struct Across {  // B(k, n) = X[n][k]
@@ -286,13 +280,13 @@ struct Across {  // B(k, n) = X[n][k]
   __device__ __forceinline__ void get(uint32_t (&r)[N][2], int k, int n, int t) const {
     const int l = lane_id();
     const uint32_t at = x.base + t * x.term + k * 2 + ((l >> 3) & 1) * 16;
+    static_assert(N % 2 == 0, "pairs of tiles");
 #pragma unroll
-    for (int j = 0; j + 1 < N; j += 2) {
+    for (int j = 0; j < N; j += 2) {
       uint32_t w[4];
       ld4(w, at + (n + j * 8 + (l & 7) + (l >> 4) * 8) * x.pitch);
       r[j][0] = w[0]; r[j][1] = w[1]; r[j + 1][0] = w[2]; r[j + 1][1] = w[3];
     }
-    if (N & 1) ld2(r[N - 1][0], r[N - 1][1], at + (n + (N - 1) * 8 + (l & 7)) * x.pitch);
   }
 };
 
@@ -626,7 +620,7 @@ inline int check_sizes(int32_t type, int64_t n_tokens, int32_t keys, int32_t hea
                 int64_t n_slots, bool has_state, float scale) {
   if (!train::known_type(type)) return fail(ENGRAM_E_INVALID, "type %d is not ENGRAM_T_BF16 or ENGRAM_T_F32", type);
   if (n_tokens < 0 || n_seqs < 0) return fail(ENGRAM_E_INVALID, "negative number of positions or sequences");
-  if (n_tokens > 0x7fffff00 || n_seqs > 0x7fffff00) return fail(ENGRAM_E_RANGE, "too many positions or sequences");
+  if (n_tokens > 0x7ffffc00 || n_seqs > 0x7ffffc00) return fail(ENGRAM_E_RANGE, "too many positions or sequences");
   if (keys < 1 || heads < keys || heads % keys != 0 || heads > 65535)
     return fail(ENGRAM_E_SHAPE, "value heads must be a multiple of the key heads, and at most 65535");
   if (dk < 1 || dk > kMaxDim || dv < 1 || dv > kMaxDim) return fail(ENGRAM_E_SHAPE, "head widths must be in [1, %d]", kMaxDim);

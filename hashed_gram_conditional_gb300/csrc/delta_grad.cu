@@ -800,7 +800,7 @@ extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void
     a.dk = dk;
     a.dv = dv;
     a.scale = scale;
-    a.vec = pieces(q_d, q_stride, E::kBytes) && pieces(k_d, k_stride, E::kBytes) && pieces(v_d, v_stride, E::kBytes) &&
+    a.vec = pieces(q_d, q_stride, E::kBytes) && pieces(k_d, k_stride, E::kBytes) &&
             pieces(dy_d, dy_stride, E::kBytes) && pieces(dv_d, dv_stride, E::kBytes) && aligned(carry_d, 16) && dk % 8 == 0 &&
             dv % 8 == 0;
     a.pairs = dv % 2 == 0 && dv_stride % 2 == 0 && aligned(dv_d, 2 * E::kBytes);

@@ -239,6 +239,49 @@ def test_many_short_sequences():
     run(cu[-1], 1, 1, 8, 8, cu, "f32", 140, state=True)
 
 
+def test_many_short_sequences_of_several_heads():
+    """The same where a block has four quads."""
+    S = 1300
+    lens = torch.randint(0, 3, (S,), generator=torch.Generator().manual_seed(2)).tolist()
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    run(cu[-1], 1, 2, 16, 24, cu, "bf16", 145, masked=0.1, state=True)
+
+
+def test_sequences_that_lie_over_one_another_stay_in_bounds():
+    """They are no valid call: what they give is not defined, but nothing else is touched."""
+    T, H, d = 300, 2, 16
+    for S, kind in ((8, "bf16"), (200, "bf16"), (1500, "f32")):
+        args = inputs(T, 1, H, d, d, kind, 99)
+        cu = [0, T] * (S // 2) + [0]
+        out = torch.full((T + 8, H * d), 9.0, dtype=TYPES[kind], device=DEV)
+        states = torch.full((S + 2, H, d, d), 9.0, device=DEV)
+        room, more = eg.delta_carry(T, S, 1, H, d, d, DEV).numel(), 1000
+        carry = torch.full((room + more,), 9.0, device=DEV)
+        size = eg.delta_workspace(T, S, 1, H, d, d, DEV).numel()
+        space = torch.full((size + 4096,), 9, dtype=torch.uint8, device=DEV)
+        eg.engram_delta(*args, i64(cu), 1, state=states[1:-1], y=out[4:-4], carry=carry[:room], workspace=space[:size])
+        assert (out[:4] == 9).all() and (out[-4:] == 9).all() and (states[0] == 9).all() and (states[-1] == 9).all()
+        assert (carry[room:] == 9).all() and (space[size:] == 9).all()
+
+
+def test_two_calls_at_once():
+    """Calls on two streams with workspaces of their own."""
+    T, keys, H, dk, dv = 700, 2, 8, 128, 64
+    sets, cu = [inputs(T, keys, H, dk, dv, "bf16", 155 + 9 * k) for k in range(2)], i64([0, 200, 700])
+    want = [eg.engram_delta(*args, cu, keys) for args in sets]
+    sides = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for side, args in zip(sides, sets):
+            with torch.cuda.stream(side):
+                got.append(eg.engram_delta(*args, cu, keys))
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_no_positions():
     H, d = 2, 8
     e = [torch.empty((0, n), device=DEV) for n in (d, d, H * d, H, H)]

@@ -191,6 +191,32 @@ def test_outputs_between_other_columns_and_positions_outside():
         assert (u[:10] == 3).all() and (u[90:] == 3).all() and (o[:, :2] == 3).all() and (o[:, -3:] == 3).all()
 
 
+@pytest.mark.parametrize("S,keys,H,dk,dv,kind", [(1300, 1, 2, 16, 24, "bf16"), (1100, 1, 1, 8, 8, "f32")])
+def test_many_short_sequences(S, keys, H, dk, dv, kind):
+    """More sequences than are sorted by length."""
+    cu = [0]
+    for n in torch.randint(0, 3, (S,), generator=torch.Generator().manual_seed(3)).tolist():
+        cu.append(cu[-1] + n)
+    run(cu[-1], keys, H, dk, dv, cu, kind, 97, masked=0.1, state=True)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,keys,H,dk,dv", [(130, 1, 2, 32, 40), (90, 2, 2, 128, 64)])
+def test_a_carry_at_any_element(T, keys, H, dk, dv, kind):
+    """The kept states may lie at any multiple of four bytes, and the last of them ends inside a chunk."""
+    args, dy, cu = inputs(T, keys, H, dk, dv, kind, 98), make((T, H * dv), kind, 99), i64([0, 70, T])
+    room, want = eg.delta_carry(T, 2, keys, H, dk, dv, DEV).numel(), None
+    for shift in (0, 1, 2):
+        carry = torch.full((room + 4,), 7.0, device=DEV)
+        part = carry[shift:shift + room]
+        eg.engram_delta(*args, cu, keys, carry=part)
+        got = eg.engram_delta_grad(dy, *args, part, cu, keys)
+        want = got if want is None else want
+        for u, w in zip(got, want):
+            assert torch.equal(u, w)
+        assert (carry[:shift] == 7).all() and (carry[shift + room:] == 7).all()
+
+
 def test_captured_beside_an_eager_backward_pass():
     """Forward and backward in a graph, replayed on other inputs; results are the same from run to run."""
     T, keys, H, dk, dv, cu = 300, 2, 4, 128, 64, i64([0, 130, 300])
