@@ -45,7 +45,7 @@ struct Args {
   float* parts;  // [2][blocks][dim]: the sums of l silu(gate) y r, for w and scale, and of dx h' r, for w_next
   int64_t rows;
   int32_t dim, groups, width;  // width: of a group
-  int32_t vecs, vecs_log2;     // 16-byte vectors of a row; log2 of a group's if they are a power of two, else -1
+  int32_t vecs, vecs_log2;     // 16-byte vectors of a row; log2 of a group's if they are 1, 2, 4 .. 32, else -1
   float eps;
 };
 
@@ -795,7 +795,7 @@ int opt_in(const void* kernel, std::atomic<uint64_t>& done) {
 }
 
 template <class E>
-bool by_vectors(const Args& a, bool grad) {
+bool by_vectors(const Args& a) {
   auto ok = [](const void* p, int64_t stride) { return p == nullptr || (aligned(p, 16) && stride * E::kBytes % 16 == 0); };
   return a.width % Wide<E>::N == 0 && ok(a.y, a.y_stride) && ok(a.gate, a.gate_stride) && ok(a.h, a.h_stride) &&
          ok(a.dh, a.dh_stride) && ok(a.dx, a.dx_stride) && ok(a.h_out, a.h_out_stride) && ok(a.x_out, a.x_stride) &&
@@ -815,7 +815,7 @@ void set_vecs(Args& a) {
 template <class E>
 int launch_norm(Args a, cudaStream_t st) {
   const unsigned rows = static_cast<unsigned>(a.rows);
-  const bool wide = by_vectors<E>(a, false);
+  const bool wide = by_vectors<E>(a);
   if (!wide && a.dim > kSingles * Single<E>::kMost) {
     norm_any_kernel<E><<<rows, kAnyThreads, 0, st>>>(a);
     return check_launch("norm_any_kernel");
@@ -836,7 +836,7 @@ int launch_norm(Args a, cudaStream_t st) {
 template <class E>
 int launch_grad(Args a, float* dw, float* ds, float* dn, int sms, cudaStream_t st) {
   // two blocks an SM, or one where a block's rows take more than half of the shared memory
-  const bool wide = by_vectors<E>(a, true);
+  const bool wide = by_vectors<E>(a);
   const int at_once = wide && kRing * kArrays * static_cast<int64_t>(a.dim) * E::kBytes > 112 * 1024 ? 1 : 2;
   const int blocks = static_cast<int>(std::min<int64_t>(a.rows, std::min(kParts, at_once * sms)));
   if (blocks > 0) {
