@@ -11,24 +11,17 @@ namespace delta {
 
 // ------------------------------------------------------------------- chunks
 
-// first[s]: how many chunks the sequences before s have.  order[]: the sequences by length,
-// as far as one block sorts them by counting (1024), else as they come.
+// first[s]: how many chunks the sequences before s have.  line[s]: how much of a head's line
+// they take (see Item), and behind the last one the blocks' share of it.
 template <class E>
 __global__ void __launch_bounds__(1024) first_kernel(Args<E> a) {
-  __shared__ int counts[1024];
-  __shared__ int64_t warp_sum[32], before;
+  __shared__ int64_t sums[2][32], before[2];
+  __shared__ int most[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) before = 0;
-  for (int s0 = 0; s0 < a.n_seqs; s0 += 1024) {
-    const int s = s0 + threadIdx.x;
-    int n = 0;
-    if (s < a.n_seqs) {
-      int lo, hi;
-      bounds(a, s, lo, hi);
-      n = (hi - lo + kC - 1) / kC;
-    }
-    if (a.n_seqs <= 1024) counts[threadIdx.x] = n;
-    else if (s < a.n_seqs) a.order[s] = s;
+  if (threadIdx.x < 2) before[threadIdx.x] = 0;
+  for (int k = threadIdx.x; k < a.blocks; k += 1024) a.given[k] = 0;
+  // the sum over the block's threads before this one and over what came before, and on to the next 1024
+  auto sum_before = [&](int64_t n, int which) {
     int64_t sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -36,22 +29,45 @@ __global__ void __launch_bounds__(1024) first_kernel(Args<E> a) {
       if (lane >= o) sum += x;
     }
     __syncthreads();
-    if (lane == 31) warp_sum[warp] = sum;
+    if (lane == 31) sums[which][warp] = sum;
     __syncthreads();
-    int64_t at = before + sum - n;
-    for (int w = 0; w < warp; ++w) at += warp_sum[w];
+    int64_t at = before[which] + sum - n;
+    for (int w = 0; w < warp; ++w) at += sums[which][w];
+    __syncthreads();
+    if (threadIdx.x == 1023) before[which] = at + n;
+    return at;
+  };
+  int longest = 1;
+  for (int s0 = 0; s0 < a.n_seqs; s0 += 1024) {
+    const int s = s0 + threadIdx.x;
+    int n = 0, cost = 0;
+    if (s < a.n_seqs) {
+      int lo, hi;
+      bounds(a, s, lo, hi);
+      n = (hi - lo + kC - 1) / kC;
+    }
     // (sequences that lie over one another could give more chunks than there is room for)
-    if (s < a.n_seqs) a.first[s] = static_cast<int>(at < a.max_chunks ? at : a.max_chunks);
-    __syncthreads();
-    if (threadIdx.x == 1023) before = at + n;
+    const int64_t all = sum_before(n, 0);
+    const int at = static_cast<int>(all < a.max_chunks ? all : a.max_chunks);
+    if (s < a.n_seqs) {
+      int64_t slot;
+      cost = live_slot(a, s, slot) ? min(n, a.max_chunks - at) + 1 : 1;
+      longest = max(longest, cost);
+      a.first[s] = at;
+    }
+    const int64_t line = sum_before(cost, 1);
+    if (s < a.n_seqs) a.line[s] = line;
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+  if (lane == 0) most[warp] = longest;
   __syncthreads();
-  if (threadIdx.x == 0) a.first[a.n_seqs] = static_cast<int>(before < a.max_chunks ? before : a.max_chunks);
-  const int s = threadIdx.x;
-  if (a.n_seqs > 1024 || s >= a.n_seqs) return;
-  int rank = 0;
-  for (int o = 0; o < a.n_seqs; ++o) rank += counts[o] > counts[s] || (counts[o] == counts[s] && o < s);
-  a.order[rank] = s;
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < 32; ++w) longest = max(longest, most[w]);
+  a.first[a.n_seqs] = static_cast<int>(before[0] < a.max_chunks ? before[0] : a.max_chunks);
+  const int64_t share = (before[1] * a.heads * a.slices + a.blocks - 1) / a.blocks;
+  a.line[a.n_seqs] = before[1];
+  a.line[a.n_seqs + 1] = share > longest ? share : longest;
 }
 
 // ---------------------------------------------------------------- M, P, gates
@@ -297,16 +313,18 @@ template int launch_prepare<train::F32>(const Args<train::F32>&, cudaStream_t);
 // P U in two.  bf16: the next chunk's inputs are copied meanwhile; fp32's terms are made
 // on the way to shared memory and take the room.
 //
-// Four quads a block (16,384 positions in 4 sequences, 40 heads of 128, bf16: about 1000 us): the
-// tensor cores are busy for 41 % of the time and shared memory for 70; what is left are
-// waits of warps that have nothing else to do between the barriers.  One quad (16,381
+// Four quads a block (16,384 positions in 4 sequences, 40 heads of 128, bf16: 768 us where no
+// sequence is longer than a block's share, 5.6 a chunk): the tensor cores are busy for 42 %
+// of the time and shared memory for 76; what is left are waits of warps that have nothing
+// else to do between a quad's barriers.  One quad (16,381
 // positions, 10 heads: 520 us, 2.0 a chunk): instructions that follow one another.  A form
 // with 16 columns and the whole of their state a warp, without anything handed on, read a
 // third of the shared memory and took as long: two warps on each part of an SM are all
 // that its registers allow.
 template <class E, int KD, int NQ>
 struct Scan {
-  static constexpr int kT = kAlone<NQ> ? kCopiers : NQ * 128, kThreads = kAlone<NQ> ? 256 + kCopiers : kT, kStages = E::kBytes == 2 ? 2 : 1, kB = kC / 16;
+  static constexpr int kT = kAlone<NQ> ? kCopiers : NQ * 128, kThreads = kAlone<NQ> ? 256 + kCopiers : kT;
+  static constexpr int kStages = E::kBytes == 2 ? 2 : 1, kB = kC / 16;
   static constexpr int kK = 0, kQ = kK + kIn<E> * mat_bytes(kC, KD), kV = kQ + kIn<E> * mat_bytes(kC, KD);
   static constexpr int kM = kV + kIn<E> * mat_bytes(kC, 16 * NQ), kP = kM + kStateTerms * kTerm, kG = kP + kOut<E> * kTerm;
   static constexpr int kStage = kG + static_cast<int>(sizeof(Gates)), kQuads = kStages * kStage;
@@ -322,273 +340,303 @@ __global__ void __launch_bounds__(Scan<E, KD, NQ>::kThreads, 1) scan_kernel(Args
   using L = Scan<E, KD, NQ>;
   constexpr int kT = L::kT, kI = kIn<E>, kO = kOut<E>, kS = kStateTerms, kB = L::kB, kR = KD / 64;  // kR: a warp's blocks of S^T
   extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ Stages stages;
+  __shared__ Item item;
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t2 = (lane & 3) * 2;
   const int quad = kAlone<NQ> ? 0 : tid >> 7, w = ((tid >> 5) + quad) & 3;  // w: the warp's quarter
-  int seq, h, v0;
-  place_of(a, 16 * NQ, seq, h, v0);
-  const int cols = min(a.dv - v0, 16 * NQ);
-  const int hk = h / (a.heads / a.keys), vw = v0 + quad * 16;
-  int lo, hi;
-  bounds(a, seq, lo, hi);
-  const int c0 = a.first[seq], n = min((hi - lo + kC - 1) / kC, a.max_chunks - c0);
   const size_t matrix = static_cast<size_t>(a.dk) * a.dv, saved = saved_floats<E>(a.dk, a.dv);
-  int64_t slot;
-  if (!live_slot(a, seq, slot)) {
-    if (tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
-    padding_zeros(a, lo, hi, c0, n, h, v0, cols, blockDim.x);
-    return;
+  if (tid == 0) {
+    item.seq = -1;
+    item.give = false;
   }
-  const uint32_t own = base + L::kQuads + quad * L::kQuad;
-  float S[2 * kR][4];
-  auto each = [&](auto f) {  // f(tile, place, the element's place in a state)
-#pragma unroll
-    for (int t = 0; t < 2 * kR; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int v = vw + g + (j >> 1) * 8, k = w * kR * 16 + t * 8 + t2 + (j & 1);
-        if (v < a.dv && k < a.dk) f(t, j, static_cast<size_t>(k) * a.dv + v);
-      }
-  };
-  clear(S);
-  if (a.state != nullptr) {
-    const float* from = a.state + (slot * a.heads + h) * matrix;
-    each([&](int t, int j, size_t at) { S[t][j] = from[at]; });
-  }
-  auto hand_state = [&](int i) {  // the state in front of chunk i
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      const int kb = w * kR + r;
-      uint32_t f[kS][4];
-      as_operand<kS>(f, S[2 * r], S[2 * r + 1]);
-      hand<kS>(own + kb * (kS * 512), f);
-      if (a.carry == nullptr || vw >= a.dv || kb * 16 >= a.dk) continue;
-      float* to = a.carry + unit_of(a, c0 + i, h) * saved;
-      if constexpr (E::kBytes == 2) save_block(block_of(to, a.dk, vw >> 4, kb), f);
-      else save_rows(to, a.dk, a.dv, vw, kb * 16, S[2 * r], S[2 * r + 1]);
+  if (!kAlone<NQ>) stages_begin(stages, kT, kT / 32);
+  for (int used = 0;;) {  // (used: how often the stages have been)
+    __syncthreads();
+    if (tid == 0) next_item(a, item, 16 * NQ);
+    __syncthreads();
+    if (!item.any) break;
+    const int h = uniform(item.h), v0 = uniform(item.v0), lo = uniform(item.lo), hi = uniform(item.hi), c0 = uniform(item.c0),
+              from = uniform(item.from), n = uniform(item.to);
+    const int cols = min(a.dv - v0, 16 * NQ);
+    const int hk = h / (a.heads / a.keys), vw = v0 + quad * 16;
+    int64_t slot;
+    if (!live_slot(a, item.seq, slot)) {
+      if (tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
+      padding_zeros(a, lo, hi, c0, item.n, h, v0, cols, blockDim.x);
+      continue;
     }
-  };
-  const int copier = tid - (kAlone<NQ> ? 256 : 0);  // a copying thread's number
-  auto load = [&](int i) {
-    const uint32_t stage = base + (i % L::kStages) * L::kStage;
-    const int64_t p = lo + static_cast<int64_t>(i) * kC;
-    const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
-    const uint8_t* mask = a.mask != nullptr ? a.mask + p : nullptr;
-    const size_t unit = unit_of(a, c0 + i, h);
-    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kK), a.k + p * a.k_stride + hk * a.dk, a.k_stride, len, a.dk, mask, a.vec, copier);
-    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kQ), a.q + p * a.q_stride + hk * a.dk, a.q_stride, len, a.dk, mask, a.vec, copier);
-    load_rows<E, 16 * NQ, kT>(mat<kC, 16 * NQ>(stage + L::kV), a.v + p * a.v_stride + static_cast<int64_t>(h) * a.dv + v0,
-                              a.v_stride, len, cols, mask, a.vec, copier);
-    load_tri<kO, kT>(stage + L::kM, stage + L::kP, a.tri + unit * kTriBytes, copier);
-    load_gates<kT>(stage + L::kG, a.gates + unit, copier);
-    copies_begun();
-  };
-  // Y^T of the warp's positions: first what Q reads of the state, then of the chunk's writes
-  using Out = Sums<2, kO == 3>;
-  auto scaled = [&](Out& y, const Gates& gt) {
+    const uint32_t own = base + L::kQuads + quad * L::kQuad;
+    float S[2 * kR][4];
+    auto each = [&](auto f) {  // f(tile, place, the element's place in a state)
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const float2 into = *reinterpret_cast<const float2*>(&gt.into[w * 16 + t * 8 + t2]);
+      for (int t = 0; t < 2 * kR; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y.main[t][j] = y.sum(t, j) * (a.scale * (j & 1 ? into.y : into.x));
-    }
-    if constexpr (kO == 3) clear(y.small);
-  };
-  auto finish = [&](Out& y, const Gates& gt, uint32_t stage, int i) {
-    for (int ib = 0; ib <= w; ++ib) {
-      uint32_t fa[kO][4];
-      take<kO>(own + L::kU + ib * (kO * 512), fa);
-#pragma unroll
-      for (int j = 0; j < kO; ++j) {
-        uint32_t fb[2][2];
-        TriAcross{stage + L::kP}.get(fb, ib, w, j);
-        terms<kO, kO>(y, fa, fb, j);
-      }
-    }
-    float out[2][4];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) out[t][j] = y.sum(t, j);
-    const int64_t p = lo + static_cast<int64_t>(i) * kC;
-    store_rows<E>(a.y + p * a.y_stride + static_cast<int64_t>(h) * a.dv, a.y_stride, w * 16,
-                  hi - p < kC ? static_cast<int>(hi - p) : kC, vw, a.dv, a.pairs, gt.beta, out);
-  };
-  if (kAlone<NQ> && copier >= 0) {
-    if (n > 0) load(0);
-    for (int i = 0; i < n; ++i) {
-      copies_done();
-      __syncthreads();
-      if (L::kStages == 1 && i + 1 < n) __syncthreads();
-      if (i + 1 < n) load(i + 1);
-    }
-    return;
-  }
-  if (kAlone<NQ> && tid >= 128) {  // the quad's Y
-    for (int i = 0; i < n; ++i) {
-      const uint32_t stage = base + (i % L::kStages) * L::kStage;
-      const Mat Q = mat<kC, KD>(stage + L::kQ);
-      const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
-      __syncthreads();
-      Out y;
-      y.clear_all();
-#pragma unroll 4
-      for (int kb = 0; kb < KD / 16; ++kb) {
-        uint32_t fa[kO][4];
-        take<kO>(own + kb * (kS * 512), fa);
-#pragma unroll
-        for (int j = 0; j < kI; ++j) {
-          uint32_t fb[2][2];
-          Across{Q}.get<2>(fb, kb * 16, w * 16, j);
-          terms<kO, kO>(y, fa, fb, j);
+        for (int j = 0; j < 4; ++j) {
+          const int v = vw + g + (j >> 1) * 8, k = w * kR * 16 + t * 8 + t2 + (j & 1);
+          if (v < a.dv && k < a.dk) f(t, j, static_cast<size_t>(k) * a.dv + v);
         }
+    };
+    const int share = gridDim.x - 1 - blockIdx.x;
+    auto stage_of = [&](int i) { return kAlone<NQ> ? i % L::kStages : (used + i - from) & 1; };
+    auto hand_state = [&](int i) {  // the state in front of chunk i
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        const int kb = w * kR + r;
+        uint32_t f[kS][4];
+        as_operand<kS>(f, S[2 * r], S[2 * r + 1]);
+        hand<kS>(own + kb * (kS * 512), f);
+        if (a.carry == nullptr || vw >= a.dv || kb * 16 >= a.dk) continue;
+        float* to = a.carry + unit_of(a, c0 + i, h) * saved;
+        if constexpr (E::kBytes == 2) save_block(block_of(to, a.dk, vw >> 4, kb), f);
+        else save_rows(to, a.dk, a.dv, vw, kb * 16, S[2 * r], S[2 * r + 1]);
       }
-      asm volatile("bar.arrive 6, 256;" ::: "memory");  // S^T is no longer needed here
-      scaled(y, gt);
-      asm volatile("bar.sync 5, 256;" ::: "memory");  // U^T is here
-      finish(y, gt, stage, i);
-      if (L::kStages == 1 && i + 1 < n) __syncthreads();
-    }
-    return;
-  }
-  if (n > 0) {
-    hand_state(0);
-    if (!kAlone<NQ>) load(0);
-  }
-  for (int i = 0; i < n; ++i) {
-    const uint32_t stage = base + (i % L::kStages) * L::kStage;
-    const Mat K = mat<kC, KD>(stage + L::kK), Q = mat<kC, KD>(stage + L::kQ), V = mat<kC, 16 * NQ>(stage + L::kV);
-    const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
-    copies_done();
-    __syncthreads();  // the chunk and the states are here, and the other stage is free
-    if (!kAlone<NQ> && L::kStages == 2 && i + 1 < n) load(i + 1);
-    // ---- (K S)^T and (Q S)^T
-    Sums<2, true> x;
-    Out y;
-    x.clear_all();
-    if (!kAlone<NQ>) y.clear_all();
-#pragma unroll 4
-    for (int kb = 0; kb < KD / 16; ++kb) {
-      uint32_t fa[kS][4];
-      take<kS>(own + kb * (kS * 512), fa);
-#pragma unroll
-      for (int j = 0; j < kI; ++j) {
-        uint32_t fk[2][2], fq[2][2];
-        Across{K}.get<2>(fk, kb * 16, w * 16, j);
-        if (!kAlone<NQ>) Across{Q}.get<2>(fq, kb * 16, w * 16, j);
-#pragma unroll
-        for (int e = 0; e < kS; ++e) {
-          if (e + j < kS) x.add(e, j, fa[e], fk);
-          if (!kAlone<NQ> && e + j < kO) y.add(e, j, fa[e], fq);
-        }
+    };
+    const int copier = tid - (kAlone<NQ> ? 256 : 0);  // a copying thread's number
+    auto load = [&](int i) {
+      const uint32_t stage = base + stage_of(i) * L::kStage;
+      const int64_t p = lo + static_cast<int64_t>(i) * kC;
+      const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
+      const uint8_t* mask = a.mask != nullptr ? a.mask + p : nullptr;
+      const size_t unit = unit_of(a, c0 + i, h);
+      load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kK), a.k + p * a.k_stride + hk * a.dk, a.k_stride, len, a.dk, mask, a.vec, copier);
+      load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kQ), a.q + p * a.q_stride + hk * a.dk, a.q_stride, len, a.dk, mask, a.vec, copier);
+      load_rows<E, 16 * NQ, kT>(mat<kC, 16 * NQ>(stage + L::kV), a.v + p * a.v_stride + static_cast<int64_t>(h) * a.dv + v0,
+                                a.v_stride, len, cols, mask, a.vec, copier);
+      if constexpr (kAlone<NQ>) {
+        load_tri<kO, kT>(stage + L::kM, stage + L::kP, a.tri + unit * kTriBytes, copier);
+        load_gates<kT>(stage + L::kG, a.gates + unit, copier);
+        copies_begun();
+      } else {
+        stage_copies(stages, stage_of(i), stage + L::kM, a.tri + unit * kTriBytes, (kS + kO) * kTerm, stage + L::kG, a.gates + unit,
+                     a.vec);
       }
-    }
-    // ---- X^T, of the warp's positions: rows w * 16 + t2 (+ 1, + 8), columns vw + g (+ 8)
-    {
-      float c[2][4];
-      clear(c);
-#pragma unroll
-      for (int j = kI - 1; j >= 0; --j) {
-        uint32_t f[4];
-        Cols{V}(f, quad * 16, w * 16, j);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          c[q >> 1][(q & 1) * 2] += lo_of(f[q]);
-          c[q >> 1][(q & 1) * 2 + 1] += hi_of(f[q]);
-        }
-      }
+    };
+    if (!kAlone<NQ> && n > from) load(from);
+    // Y^T of the warp's positions: first what Q reads of the state, then of the chunk's writes
+    using Out = Sums<2, kO == 3>;
+    auto scaled = [&](Out& y, const Gates& gt) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const float2 into = *reinterpret_cast<const float2*>(&gt.into[w * 16 + t * 8 + t2]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[t][j] = fmaf(-(j & 1 ? into.y : into.x), x.sum(t, j), c[t][j]);
+        for (int j = 0; j < 4; ++j) y.main[t][j] = y.sum(t, j) * (a.scale * (j & 1 ? into.y : into.x));
       }
-      if (!kAlone<NQ>) scaled(y, gt);
-      uint32_t f[kS][4];
-      as_operand<kS>(f, c[0], c[1]);
-      hand<kS>(own + L::kX + w * (kS * 512), f);
-    }
-    quad_sync(quad);
-    // ---- U^T
-    x.clear_all();
-    for (int ib = 0; ib <= w; ++ib) {
-      uint32_t fa[kS][4];
-      take<kS>(own + L::kX + ib * (kS * 512), fa);
+      if constexpr (kO == 3) clear(y.small);
+    };
+    auto finish = [&](Out& y, const Gates& gt, uint32_t stage, int i) {
+      for (int ib = 0; ib <= w; ++ib) {
+        uint32_t fa[kO][4];
+        take<kO>(own + L::kU + ib * (kO * 512), fa);
 #pragma unroll
-      for (int j = 0; j < kS; ++j) {
-        uint32_t fb[2][2];
-        TriAcross{stage + L::kM}.get(fb, ib, w, j);
-        terms<kS, kS>(x, fa, fb, j);
+        for (int j = 0; j < kO; ++j) {
+          uint32_t fb[2][2];
+          TriAcross{stage + L::kP}.get(fb, ib, w, j);
+          terms<kO, kO>(y, fa, fb, j);
+        }
       }
-    }
-    {
-      float u[2][4];
+      float out[2][4];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[t][j] = x.sum(t, j);
-      uint32_t f[kO][4], fl[kS][4];
-      as_operand<kO>(f, u[0], u[1]);
-      hand<kO>(own + L::kU + w * (kO * 512), f);
-      if (kAlone<NQ>) asm volatile("bar.arrive 5, 256;" ::: "memory");
-      if (a.carry != nullptr) {  // for the backward pass
-        const int64_t p = lo + static_cast<int64_t>(i) * kC, wide = static_cast<int64_t>(a.heads) * a.dv;
-        auto* to = kept_writes<E>(a) + p * wide + static_cast<int64_t>(h) * a.dv;
-        const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
-        store_rows<E>(to, wide, w * 16, len, vw, a.dv, a.dv % 2 == 0, gt.beta, u);
-        if constexpr (E::kBytes == 2) {
-          float rest[2][4];
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) rest[t][j] = u[t][j] - lo_of(pack(u[t][j], 0.f));
-          store_rows<E>(to + a.n_tokens * wide, wide, w * 16, len, vw, a.dv, a.dv % 2 == 0, gt.beta, rest);
-        }
+        for (int j = 0; j < 4; ++j) out[t][j] = y.sum(t, j);
+      const int64_t p = lo + static_cast<int64_t>(i) * kC;
+      store_rows<E>(a.y + p * a.y_stride + static_cast<int64_t>(h) * a.dv, a.y_stride, w * 16,
+                    hi - p < kC ? static_cast<int>(hi - p) : kC, vw, a.dv, a.pairs, gt.beta, out);
+    };
+    if (kAlone<NQ> && copier >= 0) {
+      if (n > from) load(from);
+      for (int i = from; i < n; ++i) {
+        copies_done();
+        __syncthreads();
+        if (L::kStages == 1 && i + 1 < n) __syncthreads();
+        if (i + 1 < n) load(i + 1);
       }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float2 last = *reinterpret_cast<const float2*>(&gt.last[w * 16 + t * 8 + t2]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) u[t][j] *= j & 1 ? last.y : last.x;
-      }
-      as_operand<kS>(fl, u[0], u[1]);
-      if (!kAlone<NQ>) quad_sync(quad);  // X^T is no longer needed
-      hand<kS>(own + L::kL + w * (kS * 512), fl);
+      continue;
     }
-    quad_sync(quad);
-    // ---- S^T
-    {
-      const float total = gt.into[kC - 1];
-      Sums<2 * kR, true> d;
-      d.clear_all();
+    if (kAlone<NQ> && tid >= 128) {  // the quad's Y
+      for (int i = from; i < n; ++i) {
+        const uint32_t stage = base + (i % L::kStages) * L::kStage;
+        const Mat Q = mat<kC, KD>(stage + L::kQ);
+        const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
+        __syncthreads();
+        Out y;
+        y.clear_all();
+#pragma unroll 4
+        for (int kb = 0; kb < KD / 16; ++kb) {
+          uint32_t fa[kO][4];
+          take<kO>(own + kb * (kS * 512), fa);
 #pragma unroll
-      for (int cb = 0; cb < kB; ++cb) {
+          for (int j = 0; j < kI; ++j) {
+            uint32_t fb[2][2];
+            Across{Q}.get<2>(fb, kb * 16, w * 16, j);
+            terms<kO, kO>(y, fa, fb, j);
+          }
+        }
+        asm volatile("bar.arrive 6, 256;" ::: "memory");  // S^T is no longer needed here
+        scaled(y, gt);
+        asm volatile("bar.sync 5, 256;" ::: "memory");  // U^T is here
+        finish(y, gt, stage, i);
+        if (L::kStages == 1 && i + 1 < n) __syncthreads();
+      }
+      continue;
+    }
+    clear(S);
+    if (item.take) {
+      take_state(a.between + static_cast<size_t>(share + 1) * kHandedOn, S, NQ * 128);
+    } else if (a.state != nullptr) {
+      const float* given = a.state + (slot * a.heads + h) * matrix;
+      each([&](int t, int j, size_t at) { S[t][j] = given[at]; });
+    }
+    if (n > from) hand_state(from);
+    for (int i = from; i < n; ++i) {
+      const uint32_t stage = base + stage_of(i) * L::kStage;
+      const Mat K = mat<kC, KD>(stage + L::kK), Q = mat<kC, KD>(stage + L::kQ), V = mat<kC, 16 * NQ>(stage + L::kV);
+      const Gates& gt = *reinterpret_cast<const Gates*>(smem + stage_of(i) * L::kStage + L::kG);
+      if constexpr (kAlone<NQ>) {
+        __syncthreads();  // the chunk and the states are here, and the other stage is free
+      } else {
+        quad_sync(quad);  // the states are here
+        stage_wait(stages, stages.here[stage_of(i)], (used + i - from) >> 1, a.status);
+      }
+      // ---- (K S)^T and (Q S)^T
+      Sums<2, true> x;
+      Out y;
+      x.clear_all();
+      if (!kAlone<NQ>) y.clear_all();
+#pragma unroll 4
+      for (int kb = 0; kb < KD / 16; ++kb) {
         uint32_t fa[kS][4];
-        take<kS>(own + L::kL + cb * (kS * 512), fa);
+        take<kS>(own + kb * (kS * 512), fa);
 #pragma unroll
         for (int j = 0; j < kI; ++j) {
-          uint32_t fb[2 * kR][2];
-          Down{K}.get<2 * kR>(fb, cb * 16, w * kR * 16, j);
-          terms<kS, kS>(d, fa, fb, j);
+          uint32_t fk[2][2], fq[2][2];
+          Across{K}.get<2>(fk, kb * 16, w * 16, j);
+          if (!kAlone<NQ>) Across{Q}.get<2>(fq, kb * 16, w * 16, j);
+#pragma unroll
+          for (int e = 0; e < kS; ++e) {
+            if (e + j < kS) x.add(e, j, fa[e], fk);
+            if (!kAlone<NQ> && e + j < kO) y.add(e, j, fa[e], fq);
+          }
         }
       }
+      // ---- X^T, of the warp's positions: rows w * 16 + t2 (+ 1, + 8), columns vw + g (+ 8)
+      {
+        float c[2][4];
+        clear(c);
 #pragma unroll
-      for (int t = 0; t < 2 * kR; ++t)
+        for (int j = kI - 1; j >= 0; --j) {
+          uint32_t f[4];
+          Cols{V}(f, quad * 16, w * 16, j);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) S[t][j] = fmaf(S[t][j], total, d.sum(t, j));
+          for (int q = 0; q < 4; ++q) {
+            c[q >> 1][(q & 1) * 2] += lo_of(f[q]);
+            c[q >> 1][(q & 1) * 2 + 1] += hi_of(f[q]);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float2 into = *reinterpret_cast<const float2*>(&gt.into[w * 16 + t * 8 + t2]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) c[t][j] = fmaf(-(j & 1 ? into.y : into.x), x.sum(t, j), c[t][j]);
+        }
+        if (!kAlone<NQ>) scaled(y, gt);
+        uint32_t f[kS][4];
+        as_operand<kS>(f, c[0], c[1]);
+        hand<kS>(own + L::kX + w * (kS * 512), f);
+      }
+      quad_sync(quad);
+      // ---- U^T
+      x.clear_all();
+      for (int ib = 0; ib <= w; ++ib) {
+        uint32_t fa[kS][4];
+        take<kS>(own + L::kX + ib * (kS * 512), fa);
+#pragma unroll
+        for (int j = 0; j < kS; ++j) {
+          uint32_t fb[2][2];
+          TriAcross{stage + L::kM}.get(fb, ib, w, j);
+          terms<kS, kS>(x, fa, fb, j);
+        }
+      }
+      {
+        float u[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u[t][j] = x.sum(t, j);
+        uint32_t f[kO][4], fl[kS][4];
+        as_operand<kO>(f, u[0], u[1]);
+        hand<kO>(own + L::kU + w * (kO * 512), f);
+        if (kAlone<NQ>) asm volatile("bar.arrive 5, 256;" ::: "memory");
+        if (a.carry != nullptr) {  // for the backward pass
+          const int64_t p = lo + static_cast<int64_t>(i) * kC, wide = static_cast<int64_t>(a.heads) * a.dv;
+          auto* to = kept_writes<E>(a) + p * wide + static_cast<int64_t>(h) * a.dv;
+          const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
+          store_rows<E>(to, wide, w * 16, len, vw, a.dv, a.dv % 2 == 0, gt.beta, u);
+          if constexpr (E::kBytes == 2) {
+            float rest[2][4];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) rest[t][j] = u[t][j] - lo_of(pack(u[t][j], 0.f));
+            store_rows<E>(to + a.n_tokens * wide, wide, w * 16, len, vw, a.dv, a.dv % 2 == 0, gt.beta, rest);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float2 last = *reinterpret_cast<const float2*>(&gt.last[w * 16 + t * 8 + t2]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u[t][j] *= j & 1 ? last.y : last.x;
+        }
+        as_operand<kS>(fl, u[0], u[1]);
+        if (!kAlone<NQ>) quad_sync(quad);  // X^T is no longer needed
+        hand<kS>(own + L::kL + w * (kS * 512), fl);
+      }
+      if (!kAlone<NQ> && i + 1 < n) {
+        if (i > from) stage_wait(stages, stages.done[stage_of(i + 1)], (used + i - 1 - from) >> 1, a.status);
+        load(i + 1);
+      }
+      quad_sync(quad);
+      // ---- S^T
+      {
+        const float total = gt.into[kC - 1];
+        Sums<2 * kR, true> d;
+        d.clear_all();
+#pragma unroll
+        for (int cb = 0; cb < kB; ++cb) {
+          uint32_t fa[kS][4];
+          take<kS>(own + L::kL + cb * (kS * 512), fa);
+#pragma unroll
+          for (int j = 0; j < kI; ++j) {
+            uint32_t fb[2 * kR][2];
+            Down{K}.get<2 * kR>(fb, cb * 16, w * kR * 16, j);
+            terms<kS, kS>(d, fa, fb, j);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 2 * kR; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) S[t][j] = fmaf(S[t][j], total, d.sum(t, j));
+      }
+      if (kAlone<NQ>) asm volatile("bar.sync 6, 256;" ::: "memory");  // Q has read S^T
+      if (i + 1 < n) hand_state(i + 1);
+      if constexpr (kAlone<NQ>) {
+        if (L::kStages == 1 && i + 1 < n) __syncthreads();  // the stage is free
+      } else {
+        finish(y, gt, stage, i);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&stages.done[stage_of(i)]));
+      }
     }
-    if (kAlone<NQ>) asm volatile("bar.sync 6, 256;" ::: "memory");  // Q has read S^T
-    if (i + 1 < n) hand_state(i + 1);
-    if (!kAlone<NQ>) finish(y, gt, stage, i);
-    if (L::kStages == 1 && i + 1 < n) {
-      __syncthreads();  // the stage is free
-      if (!kAlone<NQ>) load(i + 1);
+    used += n - from;
+    if (item.give) {
+      give_state(a.between + static_cast<size_t>(share) * kHandedOn, S, NQ * 128);
+    } else if (a.state_out != nullptr) {
+      float* to = a.state_out + (slot * a.heads + h) * matrix;
+      each([&](int t, int j, size_t at) { to[at] = S[t][j]; });
     }
   }
-  if (a.state_out != nullptr) {
-    float* to = a.state_out + (slot * a.heads + h) * matrix;
-    each([&](int t, int j, size_t at) { to[at] = S[t][j]; });
-  }
+  if (!kAlone<NQ>) stages_end(stages);
 }
 
 template <class E>
@@ -596,9 +644,7 @@ int launch_scan(const Args<E>& a, int sms, cudaStream_t st) {
   auto go = [&](auto kernel, int smem, int nq, std::atomic<uint64_t>& flag) {
     int r = opt_in(reinterpret_cast<const void*>(kernel), smem, flag);
     if (r) return r;
-    const int64_t blocks = static_cast<int64_t>(a.n_seqs) * a.heads * ((a.dv + 16 * nq - 1) / (16 * nq));
-    if (blocks > 0x7fffffff) return fail(ENGRAM_E_RANGE, "too many sequences times heads");
-    kernel<<<static_cast<unsigned>(blocks), nq == 1 ? 256 + kCopiers : nq * 128, smem, st>>>(a);
+    kernel<<<a.blocks, nq == 1 ? 256 + kCopiers : nq * 128, smem, st>>>(a);
     return check_launch("scan_kernel");
   };
   static std::atomic<uint64_t> done[4] = {{0}, {0}, {0}, {0}};
@@ -609,7 +655,7 @@ int launch_scan(const Args<E>& a, int sms, cudaStream_t st) {
   return a.dk <= 64 ? go(scan_kernel<E, 64, 1>, Scan<E, 64, 1>::kSmem, 1, done[2])
                     : go(scan_kernel<E, 128, 1>, Scan<E, 128, 1>::kSmem, 1, done[3]);
 }
-static_assert(Scan<train::Bf16, 128, 4>::kSmem <= 232448 && Scan<train::F32, 128, 1>::kSmem <= 232448, "a block's shared memory");
+static_assert(Scan<train::Bf16, 128, 4>::kSmem + sizeof(Stages) + sizeof(Item) <= 232448 && Scan<train::F32, 128, 1>::kSmem <= 232448, "a block's shared memory");
 
 // --------------------------------------------------------------------- step
 
@@ -732,7 +778,10 @@ Space space(void* base, int64_t n_tokens, int64_t n_seqs, int32_t keys, int32_t 
     return p;
   };
   s.first = reinterpret_cast<int32_t*>(take(sizeof(int32_t) * (n_seqs + 1)));
-  s.order = reinterpret_cast<int32_t*>(take(sizeof(int32_t) * n_seqs));
+  s.line = reinterpret_cast<int64_t*>(take(sizeof(int64_t) * (n_seqs + 2)));
+  const int64_t blocks = std::min<int64_t>(kMaxBlocks, n_seqs * heads * slices_of(dv, 1));
+  s.given = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * blocks));
+  s.between = reinterpret_cast<float*>(take(sizeof(float) * kHandedOn * blocks));
   s.tri = take(units * kTriBytes);
   s.gates = reinterpret_cast<Gates*>(take(units * sizeof(Gates)));
   if (backward) {
@@ -740,7 +789,8 @@ Space space(void* base, int64_t n_tokens, int64_t n_seqs, int32_t keys, int32_t 
     s.writes = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(n_tokens) * heads * dv * sizeof(uint16_t)));
     // (a block's threads leave a chunk's sums, 64 x 128 of queries and of keys, as they hold them)
     if (heads > keys)
-      s.shared = reinterpret_cast<float*>(take(static_cast<size_t>(max_chunks(n_tokens, n_seqs)) * keys * 2 * kC * (dk <= 64 ? 64 : 128) * sizeof(float)));
+      s.shared = reinterpret_cast<float*>(
+          take(static_cast<size_t>(max_chunks(n_tokens, n_seqs)) * keys * 2 * kC * (dk <= 64 ? 64 : 128) * sizeof(float)));
   }
   s.bytes = at;
   return s;
@@ -833,7 +883,10 @@ extern "C" int engram_delta(const void* q_d, int64_t q_stride, const void* k_d, 
     a.status = status_d;
     const Space s = space(workspace_d, n_tokens, n_seqs, key_heads, heads, dk, dv, false);
     a.first = s.first;
-    a.order = s.order;
+    a.line = s.line;
+    a.given = s.given;
+    a.between = s.between;
+    set_blocks(a, sms);
     a.tri = s.tri;
     a.gates = s.gates;
     int r = launch_prepare<E>(a, as_stream(stream));

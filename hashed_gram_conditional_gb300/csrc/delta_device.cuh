@@ -80,7 +80,10 @@ struct Args {
   bool has_state;  // slots are checked against n_slots
   // workspace
   int32_t* first;  // [n_seqs + 1] number of a sequence's first chunk
-  int32_t* order;  // [n_seqs] the sequences, long ones first
+  int64_t* line;   // [n_seqs + 2] what the sequences before s take of a head's line; the blocks' share (see Item)
+  uint32_t* given;  // [blocks] whether a block's first state has been handed on
+  float* between;   // the states that are handed on, kHandedOn floats a block
+  int32_t blocks, slices;  // of the kernels that follow the sequences; slices of a head's value columns
   unsigned char* tri;
   Gates* gates;
   // backward: states' gradients behind the chunks, as `carry` has the states in front of them; the second terms of
@@ -433,14 +436,115 @@ __device__ __forceinline__ void load_gates(uint32_t to, const Gates* from, int t
     copy16(to + i * 16, reinterpret_cast<const unsigned char*>(from) + i * 16, true);
 }
 
-// A block's sequence, head and first value column, of a grid of one dimension with the
-// longest sequences first: a block that follows a long one is not begun last.
+// The kernels that follow the sequences have a block on each SM.  What there is to do, a
+// sequence in a slice of a head's columns after the other, lies on a line, a sequence's
+// chunks and one more for its state; each block has an equal share of it, T, or as much as
+// the longest sequence takes.  Where the end of a share cuts a sequence, the next block
+// takes its first chunks, as the first thing that it does, and hands the state on; this block
+// takes the others as its last.  The two do not overlap as no sequence is longer than T.
+// Shares are given from the line's end on, so that a block waits only for one that was
+// launched before it, and what it waits for waits for nothing.  (16,384 positions of 40
+// heads in four sequences of 114, 91, 50 and 3 chunks, forwards: 1049 us with a block for
+// each sequence and slice, longest first, 768 this way; where the longest sequence alone
+// takes as long, 201 of 259 chunks, 1121 and 1116.)
+constexpr int kMaxBlocks = 256, kHandedOn = 512 * 16;
+struct Item {
+  int64_t at, end;        // on the line, and the share's end
+  int64_t begin, behind;  // the sequence's part of the line, and what it takes in each slice
+  int cost;
+  int seq, h, v0;
+  int lo, hi, c0, n;      // positions, chunks
+  int from, to;           // the chunks that are done here, in the order of the kernel
+  bool any, take, give;
+};
+// The same value in every lane, known as such: what is worked out from it is worked out once a warp.
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
 template <class E>
-__device__ __forceinline__ void place_of(const Args<E>& a, int across, int& seq, int& h, int& v0) {
-  const int slices = (a.dv + across - 1) / across, per = slices * a.heads, i = blockIdx.x;
-  seq = a.order[i / per];
-  h = i % per / slices;
-  v0 = i % slices * across;
+__device__ __forceinline__ int chunks_of(const Args<E>& a, int s, int& lo, int& hi) {
+  bounds(a, s, lo, hi);
+  return min((hi - lo + kC - 1) / kC, a.max_chunks - a.first[s]);
+}
+// The block's next item, by one thread; the first one if `it.seq` is negative.
+template <class E>
+__device__ __forceinline__ void next_item(const Args<E>& a, Item& it, int across) {
+  const int64_t per = static_cast<int64_t>(a.heads) * a.slices, share = gridDim.x - 1 - blockIdx.x;
+  auto enter = [&](int s) {
+    it.seq = s;
+    it.begin = a.line[s] * per;
+    it.behind = a.line[s + 1] * per;
+    it.cost = static_cast<int>(a.line[s + 1] - a.line[s]);
+    it.n = chunks_of(a, s, it.lo, it.hi);
+    it.c0 = a.first[s];
+  };
+  if (it.seq < 0) {
+    const int64_t T = a.line[a.n_seqs + 1];
+    it.at = share * T;
+    it.end = min(it.at + T, a.line[a.n_seqs] * per);
+    int lo = 0, hi = a.n_seqs - 1;  // the last sequence that begins at or before the share
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.line[mid] * per <= it.at) lo = mid;
+      else hi = mid - 1;
+    }
+    enter(lo);
+  } else if (it.give) {  // (its writers have made it visible before the barrier in front of this)
+    __threadfence();
+    atomicExch(a.given + share, 1u);
+  }
+  it.take = it.give = false;
+  for (;;) {
+    it.any = it.at < it.end;
+    if (!it.any) return;
+    if (it.at >= it.behind) enter(it.seq + 1);  // (each of them takes something)
+    const int rest = static_cast<int>((it.at - it.begin) % it.cost), task = static_cast<int>((it.at - it.begin) / it.cost);
+    const int64_t behind = it.at - rest + it.cost;
+    it.from = 0;
+    it.to = it.cost - 1;
+    if (rest > 0) {  // another block has its last chunks
+      it.to = it.cost - rest - 1;
+      it.at = behind;
+      if (it.to == 0) continue;  // all of them
+      it.give = true;
+    } else if (behind > it.end) {
+      it.from = static_cast<int>(behind - it.end) - 1;
+      it.take = it.from > 0;
+      it.at = it.end;
+    } else {
+      it.at = behind;
+    }
+    it.h = task / a.slices;
+    it.v0 = task % a.slices * across;
+    break;
+  }
+  if (!it.take) return;
+  const long long begun = clock64();
+  for (;;) {
+    uint32_t there;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(there) : "l"(a.given + share + 1) : "memory");
+    if (there) return;
+    if (clock64() - begun > kWaitBudgetCycles) {
+      if (a.status != nullptr) atomicOr(a.status, ENGRAM_ST_TIMEOUT);
+      return;
+    }
+    __nanosleep(200);
+  }
+}
+// A thread's part of a state that is handed on.
+template <int N>
+__device__ __forceinline__ void give_state(float* between, const float (&S)[N][4], int threads) {
+  float4* to = reinterpret_cast<float4*>(between) + threadIdx.x;
+#pragma unroll
+  for (int t = 0; t < N; ++t) to[t * threads] = make_float4(S[t][0], S[t][1], S[t][2], S[t][3]);
+  __threadfence();
+}
+template <int N>
+__device__ __forceinline__ void take_state(const float* between, float (&S)[N][4], int threads) {
+  const float4* from = reinterpret_cast<const float4*>(between) + threadIdx.x;
+#pragma unroll
+  for (int t = 0; t < N; ++t) {
+    const float4 x = __ldcg(from + t * threads);
+    S[t][0] = x.x; S[t][1] = x.y; S[t][2] = x.z; S[t][3] = x.w;
+  }
 }
 
 template <class E>
@@ -526,6 +630,52 @@ __device__ __forceinline__ void quad_sync(int quad) { asm volatile("bar.sync %0,
 template <int NQ>
 constexpr bool kAlone = NQ == 1;
 constexpr int kCopiers = 128;
+// The quads of a block of four go on by themselves, as far as the two stages of the chunks'
+// inputs let them: `here` counts the threads whose copies have come, `done` the warps that
+// no longer need a stage.  (201 chunks one after another, forwards: 1161 us with a barrier of
+// the block at each, 1121 so.)
+struct Stages {
+  uint64_t here[2], done[2];
+  int late;
+};
+__device__ __forceinline__ void stages_begin(Stages& s, int threads, int warps) {
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(smem_u32(&s.here[k]), threads + 1);
+      mbar_init(smem_u32(&s.done[k]), warps);
+    }
+    s.late = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+}
+// (a wait that runs out is reported, and the next ones with it; the block goes on to its end)
+__device__ __forceinline__ void stage_wait(Stages& s, uint64_t& bar, int use, int32_t* status) {
+  if (mbar_wait_bounded(smem_u32(&bar), use & 1, &s.late)) return;
+  *reinterpret_cast<volatile int*>(&s.late) = 1;
+  if (status != nullptr) atomicOr(status, ENGRAM_ST_TIMEOUT);
+}
+// The rest of a stage behind its rows: the triangles (`tri` bytes) and gates by one thread's
+// bulk copies.  A thread's own copies of rows count when they have come.
+__device__ __forceinline__ void stage_copies(Stages& s, int stage, uint32_t to_tri, const unsigned char* from_tri, int tri,
+                                             uint32_t to_gates, const Gates* from_gates, bool vec) {
+  const uint32_t bar = smem_u32(&s.here[stage]);
+  if (threadIdx.x == 0) {
+    mbar_arrive_expect_tx(bar, tri + static_cast<int>(sizeof(Gates)));
+    bulk_g2s(to_tri, from_tri, tri, bar);
+    bulk_g2s(to_gates, from_gates, sizeof(Gates), bar);
+  }
+  if (vec) asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+  else mbar_arrive(bar);
+}
+// (copies that were not waited for land before the shared memory is released)
+__device__ __forceinline__ void stages_end(Stages& s) {
+  if (!*reinterpret_cast<volatile int*>(&s.late)) return;
+  copies_done();
+  const long long begun = clock64();
+  while (clock64() - begun < (1 << 20)) {
+  }
+}
 template <int N>
 __device__ __forceinline__ void hand(uint32_t at, const uint32_t (&f)[N][4]) {
 #pragma unroll
@@ -576,7 +726,10 @@ __device__ __forceinline__ void terms(Sums<N, kApart>& c, const uint32_t (&a)[TA
 
 // The space behind a call's chunks.
 struct Space {
-  int32_t *first, *order;
+  int32_t* first;
+  int64_t* line;
+  uint32_t* given;
+  float* between;
   unsigned char* tri;
   Gates* gates;
   float* after;
@@ -604,14 +757,24 @@ inline int opt_in(const void* kernel, int smem, std::atomic<uint64_t>& done) {
   return ENGRAM_OK;
 }
 
+inline int slices_of(int dv, int quads) { return (dv + 16 * quads - 1) / (16 * quads); }
+
 // Quads of a block: four, which share the copies of a chunk's inputs, where such blocks
 // come to three quarters of the SMs or more; else one, so that few sequences and heads
-// spread over more SMs.  (dk = dv = 128, bf16: a chunk takes a block of four quads 6.4 us
+// spread over more SMs.  (dk = dv = 128, bf16: a chunk takes a block of four quads 5.6 us
 // and one of one 2.0, measured forwards: four blocks of one on an SM one after another
 // take 8.0, three 6.0.)
 template <class E>
 bool many_quads(const Args<E>& a, int sms) {
-  return E::kBytes == 2 && static_cast<int64_t>(a.n_seqs) * a.heads * ((a.dv + 63) / 64) * 4 >= 3 * static_cast<int64_t>(sms);
+  return E::kBytes == 2 && static_cast<int64_t>(a.n_seqs) * a.heads * slices_of(a.dv, 4) * 4 >= 3 * static_cast<int64_t>(sms);
+}
+// The blocks that follow the sequences: one on each SM at most (their shared memory and
+// registers leave no room for two).
+template <class E>
+void set_blocks(Args<E>& a, int sms) {
+  a.slices = slices_of(a.dv, many_quads(a, sms) ? 4 : 1);
+  a.blocks = static_cast<int32_t>(
+      std::min<int64_t>(std::min(sms, kMaxBlocks), static_cast<int64_t>(a.n_seqs) * a.heads * a.slices));
 }
 
 inline bool pieces(const void* p, int64_t stride, int bytes) { return aligned(p, 16) && stride * bytes % 16 == 0; }

@@ -21,11 +21,12 @@ namespace {
 // ------------------------------------------------ the state's gradient, backwards
 
 // A quad goes backwards as scan_kernel's go forwards, with dS^T in its registers.  (4096
-// positions in 7 sequences, 40 heads of 128, bf16: 277 us; the tensor cores are busy for
-// 42 % of the time and shared memory for 65.)
+// positions in 7 sequences, 40 heads of 128, bf16: 274 us; the tensor cores are busy for
+// 43 % of the time and shared memory for 68.)
 template <class E, int KD, int NQ>
 struct Back {
-  static constexpr int kT = kAlone<NQ> ? kCopiers : NQ * 128, kThreads = kAlone<NQ> ? 128 + kCopiers : kT, kStages = E::kBytes == 2 ? 2 : 1, kB = kC / 16;
+  static constexpr int kT = kAlone<NQ> ? kCopiers : NQ * 128, kThreads = kAlone<NQ> ? 128 + kCopiers : kT;
+  static constexpr int kStages = E::kBytes == 2 ? 2 : 1, kB = kC / 16;
   static constexpr int kK = 0, kQ = kK + kIn<E> * mat_bytes(kC, KD), kY = kQ + kIn<E> * mat_bytes(kC, KD);
   static constexpr int kM = kY + kIn<E> * mat_bytes(kC, 16 * NQ), kP = kM + kStateTerms * kTerm, kG = kP + kStateTerms * kTerm;
   static constexpr int kStage = kG + static_cast<int>(sizeof(Gates)), kQuads = kStages * kStage;
@@ -40,232 +41,263 @@ __global__ void __launch_bounds__(Back<E, KD, NQ>::kThreads, 1) back_kernel(Args
   using L = Back<E, KD, NQ>;
   constexpr int kT = L::kT, kI = kIn<E>, kS = kStateTerms, kB = L::kB, kR = KD / 64;
   extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ Stages stages;
+  __shared__ Item item;
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t2 = (lane & 3) * 2;
   const int quad = kAlone<NQ> ? 0 : tid >> 7, w = ((tid >> 5) + quad) & 3;
-  int seq, h, v0;
-  place_of(a, 16 * NQ, seq, h, v0);
-  const int cols = min(a.dv - v0, 16 * NQ);
-  const int hk = h / (a.heads / a.keys), vw = v0 + quad * 16;
-  int lo, hi;
-  bounds(a, seq, lo, hi);
-  const int c0 = a.first[seq], n = min((hi - lo + kC - 1) / kC, a.max_chunks - c0);
   const size_t matrix = static_cast<size_t>(a.dk) * a.dv, saved = saved_floats<E>(a.dk, a.dv);
-  int64_t slot;
-  if (!live_slot(a, seq, slot)) {
-    if (tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
-    padding_zeros(a, lo, hi, c0, n, h, v0, cols, blockDim.x);
-    return;
+  if (tid == 0) {
+    item.seq = -1;
+    item.give = false;
   }
-  const uint32_t own = base + L::kQuads + quad * L::kQuad;
-  float S[2 * kR][4];
-  auto each = [&](auto f) {  // f(tile, place, the element's place in a state)
-#pragma unroll
-    for (int t = 0; t < 2 * kR; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int v = vw + g + (j >> 1) * 8, k = w * kR * 16 + t * 8 + t2 + (j & 1);
-        if (v < a.dv && k < a.dk) f(t, j, static_cast<size_t>(k) * a.dv + v);
-      }
-  };
-  clear(S);
-  if (a.state_out != nullptr) {
-    const float* from = a.state_out + (slot * a.heads + h) * matrix;
-    each([&](int t, int j, size_t at) { S[t][j] = from[at]; });
-  }
-  auto hand_state = [&](int i) {  // the gradient of the state behind chunk i
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      const int kb = w * kR + r;
-      uint32_t f[kS][4];
-      as_operand<kS>(f, S[2 * r], S[2 * r + 1]);
-      hand<kS>(own + kb * (kS * 512), f);
-      if (vw >= a.dv || kb * 16 >= a.dk) continue;
-      float* to = a.after + unit_of(a, c0 + i, h) * saved;
-      if constexpr (E::kBytes == 2) save_block(block_of(to, a.dk, vw >> 4, kb), f);
-      else save_rows(to, a.dk, a.dv, vw, kb * 16, S[2 * r], S[2 * r + 1]);
+  if (!kAlone<NQ>) stages_begin(stages, kT, kT / 32);
+  for (int used = 0;;) {  // (used: how often the stages have been)
+    __syncthreads();
+    if (tid == 0) next_item(a, item, 16 * NQ);
+    __syncthreads();
+    if (!item.any) break;
+    // its chunks, from the last of the sequence's backwards: first, first - 1, .. last
+    const int h = uniform(item.h), v0 = uniform(item.v0), lo = uniform(item.lo), hi = uniform(item.hi), c0 = uniform(item.c0);
+    const int first = uniform(item.n - 1 - item.from), last_one = uniform(item.n - item.to);
+    const int cols = min(a.dv - v0, 16 * NQ);
+    const int hk = h / (a.heads / a.keys), vw = v0 + quad * 16;
+    int64_t slot;
+    if (!live_slot(a, item.seq, slot)) {
+      if (tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
+      padding_zeros(a, lo, hi, c0, item.n, h, v0, cols, blockDim.x);
+      continue;
     }
-  };
-  const int copier = tid - (kAlone<NQ> ? NQ * 128 : 0);  // a copying thread's number
-  auto load = [&](int i) {
-    const uint32_t stage = base + (i % L::kStages) * L::kStage;
-    const int64_t p = lo + static_cast<int64_t>(i) * kC;
-    const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
-    const uint8_t* mask = a.mask != nullptr ? a.mask + p : nullptr;
-    const size_t unit = unit_of(a, c0 + i, h);
-    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kK), a.k + p * a.k_stride + hk * a.dk, a.k_stride, len, a.dk, mask, a.vec, copier);
-    load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kQ), a.q + p * a.q_stride + hk * a.dk, a.q_stride, len, a.dk, mask, a.vec, copier);
-    load_rows<E, 16 * NQ, kT>(mat<kC, 16 * NQ>(stage + L::kY), a.dy + p * a.dy_stride + static_cast<int64_t>(h) * a.dv + v0,
-                              a.dy_stride, len, cols, mask, a.vec, copier);
-    load_tri<kS, kT>(stage + L::kM, stage + L::kP, a.tri + unit * kTriBytes, copier);
-    load_gates<kT>(stage + L::kG, a.gates + unit, copier);
-    copies_begun();
-  };
-  if (kAlone<NQ> && copier >= 0) {
-    if (n > 0) load(n - 1);
-    for (int i = n - 1; i >= 0; --i) {
-      copies_done();
-      __syncthreads();
-      if (L::kStages == 1 && i > 0) __syncthreads();
-      if (i > 0) load(i - 1);
-    }
-    return;
-  }
-  if (n > 0) {
-    hand_state(n - 1);
-    if (!kAlone<NQ>) load(n - 1);
-  }
-  for (int i = n - 1; i >= 0; --i) {
-    const uint32_t stage = base + (i % L::kStages) * L::kStage;
-    const Mat K = mat<kC, KD>(stage + L::kK), Q = mat<kC, KD>(stage + L::kQ), Y = mat<kC, 16 * NQ>(stage + L::kY);
-    const Gates& gt = *reinterpret_cast<const Gates*>(smem + (i % L::kStages) * L::kStage + L::kG);
-    copies_done();
-    __syncthreads();  // the chunk and the states' gradients are here, and the other stage is free
-    if (!kAlone<NQ> && L::kStages == 2 && i > 0) load(i - 1);
-    float2 into[2], last[2];  // of the warp's positions
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      into[t] = *reinterpret_cast<const float2*>(&gt.into[w * 16 + t * 8 + t2]);
-      last[t] = *reinterpret_cast<const float2*>(&gt.last[w * 16 + t * 8 + t2]);
-    }
-    // ---- dU^T = e^(c_last - c) (K dS)^T + dY^T P
-    Sums<2, true> x;
-    x.clear_all();
-#pragma unroll 4
-    for (int kb = 0; kb < KD / 16; ++kb) {
-      uint32_t fa[kS][4];
-      take<kS>(own + kb * (kS * 512), fa);
-#pragma unroll
-      for (int j = 0; j < kI; ++j) {
-        uint32_t fb[2][2];
-        Across{K}.get<2>(fb, kb * 16, w * 16, j);
-        terms<kS, kS>(x, fa, fb, j);
-      }
-    }
-    float u[2][4];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[t][j] = x.sum(t, j) * (j & 1 ? last[t].y : last[t].x);
-    x.clear_all();
-    for (int tb = w; tb < kB; ++tb) {
-      uint32_t fa[kI][4];
-#pragma unroll
-      for (int j = 0; j < kI; ++j) Cols{Y}(fa[j], quad * 16, tb * 16, j);
-#pragma unroll
-      for (int j = 0; j < kS; ++j) {
-        uint32_t fb[2][2];
-        TriDown{stage + L::kP}.get(fb, tb, w, j);
-        terms<kI, kS>(x, fa, fb, j);
-      }
-    }
-    {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) u[t][j] += x.sum(t, j);
-      uint32_t f[kS][4];
-      as_operand<kS>(f, u[0], u[1]);
-      hand<kS>(own + L::kU + w * (kS * 512), f);
-    }
-    quad_sync(quad);  // and dS^T is no longer needed
-    {
-      float r[2][4];
-      clear(r);
-#pragma unroll
-      for (int j = kI - 1; j >= 0; --j) {
-        uint32_t f[4];
-        Cols{Y}(f, quad * 16, w * 16, j);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          r[q >> 1][(q & 1) * 2] += lo_of(f[q]);
-          r[q >> 1][(q & 1) * 2 + 1] += hi_of(f[q]);
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) r[t][j] *= a.scale * (j & 1 ? into[t].y : into[t].x);
-      uint32_t f[kS][4];
-      as_operand<kS>(f, r[0], r[1]);
-      hand<kS>(own + L::kR + w * (kS * 512), f);
-    }
-    // ---- dV^T = dU^T M
-    x.clear_all();
-    for (int tb = w; tb < kB; ++tb) {
-      uint32_t fa[kS][4];
-      take<kS>(own + L::kU + tb * (kS * 512), fa);
-#pragma unroll
-      for (int j = 0; j < kS; ++j) {
-        uint32_t fb[2][2];
-        TriDown{stage + L::kM}.get(fb, tb, w, j);
-        terms<kS, kS>(x, fa, fb, j);
-      }
-    }
-    float rest[2][4];  // what the output's rounding leaves
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        u[t][j] = x.sum(t, j);
-        rest[t][j] = u[t][j] - lo_of(pack(u[t][j], 0.f));
-      }
-    {
-      float c[2][4];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[t][j] = -u[t][j] * (j & 1 ? into[t].y : into[t].x);
-      uint32_t f[kS][4];
-      as_operand<kS>(f, c[0], c[1]);
-      quad_sync(quad);  // dU^T is no longer needed
-      hand<kS>(own + L::kU + w * (kS * 512), f);
-    }
-    quad_sync(quad);
-    // ---- dS^T
-    {
-      const float total = gt.into[kC - 1];
-      Sums<2 * kR, true> d;
-      d.clear_all();
-#pragma unroll
-      for (int cb = 0; cb < kB; ++cb) {
-        uint32_t fr[kS][4], fw[kS][4];
-        take<kS>(own + L::kR + cb * (kS * 512), fr);
-        take<kS>(own + L::kU + cb * (kS * 512), fw);
-#pragma unroll
-        for (int j = 0; j < kI; ++j) {
-          uint32_t fb[2 * kR][2];
-          Down{Q}.get<2 * kR>(fb, cb * 16, w * kR * 16, j);
-          terms<kS, kS>(d, fr, fb, j);
-          Down{K}.get<2 * kR>(fb, cb * 16, w * kR * 16, j);
-          terms<kS, kS>(d, fw, fb, j);
-        }
-      }
+    const uint32_t own = base + L::kQuads + quad * L::kQuad;
+    float S[2 * kR][4];
+    auto each = [&](auto f) {  // f(tile, place, the element's place in a state)
 #pragma unroll
       for (int t = 0; t < 2 * kR; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) S[t][j] = fmaf(S[t][j], total, d.sum(t, j));
+        for (int j = 0; j < 4; ++j) {
+          const int v = vw + g + (j >> 1) * 8, k = w * kR * 16 + t * 8 + t2 + (j & 1);
+          if (v < a.dv && k < a.dk) f(t, j, static_cast<size_t>(k) * a.dv + v);
+        }
+    };
+    const int share = gridDim.x - 1 - blockIdx.x;
+    auto stage_of = [&](int i) { return kAlone<NQ> ? i % L::kStages : (used + first - i) & 1; };
+    auto hand_state = [&](int i) {  // the gradient of the state behind chunk i
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        const int kb = w * kR + r;
+        uint32_t f[kS][4];
+        as_operand<kS>(f, S[2 * r], S[2 * r + 1]);
+        hand<kS>(own + kb * (kS * 512), f);
+        if (vw >= a.dv || kb * 16 >= a.dk) continue;
+        float* to = a.after + unit_of(a, c0 + i, h) * saved;
+        if constexpr (E::kBytes == 2) save_block(block_of(to, a.dk, vw >> 4, kb), f);
+        else save_rows(to, a.dk, a.dv, vw, kb * 16, S[2 * r], S[2 * r + 1]);
+      }
+    };
+    const int copier = tid - (kAlone<NQ> ? NQ * 128 : 0);  // a copying thread's number
+    auto load = [&](int i) {
+      const uint32_t stage = base + stage_of(i) * L::kStage;
+      const int64_t p = lo + static_cast<int64_t>(i) * kC;
+      const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
+      const uint8_t* mask = a.mask != nullptr ? a.mask + p : nullptr;
+      const size_t unit = unit_of(a, c0 + i, h);
+      load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kK), a.k + p * a.k_stride + hk * a.dk, a.k_stride, len, a.dk, mask, a.vec, copier);
+      load_rows<E, KD, kT>(mat<kC, KD>(stage + L::kQ), a.q + p * a.q_stride + hk * a.dk, a.q_stride, len, a.dk, mask, a.vec, copier);
+      load_rows<E, 16 * NQ, kT>(mat<kC, 16 * NQ>(stage + L::kY), a.dy + p * a.dy_stride + static_cast<int64_t>(h) * a.dv + v0,
+                                a.dy_stride, len, cols, mask, a.vec, copier);
+      if constexpr (kAlone<NQ>) {
+        load_tri<kS, kT>(stage + L::kM, stage + L::kP, a.tri + unit * kTriBytes, copier);
+        load_gates<kT>(stage + L::kG, a.gates + unit, copier);
+        copies_begun();
+      } else {
+        stage_copies(stages, stage_of(i), stage + L::kM, a.tri + unit * kTriBytes, 2 * kS * kTerm, stage + L::kG, a.gates + unit,
+                     a.vec);
+      }
+    };
+    if (kAlone<NQ> && copier >= 0) {
+      if (first >= last_one) load(first);
+      for (int i = first; i >= last_one; --i) {
+        copies_done();
+        __syncthreads();
+        if (L::kStages == 1 && i > last_one) __syncthreads();
+        if (i > last_one) load(i - 1);
+      }
+      continue;
     }
-    if (i > 0) {
-      quad_sync(quad);  // the operands have been taken
-      hand_state(i - 1);
+    if (!kAlone<NQ> && first >= last_one) load(first);
+    clear(S);
+    if (item.take) {
+      take_state(a.between + static_cast<size_t>(share + 1) * kHandedOn, S, NQ * 128);
+    } else if (a.state_out != nullptr) {
+      const float* given = a.state_out + (slot * a.heads + h) * matrix;
+      each([&](int t, int j, size_t at) { S[t][j] = given[at]; });
     }
-    const int64_t p = lo + static_cast<int64_t>(i) * kC;
-    const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
-    store_rows<E>(a.dv_out + p * a.dv_stride + static_cast<int64_t>(h) * a.dv, a.dv_stride, w * 16, len, vw, a.dv, a.pairs,
-                  gt.beta, u);
-    if constexpr (E::kBytes == 2)
-      store_rows<E>(a.writes + (p * a.heads + h) * a.dv, static_cast<int64_t>(a.heads) * a.dv, w * 16, len, vw, a.dv,
-                    a.dv % 2 == 0, gt.beta, rest);
-    if (L::kStages == 1 && i > 0) {
-      __syncthreads();  // the stage is free
-      if (!kAlone<NQ>) load(i - 1);
+    if (first >= last_one) hand_state(first);
+    for (int i = first; i >= last_one; --i) {
+      const uint32_t stage = base + stage_of(i) * L::kStage;
+      const Mat K = mat<kC, KD>(stage + L::kK), Q = mat<kC, KD>(stage + L::kQ), Y = mat<kC, 16 * NQ>(stage + L::kY);
+      const Gates& gt = *reinterpret_cast<const Gates*>(smem + stage_of(i) * L::kStage + L::kG);
+      if constexpr (kAlone<NQ>) {
+        __syncthreads();  // the chunk and the states' gradients are here, and the other stage is free
+      } else {
+        quad_sync(quad);  // the states' gradients are here
+        stage_wait(stages, stages.here[stage_of(i)], (used + first - i) >> 1, a.status);
+      }
+      float2 into[2], last[2];  // of the warp's positions
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        into[t] = *reinterpret_cast<const float2*>(&gt.into[w * 16 + t * 8 + t2]);
+        last[t] = *reinterpret_cast<const float2*>(&gt.last[w * 16 + t * 8 + t2]);
+      }
+      // ---- dU^T = e^(c_last - c) (K dS)^T + dY^T P
+      Sums<2, true> x;
+      x.clear_all();
+#pragma unroll 4
+      for (int kb = 0; kb < KD / 16; ++kb) {
+        uint32_t fa[kS][4];
+        take<kS>(own + kb * (kS * 512), fa);
+#pragma unroll
+        for (int j = 0; j < kI; ++j) {
+          uint32_t fb[2][2];
+          Across{K}.get<2>(fb, kb * 16, w * 16, j);
+          terms<kS, kS>(x, fa, fb, j);
+        }
+      }
+      float u[2][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[t][j] = x.sum(t, j) * (j & 1 ? last[t].y : last[t].x);
+      x.clear_all();
+      for (int tb = w; tb < kB; ++tb) {
+        uint32_t fa[kI][4];
+#pragma unroll
+        for (int j = 0; j < kI; ++j) Cols{Y}(fa[j], quad * 16, tb * 16, j);
+#pragma unroll
+        for (int j = 0; j < kS; ++j) {
+          uint32_t fb[2][2];
+          TriDown{stage + L::kP}.get(fb, tb, w, j);
+          terms<kI, kS>(x, fa, fb, j);
+        }
+      }
+      {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u[t][j] += x.sum(t, j);
+        uint32_t f[kS][4];
+        as_operand<kS>(f, u[0], u[1]);
+        hand<kS>(own + L::kU + w * (kS * 512), f);
+      }
+      quad_sync(quad);  // and dS^T is no longer needed
+      {
+        float r[2][4];
+        clear(r);
+#pragma unroll
+        for (int j = kI - 1; j >= 0; --j) {
+          uint32_t f[4];
+          Cols{Y}(f, quad * 16, w * 16, j);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            r[q >> 1][(q & 1) * 2] += lo_of(f[q]);
+            r[q >> 1][(q & 1) * 2 + 1] += hi_of(f[q]);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) r[t][j] *= a.scale * (j & 1 ? into[t].y : into[t].x);
+        uint32_t f[kS][4];
+        as_operand<kS>(f, r[0], r[1]);
+        hand<kS>(own + L::kR + w * (kS * 512), f);
+      }
+      // ---- dV^T = dU^T M
+      x.clear_all();
+      for (int tb = w; tb < kB; ++tb) {
+        uint32_t fa[kS][4];
+        take<kS>(own + L::kU + tb * (kS * 512), fa);
+#pragma unroll
+        for (int j = 0; j < kS; ++j) {
+          uint32_t fb[2][2];
+          TriDown{stage + L::kM}.get(fb, tb, w, j);
+          terms<kS, kS>(x, fa, fb, j);
+        }
+      }
+      float rest[2][4];  // what the output's rounding leaves
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          u[t][j] = x.sum(t, j);
+          rest[t][j] = u[t][j] - lo_of(pack(u[t][j], 0.f));
+        }
+      {
+        float c[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) c[t][j] = -u[t][j] * (j & 1 ? into[t].y : into[t].x);
+        uint32_t f[kS][4];
+        as_operand<kS>(f, c[0], c[1]);
+        quad_sync(quad);  // dU^T is no longer needed
+        hand<kS>(own + L::kU + w * (kS * 512), f);
+      }
+      if (!kAlone<NQ> && i > last_one) {
+        if (i < first) stage_wait(stages, stages.done[stage_of(i - 1)], (used + first - i - 1) >> 1, a.status);
+        load(i - 1);
+      }
+      quad_sync(quad);
+      // ---- dS^T
+      {
+        const float total = gt.into[kC - 1];
+        Sums<2 * kR, true> d;
+        d.clear_all();
+#pragma unroll
+        for (int cb = 0; cb < kB; ++cb) {
+          uint32_t fr[kS][4], fw[kS][4];
+          take<kS>(own + L::kR + cb * (kS * 512), fr);
+          take<kS>(own + L::kU + cb * (kS * 512), fw);
+#pragma unroll
+          for (int j = 0; j < kI; ++j) {
+            uint32_t fb[2 * kR][2];
+            Down{Q}.get<2 * kR>(fb, cb * 16, w * kR * 16, j);
+            terms<kS, kS>(d, fr, fb, j);
+            Down{K}.get<2 * kR>(fb, cb * 16, w * kR * 16, j);
+            terms<kS, kS>(d, fw, fb, j);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 2 * kR; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) S[t][j] = fmaf(S[t][j], total, d.sum(t, j));
+      }
+      if (i > last_one) {
+        quad_sync(quad);  // the operands have been taken
+        hand_state(i - 1);
+      }
+      const int64_t p = lo + static_cast<int64_t>(i) * kC;
+      const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
+      store_rows<E>(a.dv_out + p * a.dv_stride + static_cast<int64_t>(h) * a.dv, a.dv_stride, w * 16, len, vw, a.dv, a.pairs,
+                    gt.beta, u);
+      if constexpr (E::kBytes == 2)
+        store_rows<E>(a.writes + (p * a.heads + h) * a.dv, static_cast<int64_t>(a.heads) * a.dv, w * 16, len, vw, a.dv,
+                      a.dv % 2 == 0, gt.beta, rest);
+      if constexpr (kAlone<NQ>) {
+        if (L::kStages == 1 && i > last_one) __syncthreads();  // the stage is free
+      } else {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&stages.done[stage_of(i)]));
+      }
+    }
+    used += first + 1 - last_one;
+    if (item.give) {
+      give_state(a.between + static_cast<size_t>(share) * kHandedOn, S, NQ * 128);
+    } else if (a.state_out != nullptr) {
+      float* to = a.state_out + (slot * a.heads + h) * matrix;
+      each([&](int t, int j, size_t at) { to[at] = S[t][j]; });
     }
   }
-  if (a.state_out != nullptr) {
-    float* to = a.state_out + (slot * a.heads + h) * matrix;
-    each([&](int t, int j, size_t at) { to[at] = S[t][j]; });
-  }
+  if (!kAlone<NQ>) stages_end(stages);
 }
 
 // ------------------------------------------------------- all chunks' gradients
@@ -693,9 +725,7 @@ int launch_grad(const Args<E>& a, int sms, cudaStream_t st) {
   constexpr int VG = E::kBytes == 2 ? 32 : 16;
   const dim3 grads(a.max_chunks, a.keys);
   auto back = [&](auto kernel, int smem, int nq, std::atomic<uint64_t>& flag) {
-    const int64_t blocks = static_cast<int64_t>(a.n_seqs) * a.heads * ((a.dv + 16 * nq - 1) / (16 * nq));
-    if (blocks > 0x7fffffff) return fail(ENGRAM_E_RANGE, "too many sequences times heads");
-    return go(kernel, smem, dim3(static_cast<unsigned>(blocks)), flag, "back_kernel",
+    return go(kernel, smem, dim3(a.blocks), flag, "back_kernel",
               nq == 1 ? 128 + kCopiers : nq * 128);
   };
   bool many = false;
@@ -714,7 +744,7 @@ int launch_grad(const Args<E>& a, int sms, cudaStream_t st) {
                     : go(grads_kernel<E, 128, VG>, Grads<E, 128, VG>::kSmem, grads, done[3], "grads_kernel", Grads<E, 128, VG>::kT);
 }
 
-static_assert(Back<train::Bf16, 128, 4>::kSmem <= 232448 && Back<train::F32, 128, 1>::kSmem <= 232448 &&
+static_assert(Back<train::Bf16, 128, 4>::kSmem + sizeof(Stages) + sizeof(Item) <= 232448 && Back<train::F32, 128, 1>::kSmem <= 232448 &&
                   Grads<train::Bf16, 128, 32>::kSmem <= 232448 && Grads<train::F32, 128, 16>::kSmem <= 232448,
               "a block's shared memory");
 
@@ -809,7 +839,10 @@ extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void
     a.status = status_d;
     const Space s = space(workspace_d, n_tokens, n_seqs, key_heads, heads, dk, dv, true);
     a.first = s.first;
-    a.order = s.order;
+    a.line = s.line;
+    a.given = s.given;
+    a.between = s.between;
+    set_blocks(a, sms);
     a.tri = s.tri;
     a.gates = s.gates;
     a.after = s.after;

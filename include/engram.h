@@ -745,7 +745,9 @@ int engram_recurrence_step(const void* x_d, int64_t x_stride, const void* g_d, i
  * overlap no input (but state_out_d may be state_d).  States and sums are fp32.  g below
  * -80 counts as -80 and b below -40 as -40.  An infinity or a NaN in a position that is
  * not masked spoils its sequence and head from the beginning of its chunk on.  Positions
- * outside every sequence are left as they are.  Results are the same from run to run. */
+ * outside every sequence are left as they are.  A block that takes a sequence over from
+ * another waits for its state; a wait that runs out sets ENGRAM_ST_TIMEOUT, and the outputs
+ * are then undefined.  Results are the same from run to run. */
 #define ENGRAM_DELTA_CHUNK 64
 #define ENGRAM_DELTA_MAX_DIM 128
 size_t engram_delta_carry_bytes(int64_t n_tokens, int64_t n_seqs, int32_t heads, int32_t dk, int32_t dv);

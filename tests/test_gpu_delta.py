@@ -249,6 +249,17 @@ def test_many_short_sequences_of_several_heads():
     run(cu[-1], 1, 2, 16, 24, cu, "bf16", 145, masked=0.1, state=True)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,S,H,masked", [(2000, 12, 40, 0.0), (1900, 5, 48, 0.1), (700, 60, 20, 0.0)])
+def test_more_than_the_blocks_hold(T, S, H, masked, kind):
+    """Sequences that go over from one block to the next, some of them after a few of their chunks; with the longest one
+    much longer than the others, and with empty ones among them."""
+    cu = cuts(T, S, 200 + S)
+    run(T, 4, H, 16, 40, cu, kind, 200, masked=masked, state=True)
+    cu = [0, T // 2] + [T // 2] * 3 + [T // 2 + k * (T // 2) // (S - 1) for k in range(1, S)]
+    run(T, 4, H, 16, 40, cu, kind, 210, masked=masked)
+
+
 def test_sequences_that_lie_over_one_another_stay_in_bounds():
     """They are no valid call: what they give is not defined, but nothing else is touched."""
     T, H, d = 300, 2, 16

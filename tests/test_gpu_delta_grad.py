@@ -191,9 +191,15 @@ def test_outputs_between_other_columns_and_positions_outside():
         assert (u[:10] == 3).all() and (u[90:] == 3).all() and (o[:, :2] == 3).all() and (o[:, -3:] == 3).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,S,H,masked", [(2000, 12, 40, 0.0), (1900, 5, 48, 0.1), (700, 60, 20, 0.0)])
+def test_more_than_the_blocks_hold(T, S, H, masked, kind):
+    run(T, 4, H, 16, 40, cuts(T, S, 200 + S), kind, 200, masked=masked, state=True)
+
+
 @pytest.mark.parametrize("S,keys,H,dk,dv,kind", [(1300, 1, 2, 16, 24, "bf16"), (1100, 1, 1, 8, 8, "f32")])
 def test_many_short_sequences(S, keys, H, dk, dv, kind):
-    """More sequences than are sorted by length."""
+    """More sequences than one block numbers at a time."""
     cu = [0]
     for n in torch.randint(0, 3, (S,), generator=torch.Generator().manual_seed(3)).tolist():
         cu.append(cu[-1] + n)
