@@ -413,6 +413,32 @@ __device__ __forceinline__ void both_products(float (&c)[N][4], float (&d)[N][4]
   }
 }
 
+__device__ __forceinline__ void ld128(uint32_t (&x)[4], uint32_t at) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
+}
+// four neighbouring values of N terms
+template <int N>
+__device__ __forceinline__ void get4(uint32_t at, int term, float (&x)[4]) {
+  x[0] = x[1] = x[2] = x[3] = 0.f;
+#pragma unroll
+  for (int n = N - 1; n >= 0; --n) {
+    uint32_t w0, w1;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(at + n * term) : "memory");
+    x[0] += lo_of(w0);
+    x[1] += hi_of(w0);
+    x[2] += lo_of(w1);
+    x[3] += hi_of(w1);
+  }
+}
+// an element of an operand's terms: of pair p its first or second
+template <int N>
+__device__ __forceinline__ float of_rows(const uint32_t (&f)[N][4], int p, int e) {
+  float x = 0.f;
+#pragma unroll
+  for (int n = N - 1; n >= 0; --n) x += e ? hi_of(f[n][p]) : lo_of(f[n][p]);
+  return x;
+}
+
 __device__ __forceinline__ float quad_sum(float v) {
   v += __shfl_xor_sync(0xffffffffu, v, 1);
   return v + __shfl_xor_sync(0xffffffffu, v, 2);
@@ -512,13 +538,19 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
       if (L::kStages == 2 && step + 1 < steps) load(step + 1);
       // S . dS, wherever their values lie
       if constexpr (E::kBytes == 2) {
+        if (VS / 16 * (KD / 16) * 32 == kT || tid < VS / 16 * (KD / 16) * 32) {
+          const uint32_t to = at + (tid >> 5) * kBlockBytes + lane * 16;
+          uint32_t s[2][4], d[2][4];
 #pragma unroll
-        for (int i0 = 0; i0 < VS / 16 * (KD / 16) * 128; i0 += kT) {
-          const uint32_t word = static_cast<uint32_t>(i0 + tid), to = at + (word >> 7) * kBlockBytes + (word & 127) * 4;
-          float s[2], d[2];
-          get<kO>(to + L::kS, 512, s[0], s[1]);
-          get<kO>(to + L::kD, 512, d[0], d[1]);
-          whole = fmaf(s[0], d[0], fmaf(s[1], d[1], whole));
+          for (int n = 0; n < 2; ++n) {
+            ld128(s[n], to + L::kS + n * 512);
+            ld128(d[n], to + L::kD + n * 512);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            whole = fmaf(lo_of(s[0][j]) + lo_of(s[1][j]), lo_of(d[0][j]) + lo_of(d[1][j]), whole);
+            whole = fmaf(hi_of(s[0][j]) + hi_of(s[1][j]), hi_of(d[0][j]) + hi_of(d[1][j]), whole);
+          }
         }
       } else {
         const Mat sm = mat<VS, KD>(at + L::kS), dm = mat<VS, KD>(at + L::kD);
@@ -532,15 +564,14 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
       }
       // dV . U of the block's positions: kT / 64 neighbouring threads a position
       {
-        constexpr int kBy = kT / kC, kPairs = VS / 2 / kBy;
-        const uint32_t off = (tid / kBy) * W.pitch + tid % kBy * kPairs * 4;
+        constexpr int kBy = kT / kC;
+        static_assert(VS / kBy == 4, "four columns a thread");
+        const uint32_t off = (tid / kBy) * W.pitch + tid % kBy * 8;
+        float u[4], w[4];
+        get4<kO>(U.base + off, U.term, u);
+        get4<kO>(W.base + off, W.term, w);
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          float u[2], w[2];
-          get<kO>(U.base + off + i * 4, U.term, u[0], u[1]);
-          get<kO>(W.base + off + i * 4, W.term, w[0], w[1]);
-          dot = fmaf(u[0], w[0], fmaf(u[1], w[1], dot));
-        }
+        for (int i = 0; i < 4; ++i) dot = fmaf(u[i], w[i], dot);
       }
       both_products<kIn<E>, kO>(cq, ck, Rows{Y}, Rows{W}, S, m, nk, VS);
       product<kO, kO, kO>(cw, Rows{U}, D, m, nk, 0, VS);
@@ -571,26 +602,31 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
         column += __shfl_xor_sync(0xffffffffu, column, 16);
         if (g == 0) columns[(m >> 4) * kC + i] = column;
       }
+    // (an operand A's places are those of two neighbouring accumulators)
+    uint32_t fq[L::kKN / 2][kIn<E>][4], fk[L::kKN / 2][kIn<E>][4];
+#pragma unroll
+    for (int t = 0; t < L::kKN / 2; ++t)
+#pragma unroll
+      for (int n = 0; n < kIn<E>; ++n) {
+        Rows{Q}(fq[t][n], m, nk + t * 16, n);
+        Rows{K}(fk[t][n], m, nk + t * 16, n);
+      }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int r = m + g + j * 8;
       const float into = gt.into[r], last = gt.last[r];
       float read = 0.f, write = 0.f;
 #pragma unroll
-      for (int t = 0; t < L::kKN; ++t) {
-        const uint32_t at = r * K.pitch + (nk + t * 8 + t2) * 2;
-        float q[2], k[2];
-        get<kIn<E>>(Q.base + at, Q.term, q[0], q[1]);
-        get<kIn<E>>(K.base + at, K.term, k[0], k[1]);
+      for (int t = 0; t < L::kKN; ++t)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          const float q = of_rows<kIn<E>>(fq[t / 2], (t & 1) * 2 + j, e), k = of_rows<kIn<E>>(fk[t / 2], (t & 1) * 2 + j, e);
           cq[t][2 * j + e] *= a.scale * into;
           const float seen = -into * ck[t][2 * j + e], left = last * cw[t][2 * j + e];
-          read = fmaf(q[e], cq[t][2 * j + e], fmaf(k[e], seen, read));
-          write = fmaf(k[e], left, write);
+          read = fmaf(q, cq[t][2 * j + e], fmaf(k, seen, read));
+          write = fmaf(k, left, write);
           ck[t][2 * j + e] = seen + left;
         }
-      }
       const float sum_row = quad_sum(row[j]), sum_read = quad_sum(read), sum_write = quad_sum(write);
       if (t2 == 0) {
         rows[part * kC + r] = sum_row;
