@@ -289,10 +289,17 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(Args<E> a) {
 }
 
 template <class E>
-int launch_prepare(const Args<E>& a, cudaStream_t st) {
+int launch_first(const Args<E>& a, cudaStream_t st) {
   first_kernel<E><<<1, 1024, 0, st>>>(a);
-  int rc = check_launch("first_kernel");
-  if (rc || a.max_chunks == 0) return rc;
+  return check_launch("first_kernel");
+}
+template int launch_first<train::Bf16>(const Args<train::Bf16>&, cudaStream_t);
+template int launch_first<train::F32>(const Args<train::F32>&, cudaStream_t);
+
+// M, P and the gates of all chunks.
+template <class E>
+int launch_prepare(const Args<E>& a, cudaStream_t st) {
+  if (a.max_chunks == 0) return ENGRAM_OK;
   auto go = [&](auto kernel, int smem, std::atomic<uint64_t>& done) {
     int r = opt_in(reinterpret_cast<const void*>(kernel), smem, done);
     if (r) return r;
@@ -303,8 +310,6 @@ int launch_prepare(const Args<E>& a, cudaStream_t st) {
   return a.dk <= 64 ? go(prepare_kernel<E, 64>, kPrepareSmem<E, 64>, done[0])
                     : go(prepare_kernel<E, 128>, kPrepareSmem<E, 128>, done[1]);
 }
-template int launch_prepare<train::Bf16>(const Args<train::Bf16>&, cudaStream_t);
-template int launch_prepare<train::F32>(const Args<train::F32>&, cudaStream_t);
 
 // --------------------------------------------------------------------- scan
 
@@ -782,9 +787,10 @@ Space space(void* base, int64_t n_tokens, int64_t n_seqs, int32_t keys, int32_t 
   const int64_t blocks = std::min<int64_t>(kMaxBlocks, n_seqs * heads * slices_of(dv, 1));
   s.given = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * blocks));
   s.between = reinterpret_cast<float*>(take(sizeof(float) * kHandedOn * blocks));
-  s.tri = take(units * kTriBytes);
-  s.gates = reinterpret_cast<Gates*>(take(units * sizeof(Gates)));
-  if (backward) {
+  if (!backward) {
+    s.tri = take(units * kTriBytes);
+    s.gates = reinterpret_cast<Gates*>(take(units * sizeof(Gates)));
+  } else {
     s.after = reinterpret_cast<float*>(take(units * saved_floats<train::Bf16>(dk, dv) * sizeof(float)));
     s.writes = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(n_tokens) * heads * dv * sizeof(uint16_t)));
     // (a block's threads leave a chunk's sums, 64 x 128 of queries and of keys, as they hold them)
@@ -805,8 +811,8 @@ using namespace engram::delta;
 extern "C" size_t engram_delta_carry_bytes(int64_t n_tokens, int64_t n_seqs, int32_t heads, int32_t dk, int32_t dv) {
   if (n_tokens < 0 || n_seqs < 0 || heads < 1 || dk < 1 || dv < 1) return 0;
   // (both types' room: bf16's blocks are padded, fp32's matrices are not)
-  return (static_cast<size_t>(max_chunks(n_tokens, n_seqs)) * heads * saved_floats<train::Bf16>(dk, dv) +
-          static_cast<size_t>(n_tokens) * heads * dv) * sizeof(float);
+  const int64_t chunks = max_chunks(n_tokens, n_seqs);
+  return kept_triangles_at(n_tokens, chunks, heads, dk, dv) + static_cast<size_t>(chunks) * heads * (kTriBytes + sizeof(Gates));
 }
 
 extern "C" size_t engram_delta_workspace_bytes(int64_t n_tokens, int64_t n_seqs, int32_t key_heads, int32_t heads, int32_t dk,
@@ -837,8 +843,8 @@ extern "C" int engram_delta(const void* q_d, int64_t q_stride, const void* k_d, 
   } else if (state_out_d == nullptr || state_out_d == state_d) {
     return ENGRAM_OK;
   }
-  if (!aligned(state_d, 4) || !aligned(state_out_d, 4) || !aligned(carry_d, 4))
-    return fail(ENGRAM_E_ALIGN, "states and carry must be aligned to their elements");
+  if (!aligned(state_d, 4) || !aligned(state_out_d, 4)) return fail(ENGRAM_E_ALIGN, "states must be aligned to their elements");
+  if (!aligned(carry_d, 16)) return fail(ENGRAM_E_ALIGN, "carry must be 16-byte aligned");
   if (!workspace_d) return fail(ENGRAM_E_INVALID, "null device pointer: workspace");
   if (!aligned(workspace_d, 256)) return fail(ENGRAM_E_ALIGN, "workspace must be 256-byte aligned");
   if (workspace_bytes < engram_delta_workspace_bytes(n_tokens, n_seqs, key_heads, heads, dk, dv, 0))
@@ -889,7 +895,9 @@ extern "C" int engram_delta(const void* q_d, int64_t q_stride, const void* k_d, 
     set_blocks(a, sms);
     a.tri = s.tri;
     a.gates = s.gates;
-    int r = launch_prepare<E>(a, as_stream(stream));
+    if (a.carry != nullptr) use_kept_triangles(a);
+    int r = launch_first<E>(a, as_stream(stream));
+    if (!r) r = launch_prepare<E>(a, as_stream(stream));
     return r ? r : launch_scan<E>(a, sms, as_stream(stream));
   };
   return type == ENGRAM_T_BF16 ? go(train::Bf16{}) : go(train::F32{});

@@ -559,6 +559,18 @@ __device__ __forceinline__ typename E::T* kept_writes(const Args<E>& a) {
   return reinterpret_cast<typename E::T*>(a.carry + static_cast<size_t>(a.max_chunks) * a.heads * saved_floats<E>(a.dk, a.dv));
 }
 
+// Behind those the chunks' triangles and gates, where either type's have their place.
+inline size_t kept_triangles_at(int64_t n_tokens, int64_t chunks, int32_t heads, int32_t dk, int32_t dv) {  // bytes
+  const size_t floats =
+      static_cast<size_t>(chunks) * heads * saved_floats<train::Bf16>(dk, dv) + static_cast<size_t>(n_tokens) * heads * dv;
+  return (floats * sizeof(float) + 15) & ~size_t(15);
+}
+template <class E>
+void use_kept_triangles(Args<E>& a) {
+  a.tri = reinterpret_cast<unsigned char*>(a.carry) + kept_triangles_at(a.n_tokens, a.max_chunks, a.heads, a.dk, a.dv);
+  a.gates = reinterpret_cast<Gates*>(a.tri + static_cast<size_t>(a.max_chunks) * a.heads * kTriBytes);
+}
+
 // The outputs (y, or the values' gradient) of a sequence without a slot, and the states
 // that it would have left for the backward pass.
 template <class E>
@@ -742,9 +754,9 @@ inline int64_t max_chunks(int64_t n_tokens, int64_t n_seqs) {
 }
 Space space(void* base, int64_t n_tokens, int64_t n_seqs, int32_t keys, int32_t heads, int32_t dk, int32_t dv, bool backward);
 
-// first[], M, P and the gates of all chunks.
+// The chunks' numbers and the blocks' shares of them.
 template <class E>
-int launch_prepare(const Args<E>& a, cudaStream_t st);
+int launch_first(const Args<E>& a, cudaStream_t st);
 
 inline int opt_in(const void* kernel, int smem, std::atomic<uint64_t>& done) {
   int dev = 0;

@@ -10,8 +10,9 @@
 //   db_t = (dV_t . U_t) (1 - beta_t) / beta_t
 //   dg_t = (1 - f_t) (what crosses t: reads of S at t and later, writes before t that
 //          reach dS, pairs of the two of them, and e^c_last S . dS)
-// The states in front of the chunks and U come from the forward pass; M and P are
-// computed again.
+// The states in front of the chunks, U, M and P come from the forward pass.  (M and P made
+// again took 55 of 1020 us for 4096 positions of 40 heads, both passes together; they are a
+// quarter of what is kept, and would take the same room here while they are used.)
 #include "delta_device.cuh"
 
 namespace engram {
@@ -332,24 +333,16 @@ struct Grads {
 
 // `cols` columns of a saved state, from column v0 on, zeros around them.
 template <class E, int KD, int VS, int kT>
-__device__ __forceinline__ void load_state(uint32_t to, const float* from, int v0, int cols, int dk, bool vec) {
+__device__ __forceinline__ void load_state(uint32_t to, const float* from, int v0, int cols, int dk) {
   if constexpr (E::kBytes == 2) {
     // blocks as they lie, and zeros where the head has none
     const int across = (dk + 15) / 16;
     const uint32_t* blocks = reinterpret_cast<const uint32_t*>(from) + static_cast<size_t>(v0 / 16) * across * (kBlockBytes / 4);
-    if (vec) {
 #pragma unroll
-      for (int i0 = 0; i0 < VS / 16 * (KD / 16) * (kBlockBytes / 16); i0 += kT) {
-        const int i = i0 + threadIdx.x, b = i / (kBlockBytes / 16), vb = b / (KD / 16), kb = b % (KD / 16);
-        const bool on = vb * 16 < cols && kb < across;
-        copy16(to + i * 16, on ? blocks + (vb * across + kb) * (kBlockBytes / 4) + i % (kBlockBytes / 16) * 4 : blocks, on);
-      }
-    } else {
-      for (int i = threadIdx.x; i < VS / 16 * (KD / 16) * (kBlockBytes / 4); i += kT) {
-        const int b = i / (kBlockBytes / 4), vb = b / (KD / 16), kb = b % (KD / 16);
-        const bool on = vb * 16 < cols && kb < across;
-        st32(to + i * 4, on ? blocks[(vb * across + kb) * (kBlockBytes / 4) + i % (kBlockBytes / 4)] : 0u);
-      }
+    for (int i0 = 0; i0 < VS / 16 * (KD / 16) * (kBlockBytes / 16); i0 += kT) {
+      const int i = i0 + threadIdx.x, b = i / (kBlockBytes / 16), vb = b / (KD / 16), kb = b % (KD / 16);
+      const bool on = vb * 16 < cols && kb < across;
+      copy16(to + i * 16, on ? blocks + (vb * across + kb) * (kBlockBytes / 4) + i % (kBlockBytes / 16) * 4 : blocks, on);
     }
   } else {
     const Mat m = mat<VS, KD>(to);
@@ -496,8 +489,8 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
       load_rows<E, VS, kT>(second(W), a.writes + p * wide + column, wide, ch.len, cols, nullptr, a.vec);
       load_rows<E, VS, kT>(second(U), kept + a.n_tokens * wide, wide, ch.len, cols, nullptr, a.vec);
     }
-    load_state<E, KD, VS, kT>(at + L::kS, a.carry + unit * saved, v0, cols, a.dk, a.vec);
-    load_state<E, KD, VS, kT>(at + L::kD, a.after + unit * saved, v0, cols, a.dk, a.vec);
+    load_state<E, KD, VS, kT>(at + L::kS, a.carry + unit * saved, v0, cols, a.dk);
+    load_state<E, KD, VS, kT>(at + L::kD, a.after + unit * saved, v0, cols, a.dk);
     copies_begun();
   };
   load_rows<E, KD, kT>(K, a.k + p * a.k_stride + hk * a.dk, a.k_stride, ch.len, a.dk, mask, a.vec);
@@ -749,7 +742,7 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
 
 template <class E>
 int launch_grad(const Args<E>& a, int sms, cudaStream_t st) {
-  int rc = launch_prepare<E>(a, st);
+  int rc = launch_first<E>(a, st);
   if (rc) return rc;
   static std::atomic<uint64_t> done[4] = {{0}, {0}, {0}, {0}};
   auto go = [&](auto kernel, int smem, dim3 grid, std::atomic<uint64_t>& flag, const char* name, int threads = kThreads) {
@@ -817,8 +810,8 @@ extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void
   if ((rc = check_rows(dv_d, type, dv_stride, wide_v, "dv"))) return rc;
   if ((rc = check_rows(dg_d, type, dg_stride, heads, "dg"))) return rc;
   if ((rc = check_rows(db_d, type, db_stride, heads, "db"))) return rc;
-  if (!aligned(dstate_d, 4) || !aligned(carry_d, 4))
-    return fail(ENGRAM_E_ALIGN, "states and carry must be aligned to their elements");
+  if (!aligned(dstate_d, 4)) return fail(ENGRAM_E_ALIGN, "states must be aligned to their elements");
+  if (!aligned(carry_d, 16)) return fail(ENGRAM_E_ALIGN, "carry must be 16-byte aligned");
   if (!workspace_d) return fail(ENGRAM_E_INVALID, "null device pointer: workspace");
   if (!aligned(workspace_d, 256)) return fail(ENGRAM_E_ALIGN, "workspace must be 256-byte aligned");
   if (workspace_bytes < engram_delta_workspace_bytes(n_tokens, n_seqs, key_heads, heads, dk, dv, 1))
@@ -867,8 +860,7 @@ extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void
     a.dv = dv;
     a.scale = scale;
     a.vec = pieces(q_d, q_stride, E::kBytes) && pieces(k_d, k_stride, E::kBytes) &&
-            pieces(dy_d, dy_stride, E::kBytes) && pieces(dv_d, dv_stride, E::kBytes) && aligned(carry_d, 16) && dk % 8 == 0 &&
-            dv % 8 == 0;
+            pieces(dy_d, dy_stride, E::kBytes) && pieces(dv_d, dv_stride, E::kBytes) && dk % 8 == 0 && dv % 8 == 0;
     a.pairs = dv % 2 == 0 && dv_stride % 2 == 0 && aligned(dv_d, 2 * E::kBytes);
     a.key_pairs = dk % 2 == 0 && dq_stride % 2 == 0 && dk_stride % 2 == 0 && aligned(dq_d, 2 * E::kBytes) &&
                   aligned(dk_d, 2 * E::kBytes);
@@ -879,8 +871,7 @@ extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void
     a.given = s.given;
     a.between = s.between;
     set_blocks(a, sms);
-    a.tri = s.tri;
-    a.gates = s.gates;
+    use_kept_triangles(a);
     a.after = s.after;
     a.writes = s.writes;
     a.shared = s.shared;

@@ -735,9 +735,10 @@ int engram_recurrence_step(const void* x_d, int64_t x_stride, const void* g_d, i
  *                positions, or NULL (zeros)
  *   state_out_d  the same, the states after the last positions (an empty sequence's is
  *                its first), or NULL; may be state_d
- *   carry_d      float32, engram_delta_carry_bytes(...) bytes, or NULL: for the backward
- *                pass, the state in front of every ENGRAM_DELTA_CHUNK positions of a
- *                sequence and every position's u, laid out as that pass reads them
+ *   carry_d      engram_delta_carry_bytes(...) bytes, 16-byte aligned, or NULL: for the
+ *                backward pass, the state in front of every ENGRAM_DELTA_CHUNK positions
+ *                of a sequence, every position's u and the chunks' triangles, laid out as
+ *                that pass reads them
  *   workspace_d  engram_delta_workspace_bytes(..., 0) bytes, 256-byte aligned; its
  *                contents on entry do not matter, and the call has it to itself until
  *                it is done (two graphs that may run at once have two)
@@ -762,7 +763,7 @@ int engram_delta(const void* q_d, int64_t q_stride, const void* k_d, int64_t k_s
 
 /* The gradients of q, k, v, g, b and the first states; those of a key head are summed over
  * the value heads that share it.  carry_d is what a forward call on the same arguments
- * filled; the chunks are computed again from it.
+ * filled.
  *   dstate_d     float32 [n_slots][heads][dk][dv] in/out, or NULL (zeros in): the
  *                gradients of the last states on entry, of the first states on return
  *   workspace_d  engram_delta_workspace_bytes(..., 1) bytes */

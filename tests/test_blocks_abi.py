@@ -113,7 +113,7 @@ def test_delta(lib):
     need = lib.engram_delta_workspace_bytes(70, 2, 1, 2, 8, 8, 0)
     assert need > 0 and lib.engram_delta_workspace_bytes(-1, 2, 1, 2, 8, 8, 0) == 0
     # at most floor((70 + 63 * 2) / 64) chunks, matrices padded to 16 x 16, and the writes
-    assert lib.engram_delta_carry_bytes(70, 2, 2, 8, 8) == (3 * 2 * 16 * 16 + 70 * 2 * 8) * 4
+    assert lib.engram_delta_carry_bytes(70, 2, 2, 8, 8) == (3 * 2 * 16 * 16 + 70 * 2 * 8) * 4 + 3 * 2 * (2 * 3 * 5120 + 1280)
     assert lib.engram_delta_carry_bytes(0, 2, 2, 8, 8) == 0
 
     def call(q=P(16), qs=8, k=P(16), ks=8, v=P(16), vs=16, g=P(16), gs=2, b=P(16), bs=2, ty=F32, T=70, keys=1, H=2, dk=8,

@@ -208,12 +208,12 @@ def test_many_short_sequences(S, keys, H, dk, dv, kind):
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("T,keys,H,dk,dv", [(130, 1, 2, 32, 40), (90, 2, 2, 128, 64)])
-def test_a_carry_at_any_element(T, keys, H, dk, dv, kind):
-    """The kept states may lie at any multiple of four bytes, and the last of them ends inside a chunk."""
+def test_a_carry_within_a_larger_one(T, keys, H, dk, dv, kind):
+    """What is kept may lie at any multiple of 16 bytes; the last sequence ends inside a chunk."""
     args, dy, cu = inputs(T, keys, H, dk, dv, kind, 98), make((T, H * dv), kind, 99), i64([0, 70, T])
     room, want = eg.delta_carry(T, 2, keys, H, dk, dv, DEV).numel(), None
-    for shift in (0, 1, 2):
-        carry = torch.full((room + 4,), 7.0, device=DEV)
+    for shift in (0, 4, 8):
+        carry = torch.full((room + 12,), 7.0, device=DEV)
         part = carry[shift:shift + room]
         eg.engram_delta(*args, cu, keys, carry=part)
         got = eg.engram_delta_grad(dy, *args, part, cu, keys)
@@ -221,6 +221,9 @@ def test_a_carry_at_any_element(T, keys, H, dk, dv, kind):
         for u, w in zip(got, want):
             assert torch.equal(u, w)
         assert (carry[:shift] == 7).all() and (carry[shift + room:] == 7).all()
+    for call in (lambda c: eg.engram_delta(*args, cu, keys, carry=c), lambda c: eg.engram_delta_grad(dy, *args, c, cu, keys)):
+        with pytest.raises(eg.EngramError):
+            call(carry[1:1 + room])
 
 
 def test_captured_beside_an_eager_backward_pass():
