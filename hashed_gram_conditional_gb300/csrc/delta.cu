@@ -134,8 +134,15 @@ __device__ __forceinline__ void put_tri(unsigned char* base, int t, int i, float
 }
 
 constexpr int kPrepareThreads = 128;
+// Factors of D between two blocks of 16 positions: from a block's first position to its
+// others, and from positions before it to its first.
+struct Factors {
+  float row[kC], column[3][kC];  // column[bt - 1][i], i < 16 bt
+};
 template <class E, int KD>
-constexpr int kPrepareSmem = std::max(2 * kIn<E> * mat_bytes(kC, KD), 2 * kC * kPitch * 4) + static_cast<int>(sizeof(Gates));
+constexpr int kPrepareRoom = std::max(2 * kIn<E> * mat_bytes(kC, KD), 2 * kC * kPitch * 4);
+template <class E, int KD>
+constexpr int kPrepareSmem = kPrepareRoom<E, KD> + static_cast<int>(sizeof(Gates) + sizeof(Factors));
 
 // A block of four warps makes M and P of one head in one chunk.  K K^T and Q K^T stay in
 // the registers until they are A and P; A and M take the place of K and Q.  Heads that
@@ -145,7 +152,7 @@ constexpr int kPrepareSmem = std::max(2 * kIn<E> * mat_bytes(kC, KD), 2 * kC * k
 // between the inverse's steps.
 template <class E, int KD>
 __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(Args<E> a) {
-  constexpr int kRoom = std::max(2 * kIn<E> * mat_bytes(kC, KD), 2 * kC * kPitch * 4);
+  constexpr int kRoom = kPrepareRoom<E, KD>;
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
   Chunk ch;
@@ -153,6 +160,7 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(Args<E> a) {
   const Mat K = mat<kC, KD>(smem_u32(smem)), Q = mat<kC, KD>(K.base + kIn<E> * K.term);
   float *A = reinterpret_cast<float*>(smem), *M = A + kC * kPitch;
   Gates& gt = *reinterpret_cast<Gates*>(smem + kRoom);
+  Factors& fc = *reinterpret_cast<Factors*>(smem + kRoom + sizeof(Gates));
   const uint8_t* mask = a.mask != nullptr ? a.mask + ch.start : nullptr;
   const int h = blockIdx.y, hk = h / (a.heads / a.keys);
   load_rows<E, KD, kPrepareThreads>(K, a.k + ch.start * a.k_stride + hk * a.dk, a.k_stride, ch.len, a.dk, mask, a.vec);
@@ -204,6 +212,11 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(Args<E> a) {
   }
   copies_done();
   __syncthreads();
+  // (each factor is at most 1: what underflows is nothing beside D's own 2^-126)
+  for (int i = tid; i < 4 * kC; i += kPrepareThreads) {
+    const int bt = i < kC ? (i >> 4) : (i >> 6), to = i < kC ? i : bt * 16, from = i < kC ? bt * 16 : i & 63;
+    if (from <= to) (&fc.row[0])[i] = expf((gt.hi[to] - gt.hi[from]) + (gt.lo[to] - gt.lo[from]));
+  }
   // K K^T and Q K^T: the triangle's ten blocks of 16 x 16 in turn, three a warp at most
   float ck[3][2][4], cq[3][2][4];
   auto block = [&](int n, int& bt, int& bi) {
@@ -218,8 +231,23 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(Args<E> a) {
     clear(cq[n]);
     int bt, bi;
     if (!block(n, bt, bi)) continue;
-    product<kIn<E>, kIn<E>, kIn<E>>(ck[n], Rows{K}, Across{K}, bt * 16, bi * 16, 0, KD);
-    product<kIn<E>, kIn<E>, kIn<E>>(cq[n], Rows{Q}, Across{K}, bt * 16, bi * 16, 0, KD);
+    if constexpr (kIn<E> == 1) {
+#pragma unroll 4
+      for (int k = 0; k < KD; k += 16) {
+        uint32_t fk[4], fq[4], fb[2][2];
+        Rows{K}(fk, bt * 16, k, 0);
+        Rows{Q}(fq, bt * 16, k, 0);
+        Across{K}.get<2>(fb, k, bi * 16, 0);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mma(ck[n][e], fk, fb[e][0], fb[e][1]);
+          mma(cq[n][e], fq, fb[e][0], fb[e][1]);
+        }
+      }
+    } else {
+      product<kIn<E>, kIn<E>, kIn<E>>(ck[n], Rows{K}, Across{K}, bt * 16, bi * 16, 0, KD);
+      product<kIn<E>, kIn<E>, kIn<E>>(cq[n], Rows{Q}, Across{K}, bt * 16, bi * 16, 0, KD);
+    }
   }
   __syncthreads();  // K and Q are no longer needed
   const size_t unit = unit_of(a, blockIdx.x, h);
@@ -237,12 +265,27 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(Args<E> a) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int t = bt * 16 + g + j * 8;
-        const float d0 = i <= t ? expf((gt.hi[t] - hi.x) + (gt.lo[t] - lo.x)) : 0.f;
-        const float d1 = i + 1 <= t ? expf((gt.hi[t] - hi.y) + (gt.lo[t] - lo.y)) : 0.f;
-        *reinterpret_cast<float2*>(A + t * kPitch + i) =
-            make_float2(i < t ? gt.beta[t] * d0 * ck[n][e][2 * j] : 0.f, i + 1 < t ? gt.beta[t] * d1 * ck[n][e][2 * j + 1] : 0.f);
-        put_tri<kStateTerms>(tri + kStateTerms * kTerm, t, i, i <= t ? a.scale * d0 * cq[n][e][2 * j] : 0.f,
-                             i + 1 <= t ? a.scale * d1 * cq[n][e][2 * j + 1] : 0.f);
+        float d0, d1;
+        if (bt > bi) {
+          const float2 c = *reinterpret_cast<const float2*>(&fc.column[bt - 1][i]);
+          d0 = fc.row[t] * c.x;
+          d1 = fc.row[t] * c.y;
+        } else {
+          d0 = expf((gt.hi[t] - hi.x) + (gt.lo[t] - lo.x));
+          d1 = expf((gt.hi[t] - hi.y) + (gt.lo[t] - lo.y));
+        }
+        const float beta = gt.beta[t];
+        float k0 = beta * d0 * ck[n][e][2 * j], k1 = beta * d1 * ck[n][e][2 * j + 1];
+        float q0 = a.scale * d0 * cq[n][e][2 * j], q1 = a.scale * d1 * cq[n][e][2 * j + 1];
+        if (bt == bi) {  // (above the diagonal there may be anything)
+          if (i >= t) k0 = 0.f;
+          if (i + 1 >= t) k1 = 0.f;
+          if (i > t) q0 = 0.f;
+          if (i + 1 > t) q1 = 0.f;
+        }
+        *reinterpret_cast<float2*>(A + t * kPitch + i) = make_float2(k0, k1);
+        if (E::kBytes == 4 || a.carry != nullptr) put_tri<kStateTerms>(tri + kStateTerms * kTerm, t, i, q0, q1);
+        else put_tri<kOut<E>>(tri + kStateTerms * kTerm, t, i, q0, q1);
       }
     }
   }
