@@ -13,9 +13,10 @@
 //   dw_next = sum dx h' r(h'),  dscale = sum l n,  dw = sum dn silu(gate) y r
 //
 // Every array is read or written once.  A block holds a row in registers, in 16-byte
-// vectors, from the first sum to the last store; the gradient's blocks stay, go from row
-// to row with the next rows on their way, and keep the weights' sums of their columns.
-// 16,384 x 5120 bf16 with gate, residual and next norm: 146 us (5.8 TB/s, 86 % of a copy's
+// vectors, from the first sum to the last store; with many rows of one group the blocks
+// stay and go from row to row with the next rows on their way; the gradient's always do, and
+// keep the weights' sums of their columns.
+// 16,384 x 5120 bf16 with gate, residual and next norm: 130 us (6.5 TB/s, 97 % of a copy's
 // rate), bound by memory, as is the gradient: 237 us, of which 227 (5.9 TB/s) for the rows and
 // 9 for the weights' sums.  Rows that are not 16-byte aligned go a value a thread
 // (8192 x 5119: 381 and 960 us), and rows longer than a block's threads hold are walked
@@ -265,6 +266,16 @@ __device__ __forceinline__ const float* weights_at(const Args& a, int e) {
   return a.w == nullptr ? nullptr : a.w + (a.groups == 1 ? e : e % a.width);
 }
 
+__device__ __forceinline__ void copy_vec(uint32_t to, const uint4* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ uint4 own_vec(uint32_t at) {
+  uint4 x;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+  return x;
+}
+constexpr int kRingThreads = 640, kRingSmem = 220 * 1024;
+
 // ------------------------------------------------------------------- forward
 
 template <class P, int kPer>
@@ -336,6 +347,110 @@ __global__ void __launch_bounds__(P::kMost) norm_kernel(Args a) {
     for (int j = 0; j < N; ++j) h[j] *= r * w[j];
     row_of<E, Raw>(a.x_out, row, a.x_stride)[v] = P::narrow(h);
   }
+}
+
+// The same for many rows of one group: the blocks stay and go from row to row, with the next
+// rows on their way through shared memory (a thread copies and reads its own vectors, one of
+// each array) and the weights of their columns in registers.  A row's sum of h'^2 and the
+// next one's of y^2 are joined at one barrier.  (us, this form and a block for each row,
+// bf16: 16,384 x 5120 130 and 147; 32,768 x 1280 74 and 80; 2048 x 5120 26 and 27; 700 x 5120
+// 17 and 16; in 40 groups, which the lanes join, 16,384 x 5120 156 and 152.)
+constexpr int kAheadRows = 4;  // rows in use and on their way
+template <class E>
+__global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(Args a) {
+  using V = Pairs<E>;
+  constexpr int N = V::N;
+  extern __shared__ __align__(16) float part[];
+  __shared__ float2 slot[2][32];
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5, v = threadIdx.x;
+  const bool in = v < a.vecs;
+  const uint32_t ring = smem_u32(part) + v * 16;
+  auto place = [&](int stage, int array) { return ring + (stage * 3 + array) * a.vecs * 16; };
+  const float inv_dim = 1.f / a.dim;
+  uint64_t ws[N], wn[N];  // w times scale, and w_next
+  if (in) {
+    uint64_t s[N];
+    V::weights(a.w ? a.w + v * 2 * N : nullptr, ws);
+    V::weights(a.scale ? a.scale + v * 2 * N : nullptr, s);
+    V::weights(a.w_next ? a.w_next + v * 2 * N : nullptr, wn);
+#pragma unroll
+    for (int j = 0; j < N; ++j) ws[j] = f2_mul(ws[j], s[j]);
+  }
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < a.rows && in) {
+      copy_vec(place(stage, 0), row_of<E, uint4>(a.y, row, a.y_stride) + v);
+      if (a.gate) copy_vec(place(stage, 1), row_of<E, uint4>(a.gate, row, a.gate_stride) + v);
+      if (a.h) copy_vec(place(stage, 2), row_of<E, uint4>(a.h, row, a.h_stride) + v);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto square = [&](int stage) {
+    if (!in) return 0.f;
+    uint64_t y[N], yy = f2_both(0.f);
+    V::widen(own_vec(place(stage, 0)), y);
+#pragma unroll
+    for (int j = 0; j < N; ++j) yy = f2_fma(y[j], y[j], yy);
+    return f2_sum(yy);
+  };
+  // The block's two sums at one barrier, in places that the next but one takes again.
+  int parity = 0;
+  auto join = [&](float& s0, float& s1) {
+    s0 = warp_sum(s0);
+    s1 = warp_sum(s1);
+    if (warps == 1) return;
+    float2* to = slot[parity];
+    parity ^= 1;
+    if (lane == 0) to[threadIdx.x >> 5] = make_float2(s0, s1);
+    __syncthreads();
+    const float2 x = lane < warps ? to[lane] : make_float2(0.f, 0.f);
+    s0 = warp_sum(x.x);
+    s1 = warp_sum(x.y);
+  };
+  for (int k = 0; k < kAheadRows - 1; ++k) fetch(blockIdx.x + static_cast<int64_t>(k) * gridDim.x, k);
+  asm volatile("cp.async.wait_group %0;" ::"n"(kAheadRows - 2) : "memory");
+  float sum = 0.f, sq = square(0);
+  join(sum, sq);
+  int stage = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const int next = stage + 1 == kAheadRows ? 0 : stage + 1;
+    fetch(row + static_cast<int64_t>(kAheadRows - 1) * gridDim.x, stage == 0 ? kAheadRows - 1 : stage - 1);
+    uint64_t h[N], hh = f2_both(0.f);
+    if (in) {
+      const float r = rsqrtf(sq * inv_dim + a.eps);
+      uint64_t y[N];
+      V::widen(own_vec(place(stage, 0)), y);
+#pragma unroll
+      for (int j = 0; j < N; ++j) y[j] = f2_mul(f2_mul(y[j], f2_both(r)), ws[j]);
+      if (a.gate) {
+        uint64_t z[N];
+        V::widen(own_vec(place(stage, 1)), z);
+#pragma unroll
+        for (int j = 0; j < N; ++j) y[j] = f2_mul(y[j], f2_mul(z[j], sigmoid_pair<E>(z[j])));
+      }
+      if (a.h) {
+        V::widen(own_vec(place(stage, 2)), h);
+#pragma unroll
+        for (int j = 0; j < N; ++j) y[j] = f2_add(y[j], h[j]);
+      }
+      const uint4 kept = V::narrow(y);
+      row_of<E, uint4>(a.h_out, row, a.h_out_stride)[v] = kept;
+      V::widen(kept, h);
+#pragma unroll
+      for (int j = 0; j < N; ++j) hh = f2_fma(h[j], h[j], hh);
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAheadRows - 2) : "memory");
+    sq = square(next);  // (of a row behind the last: not used)
+    sum = f2_sum(hh);
+    join(sum, sq);
+    if (in && a.x_out != nullptr) {
+      const float r = rsqrtf(sum * inv_dim + a.eps);
+#pragma unroll
+      for (int j = 0; j < N; ++j) h[j] = f2_mul(f2_mul(h[j], f2_both(r)), wn[j]);
+      row_of<E, uint4>(a.x_out, row, a.x_stride)[v] = V::narrow(h);
+    }
+    stage = next;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // out[g] = last(sum over the group's values of f(g, place in it)), by a warp for each group
@@ -527,18 +642,8 @@ __global__ void __launch_bounds__(kMost) norm_grad_kernel(Args a) {
 // registers hold little more than the weights and their sums and no barrier is for the
 // copies.  (16,384 x 5120 bf16, us: 319 with single values and the weights read again for
 // every row, 300 in pairs of values, 280 with w and scale in registers, 227 with w_next too.)
-__device__ __forceinline__ void copy_vec(uint32_t to, const uint4* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ uint4 own_vec(uint32_t at) {
-  uint4 x;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
-  return x;
-}
 constexpr int kRing = 3;  // rows of a block in use, next, and on their way
-constexpr int kRingThreads = 640;
 constexpr int kArrays = 5;   // y, gate, dh, h', dx
-constexpr int kRingSmem = 220 * 1024;
 
 template <class E, int kPer>
 __global__ void __launch_bounds__(kPer == 1 ? kRingThreads : kThreads, 1) norm_grad_ring_kernel(Args a) {
@@ -906,8 +1011,10 @@ void set_vecs(Args& a) {
     if (per == 1 << k) a.vecs_log2 = k;
 }
 
+// Rows for each block from which on the blocks stay (see norm_ring_kernel).
+constexpr int kManyRows = 8;
 template <class E>
-int launch_norm(Args a, cudaStream_t st) {
+int launch_norm(Args a, int sms, cudaStream_t st) {
   const unsigned rows = static_cast<unsigned>(a.rows);
   const bool wide = by_vectors<E>(a);
   if (!wide && a.dim > kSingles * Single<E>::kMost) {
@@ -916,6 +1023,18 @@ int launch_norm(Args a, cudaStream_t st) {
   }
   if (wide) set_vecs<Wide<E>>(a);
   else set_vecs<Single<E>>(a);
+  if (wide && a.groups == 1 && a.vecs <= kRingThreads) {
+    const size_t ring = static_cast<size_t>(kAheadRows) * 3 * a.vecs * 16;
+    const int threads = (a.vecs + 31) / 32 * 32, at_once = std::min(kRingThreads / threads, static_cast<int>(kRingSmem / ring));
+    const int64_t blocks = static_cast<int64_t>(std::min(at_once, 8)) * sms;
+    if (a.rows >= kManyRows * blocks) {
+      static std::atomic<uint64_t> done{0};
+      const int r = opt_in(reinterpret_cast<const void*>(norm_ring_kernel<E>), done);
+      if (r) return r;
+      norm_ring_kernel<E><<<static_cast<unsigned>(blocks), threads, ring, st>>>(a);
+      return check_launch("norm_ring_kernel");
+    }
+  }
   const int per = wide ? per_thread(a.vecs, 4) : a.vecs <= 4 * kThreads ? 4 : kSingles;
   const int threads = ((a.vecs + per - 1) / per + 31) / 32 * 32;
   const size_t smem = a.groups > 1 && a.vecs_log2 < 0 ? sizeof(float) * (a.vecs + a.groups) : 0;
@@ -1021,7 +1140,8 @@ extern "C" int engram_norm_add(const void* y_d, int64_t y_stride, const void* ga
   if ((rc = check_rows(x_d, type, x_stride, dim, "x", false))) return rc;
   if ((rc = check_weights(w_d, scale_d, w_next_d))) return rc;
   if (h_out_d == h_d && h_out_stride != h_stride) return fail(ENGRAM_E_SHAPE, "in place, h_out has the stride of h");
-  if ((rc = check_device(nullptr))) return rc;
+  int sms = 0;
+  if ((rc = check_device(&sms))) return rc;
   Args a{};
   a.y = y_d;
   a.gate = gate_d;
@@ -1041,8 +1161,8 @@ extern "C" int engram_norm_add(const void* y_d, int64_t y_stride, const void* ga
   a.groups = groups;
   a.width = dim / groups;
   a.eps = eps;
-  return type == ENGRAM_T_BF16 ? launch_norm<train::Bf16>(a, as_stream(stream))
-                               : launch_norm<train::F32>(a, as_stream(stream));
+  return type == ENGRAM_T_BF16 ? launch_norm<train::Bf16>(a, sms, as_stream(stream))
+                               : launch_norm<train::F32>(a, sms, as_stream(stream));
 }
 
 extern "C" size_t engram_norm_add_workspace_bytes(int64_t n_rows, int32_t dim) {

@@ -72,6 +72,23 @@ def test_forward_and_gradient(T, D, groups, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D,groups", [(1300, 2560, 1), (1301, 2560, 20), (1400, 2400, 50), (2700, 1280, 10), (6000, 8, 1),
+                                        (5100, 264, 3), (700, 5120, 1), (640, 5120, 40), (1300, 2000, 5)])
+def test_many_rows_for_each_block(T, D, groups, kind):
+    run(T, D, kind, 400, groups)
+    run(T, D, kind, 410, groups, gate=False, res=False, scaled=False, weighted=groups > 1, nxt=groups == 1)
+
+
+def test_many_rows_in_place():
+    T, D = 1300, 2000
+    y, z, h = (make((T, D), "bf16", 420 + k) for k in range(3))
+    w, s, wn = (make((D,), "f32", 430 + k) for k in range(3))
+    out, x = eg.engram_norm_add(y, w, gate=z, h=h, scale=s, w_next=wn)
+    kept, again = eg.engram_norm_add(y, w, gate=z, h=h, scale=s, w_next=wn, h_out=h)
+    assert kept is h and torch.equal(h, out) and torch.equal(again, x)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("gate,res,scaled,weighted,nxt,dh", [(False, False, False, False, False, True),
                                                              (False, False, False, True, True, False),
                                                              (True, False, False, True, False, True),
