@@ -1365,7 +1365,7 @@ def _call(idx: int, name: str, fn, *args):
 
 
 def delta_carry(n_tokens: int, n_seqs: int, key_heads: int, heads: int, dk: int, dv: int, device) -> torch.Tensor:
-    """Buffer for the states that engram_delta saves for its backward pass."""
+    """Buffer for what engram_delta saves for its backward pass: states, writes and the chunks' triangles."""
     n = _bytes_of("engram_delta_carry_bytes", n_tokens, n_seqs, heads, dk, dv) // 4
     return torch.empty(max(n, 1), dtype=torch.float32, device=device)
 

@@ -147,8 +147,8 @@ constexpr int kPrepareSmem = kPrepareRoom<E, KD> + static_cast<int>(sizeof(Gates
 // A block of four warps makes M and P of one head in one chunk.  K K^T and Q K^T stay in
 // the registers until they are A and P; A and M take the place of K and Q.  Heads that
 // share a key head compute its products again, which is little beside the rest; blocks of
-// eight warps for all of them took twice as long (110 us against 52 for 2560 chunks and
-// heads, dk = 128).  Bound by instructions issued (1.8 a clock and SM) and the waits
+// eight warps for all of them took twice as long (110 us against 52, now 48, for 2560 chunks
+// and heads, dk = 128).  Bound by instructions issued (2.0 a clock and SM) and the waits
 // between the inverse's steps.
 template <class E, int KD>
 __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(Args<E> a) {
@@ -363,7 +363,7 @@ int launch_prepare(const Args<E>& a, cudaStream_t st) {
 //
 // Four quads a block (16,384 positions in 4 sequences, 40 heads of 128, bf16: 768 us where no
 // sequence is longer than a block's share, 5.6 a chunk): the tensor cores are busy for 42 %
-// of the time and shared memory for 76; what is left are waits of warps that have nothing
+// of the time and shared memory for 72; what is left are waits of warps that have nothing
 // else to do between a quad's barriers.  One quad (16,381
 // positions, 10 heads: 520 us, 2.0 a chunk): instructions that follow one another.  A form
 // with 16 columns and the whole of their state a warp, without anything handed on, read a

@@ -23,7 +23,7 @@ namespace {
 
 // A quad goes backwards as scan_kernel's go forwards, with dS^T in its registers.  (4096
 // positions in 7 sequences, 40 heads of 128, bf16: 274 us; the tensor cores are busy for
-// 43 % of the time and shared memory for 68.)
+// 42 % of the time and shared memory for 65.)
 template <class E, int KD, int NQ>
 struct Back {
   static constexpr int kT = kAlone<NQ> ? kCopiers : NQ * 128, kThreads = kAlone<NQ> ? 128 + kCopiers : kT;
@@ -307,8 +307,8 @@ __global__ void __launch_bounds__(Back<E, KD, NQ>::kThreads, 1) back_kernel(Args
 // value columns in slices of VS.  The next slice's inputs are copied while this one is
 // used (bf16: all of them are operands as they lie in memory; fp32 are made terms on
 // the way).  A warp has 16 rows and a part of the columns of each product: a quarter, or
-// of type fp32, whose operands take more registers, half.  (The same 4096 x 40: 366 us, of
-// which the tensor cores are busy for 31 %; the rest is the instructions of a head's end,
+// of type fp32, whose operands take more registers, half.  (The same 4096 x 40: 353 us, of
+// which the tensor cores are busy for 32 %; the rest is the instructions of a head's end,
 // where F and E are made, and the barriers around them.  Making U again in place of reading
 // it took 561 us: two more barriers a slice.)
 template <class E, int KD, int VS>

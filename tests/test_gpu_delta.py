@@ -90,7 +90,7 @@ def test_packed_sequences(T, S, masked, state, kind):
                                                            (300, 80, 1, 2, 33, 125, 0.3, True), (500, 1, 38, 76, 128, 24, 0.0, False),
                                                            (400, 2, 20, 40, 65, 128, 0.0, False), (130, 40, 2, 2, 8, 1, 0.0, True)])
 def test_many_sequences_and_heads(T, S, keys, H, dk, dv, masked, state):
-    """Where a warp follows a sequence in a head."""
+    """Where a block has four quads."""
     run(T, keys, H, dk, dv, cuts(T, S, S), "bf16", 35, masked, state)
 
 
@@ -258,6 +258,31 @@ def test_more_than_the_blocks_hold(T, S, H, masked, kind):
     run(T, 4, H, 16, 40, cu, kind, 200, masked=masked, state=True)
     cu = [0, T // 2] + [T // 2] * 3 + [T // 2 + k * (T // 2) // (S - 1) for k in range(1, S)]
     run(T, 4, H, 16, 40, cu, kind, 210, masked=masked)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_padding_among_more_than_the_blocks_hold(kind):
+    """Sequences without a slot change where the others are cut, and none of their results; the backward pass likewise."""
+    T, S, keys, H, dk, dv = 2500, 21, 4, 40, 16, 40
+    args, cu = inputs(T, keys, H, dk, dv, kind, 220), [0] + list(range(61, T, 120))[:S - 1] + [T]
+    dy, s0 = make((T, H * dv), kind, 229), make((S, H, dk, dv), "f32", 230, 0.3)
+    slots = list(range(S))
+    res = []
+    for gone in ((), (0, 3, 4, 5, 11, S - 1)):
+        sl = i32([-1 if s in gone else s for s in slots])
+        out, ds, carry = s0.clone(), s0.clone(), eg.delta_carry(T, S, keys, H, dk, dv, DEV)
+        y = eg.engram_delta(*args, i64(cu), keys, state=out, slots=sl, carry=carry)
+        res.append((y, out, *eg.engram_delta_grad(dy, *args, carry, i64(cu), keys, slots=sl, dstate=ds), ds))
+    kept = torch.ones(T, dtype=torch.bool)
+    for s in gone:
+        kept[cu[s]:cu[s + 1]] = False
+    kept = kept.to(DEV)
+    rest = [s for s in slots if s not in gone]
+    for u, w in zip(*res):
+        if u.dim() == 4:
+            assert torch.equal(u[rest], w[rest]) and torch.equal(w[list(gone)], s0[list(gone)])
+        else:
+            assert torch.equal(u[kept], w[kept]) and (w[~kept] == 0).all()
 
 
 def test_sequences_that_lie_over_one_another_stay_in_bounds():

@@ -74,7 +74,7 @@ def test_packed_sequences(T, S, masked, state, kind):
                                                            (300, 80, 1, 2, 33, 125, 0.3, True), (500, 1, 38, 76, 128, 24, 0.0, False),
                                                            (400, 2, 20, 40, 65, 128, 0.0, False), (130, 40, 2, 2, 8, 1, 0.0, True)])
 def test_many_sequences_and_heads(T, S, keys, H, dk, dv, masked, state):
-    """Where a warp follows a sequence in a head."""
+    """Where a block has four quads."""
     run(T, keys, H, dk, dv, cuts(T, S, S), "bf16", 35, masked, state)
 
 
