@@ -79,6 +79,31 @@ def test_many_rows_for_each_block(T, D, groups, kind):
     run(T, D, kind, 410, groups, gate=False, res=False, scaled=False, weighted=groups > 1, nxt=groups == 1)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [40, 1000, 2560, 5120])
+@pytest.mark.parametrize("gate,nxt,dh", [(True, False, True), (False, False, True), (False, True, False)])
+def test_parts_left_out_of_many_rows(D, gate, nxt, dh, kind):
+    T = 1400 if D > 2000 else 5000
+    run(T, D, kind, 440, 1, gate=gate, nxt=nxt, dh=dh)
+
+
+def test_many_rows_with_nan_and_zeros():
+    """They stay in their row, in the rows of a block before and after it too."""
+    T, D = 2600, 2000
+    y, z, h, wn = make((T, D), "bf16", 450), make((T, D), "bf16", 451), make((T, D), "bf16", 452), make((D,), "f32", 453)
+    clean, cx = eg.engram_norm_add(y, gate=z, h=h, w_next=wn)
+    y[1000, 5], h[1700, 9] = float("nan"), float("inf")
+    y[1300] = 0.0
+    out, x = eg.engram_norm_add(y, gate=z, h=h, w_next=wn)
+    rest = torch.ones(T, dtype=torch.bool, device=DEV)
+    rest[[1000, 1300, 1700]] = False
+    assert torch.equal(out[rest], clean[rest]) and torch.equal(x[rest], cx[rest])
+    assert torch.isnan(out[1000]).all() and torch.equal(out[1300], h[1300])
+    g = torch.ones_like(y)
+    got = eg.engram_norm_add_grad(g, y, gate=z, h_out=out, dx=g, w_next=wn)
+    assert all(torch.isfinite(t[rest]).all() for t in got[:3])
+
+
 def test_many_rows_in_place():
     T, D = 1300, 2000
     y, z, h = (make((T, D), "bf16", 420 + k) for k in range(3))
