@@ -835,7 +835,7 @@ Space space(void* base, int64_t n_tokens, int64_t n_seqs, int32_t keys, int32_t 
     s.gates = reinterpret_cast<Gates*>(take(units * sizeof(Gates)));
   } else {
     s.after = reinterpret_cast<float*>(take(units * saved_floats<train::Bf16>(dk, dv) * sizeof(float)));
-    s.writes = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(n_tokens) * heads * dv * sizeof(uint16_t)));
+    s.writes = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(n_tokens) * heads * dv * 2 * sizeof(uint16_t)));
     // (a block's threads leave a chunk's sums, 64 x 128 of queries and of keys, as they hold them)
     if (heads > keys)
       s.shared = reinterpret_cast<float*>(

@@ -86,8 +86,8 @@ struct Args {
   int32_t blocks, slices;  // of the kernels that follow the sequences; slices of a head's value columns
   unsigned char* tri;
   Gates* gates;
-  // backward: states' gradients behind the chunks, as `carry` has the states in front of them; the second terms of
-  // the values' gradients (bf16); sums over heads that share a key
+  // backward: states' gradients behind the chunks, as `carry` has the states in front of them; the second and the third
+  // terms of the values' gradients (bf16), one array behind the other; sums over heads that share a key
   float* after;
   uint16_t* writes;
   float* shared;

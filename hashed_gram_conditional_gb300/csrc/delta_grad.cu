@@ -280,9 +280,16 @@ __global__ void __launch_bounds__(Back<E, KD, NQ>::kThreads, 1) back_kernel(Args
       const int len = hi - p < kC ? static_cast<int>(hi - p) : kC;
       store_rows<E>(a.dv_out + p * a.dv_stride + static_cast<int64_t>(h) * a.dv, a.dv_stride, w * 16, len, vw, a.dv, a.pairs,
                     gt.beta, u);
-      if constexpr (E::kBytes == 2)
-        store_rows<E>(a.writes + (p * a.heads + h) * a.dv, static_cast<int64_t>(a.heads) * a.dv, w * 16, len, vw, a.dv,
-                      a.dv % 2 == 0, gt.beta, rest);
+      if constexpr (E::kBytes == 2) {
+        const int64_t wide = static_cast<int64_t>(a.heads) * a.dv;
+        auto* to = a.writes + p * wide + static_cast<int64_t>(h) * a.dv;
+        store_rows<E>(to, wide, w * 16, len, vw, a.dv, a.dv % 2 == 0, gt.beta, rest);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) rest[t][j] -= lo_of(pack(rest[t][j], 0.f));
+        store_rows<E>(to + a.n_tokens * wide, wide, w * 16, len, vw, a.dv, a.dv % 2 == 0, gt.beta, rest);
+      }
       if constexpr (kAlone<NQ>) {
         if (L::kStages == 1 && i > last_one) __syncthreads();  // the stage is free
       } else {
@@ -311,9 +318,15 @@ __global__ void __launch_bounds__(Back<E, KD, NQ>::kThreads, 1) back_kernel(Args
 // which the tensor cores are busy for 32 %; the rest is the instructions of a head's end,
 // where F and E are made, and the barriers around them.  Making U again in place of reading
 // it took 561 us: two more barriers a slice.)
+//
+// dV is three terms for either type.  Where a write overwrites what its key held (beta near
+// 1, keys that come back), dg is what is left of reads by queries and by corrections that
+// cancel, and what does not cancel is dV's rounding: S, dS and U are the same in both.  With
+// 16 bits of dV, and products of its and their second terms left out, dg was off by 2.3 % for one key again
+// and again at beta = 0.9997 (bf16's own rounding: 0.17 %).
 template <class E, int KD, int VS>
 struct Grads {
-  static constexpr int kO = kOut<E>, kStages = E::kBytes == 2 ? 2 : 1, kParts = E::kBytes == 2 ? 4 : 2;
+  static constexpr int kO = kOut<E>, kWT = kStateTerms, kStages = E::kBytes == 2 ? 2 : 1, kParts = E::kBytes == 2 ? 4 : 2;
   static constexpr int kT = 4 * kParts * 32;  // threads
   static constexpr int kK = 0, kQ = kK + kIn<E> * mat_bytes(kC, KD);
   static constexpr int kHead = kQ + kIn<E> * mat_bytes(kC, KD);  // the gates, of this head and the next
@@ -326,7 +339,7 @@ struct Grads {
   // a slice of the value columns: S^T, dS^T, dY, dV, U
   static constexpr int kState = E::kBytes == 2 ? VS / 16 * (KD / 16) * kBlockBytes : kO * mat_bytes(VS, KD);
   static constexpr int kS = 0, kD = kS + kState, kY = kD + kState, kW = kY + kIn<E> * mat_bytes(kC, VS);
-  static constexpr int kU = kW + kO * mat_bytes(kC, VS), kSliceBytes = kU + kO * mat_bytes(kC, VS);
+  static constexpr int kU = kW + kWT * mat_bytes(kC, VS), kSliceBytes = kU + kO * mat_bytes(kC, VS);
   static constexpr int kEnd = kSlice + kStages * kSliceBytes, kSmem = kEnd > kEndF ? kEnd : kEndF;
   static constexpr int kCN = kC / 8 / kParts, kKN = KD / 8 / kParts;  // a warp's tiles of 8 columns
 };
@@ -373,34 +386,34 @@ __device__ __forceinline__ auto state_down(uint32_t at) {
   else return Down{mat<VS, KD>(at)};
 }
 
-// c += A B and d += A2 B, of TA and TB (A2: TB) terms, over k from 0 to k1
-template <int TA, int TB, int N, class A, class A2, class B>
+// c += A B and d += A2 B, of TA, TB and (A2) TD terms, over k from 0 to k1: the products
+// below 2^-8 TB of the first one are left out for A, those below 2^-8 TD for A2
+template <int TA, int TB, int TD, int N, class A, class A2, class B>
 __device__ __forceinline__ void both_products(float (&c)[N][4], float (&d)[N][4], const A& a, const A2& a2, const B& b, int m,
                                               int n, int k1) {
   if constexpr (TA == TB) {
     product<TA, TB, TB>(c, a, b, m, n, 0, k1);
-    product<TB, TB, TB>(d, a2, b, m, n, 0, k1);
+    product<TD, TB, TD>(d, a2, b, m, n, 0, k1);
   } else {
 #pragma unroll
     for (int k = 0; k < k1; k += 16) {
-      uint32_t fa[TA][4], fd[TB][4];
+      uint32_t fa[TA][4], fd[TD][4];
 #pragma unroll
       for (int i = 0; i < TA; ++i) a(fa[i], m, k, i);
 #pragma unroll
-      for (int i = 0; i < TB; ++i) a2(fd[i], m, k, i);
+      for (int i = 0; i < TD; ++i) a2(fd[i], m, k, i);
 #pragma unroll
       for (int j = 0; j < TB; ++j) {
         uint32_t fb[N][2];
         b.template get<N>(fb, k, n, j);
 #pragma unroll
-        for (int i = 0; i < TB; ++i)
-          if (i + j < TB) {
+        for (int i = 0; i < TD; ++i) {
 #pragma unroll
-            for (int t = 0; t < N; ++t) {
-              if (i < TA) mma(c[t], fa[i < TA ? i : 0], fb[t][0], fb[t][1]);
-              mma(d[t], fd[i], fb[t][0], fb[t][1]);
-            }
+          for (int t = 0; t < N; ++t) {
+            if (i < TA && i + j < TB) mma(c[t], fa[i < TA ? i : 0], fb[t][0], fb[t][1]);
+            if (i + j < TD) mma(d[t], fd[i], fb[t][0], fb[t][1]);
           }
+        }
       }
     }
   }
@@ -478,16 +491,18 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
     const int64_t column = static_cast<int64_t>(h) * a.dv + v0;
     if (v0 == 0) load_gates<kT>(base + L::kHead + (h % L::kStages) * L::kHeadBytes, a.gates + unit);
     load_rows<E, VS, kT>(mat<kC, VS>(at + L::kY), a.dy + p * a.dy_stride + column, a.dy_stride, ch.len, cols, mask, a.vec);
-    // of type bf16 dV's first term is the output, and U's terms are kept apart
+    // of type bf16 dV's first term is the output, and its others and U's terms are kept apart
     const int64_t wide = static_cast<int64_t>(a.heads) * a.dv;
     const Mat W = mat<kC, VS>(at + L::kW), U = mat<kC, VS>(at + L::kU);
     const auto* kept = kept_writes<E>(a) + p * wide + column;
     load_rows<E, VS, kT>(W, a.dv_out + p * a.dv_stride + column, a.dv_stride, ch.len, cols, nullptr, a.vec);
     load_rows<E, VS, kT>(U, kept, wide, ch.len, cols, nullptr, a.vec);
     if constexpr (E::kBytes == 2) {
-      auto second = [](const Mat& m) { return Mat{m.base + static_cast<uint32_t>(m.term), m.pitch, m.term}; };
-      load_rows<E, VS, kT>(second(W), a.writes + p * wide + column, wide, ch.len, cols, nullptr, a.vec);
-      load_rows<E, VS, kT>(second(U), kept + a.n_tokens * wide, wide, ch.len, cols, nullptr, a.vec);
+      auto term = [](const Mat& m, int n) { return Mat{m.base + static_cast<uint32_t>(n * m.term), m.pitch, m.term}; };
+      const auto* rest = a.writes + p * wide + column;
+      load_rows<E, VS, kT>(term(W, 1), rest, wide, ch.len, cols, nullptr, a.vec);
+      load_rows<E, VS, kT>(term(W, 2), rest + a.n_tokens * wide, wide, ch.len, cols, nullptr, a.vec);
+      load_rows<E, VS, kT>(term(U, 1), kept + a.n_tokens * wide, wide, ch.len, cols, nullptr, a.vec);
     }
     load_state<E, KD, VS, kT>(at + L::kS, a.carry + unit * saved, v0, cols, a.dk);
     load_state<E, KD, VS, kT>(at + L::kD, a.after + unit * saved, v0, cols, a.dk);
@@ -562,13 +577,13 @@ __global__ void __launch_bounds__(Grads<E, KD, VS>::kT, 1) grads_kernel(Args<E> 
         const uint32_t off = (tid / kBy) * W.pitch + tid % kBy * 8;
         float u[4], w[4];
         get4<kO>(U.base + off, U.term, u);
-        get4<kO>(W.base + off, W.term, w);
+        get4<L::kWT>(W.base + off, W.term, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) dot = fmaf(u[i], w[i], dot);
       }
-      both_products<kIn<E>, kO>(cq, ck, Rows{Y}, Rows{W}, S, m, nk, VS);
+      both_products<kIn<E>, kO, L::kWT>(cq, ck, Rows{Y}, Rows{W}, S, m, nk, VS);
       product<kO, kO, kO>(cw, Rows{U}, D, m, nk, 0, VS);
-      if (low) both_products<kIn<E>, kO>(cf, ce, Rows{Y}, Rows{W}, Across{U}, m, nc, VS);
+      if (low) both_products<kIn<E>, kO, L::kWT>(cf, ce, Rows{Y}, Rows{W}, Across{U}, m, nc, VS);
     }
     // ---- F and E, the pairs of reads and writes, and what reads S and reaches dS
     float row[2] = {0.f, 0.f};
