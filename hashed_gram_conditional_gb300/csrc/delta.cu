@@ -51,7 +51,8 @@ __global__ void __launch_bounds__(1024) first_kernel(Args<E> a) {
     const int at = static_cast<int>(all < a.max_chunks ? all : a.max_chunks);
     if (s < a.n_seqs) {
       int64_t slot;
-      cost = live_slot(a, s, slot) ? min(n, a.max_chunks - at) + 1 : 1;
+      n = min(n, a.max_chunks - at);
+      cost = live_slot(a, s, at, n, slot) ? n + 1 : 1;
       longest = max(longest, cost);
       a.first[s] = at;
     }
@@ -156,7 +157,11 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(Args<E> a) {
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
   Chunk ch;
-  if (!chunk_at(a, blockIdx.x, ch) || !ch.live) return;
+  if (!chunk_at(a, blockIdx.x, ch)) return;
+  if (!ch.live) {
+    if (a.carry != nullptr && tid == 0) a.gates[unit_of(a, blockIdx.x, blockIdx.y)].into[0] = kPadding;
+    return;
+  }
   const Mat K = mat<kC, KD>(smem_u32(smem)), Q = mat<kC, KD>(K.base + kIn<E> * K.term);
   float *A = reinterpret_cast<float*>(smem), *M = A + kC * kPitch;
   Gates& gt = *reinterpret_cast<Gates*>(smem + kRoom);
@@ -409,7 +414,7 @@ __global__ void __launch_bounds__(Scan<E, KD, NQ>::kThreads, 1) scan_kernel(Args
     const int cols = min(a.dv - v0, 16 * NQ);
     const int hk = h / (a.heads / a.keys), vw = v0 + quad * 16;
     int64_t slot;
-    if (!live_slot(a, item.seq, slot)) {
+    if (!live_slot(a, item.seq, c0, item.n, slot)) {
       if (tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
       padding_zeros(a, lo, hi, c0, item.n, h, v0, cols, blockDim.x);
       continue;

@@ -109,11 +109,15 @@ __device__ __forceinline__ void bounds(const Args<E>& a, int s, int& lo, int& hi
   hi = static_cast<int>(y < lo ? lo : y > n ? n : y);
 }
 
-// Whether the sequence has a state slot of its own, or needs none.
+// Whether the sequence, of n chunks from c0 on, has a state slot of its own, or needs none.
+// A sequence that the forward pass took for padding has left nothing but kPadding in its
+// chunks' gates: it is padding in the backward pass too, which need not have the states.
+constexpr float kPadding = -1.f;  // in place of e^c
 template <class E>
-__device__ __forceinline__ bool live_slot(const Args<E>& a, int s, int64_t& slot) {
+__device__ __forceinline__ bool live_slot(const Args<E>& a, int s, int c0, int n, int64_t& slot) {
   slot = a.slots != nullptr ? a.slots[s] : s;
-  return slot >= 0 && !(a.has_state && slot >= a.n_slots);
+  if (slot < 0 || (a.has_state && slot >= a.n_slots)) return false;
+  return a.y != nullptr || n == 0 || a.gates[static_cast<size_t>(c0) * a.heads].into[0] != kPadding;
 }
 
 // Chunk number c, or false where there are fewer.
@@ -132,7 +136,7 @@ __device__ __forceinline__ bool chunk_at(const Args<E>& a, int c, Chunk& ch) {
   ch.start = from + (c - a.first[lo]) * kC;
   ch.len = to - ch.start < kC ? to - ch.start : kC;
   int64_t slot;
-  ch.live = live_slot(a, lo, slot);
+  ch.live = live_slot(a, lo, a.first[lo], 1, slot);
   return ch.len > 0;
 }
 

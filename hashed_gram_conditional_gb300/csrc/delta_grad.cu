@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(Back<E, KD, NQ>::kThreads, 1) back_kernel(Args
     const int cols = min(a.dv - v0, 16 * NQ);
     const int hk = h / (a.heads / a.keys), vw = v0 + quad * 16;
     int64_t slot;
-    if (!live_slot(a, item.seq, slot)) {
+    if (!live_slot(a, item.seq, c0, item.n, slot)) {
       if (tid == 0 && h == 0 && v0 == 0 && a.status != nullptr && slot >= 0) atomicOr(a.status, ENGRAM_ST_BAD_SLOT);
       padding_zeros(a, lo, hi, c0, item.n, h, v0, cols, blockDim.x);
       continue;
