@@ -134,6 +134,8 @@ _SIGS = {
                                _P, _P, _P, _P],
     "engram_selftest_wait": [_I32, _P, _P, _P],
     "engram_selftest_distill_wait": [_P, _I32, _I64, _I64, _I64, _P, _P, _I32, _P, _P, _I64, _P, _P],
+    "engram_selftest_delta_wait": [_I32, _P, _P, _P, _P, _P, _P, _I32, _I64, _I32, _I32, _I32, _I32, _P, _I64, _P, _P, _P, _P,
+                                   _P, _P, _P, _P, ctypes.c_size_t, _P, _P],
     "engram_selftest_grad_wait": [_P, _I32, _I64, _P, _I64, _I32, _I32, _I64, _P, _P, _P, _P, ctypes.c_size_t, _P,
                                   _P],
     "engram_gather_rows_bf16": [_P, _I64, _I32, _P, _I64, _I32, _P, _P, _P],
@@ -1680,6 +1682,29 @@ def engram_selftest_distill_wait(logits: torch.Tensor, teacher_ids: torch.Tensor
                                           teacher_logits.data_ptr(), teacher_ids.shape[1], loss.data_ptr(),
                                           _addr(dlogits), ds, _word(status, logits, idx), _raw_stream(idx)),
            "engram_selftest_distill_wait")
+
+
+def engram_selftest_delta_wait(which: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, b: torch.Tensor,
+                               cu_seqlens: torch.Tensor, key_heads: int, status: torch.Tensor, carry: torch.Tensor,
+                               y: Optional[torch.Tensor] = None, dy: Optional[torch.Tensor] = None,
+                               grads: Sequence[torch.Tensor] = ()):
+    """Diagnostic: a delta rule of scale 1 (into y and carry) or, with dy, its gradients (into the five of grads), in
+    which copies (which 0) or other blocks' states (1) are waited for that never come; after a few seconds it has set
+    ST_TIMEOUT in ``status``, and the outputs are undefined.  Rows are contiguous.  Asynchronous on the current stream."""
+    L = _load()
+    idx, T, shape, args = _delta_inputs(q, k, v, g, b, key_heads)
+    n_seqs = _delta_sequences(cu_seqlens, None, None, 0, q, idx, T)
+    _flat(carry, "carry", torch.float32, q, idx)
+    if carry.numel() * 4 < _bytes_of("engram_delta_carry_bytes", T, n_seqs, *shape[1:]):
+        raise ValueError("carry is too small (delta_carry)")
+    likes = ((y, v),) if dy is None else ((dy, v), *zip(grads, (q, k, v, g, b), strict=True))
+    for t, like in (*likes, (q, q), (k, k), (v, v), (g, g), (b, b)):
+        _flat(t, "rows", q.dtype, q, idx, like.numel())
+    out = [t.data_ptr() for t in grads] if dy is not None else [None] * 5
+    workspace = delta_workspace(T, n_seqs, *shape, q.device, dy is not None)
+    _call(idx, "engram_selftest_delta_wait", L.engram_selftest_delta_wait, which, _addr(dy), *args[:10:2], args[10], T, *shape,
+          cu_seqlens.data_ptr(), n_seqs, _addr(y), carry.data_ptr(), *out, workspace.data_ptr(), workspace.numel(),
+          _word(status, q, idx))
 
 
 class EngramLayer:

@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(Scan<E, KD, NQ>::kThreads, 1) scan_kernel(Args
         copies_begun();
       } else {
         stage_copies(stages, stage_of(i), stage + L::kM, a.tri + unit * kTriBytes, (kS + kO) * kTerm, stage + L::kG, a.gates + unit,
-                     a.vec);
+                     a.vec, a.absent);
       }
     };
     if (!kAlone<NQ> && n > from) load(from);
@@ -821,6 +821,8 @@ int launch_step(const Args<E>& a, int64_t batch, cudaStream_t st) {
   return check_launch("step_kernel");
 }
 
+thread_local int selftest_absent = 0;
+
 Space space(void* base, int64_t n_tokens, int64_t n_seqs, int32_t keys, int32_t heads, int32_t dk, int32_t dv, bool backward) {
   Space s{};
   const size_t units = static_cast<size_t>(max_chunks(n_tokens, n_seqs)) * heads;
@@ -944,6 +946,7 @@ extern "C" int engram_delta(const void* q_d, int64_t q_stride, const void* k_d, 
     a.tri = s.tri;
     a.gates = s.gates;
     if (a.carry != nullptr) use_kept_triangles(a);
+    set_absent(a);
     int r = launch_first<E>(a, as_stream(stream));
     if (!r) r = launch_prepare<E>(a, as_stream(stream));
     return r ? r : launch_scan<E>(a, sms, as_stream(stream));
@@ -997,4 +1000,24 @@ extern "C" int engram_delta_step(const void* q_d, int64_t q_stride, const void* 
     return launch_step<E>(a, batch, as_stream(stream));
   };
   return type == ENGRAM_T_BF16 ? go(train::Bf16{}) : go(train::F32{});
+}
+
+extern "C" int engram_selftest_delta_wait(int32_t which, const void* dy_d, const void* q_d, const void* k_d, const void* v_d,
+                                          const void* g_d, const void* b_d, int32_t type, int64_t n_tokens, int32_t key_heads,
+                                          int32_t heads, int32_t dk, int32_t dv, const int64_t* cu_seqlens_d, int64_t n_seqs,
+                                          void* y_d, float* carry_d, void* dq_d, void* dk_d, void* dv_d, void* dg_d, void* db_d,
+                                          void* workspace_d, size_t workspace_bytes, int32_t* status_d, void* stream) {
+  if (which != 0 && which != 1) return fail(ENGRAM_E_INVALID, "which %d is not 0 or 1", which);
+  const int64_t wk = static_cast<int64_t>(key_heads) * dk, wv = static_cast<int64_t>(heads) * dv;
+  selftest_absent = which + 1;
+  const int rc =
+      dy_d == nullptr
+          ? engram_delta(q_d, wk, k_d, wk, v_d, wv, g_d, heads, b_d, heads, type, n_tokens, key_heads, heads, dk, dv, 1.f,
+                         cu_seqlens_d, n_seqs, nullptr, nullptr, nullptr, nullptr, 0, y_d, wv, carry_d, workspace_d,
+                         workspace_bytes, status_d, stream)
+          : engram_delta_grad(dy_d, wv, q_d, wk, k_d, wk, v_d, wv, g_d, heads, b_d, heads, type, n_tokens, key_heads, heads, dk,
+                              dv, 1.f, cu_seqlens_d, n_seqs, nullptr, nullptr, carry_d, nullptr, 0, dq_d, wk, dk_d, wk, dv_d, wv,
+                              dg_d, heads, db_d, heads, workspace_d, workspace_bytes, status_d, stream);
+  selftest_absent = 0;
+  return rc;
 }

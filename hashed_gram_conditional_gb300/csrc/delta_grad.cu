@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(Back<E, KD, NQ>::kThreads, 1) back_kernel(Args
         copies_begun();
       } else {
         stage_copies(stages, stage_of(i), stage + L::kM, a.tri + unit * kTriBytes, 2 * kS * kTerm, stage + L::kG, a.gates + unit,
-                     a.vec);
+                     a.vec, a.absent);
       }
     };
     if (kAlone<NQ> && copier >= 0) {
@@ -890,6 +890,7 @@ extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void
     a.after = s.after;
     a.writes = s.writes;
     a.shared = s.shared;
+    set_absent(a);
     return launch_grad<E>(a, sms, as_stream(stream));
   };
   return type == ENGRAM_T_BF16 ? go(train::Bf16{}) : go(train::F32{});

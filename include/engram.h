@@ -1002,6 +1002,20 @@ int engram_selftest_distill_wait(const void* logits_d, int32_t type, int64_t n_t
                                  int32_t top, float* loss_d, void* dlogits_d, int64_t dlogits_stride,
                                  int32_t* status_d, void* stream);
 
+/* The same for the waits between the blocks, and within a block, of engram_delta (dy_d
+ * NULL: y_d and, unless it is NULL, carry_d are its outputs) or engram_delta_grad (carry_d
+ * as a forward call of scale 1 filled it); rows lie one behind the other, without mask,
+ * slots and states, scale 1.
+ *   which  0: every chunk's copies are expected to bring more bytes than they do (bf16
+ *          and so many sequences and heads that a block has four quads); 1: no block
+ *          says that it has handed a state on (more sequences and heads than SMs).
+ *          Where a call has no such wait it is an ordinary one */
+int engram_selftest_delta_wait(int32_t which, const void* dy_d, const void* q_d, const void* k_d, const void* v_d,
+                               const void* g_d, const void* b_d, int32_t type, int64_t n_tokens, int32_t key_heads,
+                               int32_t heads, int32_t dk, int32_t dv, const int64_t* cu_seqlens_d, int64_t n_seqs,
+                               void* y_d, float* carry_d, void* dq_d, void* dk_d, void* dv_d, void* dg_d, void* db_d,
+                               void* workspace_d, size_t workspace_bytes, int32_t* status_d, void* stream);
+
 /* Thread-local message of the last failure (empty string if none). */
 const char* engram_last_error(void);
 /* Name of an ENGRAM_* return code. */
