@@ -146,6 +146,7 @@ struct Teacher {
   using Args = engram::Args;
   using Entries = Held;
   static constexpr int kEntryBytes = engram::kEntryBytes;
+  static constexpr bool kKnown = true;
   static int table_log2(int top) { return engram::table_log2(top); }
   static __host__ __device__ constexpr size_t table_bytes(int log2) { return engram::table_bytes(log2); }
   static __device__ __forceinline__ float weight(const Args& a, int64_t row) {

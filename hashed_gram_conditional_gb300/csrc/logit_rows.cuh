@@ -19,6 +19,7 @@
 //   weight        the row's weight; rows of weight 0 are not read
 //   read          a warp reads a row's entries before the row's logits are
 //                 overwritten, and gives two numbers on them
+//   kKnown        whether the second of those is P, which no walk then has to make and hand on
 //   mass          P, once the row's maximum and sum are known; 0: nothing to learn
 //   fix           the entries' gradients, over what the row's walk wrote there
 //   finish        a warp writes the row's loss
@@ -313,7 +314,7 @@ struct Head {  // in front of the dynamic shared memory
   uint64_t known[kTold], used[kTold];  // the target's entries are ready / no longer needed
   float2 pair[kPairs][kMaxCluster * kW];
   float2 stats[kMaxDepth];     // a row's (maximum, sum), for the copying warp
-  float weight[kMaxDepth], mass[kMaxDepth];
+  float weight[kMaxDepth], mass[kMaxDepth];  // (the mass where `read` does not know it)
   float2 told[kTold];    // what the target keeps of a row
   int abort;
 };
@@ -415,8 +416,9 @@ __global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const t
       const float w = h.weight[i % a.depth];
       const float2 known = h.told[i % a.keep], st = h.stats[i % a.depth];
       const typename G::Entries e = entries(i);
-      const float mass = h.mass[i % a.depth];  // (made by the walk: the next copy does not wait for it)
-      const bool none = mass == 0.f;
+      // (made by the walk where it is not known before: the next copy does not wait for it)
+      const float mass = G::kKnown ? known.y : h.mass[i % a.depth];
+      const bool none = w == 0.f || mass == 0.f;
       int edge = -1;  // a value of the row's first or last vector that this lane finishes
       float edge_z = 0.f;
       if (dz != nullptr && !none) {
@@ -485,15 +487,16 @@ __global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const t
         join(m, s, q.x, q.y, c);
       }
       join_warp(m, s, c);
-      const float w = h.weight[i % a.depth];
-      const float mass = w == 0.f ? 0.f : G::mass(a, entries(i), h.told[i % a.keep], m, s, inv_tau);
+      // (the mass of a row without weight is made of what an earlier row has left, and not used:
+      // a branch around it took the distillation of 4096 x 129,280 from 377 us to 395)
+      const float w = h.weight[i % a.depth], mass = G::mass(a, entries(i), h.told[i % a.keep], m, s, inv_tau);
       if (tid == 0) {
         h.stats[i % a.depth] = make_float2(m, s);
-        h.mass[i % a.depth] = mass;
+        if constexpr (!G::kKnown) h.mass[i % a.depth] = mass;
       }
       if (dz != nullptr) {
         r.at(z, dz, a, row_at(i), rank, true);
-        if (mass == 0.f) {  // nothing to learn here
+        if (w == 0.f || mass == 0.f) {  // nothing to learn here
           r.zeros(tid, kData);
         } else {
           const float coef = w * a.tau * mass / s;

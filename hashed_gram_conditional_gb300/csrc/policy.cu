@@ -30,6 +30,7 @@ struct Numbers {
 struct Sampled {
   using Args = engram::Args;
   static constexpr int kEntryBytes = sizeof(Numbers);
+  static constexpr bool kKnown = false;
   struct Entries {
     Numbers* at;
     __device__ __forceinline__ Entries(void* base, int) : at(static_cast<Numbers*>(base)) {}
