@@ -44,3 +44,26 @@ def test_a_decay_that_hardly_matters(T, keys, H, d, shift, kind):
     tol = 2.0 ** -21 * later(parts[0].abs() + parts[1].abs()) + half * want["dg"].abs() * (1 + 1e-6)
     off = (got - want["dg"]).abs()
     assert (off <= tol).all(), (int((off > tol).sum()), float((off / tol).max()))
+
+
+@pytest.mark.parametrize("T,keys,H,dk,dv,S", [(200, 2, 4, 64, 64, 1), (300, 2, 4, 40, 72, 3), (130, 1, 1, 64, 16, 1)])
+def test_fp32_keeps_its_digits(T, keys, H, dk, dv, S):
+    """All outputs of type fp32, each by its error's norm against its own.
+
+    An operand's three terms are 24 bits and an fp32 sum's roundings less than the tensor cores' cuts: of a product's main
+    accumulator one for every 16 terms, 2^-24 of what it then holds on average, at most 2 of them in all for 64 terms whose
+    partial sums grow to the whole, and the triangles' products the same: 2^-23 a product.  Of the products that follow
+    one another, no output has more than 16 in front of it, and their errors are independent: 2^-21.  An operand of 16 bits
+    would show: 2^-18 / sqrt(3) and more of what it is multiplied into."""
+    cu = [T * s // S for s in range(S + 1)]
+    args, dy = inputs(T, keys, H, dk, dv, "f32", 320), make((T, H * dv), "f32", 330)
+    s0, ds = make((S, H, dk, dv), "f32", 331, 0.3), make((S, H, dk, dv), "f32", 332, 0.3)
+    carry, out, back = eg.delta_carry(T, S, keys, H, dk, dv, DEV), torch.empty_like(s0), ds.clone()
+    y = eg.engram_delta(*args, i64(cu), keys, state=s0, state_out=out, carry=carry)
+    grads = eg.engram_delta_grad(dy, *args, carry, i64(cu), keys, dstate=back)
+    fwd = OB.delta(*d64(*args), cu, keys, dk ** -0.5, state=s0.double())
+    want = OB.delta_grad(dy.double(), *d64(*args), cu, keys, dk ** -0.5, state=s0.double(), dstate=ds.double())
+    got = dict(y=y, state=out, **dict(zip(("dq", "dk", "dv", "dg", "db"), grads)), dstate=back)
+    for name, t in got.items():
+        w = fwd[name] if name in ("y", "state") else want[name]
+        assert float((t.double() - w).norm() / w.norm()) <= 2.0 ** -21, name
