@@ -1367,7 +1367,8 @@ def _call(idx: int, name: str, fn, *args):
 
 
 def delta_carry(n_tokens: int, n_seqs: int, key_heads: int, heads: int, dk: int, dv: int, device) -> torch.Tensor:
-    """Buffer for what engram_delta saves for its backward pass: states, writes and the chunks' triangles."""
+    """Buffer for what engram_delta saves for its backward pass: states, writes and the chunks' triangles.  (Its size does
+    not depend on key_heads.)"""
     n = _bytes_of("engram_delta_carry_bytes", n_tokens, n_seqs, heads, dk, dv) // 4
     return torch.empty(max(n, 1), dtype=torch.float32, device=device)
 
@@ -1466,8 +1467,9 @@ def engram_delta_grad(dy: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: tor
                       dv: Optional[torch.Tensor] = None, dg: Optional[torch.Tensor] = None,
                       db: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                       status: Optional[torch.Tensor] = None):
-    """The gradients (dq, dk, dv, dg, db) of engram_delta, from the carry that the forward call filled.  dstate f32
-    [n_slots][heads][dk][dv]: the gradient of the last states, replaced by that of the first."""
+    """The gradients (dq, dk, dv, dg, db) of engram_delta, from the carry that the forward call filled (v gives its shape
+    alone: its values are not read).  dstate f32 [n_slots][heads][dk][dv]: the gradient of the last states, replaced by
+    that of the first."""
     L = _lib or _load()
     idx, T, shape, args = _delta_inputs(q, k, v, g, b, key_heads)
     n_slots = 0 if dstate is None else _delta_state(dstate, "dstate", q, idx, shape)

@@ -817,7 +817,7 @@ extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void
   if ((rc = check_rows(dy_d, type, dy_stride, wide_v, "dy"))) return rc;
   if ((rc = check_rows(q_d, type, q_stride, wide_k, "q"))) return rc;
   if ((rc = check_rows(k_d, type, k_stride, wide_k, "k"))) return rc;
-  if ((rc = check_rows(v_d, type, v_stride, wide_v, "v"))) return rc;
+  if (v_d != nullptr && (rc = check_rows(v_d, type, v_stride, wide_v, "v"))) return rc;  // (it is not read)
   if ((rc = check_rows(g_d, type, g_stride, heads, "g"))) return rc;
   if ((rc = check_rows(b_d, type, b_stride, heads, "b"))) return rc;
   if ((rc = check_rows(dq_d, type, dq_stride, wide_k, "dq"))) return rc;
@@ -840,7 +840,6 @@ extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void
     a.dy = static_cast<const T*>(dy_d);
     a.q = static_cast<const T*>(q_d);
     a.k = static_cast<const T*>(k_d);
-    a.v = static_cast<const T*>(v_d);
     a.g = static_cast<const T*>(g_d);
     a.b = static_cast<const T*>(b_d);
     a.dq = static_cast<T*>(dq_d);
@@ -851,7 +850,6 @@ extern "C" int engram_delta_grad(const void* dy_d, int64_t dy_stride, const void
     a.dy_stride = dy_stride;
     a.q_stride = q_stride;
     a.k_stride = k_stride;
-    a.v_stride = v_stride;
     a.g_stride = g_stride;
     a.b_stride = b_stride;
     a.dq_stride = dq_stride;

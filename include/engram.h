@@ -764,7 +764,9 @@ int engram_delta(const void* q_d, int64_t q_stride, const void* k_d, int64_t k_s
 /* The gradients of q, k, v, g, b and the first states; those of a key head are summed over
  * the value heads that share it.  carry_d is what a forward call on the same arguments
  * filled; a sequence that was padding there (a slot that the forward call's states do not
- * have) is padding here, with or without dstate_d.
+ * have) is padding here, with or without dstate_d.  Positions outside every sequence are
+ * left as they are; outputs overlap no input and not one another.
+ *   v_d          not read: NULL, or what the forward call had, whatever it holds now
  *   dstate_d     float32 [n_slots][heads][dk][dv] in/out, or NULL (zeros in): the
  *                gradients of the last states on entry, of the first states on return
  *   workspace_d  engram_delta_workspace_bytes(..., 1) bytes */

@@ -64,3 +64,26 @@ def test_without_a_state_any_slot_will_do():
         rows.append((y, *eg.engram_delta_grad(dy, *args, carry, cu, keys, slots=i32(slots))))
     for u, w in zip(*rows):
         assert torch.equal(u, w)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_the_backward_call_does_not_need_the_values(kind):
+    """v may hold anything by then, and the C call takes none at all."""
+    T, keys, H, dk, dv, cu = 150, 1, 2, 32, 40, i64([0, 70, 150])
+    (q, k, v, g, b), dy = inputs(T, keys, H, dk, dv, kind, 560), make((T, H * dv), kind, 570)
+    carry = eg.delta_carry(T, 2, keys, H, dk, dv, DEV)
+    eg.engram_delta(q, k, v, g, b, cu, keys, carry=carry)
+    want = eg.engram_delta_grad(dy, q, k, v, g, b, carry, cu, keys)
+    v.fill_(float("nan"))
+    for u, w in zip(eg.engram_delta_grad(dy, q, k, v, g, b, carry, cu, keys), want):
+        assert torch.equal(u, w)
+    got, ws = [torch.empty_like(t) for t in want], eg.delta_workspace(T, 2, keys, H, dk, dv, DEV, True)
+    wk, wv = keys * dk, H * dv
+    rc = eg.lib().engram_delta_grad(
+        dy.data_ptr(), wv, q.data_ptr(), wk, k.data_ptr(), wk, None, wv, g.data_ptr(), H, b.data_ptr(), H, 0 if kind == "bf16" else 1,
+        T, keys, H, dk, dv, dk ** -0.5, cu.data_ptr(), 2, None, None, carry.data_ptr(), None, 0,
+        *(x for t in got for x in (t.data_ptr(), t.shape[1])), ws.data_ptr(), ws.numel(), None,
+        torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    for u, w in zip(got, want):
+        assert torch.equal(u, w)
