@@ -152,6 +152,7 @@ struct Teacher {
   static __device__ __forceinline__ float weight(const Args& a, int64_t row) {
     return a.weight != nullptr ? __ldg(a.weight + row) : 1.f;
   }
+  static __device__ __forceinline__ float factor(const Args& a, float w) { return w * a.tau; }
   // the normaliser and the mass
   template <class E>
   static __device__ __forceinline__ void read(const Args& a, const typename E::T* z, int64_t row, float inv_tau, int lane,

@@ -2,7 +2,7 @@
 // loss share.
 //
 // With q = softmax(z / tau), a target's mass P and its mass p_v at a few entries:
-//   dz_v = w tau (P q_v - p_v)
+//   dz_v = W (P q_v - p_v)
 //
 // A position's gradient needs its whole row's maximum and sum, so a row is
 // read once and kept: the blocks of a cluster hold its parts in shared memory,
@@ -17,6 +17,7 @@
 //   Args          its arrays, derived from RowArgs
 //   kEntryBytes   shared memory for each of a row's `top` entries
 //   weight        the row's weight; rows of weight 0 are not read
+//   factor        W of a row of that weight
 //   read          a warp reads a row's entries before the row's logits are
 //                 overwritten, and gives two numbers on them
 //   kKnown        whether the second of those is P, which no walk then has to make and hand on
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const t
       next = ahead;
       if (dz != nullptr && !none) {
         r.at(z, dz, a, row_at(i), rank, true);
-        const float scale = w * a.tau, coef = scale * mass / st.y;
+        const float scale = G::factor(a, w), coef = scale * mass / st.y;
         if (edge >= 0) E::store(r.dz + edge, ex2((edge_z - st.x) * c) * coef);
         __syncwarp();
         G::template fix<E>(a, r, e, mass, st.x, c, coef, scale, lane, 32);
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__((kW + 1 + kPrep<kW>) * 32) rows_kernel(const t
         if (w == 0.f || mass == 0.f) {  // nothing to learn here
           r.zeros(tid, kData);
         } else {
-          const float coef = w * a.tau * mass / s;
+          const float coef = G::factor(a, w) * mass / s;
           const uint4* src = slot(i) - r.v0;
           if (r.off == r.doff) {
             uint4* dv = reinterpret_cast<uint4*>(r.dz - r.off);
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(kLongThreads, 3) long_rows_kernel(const typena
     r.zeros(tid, kLongThreads);
     return;
   }
-  const float scale = w * a.tau, coef = scale * mass / s;
+  const float scale = G::factor(a, w), coef = scale * mass / s;
   if (r.off == r.doff) {
     uint4* dv = reinterpret_cast<uint4*>(r.dz - r.off);
 #pragma unroll 4
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__(kShortWarps * 32, 8) short_rows_kernel(const t
       r.zeros(lane, 32);
       continue;
     }
-    const float scale = w * a.tau, coef = scale * mass / s;
+    const float scale = G::factor(a, w), coef = scale * mass / s;
     if (r.off == r.doff) {
       uint4* dv = reinterpret_cast<uint4*>(r.dz - r.off);
 #pragma unroll 4

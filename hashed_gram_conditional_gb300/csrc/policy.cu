@@ -6,7 +6,8 @@
 //   loss = w (-min(r A, clip(r, 1 - low, 1 + high) A) + kl (e^d - 1 - d))
 //   dloss/dl = w (-[not clipped] r A - kl (e^d - 1))
 //   dz_v = dloss/dl ([v = a] - q_v) / tau
-// which is a softmax row with one entry: P = p_a = -(dloss/dl) / (w tau^2).  The rows
+// which is a softmax row with one entry: W = w, P = p_a = -(dloss/dl) / (w tau).  (W = w tau, as
+// the distillation has it, would take tau^-2, which an fp32 number need not hold.)  The rows
 // are walked by the kernels of logit_rows.cuh.
 #include "logit_rows.cuh"
 
@@ -43,6 +44,7 @@ struct Sampled {
     if (id < 0 || id >= a.vocab) return 0.f;
     return a.weight != nullptr ? __ldg(a.weight + row) : 1.f;
   }
+  static __device__ __forceinline__ float factor(const Args&, float w) { return w; }
   static __device__ __forceinline__ void skip(const Args& a, int64_t row, int lane) {
     if (lane == 0 && __ldg(a.ids + row) >= a.vocab && a.status != nullptr) atomicOr(a.status, ENGRAM_ST_BAD_TOKEN);
   }
@@ -82,7 +84,7 @@ struct Sampled {
       // e^x - 1; for small x, where the difference would cancel, from its series
       d = fmaf(a.kl, fabsf(x) < 0.125f ? fmaf(gap_series(x) * x, x, x) : rows::ex2(x * kLog2e) - 1.f, d);
     }
-    return d * inv_tau * inv_tau;
+    return d * inv_tau;
   }
   template <class E>
   static __device__ __forceinline__ void fix(const Args& a, const rows::Row<E>& r, const Entries& e, float mass, float m,
