@@ -19,8 +19,11 @@
 // 16,384 x 5120 bf16 with gate, residual and next norm: 130 us (6.5 TB/s, 97 % of a copy's
 // rate), bound by memory, as is the gradient: 237 us, of which 227 (5.9 TB/s) for the rows and
 // 9 for the weights' sums.  Rows that are not 16-byte aligned go a value a thread
-// (8192 x 5119: 381 and 960 us), and rows longer than a block's threads hold are walked
-// several times.
+// (8192 x 5119: 381 and 950 us), and rows longer than a block's threads hold are walked
+// several times.  The gradient of aligned rows of more than 7504 bf16 or 3752 fp32 values, of
+// which no three fit a block's shared memory, goes without rows on their way: 16,384 x 8192
+// bf16 701 us (3.1 TB/s), 16,384 x 5120 fp32 721 (3.7), where sums of columns take registers
+// that are not there.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -166,8 +169,9 @@ __device__ __forceinline__ float inverse_fast(float x) {
   return r;
 }
 
-// sigmoid(z): bf16's from the hardware's exponential and division (2^-21, far
-// below a bf16 rounding), fp32's from the rounded ones.
+// sigmoid(z): bf16's from the hardware's exponential and division (2^-21, and 2^-24 |z| from
+// the exponent's rounding: 2^-17 at |z| = 80, far below a bf16 rounding), fp32's from the
+// rounded ones.
 template <class E>
 __device__ __forceinline__ float sigmoid(float z) {
   if constexpr (E::kBytes == 2) return __fdividef(1.f, 1.f + __expf(-z));
@@ -1046,51 +1050,62 @@ int launch_norm(Args a, int sms, cudaStream_t st) {
   return check_launch("norm_kernel");
 }
 
+// Blocks of a gradient's kernel that stay on an SM together: two where registers and shared
+// memory leave room, else one.
+int staying(const void* kernel, std::atomic<int>& registers, int threads, size_t smem, int* out) {
+  int regs = registers.load(std::memory_order_relaxed);
+  if (regs == 0) {
+    cudaFuncAttributes at;
+    cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+    if (e != cudaSuccess) return fail(ENGRAM_E_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(e));
+    registers.store(regs = (at.numRegs + 7) / 8 * 8, std::memory_order_relaxed);
+  }
+  // (each of the SM's four parts has 16,384 registers for its warps)
+  *out = (2 * (threads / 32) + 3) / 4 * 32 * regs <= 16384 && 2 * (smem + 10 * 1024) <= 228 * 1024 ? 2 : 1;
+  return ENGRAM_OK;
+}
+
 template <class E>
 int launch_grad(Args a, float* dw, float* ds, float* dn, int sms, cudaStream_t st) {
-  // two blocks an SM, or one where a block's rows take more than half of the shared memory
+  int blocks = 0;
+  // (16,384 rows, bf16: of 3600 in blocks of 480 threads and 96 registers 212 us with two for each SM,
+  // one after the other, 207 with one; of 2560 in blocks of 320 threads 173 with one, 129 with two; of
+  // 8192 without a ring, 512 threads and 64 registers, 1113 with one, 701 with two)
+  auto go = [&](auto kernel, std::atomic<uint64_t>& done, std::atomic<int>& registers, int threads, size_t smem) {
+    const void* fn = reinterpret_cast<const void*>(kernel);
+    int at_once = 0, r = smem > 0 ? opt_in(fn, done) : ENGRAM_OK;
+    if (r || (r = staying(fn, registers, threads, smem, &at_once))) return r;
+    blocks = static_cast<int>(std::min<int64_t>(a.rows, std::min(kParts, at_once * sms)));
+    kernel<<<blocks, threads, smem, st>>>(a);
+    return check_launch("norm_grad_kernel");
+  };
   const bool wide = by_vectors<E>(a);
-  const int at_once = wide && kRing * kArrays * static_cast<int64_t>(a.dim) * E::kBytes > 112 * 1024 ? 1 : 2;
-  const int blocks = static_cast<int>(std::min<int64_t>(a.rows, std::min(kParts, at_once * sms)));
-  if (blocks > 0) {
-    if (!wide && a.dim > kSingles * Single<E>::kMost) {
-      norm_grad_any_kernel<E><<<blocks, kAnyThreads, 0, st>>>(a);
-    } else if (!wide) {
-      set_vecs<Single<E>>(a);
-      const int per = a.vecs <= 4 * kThreads ? 4 : kSingles, threads = ((a.vecs + per - 1) / per + 31) / 32 * 32;
-      const size_t smem = sizeof(float) * (2 * a.vecs + (a.groups > 1 && a.vecs_log2 < 0 ? a.vecs + a.groups : 0));
-      auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
-        int r = opt_in(reinterpret_cast<const void*>(kernel), done);
-        if (r == ENGRAM_OK) kernel<<<blocks, threads, smem, st>>>(a);
-        return r;
-      };
-      static std::atomic<uint64_t> done[2] = {{0}, {0}};
-      int r = per == 4 ? go(norm_grad_kernel<Single<E>, 4, kThreads>, done[0])
-                       : go(norm_grad_kernel<Single<E>, kSingles, 1024>, done[1]);
-      if (r) return r;
-    } else {
-      set_vecs<Wide<E>>(a);
-      // two vectors a thread at most: the sums of four's columns would not fit the registers
-      const int per = a.vecs <= kRingThreads ? 1 : 2, threads = ((a.vecs + per - 1) / per + 31) / 32 * 32;
-      const size_t smem = a.groups > 1 && a.vecs_log2 < 0 ? static_cast<size_t>(a.vecs + a.groups + 3) / 4 * 16 : 0;
-      const size_t ring = smem + static_cast<size_t>(kRing) * kArrays * a.vecs * 16;
-      if (ring > kRingSmem) {
-        norm_grad_kernel<Wide<E>, 2, 2 * kThreads><<<blocks, threads, smem, st>>>(a);
-      } else {
-        auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
-          int r = opt_in(reinterpret_cast<const void*>(kernel), done);
-          if (r == ENGRAM_OK) kernel<<<blocks, threads, ring, st>>>(a);
-          return r;
-        };
-        static std::atomic<uint64_t> done[2] = {{0}, {0}};
-        int r = per == 1 ? go(norm_grad_ring_kernel<E, 1>, done[0]) : go(norm_grad_ring_kernel<E, 2>, done[1]);
-        if (r) return r;
-      }
-    }
-    int rc = check_launch("norm_grad_kernel");
-    if (rc) return rc;
+  int rc;
+  if (!wide && a.dim > kSingles * Single<E>::kMost) {
+    static std::atomic<uint64_t> done{0};
+    static std::atomic<int> registers{0};
+    rc = go(norm_grad_any_kernel<E>, done, registers, kAnyThreads, 0);
+  } else if (!wide) {
+    static std::atomic<uint64_t> done[2] = {{0}, {0}};
+    static std::atomic<int> registers[2] = {{0}, {0}};
+    set_vecs<Single<E>>(a);
+    const int per = a.vecs <= 4 * kThreads ? 4 : kSingles, threads = ((a.vecs + per - 1) / per + 31) / 32 * 32;
+    const size_t smem = sizeof(float) * (2 * a.vecs + (a.groups > 1 && a.vecs_log2 < 0 ? a.vecs + a.groups : 0));
+    rc = per == 4 ? go(norm_grad_kernel<Single<E>, 4, kThreads>, done[0], registers[0], threads, smem)
+                  : go(norm_grad_kernel<Single<E>, kSingles, 1024>, done[1], registers[1], threads, smem);
+  } else {
+    static std::atomic<uint64_t> done[3] = {{0}, {0}, {0}};
+    static std::atomic<int> registers[3] = {{0}, {0}, {0}};
+    set_vecs<Wide<E>>(a);
+    // two vectors a thread at most: the sums of four's columns would not fit the registers
+    const int per = a.vecs <= kRingThreads ? 1 : 2, threads = ((a.vecs + per - 1) / per + 31) / 32 * 32;
+    const size_t smem = a.groups > 1 && a.vecs_log2 < 0 ? static_cast<size_t>(a.vecs + a.groups + 3) / 4 * 16 : 0;
+    const size_t ring = smem + static_cast<size_t>(kRing) * kArrays * a.vecs * 16;
+    rc = ring > kRingSmem ? go(norm_grad_kernel<Wide<E>, 2, 2 * kThreads>, done[0], registers[0], threads, smem)
+         : per == 1       ? go(norm_grad_ring_kernel<E, 1>, done[1], registers[1], threads, ring)
+                          : go(norm_grad_ring_kernel<E, 2>, done[2], registers[2], threads, ring);
   }
-  if (a.parts == nullptr) return ENGRAM_OK;
+  if (rc || a.parts == nullptr) return rc;
   const int across = std::max((a.dim + 31) / 32, a.groups > 1 ? (a.width + 7) / 8 : 0);
   norm_join_kernel<<<dim3(across, 3), kJoinThreads, 0, st>>>(a, blocks, dw, ds, dn);
   return check_launch("norm_join_kernel");
