@@ -15,15 +15,17 @@
 // Precision.  The states and sums are fp32.  A product's operands are sums of bf16
 // terms (8 bits each): an input of type bf16 is one term and exact; what is
 // computed on the way is three (24 bits, as fp32 has) wherever it reaches a state,
-// and two (16 bits, far below bf16's own rounding) where it only reaches outputs of
-// type bf16.  Of the terms' products those are taken that are not below the last
-// bit that is kept.  (mma.sync's bf16 form does 1024 multiply-adds a clock and SM
-// here and its tf32 form 512, measured: three bf16 terms of one operand cost less
-// than two tf32 ones.)  The tcgen05 form, three times as fast (1920 TFLOP/s against
-// 592), wants 128 rows: the whole of a head's value columns.  One block a head would
-// leave most SMs without work where there are few sequences, and between any two
-// products every value has to come to registers all the same, to be scaled and
-// split; here that is where they are, and the value columns are spread over blocks.
+// and two (16 bits) where it only reaches outputs of type bf16: 2^-17 of the terms
+// that an output is made of, far below bf16's own rounding unless these cancel.  (A
+// decay's gradient is where they do: see delta_grad.cu.)  Of the terms' products those
+// are taken that are not below the last bit that is kept.  (mma.sync's bf16 form does
+// 1024 multiply-adds a clock and SM here and its tf32 form 512, measured: three bf16
+// terms of one operand cost less than two tf32 ones.)  The tcgen05 form is three times
+// as fast (1920 TFLOP/s against 590) and has not been tried.  With the value columns as
+// its 128 rows it would be one block a head; with a chunk's rows of K over those of Q,
+// and the key columns, as its rows, the value columns could be spread over blocks as
+// they are here.  Every value would come from tensor memory to registers between any two
+// products, to be scaled and split; here that is where they are.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -798,7 +800,10 @@ inline int slices_of(int dv, int quads) { return (dv + 16 * quads - 1) / (16 * q
 // come to three quarters of the SMs or more; else one, so that few sequences and heads
 // spread over more SMs.  (dk = dv = 128, bf16: a chunk takes a block of four quads 5.6 us
 // and one of one 2.0, measured forwards: four blocks of one on an SM one after another
-// take 8.0, three 6.0.)
+// take 8.0, three 6.0.)  Sequences are counted and not measured, as their lengths are not
+// known here: where one is much longer than all others together, one quad would be
+// better also for many (16,381 positions in 10 heads 580 us, with five sequences of 10
+// beside them, which make it four quads, 1434; backwards 1099 and 2221).
 template <class E>
 bool many_quads(const Args<E>& a, int sms) {
   return E::kBytes == 2 && static_cast<int64_t>(a.n_seqs) * a.heads * slices_of(a.dv, 4) * 4 >= 3 * static_cast<int64_t>(sms);

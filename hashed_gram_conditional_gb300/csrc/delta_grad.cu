@@ -22,8 +22,8 @@ namespace {
 // ------------------------------------------------ the state's gradient, backwards
 
 // A quad goes backwards as scan_kernel's go forwards, with dS^T in its registers.  (4096
-// positions in 7 sequences, 40 heads of 128, bf16: 274 us; the tensor cores are busy for
-// 42 % of the time and shared memory for 65.)
+// positions in 7 sequences, 40 heads of 128, bf16: 287 us; the tensor cores are busy for
+// 40 % of the time and shared memory for 66.)
 template <class E, int KD, int NQ>
 struct Back {
   static constexpr int kT = kAlone<NQ> ? kCopiers : NQ * 128, kThreads = kAlone<NQ> ? 128 + kCopiers : kT;
@@ -314,16 +314,17 @@ __global__ void __launch_bounds__(Back<E, KD, NQ>::kThreads, 1) back_kernel(Args
 // value columns in slices of VS.  The next slice's inputs are copied while this one is
 // used (bf16: all of them are operands as they lie in memory; fp32 are made terms on
 // the way).  A warp has 16 rows and a part of the columns of each product: a quarter, or
-// of type fp32, whose operands take more registers, half.  (The same 4096 x 40: 353 us, of
-// which the tensor cores are busy for 32 %; the rest is the instructions of a head's end,
+// of type fp32, whose operands take more registers, half.  (The same 4096 x 40: 393 us, of
+// which the tensor cores are busy for 35 %; the rest is the instructions of a head's end,
 // where F and E are made, and the barriers around them.  Making U again in place of reading
 // it took 561 us: two more barriers a slice.)
 //
 // dV is three terms for either type.  Where a write overwrites what its key held (beta near
 // 1, keys that come back), dg is what is left of reads by queries and by corrections that
 // cancel, and what does not cancel is dV's rounding: S, dS and U are the same in both.  With
-// 16 bits of dV, and products of its and their second terms left out, dg was off by 2.3 % for one key again
-// and again at beta = 0.9997 (bf16's own rounding: 0.17 %).
+// 16 bits of dV, and the products of second terms left out, dg was off by 2.3 % for one key
+// again and again at beta = 0.9997, where it is off by 0.24 % (bf16's own rounding: 0.17 %);
+// this kernel took 353 us and the backward scan 274.
 template <class E, int KD, int VS>
 struct Grads {
   static constexpr int kO = kOut<E>, kWT = kStateTerms, kStages = E::kBytes == 2 ? 2 : 1, kParts = E::kBytes == 2 ? 4 : 2;

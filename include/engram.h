@@ -721,8 +721,9 @@ int engram_recurrence_step(const void* x_d, int64_t x_stride, const void* g_d, i
  * each position, with f = sigmoid(g) and beta = sigmoid(b):
  *   S <- f S,  u = beta (v - S^T k),  S <- S + k u^T,  y = scale S^T q
  * Where engram_recurrence keeps one number a channel, this keeps what was last written
- * at a key and finds it again by a query.  Keys are used as they come: norms near 1
- * (engram_norm_add by heads gives them) keep the rule stable.  A masked position
+ * at a key and finds it again by a query.  Keys are used as they come: the rule is stable
+ * where beta |k|^2 is below 2, as it is for norms near 1 (engram_norm_add by heads gives
+ * them with w = dk^-1/2; without w its norms are dk^1/2).  A masked position
  * (mask_d[t] != 0) holds the state, gives y = 0 and takes no gradient, whatever its row
  * holds.
  *
@@ -743,12 +744,16 @@ int engram_recurrence_step(const void* x_d, int64_t x_stride, const void* g_d, i
  *                contents on entry do not matter, and the call has it to itself until
  *                it is done (two graphs that may run at once have two)
  * 1 <= dk, dv <= ENGRAM_DELTA_MAX_DIM; any stride and element-aligned pointers; outputs
- * overlap no input (but state_out_d may be state_d).  States and sums are fp32.  g below
+ * overlap no input (but state_out_d may be state_d).  States and sums are fp32; for inputs
+ * of type bf16 what is computed on the way to y, and to the gradients of q, k, v and b,
+ * alone is rounded to 16 bits, so that they are off by some 2^-16 of the terms that they
+ * are made of besides their own rounding (fp32, and the gradient of g: 2^-21).  g below
  * -80 counts as -80 and b below -40 as -40.  An infinity or a NaN in a position that is
  * not masked spoils its sequence and head from the beginning of its chunk on.  Positions
  * outside every sequence are left as they are.  A block that takes a sequence over from
- * another waits for its state; a wait that runs out sets ENGRAM_ST_TIMEOUT, and the outputs
- * are then undefined.  Results are the same from run to run. */
+ * another waits for its state, and a block's warps for its copies; a wait that runs out sets
+ * ENGRAM_ST_TIMEOUT (without status_d nobody hears of it), and the outputs are then
+ * undefined.  Results are the same from run to run. */
 #define ENGRAM_DELTA_CHUNK 64
 #define ENGRAM_DELTA_MAX_DIM 128
 size_t engram_delta_carry_bytes(int64_t n_tokens, int64_t n_seqs, int32_t heads, int32_t dk, int32_t dv);
@@ -897,7 +902,8 @@ int engram_norm_add(const void* y_d, int64_t y_stride, const void* gate_d, int64
  *   dw_d      float32 [dim/groups], dscale_d, dw_next_d float32 [dim], each or NULL
  *   workspace_d  engram_norm_add_workspace_bytes(...) bytes, 256-byte aligned, needed
  *             for the last three; its contents on entry do not matter
- * The sums over rows are taken in a fixed order: results are the same from run to run. */
+ * Outputs overlap no input (but dres_d may be dh_d) and not one another.  The sums over
+ * rows are taken in a fixed order: results are the same from run to run. */
 size_t engram_norm_add_workspace_bytes(int64_t n_rows, int32_t dim);
 int engram_norm_add_grad(const void* dh_d, int64_t dh_stride, const void* dx_d, int64_t dx_stride, const void* y_d,
                          int64_t y_stride, const void* gate_d, int64_t gate_stride, const void* h_out_d,
